@@ -483,6 +483,279 @@ simsd_status simsd_commit(const simsd_commit_desc *d, void *stream);
 simsd_status simsd_accept_noalloc(const simsd_accept_desc *d, void *stream);
 
 /* ------------------------------------------------------------------------
+ * Rotary positions as the calls below take them.  Pair i < rotary_dim / 2 of
+ * a head turns by position * w_i, w_i = base^(-2i / rotary_dim) scaled for
+ * long contexts; elements from rotary_dim on pass unchanged.
+ *   SIMSD_ROPE_LINEAR  w_i / factor
+ *   SIMSD_ROPE_NTK     w_i of the base base * factor^(rd / (rd - 2))
+ *   SIMSD_ROPE_YARN    w_i (1 - r) + w_i / factor * r, r rising in i from 0
+ *                      at floor(i(fast)) to 1 at ceil(i(slow)), where i(n) =
+ *                      rd ln(original_len / (2 pi n)) / (2 ln base) is the
+ *                      pair that makes n turns over original_len positions
+ *                      (the two ends kept within 0..rd-1 and at least 0.001
+ *                      apart)
+ *   SIMSD_ROPE_BANDED  w_i / factor * (1 - r) + w_i * r, r = (turns - slow)
+ *                      / (fast - slow) kept within 0..1, turns =
+ *                      original_len w_i / (2 pi)
+ * attn_factor multiplies the cosines and sines (so scores grow by its
+ * square); 0 selects 0.1 ln(factor) + 1 for YARN and 1 otherwise.
+ * Angles are formed to ~3e-7 rad at every position (64 bits past 2^24).
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  SIMSD_ROPE_HALF = 0,        /* pairs (i, i + rotary_dim / 2)               */
+  SIMSD_ROPE_INTERLEAVED = 1  /* pairs (2i, 2i + 1)                          */
+} simsd_rope_style;
+
+typedef enum {
+  SIMSD_ROPE_PLAIN = 0,
+  SIMSD_ROPE_LINEAR = 1,
+  SIMSD_ROPE_NTK = 2,
+  SIMSD_ROPE_YARN = 3,
+  SIMSD_ROPE_BANDED = 4
+} simsd_rope_scaling;
+
+typedef struct {
+  float base;                 /* > 1                                        */
+  int32_t rotary_dim;         /* even, 2..head_dim; 0 selects head_dim
+                                 (NTK: at least 4)                          */
+  simsd_rope_style style;
+  simsd_rope_scaling scaling;
+  float factor;               /* >= 1; not read by PLAIN                    */
+  int32_t original_len;       /* >= 1; read by YARN and BANDED              */
+  float fast, slow;           /* 0 < slow < fast; read by YARN and BANDED   */
+  float attn_factor;          /* >= 0                                       */
+} simsd_rope_spec;
+
+/* ------------------------------------------------------------------------
+ * simsd_rope -- rotates rows of heads (a pass's queries and its keys in one
+ * launch).  inverse = 1 turns by the negative angle: the gradient of the
+ * rotation with respect to its input (attn_factor multiplies it as well).
+ *   positions  device int32[rows], any value in -2^30..2^30
+ *   x0, y0     device, num_heads0 heads of every row in and out; head h of
+ *              row r starts at x0 + r * x0_row + h * x0_head (elements; a
+ *              head's head_dim elements are contiguous).  y0 may be x0 with
+ *              the same strides; other overlaps, and rows or heads of y that
+ *              overlap one another, are not allowed
+ *   x1, y1     the same for a second tensor; num_heads1 = 0: none
+ * Arrays and strides that are multiples of 16 bytes, with rotary_dim a
+ * multiple of 32 bytes, move in 16-byte vectors; others element by element
+ * (each pointer aligned to its element, SIMSD_ERR_ALIGN otherwise).
+ * rows = 0 returns SIMSD_OK.  Limits: heads <= 16384 each, rows <= 2^30.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t rows;
+  int32_t num_heads0;         /* >= 1                                       */
+  int32_t num_heads1;         /* >= 0                                       */
+  int32_t head_dim;           /* 64 or 128                                  */
+  simsd_dtype dtype;
+  int32_t inverse;            /* 0 or 1                                     */
+  simsd_rope_spec rope;
+  const int32_t *positions;
+  const void *x0;
+  void *y0;
+  const void *x1;
+  void *y1;
+  int64_t x0_row, x0_head, y0_row, y0_head;
+  int64_t x1_row, x1_head, y1_row, y1_head;
+} simsd_rope_desc;
+
+simsd_status simsd_rope(const simsd_rope_desc *d, void *stream);
+
+/* ------------------------------------------------------------------------
+ * simsd_page_map -- block tables and slot maps from request lengths, on the
+ * GPU.  Sequence b shall hold need_b = ceil((lens[b] + n_b) / 16) pages,
+ * n_b = cu_n[b+1] - cu_n[b] its tokens about to be written.  Pages come from
+ * and go back to a ring of free ones; what a call gives back can be taken
+ * from the next call on.
+ *   - need_b > held[b]: the row's entries held[b].. take the next free pages,
+ *     in the order of the sequences.  A sequence that the pages free at the
+ *     call's start do not reach to is not served (served[b] = 0, nothing of
+ *     it changes, its slots are -1), and neither is any growing one after it;
+ *   - need_b < held[b]: the entries need_b.. go to the ring's end, in the
+ *     order of the sequences (a finished request: lens = n = 0);
+ *   - slots[t] = page * 16 + offset of token t = cu_n[b] + i, at position
+ *     lens[b] + i.  Tokens past cu_n[batch] are left as they were.
+ * The ring: free_pages[(head + i) mod num_pages], i < count; queue holds
+ * {head, count}.  Pages held and free together are at most num_pages.
+ *   lens       device int32[batch]
+ *   cu_n       device int32[batch+1], non-decreasing, within 0..total_n; may
+ *              be NULL when total_n = 0 (n_b = 0)
+ *   held       device int32[batch]; held_out (may be held) the new counts
+ *   queue      device int32[2]; queue_out (may be queue) the new ring
+ *   free_pages device int32[num_pages] in/out
+ *   block_table device int32[batch][max_pages_per_seq] in/out
+ *   served     device int32[batch] out
+ *   slots      device int64[total_n] out, or NULL
+ * A sequence whose numbers are out of range (lens < 0, need_b or held
+ * outside 0..max_pages_per_seq, a cu_n range outside 0..total_n) sets the
+ * bad-input bit, is not served and is left unchanged (its slots, where its
+ * cu_n range is valid, are -1); a ring out of range (head, count, or more
+ * free and given back pages than num_pages) sets it and serves none.  A free
+ * page id outside 0..num_pages-1 sets it and is handed on as it is.
+ * Limits: batch <= 16384; batch * max_pages_per_seq < 2^31; num_pages < 2^30.
+ * Workspace: 256 bytes (status word and a counter that each call leaves at
+ * zero), one for each call that may run at the same time as another.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;
+  int32_t page_size;          /* 16                                         */
+  int32_t num_pages;          /* pages of the cache = entries of the ring   */
+  int32_t max_pages_per_seq;
+  int32_t total_n;            /* entries of slots (host copy), >= 0         */
+  const int32_t *lens;
+  const int32_t *cu_n;
+  const int32_t *held;
+  const int32_t *queue;
+  int32_t *free_pages;
+  int32_t *block_table;
+  int32_t *held_out;
+  int32_t *queue_out;
+  int32_t *served;
+  int64_t *slots;
+  void *workspace;            /* device, 256-byte aligned                   */
+  size_t workspace_bytes;
+} simsd_page_map_desc;
+
+size_t simsd_page_map_workspace_size(const simsd_page_map_desc *d);
+simsd_status simsd_page_map(const simsd_page_map_desc *d, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit cache.  k_cache, v_cache: device e4m3 [num_pages][Hkv][16][hd];
+ * k_scale, v_scale: device uint8 [num_pages][Hkv], the exponent of a page
+ * and head's scale plus 127 (an e8m0 value): a stored code c stands for
+ * c * 2^(scale - 127).  Exponents lie in -64..7, so magnitudes up to 57344;
+ * 255 marks a page and head that got a NaN or an infinity: every value of it
+ * reads as NaN.  A power of two changes no mantissa, so a page whose scale
+ * grows keeps its older codes' values (those of the few smallest binades are
+ * rounded again).
+ *
+ * simsd_kvq_append -- rotates n_b keys of sequence b at positions start[b]
+ * .. start[b]+n_b-1 and writes them and the values into those cache slots.
+ * A page's scale is the smallest one that covers its new tokens, and where
+ * tokens before start[b] lie in the page, not below its present scale (their
+ * codes are moved to the new one).  Slots at and past start[b]+n_b keep
+ * their codes; a later append writes them.
+ *   k, v     device; head h of row r at r * k_row + h * hd (elements; 0
+ *            selects Hkv * hd), sequence b's rows at cu_n[b]..; 16-byte
+ *            aligned arrays and strides
+ *   start    device int32[batch]
+ *   cu_n     device int32[batch+1] prefix sums of the rows
+ *   take     device int32[batch] or NULL: n_b = take[b] <= the sequence's
+ *            rows (the first take[b] of them are written; 0: none), e.g. the
+ *            data section's tokens of a block that closed
+ *   total_n  host: rows of k and v
+ * A sequence whose numbers are out of range, or whose table row does not
+ * cover its slots or holds a page id outside the cache, sets the workspace's
+ * bad-input bit; nothing is written for that sequence, or of that page.
+ * Two sequences must not write the same page in one call.
+ * Limits: num_kv_heads <= 1024; batch <= 2^20.  Workspace: the status word
+ * (256 bytes).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;
+  int32_t num_kv_heads;
+  int32_t head_dim;           /* 64 or 128                                  */
+  int32_t page_size;          /* 16                                         */
+  int32_t num_pages;
+  int32_t max_pages_per_seq;
+  int32_t total_n;
+  simsd_dtype dtype;          /* of k and v                                 */
+  simsd_rope_spec rope;
+  int64_t k_row, v_row;       /* row strides in elements; 0: Hkv * hd       */
+  const void *k;
+  const void *v;
+  const int32_t *start;
+  const int32_t *cu_n;
+  const int32_t *take;
+  void *k_cache;
+  void *v_cache;
+  uint8_t *k_scale;
+  uint8_t *v_scale;
+  const int32_t *block_table;
+  void *workspace;            /* device, 256-byte aligned                   */
+  size_t workspace_bytes;
+} simsd_kvq_append_desc;
+
+simsd_status simsd_kvq_append(const simsd_kvq_append_desc *d, void *stream);
+
+/* ------------------------------------------------------------------------
+ * simsd_kvq_verify -- one attention layer of a pass over [8-bit prompt cache
+ * | new tokens].  The cache is only read: the new tokens' keys (rotated
+ * here) and values take part as they are, unquantised, and a rejected draft
+ * leaves no trace; simsd_kvq_append writes what is kept.
+ *   SIMSD_ORDER_PAIRED  simsd_verify_attn's layout: sequence b's n_b = 2 B_b
+ *                       new tokens are D_1..D_B, D~_1..D~_B, tokens k of
+ *                       both sections at position lens[b] + k - 1, under the
+ *                       temporal mask of tau; B_max <= 32
+ *   SIMSD_ORDER_NODES   n_b = B_b tokens, nodes of node_size tokens one after
+ *                       another, token k of every node at position lens[b] +
+ *                       k; a row sees the prompt and its own node (one node:
+ *                       a block that sees itself); B_max <= 64
+ *   SIMSD_ORDER_CAUSAL  n_b = B_b tokens at positions lens[b].., a row sees
+ *                       the prompt and the tokens up to itself (B_b = 1: a
+ *                       decode step); B_max <= 64
+ * With T = 2 total_B (paired) or total_B tokens:
+ *   q            device [T][Hq][hd], raw; row stride q_row
+ *   k_new, v_new device [T][Hkv][hd], raw; row strides k_row, v_row
+ *   out          device [T][Hq][hd], contiguous
+ *   block_table  device int32[batch][max_pages_per_seq]; entries
+ *                0..ceil(lens[b]/16)-1 are read
+ *   tau, lens, cu_B  as for simsd_verify_attn (tau: paired only)
+ * Strides are in elements, 0 selects contiguous rows; arrays and strides are
+ * multiples of 16 bytes (SIMSD_ERR_ALIGN).  The prompt's values in slots at
+ * and past lens[b] are never used.  bf16: scores from the codes themselves,
+ * a query row split into two e4m3 parts (2^-8 of a value, as rounding it to
+ * bf16) on the tensor cores.  fp32: fp32 arithmetic throughout.
+ * A sequence whose device arrays are out of range (cu_B, B_b outside
+ * 1..B_max, lens[b] outside 0..16 max_pages_per_seq, n_b not a multiple of
+ * node_size) sets the bad-input bit and its rows of out are not written; a
+ * page id outside the cache sets it too, and that page counts as absent.
+ * Limits: Hq % Hkv == 0, head_dim 64 or 128.  The workspace size follows the
+ * key-split plan (the current device's SM count).
+ * ---------------------------------------------------------------------- */
+typedef enum {
+  SIMSD_ORDER_PAIRED = 0,
+  SIMSD_ORDER_NODES = 1,
+  SIMSD_ORDER_CAUSAL = 2
+} simsd_order;
+
+typedef struct {
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;           /* 64 or 128                                  */
+  int32_t page_size;          /* 16                                         */
+  int32_t num_pages;
+  int32_t max_pages_per_seq;
+  int32_t total_B;            /* sum_b B_b (host copy)                      */
+  int32_t B_max;              /* max_b B_b (host copy)                      */
+  simsd_dtype dtype;          /* of q, k_new, v_new, out                    */
+  simsd_order order;
+  int32_t node_size;          /* SIMSD_ORDER_NODES: >= 1; otherwise 0       */
+  simsd_rope_spec rope;
+  float sm_scale;             /* finite, > 0                                */
+  int32_t wait_polls;         /* as in simsd_verify_desc                    */
+  int64_t q_row, k_row, v_row;
+  const void *q;
+  const void *k_cache;
+  const void *v_cache;
+  const uint8_t *k_scale;
+  const uint8_t *v_scale;
+  const int32_t *block_table;
+  const void *k_new;
+  const void *v_new;
+  const int32_t *tau;
+  const int32_t *lens;
+  const int32_t *cu_B;
+  void *out;
+  void *workspace;            /* device, 256-byte aligned                   */
+  size_t workspace_bytes;
+} simsd_kvq_verify_desc;
+
+size_t simsd_kvq_verify_workspace_size(const simsd_kvq_verify_desc *d);
+simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream);
+
+/* ------------------------------------------------------------------------
  * simsd_read_status -- synchronise `stream`, copy the device status word of
  * a workspace used by simsd_verify_attn / simsd_accept to *word_out (bit 0:
  * a bounded wait ran out) and clear it, together with the chunk pass's

@@ -7,10 +7,12 @@ libsimsd.so behind the C ABI in include/simsd.h.  ``binding`` marshals torch
 tensors into that ABI; ``staging`` moves host arrays into the device layouts
 the ABI expects.  There is no CPU fallback.
 """
-from .binding import (SimsdError, accept, accept_workspace_size, layout, lib,
-                      prompt_append, read_status, status_string, verify_attn,
-                      verify_workspace_size)
+from .binding import (SIMSD_ORDER_CAUSAL, SIMSD_ORDER_NODES, SIMSD_ORDER_PAIRED, SimsdError, accept,
+                      accept_workspace_size, kvq_append, kvq_verify, kvq_verify_workspace_size,
+                      layout, lib, page_map, page_map_workspace_size, prompt_append, read_status,
+                      rope, rope_spec, status_string, verify_attn, verify_workspace_size)
 
-__all__ = ["SimsdError", "accept", "accept_workspace_size", "layout", "lib",
-           "prompt_append", "read_status", "status_string", "verify_attn",
-           "verify_workspace_size"]
+__all__ = ["SIMSD_ORDER_CAUSAL", "SIMSD_ORDER_NODES", "SIMSD_ORDER_PAIRED", "SimsdError", "accept",
+           "accept_workspace_size", "kvq_append", "kvq_verify", "kvq_verify_workspace_size",
+           "layout", "lib", "page_map", "page_map_workspace_size", "prompt_append", "read_status",
+           "rope", "rope_spec", "status_string", "verify_attn", "verify_workspace_size"]

@@ -16,11 +16,15 @@ LIB_PATH = os.path.join(HERE, "libsimsd.so")
 
 SIMSD_F32, SIMSD_BF16 = 0, 1
 SIMSD_ACCEPT_SAMPLE, SIMSD_ACCEPT_GREEDY, SIMSD_ACCEPT_MATCH = 0, 1, 2
+SIMSD_ROPE_HALF, SIMSD_ROPE_INTERLEAVED = 0, 1
+SIMSD_ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
+SIMSD_ORDER_PAIRED, SIMSD_ORDER_NODES, SIMSD_ORDER_CAUSAL = 0, 1, 2
 STATUS = {0: "SIMSD_OK", 1: "SIMSD_ERR_NULL", 2: "SIMSD_ERR_SHAPE",
           3: "SIMSD_ERR_TAU", 4: "SIMSD_ERR_DTYPE", 5: "SIMSD_ERR_WORKSPACE",
           6: "SIMSD_ERR_CUDA", 7: "SIMSD_ERR_TIMEOUT", 8: "SIMSD_ERR_ALIGN"}
 
 _i32, _f32, _vp, _sz = ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 
 class VerifyDesc(ctypes.Structure):
@@ -64,6 +68,49 @@ class CommitDesc(ctypes.Structure):
                 ("tau", _vp), ("n_accept", _vp), ("token", _vp), ("pos", _vp),
                 ("tokens", _vp), ("decided", _vp), ("lens", _vp), ("done", _vp),
                 ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class RopeSpec(ctypes.Structure):
+    _fields_ = [("base", _f32), ("rotary_dim", _i32), ("style", ctypes.c_int),
+                ("scaling", ctypes.c_int), ("factor", _f32), ("original_len", _i32),
+                ("fast", _f32), ("slow", _f32), ("attn_factor", _f32)]
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("num_heads0", _i32), ("num_heads1", _i32), ("head_dim", _i32),
+                ("dtype", ctypes.c_int), ("inverse", _i32), ("rope", RopeSpec), ("positions", _vp),
+                ("x0", _vp), ("y0", _vp), ("x1", _vp), ("y1", _vp),
+                ("x0_row", _i64), ("x0_head", _i64), ("y0_row", _i64), ("y0_head", _i64),
+                ("x1_row", _i64), ("x1_head", _i64), ("y1_row", _i64), ("y1_head", _i64)]
+
+
+class PageMapDesc(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("page_size", _i32), ("num_pages", _i32),
+                ("max_pages_per_seq", _i32), ("total_n", _i32), ("lens", _vp), ("cu_n", _vp),
+                ("held", _vp), ("queue", _vp), ("free_pages", _vp), ("block_table", _vp),
+                ("held_out", _vp), ("queue_out", _vp), ("served", _vp), ("slots", _vp),
+                ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class KvqAppendDesc(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("page_size", _i32),
+                ("num_pages", _i32), ("max_pages_per_seq", _i32), ("total_n", _i32),
+                ("dtype", ctypes.c_int), ("rope", RopeSpec), ("k_row", _i64), ("v_row", _i64),
+                ("k", _vp), ("v", _vp), ("start", _vp), ("cu_n", _vp), ("take", _vp),
+                ("k_cache", _vp), ("v_cache", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("block_table", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class KvqVerifyDesc(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32),
+                ("head_dim", _i32), ("page_size", _i32), ("num_pages", _i32),
+                ("max_pages_per_seq", _i32), ("total_B", _i32), ("B_max", _i32),
+                ("dtype", ctypes.c_int), ("order", ctypes.c_int), ("node_size", _i32),
+                ("rope", RopeSpec), ("sm_scale", _f32), ("wait_polls", _i32),
+                ("q_row", _i64), ("k_row", _i64), ("v_row", _i64), ("q", _vp), ("k_cache", _vp),
+                ("v_cache", _vp), ("k_scale", _vp), ("v_scale", _vp), ("block_table", _vp),
+                ("k_new", _vp), ("v_new", _vp), ("tau", _vp), ("lens", _vp), ("cu_B", _vp),
+                ("out", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
 
 
 class SimsdError(RuntimeError):
@@ -111,6 +158,13 @@ def lib():
         L.simsd_commit_workspace_size.argtypes = [ctypes.POINTER(CommitDesc)]
         L.simsd_commit.restype = ctypes.c_int
         L.simsd_commit.argtypes = [ctypes.POINTER(CommitDesc), _vp]
+        for name, desc in (("rope", RopeDesc), ("page_map", PageMapDesc),
+                           ("kvq_append", KvqAppendDesc), ("kvq_verify", KvqVerifyDesc)):
+            f = getattr(L, "simsd_" + name)
+            f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(desc), _vp]
+            if name in ("page_map", "kvq_verify"):
+                f = getattr(L, "simsd_%s_workspace_size" % name)
+                f.restype, f.argtypes = _sz, [ctypes.POINTER(desc)]
         L.simsd_read_status.restype = ctypes.c_int
         L.simsd_read_status.argtypes = [_vp, _vp, ctypes.POINTER(ctypes.c_uint32)]
         _LIB = L
@@ -346,6 +400,203 @@ def commit(cu_B, tau, n_accept, token, pos, tokens, decided, lens, done, workspa
     d.tokens, d.decided, d.lens, d.done = _ptr(tokens), _ptr(decided), _ptr(lens), _ptr(done)
     d.workspace, d.workspace_bytes = _status_ws(workspace)
     _check(lib().simsd_commit(ctypes.byref(d), _stream(stream)), "simsd_commit")
+
+
+def rope_spec(base=1.0e4, rotary_dim=0, interleaved=False, scaling="plain", factor=1.0,
+              original_len=0, fast=32.0, slow=1.0, attn_factor=0.0):
+    """A simsd_rope_spec; scaling: plain, linear, ntk, yarn or banded."""
+    if scaling not in SIMSD_ROPE_SCALING:
+        raise ValueError("unknown rotary scaling %r" % (scaling,))
+    return RopeSpec(base, rotary_dim, SIMSD_ROPE_INTERLEAVED if interleaved else SIMSD_ROPE_HALF,
+                    SIMSD_ROPE_SCALING[scaling], factor, original_len, fast, slow, attn_factor)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _heads_of(t, like, what):
+    """(row stride, head stride) of a [rows, heads, hd] tensor whose heads are contiguous."""
+    if t.dim() != 3 or t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]:
+        raise ValueError("%s: expected [rows, heads, head_dim] of one dtype" % what)
+    if t.stride(2) != 1:
+        raise ValueError("%s: a head's elements must be contiguous" % what)
+    return t.stride(0), t.stride(1)
+
+
+def _row_stride(t, what):
+    """Row stride of a [rows, heads, hd] tensor whose rows are contiguous."""
+    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError("%s: expected [rows, heads, head_dim] with contiguous rows" % what)
+    if t.stride(0) == 0 and t.shape[0] > 1:      # 0 means contiguous rows to the ABI
+        raise ValueError("%s: rows that share memory" % what)
+    return t.stride(0)
+
+
+def _on_current_device(*tensors):
+    """Every tensor (None passes) lies on the current CUDA device, where the call runs."""
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("a tensor is on %s, not on the current CUDA device" % t.device)
+
+
+def _same_dtype(like, **tensors):
+    for name, t in tensors.items():
+        if t.dtype != like.dtype:
+            raise TypeError("%s is %s, not %s" % (name, t.dtype, like.dtype))
+
+
+def _ints(dtype, **tensors):
+    """Index arrays: contiguous tensors of the ABI's integer type (None passes)."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if t.dtype != dtype:
+            raise TypeError("%s is %s, not %s" % (name, t.dtype, dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s is not contiguous" % name)
+
+
+def _codes(**tensors):
+    """8-bit arrays of the cache: contiguous, one byte an element."""
+    for name, t in tensors.items():
+        if t.element_size() != 1:
+            raise TypeError("%s is %s, not an 8-bit type" % (name, t.dtype))
+        if not t.is_contiguous():
+            raise ValueError("%s is not contiguous" % name)
+
+
+def rope(x, positions, spec, out, x2=None, out2=None, inverse=False, stream=None):
+    """simsd_rope: x [rows, heads, hd] (any row and head strides) rotated into
+    out, and x2 into out2 (other head count, same rows) in the same launch.
+    out may be x.  positions int32 [rows]; inverse turns back (the gradient)."""
+    if (x2 is None) != (out2 is None):
+        raise ValueError("x2 and out2 come together")
+    _ints(torch.int32, positions=positions)
+    if positions.shape[0] != x.shape[0]:
+        raise ValueError("positions: one for each row of x")
+    if out.shape != x.shape or (x2 is not None and out2.shape != x2.shape):
+        raise ValueError("out: shape of x")
+    h2, s2, o2 = (0, (0, 0), (0, 0)) if x2 is None else (
+        x2.shape[1], _heads_of(x2, x, "x2"), _heads_of(out2, x, "out2"))
+    _on_current_device(x, positions, out, x2, out2)
+    d = RopeDesc(x.shape[0], x.shape[1], h2, x.shape[2], _dtype_code(x), int(bool(inverse)), spec,
+                 positions.data_ptr(), x.data_ptr(), out.data_ptr(), _addr(x2), _addr(out2),
+                 *_heads_of(x, x, "x"), *_heads_of(out, x, "out"), *s2, *o2)
+    _check(lib().simsd_rope(ctypes.byref(d), _stream(stream)), "simsd_rope")
+
+
+def page_map_workspace_size(lens, block_table, free_pages, total_n):
+    d = PageMapDesc(lens.shape[0], 16, free_pages.shape[0], block_table.shape[1], int(total_n))
+    n = lib().simsd_page_map_workspace_size(ctypes.byref(d))
+    if n == 0:
+        raise SimsdError(2, "simsd_page_map_workspace_size")
+    return int(n)
+
+
+def page_map(lens, cu_n, held, queue, free_pages, block_table, held_out, queue_out, served, slots,
+             workspace, total_n, stream=None):
+    """simsd_page_map: block_table and free_pages in place, held/queue to
+    held_out/queue_out (may be the same tensors); cu_n and slots may be None."""
+    _ints(torch.int32, lens=lens, cu_n=cu_n, held=held, queue=queue, free_pages=free_pages,
+          block_table=block_table, held_out=held_out, queue_out=queue_out, served=served)
+    _ints(torch.int64, slots=slots)
+    batch = lens.shape[0]
+    if (held.shape[0] != batch or held_out.shape[0] != batch or served.shape[0] != batch or
+            block_table.shape[0] != batch or (cu_n is not None and cu_n.shape[0] != batch + 1) or
+            queue.numel() != 2 or queue_out.numel() != 2 or
+            (slots is not None and slots.shape[0] < total_n)):
+        raise ValueError("page_map: sizes of the arrays disagree")
+    _on_current_device(lens, cu_n, held, queue, free_pages, block_table, held_out, queue_out, served,
+                       slots, workspace)
+    d = PageMapDesc(batch, 16, free_pages.shape[0], block_table.shape[1], int(total_n),
+                    lens.data_ptr(), _addr(cu_n), held.data_ptr(), queue.data_ptr(),
+                    free_pages.data_ptr(), block_table.data_ptr(), held_out.data_ptr(),
+                    queue_out.data_ptr(), served.data_ptr(), _addr(slots), *_ws(workspace))
+    _check(lib().simsd_page_map(ctypes.byref(d), _stream(stream)), "simsd_page_map")
+
+
+def _ws(workspace):
+    return (None, 0) if workspace is None else (
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def kvq_append(k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_table, workspace, spec,
+               take=None, stream=None):
+    """simsd_kvq_append: k (rotated by spec) and v [total_n, Hkv, hd] into the
+    e4m3 caches [num_pages, Hkv, 16, hd] with e8m0 scales [num_pages, Hkv]."""
+    _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table, take=take)
+    _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    _same_dtype(k, v=v)
+    batch, hkv = start.shape[0], k.shape[1]
+    if (v.shape != k.shape or k_cache.shape != v_cache.shape or k_cache.shape[1] != hkv or
+            k_cache.shape[3] != k.shape[2] or tuple(k_scale.shape) != tuple(k_cache.shape[:2]) or
+            tuple(v_scale.shape) != tuple(k_cache.shape[:2]) or cu_n.shape[0] != batch + 1 or
+            block_table.shape[0] != batch or (take is not None and take.shape[0] != batch)):
+        raise ValueError("kvq_append: sizes of the arrays disagree")
+    _on_current_device(k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_table, workspace,
+                       take)
+    d = KvqAppendDesc(batch, hkv, k.shape[2], k_cache.shape[2], k_cache.shape[0],
+                      block_table.shape[1], k.shape[0], _dtype_code(k), spec,
+                      _row_stride(k, "k"), _row_stride(v, "v"), k.data_ptr(), v.data_ptr(),
+                      start.data_ptr(), cu_n.data_ptr(), _addr(take), k_cache.data_ptr(),
+                      v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                      block_table.data_ptr(), *_ws(workspace))
+    _check(lib().simsd_kvq_append(ctypes.byref(d), _stream(stream)), "simsd_kvq_append")
+
+
+def _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
+                     cu_B, out, workspace, total_B, B_max, spec, sm_scale, order, node_size,
+                     wait_polls=0):
+    _ints(torch.int32, block_table=block_table, tau=tau, lens=lens, cu_B=cu_B)
+    _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    _same_dtype(q, k_new=k_new, v_new=v_new, out=out)
+    batch, hkv, hd = lens.shape[0], k_new.shape[1], q.shape[2]
+    rows = int(total_B) * (2 if order == SIMSD_ORDER_PAIRED else 1)
+    if (out.shape != q.shape or q.shape[0] < rows or k_new.shape[0] < rows or
+            v_new.shape != k_new.shape or k_new.shape[2] != hd or k_cache.shape != v_cache.shape or
+            k_cache.shape[1] != hkv or k_cache.shape[3] != hd or
+            tuple(k_scale.shape) != tuple(k_cache.shape[:2]) or
+            tuple(v_scale.shape) != tuple(k_cache.shape[:2]) or cu_B.shape[0] != batch + 1 or
+            block_table.shape[0] != batch or
+            (order == SIMSD_ORDER_PAIRED and tau is not None and tau.shape[0] < total_B)):
+        raise ValueError("kvq_verify: sizes of the arrays disagree")
+    if not out.is_contiguous():
+        raise ValueError("out is not contiguous")
+    _on_current_device(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens, cu_B,
+                       out, workspace)
+    return KvqVerifyDesc(batch, q.shape[1], hkv, hd, k_cache.shape[2], k_cache.shape[0],
+                         block_table.shape[1], int(total_B), int(B_max), _dtype_code(q), int(order),
+                         int(node_size), spec, float(sm_scale), int(wait_polls),
+                         _row_stride(q, "q"), _row_stride(k_new, "k_new"),
+                         _row_stride(v_new, "v_new"), q.data_ptr(), k_cache.data_ptr(),
+                         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                         block_table.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _addr(tau),
+                         lens.data_ptr(), cu_B.data_ptr(), out.data_ptr(), *_ws(workspace))
+
+
+def kvq_verify_workspace_size(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau,
+                              lens, cu_B, out, total_B, B_max, spec, sm_scale,
+                              order=SIMSD_ORDER_PAIRED, node_size=0):
+    d = _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
+                         cu_B, out, None, total_B, B_max, spec, sm_scale, order, node_size)
+    n = lib().simsd_kvq_verify_workspace_size(ctypes.byref(d))
+    if n == 0:
+        raise SimsdError(2, "simsd_kvq_verify_workspace_size")
+    return int(n)
+
+
+def kvq_verify(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens, cu_B, out,
+               workspace, total_B, B_max, spec, sm_scale, order=SIMSD_ORDER_PAIRED, node_size=0,
+               wait_polls=0, stream=None):
+    """simsd_kvq_verify: attention of the new tokens over the 8-bit prompt
+    cache and themselves; spec from rope_spec; tau may be None unless the
+    order is SIMSD_ORDER_PAIRED."""
+    d = _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
+                         cu_B, out, workspace, total_B, B_max, spec, sm_scale, order, node_size,
+                         wait_polls)
+    _check(lib().simsd_kvq_verify(ctypes.byref(d), _stream(stream)), "simsd_kvq_verify")
 
 
 def read_status(workspace, stream=None):

@@ -1,0 +1,464 @@
+// kvq_attn.cu -- simsd_kvq_verify: the host side (checks, key-split plan), the
+// CUDA-core attention kernel and the merge of key splits.
+//
+// For a query row r (new token and query head) with visible keys j,
+//   out = sum_j 2^(s_j - m) v_j / sum_j 2^(s_j - m),  s_j = scale q_r . k_j
+// (scale holds log2 e), the keys being the prompt's e4m3 codes times their
+// page's scale and the new tokens' own rotated keys; a running maximum m and
+// sum per row, one pass over the keys.
+//
+// The CUDA-core kernel (fp32 data: fp32 arithmetic throughout) takes 16 rows
+// of a (sequence, KV head) against tiles of 64 keys that are decoded into
+// shared memory once for all rows; a warp owns four rows, its lanes two keys
+// each for the scores and four columns each for the values.
+#include <math.h>
+#include <string.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "kvq.cuh"
+#include "kvq_attn.cuh"
+#include "vec.cuh"
+
+namespace simsd {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kRows = 16;                // rows of a CTA
+constexpr int kRowsPerWarp = 4;
+constexpr int kTile = 64;                // keys of a tile = the most new tokens
+static_assert(kTile == kMaxNew, "the new tokens are one tile");
+
+template <int HD>
+struct SimtSmem {
+  static constexpr int kLd = HD + 4;     // row stride of q and k: lanes on different banks
+  float q[kRows][kLd];
+  float k[kTile][kLd];
+  float v[kTile][HD];                    // also the angles of the new tokens' positions
+  float p[kRows][kTile];
+};
+
+// Element e of a rotated row x with angles cs.
+template <typename T>
+__device__ __forceinline__ float rotated(const RopePlan &p, const float2 *cs, const T *x, int e) {
+  const float u = Elem<T>::load(x + e);
+  if (e >= 2 * p.half) return u;
+  const bool low = p.interleaved ? !(e & 1) : e < p.half;
+  const int partner = p.interleaved ? (e ^ 1) : (low ? e + p.half : e - p.half);
+  const float2 w = cs[p.interleaved ? e >> 1 : (low ? e : e - p.half)];
+  const float y = Elem<T>::load(x + partner);
+  return low ? u * w.x - y * w.y : u * w.x + y * w.y;
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kThreads)
+kvq_simt_kernel(const __grid_constant__ KvqParams a) {
+  constexpr int PER = HD / 32;           // columns of a lane
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SimtSmem<HD> &s = *reinterpret_cast<SimtSmem<HD> *>(smem_raw);
+  __shared__ int tau_s[kMaxB];
+  grid_dep_launch();
+  const KvqWork w = kvq_work(a);
+  if (!w.ok) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = min(kRows, w.M - w.row0);
+  if (a.order == SIMSD_ORDER_PAIRED && threadIdx.x < w.B) tau_s[threadIdx.x] = __ldg(a.tau + w.c0 + threadIdx.x);
+  const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
+  const int half = a.plan.half;
+  float2 *cs = reinterpret_cast<float2 *>(&s.v[0][0]);   // [kMaxNew][HD / 2]
+  for (int e = threadIdx.x; e < npos * half; e += kThreads)
+    cs[(e / half) * (HD / 2) + e % half] = rope_plan_cs(a.plan, e % half, w.P + e / half);
+  __syncthreads();
+  const int64_t t0 = (int64_t)a.per * w.c0;              // first new token's row
+  for (int e = threadIdx.x; e < kRows * HD; e += kThreads) {
+    const int r = e / HD, d = e % HD;
+    float x = 0.f;
+    if (r < rows) {
+      const int tok = (w.row0 + r) / a.G, head = w.kvh * a.G + (w.row0 + r) % a.G;
+      x = rotated(a.plan, cs + kvq_offset(a, w.B, tok) * (HD / 2),
+                  (const T *)a.q + (t0 + tok) * a.q_row + head * HD, d) * a.scale;
+    }
+    s.q[r][d] = x;
+  }
+  if (w.first) {
+    for (int e = threadIdx.x; e < kTile * HD; e += kThreads) {
+      const int j = e / HD, d = e % HD;
+      s.k[j][d] = j < w.n ? rotated(a.plan, cs + kvq_offset(a, w.B, j) * (HD / 2),
+                                    (const T *)a.k_new + (t0 + j) * a.k_row + w.kvh * HD, d) : 0.f;
+    }
+    __syncthreads();                                     // the angles are read
+    for (int e = threadIdx.x; e < kTile * HD; e += kThreads) {
+      const int j = e / HD, d = e % HD;
+      s.v[j][d] = j < w.n ? Elem<T>::load((const T *)a.v_new + (t0 + j) * a.v_row + w.kvh * HD + d) : 0.f;
+    }
+  }
+  uint64_t newvis[kRowsPerWarp];
+  const int r0 = warp * kRowsPerWarp;
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i)
+    newvis[i] = r0 + i < rows ? kvq_visible(a, w.B, tau_s, (w.row0 + r0 + i) / a.G) : 0ull;
+  float m[kRowsPerWarp], l[kRowsPerWarp], o[kRowsPerWarp][PER];
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < PER; ++c) o[i][c] = 0.f;
+  }
+  const int32_t *bt = a.block_table + (int64_t)w.b * a.max_pages;
+  for (int base = w.first ? w.k_begin - kTile : w.k_begin; base < w.k_end; base += kTile) {
+    const bool fresh = base < w.k_begin;                 // the new tokens' tile
+    uint64_t there = ~0ull;                              // keys of the tile that exist
+    if (!fresh) {
+      __syncthreads();                                   // the last tile is read
+      there = kvq_low_bits(w.k_end - base);
+      constexpr int CH = HD / 16;                        // 16-byte chunks of a row
+      for (int e = threadIdx.x; e < 2 * kTile * CH; e += kThreads) {
+        const bool is_v = e >= kTile * CH;
+        const int j = (is_v ? e - kTile * CH : e) / CH, c = e % CH, key = base + j;
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        float sc = 0.f;
+        if (key < w.k_end) {
+          const int page = __ldg(bt + key / kPage);
+          if (page >= 0 && page < a.num_pages) {
+            const int64_t at = (int64_t)page * a.Hkv + w.kvh;
+            raw = __ldg(reinterpret_cast<const uint4 *>((is_v ? a.v_cache : a.k_cache) + (at * kPage + key % kPage) * HD) + c);
+            sc = scale_value(__ldg((is_v ? a.v_scale : a.k_scale) + at));
+          } else {
+            raise_status(a.status, kStatusBadInput);
+          }
+        }
+        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+        float *dst = is_v ? &s.v[j][c * 16] : &s.k[j][c * 16];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = unpack_e4m3x2(u[i] & 0xffffu), g = unpack_e4m3x2(u[i] >> 16);
+          reinterpret_cast<float4 *>(dst)[i] = make_float4(f.x * sc, f.y * sc, g.x * sc, g.y * sc);
+        }
+      }
+      // keys of pages outside the cache count as absent
+      for (int q = 0; q < kTile / kPage; ++q) {
+        const int key = base + q * kPage;
+        const int page = key < w.k_end ? __ldg(bt + key / kPage) : 0;
+        if (page < 0 || page >= a.num_pages) there &= ~(0xffffull << (q * kPage));
+      }
+    }
+    __syncthreads();
+    // scores of the warp's rows: keys lane and lane + 32
+    float acc[kRowsPerWarp][2];
+#pragma unroll
+    for (int i = 0; i < kRowsPerWarp; ++i) acc[i][0] = acc[i][1] = 0.f;
+#pragma unroll 8
+    for (int d = 0; d < HD; d += 4) {
+      const float4 k0 = *reinterpret_cast<const float4 *>(&s.k[lane][d]);
+      const float4 k1 = *reinterpret_cast<const float4 *>(&s.k[lane + 32][d]);
+#pragma unroll
+      for (int i = 0; i < kRowsPerWarp; ++i) {
+        const float4 q = *reinterpret_cast<const float4 *>(&s.q[r0 + i][d]);
+        acc[i][0] = fmaf(q.x, k0.x, fmaf(q.y, k0.y, fmaf(q.z, k0.z, fmaf(q.w, k0.w, acc[i][0]))));
+        acc[i][1] = fmaf(q.x, k1.x, fmaf(q.y, k1.y, fmaf(q.z, k1.z, fmaf(q.w, k1.w, acc[i][1]))));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRowsPerWarp; ++i) {
+      const uint64_t vis = fresh ? newvis[i] : there;
+      const float s0 = (vis >> lane) & 1ull ? acc[i][0] : -INFINITY;
+      const float s1 = (vis >> (lane + 32)) & 1ull ? acc[i][1] : -INFINITY;
+      float mx = fmaxf(s0, s1);
+#pragma unroll
+      for (int t = 16; t > 0; t >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, t));
+      const float m_new = fmaxf(m[i], mx), mu = m_new == -INFINITY ? 0.f : m_new;
+      const float alpha = exp2f(m[i] - mu);              // m = -inf: 0
+      const float p0 = exp2f(s0 - mu), p1 = exp2f(s1 - mu);
+      float ps = p0 + p1;
+#pragma unroll
+      for (int t = 16; t > 0; t >>= 1) ps += __shfl_xor_sync(0xffffffffu, ps, t);
+      l[i] = l[i] * alpha + ps;
+      m[i] = m_new;
+#pragma unroll
+      for (int c = 0; c < PER; ++c) o[i][c] *= alpha;
+      s.p[r0 + i][lane] = p0;
+      s.p[r0 + i][lane + 32] = p1;
+    }
+    __syncwarp();
+    // values: columns lane * PER ..
+#pragma unroll 2
+    for (int j = 0; j < kTile; j += 4) {
+      float4 p[kRowsPerWarp];
+#pragma unroll
+      for (int i = 0; i < kRowsPerWarp; ++i) p[i] = *reinterpret_cast<const float4 *>(&s.p[r0 + i][j]);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        float v[PER];
+#pragma unroll
+        for (int c = 0; c < PER; ++c) v[c] = s.v[j + jj][lane * PER + c];
+#pragma unroll
+        for (int i = 0; i < kRowsPerWarp; ++i) {
+          const float pj = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
+#pragma unroll
+          for (int c = 0; c < PER; ++c) o[i][c] = fmaf(pj, v[c], o[i][c]);
+        }
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < kRowsPerWarp; ++i) {
+    if (r0 + i >= rows) continue;
+    const int grow = w.row0 + r0 + i;
+    const int64_t row = (t0 + grow / a.G) * a.Hq + w.kvh * a.G + grow % a.G;
+    if (w.n_splits == 1) {
+      const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+#pragma unroll
+      for (int c = 0; c < PER; ++c) Elem<T>::store((T *)a.out + row * HD + lane * PER + c, o[i][c] * inv);
+    } else {
+      const int64_t prow = (int64_t)w.split * a.T * a.Hq + row;
+#pragma unroll
+      for (int c = 0; c < PER; ++c) a.o_part[prow * HD + lane * PER + c] = o[i][c];
+      if (lane == 0) a.ml_part[prow] = make_float2(m[i], l[i]);
+    }
+  }
+}
+
+// Merge: out = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s, a warp per
+// (token, head) row of a split unit.  The row's sequence is looked up before
+// the wait for the attention kernel (its arrays are inputs of the call).
+constexpr int kMergeThreads = 256;
+constexpr int kMergeRows = kMergeThreads / 32;
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kMergeThreads)
+kvq_merge_kernel(const __grid_constant__ KvqParams a, int tok0) {
+  constexpr int PER = HD / 32;
+  const int tok_row = tok0 + (int)blockIdx.x, lane = threadIdx.x & 31;
+  const int hq = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
+  const int b = find_seq(a.cu_B, a.batch, tok_row / a.per);
+  const int c0 = __ldg(a.cu_B + b), B = __ldg(a.cu_B + b + 1) - c0, P = __ldg(a.lens + b);
+  grid_dep_wait();
+  const int tok = tok_row - a.per * c0;
+  if (hq >= a.Hq || kvq_bad(a, c0, B, P) || tok < 0 || tok >= a.per * B) return;
+  const int g = hq / a.G;
+  const int rtile = (tok * a.G + hq % a.G) / a.rows_per_tile;
+  const int unit = b * a.Hkv * a.row_tiles + rtile * a.Hkv + g;
+  const int ns = unit >= a.tail_from ? (P + a.chunk_tail - 1) / a.chunk_tail : 1;
+  if (ns <= 1) return;
+  const int64_t row = (int64_t)tok_row * a.Hq + hq, step = (int64_t)a.T * a.Hq;
+  float m = -INFINITY;
+  for (int s = lane; s < ns; s += 32) m = fmaxf(m, __ldcg(a.ml_part + row + s * step).x);
+#pragma unroll
+  for (int t = 16; t > 0; t >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, t));
+  const float mu = m == -INFINITY ? 0.f : m;
+  float den = 0.f, o[PER];
+#pragma unroll
+  for (int c = 0; c < PER; ++c) o[c] = 0.f;
+#pragma unroll 4
+  for (int s = 0; s < ns; ++s) {
+    const float2 ml = __ldcg(a.ml_part + row + s * step);
+    const float wgt = exp2f(ml.x - mu);
+    den = fmaf(wgt, ml.y, den);
+    const float *src = a.o_part + (row + s * step) * HD + lane * PER;
+    float v[PER];
+    if constexpr (PER == 4) {
+      const float4 x = __ldcg(reinterpret_cast<const float4 *>(src));
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    } else {
+      const float2 x = __ldcg(reinterpret_cast<const float2 *>(src));
+      v[0] = x.x; v[1] = x.y;
+    }
+#pragma unroll
+    for (int c = 0; c < PER; ++c) o[c] = fmaf(wgt, v[c], o[c]);
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  T *dst = (T *)a.out + row * HD + lane * PER;
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int c = 0; c < PER; c += 2)
+      reinterpret_cast<uint32_t *>(dst)[c / 2] = pack_bf16x2(o[c] * inv, o[c + 1] * inv);
+  } else {
+#pragma unroll
+    for (int c = 0; c < PER; ++c) dst[c] = o[c] * inv;
+  }
+}
+
+template <typename T, int HD>
+cudaError_t launch_simt_t(const KvqPlan &p, const KvqParams &a, cudaStream_t stream) {
+  auto kern = kvq_simt_kernel<T, HD>;
+  const int smem = (int)sizeof(SimtSmem<HD>);
+  static std::atomic<uint64_t> configured{0};   // one bit per device
+  const int dev = current_device();
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0;
+  if (!bit || !(configured.load() & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  kern<<<p.grid, kThreads, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// Key splits: every unit alike where the table's width makes a unit long, or
+// only the units of the last partial wave (as simsd_verify_attn's plan).  In
+// block-times of 128 keys on an SM; a wave of n CTAs of `per` blocks costs
+// per * max(n / slots, kRho) plus a ramp, and splits the merge's reads.
+void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t slots, int max_n_tokens,
+                 KvqPlan *p) {
+  constexpr double kRho = 0.85, kRamp = 6.0;
+  const int64_t blocks = std::max<int64_t>(1, (max_keys + kBlockKeys - 1) / kBlockKeys);
+  const int64_t pairs = batch * units_per_seq;
+  int64_t splits = 1;
+  double best = 1e300;
+  for (int64_t s = 1; s <= blocks && s <= 64; ++s) {
+    const int64_t per = (blocks + s - 1) / s;
+    if (s > 1 && (blocks + per - 1) / per < s) continue;   // same split as a smaller s
+    const int64_t ctas = pairs * s, full = ctas / slots, rest = ctas % slots;
+    double cost = (double)full * ((double)per + kRamp);
+    if (rest > 0) cost += (double)per * std::max((double)rest / (double)slots, kRho) + kRamp;
+    if (s > 1) cost += 2.0 + 2.0 * (double)ctas / (double)slots;
+    if (cost < best - 1e-9) { best = cost; splits = s; }
+  }
+  const int64_t per = (blocks + splits - 1) / splits;
+  p->chunk_tail = (int)(per * kBlockKeys);
+  p->n_splits = (int)((blocks + per - 1) / per);
+  p->s_tail = p->n_splits;
+  p->tail_from = p->n_splits > 1 ? 0 : (int)pairs;
+  p->tail_first = 0;
+  p->grid = (int)(pairs * p->n_splits);
+  p->merge_tokens = p->T;
+  if (p->n_splits == 1 && pairs > slots && pairs % slots != 0) {
+    const int64_t W = pairs / slots, r = pairs - W * slots;
+    const int64_t s = std::min<int64_t>(slots / r, blocks);
+    if (s >= 2) {
+      const int64_t pt = (blocks + s - 1) / s;
+      const double whole = (double)(W + 1) * ((double)blocks + kRamp);
+      const double tail = (double)W * ((double)blocks + kRamp) + (double)pt + kRamp + 2.0 +
+                          2.0 * (double)(r * s) / (double)slots;
+      if (tail < whole - 1e-9) {
+        p->tail_from = (int)(W * slots);
+        p->tail_first = W <= 4;      // few full waves: the split units' SMs start offset
+        p->s_tail = (int)s;
+        p->chunk_tail = (int)(pt * kBlockKeys);
+        p->n_splits = (int)((blocks + pt - 1) / pt);
+        p->grid = (int)(W * slots + r * s);
+        const int64_t seqs = std::min<int64_t>(batch, (r + units_per_seq - 1) / units_per_seq + 1);
+        p->merge_tokens = std::min<int64_t>(p->T, seqs * max_n_tokens);
+      }
+    }
+  }
+}
+
+simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {
+  if (d == nullptr) return SIMSD_ERR_NULL;
+  if (d->dtype != SIMSD_F32 && d->dtype != SIMSD_BF16) return SIMSD_ERR_DTYPE;
+  const bool paired = d->order == SIMSD_ORDER_PAIRED;
+  if (d->batch < 1 || d->num_q_heads < 1 || d->num_kv_heads < 1 || d->num_q_heads % d->num_kv_heads != 0 ||
+      d->num_q_heads > 65535 || (d->head_dim != 64 && d->head_dim != 128) || d->page_size != kPageTokens ||
+      d->num_pages < 1 || d->max_pages_per_seq < 1 || d->max_pages_per_seq >= (1 << 26) ||
+      d->order < SIMSD_ORDER_PAIRED || d->order > SIMSD_ORDER_CAUSAL || d->B_max < 1 ||
+      d->B_max > (paired ? kMaxB : kMaxNew) || d->total_B < d->batch || d->total_B > (1 << 28) ||
+      (int64_t)d->total_B > (int64_t)d->batch * d->B_max || !(d->sm_scale > 0.0f) ||
+      !(d->sm_scale < INFINITY) || d->q_row < 0 || d->k_row < 0 || d->v_row < 0 ||
+      (d->order == SIMSD_ORDER_NODES ? d->node_size < 1 || d->node_size > kMaxNew : d->node_size != 0))
+    return SIMSD_ERR_SHAPE;
+  RopePlan rope;
+  const simsd_status st = make_rope_plan(d->rope, d->head_dim, &rope);
+  if (st != SIMSD_OK) return st;
+  memset(p, 0, sizeof(*p));
+  p->per = paired ? 2 : 1;
+  p->T = p->per * d->total_B;
+  p->G = d->num_q_heads / d->num_kv_heads;
+  p->esize = d->dtype == SIMSD_BF16 ? 2 : 4;
+  const int max_n = p->per * d->B_max;
+  p->rows_per_tile = kRows;
+  const int64_t max_rows = (int64_t)max_n * p->G;
+  p->row_tiles = (int)((max_rows + p->rows_per_tile - 1) / p->rows_per_tile);
+  const int64_t per_seq = (int64_t)d->num_kv_heads * p->row_tiles;
+  if (per_seq * d->batch * 64 >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
+  plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens, 2 * device_sm_count(), max_n, p);
+  size_t off = kAlign;
+  p->off_opart = p->off_ml = off;
+  if (p->n_splits > 1) {
+    const size_t rows = (size_t)p->n_splits * p->T * d->num_q_heads;
+    off = align_up(off + rows * d->head_dim * sizeof(float), kAlign);
+    p->off_ml = off;
+    off = align_up(off + rows * sizeof(float2), kAlign);
+  }
+  p->total = off;
+  return SIMSD_OK;
+}
+
+}  // namespace
+
+cudaError_t launch_kvq_simt(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
+                            cudaStream_t stream) {
+  if (d->dtype == SIMSD_BF16)
+    return d->head_dim == 128 ? launch_simt_t<__nv_bfloat16, 128>(p, a, stream)
+                              : launch_simt_t<__nv_bfloat16, 64>(p, a, stream);
+  return d->head_dim == 128 ? launch_simt_t<float, 128>(p, a, stream)
+                            : launch_simt_t<float, 64>(p, a, stream);
+}
+
+cudaError_t launch_kvq_merge(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
+                             cudaStream_t stream) {
+  const dim3 grid((unsigned)p.merge_tokens, (unsigned)((d->num_q_heads + kMergeRows - 1) / kMergeRows));
+  const dim3 block(kMergeThreads);
+  const int tok0 = (int)(p.T - p.merge_tokens);
+  if (d->dtype == SIMSD_BF16)
+    return d->head_dim == 128 ? launch_pdl(kvq_merge_kernel<__nv_bfloat16, 128>, grid, block, 0, stream, a, tok0)
+                              : launch_pdl(kvq_merge_kernel<__nv_bfloat16, 64>, grid, block, 0, stream, a, tok0);
+  return d->head_dim == 128 ? launch_pdl(kvq_merge_kernel<float, 128>, grid, block, 0, stream, a, tok0)
+                            : launch_pdl(kvq_merge_kernel<float, 64>, grid, block, 0, stream, a, tok0);
+}
+
+}  // namespace simsd
+
+using namespace simsd;
+
+extern "C" {
+
+size_t simsd_kvq_verify_workspace_size(const simsd_kvq_verify_desc *d) {
+  KvqPlan p;
+  return kvq_plan(d, &p) == SIMSD_OK ? p.total : 0;
+}
+
+simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream_ptr) {
+  KvqPlan p;
+  const simsd_status st = kvq_plan(d, &p);
+  if (st != SIMSD_OK) return st;
+  if (!d->q || !d->k_cache || !d->v_cache || !d->k_scale || !d->v_scale || !d->block_table || !d->k_new ||
+      !d->v_new || (d->order == SIMSD_ORDER_PAIRED && !d->tau) || !d->lens || !d->cu_B || !d->out)
+    return SIMSD_ERR_NULL;
+  KvqParams a;
+  (void)make_rope_plan(d->rope, d->head_dim, &a.plan);
+  a.q_row = d->q_row ? d->q_row : (int64_t)d->num_q_heads * d->head_dim;
+  a.k_row = d->k_row ? d->k_row : (int64_t)d->num_kv_heads * d->head_dim;
+  a.v_row = d->v_row ? d->v_row : (int64_t)d->num_kv_heads * d->head_dim;
+  const int es = (int)p.esize;
+  if (!aligned16(d->q) || !aligned16(d->k_cache) || !aligned16(d->v_cache) || !aligned16(d->k_new) ||
+      !aligned16(d->v_new) || !aligned16(d->out) || (a.q_row * es) % 16 != 0 || (a.k_row * es) % 16 != 0 ||
+      (a.v_row * es) % 16 != 0)
+    return SIMSD_ERR_ALIGN;
+  if (d->workspace == nullptr || ((uintptr_t)d->workspace % kAlign) != 0 || d->workspace_bytes < p.total)
+    return SIMSD_ERR_WORKSPACE;
+  char *ws = (char *)d->workspace;
+  a.q = d->q; a.k_new = d->k_new; a.v_new = d->v_new; a.out = d->out;
+  a.k_cache = (const uint8_t *)d->k_cache; a.v_cache = (const uint8_t *)d->v_cache;
+  a.k_scale = d->k_scale; a.v_scale = d->v_scale;
+  a.block_table = d->block_table; a.tau = d->tau; a.lens = d->lens; a.cu_B = d->cu_B;
+  a.o_part = (float *)(ws + p.off_opart);
+  a.ml_part = (float2 *)(ws + p.off_ml);
+  a.status = (uint32_t *)ws;
+  a.batch = d->batch; a.Hq = d->num_q_heads; a.Hkv = d->num_kv_heads; a.G = p.G; a.T = p.T;
+  a.total_B = d->total_B; a.B_max = d->B_max; a.order = d->order; a.node_size = d->node_size; a.per = p.per;
+  a.max_pages = d->max_pages_per_seq; a.num_pages = d->num_pages;
+  a.rows_per_tile = p.rows_per_tile; a.row_tiles = p.row_tiles;
+  a.tail_from = p.tail_from; a.s_tail = p.s_tail; a.chunk_tail = p.chunk_tail; a.tail_first = p.tail_first;
+  a.polls = wait_polls_of(d->wait_polls);
+  a.scale = d->sm_scale * 1.4426950408889634f;
+  cudaStream_t stream = (cudaStream_t)stream_ptr;
+  cudaError_t e = launch_kvq_simt(d, p, a, stream);
+  if (e == cudaSuccess && p.n_splits > 1) e = launch_kvq_merge(d, p, a, stream);
+  return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,120 @@
+// kvq_attn.cuh -- what the two kernels of simsd_kvq_verify (tensor cores for
+// bf16, CUDA cores for fp32) and their merge share.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "rope_spec.cuh"
+
+namespace simsd {
+
+constexpr int kMaxNew = 64;              // new tokens of a sequence
+
+// Units (sequence, KV head, row tile) run whole or in key splits, as in
+// VerifyPlan: the first tail_from whole, each later one in s_tail splits of
+// chunk_tail prompt keys.
+struct KvqPlan {
+  int T, per, G, rows_per_tile, row_tiles;
+  int n_splits, tail_from, s_tail, chunk_tail, tail_first, grid;
+  int64_t merge_tokens;                  // the merge's tokens are the last ones
+  size_t esize, off_opart, off_ml, total;
+};
+
+struct KvqParams {
+  RopePlan plan;
+  const void *q, *k_new, *v_new;
+  void *out;
+  const uint8_t *k_cache, *v_cache, *k_scale, *v_scale;
+  const int32_t *block_table, *tau, *lens, *cu_B;
+  float *o_part;                         // [n_splits][T][Hq][hd], unnormalised
+  float2 *ml_part;                       // [n_splits][T][Hq] (log2 reference, sum)
+  uint32_t *status;
+  int64_t q_row, k_row, v_row;
+  int batch, Hq, Hkv, G, T, total_B, B_max, order, node_size, per;
+  int max_pages, num_pages;
+  int rows_per_tile, row_tiles, tail_from, s_tail, chunk_tail, tail_first;
+  uint32_t polls;
+  float scale;                           // sm_scale * log2(e)
+};
+
+// The sequence, KV head, row tile and split of a CTA, and the keys it owns.
+struct KvqWork {
+  int b, kvh, rtile, split;
+  int c0, B, n, P, M, row0;              // first section entry, sections, new tokens, prompt, rows
+  int k_begin, k_end, n_splits;
+  bool first;                            // owns the new tokens' keys
+  bool ok;                               // there is something to do
+};
+
+__device__ __forceinline__ bool kvq_bad(const KvqParams &a, int c0, int B, int P) {
+  return B < 1 || B > a.B_max || c0 < 0 || c0 > a.total_B - B || P < 0 ||
+         (int64_t)P > (int64_t)a.max_pages * kPage ||
+         (a.order == SIMSD_ORDER_NODES && B % a.node_size != 0);
+}
+
+__device__ __forceinline__ KvqWork kvq_work(const KvqParams &a) {
+  KvqWork w;
+  const int ci = blockIdx.x;
+  const int n_tail = (int)gridDim.x - a.tail_from;   // CTAs of split units
+  const bool tail = a.tail_first ? ci < n_tail : ci >= a.tail_from;
+  const int ti = a.tail_first ? ci : ci - a.tail_from;
+  const int unit = tail ? a.tail_from + ti / a.s_tail : (a.tail_first ? ci - n_tail : ci);
+  const int chunk = tail ? a.chunk_tail : a.max_pages * kPage;
+  const int per_seq = a.Hkv * a.row_tiles;
+  w.split = tail ? ti % a.s_tail : 0;
+  w.b = unit / per_seq;
+  w.kvh = unit % per_seq % a.Hkv;
+  w.rtile = unit % per_seq / a.Hkv;
+  w.c0 = __ldg(a.cu_B + w.b);
+  w.B = __ldg(a.cu_B + w.b + 1) - w.c0;
+  w.P = __ldg(a.lens + w.b);
+  w.ok = false;
+  if (kvq_bad(a, w.c0, w.B, w.P)) {
+    if (threadIdx.x == 0 && w.split == 0 && unit % per_seq == 0) raise_status(a.status, kStatusBadInput);
+    return w;
+  }
+  w.n = a.per * w.B;
+  w.M = w.n * a.G;
+  w.row0 = w.rtile * a.rows_per_tile;
+  w.k_begin = w.split * chunk;
+  w.first = w.split == 0;
+  w.ok = w.row0 < w.M && (w.first || w.k_begin < w.P);
+  w.k_end = min(w.P, w.k_begin + chunk);
+  w.n_splits = max(1, (w.P + chunk - 1) / chunk);
+  return w;
+}
+
+// Position of new token `tok` past the prompt.
+__device__ __forceinline__ int kvq_offset(const KvqParams &a, int B, int tok) {
+  return a.order == SIMSD_ORDER_PAIRED ? (tok < B ? tok : tok - B)
+         : a.order == SIMSD_ORDER_NODES ? tok % a.node_size : tok;
+}
+
+// bits [0, n) set (n clamped to 0..64)
+__device__ __forceinline__ uint64_t kvq_low_bits(int n) {
+  return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull;
+}
+
+// The new tokens that row `tok` sees, one bit each; tau_s: labels of the
+// sections (paired order).
+__device__ __forceinline__ uint64_t kvq_visible(const KvqParams &a, int B, const int *tau_s, int tok) {
+  if (a.order == SIMSD_ORDER_CAUSAL) return kvq_low_bits(tok + 1);
+  if (a.order == SIMSD_ORDER_NODES)
+    return kvq_low_bits(a.node_size) << ((tok / a.node_size) * a.node_size);
+  const bool slot = tok >= B;
+  const int t = tau_s[slot ? tok - B : tok];
+  uint64_t bits = 0;
+  for (int j = 0; j < B; ++j) {
+    const int tj = tau_s[j];
+    if (slot ? tj < t : tj <= t) bits |= 1ull << j;
+    if (slot && tj >= t) bits |= 1ull << (B + j);
+  }
+  return bits;
+}
+
+cudaError_t launch_kvq_simt(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
+                            cudaStream_t stream);
+cudaError_t launch_kvq_merge(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
+                             cudaStream_t stream);
+
+}  // namespace simsd

@@ -1,0 +1,455 @@
+"""simsd_kvq_append and simsd_kvq_verify against their 64-bit forms.
+
+Append.  A stored value is the e4m3 code nearest to x 2^-E.  The kernel's x
+is fp32 (a rotation's error: 1.5e-6 (|x1| + |x2|), see test_gpu_rope), so its
+code may be the neighbouring one only where the exact value lies that close to
+the middle between two codes; the scale may differ only where the exact
+maximum lies that close to 448 2^E.  Unrotated values (v) must be equal.
+
+Verify.  kvq_ref.verify gives each output element's bound: scores off by the
+query elements' rounding (bf16: two e4m3 parts, 2^-8 of an element, and the
+new tokens' scores with q and k rounded to bf16, 2 * 2^-8; fp32: none), by
+fp32 sums (hd + 16) 2^-24 of the absolute products and 2^-20 |s| for
+exponentials; weights off by 2^-8 (bf16) before the product with the values;
+then the output's own rounding, half a step."""
+import math
+
+import pytest
+import torch
+
+import kvq_ref as ref
+import speculative_decoding_diffusion_gb300 as pkg
+
+pytestmark = pytest.mark.gpu
+PAGE = 16
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def i32(x):
+    return torch.as_tensor(x, dtype=torch.int32).cuda()
+
+
+def cu_of(n):
+    return torch.cat([torch.zeros(1, dtype=torch.int64), torch.as_tensor(n, dtype=torch.int64).cumsum(0)])
+
+
+def tables(gen, pages, spare=3):
+    """Block table with shuffled page ids; entries past a row's end hold an id out of range."""
+    pages = torch.as_tensor(pages, dtype=torch.int64)
+    total = int(pages.sum()) + spare
+    ids = torch.randperm(total, generator=gen)
+    t = torch.full((len(pages), max(1, int(pages.max()))), 2 ** 30, dtype=torch.int64)
+    at = 0
+    for b, n in enumerate(pages.tolist()):
+        t[b, :n] = ids[at:at + n]
+        at += n
+    return t, total
+
+
+class Cache:
+    """Random codes (NaN codes in unused slots stay possible) and scale bytes."""
+
+    def __init__(self, gen, pages, heads, hd, lo=118, hi=124):
+        def codes():
+            c = torch.randint(0, 256, (pages, heads, PAGE, hd), generator=gen, dtype=torch.int64).to(torch.uint8)
+            return torch.where((c & 0x7f) == 0x7f, c & 0xfe, c)
+        self.k, self.v = codes(), codes()
+        self.ks, self.vs = (torch.randint(lo, hi, (pages, heads), generator=gen, dtype=torch.int64).to(torch.uint8)
+                            for _ in range(2))
+
+    def cuda(self):
+        return [t.cuda() for t in (self.k, self.v, self.ks, self.vs)]
+
+
+def put(k, v, start, n, table, dev, spec, take=None, ws=None):
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda") if ws is None else ws
+    pkg.kvq_append(k, v, i32(start), i32(cu_of(n)), *dev, i32(table), ws, pkg.rope_spec(**spec),
+                   take=None if take is None else i32(take))
+    return ws
+
+
+def check_keys(got_codes, got_bytes, x, size, want_val, want_byte):
+    """Codes and scales of rotated keys: equal, or neighbours where the exact value says so."""
+    got_val = ref.e4m3_values(got_codes)
+    same = (got_val == want_val).all(-1).all(-1) & (got_bytes == want_byte)
+    assert (got_bytes == want_byte).float().mean() > 0.99
+    off = (got_val * torch.exp2(got_bytes.double() - 127)[..., None, None] -
+           want_val * torch.exp2(want_byte.double() - 127)[..., None, None]).abs()
+    # a neighbour is at most one step, 2^-3 of the value (or a subnormal step) away, and rare
+    step = torch.maximum(want_val.abs() * 2.0 ** -3, torch.tensor(2.0 ** -9, dtype=torch.float64))
+    step = step * torch.exp2(torch.maximum(got_bytes, want_byte).double() - 127)[..., None, None]
+    assert (off <= step).all()
+    assert (off > 0).float().mean() < 1e-3
+    return same
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("hd,H", [(128, 2), (64, 9)])
+@pytest.mark.parametrize("spec", [dict(base=1e4), dict(base=1e4, interleaved=True, rotary_dim=32),
+                                  dict(base=1e6, rotary_dim=48, scaling="linear", factor=2.0),
+                                  dict(base=1e6, rotary_dim=50)])
+def test_append_matches_definition(dtype, hd, H, spec):
+    g = torch.Generator().manual_seed(hd + H)
+    start = [0, 5, 16, 31, 100, 7, 0, 15]
+    n = [33, 1, 16, 2, 47, 0, 1, 17]
+    table, total = tables(g, [(s + m + PAGE - 1) // PAGE for s, m in zip(start, n)])
+    c = Cache(g, total, H, hd)
+    N = sum(n)
+    k = (torch.randn(N, H, hd, generator=g) * torch.exp2(torch.randint(-3, 4, (N, H, 1), generator=g).float())).to(DT[dtype])
+    v = (torch.randn(N, H, hd, generator=g) * 3).to(DT[dtype])
+    dev = c.cuda()
+    ws = put(k.cuda(), v.cuda(), start, n, table, dev, spec)
+    assert pkg.read_status(ws) == 0
+    cu = cu_of(n)
+    pos = torch.cat([torch.arange(s, s + m) for s, m in zip(start, n)])
+    xk = ref.rope(k, pos, spec)
+    wk, wkb = ref.append(xk, start, cu, table, c.k, c.ks)
+    wv, wvb = ref.append(v.double(), start, cu, table, c.v, c.vs)
+    got = [t.cpu() for t in dev]
+    assert torch.equal(got[3], wvb) and torch.equal(ref.e4m3_values(got[1]), wv)
+    check_keys(got[0], got[2], None, None, wk, wkb)
+    # the same call again finds the same state
+    dev2 = [t.clone() for t in dev]
+    put(k.cuda(), v.cuda(), start, n, table, dev2, spec)
+    assert all(torch.equal(a, b) for a, b in zip(dev, dev2))
+
+
+def test_append_scale_borders_zero_and_growth():
+    """Maxima at and around 448 2^e, all zeros, the ends of the range; growth
+    moves older codes, a smaller newcomer keeps the scale."""
+    hd, spec = 64, dict(base=1e4, rotary_dim=2)         # elements 2.. pass unrotated
+    tops = [448.0, 449.0, 447.0, 7.0, 7.03125, 0.0, 2.0 ** -60, 57344.0, 60000.0, 3e38, 1e-38, 224.0]
+    n = [3] * len(tops)
+    table, total = tables(torch.Generator().manual_seed(1), [1] * len(tops))
+    c = Cache(torch.Generator().manual_seed(2), total, 1, hd)
+    v = torch.zeros(3 * len(tops), 1, hd)
+    for i, t in enumerate(tops):
+        v[3 * i, 0, 5], v[3 * i + 1, 0, 6], v[3 * i + 2, 0, 7] = t, -t / 3, t * 2.0 ** -12
+    k = v.clone()
+    k[:, :, :2] = 0
+    dev = c.cuda()
+    put(k.cuda(), v.cuda(), [0] * len(n), n, table, dev, spec)
+    wv, wb = ref.append(v.double(), [0] * len(n), cu_of(n), table, c.v, c.vs)
+    wk, wkb = ref.append(k.double(), [0] * len(n), cu_of(n), table, c.k, c.ks)
+    got = [t.cpu() for t in dev]
+    assert torch.equal(got[3], wb) and torch.equal(ref.e4m3_values(got[1]), wv)
+    assert torch.equal(got[2], wkb) and torch.equal(ref.e4m3_values(got[0]), wk)
+    # second append behind the first: ten times larger, then a thousand times smaller
+    for f in (10.0, 1e-3):
+        before = [t.cpu() for t in dev]
+        at = [3 if f == 10.0 else 6] * len(n)
+        put((k * f).cuda(), (v * f).cuda(), at, n, table, dev, spec)
+        wv, wb = ref.append((v * f).double(), at, cu_of(n), table, before[1], before[3])
+        got = [t.cpu() for t in dev]
+        assert torch.equal(got[3], wb) and torch.equal(ref.e4m3_values(got[1]), wv)
+
+
+def test_append_nan_and_infinity_mark_the_page():
+    hd, g = 64, torch.Generator().manual_seed(5)
+    table, total = tables(g, [2, 2])
+    c = Cache(g, total, 2, hd)
+    dev = c.cuda()
+    k, v = torch.randn(40, 2, hd, generator=g), torch.randn(40, 2, hd, generator=g)
+    k[3, 0, 63], v[25, 1, 0] = math.nan, -math.inf
+    put(k.cuda(), v.cuda(), [0, 0], [20, 20], table, dev, dict(base=1e4))
+    ks, vs = dev[2].cpu(), dev[3].cpu()
+    assert ks[table[0, 0], 0] == 255 and (ks == 255).sum() == 1
+    assert vs[table[1, 0], 1] == 255 and (vs == 255).sum() == 1
+    # behind it the mark stays; from the page's first slot it goes
+    put(k[4:8].cuda(), v[4:8].cuda(), [4], [4], table[:1], dev, dict(base=1e4))
+    assert dev[2].cpu()[table[0, 0], 0] == 255
+    put(k[4:8].cuda(), v[4:8].cuda(), [0], [4], table[:1], dev, dict(base=1e4))
+    assert dev[2].cpu()[table[0, 0], 0] != 255
+
+
+def test_append_take_strides_and_untouched_slots():
+    """Fused rows, the first take[b] of each sequence's rows, and every slot and page beside them as it was."""
+    g = torch.Generator().manual_seed(6)
+    H, hd, n, take, start = 3, 128, [8, 8, 8, 8], [4, 0, 8, 1], [14, 3, 16, 0]
+    table, total = tables(g, [(s + m + PAGE - 1) // PAGE for s, m in zip(start, n)])
+    c = Cache(g, total, H, hd)
+    dev = c.cuda()
+    rows = torch.randn(sum(n), 2 + 2 * H, hd, generator=g).to(torch.bfloat16)
+    d = rows.cuda()
+    put(d[:, 2:2 + H], d[:, 2 + H:], start, n, table, dev, dict(base=1e4), take)
+    pos = torch.cat([torch.arange(s, s + m) for s, m in zip(start, n)])
+    wv, wb = ref.append(rows[:, 2 + H:].double(), start, cu_of(n), table, c.v, c.vs, take)
+    wk, wkb = ref.append(ref.rope(rows[:, 2:2 + H], pos, dict(base=1e4)), start, cu_of(n), table, c.k, c.ks, take)
+    got = [t.cpu() for t in dev]
+    assert torch.equal(got[3], wb) and torch.equal(ref.e4m3_values(got[1]), wv)
+    check_keys(got[0], got[2], None, None, wk, wkb)
+
+
+def test_append_many_sequences_and_bad_arrays():
+    g = torch.Generator().manual_seed(7)
+    n = [1 + i % 3 for i in range(700)]
+    start = [(i * 5) % 40 for i in range(700)]
+    table, total = tables(g, [(s + m + PAGE - 1) // PAGE for s, m in zip(start, n)])
+    c = Cache(g, total, 1, 64)
+    v = torch.randn(sum(n), 1, 64, generator=g)
+    dev = c.cuda()
+    bad_table = table.clone()
+    bad_table[5, start[5] // PAGE] = total                    # a page outside the cache
+    bad_table[6, start[6] // PAGE] = -1
+    bad_start = list(start)
+    bad_start[7] = -3                                         # outside the row
+    bad_start[8] = 16 * table.shape[1]
+    ws = put(v.cuda(), v.cuda(), bad_start, n, bad_table, dev, dict(base=1e4))
+    assert pkg.read_status(ws) == 2
+    good = [b for b in range(700) if b not in (5, 6, 7, 8)]
+    cu = cu_of(n)
+    keep = torch.cat([torch.arange(int(cu[b]), int(cu[b + 1])) for b in good])
+    wv, wb = ref.append(v.double()[keep], [start[b] for b in good], cu_of([n[b] for b in good]), table[good], c.v, c.vs)
+    for b in (5, 6):                                          # a second page of theirs that is fine is written
+        if (start[b] % PAGE) + n[b] > PAGE:
+            pytest.fail("choose sequences inside one page")
+    got = [t.cpu() for t in dev]
+    assert torch.equal(got[3], wb) and torch.equal(ref.e4m3_values(got[1]), wv)
+
+
+# ------------------------------------------------------------------- verify
+def case(seed, lens, Bs, order, dtype, Hq, Hkv, hd, node=0, spec=None, sd=1.0, scale=None, lo=118, hi=122):
+    g = torch.Generator().manual_seed(seed)
+    per = 2 if order == "paired" else 1
+    table, total = tables(g, [(L + PAGE - 1) // PAGE for L in lens])
+    c = Cache(g, total, Hkv, hd, lo, hi)
+    T = per * sum(Bs)
+    q = (torch.randn(T, Hq, hd, generator=g) * sd).to(DT[dtype])
+    kn, vn = (torch.randn(T, Hkv, hd, generator=g).to(DT[dtype]) for _ in range(2))
+    tau = torch.cat([torch.randperm(b, generator=g) + 1 for b in Bs])
+    return dict(q=q, c=c, table=table, kn=kn, vn=vn, tau=tau, lens=lens, Bs=Bs, cu=cu_of(Bs), order=order, node=node,
+                spec=spec or dict(base=1e4), scale=scale or 1.0 / math.sqrt(hd), dtype=dtype)
+
+
+ORDER = dict(paired=pkg.SIMSD_ORDER_PAIRED, nodes=pkg.SIMSD_ORDER_NODES, causal=pkg.SIMSD_ORDER_CAUSAL)
+
+
+def launch(s, dev=None, out=None, ws=None, B_max=None, polls=0):
+    if dev is None:
+        dev = [t.cuda() for t in (s["q"], *s["c"].cuda(), s["kn"], s["vn"])]
+    q, k, v, ks, vs, kn, vn = dev
+    out = torch.empty(q.shape, dtype=q.dtype, device="cuda") if out is None else out
+    args = (q, k, v, ks, vs, i32(s["table"]), kn, vn, i32(s["tau"]) if s["order"] == "paired" else None, i32(s["lens"]),
+            i32(s["cu"]), out)
+    total, top = int(s["cu"][-1]), B_max or max(s["Bs"])
+    kw = dict(order=ORDER[s["order"]], node_size=s["node"])
+    spec = pkg.rope_spec(**s["spec"])
+    if ws is None:
+        ws = torch.zeros(pkg.kvq_verify_workspace_size(*args, total, top, spec, s["scale"], **kw), dtype=torch.uint8, device="cuda")
+    pkg.kvq_verify(*args, ws, total, top, spec, s["scale"], wait_polls=polls, **kw)
+    return out, ws
+
+
+def check(s, out):
+    err = dict(f32=(0.0, 0.0), bf16=(2 * 2.0 ** -8, 2.0 ** -8))[s["dtype"]]
+    want, off = ref.verify(s["q"], s["c"].k, s["c"].v, s["c"].ks, s["c"].vs, s["table"], s["kn"], s["vn"], s["tau"],
+                           s["lens"], s["cu"], s["spec"], s["scale"], s["order"], s["node"], *err)
+    off = off + want.abs() * torch.finfo(DT[s["dtype"]]).eps / 2 + 1e-30
+    got = out.cpu().double()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    ok = ((got - want).abs() <= off) | torch.isnan(want)
+    assert ok.all(), float(((got - want).abs() / off).nan_to_num().max())
+
+
+LENS = [0, 1, 15, 16, 17, 127, 128, 129, 300, 513]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("order,Bs,node", [("paired", [1, 2, 3, 4, 5, 8, 4, 7, 1, 6], 0), ("nodes", [4, 8, 4, 16, 4, 4, 4, 12, 4, 8], 4),
+                                           ("causal", [1, 3, 1, 7, 2, 1, 1, 5, 1, 9], 0)])
+@pytest.mark.parametrize("Hq,Hkv,hd", [(8, 2, 128), (3, 3, 64), (7, 1, 128)])
+def test_verify_matches_definition(dtype, order, Bs, node, Hq, Hkv, hd):
+    s = case(Hq + hd, LENS, Bs, order, dtype, Hq, Hkv, hd, node)
+    out, ws = launch(s)
+    assert pkg.read_status(ws) == 0
+    check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("spec", [dict(base=1e4, interleaved=True), dict(base=1e6, rotary_dim=32),
+                                  dict(base=1e6, rotary_dim=50, interleaved=True, scaling="ntk", factor=4.0),
+                                  dict(base=1e6, rotary_dim=24), dict(base=1e6, scaling="yarn", factor=4.0, original_len=64),
+                                  dict(base=1e6, scaling="banded", factor=8.0, original_len=256, fast=4.0, rotary_dim=64)])
+def test_verify_rotary_forms(dtype, spec):
+    for hd, order in ((128, "paired"), (64, "causal")):
+        s = case(9, [40, 200, 3], [4, 2, 3], order, dtype, 4, 2, hd, 0, dict(spec))
+        out, ws = launch(s)
+        check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("order,B,Hq,Hkv", [("paired", 32, 8, 2), ("causal", 64, 5, 1), ("nodes", 64, 2, 1), ("paired", 16, 4, 1),
+                                            ("paired", 32, 7, 1)])
+def test_verify_widest_sections(dtype, order, B, Hq, Hkv):
+    """64 new tokens; one to four row tiles."""
+    s = case(B + Hq, [70, 0, 260], [B, B, 8 if order == "nodes" else 3], order, dtype, Hq, Hkv, 128, 8 if order == "nodes" else 0)
+    out, ws = launch(s)
+    assert pkg.read_status(ws) == 0
+    check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[5000], [4097, 100, 0, 2048], [3000] + [17] * 9])
+def test_verify_key_splits(dtype, lens):
+    """Few long sequences: the plan splits the keys, sequences shorter than a split among them."""
+    s = case(len(lens), lens, [2] * len(lens), "paired", dtype, 4, 1, 64)
+    out, ws = launch(s)
+    assert ws.numel() > 256 and pkg.read_status(ws) == 0
+    check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_strided_rows(dtype):
+    """q, k and v inside fused rows."""
+    s = case(21, [33, 150], [4, 3], "causal", dtype, 4, 2, 128)
+    T = 7
+    rows = torch.cat([s["q"], s["kn"], s["vn"]], 1).cuda()
+    q, kn, vn = rows[:, :4], rows[:, 4:6], rows[:, 6:]
+    assert q.stride(0) == 8 * 128 and q.shape[0] == T
+    c = s["c"].cuda()
+    out, _ = launch(s, [q, *c, kn, vn], out=torch.empty(T, 4, 128, dtype=DT[dtype], device="cuda"))
+    check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_ignores_what_lies_past_the_prompt(dtype):
+    """NaN codes in the last page's unused slots and the pages after it, and NaN scales of pages not in the table."""
+    s = case(22, [5, 130, 17], [2, 2, 2], "paired", dtype, 4, 2, 128)
+    out, _ = launch(s)
+    c = s["c"]
+    used = torch.zeros(c.k.shape[0], dtype=torch.bool)
+    for b, L in enumerate(s["lens"]):
+        for j in range((L + PAGE - 1) // PAGE):
+            used[s["table"][b, j]] = True
+        if L % PAGE:
+            c.k[s["table"][b, L // PAGE], :, L % PAGE:] = 0x7f
+            c.v[s["table"][b, L // PAGE], :, L % PAGE:] = 0xff
+    c.k[~used], c.v[~used], c.ks[~used], c.vs[~used] = 0x7f, 0x7f, 255, 255
+    again, _ = launch(s)
+    assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_marked_pages_read_as_nan(dtype):
+    s = case(23, [40, 40], [1, 1], "paired", dtype, 2, 2, 64)
+    s["c"].ks[s["table"][0, 1], 0] = 255
+    s["c"].vs[s["table"][1, 2], 1] = 255
+    out, _ = launch(s)
+    bad = torch.isnan(out.float().cpu()).all(-1)
+    # a section's rows of sequence 0 (head 0) and sequence 1 (head 1), nothing else
+    assert torch.equal(bad, torch.tensor([[True, False], [True, False], [False, True], [False, True]]))
+    assert torch.equal(torch.isnan(out.float().cpu()).any(-1), bad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lo,hi,sd", [(63, 64, 1.0), (133, 135, 1e-4), (63, 135, 0.05), (118, 122, 60.0), (118, 122, 1e-6)])
+def test_verify_scale_range_and_sharp_rows(dtype, lo, hi, sd):
+    """Scales at both ends of their range and mixed, queries from tiny to ones whose softmax is one-hot."""
+    s = case(24, [200, 31], [3, 2], "paired", dtype, 4, 2, 128, sd=sd, lo=lo, hi=hi)
+    out, _ = launch(s)
+    check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_one_large_score_and_many_small_ones(dtype):
+    """A sink 12 above 4000 equal keys: their sum counts as much as the sink."""
+    s = case(25, [4000], [1], "causal", dtype, 1, 1, 64)
+    c, hd = s["c"], 64
+    c.k[:], c.ks[:], c.vs[:] = 0, 127, 127
+    q = torch.zeros(1, 1, hd)
+    q[..., -1] = 8.0                                     # slowest pair: unrotated to 1e-3 at these positions
+    s["q"] = q.to(DT[dtype])
+    s["spec"] = dict(base=1e4, rotary_dim=2)
+    c.k[s["table"][0, 0], 0, 3, -1] = 0x54               # 12 = 1.5 * 2^3
+    s["scale"] = 0.125
+    s["kn"] = torch.zeros_like(s["kn"])
+    out, _ = launch(s)
+    check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_bad_sequences_are_skipped(dtype):
+    s = case(26, [20, 33, 48, 16], [2, 2, 2, 2], "nodes", dtype, 4, 2, 64, node=2)
+    good, _ = launch(s)
+    s["lens"] = [20, -1, 16 * s["table"].shape[1] + 1, 16]
+    out = torch.full(s["q"].shape, 7.0, dtype=DT[dtype], device="cuda")
+    out, ws = launch(s, out=out)
+    assert pkg.read_status(ws) == 2
+    assert torch.equal(out[:2], good[:2]) and torch.equal(out[6:], good[6:]) and (out[2:6] == 7).all()
+    s["lens"] = [20, 33, 48, 16]
+    s["table"][1, 1] = s["c"].k.shape[0]                  # a page outside the cache counts as absent
+    s["table"][2, 0] = -1
+    out, ws = launch(s)
+    assert pkg.read_status(ws) == 2
+    assert torch.isfinite(out.float()).all() and torch.equal(out[:2], good[:2]) and torch.equal(out[6:], good[6:])
+
+
+def test_verify_two_graphs_and_streams():
+    """Two captured calls with a workspace each, replayed at once on two streams, give what eager calls give."""
+    runs = []
+    for i in range(2):
+        s = case(30 + i, [700 + 5000 * i, 20], [4, 4], "paired", "bf16", 8, 2, 128)
+        dev = [t.cuda() for t in (s["q"], *s["c"].cuda(), s["kn"], s["vn"])]
+        want, ws = launch(s, dev)
+        args = (*dev[:5], i32(s["table"]), dev[5], dev[6], i32(s["tau"]), i32(s["lens"]), i32(s["cu"]), torch.zeros_like(want))
+        spec = pkg.rope_spec(**s["spec"])
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            pkg.kvq_verify(*args, ws, 8, 4, spec, s["scale"])
+        runs.append((graph, side, args[-1], want, (args, ws)))     # the graph's memory stays alive
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, side, _, _, _ in runs:
+            with torch.cuda.stream(side):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, out, want, _ in runs:
+        assert torch.equal(out, want)
+
+
+def test_step_of_the_loop():
+    """Requests admitted, their prompts appended, a verification pass, the kept tokens appended behind it, and the next
+    pass: every stage fed by the one before, against the same chain in 64 bits on the cache's own values."""
+    g = torch.Generator().manual_seed(40)
+    Hq, Hkv, hd, B, batch, width, cap = 4, 2, 128, 4, 3, 8, 30
+    spec = dict(base=1e4, rotary_dim=64)
+    lens0 = [37, 5, 64]
+    free, queue = i32(torch.randperm(cap, generator=g)), i32([0, cap])
+    table, held = i32(torch.zeros(batch, width)), i32([0] * batch)
+    served, ws_map = i32([0] * batch), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    c = Cache(g, cap, Hkv, hd)
+    dev = c.cuda()
+    state = [c.k, c.v, c.ks, c.vs]
+
+    def both(k, v, start, n, take=None):
+        put(k.cuda(), v.cuda(), start, n, table.cpu(), dev, spec, take)
+        pos = torch.cat([torch.arange(s, s + m) for s, m in zip(start, n)])
+        cu = cu_of(n)
+        wv, wvb = ref.append(v.double(), start, cu, table.cpu(), state[1], state[3], take)
+        wk, wkb = ref.append(ref.rope(k, pos, spec), start, cu, table.cpu(), state[0], state[2], take)
+        got = [t.cpu() for t in dev]
+        assert torch.equal(got[3], wvb) and torch.equal(ref.e4m3_values(got[1]), wv)
+        check_keys(got[0], got[2], None, None, wk, wkb)
+        state[:] = got
+
+    pkg.page_map(i32(lens0), None, held, queue, free, table, held, queue, served, None, ws_map, 0)
+    assert served.tolist() == [1, 1, 1] and held.tolist() == [3, 1, 4]
+    N = sum(lens0)
+    both(torch.randn(N, Hkv, hd, generator=g).bfloat16(), torch.randn(N, Hkv, hd, generator=g).bfloat16(), [0] * batch, lens0)
+    lens = list(lens0)
+    for step in range(2):
+        s = case(50 + step, lens, [B] * batch, "paired", "bf16", Hq, Hkv, hd, spec=spec)
+        s["c"].k, s["c"].v, s["c"].ks, s["c"].vs = state
+        s["table"] = table.cpu().long()
+        out, ws = launch(s, [s["q"].cuda(), *dev, s["kn"].cuda(), s["vn"].cuda()])
+        assert pkg.read_status(ws) == 0
+        check(s, out)
+        # sequences 0 and 2 close their block: B tokens of the data section stay
+        keep = [B, 0, B]
+        slots = torch.empty(2 * B * batch, dtype=torch.int64, device="cuda")
+        pkg.page_map(i32(lens), i32(cu_of(keep)), held, queue, free, table, held, queue, served, slots, ws_map, 2 * B * batch)
+        for i, (b, p) in enumerate([(b, lens[b] + j) for b in range(batch) for j in range(keep[b])]):
+            assert int(slots[i]) == int(table[b, p // PAGE]) * PAGE + p % PAGE
+        both(s["kn"], s["vn"], lens, [2 * B] * batch, keep)
+        lens = [L + m for L, m in zip(lens, keep)]
+    assert pkg.read_status(ws_map) == 0
