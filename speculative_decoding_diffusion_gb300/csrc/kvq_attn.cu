@@ -369,12 +369,14 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {
   p->G = d->num_q_heads / d->num_kv_heads;
   p->esize = d->dtype == SIMSD_BF16 ? 2 : 4;
   const int max_n = p->per * d->B_max;
-  p->rows_per_tile = kRows;
+  const bool tc = d->dtype == SIMSD_BF16;
+  p->rows_per_tile = tc ? 128 : kRows;
   const int64_t max_rows = (int64_t)max_n * p->G;
   p->row_tiles = (int)((max_rows + p->rows_per_tile - 1) / p->rows_per_tile);
   const int64_t per_seq = (int64_t)d->num_kv_heads * p->row_tiles;
   if (per_seq * d->batch * 64 >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
-  plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens, 2 * device_sm_count(), max_n, p);
+  plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens,
+              (tc ? 1 : 2) * device_sm_count(), max_n, p);
   size_t off = kAlign;
   p->off_opart = p->off_ml = off;
   if (p->n_splits > 1) {
@@ -391,9 +393,6 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {
 
 cudaError_t launch_kvq_simt(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                             cudaStream_t stream) {
-  if (d->dtype == SIMSD_BF16)
-    return d->head_dim == 128 ? launch_simt_t<__nv_bfloat16, 128>(p, a, stream)
-                              : launch_simt_t<__nv_bfloat16, 64>(p, a, stream);
   return d->head_dim == 128 ? launch_simt_t<float, 128>(p, a, stream)
                             : launch_simt_t<float, 64>(p, a, stream);
 }
@@ -456,7 +455,7 @@ simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream_ptr) 
   a.polls = wait_polls_of(d->wait_polls);
   a.scale = d->sm_scale * 1.4426950408889634f;
   cudaStream_t stream = (cudaStream_t)stream_ptr;
-  cudaError_t e = launch_kvq_simt(d, p, a, stream);
+  cudaError_t e = d->dtype == SIMSD_BF16 ? launch_kvq_tc(d, p, a, stream) : launch_kvq_simt(d, p, a, stream);
   if (e == cudaSuccess && p.n_splits > 1) e = launch_kvq_merge(d, p, a, stream);
   return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
 }

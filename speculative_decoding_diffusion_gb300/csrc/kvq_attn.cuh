@@ -114,6 +114,8 @@ __device__ __forceinline__ uint64_t kvq_visible(const KvqParams &a, int B, const
 
 cudaError_t launch_kvq_simt(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                             cudaStream_t stream);
+cudaError_t launch_kvq_tc(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
+                          cudaStream_t stream);
 cudaError_t launch_kvq_merge(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                              cudaStream_t stream);
 

@@ -1,6 +1,6 @@
 // tc.cuh -- 5th-generation tensor core (tcgen05) and TMEM helpers, inline PTX
 // for sm_103a: TMEM allocation, shared-memory matrix descriptors, the
-// kind::f16 MMA (bf16 in, fp32 accumulate in TMEM), commit to an mbarrier,
+// kind::f8f6f4 MMA (e4m3 in) and the kind::f16 MMA (bf16 in, fp32 accumulate in TMEM), commit to an mbarrier,
 // and 32-lane x 32-column TMEM loads/stores.
 #pragma once
 
@@ -46,6 +46,18 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t addr, uint32_t lbo,
   return d;
 }
 
+// The same for rows of 64 bytes under the 64-byte swizzle (mode 4).
+__device__ __forceinline__ uint64_t smem_desc_sw64(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return (smem_desc_sw128(addr, lbo, sbo) & ~((uint64_t)7 << 61)) | (uint64_t)4 << 61;
+}
+
+// Instruction descriptor of kind::f8f6f4 with e4m3 A and B, fp32 D, both
+// K-major; shape M x N, K = 32.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
+  return (1u << 4)                      // D: f32; A, B: e4m3 = 0
+         | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
 // Instruction descriptor of kind::f16 with bf16 A and B, fp32 D, A K-major;
 // B K-major (b_mn = 0) or MN-major (b_mn = 1); shape M x N.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn) {
@@ -77,6 +89,18 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem desc] for e4m3: A (M x 32) in TMEM, row i in
+// lane i, four consecutive K elements per 32-bit column.
+__device__ __forceinline__ void mma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -126,6 +150,12 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void st8(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
 }
 __device__ __forceinline__ void wait_st() {

@@ -453,3 +453,15 @@ def test_step_of_the_loop():
         both(s["kn"], s["vn"], lens, [2 * B] * batch, keep)
         lens = [L + m for L, m in zip(lens, keep)]
     assert pkg.read_status(ws_map) == 0
+
+
+def test_verify_timeout_writes_nothing():
+    """wait_polls < 0 gives up at once: the timeout bit, out untouched, and the workspace good for the next call."""
+    s = case(60, [300, 40], [4, 4], "paired", "bf16", 8, 2, 128)
+    want, ws = launch(s)
+    out = torch.full_like(want, 7.0)
+    launch(s, out=out, ws=ws, polls=-1)
+    assert pkg.read_status(ws) & 1
+    assert (out == 7).all()
+    again, _ = launch(s, ws=ws)
+    assert pkg.read_status(ws) == 0 and torch.equal(again, want)
