@@ -2,6 +2,7 @@
 // scales held as biased exponents (e8m0).
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -22,13 +23,18 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
          : byte == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(byte << 23);
 }
 
-// Smallest exponent E in kExpLo..kExpHi with amax <= 448 * 2^E (448 = 1.75 *
-// 2^8, so the mantissa decides between exponent - 8 and one more); amax past
-// the range takes kExpHi.  The caller handles NaN and infinity.
-__device__ __forceinline__ int scale_exponent(float amax) {
+// Smallest exponent E in lo..hi with amax <= 448 * 2^E (448 = 1.75 * 2^8, so
+// the mantissa decides between exponent - 8 and one more); amax past the
+// range takes hi.  The caller handles NaN and infinity.
+__device__ __forceinline__ int scale_exponent(float amax, int lo = kExpLo, int hi = kExpHi) {
   const uint32_t u = __float_as_uint(amax);
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
-  return min(max(e, kExpLo), kExpHi);
+  return min(max(e, lo), hi);
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // Two fp32 values to e4m3 codes (round to nearest even, saturating), lo in

@@ -7,9 +7,17 @@
 // rate, so two products cost what one in bf16 does and no key is decoded).
 // The page's key scale multiplies the score in the softmax.  The weights
 // cannot be split like that (their range is too wide for e4m3), so four warps
-// decode the value tiles to bf16, scale included (a multiply by a power of
-// two), and O += P V runs in bf16.  The new tokens are a block of their own
-// ahead of the prompt: keys rotated here, S from bf16 q and k.
+// decode the value tiles to f16 and O += P V runs in f16 with weights of 11
+// bits: bf16 weights would cost as much error as rounding the output does
+// (64 x 4096: 2.5e-3 of the result against 64 bits, 1.7e-3 of it the
+// output's).  Both stay inside f16's range by powers of two: a row's weights
+// are 2^(s - m + 7) with m at most 8 stale (2^15 at most, 2^-25 the smallest),
+// and values are taken relative to 2^vref, vref at most 6 below the largest
+// page scale so far (28672 at most; what a smaller page loses is 2^-37 of the
+// largest values).  vref follows from the page scales alone, so the decode
+// and softmax warps each keep it.  The new tokens are a block of their own
+// ahead of the prompt: keys rotated here, S from f16 q and k, each scaled by
+// a power of two.
 //
 // One CTA per (key split, KV head x 128-row tile, sequence); rows stack new
 // tokens x heads of the group, so a cache byte is read once for all of them.
@@ -44,33 +52,39 @@ constexpr int kVWarp = 6, kDecodeWarp = 7, kWarps = 11;
 constexpr int kThreads = kWarps * 32;
 constexpr int kSoftmax = 4 * 32, kDecode = 4 * 32;
 constexpr float kHeadroom = 8.f;     // log2 units a row max may grow before O is rescaled
+constexpr float kLift = 7.f;         // log2 of the largest weight right after that
+constexpr int kVLift = 3, kVHead = 6;   // page scales over vref: right after it moved, at most
+constexpr int kNoRef = -1000;        // vref before the first value
+constexpr int kNoPage = -1;          // instead of a scale byte
 constexpr uint32_t kColS = 0;        // two score / weight tiles: columns 0 and kKeys
 constexpr uint32_t kColO = 2 * kKeys;
 
 enum { kBarKFull = 0, kBarVFull = kBarKFull + kStages, kBarKEmpty = kBarVFull + kStages,
        kBarVEmpty = kBarKEmpty + kStages, kBarSFull = kBarVEmpty + kStages,
        kBarPFull = kBarSFull + 2, kBarPvDone = kBarPFull + 2, kBarVbFull = kBarPvDone + 2,
-       kBarQReady = kBarVbFull + 2, kBarKnReady, kNumBars };
+       kBarQReady = kBarVbFull + 2, kBarKnReady = kBarQReady + 1, kNumBars = kBarKnReady + 1 };
 
 template <int HD>
 struct Smem {
   static constexpr int kCodes = kKeys * HD;                 // K or V codes of a block
   static constexpr int kStage = 2 * kCodes;
-  static constexpr int kHalf = kKeys * 128;                 // 128 rows x 64 bf16 columns
-  static constexpr int kVb = (HD / 64) * kHalf;             // decoded value tile
-  static constexpr int kKnHalf = kMaxNew * 128;
+  static constexpr int kHalf = kKeys * 128;                 // 128 rows x 64 f16 columns
+  static constexpr int kVb = (HD / 64) * kHalf;             // decoded value tile, f16
+  static constexpr int kKn = kMaxNew * HD;                  // one part of the new keys
   static constexpr int kOffRing = 0;
+  static constexpr int kOffQ = (kStages - 1) * kStage;      // query parts, before the last stage's first use
   static constexpr int kOffVb = kOffRing + kStages * kStage;   // [2]; [1] holds the angles first
-  static constexpr int kOffKn = kOffVb + 2 * kVb;           // rotated new keys, bf16
-  static constexpr int kOffBar = kOffKn + (HD / 64) * kKnHalf;
+  static constexpr int kOffKn = kOffVb + 2 * kVb;           // rotated new keys, hi and lo
+  static constexpr int kOffBar = kOffKn + 2 * kKn;
   static constexpr int kOffTau = kOffBar + kNumBars * 8;
-  static constexpr int kOffMisc = kOffTau + kMaxB * 4;      // tmem address, error flag
+  static constexpr int kOffRow = kOffTau + kMaxB * 4;       // rows' score factors
+  static constexpr int kOffMisc = kOffRow + kRows * 4;      // tmem address, error flag, largest new |k| and |v|
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;              // 1024-byte alignment slack
-  static constexpr uint32_t kColQb = kColO + HD;            // q as bf16: hd / 2 columns
-  static constexpr uint32_t kColQ8 = kColQb + HD / 2;       // q hi and lo: hd / 4 columns each
+  static constexpr uint32_t kColQ = kColO + HD;             // q hi and lo: hd / 4 columns each
   static constexpr uint32_t kTmemCols = 512;
-  static_assert(kColQ8 + HD / 2 <= kTmemCols, "TMEM budget");
+  static_assert(kColQ + HD / 2 <= kTmemCols, "TMEM budget");
+  static_assert(2 * kRows * HD <= kStage, "query parts fit a stage");
   static_assert(4 * 32 * (HD + 4) * 4 <= kStages * kStage, "epilogue exchange fits the ring");
   static_assert(kMaxNew * (HD / 2) * 8 <= kVb, "angles fit the second value tile");
 };
@@ -90,33 +104,90 @@ __device__ __forceinline__ float ex2(float x) {
 
 template <int V> struct IntC { static constexpr int value = V; };
 
-__device__ __forceinline__ uint32_t word4(const uint4 &v, int i) {
-  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-
 __device__ __forceinline__ void named_sync(int id, int n) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(n) : "memory");
 }
 
 __device__ __forceinline__ uint64_t shift_right(uint64_t x, int s) { return s >= 64 ? 0ull : x >> s; }
 
-// Element i (a compile-time constant after unrolling) of a bf16 row held in
-// 16-byte vectors.
+// Byte offset of 16-byte chunk `k` of `row` in a tile of e4m3 rows: the
+// 128-byte swizzle for 128-byte rows, the 64-byte one for 64-byte rows.
 template <int HD>
-__device__ __forceinline__ float row_elem(const uint4 *qv, int i) {
-  const uint32_t w = word4(qv[i >> 3], (i >> 1) & 3);
-  return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+__device__ __forceinline__ uint32_t code_off(int row, int k) {
+  return HD == 128 ? (uint32_t)(row * 128 + ((k ^ (row & 7)) << 4))
+                   : (uint32_t)(row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
 }
 
-// Four e4m3 codes to two bf16 pairs, times a power of two: a code's exponent
-// and mantissa bits, moved to a bf16's, are its value times 2^-120 (subnormal
-// codes become subnormal bf16 values), so `mul` is 2^(120 + E) twice.
-__device__ __forceinline__ uint32_t decode2(uint32_t w, uint32_t sel, __nv_bfloat162 mul) {
-  uint32_t x;                                    // each byte sign-extended to 16 bits
-  asm("prmt.b32 %0, %1, 0, %2;" : "=r"(x) : "r"(w), "r"(sel));
-  x = (x << 4) & 0x87f087f0u;
-  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&x), mul);
+// Elements e0 .. e0 + 7 of a rotated bf16 row with angles cs (identity pairs
+// past the rotated part when interleaved).
+__device__ __forceinline__ void rotate8(const RopePlan &p, const float2 *cs, const __nv_bfloat16 *row, int e0,
+                                        float *x) {
+  load_vec<__nv_bfloat16, 8>(row + e0, x);
+  if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 z = cs[(e0 + i) >> 1];
+      const float x1 = x[i], x2 = x[i + 1];
+      x[i] = x1 * z.x - x2 * z.y;
+      x[i + 1] = x2 * z.x + x1 * z.y;
+    }
+  } else if (p.half % 8 == 0) {
+    if (e0 >= 2 * p.half) return;
+    const bool low = e0 < p.half;
+    float y[8];
+    load_vec<__nv_bfloat16, 8>(row + (low ? e0 + p.half : e0 - p.half), y);
+    const float2 *z = cs + (low ? e0 : e0 - p.half);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * z[i].x + (low ? -y[i] : y[i]) * z[i].y;
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < 8 && e0 + i < 2 * p.half; ++i) {
+      const int d = e0 + i;
+      const bool low = d < p.half;
+      const float u = __bfloat162float(row[d]), y = __bfloat162float(row[low ? d + p.half : d - p.half]);
+      const float2 z = cs[low ? d : d - p.half];
+      const float v = u * z.x + (low ? -y : y) * z.y;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = k == i ? v : x[k];   // no indexed registers
+    }
+  }
+}
+
+// Eight values in two e4m3 parts: hi, and lo = e4m3(x - hi).
+__device__ __forceinline__ void split8(const float *x, uint2 &hi, uint2 &lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = pack_e4m3x2(x[2 * i], x[2 * i + 1]);
+    const float2 f = unpack_e4m3x2(h[i]);
+    l[i] = pack_e4m3x2(x[2 * i] - f.x, x[2 * i + 1] - f.y);
+  }
+  hi = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+  lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
+}
+
+// Two e4m3 codes (low 16 bits) as f16 (exact) times a power of two.
+__device__ __forceinline__ uint32_t decode2(uint32_t codes, __half2 mul) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
+  const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), mul);
   return *reinterpret_cast<const uint32_t *>(&y);
+}
+
+// vref after a block whose largest page scale exponent is emax (kNoRef: none).
+__device__ __forceinline__ int next_vref(int vref, int emax) {
+  return emax > vref + kVHead ? emax - kVLift : vref;
+}
+
+// Largest of the eight lanes of a block.
+__device__ __forceinline__ int block_max(int e) {
+#pragma unroll
+  for (int m = 4; m > 0; m >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, m));
+  return e;
+}
+
+// 2^k as f16, 0 below its range.
+__device__ __forceinline__ uint32_t f16_pow2(int k) {
+  return k < -24 ? 0u : k < -14 ? 1u << (k + 24) : (uint32_t)(k + 15) << 10;
 }
 
 template <int HD>
@@ -131,6 +202,8 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   int *tau_s = reinterpret_cast<int *>(sb + L::kOffTau);
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sb + L::kOffMisc);
   int *flag_s = reinterpret_cast<int *>(sb + L::kOffMisc + 4);
+  float *row_s = reinterpret_cast<float *>(sb + L::kOffRow);
+  uint32_t *amax_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new keys, values
   grid_dep_launch();                         // the split merge may be scheduled
   const KvqWork w = kvq_work(a);
   if (!w.ok) return;                         // uniform: nothing to do here
@@ -146,35 +219,32 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   const int n_valid = R > 1 ? 4 : n_groups;
   const int32_t *bt = a.block_table + (int64_t)w.b * a.max_pages;
   const int64_t t0 = (int64_t)a.per * w.c0;  // first new token's row
-  // page id of page `lane` of prompt block j; -1: none (or not in the cache)
+  // Page ids and scales are requested four blocks ahead of their use and
+  // looked at only then: under load such a read takes longer than a block,
+  // and a test right after it would hold the warp (3600 of the 3900 cycles a
+  // block first took).
+  auto in_cache = [&](int page) { return page >= 0 && page < a.num_pages; };
+  // table entry of page `lane` of prompt block j (producers); -1: none
   auto block_page = [&](int j) {
-    if (j >= n_past || lane >= kPagesPerBlock) return -1;
     const int key = w.k_begin + j * kKeys + lane * kPage;
-    if (key >= w.k_end) return -1;
-    const int page = __ldg(bt + key / kPage);
-    if (page >= 0 && page < a.num_pages) return page;
-    raise_status(a.status, kStatusBadInput);
-    return -1;
+    return j < n_past && lane < kPagesPerBlock && key < w.k_end ? __ldg(bt + key / kPage) : -1;
   };
-  int pages[kStages];
-  const bool softmax_warp = warp >= 2 && warp < 6;
+  // table entry of page `lane` of the four prompt blocks 4 g ..; -1: none
+  auto group_page = [&](int g) {
+    const int64_t key = w.k_begin + ((int64_t)g * 32 + lane) * kPage;
+    return key < w.k_end ? __ldg(bt + key / kPage) : -1;
+  };
+  // scale byte of page `page` and this head; kNoPage: none
+  auto scale_byte = [&](const uint8_t *scale, int page) {
+    return in_cache(page) ? (int)__ldg(scale + (int64_t)page * a.Hkv + w.kvh) : kNoPage;
+  };
+  int pages[kStages], group0 = -1;
   if (warp == 0 || warp == kVWarp) {
     if (warp == 0 && lane == 0) prefetch_tmap(&tmK);
 #pragma unroll
     for (int d = 0; d < kStages; ++d) pages[d] = block_page(d);
-  }
-  uint4 qv[HD / 8];
-  if (softmax_warp) {
-    const int r = w.row0 + 32 * ((warp & 3) % (4 / R)) + lane;
-    if (r < w.M) {
-      const uint4 *src = reinterpret_cast<const uint4 *>(
-          (const __nv_bfloat16 *)a.q + (t0 + r / a.G) * a.q_row + (w.kvh * a.G + r % a.G) * HD);
-#pragma unroll
-      for (int e = 0; e < HD / 8; ++e) qv[e] = __ldg(src + e);
-    } else {
-#pragma unroll
-      for (int e = 0; e < HD / 8; ++e) qv[e] = make_uint4(0, 0, 0, 0);
-    }
+  } else {
+    group0 = group_page(0);
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -192,6 +262,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     mbar_init(bar(kBarQReady), 4);
     mbar_init(bar(kBarKnReady), 4);
     *flag_s = 0;
+    amax_s[0] = amax_s[1] = 0u;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -204,17 +275,113 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   const uint32_t tmem = *tmem_slot;
   int issued = 0;                            // producers: blocks whose loads were started
   float2 *cs_s = reinterpret_cast<float2 *>(sb + L::kOffVb + L::kVb);   // [kMaxNew][HD / 2]
+  // powers of two that the new tokens' keys and values are taken relative to:
+  // rotated elements stay below sqrt 2 of the largest
+  auto new_kexp = [&]() { return scale_exponent(__uint_as_float(amax_s[0]) * a.plan.mul * 1.41422f, -64, 119); };
+  auto new_vref = [&]() { return scale_exponent(__uint_as_float(amax_s[1]), -64, 119) - kVLift; };
+  // exponent of a value scale; kNoRef where there is none or it is NaN
+  auto v_exp = [&](int byte) { return byte < 0 || byte == kScaleNan ? kNoRef : min(byte - kScaleBias, kExpHi); };
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
-  // angles of the new tokens' positions (identity past the rotated part),
-  // by the softmax and decode warps together
-  auto angles = [&](int t) {
+  // The softmax and decode warps together (t: 0..255) rotate the query rows
+  // into two e4m3 parts (in the ring's last stage) and, in the CTA that owns
+  // the new tokens, their keys likewise and their values into the first value
+  // tile; rolled loops, since each CTA runs them once (unrolled per row they
+  // took as long as ten blocks, most of it instruction fetch).
+  constexpr int kPrep = kSoftmax + kDecode;
+  auto prepare = [&](int t) {
+    constexpr int CH = HD / 8;
+    const __nv_bfloat16 *ks = (const __nv_bfloat16 *)a.k_new + t0 * a.k_row + w.kvh * HD;
+    const __nv_bfloat16 *vs = (const __nv_bfloat16 *)a.v_new + t0 * a.v_row + w.kvh * HD;
+    if (fresh) {                             // the largest finite magnitudes
+      float ka = 0.f, va = 0.f;
+#pragma unroll 1
+      for (int e = t; e < w.n * CH; e += kPrep) {
+        float x[8], y[8];
+        load_vec<__nv_bfloat16, 8>(ks + (e / CH) * a.k_row + (e % CH) * 8, x);
+        load_vec<__nv_bfloat16, 8>(vs + (e / CH) * a.v_row + (e % CH) * 8, y);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ka = fmaxf(ka, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+          va = fmaxf(va, fabsf(y[i]) < INFINITY ? fabsf(y[i]) : 0.f);
+        }
+      }
+      const uint32_t kb = __reduce_max_sync(0xffffffffu, __float_as_uint(ka));
+      const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(va));
+      if (lane == 0) {
+        atomicMax(amax_s, kb);
+        atomicMax(amax_s + 1, vb);
+      }
+    }
+    // angles of the new tokens' positions (identity past the rotated part)
     const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
-    for (int e = t; e < npos * (HD / 2); e += kSoftmax + kDecode) {
+#pragma unroll 1
+    for (int e = t; e < npos * (HD / 2); e += kPrep) {
       const int d = e % (HD / 2);
       cs_s[e] = d < a.plan.half ? rope_plan_cs(a.plan, d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
     }
     if (a.order == SIMSD_ORDER_PAIRED && t < w.B) tau_s[t] = __ldg(a.tau + w.c0 + t);
-    named_sync(1, kSoftmax + kDecode);
+    named_sync(1, kPrep);
+    // query rows: CH neighbouring lanes hold a row
+    const __nv_bfloat16 *qs = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
+#pragma unroll 1
+    for (int e = t; e < n_groups * 32 * CH; e += kPrep) {
+      const int r = e / CH, c = e % CH, row = w.row0 + r;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      if (row < w.M) {
+        const int tok = row / a.G;
+        rotate8(a.plan, cs_s + kvq_offset(a, w.B, tok) * (HD / 2), qs + tok * a.q_row + (row - tok * a.G) * HD, c * 8, x);
+      }
+      float amax = 0.f;
+      bool odd = false;                      // a NaN or an infinity: the row's scores become NaN
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        odd |= !(fabsf(x[i]) < INFINITY);
+        amax = fmaxf(amax, fabsf(x[i]));
+      }
+#pragma unroll
+      for (int m = CH / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+      const uint32_t odds = (__ballot_sync(0xffffffffu, odd) >> (lane & ~(CH - 1))) & ((1u << CH) - 1u);
+      const int qe = scale_exponent(amax, -100, 119);
+      const float down = pow2i(-qe);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= down;
+      uint2 hi, lo;
+      split8(x, hi, lo);
+      uint8_t *dst = sb + L::kOffQ + code_off<HD>(r, c >> 1) + (c & 1) * 8;
+      *reinterpret_cast<uint2 *>(dst) = hi;
+      *reinterpret_cast<uint2 *>(dst + kRows * HD) = lo;
+      if (c == 0) row_s[r] = odds != 0u ? __uint_as_float(0x7fc00000u) : a.scale * pow2i(qe);
+    }
+    if (fresh) {                             // zeros up to the MMA's depth
+      const float kdown = pow2i(-new_kexp()), vdown = pow2i(-new_vref());
+#pragma unroll 1
+      for (int e = t; e < n_pad * CH; e += kPrep) {
+        const int j = e / CH, c = e % CH;
+        float x[8], v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = v[i] = 0.f;
+        if (j < w.n) {
+          load_vec<__nv_bfloat16, 8>(vs + j * a.v_row + c * 8, v);
+          rotate8(a.plan, cs_s + kvq_offset(a, w.B, j) * (HD / 2), ks + j * a.k_row, c * 8, x);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] = fabsf(x[i]) < INFINITY ? x[i] * kdown : __uint_as_float(0x7fc00000u);   // e4m3 has no infinity
+          v[i] *= vdown;
+        }
+        uint2 hi, lo;
+        split8(x, hi, lo);
+        uint8_t *dst = sb + L::kOffKn + code_off<HD>(j, c >> 1) + (c & 1) * 8;
+        *reinterpret_cast<uint2 *>(dst) = hi;
+        *reinterpret_cast<uint2 *>(dst + L::kKn) = lo;
+        *reinterpret_cast<uint4 *>(sb + L::kOffVb + (c >> 3) * L::kHalf + swz(j, c & 7)) =
+            make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+      }
+    }
+    fence_proxy_async_smem();
+    named_sync(1, kPrep);
   };
 
   if (warp == 0 || warp == kVWarp) {
@@ -228,21 +395,25 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         const int j = j0 + s;
         if (j >= n_past) break;
         const int page = pages[s];
-        const int n_pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
-        if (j >= kStages && !mbar_wait_warp(bar(empty0 + s), ((j / kStages) - 1) & 1, a.polls)) {
+        const int n_pages = __popc(__ballot_sync(0xffffffffu, in_cache(page)));
+        // (the last stage holds the query parts until they are in TMEM)
+        if ((j >= kStages && !mbar_wait_warp(bar(empty0 + s), ((j / kStages) - 1) & 1, a.polls)) ||
+            (j == kStages - 1 && !mbar_wait_warp(bar(kBarQReady), 0, a.polls))) {
           if (lane == 0) give_up();
           ok = false;
           break;
         }
         if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), n_pages * kPage * HD);
         __syncwarp();
-        if (page >= 0) {
+        if (in_cache(page)) {
           const uint32_t dst = base + L::kOffRing + s * L::kStage + (kside ? 0 : L::kCodes) + lane * kPage * HD;
           if (kside)
             tma_load_4d(dst, &tmK, bar(full0 + s), 0, 0, w.kvh, page);
           else
             bulk_load(dst, a.v_cache + ((int64_t)page * a.Hkv + w.kvh) * kPage * HD, kPage * HD, bar(full0 + s));
         }
+        if (kside && lane < kPagesPerBlock && !in_cache(page) && w.k_begin + j * kKeys + lane * kPage < w.k_end)
+          raise_status(a.status, kStatusBadInput);
         issued = j + 1;
         pages[s] = block_page(j + kStages);
       }
@@ -251,8 +422,8 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     // ---------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t idS8 = tc::idesc_e4m3(kRows, kKeys);
-      constexpr uint32_t idSn = tc::idesc_bf16(kRows, kMaxNew, 0);
-      constexpr uint32_t idO = tc::idesc_bf16(kRows, HD, 1);
+      constexpr uint32_t idSn = tc::idesc_e4m3(kRows, kMaxNew);
+      constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 1);
       bool ok = mbar_wait(bar(kBarQReady), 0, a.polls);
       int ns = 0, np = 0;
       uint64_t idle = 0;
@@ -265,22 +436,17 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
               (ns < 2 || mbar_test(bar(kBarPvDone + tb), ((ns >> 1) - 1) & 1))) {
             tc::fence_after_sync();
             const uint32_t tS = tmem + kColS + tb * kKeys;
-            if (is_new) {
+            // the parts of q against the codes, or against both parts of the new keys
+            const uint32_t kt = base + (is_new ? L::kOffKn : L::kOffRing + s * L::kStage);
+#pragma unroll 1
+            for (int part = 0; part < (is_new ? 4 : 2); ++part) {
+              const uint32_t k0 = kt + (part >> 1) * L::kKn, q0 = tmem + L::kColQ + (part & 1) * (HD / 4);
 #pragma unroll
-              for (int kk = 0; kk < HD / 16; ++kk)
-                tc::mma_bf16_ts(tS, tmem + L::kColQb + kk * 8,
-                                tc::smem_desc_sw128(base + L::kOffKn + (kk >> 2) * L::kKnHalf + (kk & 3) * 32, 16, 1024),
-                                idSn, kk > 0);
-            } else {
-              const uint32_t kt = base + L::kOffRing + s * L::kStage;
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int kk = 0; kk < HD / 32; ++kk)
-                  tc::mma_e4m3_ts(tS, tmem + L::kColQ8 + part * (HD / 4) + kk * 8,
-                                  HD == 128 ? tc::smem_desc_sw128(kt + kk * 32, 16, 1024)
-                                            : tc::smem_desc_sw64(kt + kk * 32, 16, 512),
-                                  idS8, part > 0 || kk > 0);
+              for (int kk = 0; kk < HD / 32; ++kk)
+                tc::mma_e4m3_ts(tS, q0 + kk * 8,
+                                HD == 128 ? tc::smem_desc_sw128(k0 + kk * 32, 16, 1024)
+                                          : tc::smem_desc_sw64(k0 + kk * 32, 16, 512),
+                                is_new ? idSn : idS8, part > 0 || kk > 0);
             }
             tc::commit(bar(kBarSFull + tb));
             if (!is_new) tc::commit(bar(kBarKEmpty + s));
@@ -316,90 +482,28 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   } else if (warp >= kDecodeWarp) {
     // ------------------------------------------------------------- decode
     const int dw = warp - kDecodeWarp, t = threadIdx.x - kDecodeWarp * 32;
-    angles(kSoftmax + t);
-    if (fresh) {
-      // the new tokens' keys, rotated, and their values as they are (zeros up
-      // to the MMA's depth)
-      constexpr int CH = HD / 8;
-      const __nv_bfloat16 *ks = (const __nv_bfloat16 *)a.k_new + t0 * a.k_row + w.kvh * HD;
-      const __nv_bfloat16 *vs = (const __nv_bfloat16 *)a.v_new + t0 * a.v_row + w.kvh * HD;
-      const RopePlan &p = a.plan;
-      for (int e = t; e < n_pad * CH; e += kDecode) {
-        const int j = e / CH, c = e % CH, e0 = c * 8;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        float x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.f;
-        if (j < w.n) {
-          v = __ldg(reinterpret_cast<const uint4 *>(vs + j * a.v_row + e0));
-          const __nv_bfloat16 *row = ks + j * a.k_row;
-          const float2 *cs = cs_s + kvq_offset(a, w.B, j) * (HD / 2);
-          load_vec<__nv_bfloat16, 8>(row + e0, x);
-          if (p.interleaved) {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float2 z = cs[(e0 + i) >> 1];
-              const float x1 = x[i], x2 = x[i + 1];
-              x[i] = x1 * z.x - x2 * z.y;
-              x[i + 1] = x2 * z.x + x1 * z.y;
-            }
-          } else if (p.half % 8 == 0) {
-            if (e0 < 2 * p.half) {
-              const bool low = e0 < p.half;
-              float y[8];
-              load_vec<__nv_bfloat16, 8>(row + (low ? e0 + p.half : e0 - p.half), y);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float2 z = cs[low ? e0 + i : e0 + i - p.half];
-                x[i] = low ? x[i] * z.x - y[i] * z.y : x[i] * z.x + y[i] * z.y;
-              }
-            }
-          } else {
-            for (int i = 0; i < 8; ++i) {
-              const int d = e0 + i;
-              if (d >= 2 * p.half) break;
-              const bool low = d < p.half;
-              const float y = __bfloat162float(row[low ? d + p.half : d - p.half]);
-              const float2 z = cs[low ? d : d - p.half];
-              x[i] = low ? x[i] * z.x - y * z.y : x[i] * z.x + y * z.y;
-            }
-          }
-        }
-        *reinterpret_cast<uint4 *>(sb + L::kOffVb + (c >> 3) * L::kHalf + swz(j, c & 7)) = v;
-        *reinterpret_cast<uint4 *>(sb + L::kOffKn + (c >> 3) * L::kKnHalf + swz(j, c & 7)) =
-            make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-      }
-      fence_proxy_async_smem();
-      named_sync(2, kDecode);                // every decode warp is done with the angles
-      if (lane == 0) {
-        mbar_arrive(bar(kBarKnReady));
-        mbar_arrive(bar(kBarVbFull));
-      }
+    prepare(kSoftmax + t);
+    if (fresh && lane == 0) {
+      mbar_arrive(bar(kBarKnReady));
+      mbar_arrive(bar(kBarVbFull));
     }
     // value tiles: this warp's rows are pages 2 dw and 2 dw + 1 of a block;
-    // lanes 0 and 1 keep those pages' scales, requested a block ahead
-    // (their page ids two)
-    auto page_of = [&](int jp) {
-      const int key = w.k_begin + jp * kKeys + (2 * dw + lane) * kPage;
-      if (lane >= 2 || jp >= n_past || key >= w.k_end) return -1;
-      const int page = __ldg(bt + key / kPage);
-      return page < a.num_pages ? page : -1;
-    };
-    auto scale_of = [&](int page) -> uint32_t {   // multiplier 2^(120 + E) as two bf16, 0: no page
-      if (page < 0) return 0u;
-      const uint32_t byte = __ldg(a.v_scale + (int64_t)page * a.Hkv + w.kvh);
-      const uint32_t h = byte == kScaleNan ? 0x7fc0u : min(byte + 120u, 254u) << 7;
-      return h | h << 16;
-    };
-    uint32_t next = scale_of(page_of(0));
-    int page1 = page_of(1);
+    // lane 8 q + i keeps the scale of page i of block 4 g + q, requested with
+    // the group before it (its id two groups ahead)
+    int vref = fresh ? new_vref() : kNoRef, mine = kNoPage, emax = kNoRef;
+    int next = scale_byte(a.v_scale, group0);
+    group0 = group_page(1);
     bool ok = true;
     for (int jp = 0; jp < n_past; ++jp) {
       const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1);
-      const uint32_t mine = next;
-      next = scale_of(page1);
-      page1 = page_of(jp + 2);
-      if (j == 1 && !mbar_wait_warp(bar(kBarQReady), 0, a.polls)) { ok = false; break; }   // angles are read
+      if ((jp & 3) == 0) {
+        mine = next;
+        next = scale_byte(a.v_scale, group0);
+        group0 = group_page(jp / 4 + 2);
+        emax = block_max(v_exp(mine));
+      }
+      vref = next_vref(vref, __shfl_sync(0xffffffffu, emax, 8 * (jp & 3)));
+      const uint32_t pow = mine < 0 ? 0u : mine == kScaleNan ? 0x7e00u : f16_pow2(v_exp(mine) - vref);
       if (!mbar_wait_warp(bar(kBarVFull + s), (jp / kStages) & 1, a.polls) ||
           (j >= 2 && !mbar_wait_warp(bar(kBarPvDone + tb), ((j >> 1) - 1) & 1, a.polls))) { ok = false; break; }
       const int valid = w.k_end - w.k_begin - jp * kKeys;    // rows from here on hold no key
@@ -409,15 +513,12 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
 #pragma unroll
       for (int i = 0; i < 32 / RPI; ++i) {
         const int row = 32 * dw + i * RPI + lane / C, c = lane % C;
-        const uint32_t m = __shfl_sync(0xffffffffu, mine, (i * RPI) / kPage);
-        const __nv_bfloat162 mul = *reinterpret_cast<const __nv_bfloat162 *>(&m);
+        const uint32_t m = __shfl_sync(0xffffffffu, pow, 8 * (jp & 3) + 2 * dw + (i * RPI) / kPage) * 0x10001u;
+        const __half2 mul = *reinterpret_cast<const __half2 *>(&m);
         const uint4 x = *reinterpret_cast<const uint4 *>(src + row * HD + c * 16);
-        uint4 lo, hi;                                        // selectors: bytes 0, 1 and 2, 3 with their signs
-        lo = make_uint4(decode2(x.x, 0x9180u, mul), decode2(x.x, 0xb3a2u, mul),
-                        decode2(x.y, 0x9180u, mul), decode2(x.y, 0xb3a2u, mul));
-        hi = make_uint4(decode2(x.z, 0x9180u, mul), decode2(x.z, 0xb3a2u, mul),
-                        decode2(x.w, 0x9180u, mul), decode2(x.w, 0xb3a2u, mul));
-        if (row >= valid) lo = hi = make_uint4(0, 0, 0, 0);
+        uint4 lo = make_uint4(decode2(x.x & 0xffffu, mul), decode2(x.x >> 16, mul), decode2(x.y & 0xffffu, mul), decode2(x.y >> 16, mul));
+        uint4 hi = make_uint4(decode2(x.z & 0xffffu, mul), decode2(x.z >> 16, mul), decode2(x.w & 0xffffu, mul), decode2(x.w >> 16, mul));
+        if (row >= valid || m == 0u) lo = hi = make_uint4(0, 0, 0, 0);   // no key, or no page
         uint8_t *tile = dst + (c >> 2) * L::kHalf;
         const int ch = 2 * (c & 3);
         // the two 64-column halves store their chunks in opposite order: no bank twice
@@ -447,92 +548,20 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     const bool warp_valid = w.row0 + 32 * g < w.M;
     const int tok = row_valid ? grow / a.G : 0;
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
-    // the row's power of two: rotated elements stay below 448 * 2^qe
-    float amax = 0.f;
-    bool odd = false;                        // a NaN or an infinity: the row's scores become NaN
+    prepare(threadIdx.x - 64);
+    const float rscale = row_s[32 * g + lane];
 #pragma unroll
-    for (int e = 0; e < HD; ++e) {
-      const float x = fabsf(row_elem<HD>(qv, e));
-      odd |= !(x < INFINITY);
-      amax = fmaxf(amax, x);
-    }
-    const uint32_t ab = __float_as_uint(amax * a.plan.mul * 1.41422f);
-    const int qe = min(max((int)(ab >> 23) - 127 - 8 + ((ab & 0x7fffffu) > 0x600000u ? 1 : 0), -100), 120);
-    const float down = pow2i(-qe);
-    const float rscale = odd ? __uint_as_float(0x7fc00000u) : a.scale * pow2i(qe);
-    angles(threadIdx.x - 64);
-    {
-      const float2 *cs = cs_s + kvq_offset(a, w.B, tok) * (HD / 2);
-      // 32 rotated elements at a time: bf16 for the new tokens' scores, hi
-      // and lo codes for the prompt's
-      auto emit = [&](int d0, const float *y) {
-        uint32_t wb[16], wh[8], wl[8];
+    for (int part = 0; part < 2; ++part)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) wb[i] = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float y0 = y[4 * i] * down, y1 = y[4 * i + 1] * down, y2 = y[4 * i + 2] * down, y3 = y[4 * i + 3] * down;
-          const uint32_t h0 = pack_e4m3x2(y0, y1), h1 = pack_e4m3x2(y2, y3);
-          const float2 f0 = unpack_e4m3x2(h0), f1 = unpack_e4m3x2(h1);
-          wh[i] = h0 | h1 << 16;
-          wl[i] = pack_e4m3x2(y0 - f0.x, y1 - f0.y) | pack_e4m3x2(y2 - f1.x, y3 - f1.y) << 16;
-        }
-        tc::st16(trow + L::kColQb + d0 / 2, wb);
-        tc::st8(trow + L::kColQ8 + d0 / 4, wh);
-        tc::st8(trow + L::kColQ8 + HD / 4 + d0 / 4, wl);
-      };
-      float y[32];
-      if (a.plan.interleaved) {
-#pragma unroll
-        for (int d0 = 0; d0 < HD; d0 += 32) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float2 z = cs[(d0 + i) >> 1];
-            const float x1 = row_elem<HD>(qv, d0 + i), x2 = row_elem<HD>(qv, d0 + i + 1);
-            y[i] = x1 * z.x - x2 * z.y;
-            y[i + 1] = x2 * z.x + x1 * z.y;
-          }
-          emit(d0, y);
-        }
-      } else if (a.plan.half == HD / 2) {
-#pragma unroll
-        for (int d0 = 0; d0 < HD; d0 += 32) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int d = d0 + i, dp = d < HD / 2 ? d : d - HD / 2;
-            const float2 z = cs[dp];
-            const float x1 = row_elem<HD>(qv, dp), x2 = row_elem<HD>(qv, dp + HD / 2);
-            y[i] = d < HD / 2 ? x1 * z.x - x2 * z.y : x2 * z.x + x1 * z.y;
-          }
-          emit(d0, y);
-        }
-      } else {
-        // half pairs of part of the head: a partner's place is not known at
-        // compile time, so the row goes through local memory
-        uint32_t loc[HD / 2];
-#pragma unroll
-        for (int i = 0; i < HD / 2; ++i) loc[i] = word4(qv[i >> 2], i & 3);
-        auto at = [&](int d) {
-          const uint32_t u = loc[d >> 1];
-          return __uint_as_float((d & 1) ? (u & 0xffff0000u) : (u << 16));
-        };
-        const int half = a.plan.half;
-#pragma unroll 1
-        for (int d0 = 0; d0 < HD; d0 += 32) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int d = d0 + i;
-            const bool low = d < half, turned = d < 2 * half;
-            const float2 z = turned ? cs[low ? d : d - half] : make_float2(1.f, 0.f);
-            const float x2 = at(turned ? (low ? d + half : d - half) : d);
-            y[i] = low ? at(d) * z.x - x2 * z.y : at(d) * z.x + x2 * z.y;
-          }
-          emit(d0, y);
-        }
+      for (int k = 0; k < HD / 16; k += 2) {
+        const uint8_t *src = sb + L::kOffQ + part * kRows * HD;
+        uint4 v[2];
+        v[0] = *reinterpret_cast<const uint4 *>(src + code_off<HD>(32 * g + lane, k));
+        v[1] = *reinterpret_cast<const uint4 *>(src + code_off<HD>(32 * g + lane, k + 1));
+        tc::st8(trow + L::kColQ + part * (HD / 4) + k * 4, reinterpret_cast<const uint32_t *>(v));
       }
-      tc::wait_st();
-      tc::fence_before_sync();
-    }
+    tc::wait_st();
+    tc::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kBarQReady));
     const uint64_t newvis = fresh ? kvq_visible(a, w.B, tau_s, tok) : 0ull;
@@ -540,62 +569,63 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
     int j = 0;
-    // lane i < 8: key scale of page i of a prompt block (-1: no such page),
-    // requested a block ahead (its page id two)
-    auto scale_of = [&](int page) {
-      return page < 0 ? -1.f : scale_value(__ldg(a.k_scale + (int64_t)page * a.Hkv + w.kvh));
-    };
-    float next = scale_of(block_page(0));
-    int page1 = block_page(1);
+    // lane 8 q + i: scales of page i of block 4 g + q, requested with the
+    // group before it (the page ids two groups ahead)
+    int next_k = scale_byte(a.k_scale, group0), next_v = scale_byte(a.v_scale, group0);
+    group0 = group_page(1);
+    float page_scale = 0.f;
+    uint32_t absent = 0u;
+    int emax = kNoRef, vref = fresh ? new_vref() : kNoRef;
+    const float new_scale = fresh ? rscale * pow2i(new_kexp()) : 0.f;
     // the key loop, compiled once per copy count
     auto key_loop = [&](auto rc) {
       constexpr int RC = decltype(rc)::value;
       constexpr int KW = kKeys / RC;         // this warp's keys per block
       constexpr int CB = KW < 64 ? KW : 64;  // columns per TMEM round trip
-      constexpr int NV = (KW + 63) / 64;
       const int k_lo = kp * KW;
-      for (; warp_valid && j < n_blocks; ++j) {
+      for (; ok && warp_valid && j < n_blocks; ++j) {
         const int tb = j & 1, jp = j - fresh;
         const bool is_new = jp < 0;
         const uint32_t tS = trow + kColS + tb * kKeys;
-        const float page_scale = is_new ? 1.f : next;
+        const int vref_was = vref, q8 = 8 * (jp & 3);
         if (!is_new) {
-          next = scale_of(page1);
-          page1 = block_page(jp + 2);
-        }
-        // factor of this warp's 16-key groups: row scale x page scale
-        const float rs = is_new ? a.scale : rscale;
-        float sc[KW / 16];
-#pragma unroll
-        for (int i = 0; i < KW / 16; ++i) sc[i] = rs * __shfl_sync(0xffffffffu, page_scale, is_new ? 0 : k_lo / 16 + i);
-        // keys that count, one bit each (all of a whole block's)
-        uint64_t vis[NV];
-        bool whole = false;
-        if (is_new) {
-#pragma unroll
-          for (int h = 0; h < NV; ++h) vis[h] = shift_right(newvis, k_lo + 64 * h);
-        } else {
-          const int valid = w.k_end - w.k_begin - jp * kKeys;
-          const uint32_t absent = __ballot_sync(0xffffffffu, lane < kPagesPerBlock && page_scale == -1.f);
-          whole = absent == 0;
-#pragma unroll
-          for (int h = 0; h < NV; ++h) vis[h] = kvq_low_bits(valid - k_lo - 64 * h);
-          whole = whole && valid >= kKeys;
-          if (!whole) {
-#pragma unroll
-            for (int i = 0; i < KW / 16; ++i)
-              if ((absent >> (k_lo / 16 + i)) & 1u) vis[i / 4] &= ~(0xffffull << (16 * (i % 4)));
+          if ((jp & 3) == 0) {
+            absent = __ballot_sync(0xffffffffu, next_k == kNoPage);
+            page_scale = scale_value(next_k & 255);
+            emax = block_max(v_exp(next_v));
+            next_k = scale_byte(a.k_scale, group0);
+            next_v = scale_byte(a.v_scale, group0);
+            group0 = group_page(jp / 4 + 2);
           }
+          vref = next_vref(vref, __shfl_sync(0xffffffffu, emax, q8));
         }
         if (!mbar_wait_warp(bar(kBarSFull + tb), (j >> 1) & 1, a.polls)) { ok = false; break; }
         tc::fence_after_sync();
+        // keys that count: all of a whole block's, else one bit each
+        const int valid = is_new ? 0 : w.k_end - w.k_begin - jp * kKeys;
+        const uint32_t gone = (absent >> q8) & 0xffu;
+        const bool whole = !is_new && valid >= kKeys && gone == 0u;
+        auto visible = [&](int c0) {         // bits of columns c0 ..
+          if (is_new) return shift_right(newvis, c0);
+          uint64_t v = kvq_low_bits(valid - c0);
+          for (int i = 0; i < CB / 16; ++i)
+            if ((gone >> (c0 / 16 + i)) & 1u) v &= ~(0xffffull << (16 * i));
+          return v;
+        };
+        auto factor = [&](int c) {           // of this row's scores in the 16 columns from c on
+          const float f = __shfl_sync(0xffffffffu, page_scale, q8 + c / 16);
+          return is_new ? new_scale : rscale * f;
+        };
         // pass 1: the row's maximum over this warp's keys
         float mx = -INFINITY;
-#pragma unroll
-        for (int ck = 0; ck < KW; ck += CB) {
+#pragma unroll 1
+        for (int ck = k_lo; ck < k_lo + KW; ck += CB) {
           uint32_t sr[CB];
 #pragma unroll
-          for (int q = 0; q < CB; q += 32) tc::ld32(tS + k_lo + ck + q, sr + q);
+          for (int q = 0; q < CB; q += 32) tc::ld32(tS + ck + q, sr + q);
+          float f[CB / 16];
+#pragma unroll
+          for (int i = 0; i < CB / 16; ++i) f[i] = factor(ck + 16 * i);
           tc::wait_ld();
           if (whole) {
 #pragma unroll
@@ -605,20 +635,21 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
               for (int c = 0; c < 4; ++c)
                 t4[c] = fmaxf(fmaxf(__uint_as_float(sr[i + c]), __uint_as_float(sr[i + c + 4])),
                               fmaxf(__uint_as_float(sr[i + c + 8]), __uint_as_float(sr[i + c + 12])));
-              mx = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc[(ck + i) / 16]);
+              mx = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f[i / 16]);
             }
           } else {
-            const uint64_t vh = vis[ck / 64];
+            const uint64_t vh = visible(ck);
 #pragma unroll
             for (int i = 0; i < CB; ++i)
-              if ((vh >> i) & 1ull) mx = fmaxf(mx, __uint_as_float(sr[i]) * sc[(ck + i) / 16]);
+              if ((vh >> i) & 1ull) mx = fmaxf(mx, __uint_as_float(sr[i]) * f[i / 16]);
           }
         }
-        // reference maximum: moves only when this block's max outgrows it
-        const bool move = row_valid && mx > m_ref + kHeadroom;
-        const float m_new = move ? mx : m_ref;
+        // reference: moves only when this block's max outgrows it
+        const bool move = row_valid && mx > m_ref + kLift + kHeadroom;
+        const float m_new = move ? mx - kLift : m_ref;
         const float alpha = move ? ex2(m_ref - m_new) : 1.f;     // m_ref = -inf -> 0
-        if (j > 0 && __any_sync(0xffffffffu, move)) {
+        if (j > 0 && (vref != vref_was || __any_sync(0xffffffffu, move))) {
+          const float shrink = alpha * (vref == vref_was ? 1.f : vref_was == kNoRef ? 0.f : pow2i(max(vref_was - vref, -126)));
           // rescaling O needs the previous block's P V done
           if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; break; }
           tc::fence_after_sync();
@@ -628,38 +659,48 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
             tc::ld32(tO + 32 * c, o);
             tc::wait_ld();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
             tc::st32(tO + 32 * c, o);
           }
           tc::wait_st();
         }
         l *= alpha;
         m_ref = m_new;
-        // pass 2: weights 2^(s - m_ref) as bf16 pairs over the score tile
+        // pass 2: weights 2^(s - m_ref) as f16 pairs over the score tile
         // (columns k_lo/2 .. (k_lo + KW)/2), zeros in the other copies' keys
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
         float rs4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int ck = 0; ck < KW; ck += CB) {
+#pragma unroll 1
+        for (int ck = k_lo; ck < k_lo + KW; ck += CB) {
           uint32_t sr[CB], pw[CB / 2];
 #pragma unroll
-          for (int q = 0; q < CB; q += 32) tc::ld32(tS + k_lo + ck + q, sr + q);
-          tc::wait_ld();
-          const uint64_t vh = vis[ck / 64];
+          for (int q = 0; q < CB; q += 32) tc::ld32(tS + ck + q, sr + q);
+          float f[CB / 16];
 #pragma unroll
-          for (int e = 0; e < CB / 2; ++e) {
-            const float f = sc[(ck + 2 * e) / 16];
-            float x0 = fmaf(__uint_as_float(sr[2 * e]), f, -mu), x1 = fmaf(__uint_as_float(sr[2 * e + 1]), f, -mu);
-            if (!whole) {
-              x0 = (vh >> (2 * e)) & 1ull ? x0 : -INFINITY;
-              x1 = (vh >> (2 * e + 1)) & 1ull ? x1 : -INFINITY;
+          for (int i = 0; i < CB / 16; ++i) f[i] = factor(ck + 16 * i);
+          tc::wait_ld();
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < CB / 2; ++e) {
+              const float p0 = ex2(fmaf(__uint_as_float(sr[2 * e]), f[e / 8], -mu));
+              const float p1 = ex2(fmaf(__uint_as_float(sr[2 * e + 1]), f[e / 8], -mu));
+              rs4[e & 3] += p0 + p1;
+              pw[e] = pack_f16x2(p0, p1);
             }
-            const float p0 = ex2(x0), p1 = ex2(x1);
-            rs4[e & 3] += p0 + p1;
-            pw[e] = pack_bf16x2(p0, p1);
+          } else {
+            const uint64_t vh = visible(ck);
+#pragma unroll
+            for (int e = 0; e < CB / 2; ++e) {
+              const float x0 = fmaf(__uint_as_float(sr[2 * e]), f[e / 8], -mu);
+              const float x1 = fmaf(__uint_as_float(sr[2 * e + 1]), f[e / 8], -mu);
+              const float p0 = (vh >> (2 * e)) & 1ull ? ex2(x0) : 0.f;
+              const float p1 = (vh >> (2 * e + 1)) & 1ull ? ex2(x1) : 0.f;
+              rs4[e & 3] += p0 + p1;
+              pw[e] = pack_f16x2(p0, p1);
+            }
           }
 #pragma unroll
-          for (int q = 0; q < CB / 2; q += 16) tc::st16(tS + (k_lo + ck) / 2 + q, pw + q);
+          for (int q = 0; q < CB / 2; q += 16) tc::st16(tS + ck / 2 + q, pw + q);
         }
         if (RC > 1) {
           uint32_t z[16];
@@ -686,10 +727,11 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     const bool failed = !ok || *(volatile int *)flag_s != 0;
     const int64_t orow = (t0 + tok) * a.Hq + w.kvh * a.G + (row_valid ? grow % a.G : 0);
     // columns [c0, c0 + n) of this thread's row: sums v relative to reference
-    // mr, weights' sum lt
+    // mr and 2^vref, weights' sum lt
+    const float vup = vref == kNoRef ? 1.f : pow2i(vref);
     auto write_cols = [&](const float *v, int c0, int n, float lt, float mr) {
       if (w.n_splits == 1) {
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const float inv = lt == 0.f ? 0.f : vup / lt;
         uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + orow * HD + c0);
         for (int e = 0; e < n / 8; ++e)
           dst[e] = make_uint4(pack_bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
@@ -699,7 +741,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       } else {
         const int64_t prow = (int64_t)w.split * a.T * a.Hq + orow;
         float4 *dst = reinterpret_cast<float4 *>(a.o_part + prow * HD + c0);
-        for (int e = 0; e < n / 4; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        for (int e = 0; e < n / 4; ++e) dst[e] = make_float4(v[4 * e] * vup, v[4 * e + 1] * vup, v[4 * e + 2] * vup, v[4 * e + 3] * vup);
         if (c0 == 0) a.ml_part[prow] = make_float2(mr, lt);
       }
     };

@@ -69,6 +69,11 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int b_mn) {
          | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
 
+// The same with f16 A and B.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+  return idesc_bf16(M, N, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
 // ---------------------------------------------------------------- MMA
 // D[tmem] (+)= A[smem desc] * B[smem desc]; one thread issues.
 __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
@@ -81,8 +86,8 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem desc]: A (M x 16 bf16, K-major) held in
-// TMEM, row i in lane i, two consecutive K elements per 32-bit column.
+// D[tmem] (+)= A[tmem] * B[smem desc]: A (M x 16 bf16 or, by the instruction
+// descriptor, f16; K-major) held in TMEM, row i in lane i, two consecutive K elements per 32-bit column.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -151,6 +156,11 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void st4(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
 }
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t *r) {
   asm volatile(
