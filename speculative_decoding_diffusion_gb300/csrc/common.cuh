@@ -165,6 +165,14 @@ __device__ __forceinline__ void prefetch_tmap(const void *tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
 }
 
+// Asynchronous 16-byte copy global -> shared; zeros instead when !take (the
+// source is then not read).
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // ---------------------------------------------------------------- mma.sync
 // D = A(16x16 bf16, row) * B(16x8 bf16, col) + D (fp32)
 __device__ __forceinline__ void mma_bf16_16816(float *d, const uint32_t *a,

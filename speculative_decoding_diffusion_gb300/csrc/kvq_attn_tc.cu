@@ -21,13 +21,21 @@
 //
 // One CTA per (key split, KV head x 128-row tile, sequence); rows stack new
 // tokens x heads of the group, so a cache byte is read once for all of them.
-// HBM bounds it: 32 KB per 128-key block against ~1000 tensor-core cycles.
-//   warp 0      keys: one 2 KB TMA box per page, swizzled for the MMA
-//   warp 6      values: one 2 KB bulk copy per page
-//   warp 1      TMEM owner, one lane issues every MMA as its inputs are ready
-//   warps 2-5   softmax, one thread per row; rows of tiles of at most 64 rows
-//               are replicated and the copies split each block's keys
-//   warps 7-10  the new tokens' keys and values, then value tiles to bf16
+// HBM bounds it: 32 KB per 128-key block against 1024 tensor-core cycles (an
+// MMA of N = 128 takes 64, e4m3 at K = 32 like f16 at K = 16; issued by one
+// lane of a converged warp, whose addresses stay in uniform registers, 33 to
+// 43 cycles each -- from a branch of a single thread it is 55 or more).
+//   warp 0       keys: one 2 KB TMA box per page, swizzled for the MMA
+//   warp 6       values: one 2 KB bulk copy per page
+//   warp 1       TMEM owner, issues every MMA as its inputs are ready
+//   warps 2-5 and 11-14  softmax, two warps per 32 rows: one thread of each
+//                per row, half of the block's keys each (scores stay in
+//                registers from the maximum to the weights; the halves agree
+//                on the row's reference through shared memory).  Rows of
+//                tiles of at most 64 rows are replicated and the copies split
+//                the keys again
+//   warps 7-10   value tiles to f16
+// Warps 2-5 and 7-14 first rotate and split the query rows and the new keys.
 // Every wait is bounded (status bit, drain, return).
 #include <cuda.h>
 
@@ -48,20 +56,23 @@ constexpr int kKeys = 128;           // keys per block
 static_assert(kKeys == kBlockKeys, "split chunks are whole blocks");
 constexpr int kStages = 4;
 constexpr int kPagesPerBlock = kKeys / kPage;
-constexpr int kVWarp = 6, kDecodeWarp = 7, kWarps = 11;
+constexpr int kVWarp = 6, kDecodeWarp = 7, kSoftmaxB = 11, kWarps = 15;
 constexpr int kThreads = kWarps * 32;
-constexpr int kSoftmax = 4 * 32, kDecode = 4 * 32;
+constexpr int kPrep = 12 * 32;         // threads of the softmax and decode warps
+constexpr int kHalves = 2;            // softmax warps sharing 32 rows
 constexpr float kHeadroom = 8.f;     // log2 units a row max may grow before O is rescaled
 constexpr float kLift = 7.f;         // log2 of the largest weight right after that
 constexpr int kVLift = 3, kVHead = 6;   // page scales over vref: right after it moved, at most
 constexpr int kNoRef = -1000;        // vref before the first value
 constexpr int kNoPage = -1;          // instead of a scale byte
-constexpr uint32_t kColS = 0;        // two score / weight tiles: columns 0 and kKeys
-constexpr uint32_t kColO = 2 * kKeys;
+constexpr uint32_t kColS = 0;        // two score tiles: columns 0 and kKeys
+constexpr uint32_t kColP = 2 * kKeys;   // weights as f16, two keys a column
+constexpr uint32_t kColO = kColP + kKeys / 2;
 
 enum { kBarKFull = 0, kBarVFull = kBarKFull + kStages, kBarKEmpty = kBarVFull + kStages,
        kBarVEmpty = kBarKEmpty + kStages, kBarSFull = kBarVEmpty + kStages,
-       kBarPFull = kBarSFull + 2, kBarPvDone = kBarPFull + 2, kBarVbFull = kBarPvDone + 2,
+       kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 1,
+       kBarVbFull = kBarPvDone + 2,
        kBarQReady = kBarVbFull + 2, kBarKnReady = kBarQReady + 1, kNumBars = kBarKnReady + 1 };
 
 template <int HD>
@@ -72,19 +83,24 @@ struct Smem {
   static constexpr int kVb = (HD / 64) * kHalf;             // decoded value tile, f16
   static constexpr int kKn = kMaxNew * HD;                  // one part of the new keys
   static constexpr int kOffRing = 0;
-  static constexpr int kOffQ = (kStages - 1) * kStage;      // query parts, before the last stage's first use
-  static constexpr int kOffVb = kOffRing + kStages * kStage;   // [2]; [1] holds the angles first
+  // before their first use the last two stages hold the new keys and values
+  // as they came and the query parts, the value tiles the query rows as they
+  // came and the angles
+  static constexpr int kOffNew = (kStages - 2) * kStage;
+  static constexpr int kOffQ = (kStages - 1) * kStage;
+  static constexpr int kOffVb = kOffRing + kStages * kStage;   // [2]
   static constexpr int kOffKn = kOffVb + 2 * kVb;           // rotated new keys, hi and lo
   static constexpr int kOffBar = kOffKn + 2 * kKn;
   static constexpr int kOffTau = kOffBar + kNumBars * 8;
   static constexpr int kOffRow = kOffTau + kMaxB * 4;       // rows' score factors
-  static constexpr int kOffMisc = kOffRow + kRows * 4;      // tmem address, error flag, largest new |k| and |v|
+  static constexpr int kOffMax = kOffRow + kRows * 4;       // [2 blocks][2 halves][4 quadrants][32]: row maxima, sums
+  static constexpr int kOffMisc = kOffMax + 2 * kHalves * kRows * 4;   // tmem address, error flag, largest new |k| and |v|
   static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;              // 1024-byte alignment slack
   static constexpr uint32_t kColQ = kColO + HD;             // q hi and lo: hd / 4 columns each
   static constexpr uint32_t kTmemCols = 512;
   static_assert(kColQ + HD / 2 <= kTmemCols, "TMEM budget");
-  static_assert(2 * kRows * HD <= kStage, "query parts fit a stage");
+  static_assert(2 * kRows * HD <= kStage && 4 * kMaxNew * HD <= kStage && kRows * HD * 2 <= kVb, "first contents fit");
   static_assert(4 * 32 * (HD + 4) * 4 <= kStages * kStage, "epilogue exchange fits the ring");
   static_assert(kMaxNew * (HD / 2) * 8 <= kVb, "angles fit the second value tile");
 };
@@ -118,8 +134,8 @@ __device__ __forceinline__ uint32_t code_off(int row, int k) {
                    : (uint32_t)(row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
 }
 
-// Elements e0 .. e0 + 7 of a rotated bf16 row with angles cs (identity pairs
-// past the rotated part when interleaved).
+// Elements e0 .. e0 + 7 of a rotated bf16 row (in shared memory) with angles
+// cs (identity pairs past the rotated part when interleaved).
 __device__ __forceinline__ void rotate8(const RopePlan &p, const float2 *cs, const __nv_bfloat16 *row, int e0,
                                         float *x) {
   load_vec<__nv_bfloat16, 8>(row + e0, x);
@@ -216,7 +232,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   // softmax warps that own real rows
   const int n_groups = min(4, (w.M - w.row0 + 31) / 32);
   const int R = n_groups == 1 ? 4 : n_groups == 2 ? 2 : 1;
-  const int n_valid = R > 1 ? 4 : n_groups;
+  const int n_valid = kHalves * (R > 1 ? 4 : n_groups);
   const int32_t *bt = a.block_table + (int64_t)w.b * a.max_pages;
   const int64_t t0 = (int64_t)a.per * w.c0;  // first new token's row
   // Page ids and scales are requested four blocks ahead of their use and
@@ -239,11 +255,30 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     return in_cache(page) ? (int)__ldg(scale + (int64_t)page * a.Hkv + w.kvh) : kNoPage;
   };
   int pages[kStages], group0 = -1;
+  // index among the threads that rotate and split rows
+  const int pt = threadIdx.x - (warp < kVWarp ? 64 : 96);
+  constexpr int CH = HD / 8;                 // 16-byte chunks of a bf16 row
   if (warp == 0 || warp == kVWarp) {
     if (warp == 0 && lane == 0) prefetch_tmap(&tmK);
 #pragma unroll
     for (int d = 0; d < kStages; ++d) pages[d] = block_page(d);
-  } else {
+  } else if (warp != 1) {
+    // the query rows and the new tokens' keys and values come first of all,
+    // ahead of the stream of codes
+    const __nv_bfloat16 *qs = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
+    for (int e = pt; e < n_groups * 32 * CH; e += kPrep) {
+      const int r = e / CH, c = e % CH, row = w.row0 + r, tok = row / a.G;
+      const bool take = row < w.M;
+      copy16_async(base + L::kOffVb + r * HD * 2 + c * 16,
+                   take ? qs + tok * a.q_row + (row - tok * a.G) * HD + c * 8 : (const void *)a.q, take);
+    }
+    if (fresh)
+      for (int e = pt; e < w.n * CH; e += kPrep) {
+        const int j = e / CH, c = e % CH;
+        const uint32_t dst = base + L::kOffNew + j * HD * 2 + c * 16;
+        copy16_async(dst, (const __nv_bfloat16 *)a.k_new + (t0 + j) * a.k_row + w.kvh * HD + c * 8, true);
+        copy16_async(dst + kMaxNew * HD * 2, (const __nv_bfloat16 *)a.v_new + (t0 + j) * a.v_row + w.kvh * HD + c * 8, true);
+      }
     group0 = group_page(0);
   }
   if (threadIdx.x == 0) {
@@ -255,10 +290,11 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kBarSFull + i), 1);
-      mbar_init(bar(kBarPFull + i), n_valid);
+      mbar_init(bar(kBarSEmpty + i), n_valid);
       mbar_init(bar(kBarPvDone + i), 1);
       mbar_init(bar(kBarVbFull + i), 4);
     }
+    mbar_init(bar(kBarPFull), n_valid);
     mbar_init(bar(kBarQReady), 4);
     mbar_init(bar(kBarKnReady), 4);
     *flag_s = 0;
@@ -282,23 +318,30 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   // exponent of a value scale; kNoRef where there is none or it is NaN
   auto v_exp = [&](int byte) { return byte < 0 || byte == kScaleNan ? kNoRef : min(byte - kScaleBias, kExpHi); };
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
-  // The softmax and decode warps together (t: 0..255) rotate the query rows
-  // into two e4m3 parts (in the ring's last stage) and, in the CTA that owns
-  // the new tokens, their keys likewise and their values into the first value
-  // tile; rolled loops, since each CTA runs them once (unrolled per row they
-  // took as long as ten blocks, most of it instruction fetch).
-  constexpr int kPrep = kSoftmax + kDecode;
-  auto prepare = [&](int t) {
-    constexpr int CH = HD / 8;
-    const __nv_bfloat16 *ks = (const __nv_bfloat16 *)a.k_new + t0 * a.k_row + w.kvh * HD;
-    const __nv_bfloat16 *vs = (const __nv_bfloat16 *)a.v_new + t0 * a.v_row + w.kvh * HD;
+  // The softmax and decode warps together rotate the query rows into two e4m3
+  // parts and, in the CTA that owns the new tokens, their keys likewise and
+  // their values into the first value tile; rolled loops, since each CTA runs
+  // them once (unrolled per row they took as long as ten blocks, most of it
+  // instruction fetch).
+  auto prepare = [&]() {
+    // angles of the new tokens' positions (identity past the rotated part)
+    const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
+#pragma unroll 1
+    for (int e = pt; e < npos * (HD / 2); e += kPrep) {
+      const int d = e % (HD / 2);
+      cs_s[e] = d < a.plan.half ? rope_plan_cs(a.plan, d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
+    }
+    if (a.order == SIMSD_ORDER_PAIRED && pt < w.B) tau_s[pt] = __ldg(a.tau + w.c0 + pt);
+    copy_async_wait_all();
+    named_sync(1, kPrep);
+    const __nv_bfloat16 *ks = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew), *vs = ks + kMaxNew * HD;
     if (fresh) {                             // the largest finite magnitudes
       float ka = 0.f, va = 0.f;
 #pragma unroll 1
-      for (int e = t; e < w.n * CH; e += kPrep) {
+      for (int e = pt; e < w.n * CH; e += kPrep) {
         float x[8], y[8];
-        load_vec<__nv_bfloat16, 8>(ks + (e / CH) * a.k_row + (e % CH) * 8, x);
-        load_vec<__nv_bfloat16, 8>(vs + (e / CH) * a.v_row + (e % CH) * 8, y);
+        load_vec<__nv_bfloat16, 8>(ks + e * 8, x);
+        load_vec<__nv_bfloat16, 8>(vs + e * 8, y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           ka = fmaxf(ka, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
@@ -312,27 +355,14 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         atomicMax(amax_s + 1, vb);
       }
     }
-    // angles of the new tokens' positions (identity past the rotated part)
-    const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
+    // query rows: CH neighbouring lanes hold a row (every warp's lanes take
+    // part in a pass or none do: 32 rows are a multiple of 32 chunks)
+    const __nv_bfloat16 *qs = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffVb);
 #pragma unroll 1
-    for (int e = t; e < npos * (HD / 2); e += kPrep) {
-      const int d = e % (HD / 2);
-      cs_s[e] = d < a.plan.half ? rope_plan_cs(a.plan, d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
-    }
-    if (a.order == SIMSD_ORDER_PAIRED && t < w.B) tau_s[t] = __ldg(a.tau + w.c0 + t);
-    named_sync(1, kPrep);
-    // query rows: CH neighbouring lanes hold a row
-    const __nv_bfloat16 *qs = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
-#pragma unroll 1
-    for (int e = t; e < n_groups * 32 * CH; e += kPrep) {
-      const int r = e / CH, c = e % CH, row = w.row0 + r;
+    for (int e = pt; e < n_groups * 32 * CH; e += kPrep) {
+      const int r = e / CH, c = e % CH, row = w.row0 + r, tok = row < w.M ? row / a.G : 0;
       float x[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = 0.f;
-      if (row < w.M) {
-        const int tok = row / a.G;
-        rotate8(a.plan, cs_s + kvq_offset(a, w.B, tok) * (HD / 2), qs + tok * a.q_row + (row - tok * a.G) * HD, c * 8, x);
-      }
+      rotate8(a.plan, cs_s + kvq_offset(a, w.B, tok) * (HD / 2), qs + r * HD, c * 8, x);
       float amax = 0.f;
       bool odd = false;                      // a NaN or an infinity: the row's scores become NaN
 #pragma unroll
@@ -355,16 +385,17 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       if (c == 0) row_s[r] = odds != 0u ? __uint_as_float(0x7fc00000u) : a.scale * pow2i(qe);
     }
     if (fresh) {                             // zeros up to the MMA's depth
+      named_sync(1, kPrep);                  // the query rows are read; the magnitudes are there
       const float kdown = pow2i(-new_kexp()), vdown = pow2i(-new_vref());
 #pragma unroll 1
-      for (int e = t; e < n_pad * CH; e += kPrep) {
+      for (int e = pt; e < n_pad * CH; e += kPrep) {
         const int j = e / CH, c = e % CH;
         float x[8], v[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = v[i] = 0.f;
         if (j < w.n) {
-          load_vec<__nv_bfloat16, 8>(vs + j * a.v_row + c * 8, v);
-          rotate8(a.plan, cs_s + kvq_offset(a, w.B, j) * (HD / 2), ks + j * a.k_row, c * 8, x);
+          load_vec<__nv_bfloat16, 8>(vs + e * 8, v);
+          rotate8(a.plan, cs_s + kvq_offset(a, w.B, j) * (HD / 2), ks + j * HD, c * 8, x);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -396,9 +427,10 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         if (j >= n_past) break;
         const int page = pages[s];
         const int n_pages = __popc(__ballot_sync(0xffffffffu, in_cache(page)));
-        // (the last stage holds the query parts until they are in TMEM)
+        // (the last two stages hold the rows of this CTA until they are split
+        // and in TMEM)
         if ((j >= kStages && !mbar_wait_warp(bar(empty0 + s), ((j / kStages) - 1) & 1, a.polls)) ||
-            (j == kStages - 1 && !mbar_wait_warp(bar(kBarQReady), 0, a.polls))) {
+            ((j == kStages - 2 || j == kStages - 1) && !mbar_wait_warp(bar(kBarQReady), 0, a.polls))) {
           if (lane == 0) give_up();
           ok = false;
           break;
@@ -420,69 +452,87 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idS8 = tc::idesc_e4m3(kRows, kKeys);
-      constexpr uint32_t idSn = tc::idesc_e4m3(kRows, kMaxNew);
-      constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 1);
-      bool ok = mbar_wait(bar(kBarQReady), 0, a.polls);
-      int ns = 0, np = 0;
-      uint64_t idle = 0;
-      while (ok && np < n_blocks) {
-        bool progressed = false;
-        if (ns < n_blocks) {
-          const int tb = ns & 1, jp = ns - fresh, s = jp & (kStages - 1);
-          const bool is_new = jp < 0;
-          if ((is_new ? mbar_test(bar(kBarKnReady), 0) : mbar_test(bar(kBarKFull + s), (jp / kStages) & 1)) &&
-              (ns < 2 || mbar_test(bar(kBarPvDone + tb), ((ns >> 1) - 1) & 1))) {
-            tc::fence_after_sync();
-            const uint32_t tS = tmem + kColS + tb * kKeys;
-            // the parts of q against the codes, or against both parts of the new keys
-            const uint32_t kt = base + (is_new ? L::kOffKn : L::kOffRing + s * L::kStage);
-#pragma unroll 1
-            for (int part = 0; part < (is_new ? 4 : 2); ++part) {
-              const uint32_t k0 = kt + (part >> 1) * L::kKn, q0 = tmem + L::kColQ + (part & 1) * (HD / 4);
+    // The whole warp keeps the loop (uniform addresses), one lane issues.
+    constexpr uint32_t idS8 = tc::idesc_e4m3(kRows, kKeys);
+    constexpr uint32_t idSn = tc::idesc_e4m3(kRows, kMaxNew);
+    constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 1);
+    const uint64_t dK0 = HD == 128 ? tc::smem_desc_sw128(base, 16, 1024) : tc::smem_desc_sw64(base, 16, 512);
+    const uint64_t dV0 = tc::smem_desc_sw128(base + L::kOffVb, L::kHalf, 1024);
+    // scores of the part q0 of the query rows against the tile at offset off
+    auto score = [&](uint32_t tS, uint32_t q0, uint32_t off, uint32_t idesc, bool more) {
 #pragma unroll
-              for (int kk = 0; kk < HD / 32; ++kk)
-                tc::mma_e4m3_ts(tS, q0 + kk * 8,
-                                HD == 128 ? tc::smem_desc_sw128(k0 + kk * 32, 16, 1024)
-                                          : tc::smem_desc_sw64(k0 + kk * 32, 16, 512),
-                                is_new ? idSn : idS8, part > 0 || kk > 0);
+      for (int kk = 0; kk < HD / 32; ++kk)
+        tc::mma_e4m3_ts(tS, q0 + kk * 8, dK0 + ((off + kk * 32) >> 4), idesc, more || kk > 0);
+    };
+    const uint32_t qhi = tmem + L::kColQ, qlo = qhi + HD / 4;
+    bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
+    int ns = 0, np = 0;
+    uint64_t idle = 0;
+    while (ok && np < n_blocks) {
+      bool progressed = false;
+      if (ns < n_blocks) {
+        const int tb = ns & 1, jp = ns - fresh, s = jp & (kStages - 1);
+        const bool is_new = jp < 0;
+        if (__all_sync(0xffffffffu, (is_new ? mbar_test(bar(kBarKnReady), 0)
+                                            : mbar_test(bar(kBarKFull + s), (jp / kStages) & 1)) &&
+                                        (ns < 2 || mbar_test(bar(kBarSEmpty + tb), ((ns >> 1) - 1) & 1)))) {
+          tc::fence_after_sync();
+          const uint32_t tS = tmem + kColS + tb * kKeys;
+          if (tc::elect_one()) {
+            if (is_new) {                    // both parts of q against both of the new keys
+              score(tS, qhi, L::kOffKn, idSn, false);
+              score(tS, qlo, L::kOffKn, idSn, true);
+              score(tS, qhi, L::kOffKn + L::kKn, idSn, true);
+              score(tS, qlo, L::kOffKn + L::kKn, idSn, true);
+              tc::commit(bar(kBarSFull + tb));
+            } else {
+              score(tS, qhi, s * L::kStage, idS8, false);
+              score(tS, qlo, s * L::kStage, idS8, true);
+              tc::commit(bar(kBarSFull + tb));
+              tc::commit(bar(kBarKEmpty + s));
             }
-            tc::commit(bar(kBarSFull + tb));
-            if (!is_new) tc::commit(bar(kBarKEmpty + s));
-            ++ns;
-            progressed = true;
           }
-        }
-        if (np < ns) {
-          const int tb = np & 1;
-          if (mbar_test(bar(kBarPFull + tb), (np >> 1) & 1) && mbar_test(bar(kBarVbFull + tb), (np >> 1) & 1)) {
-            tc::fence_after_sync();
-            const int jp = np - fresh;
-            const int depth = jp < 0 ? n_pad : min(kKeys, (w.k_end - w.k_begin - jp * kKeys + 15) & ~15);
-            const uint32_t vt = base + L::kOffVb + tb * L::kVb;
-            for (int kk = 0; kk < depth / 16; ++kk)
-              tc::mma_bf16_ts(tmem + kColO, tmem + kColS + tb * kKeys + kk * 8,
-                              tc::smem_desc_sw128(vt + kk * 2048, L::kHalf, 1024), idO, (np > 0 || kk > 0));
-            tc::commit(bar(kBarPvDone + tb));
-            ++np;
-            progressed = true;
-          }
-        }
-        if (progressed) {
-          idle = 0;
-        } else if (++idle > ((uint64_t)a.polls << 4)) {  // bounded: give up, flag, drain
-          ok = false;
-        } else if (idle > 8) {
-          __nanosleep(32);                   // leave the issue slots to the other warps
+          __syncwarp();
+          ++ns;
+          progressed = true;
         }
       }
-      if (!ok) give_up();
+      if (np < ns) {
+        const int tb = np & 1;
+        if (__all_sync(0xffffffffu, mbar_test(bar(kBarPFull), np & 1) && mbar_test(bar(kBarVbFull + tb), (np >> 1) & 1))) {
+          tc::fence_after_sync();
+          const int jp = np - fresh;
+          const int depth = jp < 0 ? n_pad : min(kKeys, (w.k_end - w.k_begin - jp * kKeys + 15) & ~15);
+          const uint64_t dV = dV0 + ((uint32_t)(tb * L::kVb) >> 4);
+          if (tc::elect_one()) {
+            if (depth == kKeys) {
+#pragma unroll
+              for (int kk = 0; kk < kKeys / 16; ++kk)
+                tc::mma_bf16_ts(tmem + kColO, tmem + kColP + kk * 8, dV + kk * 128, idO, np > 0 || kk > 0);
+            } else {
+              for (int kk = 0; kk < depth / 16; ++kk)
+                tc::mma_bf16_ts(tmem + kColO, tmem + kColP + kk * 8, dV + kk * 128, idO, np > 0 || kk > 0);
+            }
+            tc::commit(bar(kBarPvDone + tb));
+          }
+          __syncwarp();
+          ++np;
+          progressed = true;
+        }
+      }
+      if (progressed) {
+        idle = 0;
+      } else if (++idle > ((uint64_t)a.polls << 4)) {  // bounded: give up, flag, drain
+        ok = false;
+      } else if (idle > 8) {
+        __nanosleep(32);                     // leave the issue slots to the other warps
+      }
     }
-  } else if (warp >= kDecodeWarp) {
+    if (!ok && lane == 0) give_up();
+  } else if (warp >= kDecodeWarp && warp < kSoftmaxB) {
     // ------------------------------------------------------------- decode
-    const int dw = warp - kDecodeWarp, t = threadIdx.x - kDecodeWarp * 32;
-    prepare(kSoftmax + t);
+    const int dw = warp - kDecodeWarp;
+    prepare();
     if (fresh && lane == 0) {
       mbar_arrive(bar(kBarKnReady));
       mbar_arrive(bar(kBarVbFull));
@@ -538,8 +588,9 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     // ------------------------------------------------------------ softmax
     // With at most 64 real rows the tile's rows are replicated across the
     // four TMEM lane quadrants (R = 4 or 2 copies) and the copies split each
-    // block's keys; every copy keeps its own reference and writes weights for
-    // its keys (zeros elsewhere), and the epilogue merges the copies.
+    // block's keys; every copy keeps its own reference, its weights of the
+    // other copies' keys stay zero, and the epilogue merges the copies.
+    const int half = warp >= kSoftmaxB;
     const int q4 = warp & 3;                 // TMEM lane quadrant of this warp
     const int groups = 4 / R;
     const int g = q4 % groups, kp = q4 / groups;
@@ -548,22 +599,33 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     const bool warp_valid = w.row0 + 32 * g < w.M;
     const int tok = row_valid ? grow / a.G : 0;
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
-    prepare(threadIdx.x - 64);
+    // this row's values of the two warps that share it: [block parity][half]
+    float *both_s = reinterpret_cast<float *>(sb + L::kOffMax) + 32 * q4 + lane;
+    auto pair_sync = [&]() { named_sync(4 + q4, 64); };
+    prepare();
     const float rscale = row_s[32 * g + lane];
+    if (half == 0) {
 #pragma unroll
-    for (int part = 0; part < 2; ++part)
+      for (int part = 0; part < 2; ++part)
 #pragma unroll
-      for (int k = 0; k < HD / 16; k += 2) {
-        const uint8_t *src = sb + L::kOffQ + part * kRows * HD;
-        uint4 v[2];
-        v[0] = *reinterpret_cast<const uint4 *>(src + code_off<HD>(32 * g + lane, k));
-        v[1] = *reinterpret_cast<const uint4 *>(src + code_off<HD>(32 * g + lane, k + 1));
-        tc::st8(trow + L::kColQ + part * (HD / 4) + k * 4, reinterpret_cast<const uint32_t *>(v));
-      }
+        for (int k = 0; k < HD / 16; k += 2) {
+          const uint8_t *src = sb + L::kOffQ + part * kRows * HD;
+          uint4 v[2];
+          v[0] = *reinterpret_cast<const uint4 *>(src + code_off<HD>(32 * g + lane, k));
+          v[1] = *reinterpret_cast<const uint4 *>(src + code_off<HD>(32 * g + lane, k + 1));
+          tc::st8(trow + L::kColQ + part * (HD / 4) + k * 4, reinterpret_cast<const uint32_t *>(v));
+        }
+    } else if (R > 1) {                      // weights of the other copies' keys: zero for good
+      uint32_t z[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) z[e] = 0u;
+#pragma unroll
+      for (int c = 0; c < kKeys / 2; c += 16) tc::st16(trow + kColP + c, z);
+    }
     tc::wait_st();
     tc::fence_before_sync();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(kBarQReady));
+    pair_sync();                             // the zeros are there before the other warp's weights
+    if (half == 0 && lane == 0) mbar_arrive(bar(kBarQReady));
     const uint64_t newvis = fresh ? kvq_visible(a, w.B, tau_s, tok) : 0ull;
     const uint32_t tO = trow + kColO;
     float m_ref = -INFINITY, l = 0.f;
@@ -580,13 +642,14 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     // the key loop, compiled once per copy count
     auto key_loop = [&](auto rc) {
       constexpr int RC = decltype(rc)::value;
-      constexpr int KW = kKeys / RC;         // this warp's keys per block
-      constexpr int CB = KW < 64 ? KW : 64;  // columns per TMEM round trip
-      const int k_lo = kp * KW;
-      for (; ok && warp_valid && j < n_blocks; ++j) {
+      constexpr int KW = kKeys / (RC * kHalves);   // this warp's keys per block: 64, 32 or 16
+      const int k_lo = (kp * kHalves + half) * KW;
+      // A warp whose wait gave up still meets its partner once, with a NaN in
+      // the maximum's place (a maximum is never NaN), so both leave the loop.
+      for (; warp_valid && j < n_blocks; ++j) {
         const int tb = j & 1, jp = j - fresh;
         const bool is_new = jp < 0;
-        const uint32_t tS = trow + kColS + tb * kKeys;
+        const uint32_t tS = trow + kColS + tb * kKeys + k_lo;
         const int vref_was = vref, q8 = 8 * (jp & 3);
         if (!is_new) {
           if ((jp & 3) == 0) {
@@ -599,122 +662,107 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
           }
           vref = next_vref(vref, __shfl_sync(0xffffffffu, emax, q8));
         }
-        if (!mbar_wait_warp(bar(kBarSFull + tb), (j >> 1) & 1, a.polls)) { ok = false; break; }
-        tc::fence_after_sync();
+        // factor of this row's scores in each 16 columns (a page)
+        float f[KW / 16];
+#pragma unroll
+        for (int i = 0; i < KW / 16; ++i) {
+          const float x = __shfl_sync(0xffffffffu, page_scale, q8 + k_lo / 16 + i);
+          f[i] = is_new ? new_scale : rscale * x;
+        }
         // keys that count: all of a whole block's, else one bit each
         const int valid = is_new ? 0 : w.k_end - w.k_begin - jp * kKeys;
         const uint32_t gone = (absent >> q8) & 0xffu;
         const bool whole = !is_new && valid >= kKeys && gone == 0u;
-        auto visible = [&](int c0) {         // bits of columns c0 ..
-          if (is_new) return shift_right(newvis, c0);
-          uint64_t v = kvq_low_bits(valid - c0);
-          for (int i = 0; i < CB / 16; ++i)
-            if ((gone >> (c0 / 16 + i)) & 1u) v &= ~(0xffffull << (16 * i));
-          return v;
-        };
-        auto factor = [&](int c) {           // of this row's scores in the 16 columns from c on
-          const float f = __shfl_sync(0xffffffffu, page_scale, q8 + c / 16);
-          return is_new ? new_scale : rscale * f;
-        };
-        // pass 1: the row's maximum over this warp's keys
-        float mx = -INFINITY;
-#pragma unroll 1
-        for (int ck = k_lo; ck < k_lo + KW; ck += CB) {
-          uint32_t sr[CB];
+        ok = ok && mbar_wait_warp(bar(kBarSFull + tb), (j >> 1) & 1, a.polls);
+        tc::fence_after_sync();
+        uint32_t sr[KW];
+        if constexpr (KW == 16) {
+          tc::ld16(tS, sr);
+        } else {
 #pragma unroll
-          for (int q = 0; q < CB; q += 32) tc::ld32(tS + ck + q, sr + q);
-          float f[CB / 16];
-#pragma unroll
-          for (int i = 0; i < CB / 16; ++i) f[i] = factor(ck + 16 * i);
-          tc::wait_ld();
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < CB; i += 16) {
-              float t4[4];
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                t4[c] = fmaxf(fmaxf(__uint_as_float(sr[i + c]), __uint_as_float(sr[i + c + 4])),
-                              fmaxf(__uint_as_float(sr[i + c + 8]), __uint_as_float(sr[i + c + 12])));
-              mx = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f[i / 16]);
-            }
-          } else {
-            const uint64_t vh = visible(ck);
-#pragma unroll
-            for (int i = 0; i < CB; ++i)
-              if ((vh >> i) & 1ull) mx = fmaxf(mx, __uint_as_float(sr[i]) * f[i / 16]);
-          }
+          for (int q = 0; q < KW; q += 32) tc::ld32(tS + q, sr + q);
         }
+        tc::wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (ok && lane == 0) mbar_arrive(bar(kBarSEmpty + tb));
+        // the row's maximum over both warps' keys
+        float mx = -INFINITY;
+        if (!whole) {                        // keys that do not count score -inf from here on
+          uint64_t vis;
+          if (is_new) {
+            vis = shift_right(newvis, k_lo);
+          } else {
+            vis = kvq_low_bits(valid - k_lo);
+            for (int i = 0; i < KW / 16; ++i)
+              if ((gone >> (k_lo / 16 + i)) & 1u) vis &= ~(0xffffull << (16 * i));
+          }
+#pragma unroll
+          for (int i = 0; i < KW; ++i)
+            sr[i] = __float_as_uint((vis >> i) & 1ull ? __uint_as_float(sr[i]) * f[i / 16] : -INFINITY);
+#pragma unroll
+          for (int i = 0; i < KW / 16; ++i) f[i] = 1.f;
+        }
+#pragma unroll
+        for (int i = 0; i < KW; i += 16) {
+          float t4[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            t4[c] = fmaxf(fmaxf(__uint_as_float(sr[i + c]), __uint_as_float(sr[i + c + 4])),
+                          fmaxf(__uint_as_float(sr[i + c + 8]), __uint_as_float(sr[i + c + 12])));
+          mx = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f[i / 16]);
+        }
+        both_s[(tb * kHalves + half) * kRows] = ok ? mx : __uint_as_float(0x7fc00000u);
+        pair_sync();
+        const float theirs = both_s[(tb * kHalves + (half ^ 1)) * kRows];
+        if (!ok || theirs != theirs) { ok = false; break; }
+        mx = fmaxf(mx, theirs);
         // reference: moves only when this block's max outgrows it
         const bool move = row_valid && mx > m_ref + kLift + kHeadroom;
         const float m_new = move ? mx - kLift : m_ref;
         const float alpha = move ? ex2(m_ref - m_new) : 1.f;     // m_ref = -inf -> 0
-        if (j > 0 && (vref != vref_was || __any_sync(0xffffffffu, move))) {
-          const float shrink = alpha * (vref == vref_was ? 1.f : vref_was == kNoRef ? 0.f : pow2i(max(vref_was - vref, -126)));
-          // rescaling O needs the previous block's P V done
-          if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; break; }
-          tc::fence_after_sync();
-#pragma unroll 1
-          for (int c = 0; c < HD / 32; ++c) {
-            uint32_t o[32];
-            tc::ld32(tO + 32 * c, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
-            tc::st32(tO + 32 * c, o);
-          }
-          tc::wait_st();
-        }
         l *= alpha;
         m_ref = m_new;
-        // pass 2: weights 2^(s - m_ref) as f16 pairs over the score tile
-        // (columns k_lo/2 .. (k_lo + KW)/2), zeros in the other copies' keys
+        // weights 2^(s - m_ref) as f16 pairs
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
         float rs4[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pw[KW / 2];
+#pragma unroll
+        for (int e = 0; e < KW / 2; ++e) {
+          const float p0 = ex2(fmaf(__uint_as_float(sr[2 * e]), f[e / 8], -mu));
+          const float p1 = ex2(fmaf(__uint_as_float(sr[2 * e + 1]), f[e / 8], -mu));
+          rs4[e & 3] += p0 + p1;
+          pw[e] = pack_f16x2(p0, p1);
+        }
+        l += (rs4[0] + rs4[1]) + (rs4[2] + rs4[3]);
+        // the weight tile and O are free once the previous block's P V is done
+        if (j > 0) {
+          if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; continue; }
+          tc::fence_after_sync();
+          if (vref != vref_was || __any_sync(0xffffffffu, move)) {   // this half of O's columns
+            const float shrink = alpha * (vref == vref_was ? 1.f : vref_was == kNoRef ? 0.f : pow2i(max(vref_was - vref, -126)));
 #pragma unroll 1
-        for (int ck = k_lo; ck < k_lo + KW; ck += CB) {
-          uint32_t sr[CB], pw[CB / 2];
+            for (int c = 0; c < HD / 32; ++c) {
+              uint32_t o[16];
+              tc::ld16(tO + half * (HD / 2) + 16 * c, o);
+              tc::wait_ld();
 #pragma unroll
-          for (int q = 0; q < CB; q += 32) tc::ld32(tS + ck + q, sr + q);
-          float f[CB / 16];
-#pragma unroll
-          for (int i = 0; i < CB / 16; ++i) f[i] = factor(ck + 16 * i);
-          tc::wait_ld();
-          if (whole) {
-#pragma unroll
-            for (int e = 0; e < CB / 2; ++e) {
-              const float p0 = ex2(fmaf(__uint_as_float(sr[2 * e]), f[e / 8], -mu));
-              const float p1 = ex2(fmaf(__uint_as_float(sr[2 * e + 1]), f[e / 8], -mu));
-              rs4[e & 3] += p0 + p1;
-              pw[e] = pack_f16x2(p0, p1);
-            }
-          } else {
-            const uint64_t vh = visible(ck);
-#pragma unroll
-            for (int e = 0; e < CB / 2; ++e) {
-              const float x0 = fmaf(__uint_as_float(sr[2 * e]), f[e / 8], -mu);
-              const float x1 = fmaf(__uint_as_float(sr[2 * e + 1]), f[e / 8], -mu);
-              const float p0 = (vh >> (2 * e)) & 1ull ? ex2(x0) : 0.f;
-              const float p1 = (vh >> (2 * e + 1)) & 1ull ? ex2(x1) : 0.f;
-              rs4[e & 3] += p0 + p1;
-              pw[e] = pack_f16x2(p0, p1);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+              tc::st16(tO + half * (HD / 2) + 16 * c, o);
             }
           }
-#pragma unroll
-          for (int q = 0; q < CB / 2; q += 16) tc::st16(tS + ck / 2 + q, pw + q);
         }
-        if (RC > 1) {
-          uint32_t z[16];
+        const uint32_t tP = trow + kColP + k_lo / 2;
+        if constexpr (KW == 16) {
+          tc::st8(tP, pw);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) z[e] = 0u;
-#pragma unroll
-          for (int c = 0; c < kKeys / 2; c += 16)
-            if (c < k_lo / 2 || c >= (k_lo + KW) / 2) tc::st16(tS + c, z);
+          for (int q = 0; q < KW / 2; q += 16) tc::st16(tP + q, pw + q);
         }
         tc::wait_st();
-        l += (rs4[0] + rs4[1]) + (rs4[2] + rs4[3]);
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPFull + tb));
+        if (lane == 0) mbar_arrive(bar(kBarPFull));
       }
     };
     if (R == 4) key_loop(IntC<4>{});
@@ -726,82 +774,86 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     // -------------------------------------------------------- epilogue
     const bool failed = !ok || *(volatile int *)flag_s != 0;
     const int64_t orow = (t0 + tok) * a.Hq + w.kvh * a.G + (row_valid ? grow % a.G : 0);
-    // columns [c0, c0 + n) of this thread's row: sums v relative to reference
+    // columns [c0, c0 + n), n <= 32, of this thread's row: sums v relative to reference
     // mr and 2^vref, weights' sum lt
     const float vup = vref == kNoRef ? 1.f : pow2i(vref);
     auto write_cols = [&](const float *v, int c0, int n, float lt, float mr) {
       if (w.n_splits == 1) {
         const float inv = lt == 0.f ? 0.f : vup / lt;
         uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + orow * HD + c0);
-        for (int e = 0; e < n / 8; ++e)
-          dst[e] = make_uint4(pack_bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (8 * e < n) dst[e] = make_uint4(pack_bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
                               pack_bf16x2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
                               pack_bf16x2(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
                               pack_bf16x2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
       } else {
         const int64_t prow = (int64_t)w.split * a.T * a.Hq + orow;
         float4 *dst = reinterpret_cast<float4 *>(a.o_part + prow * HD + c0);
-        for (int e = 0; e < n / 4; ++e) dst[e] = make_float4(v[4 * e] * vup, v[4 * e + 1] * vup, v[4 * e + 2] * vup, v[4 * e + 3] * vup);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (4 * e < n) dst[e] = make_float4(v[4 * e] * vup, v[4 * e + 1] * vup, v[4 * e + 2] * vup, v[4 * e + 3] * vup);
         if (c0 == 0) a.ml_part[prow] = make_float2(mr, lt);
       }
     };
+    // the row's sum over both warps' keys (the maxima's places, block parity 0)
+    both_s[half * kRows] = l;
+    named_sync(3, 8 * 32);
+    l += both_s[(half ^ 1) * kRows];
     if (R == 1) {
       if (warp_valid) {
 #pragma unroll 1
-        for (int c = 0; c < HD / 32; ++c) {
+        for (int c = 0; c < HD / 64; ++c) {
+          const int c0 = half * (HD / 2) + 32 * c;
           uint32_t o[32];
-          tc::ld32(tO + 32 * c, o);
+          tc::ld32(tO + c0, o);
           tc::wait_ld();
           if (!row_valid || failed) continue;
-          write_cols(reinterpret_cast<const float *>(o), 32 * c, 32, l, m_ref);
+          write_cols(reinterpret_cast<const float *>(o), c0, 32, l, m_ref);
         }
       }
     } else {
-      // every copy puts its sums and reference in the idle ring; then copy kp
-      // merges the R partials of columns [kp * HD/R, ..)
+      // every copy puts its sums and reference in the idle ring; then each
+      // warp merges the R partials of its share of the columns
       float *part = reinterpret_cast<float *>(sb + L::kOffRing);   // [R][groups][32][HD + 4]
       float *mine = part + ((kp * groups + g) * 32 + lane) * (HD + 4);
 #pragma unroll 1
-      for (int c = 0; c < HD / 32; ++c) {
+      for (int c = 0; c < HD / 64; ++c) {
+        const int c0 = half * (HD / 2) + 32 * c;
         uint32_t o[32];
-        tc::ld32(tO + 32 * c, o);
+        tc::ld32(tO + c0, o);
         tc::wait_ld();
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          *reinterpret_cast<float4 *>(mine + 32 * c + 4 * e) =
+          *reinterpret_cast<float4 *>(mine + c0 + 4 * e) =
               make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                           __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
       }
-      mine[HD] = l;
-      mine[HD + 1] = m_ref;
-      named_sync(3, kSoftmax);
+      if (half == 0) {
+        mine[HD] = l;
+        mine[HD + 1] = m_ref;
+      }
+      named_sync(3, 8 * 32);
       if (row_valid && !failed) {
-        const int cw = HD / R, cb = kp * cw;    // 16, 32 or 64 columns
+        const int cw = HD / (R * kHalves), cb = (kp * kHalves + half) * cw;    // 8, 16 or 32 columns
         float mt = -INFINITY;
         for (int c = 0; c < R; ++c) mt = fmaxf(mt, part[((c * groups + g) * 32 + lane) * (HD + 4) + HD + 1]);
-        float wc[4], lt = 0.f;
+        float lt = 0.f, v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = 0.f;
         for (int c = 0; c < R; ++c) {
           const float *pc = part + ((c * groups + g) * 32 + lane) * (HD + 4);
-          wc[c] = ex2(pc[HD + 1] - (mt == -INFINITY ? 0.f : mt));   // -inf reference -> 0
-          lt += wc[c] * pc[HD];
-        }
-        for (int q = 0; q < cw; q += 32) {
-          const int n = min(32, cw - q);        // a multiple of 16
-          float v[32];
+          const float wc = ex2(pc[HD + 1] - (mt == -INFINITY ? 0.f : mt));   // -inf reference -> 0
+          lt += wc * pc[HD];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = 0.f;
-          for (int c = 0; c < R; ++c) {
-            const float *src = part + ((c * groups + g) * 32 + lane) * (HD + 4) + cb + q;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (4 * e >= n) break;
-              const float4 p4 = *reinterpret_cast<const float4 *>(src + 4 * e);
-              v[4 * e] += wc[c] * p4.x; v[4 * e + 1] += wc[c] * p4.y;
-              v[4 * e + 2] += wc[c] * p4.z; v[4 * e + 3] += wc[c] * p4.w;
-            }
+          for (int e = 0; e < 8; ++e) {
+            if (4 * e >= cw) break;
+            const float4 p4 = *reinterpret_cast<const float4 *>(pc + cb + 4 * e);
+            v[4 * e] += wc * p4.x; v[4 * e + 1] += wc * p4.y;
+            v[4 * e + 2] += wc * p4.z; v[4 * e + 3] += wc * p4.w;
           }
-          write_cols(v, cb + q, n, lt, mt);
         }
+        write_cols(v, cb, cw, lt, mt);
       }
     }
   }
