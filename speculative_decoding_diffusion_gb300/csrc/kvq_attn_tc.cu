@@ -25,9 +25,11 @@
 // MMA of N = 128 takes 64, e4m3 at K = 32 like f16 at K = 16; issued by one
 // lane of a converged warp, whose addresses stay in uniform registers, 33 to
 // 43 cycles each -- from a branch of a single thread it is 55 or more).
-//   warp 0       keys: one 2 KB TMA box per page, swizzled for the MMA
-//   warp 6       values: one 2 KB bulk copy per page
-//   warp 1       TMEM owner, issues every MMA as its inputs are ready
+//   warp 0       one 2 KB copy per page: keys by TMA, swizzled for the MMA,
+//                values as they lie
+//   warp 6       scales: page ids and scale bytes well ahead, what they mean
+//                for a group of four blocks into shared memory
+//   warp 1       TMEM owner; issues the score MMAs; warp 15 the P V MMAs
 //   warps 2-5 and 11-14  softmax, two warps per 32 rows: one thread of each
 //                per row, half of the block's keys each (scores stay in
 //                registers from the maximum to the weights; the halves agree
@@ -56,7 +58,8 @@ constexpr int kKeys = 128;           // keys per block
 static_assert(kKeys == kBlockKeys, "split chunks are whole blocks");
 constexpr int kStages = 4;
 constexpr int kPagesPerBlock = kKeys / kPage;
-constexpr int kVWarp = 6, kDecodeWarp = 7, kSoftmaxB = 11, kWarps = 15;
+constexpr int kScaleWarp = 6, kDecodeWarp = 7, kSoftmaxB = 11, kPvWarp = 15, kWarps = 16;
+constexpr int kGroup = 4, kGroupSlots = 4;   // blocks whose scales go together; groups in flight
 constexpr int kThreads = kWarps * 32;
 constexpr int kPrep = 12 * 32;         // threads of the softmax and decode warps
 constexpr int kHalves = 2;            // softmax warps sharing 32 rows
@@ -73,7 +76,15 @@ enum { kBarKFull = 0, kBarVFull = kBarKFull + kStages, kBarKEmpty = kBarVFull + 
        kBarVEmpty = kBarKEmpty + kStages, kBarSFull = kBarVEmpty + kStages,
        kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 1,
        kBarVbFull = kBarPvDone + 2,
-       kBarQReady = kBarVbFull + 2, kBarKnReady = kBarQReady + 1, kNumBars = kBarKnReady + 1 };
+       kBarQReady = kBarVbFull + 2, kBarKnReady = kBarQReady + 1,
+       kBarGFull = kBarKnReady + 1, kBarGEmpty = kBarGFull + kGroupSlots, kNumBars = kBarGEmpty + kGroupSlots };
+
+// What the scales of four blocks mean; entry 8 q + i: page i of block q.
+struct Scales {
+  float k[8 * kGroup];                 // factor of a page's scores
+  uint32_t v[8 * kGroup];              // its values' power of two relative to 2^vref, f16 twice; 0: no page
+  float2 block[kGroup];                // factor of O before the block (vref moved), pages missing (bits)
+};
 
 template <int HD>
 struct Smem {
@@ -91,14 +102,17 @@ struct Smem {
   static constexpr int kOffVb = kOffRing + kStages * kStage;   // [2]
   static constexpr int kOffKn = kOffVb + 2 * kVb;           // rotated new keys, hi and lo
   static constexpr int kOffBar = kOffKn + 2 * kKn;
-  static constexpr int kOffTau = kOffBar + kNumBars * 8;
+  static constexpr int kOffTau = kOffBar + (kNumBars + 1) / 2 * 16;
   static constexpr int kOffRow = kOffTau + kMaxB * 4;       // rows' score factors
   static constexpr int kOffMax = kOffRow + kRows * 4;       // [2 blocks][2 halves][4 quadrants][32]: row maxima, sums
-  static constexpr int kOffMisc = kOffMax + 2 * kHalves * kRows * 4;   // tmem address, error flag, largest new |k| and |v|
-  static constexpr int kBytes = kOffMisc + 16;
+  static constexpr int kOffScales = kOffMax + 2 * kHalves * kRows * 4;
+  static constexpr int kOffMisc = kOffScales + kGroupSlots * (int)sizeof(Scales);   // tmem address, error flag, largest
+                                                            // new |k| and |v|, the last vref
+  static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;              // 1024-byte alignment slack
   static constexpr uint32_t kColQ = kColO + HD;             // q hi and lo: hd / 4 columns each
   static constexpr uint32_t kTmemCols = 512;
+  static_assert(kOffScales % 16 == 0 && sizeof(Scales) % 16 == 0, "16-byte reads of the scales");
   static_assert(kColQ + HD / 2 <= kTmemCols, "TMEM budget");
   static_assert(2 * kRows * HD <= kStage && 4 * kMaxNew * HD <= kStage && kRows * HD * 2 <= kVb, "first contents fit");
   static_assert(4 * 32 * (HD + 4) * 4 <= kStages * kStage, "epilogue exchange fits the ring");
@@ -194,13 +208,6 @@ __device__ __forceinline__ int next_vref(int vref, int emax) {
   return emax > vref + kVHead ? emax - kVLift : vref;
 }
 
-// Largest of the eight lanes of a block.
-__device__ __forceinline__ int block_max(int e) {
-#pragma unroll
-  for (int m = 4; m > 0; m >>= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, m));
-  return e;
-}
-
 // 2^k as f16, 0 below its range.
 __device__ __forceinline__ uint32_t f16_pow2(int k) {
   return k < -24 ? 0u : k < -14 ? 1u << (k + 24) : (uint32_t)(k + 15) << 10;
@@ -220,6 +227,8 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   int *flag_s = reinterpret_cast<int *>(sb + L::kOffMisc + 4);
   float *row_s = reinterpret_cast<float *>(sb + L::kOffRow);
   uint32_t *amax_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new keys, values
+  int *vref_s = reinterpret_cast<int *>(sb + L::kOffMisc + 16);
+  Scales *scales_s = reinterpret_cast<Scales *>(sb + L::kOffScales);
   grid_dep_launch();                         // the split merge may be scheduled
   const KvqWork w = kvq_work(a);
   if (!w.ok) return;                         // uniform: nothing to do here
@@ -235,34 +244,34 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   const int n_valid = kHalves * (R > 1 ? 4 : n_groups);
   const int32_t *bt = a.block_table + (int64_t)w.b * a.max_pages;
   const int64_t t0 = (int64_t)a.per * w.c0;  // first new token's row
-  // Page ids and scales are requested four blocks ahead of their use and
-  // looked at only then: under load such a read takes longer than a block,
-  // and a test right after it would hold the warp (3600 of the 3900 cycles a
-  // block first took).
+  // Page ids are requested four blocks ahead of their use and looked at only
+  // then: under load such a read takes longer than a block, and a test right
+  // after it would hold the warp.
   auto in_cache = [&](int page) { return page >= 0 && page < a.num_pages; };
-  // table entry of page `lane` of prompt block j (producers); -1: none
+  // table entry of page `lane` & 7 of prompt block j (lanes 0-15); -1: none
   auto block_page = [&](int j) {
-    const int key = w.k_begin + j * kKeys + lane * kPage;
-    return j < n_past && lane < kPagesPerBlock && key < w.k_end ? __ldg(bt + key / kPage) : -1;
+    const int key = w.k_begin + j * kKeys + (lane & 7) * kPage;
+    return j < n_past && lane < 2 * kPagesPerBlock && key < w.k_end ? __ldg(bt + key / kPage) : -1;
   };
   // table entry of page `lane` of the four prompt blocks 4 g ..; -1: none
   auto group_page = [&](int g) {
-    const int64_t key = w.k_begin + ((int64_t)g * 32 + lane) * kPage;
+    const int64_t key = w.k_begin + ((int64_t)g * 8 * kGroup + lane) * kPage;
     return key < w.k_end ? __ldg(bt + key / kPage) : -1;
   };
   // scale byte of page `page` and this head; kNoPage: none
   auto scale_byte = [&](const uint8_t *scale, int page) {
     return in_cache(page) ? (int)__ldg(scale + (int64_t)page * a.Hkv + w.kvh) : kNoPage;
   };
-  int pages[kStages], group0 = -1;
+  int pages[kStages];
   // index among the threads that rotate and split rows
-  const int pt = threadIdx.x - (warp < kVWarp ? 64 : 96);
+  const int pt = threadIdx.x - (warp < kScaleWarp ? 64 : 96);
   constexpr int CH = HD / 8;                 // 16-byte chunks of a bf16 row
-  if (warp == 0 || warp == kVWarp) {
-    if (warp == 0 && lane == 0) prefetch_tmap(&tmK);
+  const bool prep_warp = warp >= 2 && warp != kScaleWarp && warp != kPvWarp;
+  if (warp == 0) {
+    if (lane == 0) prefetch_tmap(&tmK);
 #pragma unroll
     for (int d = 0; d < kStages; ++d) pages[d] = block_page(d);
-  } else if (warp != 1) {
+  } else if (prep_warp) {
     // the query rows and the new tokens' keys and values come first of all,
     // ahead of the stream of codes
     const __nv_bfloat16 *qs = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
@@ -279,7 +288,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         copy16_async(dst, (const __nv_bfloat16 *)a.k_new + (t0 + j) * a.k_row + w.kvh * HD + c * 8, true);
         copy16_async(dst + kMaxNew * HD * 2, (const __nv_bfloat16 *)a.v_new + (t0 + j) * a.v_row + w.kvh * HD + c * 8, true);
       }
-    group0 = group_page(0);
   }
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -295,6 +303,10 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       mbar_init(bar(kBarVbFull + i), 4);
     }
     mbar_init(bar(kBarPFull), n_valid);
+    for (int i = 0; i < kGroupSlots; ++i) {
+      mbar_init(bar(kBarGFull + i), 1);
+      mbar_init(bar(kBarGEmpty + i), n_valid + 4);
+    }
     mbar_init(bar(kBarQReady), 4);
     mbar_init(bar(kBarKnReady), 4);
     *flag_s = 0;
@@ -315,8 +327,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   // rotated elements stay below sqrt 2 of the largest
   auto new_kexp = [&]() { return scale_exponent(__uint_as_float(amax_s[0]) * a.plan.mul * 1.41422f, -64, 119); };
   auto new_vref = [&]() { return scale_exponent(__uint_as_float(amax_s[1]), -64, 119) - kVLift; };
-  // exponent of a value scale; kNoRef where there is none or it is NaN
-  auto v_exp = [&](int byte) { return byte < 0 || byte == kScaleNan ? kNoRef : min(byte - kScaleBias, kExpHi); };
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
   // The softmax and decode warps together rotate the query rows into two e4m3
   // parts and, in the CTA that owns the new tokens, their keys likewise and
@@ -415,10 +425,9 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     named_sync(1, kPrep);
   };
 
-  if (warp == 0 || warp == kVWarp) {
-    // --------------------------------------------------------- producers
-    const bool kside = warp == 0;
-    const int full0 = kside ? kBarKFull : kBarVFull, empty0 = kside ? kBarKEmpty : kBarVEmpty;
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer
+    const bool kside = lane < kPagesPerBlock;
     bool ok = true;
     for (int j0 = 0; ok && j0 < n_past; j0 += kStages) {
 #pragma unroll
@@ -426,38 +435,86 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         const int j = j0 + s;
         if (j >= n_past) break;
         const int page = pages[s];
-        const int n_pages = __popc(__ballot_sync(0xffffffffu, in_cache(page)));
+        const int n_pages = __popc(__ballot_sync(0xffffffffu, kside && in_cache(page)));
         // (the last two stages hold the rows of this CTA until they are split
         // and in TMEM)
-        if ((j >= kStages && !mbar_wait_warp(bar(empty0 + s), ((j / kStages) - 1) & 1, a.polls)) ||
+        if ((j >= kStages && (!mbar_wait_warp(bar(kBarKEmpty + s), ((j / kStages) - 1) & 1, a.polls) ||
+                              !mbar_wait_warp(bar(kBarVEmpty + s), ((j / kStages) - 1) & 1, a.polls))) ||
             ((j == kStages - 2 || j == kStages - 1) && !mbar_wait_warp(bar(kBarQReady), 0, a.polls))) {
           if (lane == 0) give_up();
           ok = false;
           break;
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), n_pages * kPage * HD);
-        __syncwarp();
-        if (in_cache(page)) {
-          const uint32_t dst = base + L::kOffRing + s * L::kStage + (kside ? 0 : L::kCodes) + lane * kPage * HD;
-          if (kside)
-            tma_load_4d(dst, &tmK, bar(full0 + s), 0, 0, w.kvh, page);
-          else
-            bulk_load(dst, a.v_cache + ((int64_t)page * a.Hkv + w.kvh) * kPage * HD, kPage * HD, bar(full0 + s));
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(kBarKFull + s), n_pages * kPage * HD);
+          mbar_arrive_expect_tx(bar(kBarVFull + s), n_pages * kPage * HD);
         }
-        if (kside && lane < kPagesPerBlock && !in_cache(page) && w.k_begin + j * kKeys + lane * kPage < w.k_end)
+        __syncwarp();
+        const uint32_t dst = base + L::kOffRing + s * L::kStage + (lane & 7) * kPage * HD;
+        if (in_cache(page)) {
+          if (kside)
+            tma_load_4d(dst, &tmK, bar(kBarKFull + s), 0, 0, w.kvh, page);
+          else
+            bulk_load(dst + L::kCodes, a.v_cache + ((int64_t)page * a.Hkv + w.kvh) * kPage * HD, kPage * HD,
+                      bar(kBarVFull + s));
+        } else if (kside && w.k_begin + j * kKeys + lane * kPage < w.k_end) {
           raise_status(a.status, kStatusBadInput);
+        }
         issued = j + 1;
         pages[s] = block_page(j + kStages);
       }
     }
+  } else if (warp == kScaleWarp) {
+    // ------------------------------------------------------------- scales
+    // lane 8 q + i: page i of block 4 g + q; bytes requested a group ahead,
+    // page ids two
+    int page = group_page(0);
+    int kb = scale_byte(a.k_scale, page), vb = scale_byte(a.v_scale, page);
+    page = group_page(1);
+    int vref = kNoRef;
+    bool ok = true;
+    if (fresh) {
+      ok = mbar_wait_warp(bar(kBarKnReady), 0, a.polls);
+      vref = new_vref();
+    }
+    const int groups = (n_past + kGroup - 1) / kGroup;
+    for (int g = 0; ok && g < groups; ++g) {
+      const int slot = g % kGroupSlots;
+      if (g >= kGroupSlots && !mbar_wait_warp(bar(kBarGEmpty + slot), ((g / kGroupSlots) - 1) & 1, a.polls)) {
+        ok = false;
+        break;
+      }
+      Scales &s = scales_s[slot];
+      int emax = vb < 0 || vb == kScaleNan ? kNoRef : min(vb - kScaleBias, kExpHi);   // of the lane's block
+      const int mine = emax;
+#pragma unroll
+      for (int m = 4; m > 0; m >>= 1) emax = max(emax, __shfl_xor_sync(0xffffffffu, emax, m));
+      const uint32_t missing = __ballot_sync(0xffffffffu, kb == kNoPage);
+      s.k[lane] = scale_value(kb & 255);
+#pragma unroll
+      for (int q = 0; q < kGroup; ++q) {
+        const int was = vref;
+        vref = next_vref(vref, __shfl_sync(0xffffffffu, emax, 8 * q));
+        if (lane >> 3 == q)
+          s.v[lane] = (vb < 0 ? 0u : vb == kScaleNan ? 0x7e00u : f16_pow2(mine - vref)) * 0x10001u;
+        if (lane == 8 * q)
+          s.block[q] = make_float2(vref == was ? 1.f : was == kNoRef ? 0.f : pow2i(max(was - vref, -126)),
+                                   __uint_as_float((missing >> (8 * q)) & 0xffu));
+      }
+      if (lane == 0) *vref_s = vref;
+      kb = scale_byte(a.k_scale, page);
+      vb = scale_byte(a.v_scale, page);
+      page = group_page(g + 2);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarGFull + slot));
+    }
+    if (!ok && lane == 0) give_up();
   } else if (warp == 1) {
-    // ---------------------------------------------------------- MMA issuer
+    // ------------------------------------------------------------- scores
     // The whole warp keeps the loop (uniform addresses), one lane issues.
     constexpr uint32_t idS8 = tc::idesc_e4m3(kRows, kKeys);
     constexpr uint32_t idSn = tc::idesc_e4m3(kRows, kMaxNew);
-    constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 1);
     const uint64_t dK0 = HD == 128 ? tc::smem_desc_sw128(base, 16, 1024) : tc::smem_desc_sw64(base, 16, 512);
-    const uint64_t dV0 = tc::smem_desc_sw128(base + L::kOffVb, L::kHalf, 1024);
     // scores of the part q0 of the query rows against the tile at offset off
     auto score = [&](uint32_t tS, uint32_t q0, uint32_t off, uint32_t idesc, bool more) {
 #pragma unroll
@@ -466,67 +523,55 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     };
     const uint32_t qhi = tmem + L::kColQ, qlo = qhi + HD / 4;
     bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
-    int ns = 0, np = 0;
-    uint64_t idle = 0;
-    while (ok && np < n_blocks) {
-      bool progressed = false;
-      if (ns < n_blocks) {
-        const int tb = ns & 1, jp = ns - fresh, s = jp & (kStages - 1);
-        const bool is_new = jp < 0;
-        if (__all_sync(0xffffffffu, (is_new ? mbar_test(bar(kBarKnReady), 0)
-                                            : mbar_test(bar(kBarKFull + s), (jp / kStages) & 1)) &&
-                                        (ns < 2 || mbar_test(bar(kBarSEmpty + tb), ((ns >> 1) - 1) & 1)))) {
-          tc::fence_after_sync();
-          const uint32_t tS = tmem + kColS + tb * kKeys;
-          if (tc::elect_one()) {
-            if (is_new) {                    // both parts of q against both of the new keys
-              score(tS, qhi, L::kOffKn, idSn, false);
-              score(tS, qlo, L::kOffKn, idSn, true);
-              score(tS, qhi, L::kOffKn + L::kKn, idSn, true);
-              score(tS, qlo, L::kOffKn + L::kKn, idSn, true);
-              tc::commit(bar(kBarSFull + tb));
-            } else {
-              score(tS, qhi, s * L::kStage, idS8, false);
-              score(tS, qlo, s * L::kStage, idS8, true);
-              tc::commit(bar(kBarSFull + tb));
-              tc::commit(bar(kBarKEmpty + s));
-            }
-          }
-          __syncwarp();
-          ++ns;
-          progressed = true;
+    for (int j = 0; ok && j < n_blocks; ++j) {
+      const int tb = j & 1, jp = j - fresh, s = jp & (kStages - 1);
+      ok = (jp < 0 ? mbar_wait_warp(bar(kBarKnReady), 0, a.polls)
+                   : mbar_wait_warp(bar(kBarKFull + s), (jp / kStages) & 1, a.polls)) &&
+           (j < 2 || mbar_wait_warp(bar(kBarSEmpty + tb), ((j >> 1) - 1) & 1, a.polls));
+      if (!ok) break;
+      tc::fence_after_sync();
+      const uint32_t tS = tmem + kColS + tb * kKeys;
+      if (tc::elect_one()) {
+        if (jp < 0) {                        // both parts of q against both of the new keys
+          score(tS, qhi, L::kOffKn, idSn, false);
+          score(tS, qlo, L::kOffKn, idSn, true);
+          score(tS, qhi, L::kOffKn + L::kKn, idSn, true);
+          score(tS, qlo, L::kOffKn + L::kKn, idSn, true);
+          tc::commit(bar(kBarSFull + tb));
+        } else {
+          score(tS, qhi, s * L::kStage, idS8, false);
+          score(tS, qlo, s * L::kStage, idS8, true);
+          tc::commit(bar(kBarSFull + tb));
+          tc::commit(bar(kBarKEmpty + s));
         }
       }
-      if (np < ns) {
-        const int tb = np & 1;
-        if (__all_sync(0xffffffffu, mbar_test(bar(kBarPFull), np & 1) && mbar_test(bar(kBarVbFull + tb), (np >> 1) & 1))) {
-          tc::fence_after_sync();
-          const int jp = np - fresh;
-          const int depth = jp < 0 ? n_pad : min(kKeys, (w.k_end - w.k_begin - jp * kKeys + 15) & ~15);
-          const uint64_t dV = dV0 + ((uint32_t)(tb * L::kVb) >> 4);
-          if (tc::elect_one()) {
-            if (depth == kKeys) {
+      __syncwarp();
+    }
+    if (!ok && lane == 0) give_up();
+  } else if (warp == kPvWarp) {
+    // ---------------------------------------------------------------- P V
+    constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 1);
+    const uint64_t dV0 = tc::smem_desc_sw128(base + L::kOffVb, L::kHalf, 1024);
+    bool ok = true;
+    for (int j = 0; j < n_blocks; ++j) {
+      const int tb = j & 1, jp = j - fresh;
+      ok = mbar_wait_warp(bar(kBarVbFull + tb), (j >> 1) & 1, a.polls) && mbar_wait_warp(bar(kBarPFull), j & 1, a.polls);
+      if (!ok) break;
+      tc::fence_after_sync();
+      const int depth = jp < 0 ? n_pad : min(kKeys, (w.k_end - w.k_begin - jp * kKeys + 15) & ~15);
+      const uint64_t dV = dV0 + ((uint32_t)(tb * L::kVb) >> 4);
+      if (tc::elect_one()) {
+        if (depth == kKeys) {
 #pragma unroll
-              for (int kk = 0; kk < kKeys / 16; ++kk)
-                tc::mma_bf16_ts(tmem + kColO, tmem + kColP + kk * 8, dV + kk * 128, idO, np > 0 || kk > 0);
-            } else {
-              for (int kk = 0; kk < depth / 16; ++kk)
-                tc::mma_bf16_ts(tmem + kColO, tmem + kColP + kk * 8, dV + kk * 128, idO, np > 0 || kk > 0);
-            }
-            tc::commit(bar(kBarPvDone + tb));
-          }
-          __syncwarp();
-          ++np;
-          progressed = true;
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            tc::mma_bf16_ts(tmem + kColO, tmem + kColP + kk * 8, dV + kk * 128, idO, j > 0 || kk > 0);
+        } else {
+          for (int kk = 0; kk < depth / 16; ++kk)
+            tc::mma_bf16_ts(tmem + kColO, tmem + kColP + kk * 8, dV + kk * 128, idO, j > 0 || kk > 0);
         }
+        tc::commit(bar(kBarPvDone + tb));
       }
-      if (progressed) {
-        idle = 0;
-      } else if (++idle > ((uint64_t)a.polls << 4)) {  // bounded: give up, flag, drain
-        ok = false;
-      } else if (idle > 8) {
-        __nanosleep(32);                     // leave the issue slots to the other warps
-      }
+      __syncwarp();
     }
     if (!ok && lane == 0) give_up();
   } else if (warp >= kDecodeWarp && warp < kSoftmaxB) {
@@ -537,23 +582,12 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       mbar_arrive(bar(kBarKnReady));
       mbar_arrive(bar(kBarVbFull));
     }
-    // value tiles: this warp's rows are pages 2 dw and 2 dw + 1 of a block;
-    // lane 8 q + i keeps the scale of page i of block 4 g + q, requested with
-    // the group before it (its id two groups ahead)
-    int vref = fresh ? new_vref() : kNoRef, mine = kNoPage, emax = kNoRef;
-    int next = scale_byte(a.v_scale, group0);
-    group0 = group_page(1);
+    // value tiles: this warp's rows are pages 2 dw and 2 dw + 1 of a block
     bool ok = true;
     for (int jp = 0; jp < n_past; ++jp) {
-      const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1);
-      if ((jp & 3) == 0) {
-        mine = next;
-        next = scale_byte(a.v_scale, group0);
-        group0 = group_page(jp / 4 + 2);
-        emax = block_max(v_exp(mine));
-      }
-      vref = next_vref(vref, __shfl_sync(0xffffffffu, emax, 8 * (jp & 3)));
-      const uint32_t pow = mine < 0 ? 0u : mine == kScaleNan ? 0x7e00u : f16_pow2(v_exp(mine) - vref);
+      const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1), q = jp % kGroup, slot = jp / kGroup % kGroupSlots;
+      if (q == 0 && !mbar_wait_warp(bar(kBarGFull + slot), (jp / (kGroup * kGroupSlots)) & 1, a.polls)) { ok = false; break; }
+      const uint2 mul2 = *reinterpret_cast<const uint2 *>(scales_s[slot].v + 8 * q + 2 * dw);
       if (!mbar_wait_warp(bar(kBarVFull + s), (jp / kStages) & 1, a.polls) ||
           (j >= 2 && !mbar_wait_warp(bar(kBarPvDone + tb), ((j >> 1) - 1) & 1, a.polls))) { ok = false; break; }
       const int valid = w.k_end - w.k_begin - jp * kKeys;    // rows from here on hold no key
@@ -563,7 +597,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
 #pragma unroll
       for (int i = 0; i < 32 / RPI; ++i) {
         const int row = 32 * dw + i * RPI + lane / C, c = lane % C;
-        const uint32_t m = __shfl_sync(0xffffffffu, pow, 8 * (jp & 3) + 2 * dw + (i * RPI) / kPage) * 0x10001u;
+        const uint32_t m = i * RPI < kPage ? mul2.x : mul2.y;
         const __half2 mul = *reinterpret_cast<const __half2 *>(&m);
         const uint4 x = *reinterpret_cast<const uint4 *>(src + row * HD + c * 16);
         uint4 lo = make_uint4(decode2(x.x & 0xffffu, mul), decode2(x.x >> 16, mul), decode2(x.y & 0xffffu, mul), decode2(x.y >> 16, mul));
@@ -581,6 +615,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       if (lane == 0) {
         mbar_arrive(bar(kBarVbFull + tb));
         mbar_arrive(bar(kBarVEmpty + s));
+        if (q == kGroup - 1 || jp == n_past - 1) mbar_arrive(bar(kBarGEmpty + slot));
       }
     }
     if (!ok && lane == 0) give_up();
@@ -631,13 +666,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     float m_ref = -INFINITY, l = 0.f;
     bool ok = true;
     int j = 0;
-    // lane 8 q + i: scales of page i of block 4 g + q, requested with the
-    // group before it (the page ids two groups ahead)
-    int next_k = scale_byte(a.k_scale, group0), next_v = scale_byte(a.v_scale, group0);
-    group0 = group_page(1);
-    float page_scale = 0.f;
-    uint32_t absent = 0u;
-    int emax = kNoRef, vref = fresh ? new_vref() : kNoRef;
     const float new_scale = fresh ? rscale * pow2i(new_kexp()) : 0.f;
     // the key loop, compiled once per copy count
     auto key_loop = [&](auto rc) {
@@ -650,28 +678,28 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         const int tb = j & 1, jp = j - fresh;
         const bool is_new = jp < 0;
         const uint32_t tS = trow + kColS + tb * kKeys + k_lo;
-        const int vref_was = vref, q8 = 8 * (jp & 3);
-        if (!is_new) {
-          if ((jp & 3) == 0) {
-            absent = __ballot_sync(0xffffffffu, next_k == kNoPage);
-            page_scale = scale_value(next_k & 255);
-            emax = block_max(v_exp(next_v));
-            next_k = scale_byte(a.k_scale, group0);
-            next_v = scale_byte(a.v_scale, group0);
-            group0 = group_page(jp / 4 + 2);
-          }
-          vref = next_vref(vref, __shfl_sync(0xffffffffu, emax, q8));
-        }
+        const int q = jp & (kGroup - 1), slot = jp / kGroup % kGroupSlots;
+        if (!is_new && q == 0) ok = ok && mbar_wait_warp(bar(kBarGFull + slot), (jp / (kGroup * kGroupSlots)) & 1, a.polls);
         // factor of this row's scores in each 16 columns (a page)
         float f[KW / 16];
+        float2 block = make_float2(1.f, 0.f);
+        if (is_new) {
 #pragma unroll
-        for (int i = 0; i < KW / 16; ++i) {
-          const float x = __shfl_sync(0xffffffffu, page_scale, q8 + k_lo / 16 + i);
-          f[i] = is_new ? new_scale : rscale * x;
+          for (int i = 0; i < KW / 16; ++i) f[i] = new_scale;
+        } else {
+          const float *k = scales_s[slot].k + 8 * q + k_lo / 16;
+          block = scales_s[slot].block[q];
+          if constexpr (KW == 64) {
+            const float4 x = *reinterpret_cast<const float4 *>(k);
+            f[0] = x.x * rscale; f[1] = x.y * rscale; f[2] = x.z * rscale; f[3] = x.w * rscale;
+          } else {
+#pragma unroll
+            for (int i = 0; i < KW / 16; ++i) f[i] = k[i] * rscale;
+          }
         }
         // keys that count: all of a whole block's, else one bit each
         const int valid = is_new ? 0 : w.k_end - w.k_begin - jp * kKeys;
-        const uint32_t gone = (absent >> q8) & 0xffu;
+        const uint32_t gone = __float_as_uint(block.y);
         const bool whole = !is_new && valid >= kKeys && gone == 0u;
         ok = ok && mbar_wait_warp(bar(kBarSFull + tb), (j >> 1) & 1, a.polls);
         tc::fence_after_sync();
@@ -739,8 +767,8 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         if (j > 0) {
           if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; continue; }
           tc::fence_after_sync();
-          if (vref != vref_was || __any_sync(0xffffffffu, move)) {   // this half of O's columns
-            const float shrink = alpha * (vref == vref_was ? 1.f : vref_was == kNoRef ? 0.f : pow2i(max(vref_was - vref, -126)));
+          if (__any_sync(0xffffffffu, move || block.x != 1.f)) {   // this half of O's columns
+            const float shrink = alpha * block.x;
 #pragma unroll 1
             for (int c = 0; c < HD / 32; ++c) {
               uint32_t o[16];
@@ -762,7 +790,10 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kBarPFull));
+        if (lane == 0) {
+          mbar_arrive(bar(kBarPFull));
+          if (!is_new && (q == kGroup - 1 || jp == n_past - 1)) mbar_arrive(bar(kBarGEmpty + slot));
+        }
       }
     };
     if (R == 4) key_loop(IntC<4>{});
@@ -776,7 +807,8 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     const int64_t orow = (t0 + tok) * a.Hq + w.kvh * a.G + (row_valid ? grow % a.G : 0);
     // columns [c0, c0 + n), n <= 32, of this thread's row: sums v relative to reference
     // mr and 2^vref, weights' sum lt
-    const float vup = vref == kNoRef ? 1.f : pow2i(vref);
+    const int vref = n_past > 0 ? *(volatile int *)vref_s : new_vref();
+    const float vup = vref == kNoRef || failed ? 1.f : pow2i(vref);
     auto write_cols = [&](const float *v, int c0, int n, float lt, float mr) {
       if (w.n_splits == 1) {
         const float inv = lt == 0.f ? 0.f : vup / lt;
@@ -862,9 +894,11 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   __syncthreads();
   // after a wait that gave up, the copies still in flight land before the CTA
   // can exit (default limit)
-  if ((warp == 0 || warp == kVWarp) && *(volatile int *)flag_s)
-    for (int j = max(0, issued - kStages); j < issued; ++j)
-      (void)mbar_wait_warp(bar((warp == 0 ? kBarKFull : kBarVFull) + j % kStages), (j / kStages) & 1);
+  if (warp == 0 && *(volatile int *)flag_s)
+    for (int j = max(0, issued - kStages); j < issued; ++j) {
+      (void)mbar_wait_warp(bar(kBarKFull + j % kStages), (j / kStages) & 1);
+      (void)mbar_wait_warp(bar(kBarVFull + j % kStages), (j / kStages) & 1);
+    }
   if (warp == 1) {
     tc::fence_after_sync();
     tc::dealloc(tmem, L::kTmemCols);
