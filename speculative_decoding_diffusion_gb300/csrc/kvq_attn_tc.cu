@@ -7,18 +7,15 @@
 // rate, so two products cost what one in bf16 does and no key is decoded).
 // The page's key scale multiplies the score in the softmax.  The weights
 // cannot be split like that (their range is too wide for e4m3), so four warps
-// decode the value tiles to f16 and O += P V runs in f16 with weights of 11
-// bits: bf16 weights would cost as much error as rounding the output does
-// (64 x 4096: 2.5e-3 of the result against 64 bits, 1.7e-3 of it the
-// output's).  Both stay inside f16's range by powers of two: a row's weights
-// are 2^(s - m + 7) with m at most 8 stale (2^15 at most, 2^-25 the smallest),
-// and values are taken relative to 2^vref, vref at most 6 below the largest
-// page scale so far (28672 at most; what a smaller page loses is 2^-37 of the
-// largest values).  vref follows from the page scales alone, so the decode
-// and softmax warps each keep it.  The new tokens are a block of their own
-// ahead of the prompt: keys rotated here, S from f16 q and k, each scaled by
-// a power of two.
-//
+// unpack the value codes to f16 (exact) and O += P V runs in f16.  A page's
+// value scale 2^ve goes into its keys' weights: with t = s + ve and a row
+// reference M over t, p = 2^(t - M + 7) multiplies the codes themselves, and
+// the row's sum takes 2^-ve times the sum of a page's weights -- nothing per
+// key or value.  M is at most 8 stale, so p <= 2^15 fits f16, whose 11 bits
+// keep the error against 64 bits at 1.9e-3 of the result, 1.7e-3 of it the
+// output's own rounding (bf16 weights: 2.5e-3).  The new tokens are a block of
+// their own ahead of the prompt: keys rotated and split here, values as f16
+// relative to a power of two that is their ve.
 // One CTA per (key split, KV head x 128-row tile, sequence); rows stack new
 // tokens x heads of the group, so a cache byte is read once for all of them.
 // HBM bounds it: 32 KB per 128-key block against 1024 tensor-core cycles (an
@@ -65,8 +62,6 @@ constexpr int kPrep = 12 * 32;         // threads of the softmax and decode warp
 constexpr int kHalves = 2;            // softmax warps sharing 32 rows
 constexpr float kHeadroom = 8.f;     // log2 units a row max may grow before O is rescaled
 constexpr float kLift = 7.f;         // log2 of the largest weight right after that
-constexpr int kVLift = 3, kVHead = 6;   // page scales over vref: right after it moved, at most
-constexpr int kNoRef = -1000;        // vref before the first value
 constexpr int kNoPage = -1;          // instead of a scale byte
 constexpr uint32_t kColS = 0;        // two score tiles: columns 0 and kKeys
 constexpr uint32_t kColP = 2 * kKeys;   // weights as f16, two keys a column
@@ -81,9 +76,9 @@ enum { kBarKFull = 0, kBarVFull = kBarKFull + kStages, kBarKEmpty = kBarVFull + 
 
 // What the scales of four blocks mean; entry 8 q + i: page i of block q.
 struct Scales {
-  float k[8 * kGroup];                 // factor of a page's scores
-  uint32_t v[8 * kGroup];              // its values' power of two relative to 2^vref, f16 twice; 0: no page
-  float2 block[kGroup];                // factor of O before the block (vref moved), pages missing (bits)
+  float2 kv[8 * kGroup];               // factor of a page's scores; ve
+  float inv[8 * kGroup];               // 2^-ve
+  uint32_t gone[kGroup];               // pages missing from the block (bits)
 };
 
 template <int HD>
@@ -107,8 +102,8 @@ struct Smem {
   static constexpr int kOffMax = kOffRow + kRows * 4;       // [2 blocks][2 halves][4 quadrants][32]: row maxima, sums
   static constexpr int kOffScales = kOffMax + 2 * kHalves * kRows * 4;
   static constexpr int kOffMisc = kOffScales + kGroupSlots * (int)sizeof(Scales);   // tmem address, error flag, largest
-                                                            // new |k| and |v|, the last vref
-  static constexpr int kBytes = kOffMisc + 32;
+                                                            // new |k| and |v|
+  static constexpr int kBytes = kOffMisc + 16;
   static constexpr int kAlloc = kBytes + 1024;              // 1024-byte alignment slack
   static constexpr uint32_t kColQ = kColO + HD;             // q hi and lo: hd / 4 columns each
   static constexpr uint32_t kTmemCols = 512;
@@ -196,21 +191,39 @@ __device__ __forceinline__ void split8(const float *x, uint2 &hi, uint2 &lo) {
   lo = make_uint2(l[0] | l[1] << 16, l[2] | l[3] << 16);
 }
 
-// Two e4m3 codes (low 16 bits) as f16 (exact) times a power of two.
-__device__ __forceinline__ uint32_t decode2(uint32_t codes, __half2 mul) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
-  const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), mul);
-  return *reinterpret_cast<const uint32_t *>(&y);
+// Four e4m3 codes as two f16 pairs (exact).
+__device__ __forceinline__ uint2 unpack4(uint32_t codes) {
+  uint2 h;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "mov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(h.x), "=r"(h.y)
+      : "r"(codes));
+  return h;
 }
 
-// vref after a block whose largest page scale exponent is emax (kNoRef: none).
-__device__ __forceinline__ int next_vref(int vref, int emax) {
-  return emax > vref + kVHead ? emax - kVLift : vref;
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
-// 2^k as f16, 0 below its range.
-__device__ __forceinline__ uint32_t f16_pow2(int k) {
-  return k < -24 ? 0u : k < -14 ? 1u << (k + 24) : (uint32_t)(k + 15) << 10;
+// Two fp32 operations in one instruction (half the issue slots).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)),
+        "l"(*reinterpret_cast<uint64_t *>(&c)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t *>(&a)), "l"(*reinterpret_cast<uint64_t *>(&b)));
+  return *reinterpret_cast<float2 *>(&d);
 }
 
 template <int HD>
@@ -227,7 +240,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   int *flag_s = reinterpret_cast<int *>(sb + L::kOffMisc + 4);
   float *row_s = reinterpret_cast<float *>(sb + L::kOffRow);
   uint32_t *amax_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new keys, values
-  int *vref_s = reinterpret_cast<int *>(sb + L::kOffMisc + 16);
   Scales *scales_s = reinterpret_cast<Scales *>(sb + L::kOffScales);
   grid_dep_launch();                         // the split merge may be scheduled
   const KvqWork w = kvq_work(a);
@@ -326,7 +338,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   // powers of two that the new tokens' keys and values are taken relative to:
   // rotated elements stay below sqrt 2 of the largest
   auto new_kexp = [&]() { return scale_exponent(__uint_as_float(amax_s[0]) * a.plan.mul * 1.41422f, -64, 119); };
-  auto new_vref = [&]() { return scale_exponent(__uint_as_float(amax_s[1]), -64, 119) - kVLift; };
+  auto new_vexp = [&]() { return scale_exponent(__uint_as_float(amax_s[1]), -64, 119); };
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
   // The softmax and decode warps together rotate the query rows into two e4m3
   // parts and, in the CTA that owns the new tokens, their keys likewise and
@@ -396,7 +408,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     }
     if (fresh) {                             // zeros up to the MMA's depth
       named_sync(1, kPrep);                  // the query rows are read; the magnitudes are there
-      const float kdown = pow2i(-new_kexp()), vdown = pow2i(-new_vref());
+      const float kdown = pow2i(-new_kexp()), vdown = pow2i(-new_vexp());
 #pragma unroll 1
       for (int e = pt; e < n_pad * CH; e += kPrep) {
         const int j = e / CH, c = e % CH;
@@ -471,12 +483,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     int page = group_page(0);
     int kb = scale_byte(a.k_scale, page), vb = scale_byte(a.v_scale, page);
     page = group_page(1);
-    int vref = kNoRef;
     bool ok = true;
-    if (fresh) {
-      ok = mbar_wait_warp(bar(kBarKnReady), 0, a.polls);
-      vref = new_vref();
-    }
     const int groups = (n_past + kGroup - 1) / kGroup;
     for (int g = 0; ok && g < groups; ++g) {
       const int slot = g % kGroupSlots;
@@ -485,23 +492,12 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         break;
       }
       Scales &s = scales_s[slot];
-      int emax = vb < 0 || vb == kScaleNan ? kNoRef : min(vb - kScaleBias, kExpHi);   // of the lane's block
-      const int mine = emax;
-#pragma unroll
-      for (int m = 4; m > 0; m >>= 1) emax = max(emax, __shfl_xor_sync(0xffffffffu, emax, m));
       const uint32_t missing = __ballot_sync(0xffffffffu, kb == kNoPage);
-      s.k[lane] = scale_value(kb & 255);
-#pragma unroll
-      for (int q = 0; q < kGroup; ++q) {
-        const int was = vref;
-        vref = next_vref(vref, __shfl_sync(0xffffffffu, emax, 8 * q));
-        if (lane >> 3 == q)
-          s.v[lane] = (vb < 0 ? 0u : vb == kScaleNan ? 0x7e00u : f16_pow2(mine - vref)) * 0x10001u;
-        if (lane == 8 * q)
-          s.block[q] = make_float2(vref == was ? 1.f : was == kNoRef ? 0.f : pow2i(max(was - vref, -126)),
-                                   __uint_as_float((missing >> (8 * q)) & 0xffu));
-      }
-      if (lane == 0) *vref_s = vref;
+      const int ve = min(vb - kScaleBias, kExpHi);
+      const bool nan = vb < 0 || vb == kScaleNan;
+      s.kv[lane] = make_float2(scale_value(kb & 255), nan ? __uint_as_float(0x7fc00000u) : (float)ve);
+      s.inv[lane] = pow2i(nan ? 0 : min(-ve, 127));
+      if (lane < kGroup) s.gone[lane] = (missing >> (8 * lane)) & 0xffu;
       kb = scale_byte(a.k_scale, page);
       vb = scale_byte(a.v_scale, page);
       page = group_page(g + 2);
@@ -583,32 +579,34 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       mbar_arrive(bar(kBarVbFull));
     }
     // value tiles: this warp's rows are pages 2 dw and 2 dw + 1 of a block
+    constexpr int C = HD / 8, RPI = 32 / C;                  // 8-byte chunks of a row; rows an iteration
+    const int c = lane % C, r0 = 32 * dw + lane / C;
     bool ok = true;
     for (int jp = 0; jp < n_past; ++jp) {
       const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1), q = jp % kGroup, slot = jp / kGroup % kGroupSlots;
       if (q == 0 && !mbar_wait_warp(bar(kBarGFull + slot), (jp / (kGroup * kGroupSlots)) & 1, a.polls)) { ok = false; break; }
-      const uint2 mul2 = *reinterpret_cast<const uint2 *>(scales_s[slot].v + 8 * q + 2 * dw);
       if (!mbar_wait_warp(bar(kBarVFull + s), (jp / kStages) & 1, a.polls) ||
           (j >= 2 && !mbar_wait_warp(bar(kBarPvDone + tb), ((j >> 1) - 1) & 1, a.polls))) { ok = false; break; }
       const int valid = w.k_end - w.k_begin - jp * kKeys;    // rows from here on hold no key
-      const uint8_t *src = sb + L::kOffRing + s * L::kStage + L::kCodes;
-      uint8_t *dst = sb + L::kOffVb + tb * L::kVb;
-      constexpr int C = HD / 16, RPI = 32 / C;               // 16-byte chunks of a row; rows an iteration
+      const uint32_t gone = scales_s[slot].gone[q];
+      const uint8_t *src = sb + L::kOffRing + s * L::kStage + L::kCodes + r0 * HD + c * 8;
+      uint8_t *dst = sb + L::kOffVb + tb * L::kVb + (c >> 3) * L::kHalf;
+      if (valid >= kKeys && gone == 0u) {
 #pragma unroll
-      for (int i = 0; i < 32 / RPI; ++i) {
-        const int row = 32 * dw + i * RPI + lane / C, c = lane % C;
-        const uint32_t m = i * RPI < kPage ? mul2.x : mul2.y;
-        const __half2 mul = *reinterpret_cast<const __half2 *>(&m);
-        const uint4 x = *reinterpret_cast<const uint4 *>(src + row * HD + c * 16);
-        uint4 lo = make_uint4(decode2(x.x & 0xffffu, mul), decode2(x.x >> 16, mul), decode2(x.y & 0xffffu, mul), decode2(x.y >> 16, mul));
-        uint4 hi = make_uint4(decode2(x.z & 0xffffu, mul), decode2(x.z >> 16, mul), decode2(x.w & 0xffffu, mul), decode2(x.w >> 16, mul));
-        if (row >= valid || m == 0u) lo = hi = make_uint4(0, 0, 0, 0);   // no key, or no page
-        uint8_t *tile = dst + (c >> 2) * L::kHalf;
-        const int ch = 2 * (c & 3);
-        // the two 64-column halves store their chunks in opposite order: no bank twice
-        const bool flip = c >= 4;
-        *reinterpret_cast<uint4 *>(tile + swz(row, flip ? ch + 1 : ch)) = flip ? hi : lo;
-        *reinterpret_cast<uint4 *>(tile + swz(row, flip ? ch : ch + 1)) = flip ? lo : hi;
+        for (int i = 0; i < 32 / RPI; ++i) {                 // eight lanes write a 128-byte row: no bank twice
+          const uint2 x = *reinterpret_cast<const uint2 *>(src + i * RPI * HD);
+          const uint2 a0 = unpack4(x.x), a1 = unpack4(x.y);
+          *reinterpret_cast<uint4 *>(dst + swz(r0 + i * RPI, c & 7)) = make_uint4(a0.x, a0.y, a1.x, a1.y);
+        }
+      } else {                                               // no key or no page: zeros
+#pragma unroll 1
+        for (int i = 0; i < 32 / RPI; ++i) {
+          const int row = r0 + i * RPI;
+          const uint2 x = *reinterpret_cast<const uint2 *>(src + i * RPI * HD);
+          const uint2 a0 = unpack4(x.x), a1 = unpack4(x.y);
+          const bool none = row >= valid || ((gone >> (row / kPage)) & 1u);
+          *reinterpret_cast<uint4 *>(dst + swz(row, c & 7)) = none ? make_uint4(0, 0, 0, 0) : make_uint4(a0.x, a0.y, a1.x, a1.y);
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -667,6 +665,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     bool ok = true;
     int j = 0;
     const float new_scale = fresh ? rscale * pow2i(new_kexp()) : 0.f;
+    const float new_ve = fresh ? (float)new_vexp() : 0.f, new_inv = fresh ? pow2i(-new_vexp()) : 1.f;
     // the key loop, compiled once per copy count
     auto key_loop = [&](auto rc) {
       constexpr int RC = decltype(rc)::value;
@@ -680,26 +679,25 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         const uint32_t tS = trow + kColS + tb * kKeys + k_lo;
         const int q = jp & (kGroup - 1), slot = jp / kGroup % kGroupSlots;
         if (!is_new && q == 0) ok = ok && mbar_wait_warp(bar(kBarGFull + slot), (jp / (kGroup * kGroupSlots)) & 1, a.polls);
-        // factor of this row's scores in each 16 columns (a page)
-        float f[KW / 16];
-        float2 block = make_float2(1.f, 0.f);
+        // a page's 16 keys: t = f s + ve, its weights' share of the sum 2^-ve
+        constexpr int NP = KW / 16;
+        float f[NP], ve[NP], inv[NP];
+        uint32_t gone = 0u;
         if (is_new) {
 #pragma unroll
-          for (int i = 0; i < KW / 16; ++i) f[i] = new_scale;
+          for (int i = 0; i < NP; ++i) { f[i] = new_scale; ve[i] = new_ve; inv[i] = new_inv; }
         } else {
-          const float *k = scales_s[slot].k + 8 * q + k_lo / 16;
-          block = scales_s[slot].block[q];
-          if constexpr (KW == 64) {
-            const float4 x = *reinterpret_cast<const float4 *>(k);
-            f[0] = x.x * rscale; f[1] = x.y * rscale; f[2] = x.z * rscale; f[3] = x.w * rscale;
-          } else {
+          const Scales &sc = scales_s[slot];
+          const int e0 = 8 * q + k_lo / 16;
+          gone = sc.gone[q];
 #pragma unroll
-            for (int i = 0; i < KW / 16; ++i) f[i] = k[i] * rscale;
+          for (int i = 0; i < NP; ++i) {
+            const float2 x = sc.kv[e0 + i];
+            f[i] = x.x * rscale; ve[i] = x.y; inv[i] = sc.inv[e0 + i];
           }
         }
         // keys that count: all of a whole block's, else one bit each
         const int valid = is_new ? 0 : w.k_end - w.k_begin - jp * kKeys;
-        const uint32_t gone = __float_as_uint(block.y);
         const bool whole = !is_new && valid >= kKeys && gone == 0u;
         ok = ok && mbar_wait_warp(bar(kBarSFull + tb), (j >> 1) & 1, a.polls);
         tc::fence_after_sync();
@@ -727,18 +725,18 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
           }
 #pragma unroll
           for (int i = 0; i < KW; ++i)
-            sr[i] = __float_as_uint((vis >> i) & 1ull ? __uint_as_float(sr[i]) * f[i / 16] : -INFINITY);
+            sr[i] = __float_as_uint((vis >> i) & 1ull ? fmaf(__uint_as_float(sr[i]), f[i / 16], ve[i / 16]) : -INFINITY);
 #pragma unroll
-          for (int i = 0; i < KW / 16; ++i) f[i] = 1.f;
+          for (int i = 0; i < NP; ++i) { f[i] = 1.f; ve[i] = 0.f; }
         }
 #pragma unroll
         for (int i = 0; i < KW; i += 16) {
-          float t4[4];
+          float v[16];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            t4[c] = fmaxf(fmaxf(__uint_as_float(sr[i + c]), __uint_as_float(sr[i + c + 4])),
-                          fmaxf(__uint_as_float(sr[i + c + 8]), __uint_as_float(sr[i + c + 12])));
-          mx = fmaxf(mx, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * f[i / 16]);
+          for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(sr[i + c]);
+          const float m0 = max3(max3(v[0], v[1], v[2]), v[3], v[4]), m1 = max3(max3(v[5], v[6], v[7]), v[8], v[9]);
+          const float m2 = max3(max3(v[10], v[11], v[12]), v[13], v[14]);
+          mx = fmaxf(mx, fmaf(max3(max3(m0, m1, m2), v[15], v[15]), f[i / 16], ve[i / 16]));
         }
         both_s[(tb * kHalves + half) * kRows] = ok ? mx : __uint_as_float(0x7fc00000u);
         pair_sync();
@@ -751,31 +749,34 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         const float alpha = move ? ex2(m_ref - m_new) : 1.f;     // m_ref = -inf -> 0
         l *= alpha;
         m_ref = m_new;
-        // weights 2^(s - m_ref) as f16 pairs
+        // weights 2^(t - m_ref) as f16 pairs
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        float rs4[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pw[KW / 2];
 #pragma unroll
-        for (int e = 0; e < KW / 2; ++e) {
-          const float p0 = ex2(fmaf(__uint_as_float(sr[2 * e]), f[e / 8], -mu));
-          const float p1 = ex2(fmaf(__uint_as_float(sr[2 * e + 1]), f[e / 8], -mu));
-          rs4[e & 3] += p0 + p1;
-          pw[e] = pack_f16x2(p0, p1);
+        for (int i = 0; i < NP; ++i) {
+          const float2 f2 = make_float2(f[i], f[i]), b2 = make_float2(ve[i] - mu, ve[i] - mu);
+          float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int e = 8 * i; e < 8 * i + 8; ++e) {
+            const float2 x = fma2(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, b2);
+            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+            sum = add2(sum, p);
+            pw[e] = pack_f16x2(p.x, p.y);
+          }
+          l = fmaf(sum.x + sum.y, inv[i], l);
         }
-        l += (rs4[0] + rs4[1]) + (rs4[2] + rs4[3]);
         // the weight tile and O are free once the previous block's P V is done
         if (j > 0) {
           if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; continue; }
           tc::fence_after_sync();
-          if (__any_sync(0xffffffffu, move || block.x != 1.f)) {   // this half of O's columns
-            const float shrink = alpha * block.x;
+          if (__any_sync(0xffffffffu, move)) {   // this half of O's columns
 #pragma unroll 1
             for (int c = 0; c < HD / 32; ++c) {
               uint32_t o[16];
               tc::ld16(tO + half * (HD / 2) + 16 * c, o);
               tc::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * shrink);
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
               tc::st16(tO + half * (HD / 2) + 16 * c, o);
             }
           }
@@ -805,13 +806,11 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     // -------------------------------------------------------- epilogue
     const bool failed = !ok || *(volatile int *)flag_s != 0;
     const int64_t orow = (t0 + tok) * a.Hq + w.kvh * a.G + (row_valid ? grow % a.G : 0);
-    // columns [c0, c0 + n), n <= 32, of this thread's row: sums v relative to reference
-    // mr and 2^vref, weights' sum lt
-    const int vref = n_past > 0 ? *(volatile int *)vref_s : new_vref();
-    const float vup = vref == kNoRef || failed ? 1.f : pow2i(vref);
+    // columns [c0, c0 + n), n <= 32, of this thread's row: sums v relative to
+    // reference mr, weights' sum lt
     auto write_cols = [&](const float *v, int c0, int n, float lt, float mr) {
       if (w.n_splits == 1) {
-        const float inv = lt == 0.f ? 0.f : vup / lt;
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
         uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + orow * HD + c0);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -824,7 +823,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         float4 *dst = reinterpret_cast<float4 *>(a.o_part + prow * HD + c0);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          if (4 * e < n) dst[e] = make_float4(v[4 * e] * vup, v[4 * e + 1] * vup, v[4 * e + 2] * vup, v[4 * e + 3] * vup);
+          if (4 * e < n) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         if (c0 == 0) a.ml_part[prow] = make_float2(mr, lt);
       }
     };
