@@ -7,10 +7,12 @@
 // older codes exactly (up to the subnormal codes) instead of reading the
 // tokens again.
 //
-// One CTA per touched page, a warp per head: a lane holds eight-element
-// chunks of the page's 16 rows, the maximum is a warp reduction, and the
-// rotation's partners are exchanged between lanes.  Bytes in, half as many
-// (bf16) out: DRAM bounds a prompt's append.
+// A warp takes one page and head at a time, keys then values, sixteen elements
+// of a row a lane (both halves of its rotated pairs, so nothing is exchanged);
+// the maximum is a warp reduction.  Angles: a page's first position by
+// rope_cs (two a lane), times the turn by 0..15 positions from a table that
+// the CTA makes once -- one product instead of a sine and a cosine for each
+// row.  Bytes in, half as many (bf16) out: DRAM bounds a prompt's append.
 #include <math.h>
 
 #include "common.cuh"
@@ -24,7 +26,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 8;                 // elements a lane handles together
+constexpr int kStageSeqs = 1024;          // sequences whose prefix sums are staged in shared memory
 
 struct AppendArgs {
   RopePlan plan;
@@ -34,6 +36,7 @@ struct AppendArgs {
   uint32_t *status;
   int64_t k_row, v_row;
   int batch, Hkv, max_pages, num_pages, total_n;
+  int64_t tasks;                          // (page item, head) pairs
 };
 
 // Work items: a sequence's touched pages, at most ceil((n + 15) / 16) <=
@@ -41,168 +44,203 @@ struct AppendArgs {
 // do nothing.
 __host__ __device__ __forceinline__ int64_t first_item(int32_t cu, int b) { return cu / kPage + 2LL * b; }
 
-// Rotates one chunk (elements 8 ch .. 8 ch + 7 of a head) whose row has the
-// angles cs; every lane of the warp calls it (the partners of half pairs are
-// shuffled in where they are whole chunks).  Rows that are not new (have
-// false) hold zeros and no angles.
-template <typename T, int HD>
-__device__ __forceinline__ void rotate_chunk(const RopePlan &p, const float2 *cs, const T *row,
-                                             bool have, int ch, int lane, float *x) {
-  const int e0 = ch * kChunk, rd = 2 * p.half;
-  if (p.interleaved) {
+__device__ __forceinline__ float2 turn(float2 a, float2 b) {   // complex product
+  return make_float2(a.x * b.x - a.y * b.y, a.x * b.y + a.y * b.x);
+}
+
+// Where a lane's two chunks of eight elements lie in a head: partners of half
+// pairs, else neighbours.
+struct Chunks {
+  int d1, d2;
+  bool paired;                            // (d1 + i, d2 + i) are pairs
+};
+
+// Sixteen rotated elements of a lane: u at d1.., v at d2.. (row: the head's
+// elements, for partners off the chunk grid); angles base x delta.
+template <typename T, bool IL>
+__device__ __forceinline__ void rotate16(const RopePlan &p, const Chunks &c, const float2 *base, const float2 *delta,
+                                         const T *row, float *u, float *v) {
+  if (IL) {
 #pragma unroll
-    for (int j = 0; j < kChunk; j += 2) {
-      if (have && e0 + j < rd) {
-        const float2 w = cs[(e0 + j) >> 1];
-        const float a = x[j], b = x[j + 1];
-        x[j] = a * w.x - b * w.y;
-        x[j + 1] = b * w.x + a * w.y;
+    for (int s = 0; s < 2; ++s) {
+      float *z = s ? v : u;
+      const int p0 = (s ? c.d2 : c.d1) >> 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (p0 + i < p.half) {
+          const float2 w = turn(base[p0 + i], delta[p0 + i]);
+          const float a = z[2 * i], b = z[2 * i + 1];
+          z[2 * i] = a * w.x - b * w.y;
+          z[2 * i + 1] = b * w.x + a * w.y;
+        }
       }
     }
-  } else if (p.half % kChunk == 0) {
-    const int step = p.half / kChunk;     // chunks between partners
-    const bool turned = e0 < rd, low = e0 < p.half;
-    const int src = lane + (turned ? (low ? step : -step) : 0);
+  } else if (p.half % 8 == 0) {
+    if (c.paired) {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const float y = __shfl_sync(0xffffffffu, x[j], src);
-      if (turned && have) {
-        const float2 w = cs[low ? e0 + j : e0 + j - p.half];
-        x[j] = low ? x[j] * w.x - y * w.y : x[j] * w.x + y * w.y;
+      for (int i = 0; i < 8; ++i) {
+        const float2 w = turn(base[c.d1 + i], delta[c.d1 + i]);
+        const float a = u[i], b = v[i];
+        u[i] = a * w.x - b * w.y;
+        v[i] = b * w.x + a * w.y;
       }
     }
-  } else if (have) {
+  } else {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      const int e = e0 + j;
-      if (e < rd) {
-        const bool low = e < p.half;
-        const float y = Elem<T>::load(row + (low ? e + p.half : e - p.half));
-        const float2 w = cs[low ? e : e - p.half];
-        x[j] = low ? x[j] * w.x - y * w.y : x[j] * w.x + y * w.y;
+    for (int i = 0; i < 16; ++i) {
+      const int d = (i < 8 ? c.d1 : c.d2) + (i & 7);
+      if (d < 2 * p.half) {
+        const bool low = d < p.half;
+        const int q = low ? d : d - p.half;
+        const float y = Elem<T>::load(row + (low ? d + p.half : q));
+        const float2 w = turn(base[q], delta[q]);
+        float &e = i < 8 ? u[i & 7] : v[i & 7];
+        e = low ? e * w.x - y * w.y : e * w.x + y * w.y;
       }
     }
   }
 }
 
 // One page and head of K or V: rows r_lo..r_hi-1 of the page are new (row r
-// at src + r * stride), the rows before r_lo older.
-template <typename T, int HD, bool ROT>
-__device__ __forceinline__ void put_page(const AppendArgs &a, const T *src, int64_t stride, int r_lo,
-                                         int r_hi, uint8_t *codes, uint8_t *scale,
-                                         const float2 (*cs)[64], int lane) {
-  constexpr int PER_ROW = HD / kChunk, N = kPage * PER_ROW / 32;   // chunks of a row; of a lane
-  float x[N][kChunk];
-  const int ch = lane % PER_ROW;
+// at src + r * stride), the rows before r_lo older.  base: angles of the
+// page's first position; delta: turns by 0..15 positions, [16][64].
+template <typename T, int HD, bool ROT, bool IL>
+__device__ __forceinline__ void put_page(const RopePlan &plan, const T *src, int64_t stride, int r_lo, int r_hi,
+                                         uint8_t *codes, uint8_t *scale, const float2 *base,
+                                         const float2 (*delta)[64], int lane) {
+  constexpr int L = HD / 16;                       // lanes of a row
+  constexpr int N = kPage * L / 32;                // rows of a lane
+  const int ln = lane % L, r0 = lane / L;
+  Chunks c;
+  c.paired = ROT && !IL && plan.half % 8 == 0 && ln * 8 < plan.half;
+  c.d1 = c.paired ? ln * 8 : ln * 16;
+  c.d2 = c.paired ? c.d1 + plan.half : c.d1 + 8;
+  float u[N][8], v[N][8];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int r = (lane + 32 * i) / PER_ROW;
-    const bool have = r >= r_lo && r < r_hi;
+    const int r = r0 + i * (32 / L);
+    if (r >= r_lo && r < r_hi) {
+      load_vec<T, 8>(src + r * stride + c.d1, u[i]);
+      load_vec<T, 8>(src + r * stride + c.d2, v[i]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) x[i][j] = 0.f;
-    if (have) load_vec<T, kChunk>(src + r * stride + ch * kChunk, x[i]);
-  }
-  uint2 was[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int r = (lane + 32 * i) / PER_ROW;
-    was[i] = make_uint2(0u, 0u);
-    if (r < r_lo) was[i] = *reinterpret_cast<const uint2 *>(codes + r * HD + ch * kChunk);
+      for (int e = 0; e < 8; ++e) u[i][e] = v[i][e] = 0.f;
+    }
   }
   const int old_byte = r_lo > 0 ? *scale : 0;
   float amax = 0.f;
-  bool odd = false;                        // a NaN or an infinity
+  bool odd = false;                                // a NaN or an infinity
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int r = (lane + 32 * i) / PER_ROW;
-    const bool have = r >= r_lo && r < r_hi;
-    if (ROT) rotate_chunk<T, HD>(a.plan, cs[r], src + r * stride, have, ch, lane, x[i]);
+    const int r = r0 + i * (32 / L);
+    if (ROT && r >= r_lo && r < r_hi) rotate16<T, IL>(plan, c, base, delta[r], src + r * stride, u[i], v[i]);
 #pragma unroll
-    for (int j = 0; j < kChunk; ++j) {
-      odd |= !(fabsf(x[i][j]) < INFINITY);
-      amax = fmaxf(amax, fabsf(x[i][j]));
+    for (int e = 0; e < 8; ++e) {
+      odd |= !(fabsf(u[i][e]) < INFINITY) || !(fabsf(v[i][e]) < INFINITY);
+      amax = fmaxf(amax, fmaxf(fabsf(u[i][e]), fabsf(v[i][e])));
     }
   }
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // (non-negative: ordered as bits)
   odd = __any_sync(0xffffffffu, odd) || old_byte == kScaleNan;
   int e = scale_exponent(amax);
   // older tokens keep at least their scale (a byte that no append wrote is
   // brought into the range)
-  const int old_e = min(max(old_byte - kScaleBias, kExpLo), kExpHi);
-  if (r_lo > 0) e = max(e, old_e);
-  const float down = pow2i(-e), move = pow2i(max(old_byte - kScaleBias - e, -126));
+  if (r_lo > 0) e = max(e, min(max(old_byte - kScaleBias, kExpLo), kExpHi));
+  const float down = pow2i(-e);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const int r = (lane + 32 * i) / PER_ROW;
-    uint2 w;
-    if (r < r_lo) {
-      if (odd || old_byte - kScaleBias == e) continue;
-      const uint32_t c[4] = {was[i].x & 0xffffu, was[i].x >> 16, was[i].y & 0xffffu, was[i].y >> 16};
-      uint32_t n[4];
+    const int r = r0 + i * (32 / L);
+    if (r < r_lo || r >= r_hi) continue;
+    uint8_t *dst = codes + r * HD;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = unpack_e4m3x2(c[j]);
-        n[j] = pack_e4m3x2(f.x * move, f.y * move);
-      }
-      w = make_uint2(n[0] | n[1] << 16, n[2] | n[3] << 16);
-    } else if (r < r_hi) {
-      const float *f = x[i];
-      w = make_uint2(pack_e4m3x2(f[0] * down, f[1] * down) | pack_e4m3x2(f[2] * down, f[3] * down) << 16,
+    for (int s = 0; s < 2; ++s) {
+      const float *f = s ? v[i] : u[i];
+      *reinterpret_cast<uint2 *>(dst + (s ? c.d2 : c.d1)) =
+          make_uint2(pack_e4m3x2(f[0] * down, f[1] * down) | pack_e4m3x2(f[2] * down, f[3] * down) << 16,
                      pack_e4m3x2(f[4] * down, f[5] * down) | pack_e4m3x2(f[6] * down, f[7] * down) << 16);
-    } else {
-      continue;
     }
-    *reinterpret_cast<uint2 *>(codes + r * HD + ch * kChunk) = w;
+  }
+  // codes of older tokens move to a scale that grew
+  if (r_lo > 0 && !odd && old_byte - kScaleBias != e) {
+    const float move = pow2i(max(old_byte - kScaleBias - e, -126));
+    for (int i = lane; i < r_lo * (HD / 4); i += 32) {
+      uint32_t *at = reinterpret_cast<uint32_t *>(codes) + i;
+      const uint32_t w = *at;
+      const float2 f = unpack_e4m3x2(w & 0xffffu), g = unpack_e4m3x2(w >> 16);
+      *at = pack_e4m3x2(f.x * move, f.y * move) | pack_e4m3x2(g.x * move, g.y * move) << 16;
+    }
   }
   if (lane == 0) *scale = (uint8_t)(odd ? kScaleNan : e + kScaleBias);
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads)
+// 16 warps of 128 registers an SM: 128 KB of rows in flight
+template <typename T, int HD, bool IL>
+__global__ void __launch_bounds__(kThreads, 2)
 kvq_append_kernel(const __grid_constant__ AppendArgs a) {
-  __shared__ float2 cs[kPage][64];
-  const int64_t item = blockIdx.x;
-  // the item's sequence: the last one whose first item is not above it
-  int lo = 0, hi = a.batch - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first_item(__ldg(a.cu_n + mid), mid) <= item) lo = mid; else hi = mid - 1;
-  }
-  const int b = lo;
-  const int c0 = __ldg(a.cu_n + b), rows = __ldg(a.cu_n + b + 1) - c0;
-  const int start = __ldg(a.start + b);
-  const int n = a.take != nullptr ? __ldg(a.take + b) : rows;
-  const int64_t j = item - first_item(c0, b);        // index among the sequence's touched pages
-  const int64_t end = (int64_t)start + n;
-  if (c0 < 0 || rows < 0 || (int64_t)c0 + rows > a.total_n || n < 0 || n > rows || start < 0 || j < 0 ||
-      end > (int64_t)a.max_pages * kPage) {
-    if (threadIdx.x == 0) raise_status(a.status, kStatusBadInput);
-    return;
-  }
-  const int64_t pg = start / kPage + j;               // page of the sequence
-  if (n == 0 || pg * kPage >= end) return;
-  const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + pg);
-  if (page < 0 || page >= a.num_pages) {
-    if (threadIdx.x == 0) raise_status(a.status, kStatusBadInput);
-    return;
-  }
-  const int pos0 = (int)(pg * kPage);
-  const int r_lo = max(0, start - pos0), r_hi = (int)min((int64_t)kPage, end - pos0);
+  __shared__ __align__(16) float2 delta_s[kPage][64];
+  __shared__ __align__(16) float2 base_s[kWarps][64];
+  __shared__ int32_t cu_s[kStageSeqs + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RopePlan &plan = plan_by_lane(a.plan);
+  const bool staged = a.batch <= kStageSeqs;
+  if (staged)
+    for (int i = threadIdx.x; i <= a.batch; i += kThreads) cu_s[i] = __ldg(a.cu_n + i);
   for (int e = threadIdx.x; e < kPage * 64; e += kThreads) {
     const int r = e >> 6, d = e & 63;
-    if (d < a.plan.half && r >= r_lo && r < r_hi) cs[r][d] = rope_plan_cs(a.plan, d, pos0 + r);
+    if (d < a.plan.half) delta_s[r][d] = rope_cs(plan.tab, d, r);
   }
   __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row0 = (int64_t)c0 + pos0 - start;    // row of the page's first slot (may be before c0)
-  for (int h = warp; h < a.Hkv; h += kWarps) {
+  auto cu = [&](int b) { return staged ? cu_s[b] : __ldg(a.cu_n + b); };
+  int b = -1;                                      // the last task's sequence
+  for (int64_t task = (int64_t)blockIdx.x * kWarps + warp; task < a.tasks; task += (int64_t)gridDim.x * kWarps) {
+    const int64_t item = task / a.Hkv;
+    const int h = (int)(task - item * a.Hkv);
+    // the item's sequence: the last one whose first item is not above it
+    if (b < 0) {
+      int lo = 0, hi = a.batch - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first_item(cu(mid), mid) <= item) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+    } else {
+      while (b + 1 < a.batch && first_item(cu(b + 1), b + 1) <= item) ++b;
+    }
+    const int c0 = cu(b), rows = cu(b + 1) - c0;
+    const int start = __ldg(a.start + b);
+    const int n = a.take != nullptr ? __ldg(a.take + b) : rows;
+    const int64_t j = item - first_item(c0, b);    // index among the sequence's touched pages
+    const int64_t end = (int64_t)start + n;
+    if (c0 < 0 || rows < 0 || (int64_t)c0 + rows > a.total_n || n < 0 || n > rows || start < 0 || j < 0 ||
+        end > (int64_t)a.max_pages * kPage) {
+      if (lane == 0) raise_status(a.status, kStatusBadInput);
+      continue;
+    }
+    const int64_t pg = start / kPage + j;          // page of the sequence
+    if (n == 0 || pg * kPage >= end) continue;
+    const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + pg);
+    const int pos0 = (int)(pg * kPage);
+    const int r_lo = max(0, start - pos0), r_hi = (int)min((int64_t)kPage, end - pos0);
+    __syncwarp();
+    for (int d = lane; d < a.plan.half; d += 32) base_s[warp][d] = rope_plan_cs(plan, d, pos0);
+    __syncwarp();
+    if (page < 0 || page >= a.num_pages) {
+      if (lane == 0) raise_status(a.status, kStatusBadInput);
+      continue;
+    }
+    const int64_t row0 = (int64_t)c0 + pos0 - start;   // row of the page's first slot (may be before c0)
     const int64_t at = (int64_t)page * a.Hkv + h;
-    put_page<T, HD, true>(a, (const T *)a.k + row0 * a.k_row + h * HD, a.k_row, r_lo, r_hi,
-                          a.k_cache + at * kPage * HD, a.k_scale + at, cs, lane);
-    put_page<T, HD, false>(a, (const T *)a.v + row0 * a.v_row + h * HD, a.v_row, r_lo, r_hi,
-                           a.v_cache + at * kPage * HD, a.v_scale + at, cs, lane);
+    put_page<T, HD, true, IL>(a.plan, (const T *)a.k + row0 * a.k_row + h * HD, a.k_row, r_lo, r_hi,
+                              a.k_cache + at * kPage * HD, a.k_scale + at, base_s[warp], delta_s, lane);
+    put_page<T, HD, false, IL>(a.plan, (const T *)a.v + row0 * a.v_row + h * HD, a.v_row, r_lo, r_hi,
+                               a.v_cache + at * kPage * HD, a.v_scale + at, base_s[warp], delta_s, lane);
   }
+}
+
+template <typename T, int HD>
+void launch_append(const AppendArgs &a, unsigned grid, cudaStream_t stream) {
+  if (a.plan.interleaved) kvq_append_kernel<T, HD, true><<<grid, kThreads, 0, stream>>>(a);
+  else kvq_append_kernel<T, HD, false><<<grid, kThreads, 0, stream>>>(a);
 }
 
 }  // namespace
@@ -241,14 +279,16 @@ extern "C" simsd_status simsd_kvq_append(const simsd_kvq_append_desc *d, void *s
   a.status = (uint32_t *)d->workspace;
   a.batch = d->batch; a.Hkv = d->num_kv_heads; a.max_pages = d->max_pages_per_seq;
   a.num_pages = d->num_pages; a.total_n = d->total_n;
-  const dim3 grid((unsigned)first_item(d->total_n, d->batch));
+  a.tasks = first_item(d->total_n, d->batch) * d->num_kv_heads;
+  const int64_t ctas = (a.tasks + kWarps - 1) / kWarps;
+  const unsigned grid = (unsigned)(ctas < 2 * device_sm_count() ? ctas : 2 * device_sm_count());
   cudaStream_t stream = (cudaStream_t)stream_ptr;
   if (d->dtype == SIMSD_BF16) {
-    if (d->head_dim == 128) kvq_append_kernel<__nv_bfloat16, 128><<<grid, kThreads, 0, stream>>>(a);
-    else kvq_append_kernel<__nv_bfloat16, 64><<<grid, kThreads, 0, stream>>>(a);
+    if (d->head_dim == 128) launch_append<__nv_bfloat16, 128>(a, grid, stream);
+    else launch_append<__nv_bfloat16, 64>(a, grid, stream);
   } else {
-    if (d->head_dim == 128) kvq_append_kernel<float, 128><<<grid, kThreads, 0, stream>>>(a);
-    else kvq_append_kernel<float, 64><<<grid, kThreads, 0, stream>>>(a);
+    if (d->head_dim == 128) launch_append<float, 128>(a, grid, stream);
+    else launch_append<float, 64>(a, grid, stream);
   }
   return cudaGetLastError() == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
 }

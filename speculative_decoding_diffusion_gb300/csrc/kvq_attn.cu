@@ -68,7 +68,7 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
   const int half = a.plan.half;
   float2 *cs = reinterpret_cast<float2 *>(&s.v[0][0]);   // [kMaxNew][HD / 2]
   for (int e = threadIdx.x; e < npos * half; e += kThreads)
-    cs[(e / half) * (HD / 2) + e % half] = rope_plan_cs(a.plan, e % half, w.P + e / half);
+    cs[(e / half) * (HD / 2) + e % half] = rope_plan_cs(plan_by_lane(a.plan), e % half, w.P + e / half);
   __syncthreads();
   const int64_t t0 = (int64_t)a.per * w.c0;              // first new token's row
   for (int e = threadIdx.x; e < kRows * HD; e += kThreads) {

@@ -351,7 +351,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
 #pragma unroll 1
     for (int e = pt; e < npos * (HD / 2); e += kPrep) {
       const int d = e % (HD / 2);
-      cs_s[e] = d < a.plan.half ? rope_plan_cs(a.plan, d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
+      cs_s[e] = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
     }
     if (a.order == SIMSD_ORDER_PAIRED && pt < w.B) tau_s[pt] = __ldg(a.tau + w.c0 + pt);
     copy_async_wait_all();

@@ -93,11 +93,18 @@ constexpr int kBatch = 4;         // vector pairs a thread has in flight
 struct RopeArgs {
   RopePlan plan;
   const int32_t *pos;
-  const void *x[2];
-  void *y[2];
-  int64_t x_row[2], x_head[2], y_row[2], y_head[2];
+  const void *x0, *x1;
+  void *y0, *y1;
+  int64_t x0_row, x0_head, y0_row, y0_head, x1_row, x1_head, y1_row, y1_head;
   int rows, h0, heads, hd, rows_per_cta, inverse;
   uint32_t inv_heads;             // ceil(2^32 / heads): row of a (row, head) index
+};
+
+// N elements as they lie in memory (held so until they are used: half the
+// registers of their fp32 values for bf16).
+template <typename T, int N>
+struct __align__(N * sizeof(T)) Raw {
+  T x[N];
 };
 
 // One pair of 16-byte vectors of a head.  HALF: vectors v and v + half (the
@@ -126,23 +133,29 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   } else {
     d1 = 2 * lane * N; d2 = d1 + N; turn1 = turn2 = false;
   }
-  float u[kBatch][N], v[kBatch][N];
-  auto where = [&](int i, int &r, int &t, int &h) {
+  Raw<T, N> u[kBatch], v[kBatch];
+  // row and head of item i: where they lie in the input and the output
+  auto place = [&](int i, int &r, const T *&src, T *&dst) {
     r = a.heads == 1 ? i : (int)__umulhi((uint32_t)i, a.inv_heads);
-    h = i - r * a.heads;
-    t = h >= a.h0;
-    h -= t ? a.h0 : 0;
+    int h = i - r * a.heads;
+    const bool second = h >= a.h0;
+    h -= second ? a.h0 : 0;
+    src = (const T *)(second ? a.x1 : a.x0) + (int64_t)(row0 + r) * (second ? a.x1_row : a.x0_row) +
+          h * (second ? a.x1_head : a.x0_head);
+    dst = (T *)(second ? a.y1 : a.y0) + (int64_t)(row0 + r) * (second ? a.y1_row : a.y0_row) +
+          h * (second ? a.y1_head : a.y0_head);
   };
   auto load = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * n_groups;
       if (i < total) {
-        int r, t, h;
-        where(i, r, t, h);
-        const T *src = (const T *)a.x[t] + (int64_t)(row0 + r) * a.x_row[t] + h * a.x_head[t];
-        load_vec<T, N>(src + d1, u[k]);
-        load_vec<T, N>(src + d2, v[k]);
+        int r;
+        const T *src;
+        T *dst;
+        place(i, r, src, dst);
+        u[k] = *reinterpret_cast<const Raw<T, N> *>(src + d1);
+        v[k] = *reinterpret_cast<const Raw<T, N> *>(src + d2);
       }
     }
   };
@@ -150,7 +163,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
   for (int e = threadIdx.x; e < n_rows * 64; e += kThreads) {
     const int r = e >> 6, d = e & 63;
     if (d < half) {
-      float2 cs = rope_plan_cs(a.plan, d, __ldg(a.pos + row0 + r));
+      float2 cs = rope_plan_cs(plan_by_lane(a.plan), d, __ldg(a.pos + row0 + r));
       if (a.inverse) cs.y = -cs.y;
       cs_s[r][d] = cs;
     }
@@ -162,31 +175,35 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k * n_groups;
       if (i >= total) break;
-      int r, t, h;
-      where(i, r, t, h);
-      T *dst = (T *)a.y[t] + (int64_t)(row0 + r) * a.y_row[t] + h * a.y_head[t];
+      int r;
+      const T *src;
+      T *dst;
+      place(i, r, src, dst);
       const float2 *cs = cs_s[r];
+      float x[N], y[N];
+      load_vec<T, N>(reinterpret_cast<const T *>(&u[k]), x);
+      load_vec<T, N>(reinterpret_cast<const T *>(&v[k]), y);
       if (!IL) {
         if (turn1) {
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             const float2 w = cs[d1 + j];
-            const float x1 = u[k][j], x2 = v[k][j];
-            u[k][j] = x1 * w.x - x2 * w.y;
-            v[k][j] = x2 * w.x + x1 * w.y;
+            const float x1 = x[j], x2 = y[j];
+            x[j] = x1 * w.x - x2 * w.y;
+            y[j] = x2 * w.x + x1 * w.y;
           }
         }
       } else if (N == 1) {                           // the pair itself
         if (turn1) {
           const float2 w = cs[d1 >> 1];
-          const float x1 = u[k][0], x2 = v[k][0];
-          u[k][0] = x1 * w.x - x2 * w.y;
-          v[k][0] = x2 * w.x + x1 * w.y;
+          const float x1 = x[0], x2 = y[0];
+          x[0] = x1 * w.x - x2 * w.y;
+          y[0] = x2 * w.x + x1 * w.y;
         }
       } else {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          float *z = s ? v[k] : u[k];
+          float *z = s ? y : x;
           if (!(s ? turn2 : turn1)) continue;
 #pragma unroll
           for (int j = 0; j + 1 < N; j += 2) {
@@ -197,8 +214,8 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
           }
         }
       }
-      store_vec<T, N>(dst + d1, u[k]);
-      store_vec<T, N>(dst + d2, v[k]);
+      store_vec<T, N>(dst + d1, x);
+      store_vec<T, N>(dst + d2, y);
     }
   }
 }
@@ -245,9 +262,9 @@ extern "C" simsd_status simsd_rope(const simsd_rope_desc *d, void *stream) {
   for (const int64_t t : s) vec = vec && (t * es) % 16 == 0;
   if (d->rows == 0) return SIMSD_OK;
   a.pos = d->positions;
-  a.x[0] = d->x0; a.y[0] = d->y0; a.x[1] = d->x1; a.y[1] = d->y1;
-  a.x_row[0] = d->x0_row; a.x_head[0] = d->x0_head; a.y_row[0] = d->y0_row; a.y_head[0] = d->y0_head;
-  a.x_row[1] = d->x1_row; a.x_head[1] = d->x1_head; a.y_row[1] = d->y1_row; a.y_head[1] = d->y1_head;
+  a.x0 = d->x0; a.y0 = d->y0; a.x1 = d->x1; a.y1 = d->y1;
+  a.x0_row = d->x0_row; a.x0_head = d->x0_head; a.y0_row = d->y0_row; a.y0_head = d->y0_head;
+  a.x1_row = d->x1_row; a.x1_head = d->x1_head; a.y1_row = d->y1_row; a.y1_head = d->y1_head;
   a.rows = d->rows;
   a.h0 = d->num_heads0;
   a.heads = d->num_heads0 + d->num_heads1;

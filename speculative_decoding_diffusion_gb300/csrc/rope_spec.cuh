@@ -20,6 +20,14 @@ struct RopePlan {
 // last plan is kept and copied while calls repeat the same numbers.
 simsd_status make_rope_plan(const simsd_rope_spec &s, int hd, RopePlan *p);
 
+// The same plan (a kernel parameter) read through global memory: a warp whose
+// lanes index a parameter differently reads it one lane after another.
+__device__ __forceinline__ const RopePlan &plan_by_lane(const RopePlan &p) {
+  const RopePlan *q = &p;
+  asm("" : "+l"(q));
+  return *q;
+}
+
 // (cos, sin) times the plan's factor of pair d < half at position pos
 // (negative positions turn the other way).
 __device__ __forceinline__ float2 rope_plan_cs(const RopePlan &p, int d, int pos) {

@@ -158,11 +158,14 @@ def test_verify_refusals(lib, bad, code):
     assert lib.simsd_kvq_verify(None, None) == 1 and lib.simsd_kvq_verify_workspace_size(None) == 0
 
 
-def test_verify_workspace_grows_with_key_splits_only(lib):
+def test_verify_workspace_holds_partials_where_keys_are_split(lib):
     size = lambda **kw: lib.simsd_kvq_verify_workspace_size(ctypes.byref(verify_desc(**kw)))  # noqa: E731
-    assert size() == 256                                   # 64 keys: nothing to split
-    one = size(batch=1, total_B=4, max_pages_per_seq=2048)   # one long sequence is split
-    assert one > 256 and one % 256 == 0
+    assert size(dtype=0) == 256                            # fp32, 64 keys: the status word alone
+    assert size() % 256 == 0
+    for dtype in (0, 1):
+        short, long = (size(dtype=dtype, batch=1, total_B=4, max_pages_per_seq=m) for m in (4, 2048))
+        # at least two splits of 8 rows x 4 heads: sums of 64 values, and (reference, sum)
+        assert long - short >= 2 * 8 * 4 * (64 * 4 + 8)
 
 
 def test_binding_refuses_what_it_would_misread():
