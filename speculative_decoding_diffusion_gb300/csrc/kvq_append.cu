@@ -24,7 +24,7 @@
 namespace simsd {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kStageSeqs = 1024;          // sequences whose prefix sums are staged in shared memory
 
@@ -56,93 +56,110 @@ struct Chunks {
 };
 
 // Sixteen rotated elements of a lane: u at d1.., v at d2.. (row: the head's
-// elements, for partners off the chunk grid); angles base x delta.
+// elements, for partners off the chunk grid); base: the angles of the page's
+// first position, of this lane's pairs d1.. (half pairs: base[i] belongs to
+// pair d1 + i; interleaved: base[i] to pair d1 / 2 + i, both chunks in turn);
+// delta: the turn from there to this row, by pair.
 template <typename T, bool IL>
 __device__ __forceinline__ void rotate16(const RopePlan &p, const Chunks &c, const float2 *base, const float2 *delta,
-                                         const T *row, float *u, float *v) {
+                                         const float2 *base_all, const T *row, float *u, float *v) {
   if (IL) {
+    const int p0 = c.d1 >> 1;                      // (d2 = d1 + 8: eight pairs in a row)
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      float *z = s ? v : u;
-      const int p0 = (s ? c.d2 : c.d1) >> 1;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (p0 + i < p.half) {
-          const float2 w = turn(base[p0 + i], delta[p0 + i]);
-          const float a = z[2 * i], b = z[2 * i + 1];
-          z[2 * i] = a * w.x - b * w.y;
-          z[2 * i + 1] = b * w.x + a * w.y;
-        }
+    for (int i = 0; i < 8; ++i) {
+      if (p0 + i < p.half) {
+        const float2 w = turn(base[i], delta[p0 + i]);
+        float *z = i < 4 ? u + 2 * i : v + 2 * (i - 4);
+        const float a = z[0], b = z[1];
+        z[0] = a * w.x - b * w.y;
+        z[1] = b * w.x + a * w.y;
       }
     }
   } else if (p.half % 8 == 0) {
     if (c.paired) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 w = turn(base[c.d1 + i], delta[c.d1 + i]);
-        const float a = u[i], b = v[i];
-        u[i] = a * w.x - b * w.y;
-        v[i] = b * w.x + a * w.y;
+      for (int i = 0; i < 8; i += 2) {
+        const float4 dd = *reinterpret_cast<const float4 *>(delta + c.d1 + i);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float2 w = turn(base[i + k], k ? make_float2(dd.z, dd.w) : make_float2(dd.x, dd.y));
+          const float a = u[i + k], b = v[i + k];
+          u[i + k] = a * w.x - b * w.y;
+          v[i + k] = b * w.x + a * w.y;
+        }
       }
     }
   } else {
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < 16; ++i) {
       const int d = (i < 8 ? c.d1 : c.d2) + (i & 7);
       if (d < 2 * p.half) {
         const bool low = d < p.half;
         const int q = low ? d : d - p.half;
-        const float y = Elem<T>::load(row + (low ? d + p.half : q));
-        const float2 w = turn(base[q], delta[q]);
-        float &e = i < 8 ? u[i & 7] : v[i & 7];
-        e = low ? e * w.x - y * w.y : e * w.x + y * w.y;
+        const float x = Elem<T>::load(row + d), y = Elem<T>::load(row + (low ? d + p.half : q));
+        const float2 w = turn(base_all[q], delta[q]);
+        const float z = low ? x * w.x - y * w.y : x * w.x + y * w.y;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {              // no indexed registers
+          u[k] = k == i ? z : u[k];
+          v[k] = k + 8 == i ? z : v[k];
+        }
       }
     }
   }
 }
 
-// One page and head of K or V: rows r_lo..r_hi-1 of the page are new (row r
-// at src + r * stride), the rows before r_lo older.  base: angles of the
-// page's first position; delta: turns by 0..15 positions, [16][64].
+// A lane's part of one page and head: row r0 + i (32 / L) at d1.. and d2..
+template <typename T, int HD>
+struct Rows {
+  static constexpr int L = HD / 16;                // lanes of a row
+  static constexpr int N = kPage * L / 32;         // rows of a lane
+  Raw<T, 8> u[N], v[N];
+  // rows r_lo..r_hi-1 of the page (row r at src + r * stride), zeros elsewhere
+  __device__ __forceinline__ void load(const T *src, int64_t stride, int r_lo, int r_hi, const Chunks &c, int r0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int r = r0 + i * (32 / L);
+      const bool in = r >= r_lo && r < r_hi;
+      const T *row = src + r * stride;
+      if (in) {
+        u[i] = *reinterpret_cast<const Raw<T, 8> *>(row + c.d1);
+        v[i] = *reinterpret_cast<const Raw<T, 8> *>(row + c.d2);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) u[i].x[e] = v[i].x[e] = T(0.f);
+      }
+    }
+  }
+};
+
+// One page and head of K or V: rows r_lo..r_hi-1 of the page are new, the
+// rows before r_lo older.
 template <typename T, int HD, bool ROT, bool IL>
-__device__ __forceinline__ void put_page(const RopePlan &plan, const T *src, int64_t stride, int r_lo, int r_hi,
-                                         uint8_t *codes, uint8_t *scale, const float2 *base,
-                                         const float2 (*delta)[64], int lane) {
-  constexpr int L = HD / 16;                       // lanes of a row
-  constexpr int N = kPage * L / 32;                // rows of a lane
-  const int ln = lane % L, r0 = lane / L;
-  Chunks c;
-  c.paired = ROT && !IL && plan.half % 8 == 0 && ln * 8 < plan.half;
-  c.d1 = c.paired ? ln * 8 : ln * 16;
-  c.d2 = c.paired ? c.d1 + plan.half : c.d1 + 8;
-  float u[N][8], v[N][8];
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int r = r0 + i * (32 / L);
-    if (r >= r_lo && r < r_hi) {
-      load_vec<T, 8>(src + r * stride + c.d1, u[i]);
-      load_vec<T, 8>(src + r * stride + c.d2, v[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[i][e] = v[i][e] = 0.f;
-    }
-  }
+__device__ __forceinline__ void put_page(const RopePlan &plan, const Rows<T, HD> &raw, const T *src, int64_t stride,
+                                         int r_lo, int r_hi, uint8_t *codes, uint8_t *scale, const Chunks &c, int r0,
+                                         const float2 *base_all, const float2 (*delta)[64], int lane) {
+  constexpr int L = Rows<T, HD>::L, N = Rows<T, HD>::N;
   const int old_byte = r_lo > 0 ? *scale : 0;
-  float amax = 0.f;
-  bool odd = false;                                // a NaN or an infinity
+  float2 base[8];
+  if (ROT && (IL || c.paired)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) base[i] = base_all[(IL ? c.d1 >> 1 : c.d1) + i];
+  }
+  float u[N][8], v[N][8], amax = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int r = r0 + i * (32 / L);
-    if (ROT && r >= r_lo && r < r_hi) rotate16<T, IL>(plan, c, base, delta[r], src + r * stride, u[i], v[i]);
+    load_vec<T, 8>(raw.u[i].x, u[i]);
+    load_vec<T, 8>(raw.v[i].x, v[i]);
+    if (ROT && r >= r_lo && r < r_hi) rotate16<T, IL>(plan, c, base, delta[r], base_all, src + r * stride, u[i], v[i]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      odd |= !(fabsf(u[i][e]) < INFINITY) || !(fabsf(v[i][e]) < INFINITY);
-      amax = fmaxf(amax, fmaxf(fabsf(u[i][e]), fabsf(v[i][e])));
-    }
+    for (int e = 0; e < 8; ++e) amax = absmax_nan(amax, u[i][e], v[i][e]);
   }
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));   // (non-negative: ordered as bits)
-  odd = __any_sync(0xffffffffu, odd) || old_byte == kScaleNan;
-  int e = scale_exponent(amax);
+  // (non-negative: ordered as bits; a NaN is above the infinity)
+  const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amax) & 0x7fffffffu);
+  const bool odd = top >= 0x7f800000u || old_byte == kScaleNan;   // a NaN or an infinity
+  int e = scale_exponent(__uint_as_float(top));
   // older tokens keep at least their scale (a byte that no append wrote is
   // brought into the range)
   if (r_lo > 0) e = max(e, min(max(old_byte - kScaleBias, kExpLo), kExpHi));
@@ -173,9 +190,9 @@ __device__ __forceinline__ void put_page(const RopePlan &plan, const T *src, int
   if (lane == 0) *scale = (uint8_t)(odd ? kScaleNan : e + kScaleBias);
 }
 
-// 16 warps of 128 registers an SM: 128 KB of rows in flight
+// 12 warps of up to 168 registers an SM: 96 KB of bf16 rows in flight
 template <typename T, int HD, bool IL>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
 kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ __align__(16) float2 delta_s[kPage][64];
   __shared__ __align__(16) float2 base_s[kWarps][64];
@@ -185,16 +202,48 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   const bool staged = a.batch <= kStageSeqs;
   if (staged)
     for (int i = threadIdx.x; i <= a.batch; i += kThreads) cu_s[i] = __ldg(a.cu_n + i);
-  for (int e = threadIdx.x; e < kPage * 64; e += kThreads) {
-    const int r = e >> 6, d = e & 63;
+  // turns by 1, 2, 4 and 8 positions, then the products for the rest
+  for (int e = threadIdx.x; e < 4 * 64; e += kThreads) {
+    const int r = 1 << (e >> 6), d = e & 63;
     if (d < a.plan.half) delta_s[r][d] = rope_cs(plan.tab, d, r);
+  }
+  if (threadIdx.x < 64) delta_s[0][threadIdx.x] = make_float2(1.f, 0.f);
+  __syncthreads();
+  for (int e = threadIdx.x; e < kPage * 64; e += kThreads) {
+    const int r = e >> 6, d = e & 63, low = r & -r;
+    if (r != low && d < a.plan.half) {
+      float2 w = delta_s[low][d];
+      for (int m = 2 * low; m < kPage; m <<= 1)
+        if (r & m) w = turn(w, delta_s[m][d]);
+      delta_s[r][d] = w;
+    }
   }
   __syncthreads();
   auto cu = [&](int b) { return staged ? cu_s[b] : __ldg(a.cu_n + b); };
+  using R = Rows<T, HD>;
+  const int ln = lane % R::L, r0 = lane / R::L;
+  Chunks ck, cv;                                   // of keys and of values
+  ck.paired = !IL && a.plan.half % 8 == 0 && ln * 8 < a.plan.half;
+  ck.d1 = ck.paired ? ln * 8 : ln * 16;
+  ck.d2 = ck.paired ? ck.d1 + a.plan.half : ck.d1 + 8;
+  cv.paired = false;
+  cv.d1 = ln * 16;
+  cv.d2 = cv.d1 + 8;
+  // A task: its page of the cache (looked up while the task before is worked
+  // on), the rows of the page that are new, the row of its first slot.
+  struct Task {
+    int64_t row0;
+    int page, pos0, r_lo, r_hi, h;
+    bool any, bad;                                 // new rows; numbers out of range
+  };
   int b = -1;                                      // the last task's sequence
-  for (int64_t task = (int64_t)blockIdx.x * kWarps + warp; task < a.tasks; task += (int64_t)gridDim.x * kWarps) {
+  auto find = [&](int64_t task) {
+    Task t;
+    t.any = t.bad = false;
+    t.page = -1;
+    if (task >= a.tasks) return t;
     const int64_t item = task / a.Hkv;
-    const int h = (int)(task - item * a.Hkv);
+    t.h = (int)(task - item * a.Hkv);
     // the item's sequence: the last one whose first item is not above it
     if (b < 0) {
       int lo = 0, hi = a.batch - 1;
@@ -213,27 +262,43 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
     const int64_t end = (int64_t)start + n;
     if (c0 < 0 || rows < 0 || (int64_t)c0 + rows > a.total_n || n < 0 || n > rows || start < 0 || j < 0 ||
         end > (int64_t)a.max_pages * kPage) {
-      if (lane == 0) raise_status(a.status, kStatusBadInput);
-      continue;
+      t.bad = true;
+      return t;
     }
     const int64_t pg = start / kPage + j;          // page of the sequence
-    if (n == 0 || pg * kPage >= end) continue;
-    const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + pg);
-    const int pos0 = (int)(pg * kPage);
-    const int r_lo = max(0, start - pos0), r_hi = (int)min((int64_t)kPage, end - pos0);
-    __syncwarp();
-    for (int d = lane; d < a.plan.half; d += 32) base_s[warp][d] = rope_plan_cs(plan, d, pos0);
-    __syncwarp();
-    if (page < 0 || page >= a.num_pages) {
-      if (lane == 0) raise_status(a.status, kStatusBadInput);
-      continue;
+    if (n == 0 || pg * kPage >= end) return t;
+    t.any = true;
+    t.page = __ldg(a.block_table + (int64_t)b * a.max_pages + pg);
+    t.pos0 = (int)(pg * kPage);
+    t.r_lo = max(0, start - t.pos0);
+    t.r_hi = (int)min((int64_t)kPage, end - t.pos0);
+    t.row0 = (int64_t)c0 + t.pos0 - start;         // (may be before c0)
+    return t;
+  };
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  int64_t task = (int64_t)blockIdx.x * kWarps + warp;
+  Task next = find(task);
+  for (; task < a.tasks; task += step) {
+    const Task t = next;
+    const bool good = t.any && t.page >= 0 && t.page < a.num_pages;
+    if ((t.bad || (t.any && !good)) && lane == 0) raise_status(a.status, kStatusBadInput);
+    const T *ks = (const T *)a.k + t.row0 * a.k_row + t.h * HD, *vs = (const T *)a.v + t.row0 * a.v_row + t.h * HD;
+    R rk, rv;
+    if (good) {                                    // keys and values in flight together (fp32 has no registers for it)
+      rk.load(ks, a.k_row, t.r_lo, t.r_hi, ck, r0);
+      if (sizeof(T) == 2) rv.load(vs, a.v_row, t.r_lo, t.r_hi, cv, r0);
     }
-    const int64_t row0 = (int64_t)c0 + pos0 - start;   // row of the page's first slot (may be before c0)
-    const int64_t at = (int64_t)page * a.Hkv + h;
-    put_page<T, HD, true, IL>(a.plan, (const T *)a.k + row0 * a.k_row + h * HD, a.k_row, r_lo, r_hi,
-                              a.k_cache + at * kPage * HD, a.k_scale + at, base_s[warp], delta_s, lane);
-    put_page<T, HD, false, IL>(a.plan, (const T *)a.v + row0 * a.v_row + h * HD, a.v_row, r_lo, r_hi,
-                               a.v_cache + at * kPage * HD, a.v_scale + at, base_s[warp], delta_s, lane);
+    next = find(task + step);
+    if (!good) continue;
+    __syncwarp();
+    for (int d = lane; d < a.plan.half; d += 32) base_s[warp][d] = rope_plan_cs(plan, d, t.pos0);
+    __syncwarp();
+    const int64_t at = (int64_t)t.page * a.Hkv + t.h;
+    put_page<T, HD, true, IL>(a.plan, rk, ks, a.k_row, t.r_lo, t.r_hi, a.k_cache + at * kPage * HD, a.k_scale + at, ck,
+                              r0, base_s[warp], delta_s, lane);
+    if (sizeof(T) == 4) rv.load(vs, a.v_row, t.r_lo, t.r_hi, cv, r0);
+    put_page<T, HD, false, IL>(a.plan, rv, vs, a.v_row, t.r_lo, t.r_hi, a.v_cache + at * kPage * HD, a.v_scale + at, cv,
+                               r0, base_s[warp], delta_s, lane);
   }
 }
 
@@ -281,7 +346,7 @@ extern "C" simsd_status simsd_kvq_append(const simsd_kvq_append_desc *d, void *s
   a.num_pages = d->num_pages; a.total_n = d->total_n;
   a.tasks = first_item(d->total_n, d->batch) * d->num_kv_heads;
   const int64_t ctas = (a.tasks + kWarps - 1) / kWarps;
-  const unsigned grid = (unsigned)(ctas < 2 * device_sm_count() ? ctas : 2 * device_sm_count());
+  const unsigned grid = (unsigned)(ctas < 3 * device_sm_count() ? ctas : 3 * device_sm_count());
   cudaStream_t stream = (cudaStream_t)stream_ptr;
   if (d->dtype == SIMSD_BF16) {
     if (d->head_dim == 128) launch_append<__nv_bfloat16, 128>(a, grid, stream);

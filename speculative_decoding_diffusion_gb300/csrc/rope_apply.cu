@@ -100,18 +100,11 @@ struct RopeArgs {
   uint32_t inv_heads;             // ceil(2^32 / heads): row of a (row, head) index
 };
 
-// N elements as they lie in memory (held so until they are used: half the
-// registers of their fp32 values for bf16).
-template <typename T, int N>
-struct __align__(N * sizeof(T)) Raw {
-  T x[N];
-};
-
 // One pair of 16-byte vectors of a head.  HALF: vectors v and v + half (the
 // rotated pairs), past those two neighbouring untouched ones; interleaved:
 // two neighbouring vectors, each holding its own pairs.
 template <typename T, bool IL, bool VEC>
-__global__ void __launch_bounds__(kThreads, 4)
+__global__ void __launch_bounds__(kThreads, 3)
 rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int N = VEC ? 16 / (int)sizeof(T) : 1;   // elements of a vector
   __shared__ float2 cs_s[kMaxRows][64];

@@ -43,4 +43,18 @@ __device__ __forceinline__ void store_vec(T *p, const float *f) {
   }
 }
 
+// N elements as they lie in memory, held so until they are used (bf16: half
+// the registers of their fp32 values).
+template <typename T, int N>
+struct __align__(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Raw {
+  T x[N];
+};
+
+// max(m, |a|, |b|), NaN if any is.
+__device__ __forceinline__ float absmax_nan(float m, float a, float b) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(m), "f"(a), "f"(b));
+  return d;
+}
+
 }  // namespace simsd
