@@ -499,7 +499,7 @@ simsd_status simsd_accept_noalloc(const simsd_accept_desc *d, void *stream);
  *                      original_len w_i / (2 pi)
  * attn_factor multiplies the cosines and sines (so scores grow by its
  * square); 0 selects 0.1 ln(factor) + 1 for YARN and 1 otherwise.
- * Angles are formed to ~3e-7 rad at every position (64 bits past 2^24).
+ * Angles are formed to ~3e-7 rad at every position (64 bits from 2^24 on).
  * ---------------------------------------------------------------------- */
 typedef enum {
   SIMSD_ROPE_HALF = 0,        /* pairs (i, i + rotary_dim / 2)               */

@@ -9,8 +9,8 @@
 //
 // A warp takes one page and head at a time, keys then values, sixteen elements
 // of a row a lane (both halves of its rotated pairs, so nothing is exchanged);
-// the maximum is a warp reduction.  Angles: a page's first position by
-// rope_cs (two a lane), times the turn by 0..15 positions from a table that
+// the maximum is a warp reduction.  Angles: a page's first position
+// (two a lane), times the turn by 0..15 positions from a table that
 // the CTA makes once -- one product instead of a sine and a cosine for each
 // row.  Bytes in, half as many (bf16) out: DRAM bounds a prompt's append.
 #include <math.h>
@@ -205,7 +205,7 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   // turns by 1, 2, 4 and 8 positions, then the products for the rest
   for (int e = threadIdx.x; e < 4 * 64; e += kThreads) {
     const int r = 1 << (e >> 6), d = e & 63;
-    if (d < a.plan.half) delta_s[r][d] = rope_cs(plan.tab, d, r);
+    if (d < a.plan.half) delta_s[r][d] = rope_plan_angle(plan, d, r);
   }
   if (threadIdx.x < 64) delta_s[0][threadIdx.x] = make_float2(1.f, 0.f);
   __syncthreads();

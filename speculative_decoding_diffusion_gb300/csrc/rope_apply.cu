@@ -67,9 +67,9 @@ simsd_status make_rope_plan(const simsd_rope_spec &s, int hd, RopePlan *p) {
         const double keep = t < 0.0 ? 0.0 : t > 1.0 ? 1.0 : t;
         w = w / f * (1.0 - keep) + w * keep;
       }
-      r.tab.inv_freq[i] = w;
-      r.tab.hi[i] = (float)w;
-      r.tab.lo[i] = (float)(w - (double)r.tab.hi[i]);
+      r.turns[i] = w / kTwoPi;
+      r.hi[i] = (float)r.turns[i];
+      r.lo[i] = (float)(r.turns[i] - (double)r.hi[i]);
     }
     r.half = rd / 2;
     r.interleaved = s.style == SIMSD_ROPE_INTERLEAVED;

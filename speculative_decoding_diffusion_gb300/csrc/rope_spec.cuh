@@ -1,16 +1,24 @@
 // rope_spec.cuh -- rotary positions of simsd_rope_spec: the plan made on the
-// host (frequencies in fp64, scaled for long contexts) and the (cos, sin) of
-// a pair on the device.
+// host (turns per position in fp64, scaled for long contexts) and the (cos,
+// sin) of a pair on the device.
+//
+// The angle is kept in turns, t = pos * w / (2 pi): the integer part drops
+// out exactly, and sincospif of twice the rest needs no reduction of its own.
+// With w / (2 pi) = hi + lo in two floats and the product's rounding error
+// recovered by an fma, the angle is off by ~2e-7 rad for |pos| < 2^24;
+// farther positions take fp64 (in a function of its own, so that no path
+// that does not need it issues fp64 instructions: if-converted they took a
+// fifth of the append's time).
 #pragma once
 
 #include "internal.h"
-#include "rope.cuh"
 
 namespace simsd {
 
-// What the kernels take: the scaled frequencies of the first `half` pairs.
+// What the kernels take: the first `half` pairs' turns per position.
 struct RopePlan {
-  RopeTable tab;
+  double turns[64];
+  float hi[64], lo[64];
   float mul;          // factor on cos and sin
   int half;           // rotated pairs, rotary_dim / 2
   int interleaved;    // pairs (2i, 2i+1) instead of (i, i + half)
@@ -28,11 +36,33 @@ __device__ __forceinline__ const RopePlan &plan_by_lane(const RopePlan &p) {
   return *q;
 }
 
-// (cos, sin) times the plan's factor of pair d < half at position pos
-// (negative positions turn the other way).
+// The part of a turn left at a far position.
+static __device__ __noinline__ float far_turn(double turns, int pos) {
+  const double t = (double)pos * turns;
+  return (float)(t - rint(t));
+}
+
+// (cos, sin) of pair d < half at position pos (negative positions turn the
+// other way).
+__device__ __forceinline__ float2 rope_plan_angle(const RopePlan &p, int d, int pos) {
+  float rest;
+  if (pos < (1 << 24) && pos > -(1 << 24)) {
+    const float x = (float)pos, hi = p.hi[d];        // exact
+    const float t = x * hi;
+    const float t_lo = fmaf(x, p.lo[d], fmaf(x, hi, -t));
+    rest = (t - rintf(t)) + t_lo;
+  } else {
+    rest = far_turn(p.turns[d], pos);
+  }
+  float s, c;
+  sincospif(2.f * rest, &s, &c);
+  return make_float2(c, s);
+}
+
+// The same times the plan's factor.
 __device__ __forceinline__ float2 rope_plan_cs(const RopePlan &p, int d, int pos) {
-  const float2 cs = rope_cs(p.tab, d, pos < 0 ? -pos : pos);
-  return make_float2(cs.x * p.mul, (pos < 0 ? -cs.y : cs.y) * p.mul);
+  const float2 cs = rope_plan_angle(p, d, pos);
+  return make_float2(cs.x * p.mul, cs.y * p.mul);
 }
 
 }  // namespace simsd
