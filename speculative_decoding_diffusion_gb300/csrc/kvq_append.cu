@@ -12,8 +12,14 @@
 // the maximum is a warp reduction.  Angles: a page's first position
 // (two a lane), times the turn by 0..15 positions from a table that
 // the CTA makes once -- one product instead of a sine and a cosine for each
-// row.  Bytes in, half as many (bf16) out: DRAM bounds a prompt's append.
+// row.  Bytes in, half as many (bf16) out: DRAM bounds a prompt's append, and
+// latency what it reaches of it: a warp's next page is copied into shared
+// memory (16-byte asynchronous copies) while the present one is worked on,
+// 12 warps x 16 KB an SM (in registers, 12 warps x 8 KB: 1.50 ms for 256
+// prompts; 16 x 4 KB: 2.15).
 #include <math.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -24,8 +30,9 @@
 namespace simsd {
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kWarps = kThreads / 32;
+// Warps of a CTA (one CTA an SM): two pages of raw rows, keys and values, each.
+template <typename T, int HD> constexpr int kPageBytes = 2 * kPage * HD * (int)sizeof(T);
+template <typename T, int HD> constexpr int kWarpsOf = kPageBytes<T, HD> <= 8192 ? 12 : 6;
 constexpr int kStageSeqs = 1024;          // sequences whose prefix sums are staged in shared memory
 
 struct AppendArgs {
@@ -65,10 +72,12 @@ __device__ __forceinline__ void rotate16(const RopePlan &p, const Chunks &c, con
                                          const float2 *base_all, const T *row, float *u, float *v) {
   if (IL) {
     const int p0 = c.d1 >> 1;                      // (d2 = d1 + 8: eight pairs in a row)
+    float2 dl[8];
+    load_angles8(delta, p0, dl);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (p0 + i < p.half) {
-        const float2 w = turn(base[i], delta[p0 + i]);
+        const float2 w = turn(base[i], dl[i]);
         float *z = i < 4 ? u + 2 * i : v + 2 * (i - 4);
         const float a = z[0], b = z[1];
         z[0] = a * w.x - b * w.y;
@@ -77,16 +86,14 @@ __device__ __forceinline__ void rotate16(const RopePlan &p, const Chunks &c, con
     }
   } else if (p.half % 8 == 0) {
     if (c.paired) {
+      float2 dl[8];
+      load_angles8(delta, c.d1, dl);
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float4 dd = *reinterpret_cast<const float4 *>(delta + c.d1 + i);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float2 w = turn(base[i + k], k ? make_float2(dd.z, dd.w) : make_float2(dd.x, dd.y));
-          const float a = u[i + k], b = v[i + k];
-          u[i + k] = a * w.x - b * w.y;
-          v[i + k] = b * w.x + a * w.y;
-        }
+      for (int i = 0; i < 8; ++i) {
+        const float2 w = turn(base[i], dl[i]);
+        const float a = u[i], b = v[i];
+        u[i] = a * w.x - b * w.y;
+        v[i] = b * w.x + a * w.y;
       }
     }
   } else {
@@ -97,7 +104,7 @@ __device__ __forceinline__ void rotate16(const RopePlan &p, const Chunks &c, con
         const bool low = d < p.half;
         const int q = low ? d : d - p.half;
         const float x = Elem<T>::load(row + d), y = Elem<T>::load(row + (low ? d + p.half : q));
-        const float2 w = turn(base_all[q], delta[q]);
+        const float2 w = turn(base_all[angle_at(q)], delta[angle_at(q)]);
         const float z = low ? x * w.x - y * w.y : x * w.x + y * w.y;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {              // no indexed registers
@@ -109,50 +116,29 @@ __device__ __forceinline__ void rotate16(const RopePlan &p, const Chunks &c, con
   }
 }
 
-// A lane's part of one page and head: row r0 + i (32 / L) at d1.. and d2..
-template <typename T, int HD>
-struct Rows {
-  static constexpr int L = HD / 16;                // lanes of a row
-  static constexpr int N = kPage * L / 32;         // rows of a lane
-  Raw<T, 8> u[N], v[N];
-  // rows r_lo..r_hi-1 of the page (row r at src + r * stride), zeros elsewhere
-  __device__ __forceinline__ void load(const T *src, int64_t stride, int r_lo, int r_hi, const Chunks &c, int r0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int r = r0 + i * (32 / L);
-      const bool in = r >= r_lo && r < r_hi;
-      const T *row = src + r * stride;
-      if (in) {
-        u[i] = *reinterpret_cast<const Raw<T, 8> *>(row + c.d1);
-        v[i] = *reinterpret_cast<const Raw<T, 8> *>(row + c.d2);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) u[i].x[e] = v[i].x[e] = T(0.f);
-      }
-    }
-  }
-};
-
-// One page and head of K or V: rows r_lo..r_hi-1 of the page are new, the
-// rows before r_lo older.
+// One page and head of K or V: rows r_lo..r_hi-1 of the page are new (in
+// shared memory, all 16 rows' places), the rows before r_lo older.
 template <typename T, int HD, bool ROT, bool IL>
-__device__ __forceinline__ void put_page(const RopePlan &plan, const Rows<T, HD> &raw, const T *src, int64_t stride,
-                                         int r_lo, int r_hi, uint8_t *codes, uint8_t *scale, const Chunks &c, int r0,
-                                         const float2 *base_all, const float2 (*delta)[64], int lane) {
-  constexpr int L = Rows<T, HD>::L, N = Rows<T, HD>::N;
+__device__ __forceinline__ void put_page(const RopePlan &plan, const T *rows, int r_lo, int r_hi, uint8_t *codes,
+                                         uint8_t *scale, const Chunks &c, int r0, const float2 *base_all,
+                                         const float2 (*delta)[64], int lane) {
+  constexpr int L = HD / 16;                       // lanes of a row
+  constexpr int N = kPage * L / 32;                // rows of a lane
   const int old_byte = r_lo > 0 ? *scale : 0;
   float2 base[8];
-  if (ROT && (IL || c.paired)) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) base[i] = base_all[(IL ? c.d1 >> 1 : c.d1) + i];
-  }
+  if (ROT && (IL || c.paired)) load_angles8(base_all, IL ? c.d1 >> 1 : c.d1, base);
   float u[N][8], v[N][8], amax = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int r = r0 + i * (32 / L);
-    load_vec<T, 8>(raw.u[i].x, u[i]);
-    load_vec<T, 8>(raw.v[i].x, v[i]);
-    if (ROT && r >= r_lo && r < r_hi) rotate16<T, IL>(plan, c, base, delta[r], base_all, src + r * stride, u[i], v[i]);
+    if (r >= r_lo && r < r_hi) {
+      load_vec<T, 8>(rows + r * HD + c.d1, u[i]);
+      load_vec<T, 8>(rows + r * HD + c.d2, v[i]);
+      if (ROT) rotate16<T, IL>(plan, c, base, delta[r], base_all, rows + r * HD, u[i], v[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[i][e] = v[i][e] = 0.f;
+    }
 #pragma unroll
     for (int e = 0; e < 8; ++e) amax = absmax_nan(amax, u[i][e], v[i][e]);
   }
@@ -190,11 +176,11 @@ __device__ __forceinline__ void put_page(const RopePlan &plan, const Rows<T, HD>
   if (lane == 0) *scale = (uint8_t)(odd ? kScaleNan : e + kScaleBias);
 }
 
-// 12 warps of up to 168 registers an SM: 96 KB of bf16 rows in flight
 template <typename T, int HD, bool IL>
-__global__ void __launch_bounds__(kThreads, 3)
+__global__ void __launch_bounds__(32 * kWarpsOf<T, HD>, 1)
 kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ __align__(16) float2 delta_s[kPage][64];
+  constexpr int kWarps = kWarpsOf<T, HD>, kThreads = 32 * kWarps;
   __shared__ __align__(16) float2 base_s[kWarps][64];
   __shared__ int32_t cu_s[kStageSeqs + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -205,13 +191,13 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   // turns by 1, 2, 4 and 8 positions, then the products for the rest
   for (int e = threadIdx.x; e < 4 * 64; e += kThreads) {
     const int r = 1 << (e >> 6), d = e & 63;
-    if (d < a.plan.half) delta_s[r][d] = rope_plan_angle(plan, d, r);
+    if (d < a.plan.half) delta_s[r][angle_at(d)] = rope_plan_angle(plan, d, r);
   }
   if (threadIdx.x < 64) delta_s[0][threadIdx.x] = make_float2(1.f, 0.f);
   __syncthreads();
   for (int e = threadIdx.x; e < kPage * 64; e += kThreads) {
-    const int r = e >> 6, d = e & 63, low = r & -r;
-    if (r != low && d < a.plan.half) {
+    const int r = e >> 6, d = angle_at(e & 63), low = r & -r;
+    if (r != low && (e & 63) < a.plan.half) {
       float2 w = delta_s[low][d];
       for (int m = 2 * low; m < kPage; m <<= 1)
         if (r & m) w = turn(w, delta_s[m][d]);
@@ -220,8 +206,10 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   }
   __syncthreads();
   auto cu = [&](int b) { return staged ? cu_s[b] : __ldg(a.cu_n + b); };
-  using R = Rows<T, HD>;
-  const int ln = lane % R::L, r0 = lane / R::L;
+  extern __shared__ __align__(16) uint8_t pages_s[];         // [warp][2][K, V][16][HD]
+  T *mine = reinterpret_cast<T *>(pages_s) + (int64_t)warp * 4 * kPage * HD;
+  constexpr int L = HD / 16;
+  const int ln = lane % L, r0 = lane / L;
   Chunks ck, cv;                                   // of keys and of values
   ck.paired = !IL && a.plan.half % 8 == 0 && ln * 8 < a.plan.half;
   ck.d1 = ck.paired ? ln * 8 : ln * 16;
@@ -275,37 +263,71 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
     t.row0 = (int64_t)c0 + t.pos0 - start;         // (may be before c0)
     return t;
   };
+  auto good = [&](const Task &t) { return t.any && t.page >= 0 && t.page < a.num_pages; };
+  // starts copying a task's new rows into buffer `buf`
+  auto fetch = [&](const Task &t, int buf) {
+    if (good(t)) {
+      constexpr int C = HD * (int)sizeof(T) / 16;  // 16-byte chunks of a row
+      const T *ks = (const T *)a.k + t.row0 * a.k_row + t.h * HD, *vs = (const T *)a.v + t.row0 * a.v_row + t.h * HD;
+      const uint32_t dst = smem_u32(mine + buf * 2 * kPage * HD);
+#pragma unroll
+      for (int e = lane; e < kPage * C; e += 32) {
+        const int r = e / C, ch = e % C;
+        if (r >= t.r_lo && r < t.r_hi) {
+          copy16_async(dst + e * 16, (const char *)(ks + r * a.k_row) + ch * 16, true);
+          copy16_async(dst + (kPage * C + e) * 16, (const char *)(vs + r * a.v_row) + ch * 16, true);
+        }
+      }
+    }
+    copy_async_commit();
+  };
   const int64_t step = (int64_t)gridDim.x * kWarps;
   int64_t task = (int64_t)blockIdx.x * kWarps + warp;
   Task next = find(task);
-  for (; task < a.tasks; task += step) {
+  fetch(next, 0);
+  for (int buf = 0; task < a.tasks; task += step, buf ^= 1) {
     const Task t = next;
-    const bool good = t.any && t.page >= 0 && t.page < a.num_pages;
-    if ((t.bad || (t.any && !good)) && lane == 0) raise_status(a.status, kStatusBadInput);
-    const T *ks = (const T *)a.k + t.row0 * a.k_row + t.h * HD, *vs = (const T *)a.v + t.row0 * a.v_row + t.h * HD;
-    R rk, rv;
-    if (good) {                                    // keys and values in flight together (fp32 has no registers for it)
-      rk.load(ks, a.k_row, t.r_lo, t.r_hi, ck, r0);
-      if (sizeof(T) == 2) rv.load(vs, a.v_row, t.r_lo, t.r_hi, cv, r0);
-    }
     next = find(task + step);
-    if (!good) continue;
+    if ((t.bad || (t.any && !good(t))) && lane == 0) raise_status(a.status, kStatusBadInput);
+    if (good(t))
+      for (int d = lane; d < a.plan.half; d += 32) base_s[warp][angle_at(d)] = rope_plan_cs(plan, d, t.pos0);
+    fetch(next, buf ^ 1);
+    copy_async_wait<1>();
     __syncwarp();
-    for (int d = lane; d < a.plan.half; d += 32) base_s[warp][d] = rope_plan_cs(plan, d, t.pos0);
-    __syncwarp();
-    const int64_t at = (int64_t)t.page * a.Hkv + t.h;
-    put_page<T, HD, true, IL>(a.plan, rk, ks, a.k_row, t.r_lo, t.r_hi, a.k_cache + at * kPage * HD, a.k_scale + at, ck,
-                              r0, base_s[warp], delta_s, lane);
-    if (sizeof(T) == 4) rv.load(vs, a.v_row, t.r_lo, t.r_hi, cv, r0);
-    put_page<T, HD, false, IL>(a.plan, rv, vs, a.v_row, t.r_lo, t.r_hi, a.v_cache + at * kPage * HD, a.v_scale + at, cv,
-                               r0, base_s[warp], delta_s, lane);
+    if (good(t)) {
+      const T *rows = mine + buf * 2 * kPage * HD;
+      const int64_t at = (int64_t)t.page * a.Hkv + t.h;
+      put_page<T, HD, true, IL>(a.plan, rows, t.r_lo, t.r_hi, a.k_cache + at * kPage * HD, a.k_scale + at, ck, r0,
+                                base_s[warp], delta_s, lane);
+      put_page<T, HD, false, IL>(a.plan, rows + kPage * HD, t.r_lo, t.r_hi, a.v_cache + at * kPage * HD, a.v_scale + at,
+                                 cv, r0, base_s[warp], delta_s, lane);
+    }
+    __syncwarp();                                  // the buffer and the angles are read
   }
+  copy_async_wait_all();
+}
+
+template <typename T, int HD, bool IL>
+cudaError_t launch_append_il(const AppendArgs &a, cudaStream_t stream) {
+  auto kern = kvq_append_kernel<T, HD, IL>;
+  constexpr int W = kWarpsOf<T, HD>, smem = W * 2 * kPageBytes<T, HD>;
+  static std::atomic<uint64_t> configured{0};   // one bit per device
+  const int dev = current_device();
+  const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0;
+  if (!bit || !(configured.load() & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    configured.fetch_or(bit);
+  }
+  const int64_t ctas = (a.tasks + W - 1) / W;
+  const unsigned grid = (unsigned)(ctas < device_sm_count() ? ctas : device_sm_count());
+  kern<<<grid, 32 * W, smem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename T, int HD>
-void launch_append(const AppendArgs &a, unsigned grid, cudaStream_t stream) {
-  if (a.plan.interleaved) kvq_append_kernel<T, HD, true><<<grid, kThreads, 0, stream>>>(a);
-  else kvq_append_kernel<T, HD, false><<<grid, kThreads, 0, stream>>>(a);
+cudaError_t launch_append(const AppendArgs &a, cudaStream_t stream) {
+  return a.plan.interleaved ? launch_append_il<T, HD, true>(a, stream) : launch_append_il<T, HD, false>(a, stream);
 }
 
 }  // namespace
@@ -345,15 +367,11 @@ extern "C" simsd_status simsd_kvq_append(const simsd_kvq_append_desc *d, void *s
   a.batch = d->batch; a.Hkv = d->num_kv_heads; a.max_pages = d->max_pages_per_seq;
   a.num_pages = d->num_pages; a.total_n = d->total_n;
   a.tasks = first_item(d->total_n, d->batch) * d->num_kv_heads;
-  const int64_t ctas = (a.tasks + kWarps - 1) / kWarps;
-  const unsigned grid = (unsigned)(ctas < 3 * device_sm_count() ? ctas : 3 * device_sm_count());
   cudaStream_t stream = (cudaStream_t)stream_ptr;
-  if (d->dtype == SIMSD_BF16) {
-    if (d->head_dim == 128) launch_append<__nv_bfloat16, 128>(a, grid, stream);
-    else launch_append<__nv_bfloat16, 64>(a, grid, stream);
-  } else {
-    if (d->head_dim == 128) launch_append<float, 128>(a, grid, stream);
-    else launch_append<float, 64>(a, grid, stream);
-  }
-  return cudaGetLastError() == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
+  cudaError_t e;
+  if (d->dtype == SIMSD_BF16)
+    e = d->head_dim == 128 ? launch_append<__nv_bfloat16, 128>(a, stream) : launch_append<__nv_bfloat16, 64>(a, stream);
+  else
+    e = d->head_dim == 128 ? launch_append<float, 128>(a, stream) : launch_append<float, 64>(a, stream);
+  return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
 }

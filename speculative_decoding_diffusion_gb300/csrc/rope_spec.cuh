@@ -59,6 +59,21 @@ __device__ __forceinline__ float2 rope_plan_angle(const RopePlan &p, int d, int 
   return make_float2(c, s);
 }
 
+// Place of pair d in a shared-memory row of angles that lanes read eight
+// pairs at a time: 16-byte units exchanged so that eight lanes, 64 bytes
+// apart, meet different banks.
+__device__ __forceinline__ int angle_at(int d) { return ((((d >> 1) ^ ((d >> 4) & 3)) << 1) | (d & 1)); }
+
+// Pairs d0 .. d0 + 7 (d0 a multiple of 8) of such a row.
+__device__ __forceinline__ void load_angles8(const float2 *row, int d0, float2 *w) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float4 x = *reinterpret_cast<const float4 *>(row + angle_at(d0 + i));
+    w[i] = make_float2(x.x, x.y);
+    w[i + 1] = make_float2(x.z, x.w);
+  }
+}
+
 // The same times the plan's factor.
 __device__ __forceinline__ float2 rope_plan_cs(const RopePlan &p, int d, int pos) {
   const float2 cs = rope_plan_angle(p, d, pos);
