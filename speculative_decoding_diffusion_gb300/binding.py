@@ -8,6 +8,7 @@ library is missing or cannot be loaded, every call raises.
 """
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -158,13 +159,12 @@ def lib():
         L.simsd_commit_workspace_size.argtypes = [ctypes.POINTER(CommitDesc)]
         L.simsd_commit.restype = ctypes.c_int
         L.simsd_commit.argtypes = [ctypes.POINTER(CommitDesc), _vp]
-        for name, desc in (("rope", RopeDesc), ("page_map", PageMapDesc),
-                           ("kvq_append", KvqAppendDesc), ("kvq_verify", KvqVerifyDesc)):
+        for name in ("rope", "page_map", "kvq_append", "kvq_verify"):   # descriptors as packed bytes
             f = getattr(L, "simsd_" + name)
-            f.restype, f.argtypes = ctypes.c_int, [ctypes.POINTER(desc), _vp]
-            if name in ("page_map", "kvq_verify"):
-                f = getattr(L, "simsd_%s_workspace_size" % name)
-                f.restype, f.argtypes = _sz, [ctypes.POINTER(desc)]
+            f.restype, f.argtypes = ctypes.c_int, [_vp, _vp]
+        for name in ("page_map", "kvq_verify"):
+            f = getattr(L, "simsd_%s_workspace_size" % name)
+            f.restype, f.argtypes = _sz, [_vp]
         L.simsd_read_status.restype = ctypes.c_int
         L.simsd_read_status.argtypes = [_vp, _vp, ctypes.POINTER(ctypes.c_uint32)]
         _LIB = L
@@ -411,34 +411,50 @@ def rope_spec(base=1.0e4, rotary_dim=0, interleaved=False, scaling="plain", fact
                     SIMSD_ROPE_SCALING[scaling], factor, original_len, fast, slow, attn_factor)
 
 
+# The descriptors of these calls are packed by struct (a third of the time of
+# filling a ctypes structure of forty fields); RopeDesc and the others describe
+# the same bytes.
+_PACK_ROPE = struct.Struct("@6i36s5P8q")
+_PACK_PAGE_MAP = struct.Struct("@5i11PN")
+_PACK_APPEND = struct.Struct("@8i36s2q11PN")
+_PACK_VERIFY = struct.Struct("@12i36sfi3q13PN")
+
+
 def _addr(t):
-    return None if t is None else t.data_ptr()
+    return 0 if t is None else t.data_ptr()
+
+
+def _run_on(stream, *tensors):
+    """The stream to launch on, once every tensor (None passes) is seen to lie
+    on the current CUDA device."""
+    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("a tensor is on %s, not on the current CUDA device" % t.device)
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
 
 
 def _heads_of(t, like, what):
     """(row stride, head stride) of a [rows, heads, hd] tensor whose heads are contiguous."""
     if t.dim() != 3 or t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]:
         raise ValueError("%s: expected [rows, heads, head_dim] of one dtype" % what)
-    if t.stride(2) != 1:
+    row, head, one = t.stride()
+    if one != 1:
         raise ValueError("%s: a head's elements must be contiguous" % what)
-    return t.stride(0), t.stride(1)
+    return row, head
 
 
 def _row_stride(t, what):
     """Row stride of a [rows, heads, hd] tensor whose rows are contiguous."""
-    if t.dim() != 3 or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-        raise ValueError("%s: expected [rows, heads, head_dim] with contiguous rows" % what)
-    if t.stride(0) == 0 and t.shape[0] > 1:      # 0 means contiguous rows to the ABI
+    if t.dim() != 3:
+        raise ValueError("%s: expected [rows, heads, head_dim]" % what)
+    rows, heads, hd = t.shape
+    row, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != hd):
+        raise ValueError("%s: expected contiguous rows" % what)
+    if row == 0 and rows > 1:                    # 0 means contiguous rows to the ABI
         raise ValueError("%s: rows that share memory" % what)
-    return t.stride(0)
-
-
-def _on_current_device(*tensors):
-    """Every tensor (None passes) lies on the current CUDA device, where the call runs."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("a tensor is on %s, not on the current CUDA device" % t.device)
+    return row
 
 
 def _same_dtype(like, **tensors):
@@ -452,7 +468,7 @@ def _ints(dtype, **tensors):
     for name, t in tensors.items():
         if t is None:
             continue
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("%s is %s, not %s" % (name, t.dtype, dtype))
         if not t.is_contiguous():
             raise ValueError("%s is not contiguous" % name)
@@ -467,6 +483,10 @@ def _codes(**tensors):
             raise ValueError("%s is not contiguous" % name)
 
 
+def _ws(workspace):
+    return (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
 def rope(x, positions, spec, out, x2=None, out2=None, inverse=False, stream=None):
     """simsd_rope: x [rows, heads, hd] (any row and head strides) rotated into
     out, and x2 into out2 (other head count, same rows) in the same launch.
@@ -474,22 +494,23 @@ def rope(x, positions, spec, out, x2=None, out2=None, inverse=False, stream=None
     if (x2 is None) != (out2 is None):
         raise ValueError("x2 and out2 come together")
     _ints(torch.int32, positions=positions)
-    if positions.shape[0] != x.shape[0]:
+    if x.dim() != 3 or out.shape != x.shape or (x2 is not None and out2.shape != x2.shape):
+        raise ValueError("out: shape of x, [rows, heads, head_dim]")
+    rows, heads, hd = x.shape
+    if positions.shape[0] != rows:
         raise ValueError("positions: one for each row of x")
-    if out.shape != x.shape or (x2 is not None and out2.shape != x2.shape):
-        raise ValueError("out: shape of x")
     h2, s2, o2 = (0, (0, 0), (0, 0)) if x2 is None else (
         x2.shape[1], _heads_of(x2, x, "x2"), _heads_of(out2, x, "out2"))
-    _on_current_device(x, positions, out, x2, out2)
-    d = RopeDesc(x.shape[0], x.shape[1], h2, x.shape[2], _dtype_code(x), int(bool(inverse)), spec,
-                 positions.data_ptr(), x.data_ptr(), out.data_ptr(), _addr(x2), _addr(out2),
-                 *_heads_of(x, x, "x"), *_heads_of(out, x, "out"), *s2, *o2)
-    _check(lib().simsd_rope(ctypes.byref(d), _stream(stream)), "simsd_rope")
+    d = _PACK_ROPE.pack(rows, heads, h2, hd, _dtype_code(x), 1 if inverse else 0, bytes(spec),
+                        positions.data_ptr(), x.data_ptr(), out.data_ptr(), _addr(x2), _addr(out2),
+                        *_heads_of(x, x, "x"), *_heads_of(out, x, "out"), *s2, *o2)
+    s = _run_on(stream, x, positions, out, x2, out2)
+    _check(lib().simsd_rope(d, s), "simsd_rope")
 
 
 def page_map_workspace_size(lens, block_table, free_pages, total_n):
-    d = PageMapDesc(lens.shape[0], 16, free_pages.shape[0], block_table.shape[1], int(total_n))
-    n = lib().simsd_page_map_workspace_size(ctypes.byref(d))
+    d = _PACK_PAGE_MAP.pack(lens.shape[0], 16, free_pages.shape[0], block_table.shape[1], int(total_n), *[0] * 12)
+    n = lib().simsd_page_map_workspace_size(d)
     if n == 0:
         raise SimsdError(2, "simsd_page_map_workspace_size")
     return int(n)
@@ -502,24 +523,29 @@ def page_map(lens, cu_n, held, queue, free_pages, block_table, held_out, queue_o
     _ints(torch.int32, lens=lens, cu_n=cu_n, held=held, queue=queue, free_pages=free_pages,
           block_table=block_table, held_out=held_out, queue_out=queue_out, served=served)
     _ints(torch.int64, slots=slots)
-    batch = lens.shape[0]
-    if (held.shape[0] != batch or held_out.shape[0] != batch or served.shape[0] != batch or
-            block_table.shape[0] != batch or (cu_n is not None and cu_n.shape[0] != batch + 1) or
+    (batch,), (tables, width) = lens.shape, block_table.shape
+    if (held.numel() != batch or held_out.numel() != batch or served.numel() != batch or
+            tables != batch or (cu_n is not None and cu_n.numel() != batch + 1) or
             queue.numel() != 2 or queue_out.numel() != 2 or
-            (slots is not None and slots.shape[0] < total_n)):
+            (slots is not None and slots.numel() < total_n)):
         raise ValueError("page_map: sizes of the arrays disagree")
-    _on_current_device(lens, cu_n, held, queue, free_pages, block_table, held_out, queue_out, served,
-                       slots, workspace)
-    d = PageMapDesc(batch, 16, free_pages.shape[0], block_table.shape[1], int(total_n),
-                    lens.data_ptr(), _addr(cu_n), held.data_ptr(), queue.data_ptr(),
-                    free_pages.data_ptr(), block_table.data_ptr(), held_out.data_ptr(),
-                    queue_out.data_ptr(), served.data_ptr(), _addr(slots), *_ws(workspace))
-    _check(lib().simsd_page_map(ctypes.byref(d), _stream(stream)), "simsd_page_map")
+    d = _PACK_PAGE_MAP.pack(batch, 16, free_pages.numel(), width, total_n,
+                            lens.data_ptr(), _addr(cu_n), held.data_ptr(), queue.data_ptr(),
+                            free_pages.data_ptr(), block_table.data_ptr(), held_out.data_ptr(),
+                            queue_out.data_ptr(), served.data_ptr(), _addr(slots), *_ws(workspace))
+    s = _run_on(stream, lens, cu_n, held, queue, free_pages, block_table, held_out, queue_out, served,
+                slots, workspace)
+    _check(lib().simsd_page_map(d, s), "simsd_page_map")
 
 
-def _ws(workspace):
-    return (None, 0) if workspace is None else (
-        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+def _cache_shape(k_cache, v_cache, k_scale, v_scale, hkv, hd, what):
+    """(num_pages, page_size), the four arrays being one cache of hkv heads of hd."""
+    _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    shape = k_cache.shape
+    if (len(shape) != 4 or v_cache.shape != shape or shape[1] != hkv or shape[3] != hd or
+            k_scale.shape != shape[:2] or v_scale.shape != shape[:2]):
+        raise ValueError("%s: sizes of the cache's arrays disagree" % what)
+    return shape[0], shape[2]
 
 
 def kvq_append(k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_table, workspace, spec,
@@ -527,53 +553,47 @@ def kvq_append(k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_tabl
     """simsd_kvq_append: k (rotated by spec) and v [total_n, Hkv, hd] into the
     e4m3 caches [num_pages, Hkv, 16, hd] with e8m0 scales [num_pages, Hkv]."""
     _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table, take=take)
-    _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
     _same_dtype(k, v=v)
-    batch, hkv = start.shape[0], k.shape[1]
-    if (v.shape != k.shape or k_cache.shape != v_cache.shape or k_cache.shape[1] != hkv or
-            k_cache.shape[3] != k.shape[2] or tuple(k_scale.shape) != tuple(k_cache.shape[:2]) or
-            tuple(v_scale.shape) != tuple(k_cache.shape[:2]) or cu_n.shape[0] != batch + 1 or
-            block_table.shape[0] != batch or (take is not None and take.shape[0] != batch)):
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("kvq_append: k and v are [rows, heads, head_dim]")
+    total_n, hkv, hd = k.shape
+    num_pages, page = _cache_shape(k_cache, v_cache, k_scale, v_scale, hkv, hd, "kvq_append")
+    (batch,), (tables, width) = start.shape, block_table.shape
+    if cu_n.numel() != batch + 1 or tables != batch or (take is not None and take.numel() != batch):
         raise ValueError("kvq_append: sizes of the arrays disagree")
-    _on_current_device(k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_table, workspace,
-                       take)
-    d = KvqAppendDesc(batch, hkv, k.shape[2], k_cache.shape[2], k_cache.shape[0],
-                      block_table.shape[1], k.shape[0], _dtype_code(k), spec,
-                      _row_stride(k, "k"), _row_stride(v, "v"), k.data_ptr(), v.data_ptr(),
-                      start.data_ptr(), cu_n.data_ptr(), _addr(take), k_cache.data_ptr(),
-                      v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                      block_table.data_ptr(), *_ws(workspace))
-    _check(lib().simsd_kvq_append(ctypes.byref(d), _stream(stream)), "simsd_kvq_append")
+    d = _PACK_APPEND.pack(batch, hkv, hd, page, num_pages, width, total_n, _dtype_code(k), bytes(spec),
+                          _row_stride(k, "k"), _row_stride(v, "v"), k.data_ptr(), v.data_ptr(),
+                          start.data_ptr(), cu_n.data_ptr(), _addr(take), k_cache.data_ptr(),
+                          v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                          block_table.data_ptr(), *_ws(workspace))
+    s = _run_on(stream, k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_table, workspace, take)
+    _check(lib().simsd_kvq_append(d, s), "simsd_kvq_append")
 
 
 def _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
                      cu_B, out, workspace, total_B, B_max, spec, sm_scale, order, node_size,
                      wait_polls=0):
     _ints(torch.int32, block_table=block_table, tau=tau, lens=lens, cu_B=cu_B)
-    _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
     _same_dtype(q, k_new=k_new, v_new=v_new, out=out)
-    batch, hkv, hd = lens.shape[0], k_new.shape[1], q.shape[2]
-    rows = int(total_B) * (2 if order == SIMSD_ORDER_PAIRED else 1)
-    if (out.shape != q.shape or q.shape[0] < rows or k_new.shape[0] < rows or
-            v_new.shape != k_new.shape or k_new.shape[2] != hd or k_cache.shape != v_cache.shape or
-            k_cache.shape[1] != hkv or k_cache.shape[3] != hd or
-            tuple(k_scale.shape) != tuple(k_cache.shape[:2]) or
-            tuple(v_scale.shape) != tuple(k_cache.shape[:2]) or cu_B.shape[0] != batch + 1 or
-            block_table.shape[0] != batch or
-            (order == SIMSD_ORDER_PAIRED and tau is not None and tau.shape[0] < total_B)):
+    paired = order == SIMSD_ORDER_PAIRED
+    if q.dim() != 3 or k_new.dim() != 3 or out.shape != q.shape or v_new.shape != k_new.shape:
+        raise ValueError("kvq_verify: q, out and k_new, v_new are [rows, heads, head_dim]")
+    (T, hq, hd), (Tk, hkv, hdk) = q.shape, k_new.shape
+    num_pages, page = _cache_shape(k_cache, v_cache, k_scale, v_scale, hkv, hd, "kvq_verify")
+    (batch,), (tables, width) = lens.shape, block_table.shape
+    rows = 2 * total_B if paired else total_B
+    if (T < rows or Tk < rows or hdk != hd or cu_B.numel() != batch + 1 or tables != batch or
+            (paired and tau is not None and tau.numel() < total_B)):
         raise ValueError("kvq_verify: sizes of the arrays disagree")
     if not out.is_contiguous():
         raise ValueError("out is not contiguous")
-    _on_current_device(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens, cu_B,
-                       out, workspace)
-    return KvqVerifyDesc(batch, q.shape[1], hkv, hd, k_cache.shape[2], k_cache.shape[0],
-                         block_table.shape[1], int(total_B), int(B_max), _dtype_code(q), int(order),
-                         int(node_size), spec, float(sm_scale), int(wait_polls),
-                         _row_stride(q, "q"), _row_stride(k_new, "k_new"),
-                         _row_stride(v_new, "v_new"), q.data_ptr(), k_cache.data_ptr(),
-                         v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
-                         block_table.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _addr(tau),
-                         lens.data_ptr(), cu_B.data_ptr(), out.data_ptr(), *_ws(workspace))
+    return _PACK_VERIFY.pack(batch, hq, hkv, hd, page, num_pages, width, total_B, B_max, _dtype_code(q),
+                             order, node_size, bytes(spec), sm_scale, wait_polls, _row_stride(q, "q"),
+                             _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), q.data_ptr(),
+                             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                             v_scale.data_ptr(), block_table.data_ptr(), k_new.data_ptr(),
+                             v_new.data_ptr(), _addr(tau), lens.data_ptr(), cu_B.data_ptr(),
+                             out.data_ptr(), *_ws(workspace))
 
 
 def kvq_verify_workspace_size(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau,
@@ -581,7 +601,7 @@ def kvq_verify_workspace_size(q, k_cache, v_cache, k_scale, v_scale, block_table
                               order=SIMSD_ORDER_PAIRED, node_size=0):
     d = _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
                          cu_B, out, None, total_B, B_max, spec, sm_scale, order, node_size)
-    n = lib().simsd_kvq_verify_workspace_size(ctypes.byref(d))
+    n = lib().simsd_kvq_verify_workspace_size(d)
     if n == 0:
         raise SimsdError(2, "simsd_kvq_verify_workspace_size")
     return int(n)
@@ -596,7 +616,9 @@ def kvq_verify(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new,
     d = _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
                          cu_B, out, workspace, total_B, B_max, spec, sm_scale, order, node_size,
                          wait_polls)
-    _check(lib().simsd_kvq_verify(ctypes.byref(d), _stream(stream)), "simsd_kvq_verify")
+    s = _run_on(stream, q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens, cu_B,
+                out, workspace)
+    _check(lib().simsd_kvq_verify(d, s), "simsd_kvq_verify")
 
 
 def read_status(workspace, stream=None):

@@ -13,10 +13,12 @@
 // (two a lane), times the turn by 0..15 positions from a table that
 // the CTA makes once -- one product instead of a sine and a cosine for each
 // row.  Bytes in, half as many (bf16) out: DRAM bounds a prompt's append, and
-// latency what it reaches of it: a warp's next page is copied into shared
-// memory (16-byte asynchronous copies) while the present one is worked on,
-// 12 warps x 16 KB an SM (in registers, 12 warps x 8 KB: 1.50 ms for 256
-// prompts; 16 x 4 KB: 2.15).
+// latency what it reaches of it: while a warp works on a page's values the
+// next page's keys are copied into shared memory (16-byte asynchronous
+// copies), and so in turn; 16 warps an SM.  256 prompts (1.07 M tokens, bf16,
+// 8 heads of 128): 1.24 ms, 5.3 TB/s of its bytes (12 warps with two pages of
+// buffers each 1.49; rows held in registers instead 1.50; angles by a sine
+// and a cosine for each row and lanes that met in the same banks 1.70 and up).
 #include <math.h>
 
 #include <atomic>
@@ -30,9 +32,9 @@
 namespace simsd {
 namespace {
 
-// Warps of a CTA (one CTA an SM): two pages of raw rows, keys and values, each.
+// Warps of a CTA (one CTA an SM): a page's raw rows, keys and values, each.
 template <typename T, int HD> constexpr int kPageBytes = 2 * kPage * HD * (int)sizeof(T);
-template <typename T, int HD> constexpr int kWarpsOf = kPageBytes<T, HD> <= 8192 ? 12 : 6;
+template <typename T, int HD> constexpr int kWarpsOf = kPageBytes<T, HD> <= 8192 ? 16 : 12;
 constexpr int kStageSeqs = 1024;          // sequences whose prefix sums are staged in shared memory
 
 struct AppendArgs {
@@ -180,22 +182,22 @@ template <typename T, int HD, bool IL>
 __global__ void __launch_bounds__(32 * kWarpsOf<T, HD>, 1)
 kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   __shared__ __align__(16) float2 delta_s[kPage][64];
-  constexpr int kWarps = kWarpsOf<T, HD>, kThreads = 32 * kWarps;
-  __shared__ __align__(16) float2 base_s[kWarps][64];
+  const int n_threads = blockDim.x, n_warps = n_threads / 32;
+  __shared__ __align__(16) float2 base_s[kWarpsOf<T, HD>][64];
   __shared__ int32_t cu_s[kStageSeqs + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const RopePlan &plan = plan_by_lane(a.plan);
   const bool staged = a.batch <= kStageSeqs;
   if (staged)
-    for (int i = threadIdx.x; i <= a.batch; i += kThreads) cu_s[i] = __ldg(a.cu_n + i);
+    for (int i = threadIdx.x; i <= a.batch; i += n_threads) cu_s[i] = __ldg(a.cu_n + i);
   // turns by 1, 2, 4 and 8 positions, then the products for the rest
-  for (int e = threadIdx.x; e < 4 * 64; e += kThreads) {
+  for (int e = threadIdx.x; e < 4 * 64; e += n_threads) {
     const int r = 1 << (e >> 6), d = e & 63;
     if (d < a.plan.half) delta_s[r][angle_at(d)] = rope_plan_angle(plan, d, r);
   }
   if (threadIdx.x < 64) delta_s[0][threadIdx.x] = make_float2(1.f, 0.f);
   __syncthreads();
-  for (int e = threadIdx.x; e < kPage * 64; e += kThreads) {
+  for (int e = threadIdx.x; e < kPage * 64; e += n_threads) {
     const int r = e >> 6, d = angle_at(e & 63), low = r & -r;
     if (r != low && (e & 63) < a.plan.half) {
       float2 w = delta_s[low][d];
@@ -206,8 +208,8 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   }
   __syncthreads();
   auto cu = [&](int b) { return staged ? cu_s[b] : __ldg(a.cu_n + b); };
-  extern __shared__ __align__(16) uint8_t pages_s[];         // [warp][2][K, V][16][HD]
-  T *mine = reinterpret_cast<T *>(pages_s) + (int64_t)warp * 4 * kPage * HD;
+  extern __shared__ __align__(16) uint8_t pages_s[];         // [warp][K, V][16][HD]
+  T *mine = reinterpret_cast<T *>(pages_s) + (int64_t)warp * 2 * kPage * HD;
   constexpr int L = HD / 16;
   const int ln = lane % L, r0 = lane / L;
   Chunks ck, cv;                                   // of keys and of values
@@ -264,45 +266,48 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
     return t;
   };
   auto good = [&](const Task &t) { return t.any && t.page >= 0 && t.page < a.num_pages; };
-  // starts copying a task's new rows into buffer `buf`
-  auto fetch = [&](const Task &t, int buf) {
+  // starts copying a task's new rows, keys (kv 0) or values
+  auto fetch = [&](const Task &t, int kv) {
     if (good(t)) {
       constexpr int C = HD * (int)sizeof(T) / 16;  // 16-byte chunks of a row
-      const T *ks = (const T *)a.k + t.row0 * a.k_row + t.h * HD, *vs = (const T *)a.v + t.row0 * a.v_row + t.h * HD;
-      const uint32_t dst = smem_u32(mine + buf * 2 * kPage * HD);
+      const int64_t stride = kv ? a.v_row : a.k_row;
+      const T *src = (const T *)(kv ? a.v : a.k) + t.row0 * stride + t.h * HD;
+      const uint32_t dst = smem_u32(mine + kv * kPage * HD);
 #pragma unroll
       for (int e = lane; e < kPage * C; e += 32) {
         const int r = e / C, ch = e % C;
-        if (r >= t.r_lo && r < t.r_hi) {
-          copy16_async(dst + e * 16, (const char *)(ks + r * a.k_row) + ch * 16, true);
-          copy16_async(dst + (kPage * C + e) * 16, (const char *)(vs + r * a.v_row) + ch * 16, true);
-        }
+        if (r >= t.r_lo && r < t.r_hi)
+          copy16_async(dst + e * 16, (const char *)(src + r * stride) + ch * 16, true);
       }
     }
     copy_async_commit();
   };
-  const int64_t step = (int64_t)gridDim.x * kWarps;
-  int64_t task = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t step = (int64_t)gridDim.x * n_warps;
+  int64_t task = (int64_t)blockIdx.x * n_warps + warp;
   Task next = find(task);
   fetch(next, 0);
-  for (int buf = 0; task < a.tasks; task += step, buf ^= 1) {
+  fetch(next, 1);
+  for (; task < a.tasks; task += step) {
     const Task t = next;
     next = find(task + step);
     if ((t.bad || (t.any && !good(t))) && lane == 0) raise_status(a.status, kStatusBadInput);
     if (good(t))
       for (int d = lane; d < a.plan.half; d += 32) base_s[warp][angle_at(d)] = rope_plan_cs(plan, d, t.pos0);
-    fetch(next, buf ^ 1);
-    copy_async_wait<1>();
+    const int64_t at = (int64_t)t.page * a.Hkv + t.h;
+    copy_async_wait<1>();                          // the keys
     __syncwarp();
-    if (good(t)) {
-      const T *rows = mine + buf * 2 * kPage * HD;
-      const int64_t at = (int64_t)t.page * a.Hkv + t.h;
-      put_page<T, HD, true, IL>(a.plan, rows, t.r_lo, t.r_hi, a.k_cache + at * kPage * HD, a.k_scale + at, ck, r0,
+    if (good(t))
+      put_page<T, HD, true, IL>(a.plan, mine, t.r_lo, t.r_hi, a.k_cache + at * kPage * HD, a.k_scale + at, ck, r0,
                                 base_s[warp], delta_s, lane);
-      put_page<T, HD, false, IL>(a.plan, rows + kPage * HD, t.r_lo, t.r_hi, a.v_cache + at * kPage * HD, a.v_scale + at,
+    __syncwarp();
+    fetch(next, 0);
+    copy_async_wait<1>();                          // the values
+    __syncwarp();
+    if (good(t))
+      put_page<T, HD, false, IL>(a.plan, mine + kPage * HD, t.r_lo, t.r_hi, a.v_cache + at * kPage * HD, a.v_scale + at,
                                  cv, r0, base_s[warp], delta_s, lane);
-    }
-    __syncwarp();                                  // the buffer and the angles are read
+    __syncwarp();
+    fetch(next, 1);
   }
   copy_async_wait_all();
 }
@@ -310,7 +315,7 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
 template <typename T, int HD, bool IL>
 cudaError_t launch_append_il(const AppendArgs &a, cudaStream_t stream) {
   auto kern = kvq_append_kernel<T, HD, IL>;
-  constexpr int W = kWarpsOf<T, HD>, smem = W * 2 * kPageBytes<T, HD>;
+  constexpr int W = kWarpsOf<T, HD>, smem = W * kPageBytes<T, HD>;
   static std::atomic<uint64_t> configured{0};   // one bit per device
   const int dev = current_device();
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0;
@@ -319,9 +324,12 @@ cudaError_t launch_append_il(const AppendArgs &a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  const int64_t ctas = (a.tasks + W - 1) / W;
-  const unsigned grid = (unsigned)(ctas < device_sm_count() ? ctas : device_sm_count());
-  kern<<<grid, 32 * W, smem, stream>>>(a);
+  // a CTA per SM, of fewer warps where there are few tasks (64 x 8 tokens: 8
+  // warps 5.8 us, 16 on half the SMs 7.1)
+  const int64_t sms = device_sm_count(), per_sm = (a.tasks + sms - 1) / sms;
+  const int warps = (int)(per_sm < 4 ? 4 : per_sm > W ? W : per_sm);
+  const int64_t ctas = (a.tasks + warps - 1) / warps;
+  kern<<<(unsigned)(ctas < sms ? ctas : sms), 32 * warps, warps * kPageBytes<T, HD>, stream>>>(a);
   return cudaGetLastError();
 }
 

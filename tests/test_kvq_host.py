@@ -188,3 +188,19 @@ def test_binding_refuses_what_it_would_misread():
         binding._ints(torch.int32, lens=ids.long())
     with pytest.raises(ValueError):
         binding._ints(torch.int32, lens=torch.zeros(8, dtype=torch.int32)[::2])
+
+
+@pytest.mark.parametrize("pack,desc", [("_PACK_ROPE", "RopeDesc"), ("_PACK_PAGE_MAP", "PageMapDesc"),
+                                       ("_PACK_APPEND", "KvqAppendDesc"), ("_PACK_VERIFY", "KvqVerifyDesc")])
+def test_packed_descriptors_are_the_structures(pack, desc):
+    """Packing distinct values and reading them back through the structure gives the same values in the same fields."""
+    fmt, cls = getattr(binding, pack), getattr(binding, desc)
+    assert fmt.size == ctypes.sizeof(cls)
+    spec = binding.rope_spec(base=7.0, rotary_dim=32, interleaved=True, scaling="yarn", factor=3.0, original_len=99)
+    values = [bytes(spec) if f == "rope" else i + 1 for i, (f, _) in enumerate(cls._fields_)]
+    d = cls.from_buffer_copy(fmt.pack(*values))
+    for i, (f, _) in enumerate(cls._fields_):
+        if f == "rope":
+            assert bytes(d.rope) == bytes(spec) and d.rope.original_len == 99
+        else:
+            assert getattr(d, f) == i + 1, f
