@@ -424,24 +424,34 @@ def _addr(t):
     return 0 if t is None else t.data_ptr()
 
 
+# (a torch.cuda.Stream object for the current stream takes longer to make than
+# a kernel to launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _run_on(stream, *tensors):
     """The stream to launch on, once every tensor (None passes) is seen to lie
     on the current CUDA device."""
-    dev = torch.cuda.current_device() if torch.cuda.is_available() else -2
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("a tensor is on %s, not on the current CUDA device" % t.device)
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev)
 
 
-def _heads_of(t, like, what):
-    """(row stride, head stride) of a [rows, heads, hd] tensor whose heads are contiguous."""
-    if t.dim() != 3 or t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]:
-        raise ValueError("%s: expected [rows, heads, head_dim] of one dtype" % what)
+def _heads_of(t, dtype, rows, hd, what):
+    """(heads, row stride, head stride) of a [rows, heads, hd] tensor whose heads are contiguous."""
+    if t.dim() != 3 or t.dtype is not dtype:
+        raise ValueError("%s: expected [rows, heads, head_dim] of %s" % (what, dtype))
+    r, heads, d = t.shape
     row, head, one = t.stride()
+    if r != rows or d != hd:
+        raise ValueError("%s: expected %d rows and head_dim %d" % (what, rows, hd))
     if one != 1:
         raise ValueError("%s: a head's elements must be contiguous" % what)
-    return row, head
+    return heads, row, head
 
 
 def _row_stride(t, what):
@@ -494,17 +504,24 @@ def rope(x, positions, spec, out, x2=None, out2=None, inverse=False, stream=None
     if (x2 is None) != (out2 is None):
         raise ValueError("x2 and out2 come together")
     _ints(torch.int32, positions=positions)
-    if x.dim() != 3 or out.shape != x.shape or (x2 is not None and out2.shape != x2.shape):
-        raise ValueError("out: shape of x, [rows, heads, head_dim]")
-    rows, heads, hd = x.shape
-    if positions.shape[0] != rows:
+    if x.dim() != 3:
+        raise ValueError("x: expected [rows, heads, head_dim]")
+    rows, _, hd = x.shape
+    dtype = x.dtype
+    h1, row1, head1 = _heads_of(x, dtype, rows, hd, "x")
+    k1, orow1, ohead1 = _heads_of(out, dtype, rows, hd, "out")
+    h2 = k2 = row2 = head2 = orow2 = ohead2 = 0
+    if x2 is not None:
+        h2, row2, head2 = _heads_of(x2, dtype, rows, hd, "x2")
+        k2, orow2, ohead2 = _heads_of(out2, dtype, rows, hd, "out2")
+    if k1 != h1 or k2 != h2:
+        raise ValueError("out: heads of x")
+    if positions.numel() != rows:
         raise ValueError("positions: one for each row of x")
-    h2, s2, o2 = (0, (0, 0), (0, 0)) if x2 is None else (
-        x2.shape[1], _heads_of(x2, x, "x2"), _heads_of(out2, x, "out2"))
-    d = _PACK_ROPE.pack(rows, heads, h2, hd, _dtype_code(x), 1 if inverse else 0, bytes(spec),
-                        positions.data_ptr(), x.data_ptr(), out.data_ptr(), _addr(x2), _addr(out2),
-                        *_heads_of(x, x, "x"), *_heads_of(out, x, "out"), *s2, *o2)
     s = _run_on(stream, x, positions, out, x2, out2)
+    d = _PACK_ROPE.pack(rows, h1, h2, hd, _dtype_code(x), 1 if inverse else 0, bytes(spec),
+                        positions.data_ptr(), x.data_ptr(), out.data_ptr(), _addr(x2), _addr(out2),
+                        row1, head1, orow1, ohead1, row2, head2, orow2, ohead2)
     _check(lib().simsd_rope(d, s), "simsd_rope")
 
 

@@ -177,7 +177,7 @@ def test_binding_refuses_what_it_would_misread():
     with pytest.raises(ValueError):                        # one of two second tensors
         binding.rope(q, ids, spec, q, q)
     with pytest.raises(ValueError):                        # a head's elements apart
-        binding._heads_of(q.transpose(1, 2), q, "x")
+        binding._heads_of(q.transpose(1, 2), q.dtype, 4, 2, "x")
     with pytest.raises(ValueError):                        # broadcast rows
         binding._row_stride(q[:1].expand(4, 2, 64), "k")
     with pytest.raises(ValueError):
