@@ -26,6 +26,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kMaxBatch = 16384;
+constexpr int kStaged = 8192;              // sequences whose lengths and counts are kept as well
 constexpr size_t kMapWorkspace = kAlign;   // status word; the done counter at kClaimOffset
 
 struct MapArgs {
@@ -42,22 +43,16 @@ struct Seq {
   bool ok, rows_ok;     // rows_ok: its range of cu_n is valid
 };
 
-__device__ __forceinline__ Seq load_seq(const MapArgs &a, int b) {
+__device__ __forceinline__ Seq make_seq(const MapArgs &a, int len, int held, int c0, int c1) {
   Seq s;
-  s.len = __ldg(a.lens + b);
-  s.held = __ldcg(a.held + b);
-  s.c0 = 0;
-  s.n = 0;
-  s.rows_ok = true;
-  if (a.cu_n != nullptr) {
-    s.c0 = __ldg(a.cu_n + b);
-    const int c1 = __ldg(a.cu_n + b + 1);
-    s.rows_ok = s.c0 >= 0 && c1 >= s.c0 && c1 <= a.total_n;
-    s.n = s.rows_ok ? c1 - s.c0 : 0;
-  }
-  const int64_t pages = ((int64_t)s.len + s.n + kPage - 1) / kPage;
-  s.ok = s.rows_ok && s.len >= 0 && pages <= a.width && s.held >= 0 && s.held <= a.width;
-  s.need = s.ok ? (int)pages : s.held;
+  s.len = len;
+  s.held = held;
+  s.c0 = c0;
+  s.rows_ok = c0 >= 0 && c1 >= c0 && c1 <= a.total_n;
+  s.n = s.rows_ok ? c1 - c0 : 0;
+  const int64_t pages = ((int64_t)len + s.n + kPage - 1) / kPage;
+  s.ok = s.rows_ok && len >= 0 && pages <= a.width && held >= 0 && held <= a.width;
+  s.need = s.ok ? (int)pages : held;
   return s;
 }
 
@@ -76,7 +71,14 @@ __device__ __forceinline__ int wrap(int64_t i, int cap) { return (int)(i >= cap 
 __global__ void __launch_bounds__(kThreads)
 page_map_kernel(const __grid_constant__ MapArgs a) {
   extern __shared__ int32_t smem[];
-  int *D = smem, *E = smem + a.batch + 1;        // exclusive prefix sums, [batch + 1]
+  const int n1 = a.batch + 1;
+  int *D = smem, *E = D + n1, *C = E + n1;       // exclusive prefix sums; cu_n
+  int *len_s = C + n1, *held_s = len_s + n1;     // (batches of up to kStaged)
+  const bool staged = a.batch <= kStaged;
+  auto seq = [&](int b) {
+    return staged ? make_seq(a, len_s[b], held_s[b], C[b], C[b + 1])
+                  : make_seq(a, __ldg(a.lens + b), __ldcg(a.held + b), C[b], C[b + 1]);
+  };
   __shared__ uint64_t warp_sum[32];
   __shared__ int last_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -88,7 +90,15 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
     const int b = b0 + threadIdx.x;
     uint64_t x = 0;
     if (b < a.batch) {
-      const Seq s = load_seq(a, b);
+      const int len = __ldg(a.lens + b), held = __ldcg(a.held + b);
+      const int c0 = a.cu_n != nullptr ? __ldg(a.cu_n + b) : 0, c1 = a.cu_n != nullptr ? __ldg(a.cu_n + b + 1) : 0;
+      C[b] = c0;
+      if (b == a.batch - 1) C[a.batch] = c1;
+      if (staged) {
+        len_s[b] = len;
+        held_s[b] = held;
+      }
+      const Seq s = make_seq(a, len, held, c0, c1);
       bad |= !s.ok;
       x = (uint64_t)(uint32_t)max(0, s.need - s.held) | (uint64_t)(uint32_t)max(0, s.held - s.need) << 32;
     }
@@ -130,13 +140,13 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
   if (ring_ok) {
     for (int g = t0; g < dropped; g += step) {
       const int b = last_not_above(E, a.batch, g);
-      const Seq s = load_seq(a, b);
+      const Seq s = seq(b);
       a.ring[wrap((int64_t)head + count + g, a.cap)] =       // count + dropped <= cap: one wrap
           a.table[(int64_t)b * a.width + s.need + (g - E[b])];
     }
     for (int g = t0; g < taken; g += step) {
       const int b = last_not_above(D, a.batch, g);
-      const int j = __ldcg(a.held + b) + (g - D[b]);
+      const int j = (staged ? held_s[b] : __ldcg(a.held + b)) + (g - D[b]);
       const int page = __ldcg(a.ring + wrap((int64_t)head + g, a.cap));
       if (page < 0 || page >= a.cap) raise_status(a.status, kStatusBadInput);
       a.table[(int64_t)b * a.width + j] = page;
@@ -144,10 +154,10 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
   }
   // slots of the new tokens
   if (a.slots != nullptr && a.cu_n != nullptr) {
-    const int end = min(a.total_n, __ldg(a.cu_n + a.batch));
+    const int end = min(a.total_n, C[a.batch]);
     for (int t = t0; t < end; t += step) {
-      const int b = find_seq(a.cu_n, a.batch, t);
-      const Seq s = load_seq(a, b);
+      const int b = find_seq_smem(C, a.batch, t);
+      const Seq s = seq(b);
       if (!s.rows_ok || t < s.c0 || t >= s.c0 + s.n) continue;
       const bool served = ring_ok && s.ok && (s.need <= s.held || D[b + 1] <= count);
       int64_t slot = -1;
@@ -170,7 +180,7 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
   __syncthreads();
   if (!last_s) return;
   for (int b = threadIdx.x; b < a.batch; b += kThreads) {
-    const Seq s = load_seq(a, b);
+    const Seq s = seq(b);
     const bool served = ring_ok && s.ok && (s.need <= s.held || D[b + 1] <= count);
     a.served[b] = served;
     a.held_out[b] = served ? s.need : s.held;
@@ -222,14 +232,14 @@ simsd_status simsd_page_map(const simsd_page_map_desc *d, void *stream_ptr) {
   const int64_t work = std::max<int64_t>(d->total_n / (2 * kThreads),
                                          (int64_t)d->batch * d->max_pages_per_seq / (16 * kThreads));
   const int grid = (int)std::min<int64_t>(std::max<int64_t>(work, 1), device_sm_count());
-  const size_t smem = 2 * (size_t)(d->batch + 1) * sizeof(int32_t);
+  const size_t smem = (d->batch <= kStaged ? 5 : 3) * (size_t)(d->batch + 1) * sizeof(int32_t);
   if (smem > 48 * 1024) {
     static std::atomic<uint64_t> configured{0};   // one bit per device
     const int dev = current_device();
     const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0;
     if (!bit || !(configured.load() & bit)) {
       if (cudaFuncSetAttribute(page_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               2 * (kMaxBatch + 1) * (int)sizeof(int32_t)) != cudaSuccess)
+                               3 * (kMaxBatch + 1) * (int)sizeof(int32_t)) != cudaSuccess)
         return SIMSD_ERR_CUDA;
       configured.fetch_or(bit);
     }
