@@ -39,18 +39,6 @@ struct SimtSmem {
   float p[kRows][kTile];
 };
 
-// Element e of a rotated row x with angles cs.
-template <typename T>
-__device__ __forceinline__ float rotated(const RopePlan &p, const float2 *cs, const T *x, int e) {
-  const float u = Elem<T>::load(x + e);
-  if (e >= 2 * p.half) return u;
-  const bool low = p.interleaved ? !(e & 1) : e < p.half;
-  const int partner = p.interleaved ? (e ^ 1) : (low ? e + p.half : e - p.half);
-  const float2 w = cs[p.interleaved ? e >> 1 : (low ? e : e - p.half)];
-  const float y = Elem<T>::load(x + partner);
-  return low ? u * w.x - y * w.y : u * w.x + y * w.y;
-}
-
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads)
 kvq_simt_kernel(const __grid_constant__ KvqParams a) {
@@ -65,32 +53,42 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
   const int rows = min(kRows, w.M - w.row0);
   if (a.order == SIMSD_ORDER_PAIRED && threadIdx.x < w.B) tau_s[threadIdx.x] = __ldg(a.tau + w.c0 + threadIdx.x);
   const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
-  const int half = a.plan.half;
   float2 *cs = reinterpret_cast<float2 *>(&s.v[0][0]);   // [kMaxNew][HD / 2]
-  for (int e = threadIdx.x; e < npos * half; e += kThreads)
-    cs[(e / half) * (HD / 2) + e % half] = rope_plan_cs(plan_by_lane(a.plan), e % half, w.P + e / half);
+  for (int e = threadIdx.x; e < npos * (HD / 2); e += kThreads) {
+    const int d = e % (HD / 2);
+    cs[e - d + angle_at(d)] = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
+  }
   __syncthreads();
   const int64_t t0 = (int64_t)a.per * w.c0;              // first new token's row
-  for (int e = threadIdx.x; e < kRows * HD; e += kThreads) {
-    const int r = e / HD, d = e % HD;
-    float x = 0.f;
+  constexpr int CH = HD / 8;
+  for (int e = threadIdx.x; e < kRows * CH; e += kThreads) {
+    const int r = e / CH, c = e % CH;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
     if (r < rows) {
       const int tok = (w.row0 + r) / a.G, head = w.kvh * a.G + (w.row0 + r) % a.G;
-      x = rotated(a.plan, cs + kvq_offset(a, w.B, tok) * (HD / 2),
-                  (const T *)a.q + (t0 + tok) * a.q_row + head * HD, d) * a.scale;
+      rotate8(a.plan, cs + kvq_offset(a, w.B, tok) * (HD / 2), (const T *)a.q + (t0 + tok) * a.q_row + head * HD, c * 8, x);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] *= a.scale;
     }
-    s.q[r][d] = x;
+    store_vec<float, 8>(&s.q[r][c * 8], x);
   }
-  if (w.first) {
-    for (int e = threadIdx.x; e < kTile * HD; e += kThreads) {
-      const int j = e / HD, d = e % HD;
-      s.k[j][d] = j < w.n ? rotated(a.plan, cs + kvq_offset(a, w.B, j) * (HD / 2),
-                                    (const T *)a.k_new + (t0 + j) * a.k_row + w.kvh * HD, d) : 0.f;
+  if (w.first) {                                         // keys past the last new token are masked, their values zero
+    for (int e = threadIdx.x; e < w.n * CH; e += kThreads) {
+      const int j = e / CH, c = e % CH;
+      float x[8];
+      rotate8(a.plan, cs + kvq_offset(a, w.B, j) * (HD / 2), (const T *)a.k_new + (t0 + j) * a.k_row + w.kvh * HD, c * 8, x);
+      store_vec<float, 8>(&s.k[j][c * 8], x);
     }
     __syncthreads();                                     // the angles are read
-    for (int e = threadIdx.x; e < kTile * HD; e += kThreads) {
-      const int j = e / HD, d = e % HD;
-      s.v[j][d] = j < w.n ? Elem<T>::load((const T *)a.v_new + (t0 + j) * a.v_row + w.kvh * HD + d) : 0.f;
+    for (int e = threadIdx.x; e < kTile * CH; e += kThreads) {
+      const int j = e / CH, c = e % CH;
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      if (j < w.n) load_vec<T, 8>((const T *)a.v_new + (t0 + j) * a.v_row + w.kvh * HD + c * 8, x);
+      store_vec<float, 8>(&s.v[j][c * 8], x);
     }
   }
   uint64_t newvis[kRowsPerWarp];

@@ -143,41 +143,6 @@ __device__ __forceinline__ uint32_t code_off(int row, int k) {
                    : (uint32_t)(row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
 }
 
-// Elements e0 .. e0 + 7 of a rotated bf16 row (in shared memory) with angles
-// cs (identity pairs past the rotated part when interleaved).
-__device__ __forceinline__ void rotate8(const RopePlan &p, const float2 *cs, const __nv_bfloat16 *row, int e0,
-                                        float *x) {
-  load_vec<__nv_bfloat16, 8>(row + e0, x);
-  if (p.interleaved) {
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float2 z = cs[(e0 + i) >> 1];
-      const float x1 = x[i], x2 = x[i + 1];
-      x[i] = x1 * z.x - x2 * z.y;
-      x[i + 1] = x2 * z.x + x1 * z.y;
-    }
-  } else if (p.half % 8 == 0) {
-    if (e0 >= 2 * p.half) return;
-    const bool low = e0 < p.half;
-    float y[8];
-    load_vec<__nv_bfloat16, 8>(row + (low ? e0 + p.half : e0 - p.half), y);
-    const float2 *z = cs + (low ? e0 : e0 - p.half);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = x[i] * z[i].x + (low ? -y[i] : y[i]) * z[i].y;
-  } else {
-#pragma unroll 1
-    for (int i = 0; i < 8 && e0 + i < 2 * p.half; ++i) {
-      const int d = e0 + i;
-      const bool low = d < p.half;
-      const float u = __bfloat162float(row[d]), y = __bfloat162float(row[low ? d + p.half : d - p.half]);
-      const float2 z = cs[low ? d : d - p.half];
-      const float v = u * z.x + (low ? -y : y) * z.y;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = k == i ? v : x[k];   // no indexed registers
-    }
-  }
-}
-
 // Eight values in two e4m3 parts: hi, and lo = e4m3(x - hi).
 __device__ __forceinline__ void split8(const float *x, uint2 &hi, uint2 &lo) {
   uint32_t h[4], l[4];
@@ -351,7 +316,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
 #pragma unroll 1
     for (int e = pt; e < npos * (HD / 2); e += kPrep) {
       const int d = e % (HD / 2);
-      cs_s[e] = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
+      cs_s[e - d + angle_at(d)] = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
     }
     if (a.order == SIMSD_ORDER_PAIRED && pt < w.B) tau_s[pt] = __ldg(a.tau + w.c0 + pt);
     copy_async_wait_all();

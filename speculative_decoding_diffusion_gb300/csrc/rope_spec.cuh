@@ -12,6 +12,7 @@
 #pragma once
 
 #include "internal.h"
+#include "vec.cuh"
 
 namespace simsd {
 
@@ -78,6 +79,44 @@ __device__ __forceinline__ void load_angles8(const float2 *row, int d0, float2 *
 __device__ __forceinline__ float2 rope_plan_cs(const RopePlan &p, int d, int pos) {
   const float2 cs = rope_plan_angle(p, d, pos);
   return make_float2(cs.x * p.mul, cs.y * p.mul);
+}
+
+// Elements e0 .. e0 + 7 (e0 a multiple of 8) of a head's row, rotated by the
+// angles cs (placed by angle_at, identity pairs past the rotated part).
+template <typename T>
+__device__ __forceinline__ void rotate8(const RopePlan &p, const float2 *cs, const T *row, int e0, float *x) {
+  load_vec<T, 8>(row + e0, x);
+  if (p.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 z = *reinterpret_cast<const float4 *>(cs + angle_at((e0 + i) >> 1));
+      const float a0 = x[i], b0 = x[i + 1], a1 = x[i + 2], b1 = x[i + 3];
+      x[i] = a0 * z.x - b0 * z.y;
+      x[i + 1] = b0 * z.x + a0 * z.y;
+      x[i + 2] = a1 * z.z - b1 * z.w;
+      x[i + 3] = b1 * z.z + a1 * z.w;
+    }
+  } else if (p.half % 8 == 0) {
+    if (e0 >= 2 * p.half) return;
+    const bool low = e0 < p.half;
+    float y[8];
+    float2 z[8];
+    load_vec<T, 8>(row + (low ? e0 + p.half : e0 - p.half), y);
+    load_angles8(cs, low ? e0 : e0 - p.half, z);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = x[i] * z[i].x + (low ? -y[i] : y[i]) * z[i].y;
+  } else {                                   // partners off the chunk grid
+#pragma unroll 1
+    for (int i = 0; i < 8 && e0 + i < 2 * p.half; ++i) {
+      const int d = e0 + i;
+      const bool low = d < p.half;
+      const float u = Elem<T>::load(row + d), y = Elem<T>::load(row + (low ? d + p.half : d - p.half));
+      const float2 z = cs[angle_at(low ? d : d - p.half)];
+      const float v = u * z.x + (low ? -y : y) * z.y;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = k == i ? v : x[k];   // no indexed registers
+    }
+  }
 }
 
 }  // namespace simsd
