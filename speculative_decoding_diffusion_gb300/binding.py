@@ -427,12 +427,13 @@ def _addr(t):
 # (a torch.cuda.Stream object for the current stream takes longer to make than
 # a kernel to launch)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _run_on(stream, *tensors):
     """The stream to launch on, once every tensor (None passes) is seen to lie
     on the current CUDA device."""
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    dev = _device() if torch.cuda.is_initialized() else -2
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise ValueError("a tensor is on %s, not on the current CUDA device" % t.device)
@@ -476,11 +477,9 @@ def _same_dtype(like, **tensors):
 def _ints(dtype, **tensors):
     """Index arrays: contiguous tensors of the ABI's integer type (None passes)."""
     for name, t in tensors.items():
-        if t is None:
-            continue
-        if t.dtype is not dtype:
-            raise TypeError("%s is %s, not %s" % (name, t.dtype, dtype))
-        if not t.is_contiguous():
+        if t is not None and not (t.dtype is dtype and t.is_contiguous()):
+            if t.dtype is not dtype:
+                raise TypeError("%s is %s, not %s" % (name, t.dtype, dtype))
             raise ValueError("%s is not contiguous" % name)
 
 
