@@ -11,6 +11,7 @@
 // of a (sequence, KV head) against tiles of 64 keys that are decoded into
 // shared memory once for all rows; a warp owns four rows, its lanes two keys
 // each for the scores and four columns each for the values.
+#include <limits.h>
 #include <math.h>
 #include <string.h>
 
@@ -46,6 +47,7 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem<HD> &s = *reinterpret_cast<SimtSmem<HD> *>(smem_raw);
   __shared__ int tau_s[kMaxB];
+  grid_dep_wait();
   grid_dep_launch();
   const KvqWork w = kvq_work(a);
   if (!w.ok) return;
@@ -219,29 +221,53 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
   }
 }
 
+// The order in which a launch of several waves takes its sequences: longest
+// prompt first, so that its last CTAs are short.  Thread i counts the
+// sequences ahead of its own.
+constexpr int kOrderMax = 512;           // a larger batch has many waves, whose last weighs little
+
+__global__ void __launch_bounds__(kOrderMax) kvq_order_kernel(const __grid_constant__ KvqParams a) {
+  __shared__ __align__(16) int P[kOrderMax];
+  const int i = threadIdx.x;
+  grid_dep_launch();
+  const int mine = i < a.batch ? __ldg(a.lens + i) : INT_MIN;
+  const int c0 = i < a.batch ? __ldg(a.cu_B + i) : 0, c1 = i < a.batch ? __ldg(a.cu_B + i + 1) : 0;
+  P[i] = mine;
+  __syncthreads();
+  if (i >= a.batch) return;
+  int rank = 0;
+  for (int j = 0; j < a.batch; j += 4) {
+    const int4 x = *reinterpret_cast<const int4 *>(P + j);
+    rank += (x.x > mine || (x.x == mine && j < i)) + (x.y > mine || (x.y == mine && j + 1 < i)) +
+            (x.z > mine || (x.z == mine && j + 2 < i)) + (x.w > mine || (x.w == mine && j + 3 < i));
+  }
+  a.order_ws[rank] = make_int4(i, c0, c1 - c0, mine);
+}
+
 // Merge: out = sum_s 2^(m_s - m*) O_s / sum_s 2^(m_s - m*) l_s, a warp per
-// (token, head) row of a split unit.  The row's sequence is looked up before
-// the wait for the attention kernel (its arrays are inputs of the call).
+// (token, head) row of a split unit; blockIdx.x: a token of one of the last
+// merge_seqs sequences in the units' order.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeRows = kMergeThreads / 32;
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kMergeThreads)
-kvq_merge_kernel(const __grid_constant__ KvqParams a, int tok0) {
+kvq_merge_kernel(const __grid_constant__ KvqParams a) {
   constexpr int PER = HD / 32;
-  const int tok_row = tok0 + (int)blockIdx.x, lane = threadIdx.x & 31;
-  const int hq = blockIdx.y * kMergeRows + (threadIdx.x >> 5);
-  const int b = find_seq(a.cu_B, a.batch, tok_row / a.per);
-  const int c0 = __ldg(a.cu_B + b), B = __ldg(a.cu_B + b + 1) - c0, P = __ldg(a.lens + b);
+  const int max_n = a.per * a.B_max, lane = threadIdx.x & 31;
+  const int hq = blockIdx.y * kMergeRows + (threadIdx.x >> 5), tok = (int)blockIdx.x % max_n;
+  const int rank = a.batch - a.merge_seqs + (int)blockIdx.x / max_n;
   grid_dep_wait();
-  const int tok = tok_row - a.per * c0;
-  if (hq >= a.Hq || kvq_bad(a, c0, B, P) || tok < 0 || tok >= a.per * B) return;
+  const int4 seq = kvq_sequence(a, rank);
+  const int c0 = seq.y, B = seq.z, P = seq.w;
+  if (hq >= a.Hq || kvq_bad(a, c0, B, P) || tok >= a.per * B) return;
+  const int64_t tok_row = (int64_t)a.per * c0 + tok;
   const int g = hq / a.G;
   const int rtile = (tok * a.G + hq % a.G) / a.rows_per_tile;
-  const int unit = b * a.Hkv * a.row_tiles + rtile * a.Hkv + g;
+  const int unit = rank * a.Hkv * a.row_tiles + rtile * a.Hkv + g;
   const int ns = unit >= a.tail_from ? (P + a.chunk_tail - 1) / a.chunk_tail : 1;
   if (ns <= 1) return;
-  const int64_t row = (int64_t)tok_row * a.Hq + hq, step = (int64_t)a.T * a.Hq;
+  const int64_t row = tok_row * a.Hq + hq, step = (int64_t)a.T * a.Hq;
   float m = -INFINITY;
   for (int s = lane; s < ns; s += 32) m = fmaxf(m, __ldcg(a.ml_part + row + s * step).x);
 #pragma unroll
@@ -291,16 +317,14 @@ cudaError_t launch_simt_t(const KvqPlan &p, const KvqParams &a, cudaStream_t str
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  kern<<<p.grid, kThreads, smem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(kern, dim3((unsigned)p.grid), dim3(kThreads), smem, stream, a);
 }
 
 // Key splits: every unit alike where the table's width makes a unit long, or
 // only the units of the last partial wave (as simsd_verify_attn's plan).  In
 // block-times of 128 keys on an SM; a wave of n CTAs of `per` blocks costs
 // per * max(n / slots, kRho) plus a ramp, and splits the merge's reads.
-void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t slots, int max_n_tokens,
-                 KvqPlan *p) {
+void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t slots, KvqPlan *p) {
   constexpr double kRho = 0.85, kRamp = 6.0;
   const int64_t blocks = std::max<int64_t>(1, (max_keys + kBlockKeys - 1) / kBlockKeys);
   const int64_t pairs = batch * units_per_seq;
@@ -322,7 +346,7 @@ void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t
   p->tail_from = p->n_splits > 1 ? 0 : (int)pairs;
   p->tail_first = 0;
   p->grid = (int)(pairs * p->n_splits);
-  p->merge_tokens = p->T;
+  p->merge_seqs = (int)batch;
   if (p->n_splits == 1 && pairs > slots && pairs % slots != 0) {
     const int64_t W = pairs / slots, r = pairs - W * slots;
     const int64_t s = std::min<int64_t>(slots / r, blocks);
@@ -338,11 +362,11 @@ void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t
         p->chunk_tail = (int)(pt * kBlockKeys);
         p->n_splits = (int)((blocks + pt - 1) / pt);
         p->grid = (int)(W * slots + r * s);
-        const int64_t seqs = std::min<int64_t>(batch, (r + units_per_seq - 1) / units_per_seq + 1);
-        p->merge_tokens = std::min<int64_t>(p->T, seqs * max_n_tokens);
+        p->merge_seqs = (int)std::min<int64_t>(batch, (r + units_per_seq - 1) / units_per_seq + 1);
       }
     }
   }
+  p->ranked = p->grid > slots && batch > 1 && batch <= kOrderMax;
 }
 
 simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {
@@ -374,8 +398,11 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {
   const int64_t per_seq = (int64_t)d->num_kv_heads * p->row_tiles;
   if (per_seq * d->batch * 64 >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
   plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens,
-              (tc ? 1 : 2) * device_sm_count(), max_n, p);
+              (tc ? 1 : 2) * device_sm_count(), p);
+  if ((int64_t)p->merge_seqs * max_n >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
   size_t off = kAlign;
+  p->off_order = off;
+  if (p->ranked) off = align_up(off + (size_t)d->batch * sizeof(int4), kAlign);
   p->off_opart = p->off_ml = off;
   if (p->n_splits > 1) {
     const size_t rows = (size_t)p->n_splits * p->T * d->num_q_heads;
@@ -397,14 +424,13 @@ cudaError_t launch_kvq_simt(const simsd_kvq_verify_desc *d, const KvqPlan &p, co
 
 cudaError_t launch_kvq_merge(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                              cudaStream_t stream) {
-  const dim3 grid((unsigned)p.merge_tokens, (unsigned)((d->num_q_heads + kMergeRows - 1) / kMergeRows));
+  const dim3 grid((unsigned)(p.merge_seqs * p.per * d->B_max), (unsigned)((d->num_q_heads + kMergeRows - 1) / kMergeRows));
   const dim3 block(kMergeThreads);
-  const int tok0 = (int)(p.T - p.merge_tokens);
   if (d->dtype == SIMSD_BF16)
-    return d->head_dim == 128 ? launch_pdl(kvq_merge_kernel<__nv_bfloat16, 128>, grid, block, 0, stream, a, tok0)
-                              : launch_pdl(kvq_merge_kernel<__nv_bfloat16, 64>, grid, block, 0, stream, a, tok0);
-  return d->head_dim == 128 ? launch_pdl(kvq_merge_kernel<float, 128>, grid, block, 0, stream, a, tok0)
-                            : launch_pdl(kvq_merge_kernel<float, 64>, grid, block, 0, stream, a, tok0);
+    return d->head_dim == 128 ? launch_pdl(kvq_merge_kernel<__nv_bfloat16, 128>, grid, block, 0, stream, a)
+                              : launch_pdl(kvq_merge_kernel<__nv_bfloat16, 64>, grid, block, 0, stream, a);
+  return d->head_dim == 128 ? launch_pdl(kvq_merge_kernel<float, 128>, grid, block, 0, stream, a)
+                            : launch_pdl(kvq_merge_kernel<float, 64>, grid, block, 0, stream, a);
 }
 
 }  // namespace simsd
@@ -450,10 +476,17 @@ simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream_ptr) 
   a.max_pages = d->max_pages_per_seq; a.num_pages = d->num_pages;
   a.rows_per_tile = p.rows_per_tile; a.row_tiles = p.row_tiles;
   a.tail_from = p.tail_from; a.s_tail = p.s_tail; a.chunk_tail = p.chunk_tail; a.tail_first = p.tail_first;
+  a.order_ws = p.ranked ? (int4 *)(ws + p.off_order) : nullptr;
+  a.merge_seqs = p.merge_seqs;
   a.polls = wait_polls_of(d->wait_polls);
   a.scale = d->sm_scale * 1.4426950408889634f;
   cudaStream_t stream = (cudaStream_t)stream_ptr;
-  cudaError_t e = d->dtype == SIMSD_BF16 ? launch_kvq_tc(d, p, a, stream) : launch_kvq_simt(d, p, a, stream);
+  cudaError_t e = cudaSuccess;
+  if (p.ranked) {
+    kvq_order_kernel<<<1, kOrderMax, 0, stream>>>(a);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess) e = d->dtype == SIMSD_BF16 ? launch_kvq_tc(d, p, a, stream) : launch_kvq_simt(d, p, a, stream);
   if (e == cudaSuccess && p.n_splits > 1) e = launch_kvq_merge(d, p, a, stream);
   return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
 }

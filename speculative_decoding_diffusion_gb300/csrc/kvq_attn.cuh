@@ -16,8 +16,9 @@ constexpr int kMaxNew = 64;              // new tokens of a sequence
 struct KvqPlan {
   int T, per, G, rows_per_tile, row_tiles;
   int n_splits, tail_from, s_tail, chunk_tail, tail_first, grid;
-  int64_t merge_tokens;                  // the merge's tokens are the last ones
-  size_t esize, off_opart, off_ml, total;
+  bool ranked;                           // units by the sequences' lengths (kvq_order_kernel)
+  int merge_seqs;                        // sequences (the last in the units' order) with split units
+  size_t esize, off_order, off_opart, off_ml, total;
 };
 
 struct KvqParams {
@@ -27,12 +28,13 @@ struct KvqParams {
   const uint8_t *k_cache, *v_cache, *k_scale, *v_scale;
   const int32_t *block_table, *tau, *lens, *cu_B;
   float *o_part;                         // [n_splits][T][Hq][hd], unnormalised
+  int4 *order_ws;                         // [batch] (sequence, first section, sections, prompt), or null
   float2 *ml_part;                       // [n_splits][T][Hq] (log2 reference, sum)
   uint32_t *status;
   int64_t q_row, k_row, v_row;
   int batch, Hq, Hkv, G, T, total_B, B_max, order, node_size, per;
   int max_pages, num_pages;
-  int rows_per_tile, row_tiles, tail_from, s_tail, chunk_tail, tail_first;
+  int rows_per_tile, row_tiles, tail_from, s_tail, chunk_tail, tail_first, merge_seqs;
   uint32_t polls;
   float scale;                           // sm_scale * log2(e)
 };
@@ -52,6 +54,13 @@ __device__ __forceinline__ bool kvq_bad(const KvqParams &a, int c0, int B, int P
          (a.order == SIMSD_ORDER_NODES && B % a.node_size != 0);
 }
 
+// Sequence `rank` of the units' order; its first section, sections and prompt.
+__device__ __forceinline__ int4 kvq_sequence(const KvqParams &a, int rank) {
+  if (a.order_ws != nullptr) return __ldcg(a.order_ws + rank);
+  const int c0 = __ldg(a.cu_B + rank);
+  return make_int4(rank, c0, __ldg(a.cu_B + rank + 1) - c0, __ldg(a.lens + rank));
+}
+
 __device__ __forceinline__ KvqWork kvq_work(const KvqParams &a) {
   KvqWork w;
   const int ci = blockIdx.x;
@@ -62,12 +71,13 @@ __device__ __forceinline__ KvqWork kvq_work(const KvqParams &a) {
   const int chunk = tail ? a.chunk_tail : a.max_pages * kPage;
   const int per_seq = a.Hkv * a.row_tiles;
   w.split = tail ? ti % a.s_tail : 0;
-  w.b = unit / per_seq;
+  const int4 seq = kvq_sequence(a, unit / per_seq);
+  w.b = seq.x;
+  w.c0 = seq.y;
+  w.B = seq.z;
+  w.P = seq.w;
   w.kvh = unit % per_seq % a.Hkv;
   w.rtile = unit % per_seq / a.Hkv;
-  w.c0 = __ldg(a.cu_B + w.b);
-  w.B = __ldg(a.cu_B + w.b + 1) - w.c0;
-  w.P = __ldg(a.lens + w.b);
   w.ok = false;
   if (kvq_bad(a, w.c0, w.B, w.P)) {
     if (threadIdx.x == 0 && w.split == 0 && unit % per_seq == 0) raise_status(a.status, kStatusBadInput);

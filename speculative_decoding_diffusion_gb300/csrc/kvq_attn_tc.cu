@@ -206,6 +206,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   float *row_s = reinterpret_cast<float *>(sb + L::kOffRow);
   uint32_t *amax_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new keys, values
   Scales *scales_s = reinterpret_cast<Scales *>(sb + L::kOffScales);
+  grid_dep_wait();                           // the units' order is there
   grid_dep_launch();                         // the split merge may be scheduled
   const KvqWork w = kvq_work(a);
   if (!w.ok) return;                         // uniform: nothing to do here
@@ -883,8 +884,7 @@ cudaError_t launch_tc_hd(const CUtensorMap &mk, const KvqPlan &p, const KvqParam
     if (e != cudaSuccess) return e;
     configured.fetch_or(bit);
   }
-  kern<<<p.grid, kThreads, smem, stream>>>(mk, a);
-  return cudaGetLastError();
+  return launch_pdl(kern, dim3((unsigned)p.grid), dim3(kThreads), smem, stream, mk, a);
 }
 
 }  // namespace
