@@ -710,6 +710,8 @@ simsd_status simsd_kvq_append(const simsd_kvq_append_desc *d, void *stream);
  * 1..B_max, lens[b] outside 0..16 max_pages_per_seq, n_b not a multiple of
  * node_size) sets the bad-input bit and its rows of out are not written; a
  * page id outside the cache sets it too, and that page counts as absent.
+ * A row that sees a marked page, or a new token whose value holds a NaN or an
+ * infinity, is NaN; a token that a row does not see has no effect on it.
  * Limits: Hq % Hkv == 0, head_dim 64 or 128.  The workspace size follows the
  * key-split plan (the current device's SM count).
  * ---------------------------------------------------------------------- */

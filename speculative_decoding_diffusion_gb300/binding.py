@@ -433,9 +433,11 @@ _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_devic
 def _run_on(stream, *tensors):
     """The stream to launch on, once every tensor (None passes) is seen to lie
     on the current CUDA device."""
-    dev = _device() if torch.cuda.is_initialized() else -2
+    dev = tensors[0].get_device()
+    if dev >= 0 and dev != _device():
+        dev = -2
     for t in tensors:
-        if t is not None and t.get_device() != dev:
+        if t is not None and (t.get_device() != dev or dev < 0):
             raise ValueError("a tensor is on %s, not on the current CUDA device" % t.device)
     if stream is not None:
         return stream.cuda_stream

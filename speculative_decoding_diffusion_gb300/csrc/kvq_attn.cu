@@ -47,12 +47,14 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SimtSmem<HD> &s = *reinterpret_cast<SimtSmem<HD> *>(smem_raw);
   __shared__ int tau_s[kMaxB];
+  __shared__ uint32_t odd_s[kTile / 32];                 // new tokens whose values hold a NaN or an infinity
   grid_dep_wait();
   grid_dep_launch();
   const KvqWork w = kvq_work(a);
   if (!w.ok) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = min(kRows, w.M - w.row0);
+  if (threadIdx.x < kTile / 32) odd_s[threadIdx.x] = 0u;
   if (a.order == SIMSD_ORDER_PAIRED && threadIdx.x < w.B) tau_s[threadIdx.x] = __ldg(a.tau + w.c0 + threadIdx.x);
   const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
   float2 *cs = reinterpret_cast<float2 *>(&s.v[0][0]);   // [kMaxNew][HD / 2]
@@ -90,6 +92,13 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = 0.f;
       if (j < w.n) load_vec<T, 8>((const T *)a.v_new + (t0 + j) * a.v_row + w.kvh * HD + c * 8, x);
+      bool odd = false;                                  // (times a weight of 0 it would reach every row)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        odd |= !(fabsf(x[i]) < INFINITY);
+        x[i] = fabsf(x[i]) < INFINITY ? x[i] : 0.f;
+      }
+      if (odd) atomicOr(odd_s + (j >> 5), 1u << (j & 31));
       store_vec<float, 8>(&s.v[j][c * 8], x);
     }
   }
@@ -206,6 +215,7 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
     if (r0 + i >= rows) continue;
+    if (w.first && (newvis[i] & ((uint64_t)odd_s[1] << 32 | odd_s[0])) != 0ull) l[i] = __uint_as_float(0x7fc00000u);
     const int grow = w.row0 + r0 + i;
     const int64_t row = (t0 + grow / a.G) * a.Hq + w.kvh * a.G + grow % a.G;
     if (w.n_splits == 1) {
@@ -221,10 +231,13 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
   }
 }
 
-// The order in which a launch of several waves takes its sequences: longest
-// prompt first, so that its last CTAs are short.  Thread i counts the
-// sequences ahead of its own.
-constexpr int kOrderMax = 512;           // a larger batch has many waves, whose last weighs little
+// The order in which a launch of a few waves takes its sequences: longest
+// prompt first, so that its last CTAs are short (64 sequences of up to 4096
+// keys, 3.4 waves: 99 us in the batch's order, 87 in this one; equal sequences
+// lose the 2.5 us of this kernel, and 13 waves of ragged ones gain nothing: 592
+// and 595 us).  Thread i counts the sequences ahead of its own.
+constexpr int kOrderMax = 512;
+constexpr int kOrderWaves = 8;
 
 __global__ void __launch_bounds__(kOrderMax) kvq_order_kernel(const __grid_constant__ KvqParams a) {
   __shared__ __align__(16) int P[kOrderMax];
@@ -320,53 +333,68 @@ cudaError_t launch_simt_t(const KvqPlan &p, const KvqParams &a, cudaStream_t str
   return launch_pdl(kern, dim3((unsigned)p.grid), dim3(kThreads), smem, stream, a);
 }
 
-// Key splits: every unit alike where the table's width makes a unit long, or
-// only the units of the last partial wave (as simsd_verify_attn's plan).  In
-// block-times of 128 keys on an SM; a wave of n CTAs of `per` blocks costs
-// per * max(n / slots, kRho) plus a ramp, and splits the merge's reads.
-void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t slots, KvqPlan *p) {
-  constexpr double kRho = 0.85, kRamp = 6.0;
-  const int64_t blocks = std::max<int64_t>(1, (max_keys + kBlockKeys - 1) / kBlockKeys);
-  const int64_t pairs = batch * units_per_seq;
-  int64_t splits = 1;
-  double best = 1e300;
-  for (int64_t s = 1; s <= blocks && s <= 64; ++s) {
+// Key splits, in block-times of 128 keys on an SM: a CTA costs its blocks plus
+// a ramp (set-up, rows, epilogue: 12 to 18 thousand cycles beside 1.8 to 2.6 a
+// block), and splits the merge's launch and reads.  A partial wave costs as
+// much as a full one: an SM's copies in flight bound its rate, so idle SMs do
+// not speed up the others.
+constexpr int64_t kRamp = 6;
+constexpr int kMaxSplits = 64;
+
+struct Cut {
+  int64_t per, n;                        // blocks of a piece but the last of a unit; pieces
+  double time;
+};
+
+// The best cut of `units` units of `blocks` blocks each: equal pieces, or (if
+// `uneven`) as many long ones as fit the SMs at once while the units' short
+// ends take turns on the SMs that are left (8 sequences of 32768 keys, 8 heads:
+// 64 units in halves 179 us, in 112 + 112 + 33 blocks 164).
+Cut cut_units(int64_t units, int64_t blocks, int64_t slots, bool uneven) {
+  Cut best = {blocks, 1, (double)((units + slots - 1) / slots * (blocks + kRamp))};
+  auto merged = [&](int64_t n) { return 2.0 + 2.0 * (double)(units * n) / (double)slots; };
+  const int64_t most = std::min<int64_t>(std::min<int64_t>(kMaxSplits, blocks), 4 * slots / units + 1);
+  for (int64_t s = 2; s <= most; ++s) {
     const int64_t per = (blocks + s - 1) / s;
-    if (s > 1 && (blocks + per - 1) / per < s) continue;   // same split as a smaller s
-    const int64_t ctas = pairs * s, full = ctas / slots, rest = ctas % slots;
-    double cost = (double)full * ((double)per + kRamp);
-    if (rest > 0) cost += (double)per * std::max((double)rest / (double)slots, kRho) + kRamp;
-    if (s > 1) cost += 2.0 + 2.0 * (double)ctas / (double)slots;
-    if (cost < best - 1e-9) { best = cost; splits = s; }
+    if ((blocks + per - 1) / per < s) continue;            // same split as a smaller s
+    const double t = (double)((units * s + slots - 1) / slots * (per + kRamp)) + merged(s);
+    if (t < best.time) best = {per, s, t};
   }
-  const int64_t per = (blocks + splits - 1) / splits;
-  p->chunk_tail = (int)(per * kBlockKeys);
-  p->n_splits = (int)((blocks + per - 1) / per);
-  p->s_tail = p->n_splits;
-  p->tail_from = p->n_splits > 1 ? 0 : (int)pairs;
-  p->tail_first = 0;
-  p->grid = (int)(pairs * p->n_splits);
-  p->merge_seqs = (int)batch;
-  if (p->n_splits == 1 && pairs > slots && pairs % slots != 0) {
-    const int64_t W = pairs / slots, r = pairs - W * slots;
-    const int64_t s = std::min<int64_t>(slots / r, blocks);
-    if (s >= 2) {
-      const int64_t pt = (blocks + s - 1) / s;
-      const double whole = (double)(W + 1) * ((double)blocks + kRamp);
-      const double tail = (double)W * ((double)blocks + kRamp) + (double)pt + kRamp + 2.0 +
-                          2.0 * (double)(r * s) / (double)slots;
-      if (tail < whole - 1e-9) {
-        p->tail_from = (int)(W * slots);
-        p->tail_first = W <= 4;      // few full waves: the split units' SMs start offset
-        p->s_tail = (int)s;
-        p->chunk_tail = (int)(pt * kBlockKeys);
-        p->n_splits = (int)((blocks + pt - 1) / pt);
-        p->grid = (int)(W * slots + r * s);
-        p->merge_seqs = (int)std::min<int64_t>(batch, (r + units_per_seq - 1) / units_per_seq + 1);
-      }
+  const int64_t e = std::min<int64_t>(slots / units, kMaxSplits - 1), left = slots - e * units;
+  if (uneven && e > 0 && left > 0) {
+    const int64_t k = (units + left - 1) / left;           // ends an SM takes in turn
+    const int64_t per = (k * (blocks + kRamp) - kRamp + k * e) / (1 + k * e);
+    if (per > 0 && e * per < blocks && blocks - e * per <= per) {
+      const double t = (double)std::max(per + kRamp, k * (blocks - e * per + kRamp)) + merged(e + 1);
+      if (t < best.time) best = {per, e + 1, t};
     }
   }
-  p->ranked = p->grid > slots && batch > 1 && batch <= kOrderMax;
+  return best;
+}
+
+// Every unit alike, or whole waves of whole units and the rest cut in equal
+// pieces to fill the last wave, as simsd_verify_attn's plan (64 sequences of
+// 4096 keys, 56 units of 512 in the fourth wave: 162 us whole, 156 in halves, 158
+// in 15 + 15 + 3 blocks).
+void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t slots, KvqPlan *p) {
+  const int64_t blocks = std::max<int64_t>(1, (max_keys + kBlockKeys - 1) / kBlockKeys);
+  const int64_t pairs = batch * units_per_seq, W = pairs / slots, r = pairs - W * slots;
+  Cut cut = cut_units(pairs, blocks, slots, true);
+  int64_t whole = cut.n > 1 ? 0 : pairs;
+  if (W > 0 && r > 0) {
+    const Cut tail = cut_units(r, blocks, slots, false);
+    if (tail.n > 1 && (double)(W * (blocks + kRamp)) + tail.time < cut.time) {
+      cut = tail;
+      whole = W * slots;
+    }
+  }
+  p->n_splits = p->s_tail = (int)cut.n;
+  p->chunk_tail = (int)(cut.per * kBlockKeys);
+  p->tail_from = (int)whole;
+  p->tail_first = whole > 0 && whole < pairs && W <= 4;    // few full waves: the cut units' SMs start offset
+  p->grid = (int)(whole + (pairs - whole) * cut.n);
+  p->merge_seqs = (int)(whole == 0 ? batch : std::min<int64_t>(batch, (r + units_per_seq - 1) / units_per_seq + 1));
+  p->ranked = p->grid > slots && pairs < kOrderWaves * slots && batch > 1 && batch <= kOrderMax;
 }
 
 simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {

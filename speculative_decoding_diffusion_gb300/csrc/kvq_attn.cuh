@@ -67,10 +67,14 @@ __device__ __forceinline__ KvqWork kvq_work(const KvqParams &a) {
   const int n_tail = (int)gridDim.x - a.tail_from;   // CTAs of split units
   const bool tail = a.tail_first ? ci < n_tail : ci >= a.tail_from;
   const int ti = a.tail_first ? ci : ci - a.tail_from;
-  const int unit = tail ? a.tail_from + ti / a.s_tail : (a.tail_first ? ci - n_tail : ci);
+  // split units: the whole chunks of all of them, then their last ones
+  const int n_whole = a.s_tail > 1 ? n_tail / a.s_tail * (a.s_tail - 1) : n_tail;
+  const int s_whole = max(1, a.s_tail - 1);
+  const int unit = !tail ? (a.tail_first ? ci - n_tail : ci)
+                         : a.tail_from + (ti < n_whole ? ti / s_whole : ti - n_whole);
   const int chunk = tail ? a.chunk_tail : a.max_pages * kPage;
   const int per_seq = a.Hkv * a.row_tiles;
-  w.split = tail ? ti % a.s_tail : 0;
+  w.split = !tail ? 0 : ti < n_whole ? ti % s_whole : s_whole;
   const int4 seq = kvq_sequence(a, unit / per_seq);
   w.b = seq.x;
   w.c0 = seq.y;

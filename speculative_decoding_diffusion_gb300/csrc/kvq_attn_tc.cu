@@ -102,8 +102,8 @@ struct Smem {
   static constexpr int kOffMax = kOffRow + kRows * 4;       // [2 blocks][2 halves][4 quadrants][32]: row maxima, sums
   static constexpr int kOffScales = kOffMax + 2 * kHalves * kRows * 4;
   static constexpr int kOffMisc = kOffScales + kGroupSlots * (int)sizeof(Scales);   // tmem address, error flag, largest
-                                                            // new |k| and |v|
-  static constexpr int kBytes = kOffMisc + 16;
+                                                            // new |k| and |v|, odd new values
+  static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;              // 1024-byte alignment slack
   static constexpr uint32_t kColQ = kColO + HD;             // q hi and lo: hd / 4 columns each
   static constexpr uint32_t kTmemCols = 512;
@@ -205,6 +205,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   int *flag_s = reinterpret_cast<int *>(sb + L::kOffMisc + 4);
   float *row_s = reinterpret_cast<float *>(sb + L::kOffRow);
   uint32_t *amax_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new keys, values
+  uint32_t *odd_s = amax_s + 2;              // new tokens whose values hold a NaN or an infinity, one bit each
   Scales *scales_s = reinterpret_cast<Scales *>(sb + L::kOffScales);
   grid_dep_wait();                           // the units' order is there
   grid_dep_launch();                         // the split merge may be scheduled
@@ -288,7 +289,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     mbar_init(bar(kBarQReady), 4);
     mbar_init(bar(kBarKnReady), 4);
     *flag_s = 0;
-    amax_s[0] = amax_s[1] = 0u;
+    amax_s[0] = amax_s[1] = odd_s[0] = odd_s[1] = 0u;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -379,6 +380,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       for (int e = pt; e < n_pad * CH; e += kPrep) {
         const int j = e / CH, c = e % CH;
         float x[8], v[8];
+        bool odd = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = v[i] = 0.f;
         if (j < w.n) {
@@ -388,8 +390,10 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           x[i] = fabsf(x[i]) < INFINITY ? x[i] * kdown : __uint_as_float(0x7fc00000u);   // e4m3 has no infinity
-          v[i] *= vdown;
+          odd |= !(fabsf(v[i]) < INFINITY);
+          v[i] = fabsf(v[i]) < INFINITY ? v[i] * vdown : 0.f;   // (times a weight of 0 it would reach every row)
         }
+        if (odd) atomicOr(odd_s + (j >> 5), 1u << (j & 31));
         uint2 hi, lo;
         split8(x, hi, lo);
         uint8_t *dst = sb + L::kOffKn + code_off<HD>(j, c >> 1) + (c & 1) * 8;
@@ -627,7 +631,9 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     if (half == 0 && lane == 0) mbar_arrive(bar(kBarQReady));
     const uint64_t newvis = fresh ? kvq_visible(a, w.B, tau_s, tok) : 0ull;
     const uint32_t tO = trow + kColO;
-    float m_ref = -INFINITY, l = 0.f;
+    // a row that sees a new token with an odd value is NaN
+    const bool odd = (newvis & ((uint64_t)odd_s[1] << 32 | odd_s[0])) != 0ull;
+    float m_ref = -INFINITY, l = odd ? __uint_as_float(0x7fc00000u) : 0.f;
     bool ok = true;
     int j = 0;
     const float new_scale = fresh ? rscale * pow2i(new_kexp()) : 0.f;

@@ -299,6 +299,18 @@ def test_verify_key_splits(dtype, lens):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens", [[300 - 7 * (i % 41) for i in range(60)], [200] * 60, [0] * 30 + [520] * 4 + [1] * 26,
+                                  [5 * i % 97 for i in range(600)], [1025, 1100] * 4])
+def test_verify_waves_and_cuts(dtype, lens):
+    """More units than SMs: sequences in another order than the batch's, the last wave cut; a batch too large to be
+    ordered; fewer units than SMs, cut in unequal pieces."""
+    s = case(sum(lens), lens, [1] * len(lens), "causal", dtype, 8, 8, 64)
+    out, ws = launch(s)
+    assert pkg.read_status(ws) == 0
+    check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_verify_strided_rows(dtype):
     """q, k and v inside fused rows."""
     s = case(21, [33, 150], [4, 3], "causal", dtype, 4, 2, 128)
@@ -339,6 +351,30 @@ def test_verify_marked_pages_read_as_nan(dtype):
     # a section's rows of sequence 0 (head 0) and sequence 1 (head 1), nothing else
     assert torch.equal(bad, torch.tensor([[True, False], [True, False], [False, True], [False, True]]))
     assert torch.equal(torch.isnan(out.float().cpu()).any(-1), bad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("order,B,Hq", [("paired", 4, 4), ("causal", 64, 2), ("nodes", 40, 6)])
+def test_verify_odd_new_tokens_reach_the_rows_that_see_them(dtype, order, B, Hq):
+    """NaN and infinite keys and values of a token: NaN in the rows that see it, no change in the others."""
+    node = 8 if order == "nodes" else 0
+    s = case(29, [50, 0], [B, B], order, dtype, Hq, 2, 128, node)
+    clean, _ = launch(s)
+    n = 2 * B if order == "paired" else B
+    at = {0: 1, 1: n - 2}                                 # a token of each sequence, one head of it
+    s["vn"][at[0], 0, 7], s["vn"][n + at[1], 1, 127] = math.nan, -math.inf
+    s["kn"][at[1], 1, 5] = math.nan
+    out, ws = launch(s)
+    assert pkg.read_status(ws) == 0
+    out, clean = out.cpu(), clean.cpu()
+    for b, token, head in ((0, at[0], 0), (0, at[1], 1), (1, at[1], 1)):
+        tau = s["tau"][b * B:(b + 1) * B] if order == "paired" else None
+        sees = ref.visible(order, B, tau, node)[:, token]
+        rows = out[b * n:(b + 1) * n, head * Hq // 2:(head + 1) * Hq // 2]
+        same = clean[b * n:(b + 1) * n, head * Hq // 2:(head + 1) * Hq // 2]
+        assert 0 < int(sees.sum()) < n
+        assert torch.isnan(rows[sees]).all() and torch.equal(rows[~sees], same[~sees])
+    assert torch.equal(out[n:, :Hq // 2], clean[n:, :Hq // 2])
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
