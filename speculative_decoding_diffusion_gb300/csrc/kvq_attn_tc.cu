@@ -71,8 +71,8 @@ enum { kBarKFull = 0, kBarVFull = kBarKFull + kStages, kBarKEmpty = kBarVFull + 
        kBarVEmpty = kBarKEmpty + kStages, kBarSFull = kBarVEmpty + kStages,
        kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 1,
        kBarVbFull = kBarPvDone + 2,
-       kBarQReady = kBarVbFull + 2, kBarKnReady = kBarQReady + 1,
-       kBarGFull = kBarKnReady + 1, kBarGEmpty = kBarGFull + kGroupSlots, kNumBars = kBarGEmpty + kGroupSlots };
+       kBarQReady = kBarVbFull + 2, kBarKnReady = kBarQReady + 1, kBarNewRead = kBarKnReady + 1,
+       kBarGFull = kBarNewRead + 1, kBarGEmpty = kBarGFull + kGroupSlots, kNumBars = kBarGEmpty + kGroupSlots };
 
 // What the scales of four blocks mean; entry 8 q + i: page i of block q.
 struct Scales {
@@ -191,6 +191,14 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return *reinterpret_cast<float2 *>(&d);
 }
 
+// a / d for 0 <= a < 2^24, d > 0, r = 1.f / d: the product is off by less than one.
+__device__ __forceinline__ int div_by(int a, int d, float r) {
+  int q = (int)((float)a * r);
+  const int rest = a - q * d;
+  q += rest >= d ? 1 : 0;
+  return rest < 0 ? q - 1 : q;
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
 kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ KvqParams a) {
@@ -245,6 +253,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   // index among the threads that rotate and split rows
   const int pt = threadIdx.x - (warp < kScaleWarp ? 64 : 96);
   constexpr int CH = HD / 8;                 // 16-byte chunks of a bf16 row
+  const float rG = 1.f / (float)a.G;
   const bool prep_warp = warp >= 2 && warp != kScaleWarp && warp != kPvWarp;
   if (warp == 0) {
     if (lane == 0) prefetch_tmap(&tmK);
@@ -255,7 +264,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     // ahead of the stream of codes
     const __nv_bfloat16 *qs = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
     for (int e = pt; e < n_groups * 32 * CH; e += kPrep) {
-      const int r = e / CH, c = e % CH, row = w.row0 + r, tok = row / a.G;
+      const int r = e / CH, c = e % CH, row = w.row0 + r, tok = div_by(row, a.G, rG);
       const bool take = row < w.M;
       copy16_async(base + L::kOffVb + r * HD * 2 + c * 16,
                    take ? qs + tok * a.q_row + (row - tok * a.G) * HD + c * 8 : (const void *)a.q, take);
@@ -268,28 +277,17 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         copy16_async(dst + kMaxNew * HD * 2, (const __nv_bfloat16 *)a.v_new + (t0 + j) * a.v_row + w.kvh * HD + c * 8, true);
       }
   }
-  if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(bar(kBarKFull + i), 1);
-      mbar_init(bar(kBarVFull + i), 1);
-      mbar_init(bar(kBarKEmpty + i), 1);
-      mbar_init(bar(kBarVEmpty + i), 4);
+  if (warp == kPvWarp) {
+    for (int i = lane; i < kNumBars; i += 32) {
+      const bool rows = i == kBarPFull || (i >= kBarSEmpty && i < kBarSEmpty + 2);
+      const bool tiles = (i >= kBarVEmpty && i < kBarVEmpty + kStages) || (i >= kBarVbFull && i < kBarVbFull + 2) ||
+                         i == kBarQReady || i == kBarKnReady || i == kBarNewRead;
+      mbar_init(bar(i), i >= kBarGEmpty ? n_valid + 4 : rows ? n_valid : tiles ? 4 : 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kBarSFull + i), 1);
-      mbar_init(bar(kBarSEmpty + i), n_valid);
-      mbar_init(bar(kBarPvDone + i), 1);
-      mbar_init(bar(kBarVbFull + i), 4);
+    if (lane == 0) {
+      *flag_s = 0;
+      amax_s[0] = amax_s[1] = odd_s[0] = odd_s[1] = 0u;
     }
-    mbar_init(bar(kBarPFull), n_valid);
-    for (int i = 0; i < kGroupSlots; ++i) {
-      mbar_init(bar(kBarGFull + i), 1);
-      mbar_init(bar(kBarGEmpty + i), n_valid + 4);
-    }
-    mbar_init(bar(kBarQReady), 4);
-    mbar_init(bar(kBarKnReady), 4);
-    *flag_s = 0;
-    amax_s[0] = amax_s[1] = odd_s[0] = odd_s[1] = 0u;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -308,9 +306,9 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   auto new_vexp = [&]() { return scale_exponent(__uint_as_float(amax_s[1]), -64, 119); };
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
   // The softmax and decode warps together rotate the query rows into two e4m3
-  // parts and, in the CTA that owns the new tokens, their keys likewise and
-  // their values into the first value tile; rolled loops, since each CTA runs
-  // them once (unrolled per row they took as long as ten blocks, most of it
+  // parts and, in the CTA that owns the new tokens, their keys likewise (the
+  // decode warps then take their values); rolled loops, since each CTA runs them
+  // once (unrolled per row they took as long as ten blocks, most of it
   // instruction fetch).
   auto prepare = [&]() {
     // angles of the new tokens' positions (identity past the rotated part)
@@ -322,20 +320,22 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     }
     if (a.order == SIMSD_ORDER_PAIRED && pt < w.B) tau_s[pt] = __ldg(a.tau + w.c0 + pt);
     copy_async_wait_all();
-    named_sync(1, kPrep);
     const __nv_bfloat16 *ks = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew), *vs = ks + kMaxNew * HD;
-    if (fresh) {                             // the largest finite magnitudes
+    if (fresh) {                             // the largest finite magnitudes (of what this thread copied)
       float ka = 0.f, va = 0.f;
 #pragma unroll 1
       for (int e = pt; e < w.n * CH; e += kPrep) {
         float x[8], y[8];
         load_vec<__nv_bfloat16, 8>(ks + e * 8, x);
         load_vec<__nv_bfloat16, 8>(vs + e * 8, y);
+        bool odd = false;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
+          odd |= !(fabsf(y[i]) < INFINITY);
           ka = fmaxf(ka, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
           va = fmaxf(va, fabsf(y[i]) < INFINITY ? fabsf(y[i]) : 0.f);
         }
+        if (odd) atomicOr(odd_s + (e / CH >> 5), 1u << (e / CH & 31));
       }
       const uint32_t kb = __reduce_max_sync(0xffffffffu, __float_as_uint(ka));
       const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(va));
@@ -344,63 +344,59 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         atomicMax(amax_s + 1, vb);
       }
     }
-    // query rows: CH neighbouring lanes hold a row (every warp's lanes take
-    // part in a pass or none do: 32 rows are a multiple of 32 chunks)
+    named_sync(1, kPrep);
+    // rows, query rows first: PL neighbouring lanes hold one (a warp's lanes
+    // all have query rows or all new keys: both are multiples of 32 lanes)
+    constexpr int PL = HD / 16;
     const __nv_bfloat16 *qs = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffVb);
+    const int n_q = n_groups * 32 * PL, n_all = n_q + (fresh ? n_pad * PL : 0);   // zeros up to the MMA's depth
+    const float kdown = fresh ? pow2i(-new_kexp()) : 0.f;
 #pragma unroll 1
-    for (int e = pt; e < n_groups * 32 * CH; e += kPrep) {
-      const int r = e / CH, c = e % CH, row = w.row0 + r, tok = row < w.M ? row / a.G : 0;
-      float x[8];
-      rotate8(a.plan, cs_s + kvq_offset(a, w.B, tok) * (HD / 2), qs + r * HD, c * 8, x);
-      float amax = 0.f;
-      bool odd = false;                      // a NaN or an infinity: the row's scores become NaN
+    for (int e = pt; e < n_all; e += kPrep) {
+      const bool query = e < n_q;
+      const int r = (query ? e : e - n_q) / PL, first = r - (lane / PL);   // row; the warp's first row
+      const int c = e % PL;
+      uint8_t *dst = sb + (query ? L::kOffQ : L::kOffKn);
+      uint8_t *dst_lo = dst + (query ? kRows * HD : L::kKn);
+      if (query ? w.row0 + first >= w.M : first >= w.n) {                  // none of them exist
+        *reinterpret_cast<uint4 *>(dst + code_off<HD>(r, c)) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(dst_lo + code_off<HD>(r, c)) = make_uint4(0, 0, 0, 0);
+        if (query && c == 0) row_s[r] = 0.f;
+        continue;
+      }
+      const int row = w.row0 + r;
+      const int tok = !query ? min(r, w.n - 1) : row < w.M ? div_by(row, a.G, rG) : 0;
+      int c0, c1;
+      float x[16], down = kdown;
+      rotate16(a.plan, cs_s + kvq_offset(a, w.B, tok) * (HD / 2), query ? qs + r * HD : ks + tok * HD, c, c0, c1, x);
+      if (query) {
+        float amax = 0.f, nan = 0.f;         // a NaN or an infinity: the row's scores become NaN
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        odd |= !(fabsf(x[i]) < INFINITY);
-        amax = fmaxf(amax, fabsf(x[i]));
+        for (int i = 0; i < 16; ++i) {
+          nan = fmaf(x[i], 0.f, nan);
+          amax = fmaxf(amax, fabsf(x[i]));
+        }
+#pragma unroll
+        for (int m = PL / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+        const uint32_t odds = (__ballot_sync(0xffffffffu, nan != 0.f) >> (lane & ~(PL - 1))) & ((1u << PL) - 1u);
+        const int qe = scale_exponent(amax, -100, 119);
+        down = pow2i(-qe);
+        if (c == 0) row_s[r] = odds != 0u ? __uint_as_float(0x7fc00000u) : a.scale * pow2i(qe);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)         // e4m3 has no infinity
+          x[i] = r >= w.n ? 0.f : fabsf(x[i]) < INFINITY ? x[i] : __uint_as_float(0x7fc00000u);
       }
 #pragma unroll
-      for (int m = CH / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-      const uint32_t odds = (__ballot_sync(0xffffffffu, odd) >> (lane & ~(CH - 1))) & ((1u << CH) - 1u);
-      const int qe = scale_exponent(amax, -100, 119);
-      const float down = pow2i(-qe);
+      for (int i = 0; i < 16; ++i) x[i] *= down;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] *= down;
-      uint2 hi, lo;
-      split8(x, hi, lo);
-      uint8_t *dst = sb + L::kOffQ + code_off<HD>(r, c >> 1) + (c & 1) * 8;
-      *reinterpret_cast<uint2 *>(dst) = hi;
-      *reinterpret_cast<uint2 *>(dst + kRows * HD) = lo;
-      if (c == 0) row_s[r] = odds != 0u ? __uint_as_float(0x7fc00000u) : a.scale * pow2i(qe);
-    }
-    if (fresh) {                             // zeros up to the MMA's depth
-      named_sync(1, kPrep);                  // the query rows are read; the magnitudes are there
-      const float kdown = pow2i(-new_kexp()), vdown = pow2i(-new_vexp());
-#pragma unroll 1
-      for (int e = pt; e < n_pad * CH; e += kPrep) {
-        const int j = e / CH, c = e % CH;
-        float x[8], v[8];
-        bool odd = false;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = v[i] = 0.f;
-        if (j < w.n) {
-          load_vec<__nv_bfloat16, 8>(vs + e * 8, v);
-          rotate8(a.plan, cs_s + kvq_offset(a, w.B, j) * (HD / 2), ks + j * HD, c * 8, x);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] = fabsf(x[i]) < INFINITY ? x[i] * kdown : __uint_as_float(0x7fc00000u);   // e4m3 has no infinity
-          odd |= !(fabsf(v[i]) < INFINITY);
-          v[i] = fabsf(v[i]) < INFINITY ? v[i] * vdown : 0.f;   // (times a weight of 0 it would reach every row)
-        }
-        if (odd) atomicOr(odd_s + (j >> 5), 1u << (j & 31));
+      for (int i = 0; i < 2; ++i) {
         uint2 hi, lo;
-        split8(x, hi, lo);
-        uint8_t *dst = sb + L::kOffKn + code_off<HD>(j, c >> 1) + (c & 1) * 8;
-        *reinterpret_cast<uint2 *>(dst) = hi;
-        *reinterpret_cast<uint2 *>(dst + L::kKn) = lo;
-        *reinterpret_cast<uint4 *>(sb + L::kOffVb + (c >> 3) * L::kHalf + swz(j, c & 7)) =
-            make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+        split8(x + 8 * i, hi, lo);
+        const int k = i ? c1 : c0;
+        const uint32_t off = code_off<HD>(r, k >> 1) + (k & 1) * 8;
+        *reinterpret_cast<uint2 *>(dst + off) = hi;
+        *reinterpret_cast<uint2 *>(dst_lo + off) = lo;
       }
     }
     fence_proxy_async_smem();
@@ -422,7 +418,8 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         // and in TMEM)
         if ((j >= kStages && (!mbar_wait_warp(bar(kBarKEmpty + s), ((j / kStages) - 1) & 1, a.polls) ||
                               !mbar_wait_warp(bar(kBarVEmpty + s), ((j / kStages) - 1) & 1, a.polls))) ||
-            ((j == kStages - 2 || j == kStages - 1) && !mbar_wait_warp(bar(kBarQReady), 0, a.polls))) {
+            ((j == kStages - 2 || j == kStages - 1) && !mbar_wait_warp(bar(kBarQReady), 0, a.polls)) ||
+            (j == kStages - 2 && fresh && !mbar_wait_warp(bar(kBarNewRead), 0, a.polls))) {
           if (lane == 0) give_up();
           ok = false;
           break;
@@ -544,9 +541,27 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     // ------------------------------------------------------------- decode
     const int dw = warp - kDecodeWarp;
     prepare();
-    if (fresh && lane == 0) {
-      mbar_arrive(bar(kBarKnReady));
-      mbar_arrive(bar(kBarVbFull));
+    if (fresh) {                             // the new values, as f16, are the first value tile
+      if (lane == 0) mbar_arrive(bar(kBarKnReady));
+      const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew) + kMaxNew * HD;
+      const float vdown = pow2i(-new_vexp());
+#pragma unroll 1
+      for (int e = 32 * dw + lane; e < n_pad * CH; e += 128) {
+        const int j = e / CH, c = e % CH;
+        float v[8];
+        load_vec<__nv_bfloat16, 8>(vs + e * 8, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)          // (an odd one times a weight of 0 would reach every row)
+          v[i] = j < w.n && fabsf(v[i]) < INFINITY ? v[i] * vdown : 0.f;
+        *reinterpret_cast<uint4 *>(sb + L::kOffVb + (c >> 3) * L::kHalf + swz(j, c & 7)) =
+            make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(kBarNewRead));
+        mbar_arrive(bar(kBarVbFull));
+      }
     }
     // value tiles: this warp's rows are pages 2 dw and 2 dw + 1 of a block
     constexpr int C = HD / 8, RPI = 32 / C;                  // 8-byte chunks of a row; rows an iteration

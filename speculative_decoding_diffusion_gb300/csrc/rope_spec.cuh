@@ -119,4 +119,32 @@ __device__ __forceinline__ void rotate8(const RopePlan &p, const float2 *cs, con
   }
 }
 
+// Sixteen elements of a row, rotated: its chunks (of eight) c0, in x[0..7], and
+// c1, in x[8..15], which i = 0.. (a sixteenth of the row) selects.  Where
+// partners lie on the chunk grid the two are each other's, so a pair and its
+// angle are read once.
+template <typename T>
+__device__ __forceinline__ void rotate16(const RopePlan &p, const float2 *cs, const T *row, int i, int &c0, int &c1,
+                                         float *x) {
+  if (!p.interleaved && p.half % 8 == 0 && i < p.half / 8) {
+    c0 = i;
+    c1 = i + p.half / 8;
+    float2 z[8];
+    load_vec<T, 8>(row + c0 * 8, x);
+    load_vec<T, 8>(row + c1 * 8, x + 8);
+    load_angles8(cs, c0 * 8, z);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float u = x[e], v = x[e + 8];
+      x[e] = u * z[e].x - v * z[e].y;
+      x[e + 8] = v * z[e].x + u * z[e].y;
+    }
+  } else {
+    c0 = 2 * i;
+    c1 = 2 * i + 1;
+    rotate8(p, cs, row, c0 * 8, x);
+    rotate8(p, cs, row, c1 * 8, x + 8);
+  }
+}
+
 }  // namespace simsd
