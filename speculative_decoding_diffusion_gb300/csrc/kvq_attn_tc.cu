@@ -215,11 +215,19 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   uint32_t *amax_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new keys, values
   uint32_t *odd_s = amax_s + 2;              // new tokens whose values hold a NaN or an infinity, one bit each
   Scales *scales_s = reinterpret_cast<Scales *>(sb + L::kOffScales);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 1) {
+    tc::alloc(smem_u32(tmem_slot), L::kTmemCols);
+    tc::relinquish();
+  }
   grid_dep_wait();                           // the units' order is there
   grid_dep_launch();                         // the split merge may be scheduled
   const KvqWork w = kvq_work(a);
-  if (!w.ok) return;                         // uniform: nothing to do here
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (!w.ok) {                               // uniform: nothing to do here
+    __syncthreads();
+    if (warp == 1) tc::dealloc(*tmem_slot, L::kTmemCols);
+    return;
+  }
   const int fresh = w.first ? 1 : 0;         // block 0 is the new tokens'
   const int n_past = max(0, w.k_end - w.k_begin + kKeys - 1) / kKeys;   // prompt blocks
   const int n_blocks = fresh + n_past;
@@ -289,10 +297,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       amax_s[0] = amax_s[1] = odd_s[0] = odd_s[1] = 0u;
     }
     fence_barrier_init();
-  }
-  if (warp == 1) {
-    tc::alloc(smem_u32(tmem_slot), L::kTmemCols);
-    tc::relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
