@@ -586,8 +586,9 @@ simsd_status simsd_rope(const simsd_rope_desc *d, void *stream);
  *   block_table device int32[batch][max_pages_per_seq] in/out
  *   served     device int32[batch] out
  *   slots      device int64[total_n] out, or NULL
- * A sequence whose numbers are out of range (lens < 0, need_b or held
- * outside 0..max_pages_per_seq, a cu_n range outside 0..total_n) sets the
+ * A sequence whose numbers are out of range (lens < 0, lens + n_b >= 2^31,
+ * need_b or held outside 0..max_pages_per_seq, a cu_n range outside
+ * 0..total_n) sets the
  * bad-input bit, is not served and is left unchanged (its slots, where its
  * cu_n range is valid, are -1); a ring out of range (head, count, or more
  * free and given back pages than num_pages) sets it and serves none.  A free

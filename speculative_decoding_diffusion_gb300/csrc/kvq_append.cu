@@ -208,6 +208,9 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
   }
   __syncthreads();
   auto cu = [&](int b) { return staged ? cu_s[b] : __ldg(a.cu_n + b); };
+  // (a sequence whose range is turned round may own no work item)
+  for (int i = blockIdx.x * n_threads + threadIdx.x; i < a.batch; i += gridDim.x * n_threads)
+    if (cu(i) < 0 || cu(i + 1) < cu(i) || cu(i + 1) > a.total_n) raise_status(a.status, kStatusBadInput);
   extern __shared__ __align__(16) uint8_t pages_s[];         // [warp][K, V][16][HD]
   T *mine = reinterpret_cast<T *>(pages_s) + (int64_t)warp * 2 * kPage * HD;
   constexpr int L = HD / 16;

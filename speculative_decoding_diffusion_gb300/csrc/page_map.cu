@@ -15,6 +15,8 @@
 // a CTA counts itself done, and the last one writes the new state.  Taken
 // ring entries and given-back places never overlap, since pages held and
 // free are at most the ring's entries.
+#include <limits.h>
+
 #include <algorithm>
 #include <atomic>
 
@@ -50,8 +52,8 @@ __device__ __forceinline__ Seq make_seq(const MapArgs &a, int len, int held, int
   s.c0 = c0;
   s.rows_ok = c0 >= 0 && c1 >= c0 && c1 <= a.total_n;
   s.n = s.rows_ok ? c1 - c0 : 0;
-  const int64_t pages = ((int64_t)len + s.n + kPage - 1) / kPage;
-  s.ok = s.rows_ok && len >= 0 && pages <= a.width && held >= 0 && held <= a.width;
+  const int64_t end = (int64_t)len + s.n, pages = (end + kPage - 1) / kPage;
+  s.ok = s.rows_ok && len >= 0 && end <= INT_MAX && pages <= a.width && held >= 0 && held <= a.width;
   s.need = s.ok ? (int)pages : held;
   return s;
 }

@@ -207,6 +207,25 @@ def test_append_many_sequences_and_bad_arrays():
     assert torch.equal(got[3], wb) and torch.equal(ref.e4m3_values(got[1]), wv)
 
 
+@pytest.mark.parametrize("many", [0, 1200])
+def test_append_reports_a_range_turned_round(many):
+    """cu_n that falls: the sequence between is left out and reported, the others are written."""
+    g = torch.Generator().manual_seed(8)
+    n = [64, 0, 8] + [0] * many
+    table, total = tables(g, [4, 1, 1] + [1] * many)
+    c = Cache(g, total, 1, 64)
+    v = torch.randn(72, 1, 64, generator=g)
+    dev, good = c.cuda(), c.cuda()
+    cu = torch.tensor([0, 64, 32, 40] + [40] * many, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    args = (i32(table), ws, pkg.rope_spec(base=1e4))
+    pkg.kvq_append(v.cuda(), v.cuda(), i32([0] * len(n)), cu, *dev, *args)
+    assert pkg.read_status(ws) == 2
+    order = torch.cat([v[:64], v[32:40]])
+    assert pkg.read_status(put(order.cuda(), order.cuda(), [0] * len(n), n, table, good, dict(base=1e4))) == 0
+    assert all(torch.equal(a, b) for a, b in zip(dev, good))
+
+
 # ------------------------------------------------------------------- verify
 def case(seed, lens, Bs, order, dtype, Hq, Hkv, hd, node=0, spec=None, sd=1.0, scale=None, lo=118, hi=122):
     g = torch.Generator().manual_seed(seed)

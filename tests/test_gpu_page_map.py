@@ -166,3 +166,20 @@ def test_largest_batch_and_graph_replay():
         graph.replay()
         assert [t.tolist() for t in (held, queue, ring, table, served, slots)] == list(want)
         st.held, st.queue, st.ring, st.table = want[:4]
+
+
+@pytest.mark.parametrize("n", [9, 10])
+def test_positions_at_the_end_of_32_bits(n):
+    """A row of 2^27 + 1 pages: positions up to 2^31 - 1 have a slot, a sequence that would pass it is refused."""
+    width = 2 ** 27 + 1
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    table[0, 2 ** 27 - 1] = 5
+    ring = torch.zeros(width, dtype=torch.int32, device="cuda")
+    held, queue, served = i32([2 ** 27]), i32([0, 0]), i32([7])
+    slots = torch.full((n,), -7, dtype=torch.int64, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    pkg.page_map(i32([2 ** 31 - 10]), i32([0, n]), held, queue, ring, table, held, queue, served, slots, ws, n)
+    ok = n == 9
+    assert pkg.read_status(ws) == (0 if ok else 2)
+    assert served.item() == int(ok) and held.item() == 2 ** 27 and queue.tolist() == [0, 0]
+    assert slots.tolist() == ([5 * PAGE + 6 + i for i in range(9)] if ok else [-1] * 10)
