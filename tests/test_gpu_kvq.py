@@ -462,6 +462,66 @@ def test_verify_two_graphs_and_streams():
         assert torch.equal(out, want)
 
 
+def test_append_and_verify_captured_in_several_waves():
+    """Sequences taken by length, the last wave cut, in a graph behind the append that their last pages come from."""
+    s = case(33, [397 - 8 * i for i in range(40)], [1] * 40, "causal", "bf16", 8, 8, 64)
+    q, *cache, kn, vn = (t.cuda() for t in (s["q"], *s["c"].cuda(), s["kn"], s["vn"]))
+    before = [t.clone() for t in cache]
+    table, lens, cu, start = i32(s["table"]), i32(s["lens"]), i32(s["cu"]), i32([16 * (L // 16) for L in s["lens"]])
+    spec, out = pkg.rope_spec(**s["spec"]), torch.empty_like(q)
+    args = (q, *cache, table, kn, vn, None, lens, cu, out)
+    n = pkg.kvq_verify_workspace_size(*args, 40, 1, spec, s["scale"], order=ORDER["causal"])
+    ws, wsv = (torch.zeros(m, dtype=torch.uint8, device="cuda") for m in (256, n))
+
+    def step():
+        pkg.kvq_append(kn, vn, start, cu, *cache, table, ws, spec)
+        pkg.kvq_verify(*args, wsv, 40, 1, spec, s["scale"], order=ORDER["causal"])
+
+    step()
+    want, after = out.clone(), [t.clone() for t in cache]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    for _ in range(2):
+        out.fill_(7)
+        for t, old in zip(cache, before):
+            t.copy_(old)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and all(torch.equal(t, a) for t, a in zip(cache, after))
+    assert pkg.read_status(ws) == 0 and pkg.read_status(wsv) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cache_of_more_than_32_bits(dtype):
+    """Pages and rows whose offsets pass 2^32 elements: the same codes and results as at the front."""
+    Hkv, hd, far = 8, 128, 2 ** 32 // (8 * 16 * 128) + 3
+    s = case(34, [70], [4], "paired", dtype, 8, Hkv, hd)
+    spec, n = pkg.rope_spec(**s["spec"]), 70
+    g = torch.Generator().manual_seed(35)
+    k, v = (torch.randn(n, Hkv, hd, generator=g).to(DT[dtype]).cuda() for _ in range(2))
+    shape = (far + 5, Hkv, PAGE, hd)
+    kc, vc = (torch.zeros(shape, dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(shape[:2], dtype=torch.uint8, device="cuda") for _ in range(2))
+    q, kn, vn = s["q"].cuda(), s["kn"].cuda(), s["vn"].cuda()
+    outs, stride = [], 2 ** 25 + 8 * hd                   # 70 rows of it pass 2^31 elements
+    wide = torch.zeros(n, stride, dtype=DT[dtype], device="cuda")
+    wide[:, :Hkv * hd] = k.flatten(1)
+    for at, rows in ((0, k), (far, wide[:, :Hkv * hd].unflatten(1, (Hkv, hd)))):
+        table = torch.arange(at, at + 5)[None]
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        pkg.kvq_append(rows, v, i32([0]), i32([0, n]), kc, vc, ks, vs, i32(table), ws, spec)
+        s["table"] = table
+        outs.append(launch(s, [q, kc, vc, ks, vs, kn, vn]))
+        assert pkg.read_status(ws) == 0 and pkg.read_status(outs[-1][1]) == 0
+    assert torch.equal(outs[0][0], outs[1][0]) and int(ks[far].max()) > 0
+    for t in (kc, vc, ks, vs):
+        assert torch.equal(t[:5], t[far:])
+
+
 def test_step_of_the_loop():
     """Requests admitted, their prompts appended, a verification pass, the kept tokens appended behind it, and the next
     pass: every stage fed by the one before, against the same chain in 64 bits on the cache's own values."""
