@@ -16,7 +16,7 @@
 // latency what it reaches of it: while a warp works on a page's values the
 // next page's keys are copied into shared memory (16-byte asynchronous
 // copies), and so in turn; 16 warps an SM.  256 prompts (1.07 M tokens, bf16,
-// 8 heads of 128): 1.24 ms, 5.3 TB/s of its bytes (12 warps with two pages of
+// 8 heads of 128): 1.22 ms, 5.4 TB/s of its bytes (12 warps with two pages of
 // buffers each 1.49; rows held in registers instead 1.50; angles by a sine
 // and a cosine for each row and lanes that met in the same banks 1.70 and up).
 #include <math.h>
@@ -34,6 +34,7 @@ namespace {
 
 // Warps of a CTA (one CTA an SM): a page's raw rows, keys and values, each.
 template <typename T, int HD> constexpr int kPageBytes = 2 * kPage * HD * (int)sizeof(T);
+// 16 warps where their buffers fit, for rows of 512 bytes 12.
 template <typename T, int HD> constexpr int kWarpsOf = kPageBytes<T, HD> <= 8192 ? 16 : 12;
 constexpr int kStageSeqs = 1024;          // sequences whose prefix sums are staged in shared memory
 

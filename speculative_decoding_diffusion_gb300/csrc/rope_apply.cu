@@ -3,10 +3,14 @@
 // y = R(pos) x on the pairs of the first rotary_dim elements of every head:
 //   y1 = x1 cos - x2 sin, y2 = x2 cos + x1 sin, the angle position * w_i.
 // A copy with six operations per pair, so DRAM bounds it; the 64 angles of a
-// row are formed once and shared by its heads through shared memory.
+// row are formed once and shared by its heads through shared memory, while the
+// heads' first vectors are already on their way (four pairs of 16 bytes a
+// thread).  262144 rows of 32 + 8 heads of 128, bf16: 0.91 ms, 5.9 TB/s of its
+// bytes, 0.87 of a plain copy's rate; 128 rows of 32 heads, fp32: 3.0 us.
 #include <math.h>
 #include <string.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
@@ -263,8 +267,10 @@ extern "C" simsd_status simsd_rope(const simsd_rope_desc *d, void *stream) {
   a.heads = d->num_heads0 + d->num_heads1;
   a.hd = d->head_dim;
   a.inverse = d->inverse;
-  // four rows a CTA (an angle per thread) once every SM has several such CTAs
-  a.rows_per_cta = d->rows >= kMaxRows * 4 * device_sm_count() ? kMaxRows : 1;
+  // as many rows a CTA (up to four: an angle per thread) as leave every SM one
+  // (40 heads of 128, bf16, in CTAs of one / four rows: 152 rows 3.1 / 4.6 us, 608
+  // 5.7 / 4.6, 9728 56 / 42, 65536 347 / 235)
+  a.rows_per_cta = std::min(kMaxRows, std::max(1, d->rows / device_sm_count()));
   a.inv_heads = (uint32_t)(((1ull << 32) + a.heads - 1) / a.heads);
   const cudaError_t e = d->dtype == SIMSD_BF16 ? launch_rope<__nv_bfloat16>(a, vec, (cudaStream_t)stream)
                                                : launch_rope<float>(a, vec, (cudaStream_t)stream);
