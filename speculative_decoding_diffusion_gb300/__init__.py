@@ -3,7 +3,8 @@
 The hot path -- RoPE-copy + paged KV append, split-KV attention under the
 token-level temporal causal mask, split merge, and rejection-sampling
 acceptance along the temporal order -- runs in the CUDA kernels of
-libsimsd.so behind the C ABI in include/simsd.h.  ``binding`` marshals torch
+libsimsd.so behind the C ABI in include/simsd.h; so does the loop over an
+8-bit cache (page map, rotary append, attention).  ``binding`` marshals torch
 tensors into that ABI; ``staging`` moves host arrays into the device layouts
 the ABI expects.  There is no CPU fallback.
 """

@@ -28,8 +28,8 @@
 // angles 1.8, rows 2.5 to 5 (as much instruction fetch as work), the new
 // tokens' block 3.5, epilogue 4.  Measured, bf16, 32 heads on 8 of 128: 64
 // sequences of up to 4096 keys, one token each, 86 us (3.2 TB/s of its bytes);
-// 64 of 4096, 16 rows a head, 155 us (3.6 TB/s, 440 TFLOP/s); 8 of 32768, 32 rows
-// a head, 161 us (3.4 TB/s, 850 TFLOP/s); 256 of 256..8192 588 us (4.1 TB/s).
+// 64 of 4096, 64 rows a KV head, 155 us (3.6 TB/s, 440 TFLOP/s); 8 of 32768, 128
+// rows, 161 us (3.4 TB/s, 850 TFLOP/s); 256 of 256..8192 588 us (4.1 TB/s).
 //   warp 0       one 2 KB copy per page: keys by TMA, swizzled for the MMA,
 //                values as they lie
 //   warp 6       scales: page ids and scale bytes well ahead, what they mean

@@ -48,8 +48,8 @@ def test_matches_definition(dtype, hd, rd, interleaved, scaling):
             close(ky, k, pos, spec, inverse)
 
 
-@pytest.mark.parametrize("rows", [1, 5, 2431, 2433])
-def test_row_counts_around_the_four_row_cta(rows):
+@pytest.mark.parametrize("rows", [1, 5, 303, 457, 607, 2433])
+def test_row_counts_around_the_rows_of_a_cta(rows):
     spec = dict(base=1.0e4)
     x = torch.randn(rows, 2, 64, generator=torch.Generator().manual_seed(rows))
     pos = torch.arange(rows, dtype=torch.int32)
