@@ -444,6 +444,41 @@ def _run_on(stream, *tensors):
     return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev)
 
 
+# A call's arrays are looked at in one pass by the three functions below; only
+# where something is wrong do the checks run that say what.
+def _arrays(dev, dtype, *tensors):
+    """Whether all (None passes) are contiguous, of one type, on one device."""
+    for t in tensors:
+        if t is not None and (t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous()):
+            return False
+    return True
+
+
+def _bytes(dev, *tensors):
+    """Whether all are contiguous, of one byte an element, on one device."""
+    for t in tensors:
+        if t.element_size() != 1 or t.get_device() != dev or not t.is_contiguous():
+            return False
+    return True
+
+
+def _rows_on(dev, dtype, *tensors):
+    """Whether all are of one type on one device."""
+    for t in tensors:
+        if t.dtype is not dtype or t.get_device() != dev:
+            return False
+    return True
+
+
+def _stream_on(stream, dev, workspace):
+    """The stream to launch on, for arrays on device dev; None: not the current one's."""
+    if dev < 0 or dev != _device() or (workspace is not None and workspace.get_device() != dev):
+        return None
+    if stream is not None:
+        return stream.cuda_stream
+    return torch.cuda.current_stream().cuda_stream if _raw_stream is None else _raw_stream(dev)
+
+
 def _heads_of(t, dtype, rows, hd, what):
     """(heads, row stride, head stride) of a [rows, heads, hd] tensor whose heads are contiguous."""
     if t.dim() != 3 or t.dtype is not dtype:
@@ -458,7 +493,9 @@ def _heads_of(t, dtype, rows, hd, what):
 
 
 def _row_stride(t, what):
-    """Row stride of a [rows, heads, hd] tensor whose rows are contiguous."""
+    """Row stride of a [rows, heads, hd] tensor whose rows are contiguous (0: and its rows one after another)."""
+    if t.dim() == 3 and t.is_contiguous():
+        return 0
     if t.dim() != 3:
         raise ValueError("%s: expected [rows, heads, head_dim]" % what)
     rows, heads, hd = t.shape
@@ -504,7 +541,12 @@ def rope(x, positions, spec, out, x2=None, out2=None, inverse=False, stream=None
     out may be x.  positions int32 [rows]; inverse turns back (the gradient)."""
     if (x2 is None) != (out2 is None):
         raise ValueError("x2 and out2 come together")
-    _ints(torch.int32, positions=positions)
+    dev = x.get_device()
+    s = _stream_on(stream, dev, out)
+    if s is None or not _arrays(dev, torch.int32, positions) or (
+            x2 is not None and (x2.get_device() != dev or out2.get_device() != dev)):
+        _ints(torch.int32, positions=positions)
+        s = _run_on(stream, x, positions, out, x2, out2)
     if x.dim() != 3:
         raise ValueError("x: expected [rows, heads, head_dim]")
     rows, _, hd = x.shape
@@ -519,7 +561,6 @@ def rope(x, positions, spec, out, x2=None, out2=None, inverse=False, stream=None
         raise ValueError("out: heads of x")
     if positions.numel() != rows:
         raise ValueError("positions: one for each row of x")
-    s = _run_on(stream, x, positions, out, x2, out2)
     d = _PACK_ROPE.pack(rows, h1, h2, hd, _dtype_code(x), 1 if inverse else 0, bytes(spec),
                         positions.data_ptr(), x.data_ptr(), out.data_ptr(), _addr(x2), _addr(out2),
                         row1, head1, orow1, ohead1, row2, head2, orow2, ohead2)
@@ -538,9 +579,15 @@ def page_map(lens, cu_n, held, queue, free_pages, block_table, held_out, queue_o
              workspace, total_n, stream=None):
     """simsd_page_map: block_table and free_pages in place, held/queue to
     held_out/queue_out (may be the same tensors); cu_n and slots may be None."""
-    _ints(torch.int32, lens=lens, cu_n=cu_n, held=held, queue=queue, free_pages=free_pages,
-          block_table=block_table, held_out=held_out, queue_out=queue_out, served=served)
-    _ints(torch.int64, slots=slots)
+    dev = lens.get_device()
+    s = _stream_on(stream, dev, workspace)
+    if s is None or not _arrays(dev, torch.int32, lens, cu_n, held, queue, free_pages, block_table, held_out,
+                                queue_out, served) or not _arrays(dev, torch.int64, slots):
+        _ints(torch.int32, lens=lens, cu_n=cu_n, held=held, queue=queue, free_pages=free_pages,
+              block_table=block_table, held_out=held_out, queue_out=queue_out, served=served)
+        _ints(torch.int64, slots=slots)
+        s = _run_on(stream, lens, cu_n, held, queue, free_pages, block_table, held_out, queue_out, served,
+                    slots, workspace)
     (batch,), (tables, width) = lens.shape, block_table.shape
     if (held.numel() != batch or held_out.numel() != batch or served.numel() != batch or
             tables != batch or (cu_n is not None and cu_n.numel() != batch + 1) or
@@ -551,17 +598,14 @@ def page_map(lens, cu_n, held, queue, free_pages, block_table, held_out, queue_o
                             lens.data_ptr(), _addr(cu_n), held.data_ptr(), queue.data_ptr(),
                             free_pages.data_ptr(), block_table.data_ptr(), held_out.data_ptr(),
                             queue_out.data_ptr(), served.data_ptr(), _addr(slots), *_ws(workspace))
-    s = _run_on(stream, lens, cu_n, held, queue, free_pages, block_table, held_out, queue_out, served,
-                slots, workspace)
     _check(lib().simsd_page_map(d, s), "simsd_page_map")
 
 
 def _cache_shape(k_cache, v_cache, k_scale, v_scale, hkv, hd, what):
     """(num_pages, page_size), the four arrays being one cache of hkv heads of hd."""
-    _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    shape = k_cache.shape
-    if (len(shape) != 4 or v_cache.shape != shape or shape[1] != hkv or shape[3] != hd or
-            k_scale.shape != shape[:2] or v_scale.shape != shape[:2]):
+    shape, scale = k_cache.shape, k_scale.shape
+    if (len(shape) != 4 or v_cache.shape != shape or shape[1] != hkv or shape[3] != hd or len(scale) != 2 or
+            scale[0] != shape[0] or scale[1] != hkv or v_scale.shape != scale):
         raise ValueError("%s: sizes of the cache's arrays disagree" % what)
     return shape[0], shape[2]
 
@@ -570,8 +614,14 @@ def kvq_append(k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_tabl
                take=None, stream=None):
     """simsd_kvq_append: k (rotated by spec) and v [total_n, Hkv, hd] into the
     e4m3 caches [num_pages, Hkv, 16, hd] with e8m0 scales [num_pages, Hkv]."""
-    _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table, take=take)
-    _same_dtype(k, v=v)
+    dev = k.get_device()
+    s = _stream_on(stream, dev, workspace)
+    if s is None or not _arrays(dev, torch.int32, start, cu_n, block_table, take) or not _rows_on(
+            dev, k.dtype, v) or not _bytes(dev, k_cache, v_cache, k_scale, v_scale):
+        _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table, take=take)
+        _same_dtype(k, v=v)
+        _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+        s = _run_on(stream, k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_table, workspace, take)
     if k.dim() != 3 or v.shape != k.shape:
         raise ValueError("kvq_append: k and v are [rows, heads, head_dim]")
     total_n, hkv, hd = k.shape
@@ -584,15 +634,23 @@ def kvq_append(k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_tabl
                           start.data_ptr(), cu_n.data_ptr(), _addr(take), k_cache.data_ptr(),
                           v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                           block_table.data_ptr(), *_ws(workspace))
-    s = _run_on(stream, k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_table, workspace, take)
     _check(lib().simsd_kvq_append(d, s), "simsd_kvq_append")
 
 
 def _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
                      cu_B, out, workspace, total_B, B_max, spec, sm_scale, order, node_size,
-                     wait_polls=0):
-    _ints(torch.int32, block_table=block_table, tau=tau, lens=lens, cu_B=cu_B)
-    _same_dtype(q, k_new=k_new, v_new=v_new, out=out)
+                     wait_polls=0, stream=False):
+    """(stream, descriptor); stream False: for the workspace's size, no device needed."""
+    dev = q.get_device()
+    s = None if stream is False else _stream_on(stream, dev, workspace)
+    if s is None or not _arrays(dev, torch.int32, block_table, tau, lens, cu_B) or not _rows_on(
+            dev, q.dtype, k_new, v_new, out) or not _bytes(dev, k_cache, v_cache, k_scale, v_scale):
+        _ints(torch.int32, block_table=block_table, tau=tau, lens=lens, cu_B=cu_B)
+        _same_dtype(q, k_new=k_new, v_new=v_new, out=out)
+        _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+        if stream is not False:
+            s = _run_on(stream, q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
+                        cu_B, out, workspace)
     paired = order == SIMSD_ORDER_PAIRED
     if q.dim() != 3 or k_new.dim() != 3 or out.shape != q.shape or v_new.shape != k_new.shape:
         raise ValueError("kvq_verify: q, out and k_new, v_new are [rows, heads, head_dim]")
@@ -605,20 +663,20 @@ def _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, 
         raise ValueError("kvq_verify: sizes of the arrays disagree")
     if not out.is_contiguous():
         raise ValueError("out is not contiguous")
-    return _PACK_VERIFY.pack(batch, hq, hkv, hd, page, num_pages, width, total_B, B_max, _dtype_code(q),
-                             order, node_size, bytes(spec), sm_scale, wait_polls, _row_stride(q, "q"),
-                             _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), q.data_ptr(),
-                             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
-                             v_scale.data_ptr(), block_table.data_ptr(), k_new.data_ptr(),
-                             v_new.data_ptr(), _addr(tau), lens.data_ptr(), cu_B.data_ptr(),
-                             out.data_ptr(), *_ws(workspace))
+    return s, _PACK_VERIFY.pack(batch, hq, hkv, hd, page, num_pages, width, total_B, B_max, _dtype_code(q),
+                                order, node_size, bytes(spec), sm_scale, wait_polls, _row_stride(q, "q"),
+                                _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), q.data_ptr(),
+                                k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                v_scale.data_ptr(), block_table.data_ptr(), k_new.data_ptr(),
+                                v_new.data_ptr(), _addr(tau), lens.data_ptr(), cu_B.data_ptr(),
+                                out.data_ptr(), *_ws(workspace))
 
 
 def kvq_verify_workspace_size(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau,
                               lens, cu_B, out, total_B, B_max, spec, sm_scale,
                               order=SIMSD_ORDER_PAIRED, node_size=0):
-    d = _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
-                         cu_B, out, None, total_B, B_max, spec, sm_scale, order, node_size)
+    _, d = _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
+                            cu_B, out, None, total_B, B_max, spec, sm_scale, order, node_size)
     n = lib().simsd_kvq_verify_workspace_size(d)
     if n == 0:
         raise SimsdError(2, "simsd_kvq_verify_workspace_size")
@@ -631,11 +689,9 @@ def kvq_verify(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new,
     """simsd_kvq_verify: attention of the new tokens over the 8-bit prompt
     cache and themselves; spec from rope_spec; tau may be None unless the
     order is SIMSD_ORDER_PAIRED."""
-    d = _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
-                         cu_B, out, workspace, total_B, B_max, spec, sm_scale, order, node_size,
-                         wait_polls)
-    s = _run_on(stream, q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens, cu_B,
-                out, workspace)
+    s, d = _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new, tau, lens,
+                            cu_B, out, workspace, total_B, B_max, spec, sm_scale, order, node_size,
+                            wait_polls, stream)
     _check(lib().simsd_kvq_verify(d, s), "simsd_kvq_verify")
 
 
