@@ -75,7 +75,7 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = 0.f;
     if (r < rows) {
-      const int tok = (w.row0 + r) / a.G, head = w.kvh * a.G + (w.row0 + r) % a.G;
+      const int tok = div_by(w.row0 + r, a.by_G), head = w.kvh * a.G + (w.row0 + r) - tok * a.G;
       rotate8(a.plan, cs + kvq_offset(a, w.B, tok) * (HD / 2), (const T *)a.q + (t0 + tok) * a.q_row + head * HD, c * 8, x);
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] *= a.scale;
@@ -110,7 +110,7 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
   const int r0 = warp * kRowsPerWarp;
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i)
-    newvis[i] = r0 + i < rows ? kvq_visible(a, w.B, tau_s, (w.row0 + r0 + i) / a.G) : 0ull;
+    newvis[i] = r0 + i < rows ? kvq_visible(a, w.B, tau_s, div_by(w.row0 + r0 + i, a.by_G)) : 0ull;
   float m[kRowsPerWarp], l[kRowsPerWarp], o[kRowsPerWarp][PER];
 #pragma unroll
   for (int i = 0; i < kRowsPerWarp; ++i) {
@@ -221,7 +221,8 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
     if (r0 + i >= rows) continue;
     if (w.first && (newvis[i] & ((uint64_t)odd_s[1] << 32 | odd_s[0])) != 0ull) l[i] = __uint_as_float(0x7fc00000u);
     const int grow = w.row0 + r0 + i;
-    const int64_t row = (t0 + grow / a.G) * a.Hq + w.kvh * a.G + grow % a.G;
+    const int tok = div_by(grow, a.by_G);
+    const int64_t row = (t0 + tok) * a.Hq + w.kvh * a.G + grow - tok * a.G;
     if (w.n_splits == 1) {
       const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
 #pragma unroll
@@ -510,6 +511,13 @@ simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream_ptr) 
   a.tail_from = p.tail_from; a.s_tail = p.s_tail; a.chunk_tail = p.chunk_tail; a.tail_first = p.tail_first;
   a.order_ws = p.ranked ? (int4 *)(ws + p.off_order) : nullptr;
   a.merge_seqs = p.merge_seqs;
+  a.n_tail = p.grid - p.tail_from;
+  a.n_whole = p.s_tail > 1 ? a.n_tail / p.s_tail * (p.s_tail - 1) : a.n_tail;
+  a.by_seq = make_fast_div(a.Hkv * a.row_tiles);
+  a.by_kv = make_fast_div(a.Hkv);
+  a.by_split = make_fast_div(std::max(1, p.s_tail - 1));
+  a.by_G = make_fast_div(a.G);
+  a.by_node = make_fast_div(std::max(1, a.node_size));
   a.polls = wait_polls_of(d->wait_polls);
   a.scale = d->sm_scale * 1.4426950408889634f;
   cudaStream_t stream = (cudaStream_t)stream_ptr;

@@ -10,6 +10,23 @@ namespace simsd {
 
 constexpr int kMaxNew = 64;              // new tokens of a sequence
 
+// n / d for 0 <= n < 2^31 (rounded-up reciprocal with one bit more than 32: the
+// method of Granlund and Montgomery).
+struct FastDiv {
+  uint32_t mul;
+  int shift, d;
+};
+
+inline FastDiv make_fast_div(int d) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - (uint64_t)d)) / (uint64_t)d + 1), l, d};
+}
+
+__device__ __forceinline__ int div_by(int n, const FastDiv &f) {
+  return (int)((__umulhi(f.mul, (uint32_t)n) + (uint32_t)n) >> f.shift);
+}
+
 // Units (sequence, KV head, row tile) run whole or in key splits, as in
 // VerifyPlan: the first tail_from whole, each later one in s_tail splits of
 // chunk_tail prompt keys.
@@ -35,6 +52,8 @@ struct KvqParams {
   int batch, Hq, Hkv, G, T, total_B, B_max, order, node_size, per;
   int max_pages, num_pages;
   int rows_per_tile, row_tiles, tail_from, s_tail, chunk_tail, tail_first, merge_seqs;
+  int n_tail, n_whole;                   // CTAs of split units; of them those of whole chunks, which come first
+  FastDiv by_seq, by_kv, by_split, by_G, by_node;   // units of a sequence, KV heads, whole chunks of a unit, ..
   uint32_t polls;
   float scale;                           // sm_scale * log2(e)
 };
@@ -51,7 +70,7 @@ struct KvqWork {
 __device__ __forceinline__ bool kvq_bad(const KvqParams &a, int c0, int B, int P) {
   return B < 1 || B > a.B_max || c0 < 0 || c0 > a.total_B - B || P < 0 ||
          (int64_t)P > (int64_t)a.max_pages * kPage ||
-         (a.order == SIMSD_ORDER_NODES && B % a.node_size != 0);
+         (a.order == SIMSD_ORDER_NODES && B != div_by(max(B, 0), a.by_node) * a.node_size);
 }
 
 // Sequence `rank` of the units' order; its first section, sections and prompt.
@@ -64,27 +83,25 @@ __device__ __forceinline__ int4 kvq_sequence(const KvqParams &a, int rank) {
 __device__ __forceinline__ KvqWork kvq_work(const KvqParams &a) {
   KvqWork w;
   const int ci = blockIdx.x;
-  const int n_tail = (int)gridDim.x - a.tail_from;   // CTAs of split units
-  const bool tail = a.tail_first ? ci < n_tail : ci >= a.tail_from;
+  const bool tail = a.tail_first ? ci < a.n_tail : ci >= a.tail_from;
   const int ti = a.tail_first ? ci : ci - a.tail_from;
   // split units: the whole chunks of all of them, then their last ones
-  const int n_whole = a.s_tail > 1 ? n_tail / a.s_tail * (a.s_tail - 1) : n_tail;
-  const int s_whole = max(1, a.s_tail - 1);
-  const int unit = !tail ? (a.tail_first ? ci - n_tail : ci)
-                         : a.tail_from + (ti < n_whole ? ti / s_whole : ti - n_whole);
+  const bool whole = ti < a.n_whole;
+  const int of = whole ? div_by(max(ti, 0), a.by_split) : ti - a.n_whole;
+  const int unit = !tail ? (a.tail_first ? ci - a.n_tail : ci) : a.tail_from + of;
   const int chunk = tail ? a.chunk_tail : a.max_pages * kPage;
-  const int per_seq = a.Hkv * a.row_tiles;
-  w.split = !tail ? 0 : ti < n_whole ? ti % s_whole : s_whole;
-  const int4 seq = kvq_sequence(a, unit / per_seq);
+  const int rank = div_by(unit, a.by_seq), in_seq = unit - rank * a.by_seq.d;
+  w.split = !tail ? 0 : whole ? ti - of * a.by_split.d : a.by_split.d;
+  const int4 seq = kvq_sequence(a, rank);
   w.b = seq.x;
   w.c0 = seq.y;
   w.B = seq.z;
   w.P = seq.w;
-  w.kvh = unit % per_seq % a.Hkv;
-  w.rtile = unit % per_seq / a.Hkv;
+  w.rtile = div_by(in_seq, a.by_kv);
+  w.kvh = in_seq - w.rtile * a.Hkv;
   w.ok = false;
   if (kvq_bad(a, w.c0, w.B, w.P)) {
-    if (threadIdx.x == 0 && w.split == 0 && unit % per_seq == 0) raise_status(a.status, kStatusBadInput);
+    if (threadIdx.x == 0 && w.split == 0 && in_seq == 0) raise_status(a.status, kStatusBadInput);
     return w;
   }
   w.n = a.per * w.B;
@@ -94,14 +111,14 @@ __device__ __forceinline__ KvqWork kvq_work(const KvqParams &a) {
   w.first = w.split == 0;
   w.ok = w.row0 < w.M && (w.first || w.k_begin < w.P);
   w.k_end = min(w.P, w.k_begin + chunk);
-  w.n_splits = max(1, (w.P + chunk - 1) / chunk);
+  w.n_splits = tail ? max(1, (w.P + chunk - 1) / chunk) : 1;
   return w;
 }
 
 // Position of new token `tok` past the prompt.
 __device__ __forceinline__ int kvq_offset(const KvqParams &a, int B, int tok) {
   return a.order == SIMSD_ORDER_PAIRED ? (tok < B ? tok : tok - B)
-         : a.order == SIMSD_ORDER_NODES ? tok % a.node_size : tok;
+         : a.order == SIMSD_ORDER_NODES ? tok - div_by(tok, a.by_node) * a.node_size : tok;
 }
 
 // bits [0, n) set (n clamped to 0..64)
@@ -114,7 +131,7 @@ __device__ __forceinline__ uint64_t kvq_low_bits(int n) {
 __device__ __forceinline__ uint64_t kvq_visible(const KvqParams &a, int B, const int *tau_s, int tok) {
   if (a.order == SIMSD_ORDER_CAUSAL) return kvq_low_bits(tok + 1);
   if (a.order == SIMSD_ORDER_NODES)
-    return kvq_low_bits(a.node_size) << ((tok / a.node_size) * a.node_size);
+    return kvq_low_bits(a.node_size) << (div_by(tok, a.by_node) * a.node_size);
   const bool slot = tok >= B;
   const int t = tau_s[slot ? tok - B : tok];
   uint64_t bits = 0;

@@ -199,14 +199,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return *reinterpret_cast<float2 *>(&d);
 }
 
-// a / d for 0 <= a < 2^24, d > 0, r = 1.f / d: the product is off by less than one.
-__device__ __forceinline__ int div_by(int a, int d, float r) {
-  int q = (int)((float)a * r);
-  const int rest = a - q * d;
-  q += rest >= d ? 1 : 0;
-  return rest < 0 ? q - 1 : q;
-}
-
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1)
 kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ KvqParams a) {
@@ -228,6 +220,12 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     tc::alloc(smem_u32(tmem_slot), L::kTmemCols);
     tc::relinquish();
   }
+  // the threads that rotate and split rows, their index among them, and the
+  // pair whose angles each of them makes (its plan requested here)
+  const bool prep_warp = warp >= 2 && warp != kScaleWarp && warp != kPvWarp;
+  const int pt = threadIdx.x - (warp < kScaleWarp ? 64 : 96), pair = (pt + 64) % (HD / 2);
+  static_assert(kPrep % (HD / 2) == 0, "a thread's angles are of one pair");
+  const float turn_hi = plan_by_lane(a.plan).hi[pair], turn_lo = plan_by_lane(a.plan).lo[pair];
   grid_dep_wait();                           // the units' order is there
   grid_dep_launch();                         // the split merge may be scheduled
   const KvqWork w = kvq_work(a);
@@ -266,11 +264,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     return in_cache(page) ? (int)__ldg(scale + (int64_t)page * a.Hkv + w.kvh) : kNoPage;
   };
   int pages[kStages];
-  // index among the threads that rotate and split rows
-  const int pt = threadIdx.x - (warp < kScaleWarp ? 64 : 96);
   constexpr int CH = HD / 8;                 // 16-byte chunks of a bf16 row
-  const float rG = 1.f / (float)a.G;
-  const bool prep_warp = warp >= 2 && warp != kScaleWarp && warp != kPvWarp;
   if (warp == 0) {
     if (lane == 0) prefetch_tmap(&tmK);
 #pragma unroll
@@ -280,7 +274,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     // ahead of the stream of codes
     const __nv_bfloat16 *qs = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
     for (int e = pt; e < n_groups * 32 * CH; e += kPrep) {
-      const int r = e / CH, c = e % CH, row = w.row0 + r, tok = div_by(row, a.G, rG);
+      const int r = e / CH, c = e % CH, row = w.row0 + r, tok = div_by(row, a.by_G);
       const bool take = row < w.M;
       copy16_async(base + L::kOffVb + r * HD * 2 + c * 16,
                    take ? qs + tok * a.q_row + (row - tok * a.G) * HD + c * 8 : (const void *)a.q, take);
@@ -327,8 +321,12 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
 #pragma unroll 1
     for (int e = pt; e < npos * (HD / 2); e += kPrep) {
-      const int d = e % (HD / 2);
-      cs_s[e - d + angle_at(d)] = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
+      float2 cs = make_float2(1.f, 0.f);
+      if (pair < a.plan.half) {
+        cs = rope_angle(plan_by_lane(a.plan), turn_hi, turn_lo, pair, w.P + e / (HD / 2));
+        cs = make_float2(cs.x * a.plan.mul, cs.y * a.plan.mul);
+      }
+      cs_s[e - pair + angle_at(pair)] = cs;
     }
     if (a.order == SIMSD_ORDER_PAIRED && pt < w.B) tau_s[pt] = __ldg(a.tau + w.c0 + pt);
     copy_async_wait_all();
@@ -377,7 +375,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         continue;
       }
       const int row = w.row0 + r;
-      const int tok = !query ? min(r, w.n - 1) : row < w.M ? div_by(row, a.G, rG) : 0;
+      const int tok = !query ? min(r, w.n - 1) : row < w.M ? div_by(row, a.by_G) : 0;
       int c0, c1;
       float x[16], down = kdown;
       rotate16(a.plan, cs_s + kvq_offset(a, w.B, tok) * (HD / 2), query ? qs + r * HD : ks + tok * HD, c, c0, c1, x);
@@ -627,7 +625,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     const int grow = w.row0 + 32 * g + lane;
     const bool row_valid = grow < w.M;
     const bool warp_valid = w.row0 + 32 * g < w.M;
-    const int tok = row_valid ? grow / a.G : 0;
+    const int tok = row_valid ? div_by(grow, a.by_G) : 0;
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
     // this row's values of the two warps that share it: [block parity][half]
     float *both_s = reinterpret_cast<float *>(sb + L::kOffMax) + 32 * q4 + lane;
@@ -804,7 +802,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     tc::fence_after_sync();
     // -------------------------------------------------------- epilogue
     const bool failed = !ok || *(volatile int *)flag_s != 0;
-    const int64_t orow = (t0 + tok) * a.Hq + w.kvh * a.G + (row_valid ? grow % a.G : 0);
+    const int64_t orow = (t0 + tok) * a.Hq + w.kvh * a.G + (row_valid ? grow - tok * a.G : 0);
     // columns [c0, c0 + n), n <= 32, of this thread's row: sums v relative to
     // reference mr, weights' sum lt
     auto write_cols = [&](const float *v, int c0, int n, float lt, float mr) {

@@ -44,13 +44,13 @@ static __device__ __noinline__ float far_turn(double turns, int pos) {
 }
 
 // (cos, sin) of pair d < half at position pos (negative positions turn the
-// other way).
-__device__ __forceinline__ float2 rope_plan_angle(const RopePlan &p, int d, int pos) {
+// other way); hi, lo: the plan's for d.
+__device__ __forceinline__ float2 rope_angle(const RopePlan &p, float hi, float lo, int d, int pos) {
   float rest;
   if (pos < (1 << 24) && pos > -(1 << 24)) {
-    const float x = (float)pos, hi = p.hi[d];        // exact
+    const float x = (float)pos;                      // exact
     const float t = x * hi;
-    const float t_lo = fmaf(x, p.lo[d], fmaf(x, hi, -t));
+    const float t_lo = fmaf(x, lo, fmaf(x, hi, -t));
     rest = (t - rintf(t)) + t_lo;
   } else {
     rest = far_turn(p.turns[d], pos);
@@ -58,6 +58,10 @@ __device__ __forceinline__ float2 rope_plan_angle(const RopePlan &p, int d, int 
   float s, c;
   sincospif(2.f * rest, &s, &c);
   return make_float2(c, s);
+}
+
+__device__ __forceinline__ float2 rope_plan_angle(const RopePlan &p, int d, int pos) {
+  return rope_angle(p, p.hi[d], p.lo[d], d, pos);
 }
 
 // Place of pair d in a shared-memory row of angles that lanes read eight
