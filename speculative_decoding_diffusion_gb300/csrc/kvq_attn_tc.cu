@@ -857,26 +857,29 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
               make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
                           __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
       }
-      if (half == 0) {
-        mine[HD] = l;
-        mine[HD + 1] = m_ref;
-      }
+      if (half == 0) *reinterpret_cast<float2 *>(mine + HD) = make_float2(m_ref, l);
       named_sync(3, 8 * 32);
       if (row_valid && !failed) {
         const int cw = HD / (R * kHalves), cb = (kp * kHalves + half) * cw;    // 8, 16 or 32 columns
-        float mt = -INFINITY;
-        for (int c = 0; c < R; ++c) mt = fmaxf(mt, part[((c * groups + g) * 32 + lane) * (HD + 4) + HD + 1]);
+        const float *row = part + (g * 32 + lane) * (HD + 4);                  // copy 0; the others:
+        const int next = groups * 32 * (HD + 4);
+        float2 ml[4];                          // the copies' references and sums, read together
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          ml[c] = c < R ? *reinterpret_cast<const float2 *>(row + c * next + HD) : make_float2(-INFINITY, 0.f);
+        const float mt = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
         float lt = 0.f, v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = 0.f;
-        for (int c = 0; c < R; ++c) {
-          const float *pc = part + ((c * groups + g) * 32 + lane) * (HD + 4);
-          const float wc = ex2(pc[HD + 1] - (mt == -INFINITY ? 0.f : mt));   // -inf reference -> 0
-          lt += wc * pc[HD];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= R) break;
+          const float wc = ex2(ml[c].x - (mt == -INFINITY ? 0.f : mt));   // -inf reference -> 0
+          lt += wc * ml[c].y;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             if (4 * e >= cw) break;
-            const float4 p4 = *reinterpret_cast<const float4 *>(pc + cb + 4 * e);
+            const float4 p4 = *reinterpret_cast<const float4 *>(row + c * next + cb + 4 * e);
             v[4 * e] += wc * p4.x; v[4 * e + 1] += wc * p4.y;
             v[4 * e + 2] += wc * p4.z; v[4 * e + 3] += wc * p4.w;
           }
