@@ -22,14 +22,14 @@
 // 1024 tensor-core cycles (an MMA of N = 128 takes 64, e4m3 at K = 32 like f16
 // at K = 16; issued by one lane of a converged warp, whose addresses stay in
 // uniform registers, 33 to 43 cycles each -- from a branch of a single thread
-// it is 55 or more).  It takes 1400 cycles with up to 32 rows, 1770 with 64 and
-// 2450 with 128, whose chain of waits (scores, maximum, exchange, exponentials,
-// weights, P V) bounds it, and a CTA 18 to 22 thousand cycles more: set-up 3.3,
-// angles 1.8, rows 2.5 to 5 (as much instruction fetch as work), the new
-// tokens' block 3.5, epilogue 4.  Measured, bf16, 32 heads on 8 of 128: 64
-// sequences of up to 4096 keys, one token each, 86 us (3.2 TB/s of its bytes);
-// 64 of 4096, 64 rows a KV head, 155 us (3.6 TB/s, 440 TFLOP/s); 8 of 32768, 128
-// rows, 161 us (3.4 TB/s, 850 TFLOP/s); 256 of 256..8192 588 us (4.1 TB/s).
+// it is 55 or more).  It takes 1400 cycles with up to 32 rows, 1700 with 64 and
+// 2280 with 128, where the softmax's chain (scores, maximum, exchange,
+// exponentials, weights) bounds it, and a CTA 15 to 20 thousand cycles more:
+// set-up 3, angles 1.5, rows 2 to 5 (as much instruction fetch as work), the new
+// tokens' block 3.5, epilogue 3.  Measured, bf16, 32 heads on 8 of 128: 64
+// sequences of up to 4096 keys, one token each, 82 us (3.4 TB/s of its bytes);
+// 64 of 4096, 64 rows a KV head, 148 us (3.8 TB/s, 460 TFLOP/s); 8 of 32768, 128
+// rows, 150 us (3.6 TB/s, 910 TFLOP/s); 256 of 256..8192 574 us (4.2 TB/s).
 //   warp 0       one 2 KB copy per page: keys by TMA, swizzled for the MMA,
 //                values as they lie
 //   warp 6       scales: page ids and scale bytes well ahead, what they mean
@@ -77,7 +77,7 @@ constexpr uint32_t kColO = kColP + kKeys / 2;
 
 enum { kBarKFull = 0, kBarVFull = kBarKFull + kStages, kBarKEmpty = kBarVFull + kStages,
        kBarVEmpty = kBarKEmpty + kStages, kBarSFull = kBarVEmpty + kStages,
-       kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 1,
+       kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 2,
        kBarVbFull = kBarPvDone + 2,
        kBarQReady = kBarVbFull + 2, kBarKnReady = kBarQReady + 1, kBarNewRead = kBarKnReady + 1,
        kBarGFull = kBarNewRead + 1, kBarGEmpty = kBarGFull + kGroupSlots, kNumBars = kBarGEmpty + kGroupSlots };
@@ -243,6 +243,13 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   const int n_groups = min(4, (w.M - w.row0 + 31) / 32);
   const int R = n_groups == 1 ? 4 : n_groups == 2 ? 2 : 1;
   const int n_valid = kHalves * (R > 1 ? 4 : n_groups);
+  // Weights go over the scores they come from, so that a block's need not wait
+  // for the block before to leave its own (the next scores of that buffer wait
+  // for the product instead): 128 rows, 8 x 32768 keys, 160 -> 150 us, 64 rows, 64
+  // x 4096, 149.2 -> 147.8.  With four copies the softmax is short enough for
+  // that to be the longer wait (1400 cycles a block either way): there the weights
+  // have columns of their own, where those of the other copies' keys stay zero.
+  const bool over = R < 4;
   const int32_t *bt = a.block_table + (int64_t)w.b * a.max_pages;
   const int64_t t0 = (int64_t)a.per * w.c0;  // first new token's row
   // Page ids are requested four blocks ahead of their use and looked at only
@@ -289,7 +296,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   }
   if (warp == kPvWarp) {
     for (int i = lane; i < kNumBars; i += 32) {
-      const bool rows = i == kBarPFull || (i >= kBarSEmpty && i < kBarSEmpty + 2);
+      const bool rows = i >= kBarSEmpty && i < kBarPFull + 2;
       const bool tiles = (i >= kBarVEmpty && i < kBarVEmpty + kStages) || (i >= kBarVbFull && i < kBarVbFull + 2) ||
                          i == kBarQReady || i == kBarKnReady || i == kBarNewRead;
       mbar_init(bar(i), i >= kBarGEmpty ? n_valid + 4 : rows ? n_valid : tiles ? 4 : 1);
@@ -500,7 +507,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       const int tb = j & 1, jp = j - fresh, s = jp & (kStages - 1);
       ok = (jp < 0 ? mbar_wait_warp(bar(kBarKnReady), 0, a.polls)
                    : mbar_wait_warp(bar(kBarKFull + s), (jp / kStages) & 1, a.polls)) &&
-           (j < 2 || mbar_wait_warp(bar(kBarSEmpty + tb), ((j >> 1) - 1) & 1, a.polls));
+           (j < 2 || mbar_wait_warp(bar((over ? kBarPvDone : kBarSEmpty) + tb), ((j >> 1) - 1) & 1, a.polls));
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t tS = tmem + kColS + tb * kKeys;
@@ -528,19 +535,20 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     bool ok = true;
     for (int j = 0; j < n_blocks; ++j) {
       const int tb = j & 1, jp = j - fresh;
-      ok = mbar_wait_warp(bar(kBarVbFull + tb), (j >> 1) & 1, a.polls) && mbar_wait_warp(bar(kBarPFull), j & 1, a.polls);
+      ok = mbar_wait_warp(bar(kBarVbFull + tb), (j >> 1) & 1, a.polls) && mbar_wait_warp(bar(kBarPFull + tb), (j >> 1) & 1, a.polls);
       if (!ok) break;
       tc::fence_after_sync();
       const int depth = jp < 0 ? n_pad : min(kKeys, (w.k_end - w.k_begin - jp * kKeys + 15) & ~15);
       const uint64_t dV = dV0 + ((uint32_t)(tb * L::kVb) >> 4);
+      const uint32_t tP = tmem + (over ? kColS + tb * kKeys : kColP);
       if (tc::elect_one()) {
         if (depth == kKeys) {
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_bf16_ts(tmem + kColO, tmem + kColP + kk * 8, dV + kk * 128, idO, j > 0 || kk > 0);
+            tc::mma_bf16_ts(tmem + kColO, tP + kk * 8, dV + kk * 128, idO, j > 0 || kk > 0);
         } else {
           for (int kk = 0; kk < depth / 16; ++kk)
-            tc::mma_bf16_ts(tmem + kColO, tmem + kColP + kk * 8, dV + kk * 128, idO, j > 0 || kk > 0);
+            tc::mma_bf16_ts(tmem + kColO, tP + kk * 8, dV + kk * 128, idO, j > 0 || kk > 0);
         }
         tc::commit(bar(kBarPvDone + tb));
       }
@@ -643,7 +651,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
           v[1] = *reinterpret_cast<const uint4 *>(src + code_off<HD>(32 * g + lane, k + 1));
           tc::st8(trow + L::kColQ + part * (HD / 4) + k * 4, reinterpret_cast<const uint32_t *>(v));
         }
-    } else if (R > 1) {                      // weights of the other copies' keys: zero for good
+    } else if (!over) {                      // weights of the other copies' keys: zero for good
       uint32_t z[16];
 #pragma unroll
       for (int e = 0; e < 16; ++e) z[e] = 0u;
@@ -667,6 +675,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     auto key_loop = [&](auto rc) {
       constexpr int RC = decltype(rc)::value;
       constexpr int KW = kKeys / (RC * kHalves);   // this warp's keys per block: 64, 32 or 16
+      constexpr bool OVER = RC < 4;
       const int k_lo = (kp * kHalves + half) * KW;
       // A warp whose wait gave up still meets its partner once, with a NaN in
       // the maximum's place (a maximum is never NaN), so both leave the loop.
@@ -708,7 +717,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         tc::wait_ld();
         tc::fence_before_sync();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(bar(kBarSEmpty + tb));
+        if (!OVER && ok && lane == 0) mbar_arrive(bar(kBarSEmpty + tb));
         // the row's maximum over both warps' keys
         float mx = -INFINITY;
         if (!whole) {                        // keys that do not count score -inf from here on
@@ -740,6 +749,14 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         const float theirs = both_s[(tb * kHalves + (half ^ 1)) * kRows];
         if (!ok || theirs != theirs) { ok = false; break; }
         mx = fmaxf(mx, theirs);
+        const uint32_t tW = trow + (OVER ? kColS + tb * kKeys : kColP);   // this row's weights
+        if (OVER) tc::fence_after_sync();    // both warps have their scores
+        if (RC == 2) {                       // zeros for half of the other copy's keys
+          uint32_t z[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) z[e] = 0u;
+          tc::st16(tW + (kp ^ 1) * (kKeys / 4) + half * 16, z);
+        }
         // reference: moves only when this block's max outgrows it
         const bool move = row_valid && mx > m_ref + kLift + kHeadroom;
         const float m_new = move ? mx - kLift : m_ref;
@@ -762,11 +779,12 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
           }
           l = fmaf(sum.x + sum.y, inv[i], l);
         }
-        // the weight tile and O are free once the previous block's P V is done
-        if (j > 0) {
+        // O (and weights of their own columns) wait for the previous block's P V
+        const bool any = __any_sync(0xffffffffu, move);
+        if (j > 0 && (!OVER || any)) {
           if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; continue; }
           tc::fence_after_sync();
-          if (__any_sync(0xffffffffu, move)) {   // this half of O's columns
+          if (any) {                         // this half of O's columns
 #pragma unroll 1
             for (int c = 0; c < HD / 32; ++c) {
               uint32_t o[16];
@@ -778,7 +796,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
             }
           }
         }
-        const uint32_t tP = trow + kColP + k_lo / 2;
+        const uint32_t tP = tW + k_lo / 2;
         if constexpr (KW == 16) {
           tc::st8(tP, pw);
         } else {
@@ -789,7 +807,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(bar(kBarPFull));
+          mbar_arrive(bar(kBarPFull + tb));   // (one for each parity: a warp may be a block ahead of another)
           if (!is_new && (q == kGroup - 1 || jp == n_past - 1)) mbar_arrive(bar(kBarGEmpty + slot));
         }
       }
