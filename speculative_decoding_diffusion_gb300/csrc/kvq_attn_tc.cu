@@ -72,12 +72,16 @@ constexpr float kHeadroom = 8.f;     // log2 units a row max may grow before O i
 constexpr float kLift = 7.f;         // log2 of the largest weight right after that
 constexpr int kNoPage = -1;          // instead of a scale byte
 constexpr uint32_t kColS = 0;        // two score tiles: columns 0 and kKeys
-constexpr uint32_t kColP = 2 * kKeys;   // weights as f16, two keys a column
-constexpr uint32_t kColO = kColP + kKeys / 2;
+// The weights, f16, two keys a column, go over the scores they come from, so
+// that a block's need not wait for the block before to leave its own; the next
+// scores of that buffer wait for the product instead.  (Weights in columns of
+// their own: 128 rows, 8 x 32768 keys, 160 us and not 149; 32 rows, 16 x 1024,
+// 16.2 and not 16.0.)
+constexpr uint32_t kColO = 2 * kKeys;
 
 enum { kBarKFull = 0, kBarVFull = kBarKFull + kStages, kBarKEmpty = kBarVFull + kStages,
        kBarVEmpty = kBarKEmpty + kStages, kBarSFull = kBarVEmpty + kStages,
-       kBarSEmpty = kBarSFull + 2, kBarPFull = kBarSEmpty + 2, kBarPvDone = kBarPFull + 2,
+       kBarPFull = kBarSFull + 2, kBarPvDone = kBarPFull + 2,
        kBarVbFull = kBarPvDone + 2,
        kBarQReady = kBarVbFull + 2, kBarKnReady = kBarQReady + 1, kBarNewRead = kBarKnReady + 1,
        kBarGFull = kBarNewRead + 1, kBarGEmpty = kBarGFull + kGroupSlots, kNumBars = kBarGEmpty + kGroupSlots };
@@ -243,13 +247,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   const int n_groups = min(4, (w.M - w.row0 + 31) / 32);
   const int R = n_groups == 1 ? 4 : n_groups == 2 ? 2 : 1;
   const int n_valid = kHalves * (R > 1 ? 4 : n_groups);
-  // Weights go over the scores they come from, so that a block's need not wait
-  // for the block before to leave its own (the next scores of that buffer wait
-  // for the product instead): 128 rows, 8 x 32768 keys, 160 -> 150 us, 64 rows, 64
-  // x 4096, 149.2 -> 147.8.  With four copies the softmax is short enough for
-  // that to be the longer wait (1400 cycles a block either way): there the weights
-  // have columns of their own, where those of the other copies' keys stay zero.
-  const bool over = R < 4;
   const int32_t *bt = a.block_table + (int64_t)w.b * a.max_pages;
   const int64_t t0 = (int64_t)a.per * w.c0;  // first new token's row
   // Page ids are requested four blocks ahead of their use and looked at only
@@ -296,7 +293,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   }
   if (warp == kPvWarp) {
     for (int i = lane; i < kNumBars; i += 32) {
-      const bool rows = i >= kBarSEmpty && i < kBarPFull + 2;
+      const bool rows = i >= kBarPFull && i < kBarPFull + 2;
       const bool tiles = (i >= kBarVEmpty && i < kBarVEmpty + kStages) || (i >= kBarVbFull && i < kBarVbFull + 2) ||
                          i == kBarQReady || i == kBarKnReady || i == kBarNewRead;
       mbar_init(bar(i), i >= kBarGEmpty ? n_valid + 4 : rows ? n_valid : tiles ? 4 : 1);
@@ -507,7 +504,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       const int tb = j & 1, jp = j - fresh, s = jp & (kStages - 1);
       ok = (jp < 0 ? mbar_wait_warp(bar(kBarKnReady), 0, a.polls)
                    : mbar_wait_warp(bar(kBarKFull + s), (jp / kStages) & 1, a.polls)) &&
-           (j < 2 || mbar_wait_warp(bar((over ? kBarPvDone : kBarSEmpty) + tb), ((j >> 1) - 1) & 1, a.polls));
+           (j < 2 || mbar_wait_warp(bar(kBarPvDone + tb), ((j >> 1) - 1) & 1, a.polls));
       if (!ok) break;
       tc::fence_after_sync();
       const uint32_t tS = tmem + kColS + tb * kKeys;
@@ -540,7 +537,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       tc::fence_after_sync();
       const int depth = jp < 0 ? n_pad : min(kKeys, (w.k_end - w.k_begin - jp * kKeys + 15) & ~15);
       const uint64_t dV = dV0 + ((uint32_t)(tb * L::kVb) >> 4);
-      const uint32_t tP = tmem + (over ? kColS + tb * kKeys : kColP);
+      const uint32_t tP = tmem + kColS + tb * kKeys;
       if (tc::elect_one()) {
         if (depth == kKeys) {
 #pragma unroll
@@ -651,16 +648,9 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
           v[1] = *reinterpret_cast<const uint4 *>(src + code_off<HD>(32 * g + lane, k + 1));
           tc::st8(trow + L::kColQ + part * (HD / 4) + k * 4, reinterpret_cast<const uint32_t *>(v));
         }
-    } else if (!over) {                      // weights of the other copies' keys: zero for good
-      uint32_t z[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) z[e] = 0u;
-#pragma unroll
-      for (int c = 0; c < kKeys / 2; c += 16) tc::st16(trow + kColP + c, z);
     }
     tc::wait_st();
     tc::fence_before_sync();
-    pair_sync();                             // the zeros are there before the other warp's weights
     if (half == 0 && lane == 0) mbar_arrive(bar(kBarQReady));
     const uint64_t newvis = fresh ? kvq_visible(a, w.B, tau_s, tok) : 0ull;
     const uint32_t tO = trow + kColO;
@@ -675,7 +665,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     auto key_loop = [&](auto rc) {
       constexpr int RC = decltype(rc)::value;
       constexpr int KW = kKeys / (RC * kHalves);   // this warp's keys per block: 64, 32 or 16
-      constexpr bool OVER = RC < 4;
       const int k_lo = (kp * kHalves + half) * KW;
       // A warp whose wait gave up still meets its partner once, with a NaN in
       // the maximum's place (a maximum is never NaN), so both leave the loop.
@@ -716,8 +705,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         }
         tc::wait_ld();
         tc::fence_before_sync();
-        __syncwarp();
-        if (!OVER && ok && lane == 0) mbar_arrive(bar(kBarSEmpty + tb));
         // the row's maximum over both warps' keys
         float mx = -INFINITY;
         if (!whole) {                        // keys that do not count score -inf from here on
@@ -749,13 +736,20 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         const float theirs = both_s[(tb * kHalves + (half ^ 1)) * kRows];
         if (!ok || theirs != theirs) { ok = false; break; }
         mx = fmaxf(mx, theirs);
-        const uint32_t tW = trow + (OVER ? kColS + tb * kKeys : kColP);   // this row's weights
-        if (OVER) tc::fence_after_sync();    // both warps have their scores
-        if (RC == 2) {                       // zeros for half of the other copy's keys
-          uint32_t z[16];
+        // both warps have their scores: weights may go over them, zeros for the
+        // other copies' keys first (each warp half of them)
+        const uint32_t tW = trow + kColS + tb * kKeys;
+        tc::fence_after_sync();
+        if constexpr (RC > 1) {
+          uint32_t z[KW / 2];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) z[e] = 0u;
-          tc::st16(tW + (kp ^ 1) * (kKeys / 4) + half * 16, z);
+          for (int e = 0; e < KW / 2; ++e) z[e] = 0u;
+#pragma unroll
+          for (int c = 1; c < RC; ++c) {
+            const uint32_t at = tW + ((kp + c) % RC) * KW + half * (KW / 2);
+            if constexpr (KW == 16) tc::st8(at, z);
+            else tc::st16(at, z);
+          }
         }
         // reference: moves only when this block's max outgrows it
         const bool move = row_valid && mx > m_ref + kLift + kHeadroom;
@@ -779,21 +773,18 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
           }
           l = fmaf(sum.x + sum.y, inv[i], l);
         }
-        // O (and weights of their own columns) wait for the previous block's P V
-        const bool any = __any_sync(0xffffffffu, move);
-        if (j > 0 && (!OVER || any)) {
+        // O's rows may be scaled once the previous block's P V is done
+        if (__any_sync(0xffffffffu, move) && j > 0) {
           if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; continue; }
           tc::fence_after_sync();
-          if (any) {                         // this half of O's columns
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
-              uint32_t o[16];
-              tc::ld16(tO + half * (HD / 2) + 16 * c, o);
-              tc::wait_ld();
+          for (int c = 0; c < HD / 32; ++c) {  // this half of its columns
+            uint32_t o[16];
+            tc::ld16(tO + half * (HD / 2) + 16 * c, o);
+            tc::wait_ld();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-              tc::st16(tO + half * (HD / 2) + 16 * c, o);
-            }
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::st16(tO + half * (HD / 2) + 16 * c, o);
           }
         }
         const uint32_t tP = tW + k_lo / 2;

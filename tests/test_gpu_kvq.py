@@ -329,6 +329,22 @@ def test_verify_waves_and_cuts(dtype, lens):
     check(s, out)
 
 
+@pytest.mark.parametrize("B,Hq", [(16, 8), (8, 8), (4, 8), (12, 8)])
+def test_verify_many_blocks(B, Hq):
+    """Dozens of blocks a sequence, 128 to 32 rows: warps that drift apart, no wait that runs out, the same result twice."""
+    s = case(B, [4000 - 300 * i for i in range(12)] * 4, [B] * 48, "paired", "bf16", Hq, 2, 128)
+    dev = [t.cuda() for t in (s["q"], *s["c"].cuda(), s["kn"], s["vn"])]
+    out, ws = launch(s, dev)
+    for _ in range(20):
+        assert torch.equal(launch(s, dev, ws=ws)[0], out)
+    assert pkg.read_status(ws) == 0
+    few = slice(0, 3)                                     # against 64 bits: the first sequences
+    n = 2 * B * 3
+    t = dict(s, lens=s["lens"][few], cu=s["cu"][:4], q=s["q"][:n], kn=s["kn"][:n], vn=s["vn"][:n], tau=s["tau"][:3 * B],
+             table=s["table"][few])
+    check(t, out[:n])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_verify_strided_rows(dtype):
     """q, k and v inside fused rows."""
