@@ -12,7 +12,7 @@
 // shared memory once for all rows; a warp owns four rows, its lanes two keys
 // each for the scores and four columns each for the values.  It serves fp32
 // callers and checks; the FMA pipes and shared memory bound it.  One sequence
-// of 64 keys, 8 tokens, 4 heads of 64: 10.8 us (a launch and the chain set-up, new
+// of 64 keys, 8 tokens, 4 heads of 64: 10.3 us (a launch and the chain set-up, new
 // tile, one tile of the prompt, store; 14.1 with rows loaded element by
 // element).
 #include <limits.h>

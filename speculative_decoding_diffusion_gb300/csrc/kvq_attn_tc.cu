@@ -23,13 +23,13 @@
 // at K = 16; issued by one lane of a converged warp, whose addresses stay in
 // uniform registers, 33 to 43 cycles each -- from a branch of a single thread
 // it is 55 or more).  It takes 1400 cycles with up to 32 rows, 1700 with 64 and
-// 2280 with 128, where the softmax's chain (scores, maximum, exchange,
+// 2240 with 128, where the softmax's chain (scores, maximum, exchange,
 // exponentials, weights) bounds it, and a CTA 15 to 20 thousand cycles more:
 // set-up 3, angles 1.5, rows 2 to 5 (as much instruction fetch as work), the new
 // tokens' block 3.5, epilogue 3.  Measured, bf16, 32 heads on 8 of 128: 64
-// sequences of up to 4096 keys, one token each, 82 us (3.4 TB/s of its bytes);
+// sequences of up to 4096 keys, one token each, 81 us (3.4 TB/s of its bytes);
 // 64 of 4096, 64 rows a KV head, 148 us (3.8 TB/s, 460 TFLOP/s); 8 of 32768, 128
-// rows, 150 us (3.6 TB/s, 910 TFLOP/s); 256 of 256..8192 574 us (4.2 TB/s).
+// rows, 147 us (3.7 TB/s, 930 TFLOP/s); 256 of 256..8192 574 us (4.2 TB/s).
 //   warp 0       one 2 KB copy per page: keys by TMA, swizzled for the MMA,
 //                values as they lie
 //   warp 6       scales: page ids and scale bytes well ahead, what they mean
