@@ -478,6 +478,39 @@ def test_verify_two_graphs_and_streams():
         assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("seqs", [2, 50])
+def test_verify_captured_behind_copies_and_joins(dtype, seqs):
+    """In a graph right behind a copy, behind a join of two streams, and twice in a row: what an eager call gives."""
+    s = case(36, [100 - i for i in range(seqs)], [2] * seqs, "causal", dtype, 8, 8, 64)
+    q, *rest = [t.cuda() for t in (s["q"], *s["c"].cuda(), s["kn"], s["vn"])]
+    want, ws = launch(s, [q, *rest])
+    qs, outs = torch.zeros_like(q), [torch.zeros_like(want) for _ in range(3)]
+    table, lens, cu, spec = i32(s["table"]), i32(s["lens"]), i32(s["cu"]), pkg.rope_spec(**s["spec"])
+    wss = [torch.zeros_like(ws) for _ in range(2)]
+
+    def call(out, w):
+        pkg.kvq_verify(qs, *rest[:4], table, *rest[4:], None, lens, cu, out, w, 2 * seqs, 2, spec, s["scale"], order=ORDER["causal"])
+
+    graph, side, other = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        qs.copy_(q)
+        call(outs[0], wss[0])
+        other.wait_stream(side)
+        with torch.cuda.stream(other):
+            call(outs[1], wss[1])
+        call(outs[0], wss[0])
+        side.wait_stream(other)
+        call(outs[2], wss[0])
+        qs.zero_()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+    assert all(pkg.read_status(w) == 0 for w in wss)
+
+
 def test_append_and_verify_captured_in_several_waves():
     """Sequences taken by length, the last wave cut, in a graph behind the append that their last pages come from."""
     s = case(33, [397 - 8 * i for i in range(40)], [1] * 40, "causal", "bf16", 8, 8, 64)
