@@ -5,8 +5,9 @@
 // A copy with six operations per pair, so DRAM bounds it; the 64 angles of a
 // row are formed once and shared by its heads through shared memory, while the
 // heads' first vectors are already on their way (four pairs of 16 bytes a
-// thread).  262144 rows of 32 + 8 heads of 128, bf16: 0.91 ms, 5.9 TB/s of its
-// bytes, 0.87 of a plain copy's rate; 128 rows of 32 heads, fp32: 3.0 us.
+// thread).  262144 rows of 32 + 8 heads of 128, bf16: 0.83 ms, 6.5 TB/s of its
+// bytes, 0.95 of a plain copy's rate (0.91 ms with the angles in plain order,
+// where the lanes that read them met in the same banks); 128 rows of 32 heads, fp32: 3.0 us.
 #include <math.h>
 #include <string.h>
 
@@ -111,7 +112,7 @@ template <typename T, bool IL, bool VEC>
 __global__ void __launch_bounds__(kThreads, 3)
 rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int N = VEC ? 16 / (int)sizeof(T) : 1;   // elements of a vector
-  __shared__ float2 cs_s[kMaxRows][64];
+  __shared__ __align__(16) float2 cs_s[kMaxRows][64];  // placed by angle_at
   const int row0 = blockIdx.x * a.rows_per_cta;
   const int n_rows = min(a.rows_per_cta, a.rows - row0);
   const int half = a.plan.half;
@@ -162,7 +163,7 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
     if (d < half) {
       float2 cs = rope_plan_cs(plan_by_lane(a.plan), d, __ldg(a.pos + row0 + r));
       if (a.inverse) cs.y = -cs.y;
-      cs_s[r][d] = cs;
+      cs_s[r][angle_at(d)] = cs;
     }
   }
   __syncthreads();
@@ -181,18 +182,25 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
       load_vec<T, N>(reinterpret_cast<const T *>(&u[k]), x);
       load_vec<T, N>(reinterpret_cast<const T *>(&v[k]), y);
       if (!IL) {
-        if (turn1) {
+        if (turn1 && N == 1) {
+          const float2 w = cs[angle_at(d1)];
+          const float x1 = x[0], x2 = y[0];
+          x[0] = x1 * w.x - x2 * w.y;
+          y[0] = x2 * w.x + x1 * w.y;
+        } else if (turn1) {
 #pragma unroll
-          for (int j = 0; j < N; ++j) {
-            const float2 w = cs[d1 + j];
-            const float x1 = x[j], x2 = y[j];
+          for (int j = 0; j + 1 < N; j += 2) {
+            const float4 w = *reinterpret_cast<const float4 *>(cs + angle_at(d1 + j));
+            const float x1 = x[j], x2 = y[j], x3 = x[j + 1], x4 = y[j + 1];
             x[j] = x1 * w.x - x2 * w.y;
             y[j] = x2 * w.x + x1 * w.y;
+            x[j + 1] = x3 * w.z - x4 * w.w;
+            y[j + 1] = x4 * w.z + x3 * w.w;
           }
         }
       } else if (N == 1) {                           // the pair itself
         if (turn1) {
-          const float2 w = cs[d1 >> 1];
+          const float2 w = cs[angle_at(d1 >> 1)];
           const float x1 = x[0], x2 = y[0];
           x[0] = x1 * w.x - x2 * w.y;
           y[0] = x2 * w.x + x1 * w.y;
@@ -203,11 +211,13 @@ rope_kernel(const __grid_constant__ RopeArgs a) {
           float *z = s ? y : x;
           if (!(s ? turn2 : turn1)) continue;
 #pragma unroll
-          for (int j = 0; j + 1 < N; j += 2) {
-            const float2 w = cs[((s ? d2 : d1) + j) >> 1];
-            const float x1 = z[j], x2 = z[j + 1];
+          for (int j = 0; j + 3 < N; j += 4) {
+            const float4 w = *reinterpret_cast<const float4 *>(cs + angle_at(((s ? d2 : d1) + j) >> 1));
+            const float x1 = z[j], x2 = z[j + 1], x3 = z[j + 2], x4 = z[j + 3];
             z[j] = x1 * w.x - x2 * w.y;
             z[j + 1] = x2 * w.x + x1 * w.y;
+            z[j + 2] = x3 * w.z - x4 * w.w;
+            z[j + 3] = x4 * w.z + x3 * w.w;
           }
         }
       }
@@ -268,8 +278,8 @@ extern "C" simsd_status simsd_rope(const simsd_rope_desc *d, void *stream) {
   a.hd = d->head_dim;
   a.inverse = d->inverse;
   // as many rows a CTA (up to four: an angle per thread) as leave every SM one
-  // (40 heads of 128, bf16, in CTAs of one / four rows: 152 rows 3.1 / 4.6 us, 608
-  // 5.7 / 4.6, 9728 56 / 42, 65536 347 / 235)
+  // (40 heads of 128, bf16, in CTAs of one / four rows: 152 rows 2.9 / 4.1 us, 608
+  // 4.9 / 4.1, 9728 51 / 37, 65536 321 / 214)
   a.rows_per_cta = std::min(kMaxRows, std::max(1, d->rows / device_sm_count()));
   a.inv_heads = (uint32_t)(((1ull << 32) + a.heads - 1) / a.heads);
   const cudaError_t e = d->dtype == SIMSD_BF16 ? launch_rope<__nv_bfloat16>(a, vec, (cudaStream_t)stream)
