@@ -54,19 +54,9 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
-static bool encode_cache_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd, bool codes) {
+static bool encode_cache_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
-  if (codes) {   // one byte an element; a box is a page of a head, its rows whole
-    cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)kPageTokens, (cuuint64_t)Hkv, (cuuint64_t)num_pages};
-    cuuint64_t strides[3] = {(cuuint64_t)hd, (cuuint64_t)kPageTokens * hd, (cuuint64_t)Hkv * kPageTokens * hd};
-    cuuint32_t box[4] = {(cuuint32_t)hd, (cuuint32_t)kPageTokens, 1, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, ptr, dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-  }
   cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)kPageTokens, (cuuint64_t)Hkv,
                         (cuuint64_t)num_pages};
   cuuint64_t strides[3] = {(cuuint64_t)hd * 2, (cuuint64_t)kPageTokens * hd * 2,
@@ -80,15 +70,27 @@ static bool encode_cache_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, 
 }
 
 
+bool make_codes_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)kPageTokens, (cuuint64_t)Hkv, (cuuint64_t)num_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)hd, (cuuint64_t)kPageTokens * hd, (cuuint64_t)Hkv * kPageTokens * hd};
+  cuuint32_t box[4] = {(cuuint32_t)hd, (cuuint32_t)kPageTokens, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, ptr, dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE,
+            hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int current_device() {
   int dev = -1;
   return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
 }
 
-bool make_cache_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd, bool codes) {
+bool make_cache_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd) {
   struct Entry {
     int dev, num_pages, Hkv, hd;
-    bool codes;
     void *ptr;
     CUtensorMap map;
   };
@@ -99,15 +101,14 @@ bool make_cache_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd, b
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < used; ++i) {
     const Entry &e = cache[i];
-    if (e.dev == dev && e.ptr == ptr && e.num_pages == num_pages && e.Hkv == Hkv && e.hd == hd &&
-        e.codes == codes) {
+    if (e.dev == dev && e.ptr == ptr && e.num_pages == num_pages && e.Hkv == Hkv && e.hd == hd) {
       *m = e.map;
       return true;
     }
   }
-  if (!encode_cache_map(m, ptr, num_pages, Hkv, hd, codes)) return false;
+  if (!encode_cache_map(m, ptr, num_pages, Hkv, hd)) return false;
   Entry &e = cache[next];
-  e.dev = dev; e.ptr = ptr; e.num_pages = num_pages; e.Hkv = Hkv; e.hd = hd; e.codes = codes; e.map = *m;
+  e.dev = dev; e.ptr = ptr; e.num_pages = num_pages; e.Hkv = Hkv; e.hd = hd; e.map = *m;
   next = (next + 1) % 16;
   if (used < 16) ++used;
   return true;

@@ -119,9 +119,11 @@ int device_sm_count();
 // (128 bytes) wide, 128-byte swizzle.  False if the CUDA driver's tensor-map
 // encoding fails.  Descriptors are cached per (device, pointer, sizes):
 // repeated calls on the same cache encode nothing.
-// codes: the e4m3 cache instead, one box = one page of one head, its rows
-// whole (128- or 64-byte swizzle by head_dim).
-bool make_cache_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd, bool codes = false);
+bool make_cache_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd);
+
+// Descriptor of an e4m3 cache: one box = one page of one head, its rows whole
+// (128- or 64-byte swizzle by head_dim).  Made anew by each call.
+bool make_codes_map(CUtensorMap *m, void *ptr, int num_pages, int Hkv, int hd);
 
 // Records `event` (a cudaEvent_t, may be NULL) on `stream`; under stream
 // capture it becomes an event-record node of the graph, so a replayed graph

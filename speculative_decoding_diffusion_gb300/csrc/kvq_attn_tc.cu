@@ -935,7 +935,7 @@ cudaError_t launch_tc_hd(const CUtensorMap &mk, const KvqPlan &p, const KvqParam
 cudaError_t launch_kvq_tc(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                           cudaStream_t stream) {
   CUtensorMap mk;
-  if (!make_cache_map(&mk, const_cast<void *>(d->k_cache), d->num_pages, d->num_kv_heads, d->head_dim, true))
+  if (!make_codes_map(&mk, const_cast<void *>(d->k_cache), d->num_pages, d->num_kv_heads, d->head_dim))
     return cudaErrorInvalidValue;
   return d->head_dim == 128 ? launch_tc_hd<128>(mk, p, a, stream) : launch_tc_hd<64>(mk, p, a, stream);
 }
