@@ -14,8 +14,9 @@
 // key or value.  M is at most 8 stale, so p <= 2^15 fits f16, whose 11 bits
 // keep the error against 64 bits at 1.9e-3 of the result, 1.7e-3 of it the
 // output's own rounding (bf16 weights: 2.5e-3).  The new tokens are a block of
-// their own ahead of the prompt: keys rotated and split here, values as f16
-// relative to a power of two that is their ve.
+// their own ahead of the prompt: keys rotated and split here relative to a power
+// of two of each token's, values as f16 relative to another that is the token's
+// ve, so that no token's size reaches a row that does not see it.
 // One CTA per (key split, KV head x 128-row tile, sequence); rows stack new
 // tokens x heads of the group, so a cache byte is read once for all of them.
 // A 128-key block is 32 KB, 1410 cycles of an SM's share of the HBM rate, and
@@ -112,9 +113,11 @@ struct Smem {
   static constexpr int kOffTau = kOffBar + (kNumBars + 1) / 2 * 16;
   static constexpr int kOffRow = kOffTau + kMaxB * 4;       // rows' score factors
   static constexpr int kOffMax = kOffRow + kRows * 4;       // [2 blocks][2 halves][4 quadrants][32]: row maxima, sums
-  static constexpr int kOffScales = kOffMax + 2 * kHalves * kRows * 4;
-  static constexpr int kOffMisc = kOffScales + kGroupSlots * (int)sizeof(Scales);   // tmem address, error flag, largest
-                                                            // new |k| and |v|, odd new values
+  static constexpr int kOffNewKv = kOffMax + 2 * kHalves * kRows * 4;       // new tokens: 2^ke and ve of each,
+  static constexpr int kOffNewInv = kOffNewKv + kKeys * 8;                  // and 2^-ve (zeros past the last)
+  static constexpr int kOffScales = kOffNewInv + kKeys * 4;
+  static constexpr int kOffMisc = kOffScales + kGroupSlots * (int)sizeof(Scales);   // tmem address, error flag, odd new
+                                                            // values
   static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;              // 1024-byte alignment slack
   static constexpr uint32_t kColQ = kColO + HD;             // q hi and lo: hd / 4 columns each
@@ -137,6 +140,14 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// 16 bytes of shared memory, read where it stands (a run of reads ahead of
+// their use would not leave registers for the scores).
+__device__ __forceinline__ float4 load_shared4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
 }
 
 template <int V> struct IntC { static constexpr int value = V; };
@@ -216,8 +227,10 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sb + L::kOffMisc);
   int *flag_s = reinterpret_cast<int *>(sb + L::kOffMisc + 4);
   float *row_s = reinterpret_cast<float *>(sb + L::kOffRow);
-  uint32_t *amax_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new keys, values
-  uint32_t *odd_s = amax_s + 2;              // new tokens whose values hold a NaN or an infinity, one bit each
+  uint32_t *odd_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new tokens whose values hold a NaN or an
+                                                                          // infinity, one bit each
+  float2 *new_kv_s = reinterpret_cast<float2 *>(sb + L::kOffNewKv);
+  float *new_inv_s = reinterpret_cast<float *>(sb + L::kOffNewInv);
   Scales *scales_s = reinterpret_cast<Scales *>(sb + L::kOffScales);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 1) {
@@ -300,7 +313,11 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     }
     if (lane == 0) {
       *flag_s = 0;
-      amax_s[0] = amax_s[1] = odd_s[0] = odd_s[1] = 0u;
+      odd_s[0] = odd_s[1] = 0u;
+    }
+    for (int i = lane; i < kKeys; i += 32) {
+      new_kv_s[i] = make_float2(0.f, 0.f);
+      new_inv_s[i] = 0.f;
     }
     fence_barrier_init();
   }
@@ -310,10 +327,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   const uint32_t tmem = *tmem_slot;
   int issued = 0;                            // producers: blocks whose loads were started
   float2 *cs_s = reinterpret_cast<float2 *>(sb + L::kOffVb + L::kVb);   // [kMaxNew][HD / 2]
-  // powers of two that the new tokens' keys and values are taken relative to:
-  // rotated elements stay below sqrt 2 of the largest
-  auto new_kexp = [&]() { return scale_exponent(__uint_as_float(amax_s[0]) * a.plan.mul * 1.41422f, -64, 119); };
-  auto new_vexp = [&]() { return scale_exponent(__uint_as_float(amax_s[1]), -64, 119); };
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
   // The softmax and decode warps together rotate the query rows into two e4m3
   // parts and, in the CTA that owns the new tokens, their keys likewise (the
@@ -335,27 +348,29 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     if (a.order == SIMSD_ORDER_PAIRED && pt < w.B) tau_s[pt] = __ldg(a.tau + w.c0 + pt);
     copy_async_wait_all();
     const __nv_bfloat16 *ks = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew), *vs = ks + kMaxNew * HD;
-    if (fresh) {                             // the largest finite magnitudes (of what this thread copied)
-      float ka = 0.f, va = 0.f;
+    if (fresh) {                             // each token's ve: its largest finite value (CH lanes hold its row, each
+                                             // the chunk that it copied itself)
 #pragma unroll 1
-      for (int e = pt; e < w.n * CH; e += kPrep) {
-        float x[8], y[8];
-        load_vec<__nv_bfloat16, 8>(ks + e * 8, x);
-        load_vec<__nv_bfloat16, 8>(vs + e * 8, y);
-        bool odd = false;
+      for (int e = pt; e - lane < w.n * CH; e += kPrep) {
+        float va = 0.f;
+        if (e < w.n * CH) {
+          float y[8];
+          load_vec<__nv_bfloat16, 8>(vs + e * 8, y);
+          bool odd = false;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          odd |= !(fabsf(y[i]) < INFINITY);
-          ka = fmaxf(ka, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
-          va = fmaxf(va, fabsf(y[i]) < INFINITY ? fabsf(y[i]) : 0.f);
+          for (int i = 0; i < 8; ++i) {
+            odd |= !(fabsf(y[i]) < INFINITY);
+            va = fmaxf(va, fabsf(y[i]) < INFINITY ? fabsf(y[i]) : 0.f);
+          }
+          if (odd) atomicOr(odd_s + (e / CH >> 5), 1u << (e / CH & 31));
         }
-        if (odd) atomicOr(odd_s + (e / CH >> 5), 1u << (e / CH & 31));
-      }
-      const uint32_t kb = __reduce_max_sync(0xffffffffu, __float_as_uint(ka));
-      const uint32_t vb = __reduce_max_sync(0xffffffffu, __float_as_uint(va));
-      if (lane == 0) {
-        atomicMax(amax_s, kb);
-        atomicMax(amax_s + 1, vb);
+#pragma unroll
+        for (int m = CH / 2; m > 0; m >>= 1) va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, m));
+        if (e < w.n * CH && e % CH == 0) {
+          const int ve = scale_exponent(va, -64, 119);
+          new_kv_s[e / CH].y = (float)ve;
+          new_inv_s[e / CH] = pow2i(-ve);
+        }
       }
     }
     named_sync(1, kPrep);
@@ -364,7 +379,6 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     constexpr int PL = HD / 16;
     const __nv_bfloat16 *qs = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffVb);
     const int n_q = n_groups * 32 * PL, n_all = n_q + (fresh ? n_pad * PL : 0);   // zeros up to the MMA's depth
-    const float kdown = fresh ? pow2i(-new_kexp()) : 0.f;
 #pragma unroll 1
     for (int e = pt; e < n_all; e += kPrep) {
       const bool query = e < n_q;
@@ -381,25 +395,27 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       const int row = w.row0 + r;
       const int tok = !query ? min(r, w.n - 1) : row < w.M ? div_by(row, a.by_G) : 0;
       int c0, c1;
-      float x[16], down = kdown;
+      float x[16], amax = 0.f, nan = 0.f;
       rotate16(a.plan, cs_s + kvq_offset(a, w.B, tok) * (HD / 2), query ? qs + r * HD : ks + tok * HD, c, c0, c1, x);
-      if (query) {
-        float amax = 0.f, nan = 0.f;         // a NaN or an infinity: the row's scores become NaN
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          nan = fmaf(x[i], 0.f, nan);
-          amax = fmaxf(amax, fabsf(x[i]));
-        }
-#pragma unroll
-        for (int m = PL / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
-        const uint32_t odds = (__ballot_sync(0xffffffffu, nan != 0.f) >> (lane & ~(PL - 1))) & ((1u << PL) - 1u);
-        const int qe = scale_exponent(amax, -100, 119);
-        down = pow2i(-qe);
-        if (c == 0) row_s[r] = odds != 0u ? __uint_as_float(0x7fc00000u) : a.scale * pow2i(qe);
-      } else {
+      if (!query) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)         // e4m3 has no infinity
           x[i] = r >= w.n ? 0.f : fabsf(x[i]) < INFINITY ? x[i] : __uint_as_float(0x7fc00000u);
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {         // (a NaN is not the maximum)
+        nan = fmaf(x[i], 0.f, nan);
+        amax = fmaxf(amax, fabsf(x[i]));
+      }
+#pragma unroll
+      for (int m = PL / 2; m > 0; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+      // a NaN or an infinity: the query row's scores become NaN
+      const uint32_t odds = (__ballot_sync(0xffffffffu, nan != 0.f) >> (lane & ~(PL - 1))) & ((1u << PL) - 1u);
+      const int ex = scale_exponent(amax, -100, 119);
+      const float down = pow2i(-ex);
+      if (c == 0) {
+        if (query) row_s[r] = odds != 0u ? __uint_as_float(0x7fc00000u) : a.scale * pow2i(ex);
+        else if (r < w.n) new_kv_s[r].x = pow2i(ex);
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) x[i] *= down;
@@ -559,10 +575,10 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     if (fresh) {                             // the new values, as f16, are the first value tile
       if (lane == 0) mbar_arrive(bar(kBarKnReady));
       const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew) + kMaxNew * HD;
-      const float vdown = pow2i(-new_vexp());
 #pragma unroll 1
       for (int e = 32 * dw + lane; e < n_pad * CH; e += 128) {
         const int j = e / CH, c = e % CH;
+        const float vdown = new_inv_s[j];
         float v[8];
         load_vec<__nv_bfloat16, 8>(vs + e * 8, v);
 #pragma unroll
@@ -659,18 +675,18 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     float m_ref = -INFINITY, l = odd ? __uint_as_float(0x7fc00000u) : 0.f;
     bool ok = true;
     int j = 0;
-    const float new_scale = fresh ? rscale * pow2i(new_kexp()) : 0.f;
-    const float new_ve = fresh ? (float)new_vexp() : 0.f, new_inv = fresh ? pow2i(-new_vexp()) : 1.f;
-    // the key loop, compiled once per copy count
+    // the key loop, compiled once per copy count, the new tokens' block by itself
+    // (a factor and a ve for each key: in the loop they would not leave it its
+    // registers, 64 x 4096 keys 171 us and not 148)
     auto key_loop = [&](auto rc) {
       constexpr int RC = decltype(rc)::value;
       constexpr int KW = kKeys / (RC * kHalves);   // this warp's keys per block: 64, 32 or 16
       const int k_lo = (kp * kHalves + half) * KW;
       // A warp whose wait gave up still meets its partner once, with a NaN in
       // the maximum's place (a maximum is never NaN), so both leave the loop.
-      for (; warp_valid && j < n_blocks; ++j) {
-        const int tb = j & 1, jp = j - fresh;
-        const bool is_new = jp < 0;
+      auto block = [&](auto newc) {            // block j; false: leave the loop
+        constexpr bool is_new = decltype(newc)::value != 0;
+        const int tb = is_new ? 0 : j & 1, jp = is_new ? -1 : j - fresh;
         const uint32_t tS = trow + kColS + tb * kKeys + k_lo;
         const int q = jp & (kGroup - 1), slot = jp / kGroup % kGroupSlots;
         if (!is_new && q == 0) ok = ok && mbar_wait_warp(bar(kBarGFull + slot), (jp / (kGroup * kGroupSlots)) & 1, a.polls);
@@ -678,9 +694,9 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         constexpr int NP = KW / 16;
         float f[NP], ve[NP], inv[NP];
         uint32_t gone = 0u;
-        if (is_new) {
+        if (is_new) {                        // (a factor and a ve for each key, below)
 #pragma unroll
-          for (int i = 0; i < NP; ++i) { f[i] = new_scale; ve[i] = new_ve; inv[i] = new_inv; }
+          for (int i = 0; i < NP; ++i) { f[i] = 1.f; ve[i] = 0.f; inv[i] = 0.f; }
         } else {
           const Scales &sc = scales_s[slot];
           const int e0 = 8 * q + k_lo / 16;
@@ -708,19 +724,24 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         // the row's maximum over both warps' keys
         float mx = -INFINITY;
         if (!whole) {                        // keys that do not count score -inf from here on
-          uint64_t vis;
           if (is_new) {
-            vis = shift_right(newvis, k_lo);
+            const uint64_t vis = shift_right(newvis, k_lo);
+#pragma unroll
+            for (int i = 0; i < KW; i += 2) {
+              const float4 x = load_shared4(base + L::kOffNewKv + (k_lo + i) * 8);   // of two keys
+              sr[i] = __float_as_uint((vis >> i) & 1ull ? fmaf(__uint_as_float(sr[i]), x.x * rscale, x.y) : -INFINITY);
+              sr[i + 1] = __float_as_uint((vis >> i) & 2ull ? fmaf(__uint_as_float(sr[i + 1]), x.z * rscale, x.w) : -INFINITY);
+            }
           } else {
-            vis = kvq_low_bits(valid - k_lo);
+            uint64_t vis = kvq_low_bits(valid - k_lo);
             for (int i = 0; i < KW / 16; ++i)
               if ((gone >> (k_lo / 16 + i)) & 1u) vis &= ~(0xffffull << (16 * i));
+#pragma unroll
+            for (int i = 0; i < KW; ++i)
+              sr[i] = __float_as_uint((vis >> i) & 1ull ? fmaf(__uint_as_float(sr[i]), f[i / 16], ve[i / 16]) : -INFINITY);
+#pragma unroll
+            for (int i = 0; i < NP; ++i) { f[i] = 1.f; ve[i] = 0.f; }
           }
-#pragma unroll
-          for (int i = 0; i < KW; ++i)
-            sr[i] = __float_as_uint((vis >> i) & 1ull ? fmaf(__uint_as_float(sr[i]), f[i / 16], ve[i / 16]) : -INFINITY);
-#pragma unroll
-          for (int i = 0; i < NP; ++i) { f[i] = 1.f; ve[i] = 0.f; }
         }
 #pragma unroll
         for (int i = 0; i < KW; i += 16) {
@@ -734,7 +755,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         both_s[(tb * kHalves + half) * kRows] = ok ? mx : __uint_as_float(0x7fc00000u);
         pair_sync();
         const float theirs = both_s[(tb * kHalves + (half ^ 1)) * kRows];
-        if (!ok || theirs != theirs) { ok = false; break; }
+        if (!ok || theirs != theirs) { ok = false; return false; }
         mx = fmaxf(mx, theirs);
         // both warps have their scores: weights may go over them, zeros for the
         // other copies' keys first (each warp half of them)
@@ -759,6 +780,16 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         m_ref = m_new;
         // weights 2^(t - m_ref) as f16 pairs
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
+        if (is_new) {                        // the new tokens' share of the sum, key by key
+#pragma unroll
+          for (int i = 0; i < KW; i += 4) {
+            const float4 x = load_shared4(base + L::kOffNewInv + (k_lo + i) * 4);
+            l = fmaf(ex2(__uint_as_float(sr[i]) - mu), x.x, l);
+            l = fmaf(ex2(__uint_as_float(sr[i + 1]) - mu), x.y, l);
+            l = fmaf(ex2(__uint_as_float(sr[i + 2]) - mu), x.z, l);
+            l = fmaf(ex2(__uint_as_float(sr[i + 3]) - mu), x.w, l);
+          }
+        }
         uint32_t pw[KW / 2];
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -774,8 +805,8 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
           l = fmaf(sum.x + sum.y, inv[i], l);
         }
         // O's rows may be scaled once the previous block's P V is done
-        if (__any_sync(0xffffffffu, move) && j > 0) {
-          if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; continue; }
+        if (!is_new && __any_sync(0xffffffffu, move) && j > 0) {
+          if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; return true; }
           tc::fence_after_sync();
 #pragma unroll 1
           for (int c = 0; c < HD / 32; ++c) {  // this half of its columns
@@ -801,7 +832,15 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
           mbar_arrive(bar(kBarPFull + tb));   // (one for each parity: a warp may be a block ahead of another)
           if (!is_new && (q == kGroup - 1 || jp == n_past - 1)) mbar_arrive(bar(kBarGEmpty + slot));
         }
+        return true;
+      };
+      if (!warp_valid) return;
+      if (fresh) {
+        if (!block(IntC<1>{})) return;
+        j = 1;
       }
+      for (; j < n_blocks; ++j)
+        if (!block(IntC<0>{})) return;
     };
     if (R == 4) key_loop(IntC<4>{});
     else if (R == 2) key_loop(IntC<2>{});

@@ -1,0 +1,53 @@
+"""simsd_kvq_append and simsd_kvq_verify at the ends of what their header
+allows.  Tolerances as in test_gpu_kvq (kvq_ref.verify's bound); what must
+not change is compared bit by bit."""
+import pytest
+import torch
+
+import kvq_ref as ref
+import speculative_decoding_diffusion_gb300 as pkg
+from test_gpu_kvq import DT, case, check, launch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("order,B,Hq,hd", [("paired", 4, 4, 128), ("causal", 64, 2, 128), ("nodes", 40, 6, 64), ("causal", 3, 8, 64)])
+@pytest.mark.parametrize("size", [2.0 ** 12, 1e8, 1e12, 3e38])
+def test_verify_finite_outliers_change_no_row_that_does_not_see_them(dtype, order, B, Hq, hd, size):
+    """A token's keys and values times `size` (3e38: as large as that): the same bits in the rows that do not see it,
+    and in the others what the definition gives."""
+    node = 8 if order == "nodes" else 0
+    s = case(61, [50, 0], [B, B], order, dtype, Hq, 2, hd, node)
+    clean = launch(s)[0].cpu()
+    n = 2 * B if order == "paired" else B
+    at = {0: 1, 1: n - 1}                                 # a token of each sequence; head 0 of it, head 1
+
+    def grow(x):
+        return (x.sign() * size if size > 1e30 else x * size).to(x.dtype)
+
+    for b, token in at.items():
+        for t in (s["kn"], s["vn"]):
+            t[b * n + token, b] = grow(t[b * n + token, b])
+    out, ws = launch(s)
+    assert pkg.read_status(ws) == 0
+    if size < 1e30:                                       # (a key of 3e38 leaves fp32 where it is seen)
+        check(s, out)
+    out = out.cpu()
+    for b, token in at.items():
+        tau = s["tau"][b * B:(b + 1) * B] if order == "paired" else None
+        sees = ref.visible(order, B, tau, node)[:, token]
+        rows = slice(b * n, (b + 1) * n)
+        mine, other = (slice(h * Hq // 2, (h + 1) * Hq // 2) for h in (b, 1 - b))
+        assert 0 < int(sees.sum()) < n
+        assert torch.equal(out[rows, mine][~sees], clean[rows, mine][~sees])
+        assert torch.equal(out[rows, other], clean[rows, other])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_keys_of_every_size_side_by_side(dtype):
+    """New keys from 2^-20 to 2^10 of the usual, all seen: the small ones count with their own scores."""
+    s = case(62, [0], [8], "nodes", dtype, 4, 2, 128, 8)
+    s["kn"] = (s["kn"].float() * torch.exp2(torch.tensor([-20., -10., -4., 0., 0., 3., 10., -1.]))[:, None, None]).to(DT[dtype])
+    out, _ = launch(s)
+    check(s, out)
