@@ -159,8 +159,9 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
   }
   // slots of the new tokens
   if (a.slots != nullptr && a.cu_n != nullptr) {
-    const int end = min(a.total_n, C[a.batch]);
-    for (int t = t0; t < end; t += step) {
+    const uint32_t end = (uint32_t)max(0, min(a.total_n, C[a.batch]));
+    for (uint32_t u = t0; u < end; u += step) {    // (unsigned: a step past the last token may pass 2^31)
+      const int t = (int)u;
       const int b = find_seq_smem(C, a.batch, t);
       const Seq s = seq(b);
       if (!s.rows_ok || t < s.c0 || t >= s.c0 + s.n) continue;
