@@ -574,7 +574,7 @@ simsd_status simsd_rope(const simsd_rope_desc *d, void *stream);
  *   - need_b < held[b]: the entries need_b.. go to the ring's end, in the
  *     order of the sequences (a finished request: lens = n = 0);
  *   - slots[t] = page * 16 + offset of token t = cu_n[b] + i, at position
- *     lens[b] + i.  Tokens past cu_n[batch] are left as they were.
+ *     lens[b] + i.  Tokens of no sequence's range are left as they were.
  * The ring: free_pages[(head + i) mod num_pages], i < count; queue holds
  * {head, count}.  Pages held and free together are at most num_pages.
  *   lens       device int32[batch]
@@ -587,12 +587,13 @@ simsd_status simsd_rope(const simsd_rope_desc *d, void *stream);
  *   served     device int32[batch] out
  *   slots      device int64[total_n] out, or NULL
  * A sequence whose numbers are out of range (lens < 0, lens + n_b >= 2^31,
- * need_b or held outside 0..max_pages_per_seq, a cu_n range outside
- * 0..total_n) sets the
- * bad-input bit, is not served and is left unchanged (its slots, where its
- * cu_n range is valid, are -1); a ring out of range (head, count, or more
- * free and given back pages than num_pages) sets it and serves none.  A free
- * page id outside 0..num_pages-1 sets it and is handed on as it is.
+ * need_b or held outside 0..max_pages_per_seq, a cu_n range that falls or
+ * lies outside 0..total_n) sets the bad-input bit, is not served and is left
+ * unchanged (its slots, where its cu_n range is valid, are -1); the others
+ * are served all the same (a token in the ranges of two has the later one's
+ * slot).  A ring out of range (head, count, or more free and given back pages
+ * than num_pages) sets the bit and serves none.  A free page id outside
+ * 0..num_pages-1 sets it and is handed on as it is.
  * Limits: batch <= 16384; batch * max_pages_per_seq < 2^31; num_pages < 2^30.
  * Workspace: 256 bytes (status word and a counter that each call leaves at
  * zero), one for each call that may run at the same time as another.

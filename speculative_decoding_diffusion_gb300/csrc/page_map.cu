@@ -73,7 +73,7 @@ __device__ __forceinline__ int last_not_above(const int *p, int n, int g) {
 
 __device__ __forceinline__ int wrap(int64_t i, int cap) { return (int)(i >= cap ? i - cap : i); }
 
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
 page_map_kernel(const __grid_constant__ MapArgs a) {
   extern __shared__ int32_t smem[];
   const int n1 = a.batch + 1;
@@ -90,7 +90,7 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
   const int head = __ldcg(a.queue), count = __ldcg(a.queue + 1);
   // scan of (grow | drop << 32), a chunk of kThreads sequences at a time
   uint64_t carry = 0;
-  bool bad = false;
+  bool bad = false, torn = false;
   for (int b0 = 0; b0 < a.batch; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
     uint64_t x = 0;
@@ -105,6 +105,7 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
       }
       const Seq s = make_seq(a, len, held, c0, c1);
       bad |= !s.ok;
+      torn |= !s.rows_ok;
       x = (uint64_t)(uint32_t)max(0, s.need - s.held) | (uint64_t)(uint32_t)max(0, s.held - s.need) << 32;
     }
     uint64_t incl = x;
@@ -134,7 +135,7 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
     D[a.batch] = wanted;
     E[a.batch] = dropped;
   }
-  __syncthreads();
+  const bool falls = __syncthreads_or(torn);     // cu_n is no prefix sum: it cannot be searched
   const bool ring_ok = head >= 0 && head < a.cap && count >= 0 && count <= a.cap &&
                        (int64_t)count + dropped <= a.cap;
   if ((bad || !ring_ok) && blockIdx.x == 0) raise_status(a.status, kStatusBadInput);
@@ -159,12 +160,7 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
   }
   // slots of the new tokens
   if (a.slots != nullptr && a.cu_n != nullptr) {
-    const uint32_t end = (uint32_t)max(0, min(a.total_n, C[a.batch]));
-    for (uint32_t u = t0; u < end; u += step) {    // (unsigned: a step past the last token may pass 2^31)
-      const int t = (int)u;
-      const int b = find_seq_smem(C, a.batch, t);
-      const Seq s = seq(b);
-      if (!s.rows_ok || t < s.c0 || t >= s.c0 + s.n) continue;
+    auto put = [&](int t, int b, const Seq &s) {
       const bool served = ring_ok && s.ok && (s.need <= s.held || D[b + 1] <= count);
       int64_t slot = -1;
       if (served) {
@@ -174,6 +170,21 @@ page_map_kernel(const __grid_constant__ MapArgs a) {
         slot = (int64_t)page * kPage + pos % kPage;
       }
       a.slots[t] = slot;
+    };
+    if (!falls) {
+      const uint32_t end = (uint32_t)max(0, min(a.total_n, C[a.batch]));
+      for (uint32_t u = t0; u < end; u += step) {  // (unsigned: a step past the last token may pass 2^31)
+        const int t = (int)u, b = find_seq_smem(C, a.batch, t);
+        const Seq s = seq(b);
+        if (t >= s.c0 && t < s.c0 + s.n) put(t, b, s);
+      }
+    } else {                                       // every valid range by itself, a token always by the same thread:
+      for (int b = 0; b < a.batch; ++b) {          // where two claim it, the later sequence has it
+        const Seq s = seq(b);
+        if (!s.rows_ok) continue;
+        const uint32_t skip = s.c0 > t0 ? ((uint32_t)(s.c0 - t0) + step - 1) / (uint32_t)step : 0u;
+        for (uint32_t u = t0 + skip * step; u < (uint32_t)(s.c0 + s.n); u += step) put((int)u, b, s);
+      }
     }
   }
   // the new state, once every CTA has read the old one
