@@ -625,7 +625,9 @@ simsd_status simsd_page_map(const simsd_page_map_desc *d, void *stream);
  * The 8-bit cache.  k_cache, v_cache: device e4m3 [num_pages][Hkv][16][hd];
  * k_scale, v_scale: device uint8 [num_pages][Hkv], the exponent of a page
  * and head's scale plus 127 (an e8m0 value): a stored code c stands for
- * c * 2^(scale - 127).  Exponents lie in -64..7, so magnitudes up to 57344;
+ * c * 2^(scale - 127).  The append's exponents lie in -64..7, so magnitudes up
+ * to 57344 (an older byte beyond them is brought into the range); the
+ * attention takes every byte as what it stands for.
  * 255 marks a page and head that got a NaN or an infinity: every value of it
  * reads as NaN.  A power of two changes no mantissa, so a page whose scale
  * grows keeps its older codes' values (those of the few smallest binades are

@@ -490,10 +490,10 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
       }
       Scales &s = scales_s[slot];
       const uint32_t missing = __ballot_sync(0xffffffffu, kb == kNoPage);
-      const int ve = min(vb - kScaleBias, kExpHi);
+      const int ve = vb - kScaleBias;
       const bool nan = vb < 0 || vb == kScaleNan;
       s.kv[lane] = make_float2(scale_value(kb & 255), nan ? __uint_as_float(0x7fc00000u) : (float)ve);
-      s.inv[lane] = pow2i(nan ? 0 : min(-ve, 127));
+      s.inv[lane] = nan ? 1.f : scale_value(2 * kScaleBias - vb);
       if (lane < kGroup) s.gone[lane] = (missing >> (8 * lane)) & 0xffu;
       kb = scale_byte(a.k_scale, page);
       vb = scale_byte(a.v_scale, page);

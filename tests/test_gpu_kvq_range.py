@@ -51,3 +51,16 @@ def test_verify_keys_of_every_size_side_by_side(dtype):
     s["kn"] = (s["kn"].float() * torch.exp2(torch.tensor([-20., -10., -4., 0., 0., 3., 10., -1.]))[:, None, None]).to(DT[dtype])
     out, _ = launch(s)
     check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lo,hi", [(135, 150), (180, 200), (40, 60)])
+def test_verify_value_scales_that_no_append_writes(dtype, lo, hi):
+    """A stored code stands for c 2^(byte - 127) at every byte, in both kernels."""
+    s = case(63, [150, 31], [2, 3], "paired", dtype, 4, 2, 128)
+    g = torch.Generator().manual_seed(64)
+    s["c"].vs = torch.randint(lo, hi, s["c"].vs.shape, generator=g, dtype=torch.int64).to(torch.uint8)
+    s["vn"] = (s["vn"].float() * 2.0 ** ((lo + hi) // 2 - 120)).to(DT[dtype])
+    out, ws = launch(s)
+    assert pkg.read_status(ws) == 0
+    check(s, out)
