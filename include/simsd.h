@@ -643,14 +643,16 @@ simsd_status simsd_page_map(const simsd_page_map_desc *d, void *stream);
  *            selects Hkv * hd), sequence b's rows at cu_n[b]..; 16-byte
  *            aligned arrays and strides
  *   start    device int32[batch]
- *   cu_n     device int32[batch+1] prefix sums of the rows
+ *   cu_n     device int32[batch+1] prefix sums of the rows (cu_n[0] >= 0: rows
+ *            before it are no sequence's)
  *   take     device int32[batch] or NULL: n_b = take[b] <= the sequence's
  *            rows (the first take[b] of them are written; 0: none), e.g. the
  *            data section's tokens of a block that closed
  *   total_n  host: rows of k and v
  * A sequence whose numbers are out of range, or whose table row does not
  * cover its slots or holds a page id outside the cache, sets the workspace's
- * bad-input bit; nothing is written for that sequence, or of that page.
+ * bad-input bit; nothing is written for that sequence, or of that page.  (Where
+ * cu_n falls, other sequences may be left out as well.)
  * Two sequences must not write the same page in one call.
  * Limits: num_kv_heads <= 1024; batch <= 2^20.  Workspace: the status word
  * (256 bytes).

@@ -254,13 +254,13 @@ kvq_append_kernel(const __grid_constant__ AppendArgs a) {
     const int n = a.take != nullptr ? __ldg(a.take + b) : rows;
     const int64_t j = item - first_item(c0, b);    // index among the sequence's touched pages
     const int64_t end = (int64_t)start + n;
-    if (c0 < 0 || rows < 0 || (int64_t)c0 + rows > a.total_n || n < 0 || n > rows || start < 0 || j < 0 ||
+    if (c0 < 0 || rows < 0 || (int64_t)c0 + rows > a.total_n || n < 0 || n > rows || start < 0 ||
         end > (int64_t)a.max_pages * kPage) {
       t.bad = true;
       return t;
     }
     const int64_t pg = start / kPage + j;          // page of the sequence
-    if (n == 0 || pg * kPage >= end) return t;
+    if (j < 0 || n == 0 || pg * kPage >= end) return t;   // (j < 0: rows before the first sequence's)
     t.any = true;
     t.page = __ldg(a.block_table + (int64_t)b * a.max_pages + pg);
     t.pos0 = (int)(pg * kPage);

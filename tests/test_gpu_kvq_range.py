@@ -6,7 +6,7 @@ import torch
 
 import kvq_ref as ref
 import speculative_decoding_diffusion_gb300 as pkg
-from test_gpu_kvq import DT, case, check, launch
+from test_gpu_kvq import DT, PAGE, Cache, case, check, cu_of, i32, launch, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,21 @@ def test_verify_value_scales_that_no_append_writes(dtype, lo, hi):
     out, ws = launch(s)
     assert pkg.read_status(ws) == 0
     check(s, out)
+
+
+def test_append_of_a_part_of_a_batch():
+    """cu_n of the later sequences of a larger batch: their rows, no complaint about the rows before them."""
+    g = torch.Generator().manual_seed(68)
+    n, start = [40, 25, 3, 18], [0, 7, 16, 30]
+    table, total = tables(g, [(s + m + PAGE - 1) // PAGE for s, m in zip(start, n)])
+    c = Cache(g, total, 2, 64)
+    v = torch.randn(sum(n), 2, 64, generator=g)
+    cu, spec = cu_of(n), dict(base=1e4, rotary_dim=2)
+    for first in (1, 2, 3):
+        dev = c.cuda()
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        pkg.kvq_append(v.cuda(), v.cuda(), i32(start[first:]), i32(cu[first:]), *dev, i32(table[first:]), ws, pkg.rope_spec(**spec))
+        assert pkg.read_status(ws) == 0
+        wv, wb = ref.append(v.double(), start[first:], cu[first:], table[first:], c.v, c.vs)
+        got = [t.cpu() for t in dev]
+        assert torch.equal(got[3], wb) and torch.equal(ref.e4m3_values(got[1]), wv)
