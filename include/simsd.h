@@ -540,7 +540,8 @@ typedef struct {
  * Arrays and strides that are multiples of 16 bytes, with rotary_dim a
  * multiple of 32 bytes, move in 16-byte vectors; others element by element
  * (each pointer aligned to its element, SIMSD_ERR_ALIGN otherwise).
- * rows = 0 returns SIMSD_OK.  Limits: heads <= 16384 each, rows <= 2^30.
+ * rows = 0 returns SIMSD_OK (the arrays may be NULL then).  Limits: heads <=
+ * 16384 each, rows <= 2^30.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t rows;
@@ -648,7 +649,7 @@ simsd_status simsd_page_map(const simsd_page_map_desc *d, void *stream);
  *   take     device int32[batch] or NULL: n_b = take[b] <= the sequence's
  *            rows (the first take[b] of them are written; 0: none), e.g. the
  *            data section's tokens of a block that closed
- *   total_n  host: rows of k and v
+ *   total_n  host: rows of k and v; 0: nothing is written (k and v may be NULL)
  * A sequence whose numbers are out of range, or whose table row does not
  * cover its slots or holds a page id outside the cache, sets the workspace's
  * bad-input bit; nothing is written for that sequence, or of that page.  (Where

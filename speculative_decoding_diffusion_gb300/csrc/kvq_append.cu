@@ -358,7 +358,7 @@ extern "C" simsd_status simsd_kvq_append(const simsd_kvq_append_desc *d, void *s
   AppendArgs a;
   const simsd_status st = make_rope_plan(d->rope, d->head_dim, &a.plan);
   if (st != SIMSD_OK) return st;
-  if (!d->k || !d->v || !d->start || !d->cu_n || !d->k_cache || !d->v_cache || !d->k_scale ||
+  if ((d->total_n > 0 && (!d->k || !d->v)) || !d->start || !d->cu_n || !d->k_cache || !d->v_cache || !d->k_scale ||
       !d->v_scale || !d->block_table)
     return SIMSD_ERR_NULL;
   const int64_t row = (int64_t)d->num_kv_heads * d->head_dim;

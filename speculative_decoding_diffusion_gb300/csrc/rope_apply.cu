@@ -255,6 +255,7 @@ extern "C" simsd_status simsd_rope(const simsd_rope_desc *d, void *stream) {
   RopeArgs a;
   const simsd_status st = make_rope_plan(d->rope, d->head_dim, &a.plan);
   if (st != SIMSD_OK) return st;
+  if (d->rows == 0) return SIMSD_OK;             // (tensors without rows have no memory)
   const bool two = d->num_heads1 > 0;
   if (!d->positions || !d->x0 || !d->y0 || (two && (!d->x1 || !d->y1))) return SIMSD_ERR_NULL;
   const int es = d->dtype == SIMSD_BF16 ? 2 : 4;
@@ -267,7 +268,6 @@ extern "C" simsd_status simsd_rope(const simsd_rope_desc *d, void *stream) {
     vec = vec && (uintptr_t)q % 16 == 0;
   }
   for (const int64_t t : s) vec = vec && (t * es) % 16 == 0;
-  if (d->rows == 0) return SIMSD_OK;
   a.pos = d->positions;
   a.x0 = d->x0; a.y0 = d->y0; a.x1 = d->x1; a.y1 = d->y1;
   a.x0_row = d->x0_row; a.x0_head = d->x0_head; a.y0_row = d->y0_row; a.y0_head = d->y0_head;

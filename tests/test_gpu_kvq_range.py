@@ -1,6 +1,8 @@
 """simsd_kvq_append and simsd_kvq_verify at the ends of what their header
 allows.  Tolerances as in test_gpu_kvq (kvq_ref.verify's bound); what must
 not change is compared bit by bit."""
+import math
+
 import pytest
 import torch
 
@@ -82,3 +84,18 @@ def test_append_of_a_part_of_a_batch():
         wv, wb = ref.append(v.double(), start[first:], cu[first:], table[first:], c.v, c.vs)
         got = [t.cpu() for t in dev]
         assert torch.equal(got[3], wb) and torch.equal(ref.e4m3_values(got[1]), wv)
+
+
+def test_calls_without_rows():
+    """Empty tensors (which have no memory): nothing is done and nothing refused."""
+    g = torch.Generator().manual_seed(69)
+    spec = pkg.rope_spec(base=1e4)
+    none = torch.empty(0, 2, 64, device="cuda")
+    pkg.rope(none, i32([]), spec, none, none, none)
+    table, total = tables(g, [1, 1])
+    dev = Cache(g, total, 2, 64).cuda()
+    before = [t.clone() for t in dev]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    pkg.kvq_append(none, none, i32([3, 5]), i32([0, 0, 0]), *dev, i32(table), ws, spec)
+    assert pkg.read_status(ws) == 0 and all(torch.equal(a, b) for a, b in zip(dev, before))
+    assert math.isfinite(float(dev[0].float().sum()))
