@@ -454,10 +454,16 @@ def _arrays(dev, dtype, *tensors):
     return True
 
 
-def _bytes(dev, *tensors):
-    """Whether all are contiguous, of one byte an element, on one device."""
-    for t in tensors:
-        if t.element_size() != 1 or t.get_device() != dev or not t.is_contiguous():
+# What the cache's arrays may be: their own types, or bytes (another 8-bit
+# floating type would be read as e4m3 without a word).
+_CODE_TYPES = frozenset((torch.float8_e4m3fn, torch.uint8, torch.int8))
+_SCALE_TYPES = frozenset((torch.float8_e8m0fnu, torch.uint8, torch.int8))
+
+
+def _cache_on(dev, k_cache, v_cache, k_scale, v_scale):
+    """Whether all four are contiguous, of a type of theirs, on one device."""
+    for t, types in ((k_cache, _CODE_TYPES), (v_cache, _CODE_TYPES), (k_scale, _SCALE_TYPES), (v_scale, _SCALE_TYPES)):
+        if t.dtype not in types or t.get_device() != dev or not t.is_contiguous():
             return False
     return True
 
@@ -523,10 +529,10 @@ def _ints(dtype, **tensors):
 
 
 def _codes(**tensors):
-    """8-bit arrays of the cache: contiguous, one byte an element."""
+    """8-bit arrays of the cache: contiguous, e4m3 codes or e8m0 scales (or either as bytes)."""
     for name, t in tensors.items():
-        if t.element_size() != 1:
-            raise TypeError("%s is %s, not an 8-bit type" % (name, t.dtype))
+        if t.dtype not in (_SCALE_TYPES if name.endswith("scale") else _CODE_TYPES):
+            raise TypeError("%s is %s, not %s or bytes" % (name, t.dtype, "e8m0" if name.endswith("scale") else "e4m3"))
         if not t.is_contiguous():
             raise ValueError("%s is not contiguous" % name)
 
@@ -613,11 +619,12 @@ def _cache_shape(k_cache, v_cache, k_scale, v_scale, hkv, hd, what):
 def kvq_append(k, v, start, cu_n, k_cache, v_cache, k_scale, v_scale, block_table, workspace, spec,
                take=None, stream=None):
     """simsd_kvq_append: k (rotated by spec) and v [total_n, Hkv, hd] into the
-    e4m3 caches [num_pages, Hkv, 16, hd] with e8m0 scales [num_pages, Hkv]."""
+    e4m3 caches [num_pages, Hkv, 16, hd] with e8m0 scales [num_pages, Hkv]
+    (tensors of those types, or uint8 or int8 that hold their bytes)."""
     dev = k.get_device()
     s = _stream_on(stream, dev, workspace)
     if s is None or not _arrays(dev, torch.int32, start, cu_n, block_table, take) or not _rows_on(
-            dev, k.dtype, v) or not _bytes(dev, k_cache, v_cache, k_scale, v_scale):
+            dev, k.dtype, v) or not _cache_on(dev, k_cache, v_cache, k_scale, v_scale):
         _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table, take=take)
         _same_dtype(k, v=v)
         _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
@@ -644,7 +651,7 @@ def _kvq_verify_desc(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, 
     dev = q.get_device()
     s = None if stream is False else _stream_on(stream, dev, workspace)
     if s is None or not _arrays(dev, torch.int32, block_table, tau, lens, cu_B) or not _rows_on(
-            dev, q.dtype, k_new, v_new, out) or not _bytes(dev, k_cache, v_cache, k_scale, v_scale):
+            dev, q.dtype, k_new, v_new, out) or not _cache_on(dev, k_cache, v_cache, k_scale, v_scale):
         _ints(torch.int32, block_table=block_table, tau=tau, lens=lens, cu_B=cu_B)
         _same_dtype(q, k_new=k_new, v_new=v_new, out=out)
         _codes(k_cache=k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
