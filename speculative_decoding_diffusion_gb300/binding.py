@@ -498,6 +498,21 @@ def _heads_of(t, dtype, rows, hd, what):
     return heads, row, head
 
 
+def _apart(rows, heads, hd, row, head):
+    """Whether no two heads of hd elements, at r * row + h * head, share an element."""
+    if rows <= 1 or heads <= 1:
+        return rows == 0 or heads == 0 or ((rows == 1 or row >= hd) and (heads == 1 or head >= hd))
+    if (head >= hd and row >= (heads - 1) * head + hd) or (row >= hd and head >= (rows - 1) * row + hd):
+        return True                              # one inside the other, as every ordinary layout
+    if row < hd or head < hd:
+        return False
+    for h in range(1, heads):                    # heads h apart: the rows next to that distance
+        r = h * head // row
+        if (r < rows and h * head - r * row < hd) or (r + 1 < rows and (r + 1) * row - h * head < hd):
+            return False
+    return True
+
+
 def _row_stride(t, what):
     """Row stride of a [rows, heads, hd] tensor whose rows are contiguous (0: and its rows one after another)."""
     if t.dim() == 3 and t.is_contiguous():
@@ -565,6 +580,8 @@ def rope(x, positions, spec, out, x2=None, out2=None, inverse=False, stream=None
         k2, orow2, ohead2 = _heads_of(out2, dtype, rows, hd, "out2")
     if k1 != h1 or k2 != h2:
         raise ValueError("out: heads of x")
+    if not _apart(rows, k1, hd, orow1, ohead1) or (k2 and not _apart(rows, k2, hd, orow2, ohead2)):
+        raise ValueError("out: rows or heads that share memory")
     if positions.numel() != rows:
         raise ValueError("positions: one for each row of x")
     d = _PACK_ROPE.pack(rows, h1, h2, hd, _dtype_code(x), 1 if inverse else 0, bytes(spec),

@@ -99,3 +99,22 @@ def test_calls_without_rows():
     pkg.kvq_append(none, none, i32([3, 5]), i32([0, 0, 0]), *dev, i32(table), ws, spec)
     assert pkg.read_status(ws) == 0 and all(torch.equal(a, b) for a, b in zip(dev, before))
     assert math.isfinite(float(dev[0].float().sum()))
+
+
+def test_rope_refuses_an_output_whose_rows_or_heads_share_memory():
+    x = torch.randn(5, 4, 64, device="cuda")
+    pos, spec = i32(torch.arange(5)), pkg.rope_spec(base=1e4)
+    one = torch.zeros(5, 1, 64, device="cuda")
+    row = torch.zeros(1, 4, 64, device="cuda")
+    near = torch.zeros(4096, device="cuda")
+    for out in (row.expand(5, 4, 64), one.expand(5, 4, 64), near.as_strided((5, 4, 64), (256, 32, 1)),
+                near.as_strided((5, 4, 64), (128, 64, 1)), near.as_strided((5, 4, 64), (64, 128, 1))):
+        with pytest.raises(ValueError):
+            pkg.rope(x, pos, spec, out)
+        with pytest.raises(ValueError):
+            pkg.rope(x, pos, spec, torch.empty_like(x), x, out)
+    y, z = torch.empty_like(x), near.as_strided((5, 4, 64), (64, 320, 1))      # heads first
+    pkg.rope(row.expand(5, 4, 64), pos, spec, y)                               # an input may
+    pkg.rope(x, pos, spec, y)
+    pkg.rope(x, pos, spec, z)
+    assert torch.equal(y, z)

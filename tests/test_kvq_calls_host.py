@@ -1,5 +1,5 @@
 """Host side of the 8-bit-cache calls beyond test_kvq_host: calls without
-rows, types of the cache (no GPU needed, no kernel launched)."""
+rows, types of the cache, layouts of an output (no GPU needed, no kernel launched)."""
 import ctypes
 
 import pytest
@@ -48,3 +48,18 @@ def test_a_cache_of_another_8_bit_type_is_refused(which):
     with pytest.raises(TypeError):
         binding.kvq_verify(q, *bad.values(), ids[:1].view(1, 1), q, q, None, ids[:1], ids[:2], q, ids, 4, 4, spec, 1.0,
                            order=binding.SIMSD_ORDER_CAUSAL)
+
+
+def test_heads_that_share_memory_are_found():
+    """Against every pair of heads compared, strides of every relation to hd, rows and heads."""
+    hd = 4
+    for rows in (0, 1, 2, 3, 5):
+        for heads in (1, 2, 3, 4):
+            for row in range(0, 26):
+                for head in range(0, 26):
+                    at = [r * row + h * head for r in range(rows) for h in range(heads)]
+                    want = all(abs(a - b) >= hd for i, a in enumerate(at) for b in at[:i])
+                    got = binding._apart(rows, heads, hd, row, head)
+                    assert got == want, (rows, heads, row, head)
+    assert binding._apart(7, 3, 64, 3 * 64, 64) and binding._apart(7, 3, 64, 64, 7 * 64)
+    assert not binding._apart(7, 3, 64, 0, 64) and not binding._apart(7, 3, 64, 64, 0)
