@@ -2,13 +2,16 @@
 allows.  Tolerances as in test_gpu_kvq (kvq_ref.verify's bound); what must
 not change is compared bit by bit."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import kvq_ref as ref
 import speculative_decoding_diffusion_gb300 as pkg
-from test_gpu_kvq import DT, PAGE, Cache, case, check, cu_of, i32, launch, tables
+from test_gpu_kvq import DT, PAGE, Cache, case, check, check_keys, cu_of, i32, launch, tables
 
 pytestmark = pytest.mark.gpu
 
@@ -118,3 +121,131 @@ def test_rope_refuses_an_output_whose_rows_or_heads_share_memory():
     pkg.rope(x, pos, spec, y)
     pkg.rope(x, pos, spec, z)
     assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,width", [([3000], 1024), ([900, 17, 0], 2048), ([4000, 300] * 4, 640)])
+def test_verify_tables_wider_than_the_prompts(dtype, lens, width):
+    """A table that leaves room to grow: pieces sized for the table, most of them without keys; ids behind a row's end
+    are not read."""
+    s = case(65, lens, [2] * len(lens), "paired", dtype, 4, 1, 64)
+    tight, _ = launch(s)
+    check(s, tight)
+    t = torch.full((len(lens), width), 2 ** 30, dtype=s["table"].dtype)
+    t[:, :s["table"].shape[1]] = s["table"]
+    s["table"] = t
+    out, ws = launch(s)
+    assert ws.numel() > 256 and pkg.read_status(ws) == 0
+    check(s, out)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_attention_factor(dtype):
+    """attn_factor on both sides of the scores and in the cache's keys."""
+    spec = dict(base=1e4, rotary_dim=64, scaling="linear", factor=2.0, attn_factor=1.25)
+    s = case(66, [70, 5], [3, 2], "causal", dtype, 4, 2, 128, spec=spec)
+    out, _ = launch(s)
+    check(s, out)
+    g = torch.Generator().manual_seed(67)
+    table, total = tables(g, [3])
+    c = Cache(g, total, 2, 128)
+    dev = c.cuda()
+    k = torch.randn(40, 2, 128, generator=g).to(DT[dtype])
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    pkg.kvq_append(k.cuda(), k.cuda(), i32([0]), i32([0, 40]), *dev, i32(table), ws, pkg.rope_spec(**spec))
+    wk, wkb = ref.append(ref.rope(k, torch.arange(40), spec), [0], cu_of([40]), table, c.k, c.ks)
+    got = [t.cpu() for t in dev]
+    check_keys(got[0], got[2], None, None, wk, wkb)
+    y = torch.empty_like(k, device="cuda")
+    for inverse in (False, True):
+        pkg.rope(k.cuda(), i32(torch.arange(40)), pkg.rope_spec(**spec), y, inverse=inverse)
+        want = ref.rope(k, torch.arange(40), spec, inverse)
+        size = 1.25 * 2 * k.double().abs().amax(-1, keepdim=True)
+        off = 1.5e-6 * size + torch.finfo(DT[dtype]).eps / 2 * want.abs()
+        assert ((y.cpu().double() - want).abs() <= off).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_leaves_the_rows_behind_the_last_sequence(dtype):
+    """q, k_new, v_new and out longer than the batch needs, with NaN behind it."""
+    s = case(70, [40, 3000], [3, 2], "paired", dtype, 4, 1, 64)
+    want, _ = launch(s)
+    more = {k: torch.cat([s[k], torch.full((7, *s[k].shape[1:]), math.nan, dtype=s[k].dtype)]) for k in ("q", "kn", "vn")}
+    out = torch.full(more["q"].shape, 5.0, dtype=DT[dtype], device="cuda")
+    out, ws = launch(dict(s, **more), out=out)
+    assert pkg.read_status(ws) == 0
+    assert torch.equal(out[:10], want) and (out[10:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_rows_with_odd_queries_keep_to_themselves(dtype):
+    """A NaN or an infinity in a query row: that row and head alone."""
+    s = case(71, [60, 20], [5, 5], "causal", dtype, 8, 2, 128)
+    clean = launch(s)[0].cpu()
+    s["q"][2, 3, 100], s["q"][7, 0, 1] = math.nan, math.inf
+    out = launch(s)[0].cpu()
+    bad = torch.zeros(10, 8, dtype=torch.bool)
+    bad[2, 3] = bad[7, 0] = True
+    assert torch.isnan(out[2, 3]).all() and not torch.isfinite(out[7, 0]).any()
+    assert torch.equal(out[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_sequences_that_share_their_first_pages(dtype):
+    """The same page in several rows of the table, and twice in one."""
+    s = case(72, [90, 100, 70], [2, 1, 3], "causal", dtype, 4, 2, 64)
+    s["table"][1, :4] = s["table"][0, :4]
+    s["table"][2, 1:3] = s["table"][2, 0]
+    out, ws = launch(s)
+    assert pkg.read_status(ws) == 0
+    check(s, out)
+
+
+FIRST = """
+import sys
+sys.path[:0] = %r
+import torch
+import speculative_decoding_diffusion_gb300 as pkg
+from test_gpu_kvq import case, i32, launch
+
+s = case(73, [300] * 30, [2] * 30, "causal", "bf16", 8, 8, 64)
+dev = [t.cuda() for t in (s["q"], *s["c"].cuda(), s["kn"], s["vn"])]
+q, cache, kn, vn = dev[0], dev[1:5], dev[5], dev[6]
+before = [t.clone() for t in cache]
+table, lens, cu, spec = i32(s["table"]), i32(s["lens"]), i32(s["cu"]), pkg.rope_spec(**s["spec"])
+start, pos = i32([16] * 30), i32(list(range(60)))
+held, queue, ring, served = i32([19] * 30), i32([0, 0]), i32([0] * 600), i32([0] * 30)
+slots = torch.zeros(60, dtype=torch.int64, device="cuda")
+out, y = torch.zeros_like(q), torch.zeros_like(q)
+ws = torch.zeros(1 << 24, dtype=torch.uint8, device="cuda")
+wsa, wsm = (torch.zeros(256, dtype=torch.uint8, device="cuda") for _ in range(2))
+
+def calls():
+    pkg.rope(q, pos, spec, y)
+    pkg.page_map(i32_lens, cu, held, queue, ring, table, held, queue, served, slots, wsm, 60)
+    pkg.kvq_append(kn, vn, start, cu, *cache, table, wsa, spec)
+    pkg.kvq_verify(q, *cache, table, kn, vn, None, lens, cu, out, ws, 60, 2, spec, s["scale"], order=pkg.SIMSD_ORDER_CAUSAL)
+
+i32_lens = lens.clone()
+graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=side):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in (out, y, slots, served, *cache)]
+for t, old in zip(cache, before):
+    t.copy_(old)
+calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(first, (out, y, slots, served, *cache)))
+assert not (pkg.read_status(ws) | pkg.read_status(wsa) | pkg.read_status(wsm))
+print("same")
+"""
+
+
+def test_a_process_whose_first_calls_are_captured():
+    """Every call of the loop inside a graph before any outside: what eager calls give."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST % ([here, os.path.dirname(here)],)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stdout + r.stderr
