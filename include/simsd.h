@@ -575,7 +575,8 @@ simsd_status simsd_rope(const simsd_rope_desc *d, void *stream);
  *   - need_b < held[b]: the entries need_b.. go to the ring's end, in the
  *     order of the sequences (a finished request: lens = n = 0);
  *   - slots[t] = page * 16 + offset of token t = cu_n[b] + i, at position
- *     lens[b] + i.  Tokens of no sequence's range are left as they were.
+ *     lens[b] + i: for writers of their own; the calls of this library find a
+ *     token's place by the table.  Tokens of no sequence's range are left as they were.
  * The ring: free_pages[(head + i) mod num_pages], i < count; queue holds
  * {head, count}.  Pages held and free together are at most num_pages.
  *   lens       device int32[batch]
@@ -648,15 +649,16 @@ simsd_status simsd_page_map(const simsd_page_map_desc *d, void *stream);
  *            before it are no sequence's)
  *   take     device int32[batch] or NULL: n_b = take[b] <= the sequence's
  *            rows (the first take[b] of them are written; 0: none), e.g. the
- *            data section's tokens of a block that closed
+ *            data section's tokens of a block that closed, or 0 for a sequence
+ *            that simsd_page_map did not serve (its table has no page for them)
  *   total_n  host: rows of k and v; 0: nothing is written (k and v may be NULL)
  * A sequence whose numbers are out of range, or whose table row does not
  * cover its slots or holds a page id outside the cache, sets the workspace's
  * bad-input bit; nothing is written for that sequence, or of that page.  (Where
  * cu_n falls, other sequences may be left out as well.)
  * Two sequences must not write the same page in one call.
- * Limits: num_kv_heads <= 1024; batch <= 2^20.  Workspace: the status word
- * (256 bytes).
+ * Limits: num_kv_heads <= 1024; batch <= 2^20; max_pages_per_seq <= 2^26.
+ * Workspace: the status word (256 bytes).
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t batch;
@@ -710,16 +712,29 @@ simsd_status simsd_kvq_append(const simsd_kvq_append_desc *d, void *stream);
  *   tau, lens, cu_B  as for simsd_verify_attn (tau: paired only)
  * Strides are in elements, 0 selects contiguous rows; arrays and strides are
  * multiples of 16 bytes (SIMSD_ERR_ALIGN).  The prompt's values in slots at
- * and past lens[b] are never used.  bf16: scores from the codes themselves,
- * a query row split into two e4m3 parts (2^-8 of a value, as rounding it to
- * bf16) on the tensor cores.  fp32: fp32 arithmetic throughout.
- * A sequence whose device arrays are out of range (cu_B, B_b outside
- * 1..B_max, lens[b] outside 0..16 max_pages_per_seq, n_b not a multiple of
- * node_size) sets the bad-input bit and its rows of out are not written; a
- * page id outside the cache sets it too, and that page counts as absent.
+ * and past lens[b] are never used.  fp32: fp32 arithmetic throughout.  bf16:
+ * on the tensor cores, scores from the codes themselves; sums, maxima and the
+ * output's accumulation in fp32, and in fewer bits
+ *   - the rotated query and each new key, in two e4m3 parts: an element is off
+ *     by at most 2^-9 of itself (rounding it to bf16: 2^-8) or 2^-17 of the
+ *     largest of its row, whichever is more;
+ *   - the weights that multiply the values, in f16, times the power of two of
+ *     the page's or new token's values: such a product is off by at most 2^-11
+ *     of itself or 2^-32 of the row's largest one.  (One that lies 2^110 or more
+ *     below the largest may be missing from the sum of weights as well: a row
+ *     that sees a new value of 1e25 beside pages of values below 1e-8.)
+ * Keys are split over the SMs by max_pages_per_seq, not by the lengths: one or
+ * a few long prompts run fastest in a table not much wider than they are.
+ * A sequence whose device arrays are out of range (cu_B, B_b outside 1..B_max,
+ * lens[b] outside 0..16 max_pages_per_seq, n_b not a multiple of node_size)
+ * sets the bad-input bit and its rows of out are not written; a page id outside
+ * the cache sets it too, and that page counts as absent.  (B_b = 0 is out of
+ * range: a finished request leaves the batch first.)
  * A row that sees a marked page, or a new token whose value holds a NaN or an
  * infinity, is NaN; a token that a row does not see has no effect on it.
- * Limits: Hq % Hkv == 0, head_dim 64 or 128.  The workspace size follows the
+ * Limits: Hq % Hkv == 0, Hq <= 65535, head_dim 64 or 128, max_pages_per_seq <
+ * 2^26, total_B <= 2^28, 64 batch Hkv row tiles < 2^31 (a tile: 128 of a
+ * sequence's rows for a KV head, fp32 16).  The workspace size follows the
  * key-split plan (the current device's SM count).
  * ---------------------------------------------------------------------- */
 typedef enum {

@@ -12,10 +12,10 @@
 // the maximum is a warp reduction.  Angles: a page's first position
 // (two a lane), times the turn by 0..15 positions from a table that
 // the CTA makes once -- one product instead of a sine and a cosine for each
-// row.  Bytes in, half as many (bf16) out: DRAM bounds a prompt's append, and
-// latency what it reaches of it: while a warp works on a page's values the
-// next page's keys are copied into shared memory (16-byte asynchronous
-// copies), and so in turn; 16 warps an SM.  256 prompts (1.07 M tokens, bf16,
+// row.  Bytes in, half as many (bf16) out; what keeps a prompt's append from the
+// copy rate is its arithmetic (69% of the issue slots) and latency: while a warp
+// works on a page's values the next page's keys are copied into shared memory
+// (16-byte asynchronous copies), and so in turn; 16 warps an SM.  256 prompts (1.07 M tokens, bf16,
 // 8 heads of 128): 1.22 ms, 5.4 TB/s of its bytes (12 warps with two pages of
 // buffers each 1.49; rows held in registers instead 1.50; angles by a sine
 // and a cosine for each row and lanes that met in the same banks 1.70 and up).

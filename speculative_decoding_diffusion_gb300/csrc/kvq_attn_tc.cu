@@ -2,9 +2,10 @@
 //
 // Scores of prompt keys come from the cache's e4m3 codes as they lie: a query
 // row, scaled by a power of two to the codes' range, is split into hi =
-// e4m3(q) and lo = e4m3(q - hi) (together 2^-8 of a value, a bf16 rounding),
-// and S = hi K^T + lo K^T accumulates in fp32 (kind::f8f6f4, twice the bf16
-// rate, so two products cost what one in bf16 does and no key is decoded).
+// e4m3(q) and lo = e4m3(q - hi) (together within 2^-9 of an element, half of a
+// bf16 rounding, or 2^-17 of the row's largest: lo's subnormal codes), and S =
+// hi K^T + lo K^T accumulates in fp32 (kind::f8f6f4, twice the bf16 rate, so
+// two products cost what one in bf16 does and no key is decoded).
 // The page's key scale multiplies the score in the softmax.  The weights
 // cannot be split like that (their range is too wide for e4m3), so four warps
 // unpack the value codes to f16 (exact) and O += P V runs in f16.  A page's
@@ -13,7 +14,7 @@
 // the row's sum takes 2^-ve times the sum of a page's weights -- nothing per
 // key or value.  M is at most 8 stale, so p <= 2^15 fits f16, whose 11 bits
 // keep the error against 64 bits at 1.9e-3 of the result, 1.7e-3 of it the
-// output's own rounding (bf16 weights: 2.5e-3).  The new tokens are a block of
+// output's own rounding (weights rounded to bf16: 2.5e-3).  The new tokens are a block of
 // their own ahead of the prompt: keys rotated and split here relative to a power
 // of two of each token's, values as f16 relative to another that is the token's
 // ve, so that no token's size reaches a row that does not see it.
@@ -27,10 +28,10 @@
 // 2240 with 128, where the softmax's chain (scores, maximum, exchange,
 // exponentials, weights) bounds it, and a CTA 15 to 20 thousand cycles more:
 // set-up 3, angles 1.5, rows 2 to 5 (as much instruction fetch as work), the new
-// tokens' block 3.5, epilogue 3.  Measured, bf16, 32 heads on 8 of 128: 64
-// sequences of up to 4096 keys, one token each, 81 us (3.4 TB/s of its bytes);
-// 64 of 4096, 64 rows a KV head, 148 us (3.8 TB/s, 460 TFLOP/s); 8 of 32768, 128
-// rows, 147 us (3.7 TB/s, 930 TFLOP/s); 256 of 256..8192 574 us (4.2 TB/s).
+// tokens' block 3.5 to 4, epilogue 3.  Measured, bf16, 32 heads on 8 of 128: 64
+// sequences of up to 4096 keys, one token each, 82 us (3.4 TB/s of its bytes);
+// 64 of 4096, 64 rows a KV head, 149 us (3.7 TB/s, 460 TFLOP/s); 8 of 32768, 128
+// rows, 149 us (3.6 TB/s, 920 TFLOP/s); 256 of 256..8192 577 us (4.2 TB/s).
 //   warp 0       one 2 KB copy per page: keys by TMA, swizzled for the MMA,
 //                values as they lie
 //   warp 6       scales: page ids and scale bytes well ahead, what they mean
@@ -677,7 +678,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     int j = 0;
     // the key loop, compiled once per copy count, the new tokens' block by itself
     // (a factor and a ve for each key: in the loop they would not leave it its
-    // registers, 64 x 4096 keys 171 us and not 148)
+    // registers, 64 x 4096 keys 171 us and not 149)
     auto key_loop = [&](auto rc) {
       constexpr int RC = decltype(rc)::value;
       constexpr int KW = kKeys / (RC * kHalves);   // this warp's keys per block: 64, 32 or 16

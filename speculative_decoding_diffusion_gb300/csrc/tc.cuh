@@ -1,7 +1,8 @@
 // tc.cuh -- 5th-generation tensor core (tcgen05) and TMEM helpers, inline PTX
 // for sm_103a: TMEM allocation, shared-memory matrix descriptors, the
-// kind::f8f6f4 MMA (e4m3 in) and the kind::f16 MMA (bf16 in, fp32 accumulate in TMEM), commit to an mbarrier,
-// and 32-lane x 32-column TMEM loads/stores.
+// kind::f8f6f4 MMA (e4m3 in) and the kind::f16 MMA (bf16 or f16 in), both
+// accumulating fp32 in TMEM, commit to an mbarrier, and TMEM loads/stores of 32
+// lanes and up to 32 columns.
 #pragma once
 
 #include <stdint.h>
@@ -176,11 +177,6 @@ __device__ __forceinline__ void st16(uint32_t taddr, const uint32_t *r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
       "r"(r[15])
       : "memory");
-}
-__device__ __forceinline__ void st4(uint32_t taddr, const uint32_t *r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr),
-               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-               : "memory");
 }
 __device__ __forceinline__ void st8(uint32_t taddr, const uint32_t *r) {
   asm volatile(
