@@ -63,7 +63,11 @@ typedef enum {
   SIMSD_ERR_ALIGN = 8      /* a device array is not 16-byte aligned         */
 } simsd_status;
 
-typedef enum { SIMSD_F32 = 0, SIMSD_BF16 = 1 } simsd_dtype;
+typedef enum {
+  SIMSD_F32 = 0,
+  SIMSD_BF16 = 1,
+  SIMSD_E4M3 = 2           /* simsd_kv4_read's rows only                      */
+} simsd_dtype;
 
 /* Static text for a status code; never NULL. */
 const char *simsd_status_string(int status);
@@ -778,6 +782,189 @@ typedef struct {
 
 size_t simsd_kvq_verify_workspace_size(const simsd_kvq_verify_desc *d);
 simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The 4-bit cache.  cache: device uint8 [num_pages][Hkv][18 hd], a page and
+ * head's record of 16 tokens (hd = 128: 2304 bytes, 64: 1152):
+ *   [0, 8 hd)        key codes: token i's row at i hd / 2; byte d / 2 holds
+ *                    elements d (even: low four bits) and d + 1
+ *   [8 hd, 16 hd)    value codes: element d of tokens i (even: low four bits)
+ *                    and i + 1 in byte (d / 32) 256 + (i / 2) 32 + d % 32
+ *   [16 hd, 17 hd)   key scales: group g of token i at i hd / 16 + g
+ *   [17 hd, 18 hd)   value scales: at (i / 2) hd / 8 + 2 g + i % 2
+ * A code is an e2m1 number (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives); a
+ * group is 16 neighbouring elements of a token's head; a scale byte holds bits
+ * 14..7 of a non-negative f16 number (five bits of exponent, three of
+ * mantissa).  A code stands for code * scale, which f16 holds exactly.  A byte
+ * of 0xf8 and above marks a group that got a NaN or an infinity (the append
+ * writes 0xfc): its elements read as NaN or infinities.
+ *
+ * simsd_kv4_append -- simsd_kvq_append for this cache: rotates n_b keys of
+ * sequence b at positions start[b].. and writes them and the values there.  A
+ * group's scale is the one nearest to its largest magnitude / 6 (ties to the
+ * even one), at most 10240 (magnitudes up to 61440); an element's code the one
+ * nearest to element / scale (ties to the even one, saturating).  A group
+ * below 6 * 2^-18 is zeros.  No other token's codes or scales change.
+ * Arguments, checks and bad inputs as for simsd_kvq_append, and two sequences
+ * must not write the same page in one call.
+ * Limits: num_kv_heads <= 1024; batch <= 2^20; max_pages_per_seq <= 2^26.
+ * Workspace: the status word (256 bytes).
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;
+  int32_t num_kv_heads;
+  int32_t head_dim;           /* 64 or 128                                  */
+  int32_t page_size;          /* 16                                         */
+  int32_t num_pages;
+  int32_t max_pages_per_seq;
+  int32_t total_n;
+  simsd_dtype dtype;          /* of k and v: SIMSD_F32 or SIMSD_BF16        */
+  simsd_rope_spec rope;
+  int64_t k_row, v_row;       /* row strides in elements; 0: Hkv * hd       */
+  const void *k;
+  const void *v;
+  const int32_t *start;
+  const int32_t *cu_n;
+  const int32_t *take;        /* or NULL                                    */
+  void *cache;                /* 16-byte aligned                            */
+  const int32_t *block_table;
+  void *workspace;            /* device, 256-byte aligned                   */
+  size_t workspace_bytes;
+} simsd_kv4_append_desc;
+
+simsd_status simsd_kv4_append(const simsd_kv4_append_desc *d, void *stream);
+
+/* ------------------------------------------------------------------------
+ * simsd_kv4_read -- the keys (rotated, as they lie) and values of positions
+ * start[b] .. start[b]+n_b-1 of each sequence as rows: for a prefix that moves
+ * elsewhere, or an attention that wants them plain.
+ *   start    device int32[batch]
+ *   cu_n     device int32[batch+1] prefix sums of the rows; rows of no
+ *            sequence's range are left as they were
+ *   k, v     device out, head h of row r at r * k_row + h * hd (elements; 0
+ *            selects Hkv * hd); 16-byte aligned arrays and strides.  One of
+ *            them may be NULL: not wanted.  SIMSD_F32 is exact, SIMSD_BF16
+ *            too (scales below 2^-14 included); SIMSD_E4M3 rounds to nearest
+ *            even, saturating at 448, NaN for what is not finite
+ *   total_n  host: rows of k and v; 0: nothing is written
+ * Bad inputs as for simsd_kv4_append: that sequence's rows, or those of that
+ * page, are left as they were.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;
+  int32_t num_kv_heads;
+  int32_t head_dim;           /* 64 or 128                                  */
+  int32_t page_size;          /* 16                                         */
+  int32_t num_pages;
+  int32_t max_pages_per_seq;
+  int32_t total_n;
+  simsd_dtype dtype;          /* of k and v                                 */
+  int64_t k_row, v_row;       /* row strides in elements; 0: Hkv * hd       */
+  const void *cache;          /* 16-byte aligned                            */
+  const int32_t *block_table;
+  const int32_t *start;
+  const int32_t *cu_n;
+  void *k;
+  void *v;
+  void *workspace;            /* device, 256-byte aligned                   */
+  size_t workspace_bytes;
+} simsd_kv4_read_desc;
+
+simsd_status simsd_kv4_read(const simsd_kv4_read_desc *d, void *stream);
+
+/* ------------------------------------------------------------------------
+ * simsd_kv4_verify -- simsd_kvq_verify over the 4-bit cache: the same orders,
+ * arrays, strides, limits, key splits and bad inputs.  fp32: fp32 arithmetic
+ * throughout.  bf16: on the tensor cores in f16 with fp32 sums, maxima and
+ * output; the cache's values are exact there.  In fewer bits
+ *   - the rotated query and each new key, relative to a power of two of the
+ *     row's: an element is off by at most 2^-11 of itself or 2^-33 of the
+ *     largest of its row, whichever is more;
+ *   - each new value, relative to a power of two of its token's, likewise;
+ *   - the weights that multiply the values: off by at most 2^-11 of themselves
+ *     or 2^-32 of the row's largest product.
+ * A row that sees a key of a marked group is NaN; one of a value, in that
+ * group's elements; a row that sees a new token with a NaN or an infinity is
+ * NaN.  A token that a row does not see has no effect on it.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;           /* 64 or 128                                  */
+  int32_t page_size;          /* 16                                         */
+  int32_t num_pages;
+  int32_t max_pages_per_seq;
+  int32_t total_B;            /* sum_b B_b (host copy)                      */
+  int32_t B_max;              /* max_b B_b (host copy)                      */
+  simsd_dtype dtype;          /* of q, k_new, v_new, out                    */
+  simsd_order order;
+  int32_t node_size;          /* SIMSD_ORDER_NODES: >= 1; otherwise 0       */
+  simsd_rope_spec rope;
+  float sm_scale;             /* finite, > 0                                */
+  int32_t wait_polls;         /* as in simsd_verify_desc                    */
+  int64_t q_row, k_row, v_row;
+  const void *q;
+  const void *cache;          /* 16-byte aligned                            */
+  const int32_t *block_table;
+  const void *k_new;
+  const void *v_new;
+  const int32_t *tau;
+  const int32_t *lens;
+  const int32_t *cu_B;
+  void *out;
+  void *workspace;            /* device, 256-byte aligned                   */
+  size_t workspace_bytes;
+} simsd_kv4_verify_desc;
+
+size_t simsd_kv4_verify_workspace_size(const simsd_kv4_verify_desc *d);
+simsd_status simsd_kv4_verify(const simsd_kv4_verify_desc *d, void *stream);
+
+/* ------------------------------------------------------------------------
+ * simsd_token_logprobs -- what a request gets back beside its tokens.  For
+ * each row r of logits l, p = softmax(l / T):
+ *   logprob[r]  ln p of tokens[r]
+ *   rank[r]     tokens ahead of it: #{v: l_v > l_t} + #{v < t: l_v = l_t}
+ *   entropy[r]  -sum p ln p, in nats
+ *   top_ids[r], top_logprobs[r]  the top_k likeliest tokens, likeliest first
+ *               (equal ones in index order), and their ln p
+ *   logits   device [rows] rows of vocab entries (dtype), row_stride elements
+ *            apart (0: vocab); any alignment of their type
+ *   tokens   device int32[rows] or NULL (then logprob and rank are NULL too).
+ *            -1: the row is not read, its outputs stay as they were.  Another
+ *            token outside 0..vocab-1 sets the bad-input bit; its logprob is
+ *            NaN, its rank -1
+ *   logprob, entropy  device float32[rows] or NULL; rank device int32[rows] or
+ *            NULL; top_ids device int32[rows][top_k] and top_logprobs device
+ *            float32[rows][top_k], both or none (top_k = 0)
+ * -inf entries have probability 0 (ln p = -inf).  A row that is -inf
+ * throughout or holds a NaN or +inf has NaN for logprob, entropy and
+ * top_logprobs; its rank and ids are of no use (ids lie in 0..vocab-1).
+ * Limits: 1 <= vocab <= 2^21; 0 <= rows <= 2^20; 0 <= top_k <= min(32, vocab);
+ * T as in simsd_accept_desc.  rows = 0 returns SIMSD_OK.
+ * Workspace: simsd_token_logprobs_workspace_size, 256 + rows * C * 48 bytes
+ * rounded up to a multiple of 256, with C = ceil(vocab / 2048) + 1.
+ * ---------------------------------------------------------------------- */
+typedef struct {
+  int32_t rows;
+  int32_t vocab;
+  int32_t top_k;
+  simsd_dtype dtype;          /* of the logits: SIMSD_F32 or SIMSD_BF16     */
+  float temperature;          /* > 0; 0 selects 1                           */
+  int64_t row_stride;
+  const void *logits;
+  const int32_t *tokens;
+  float *logprob;
+  int32_t *rank;
+  float *entropy;
+  int32_t *top_ids;
+  float *top_logprobs;
+  void *workspace;            /* device, 256-byte aligned                   */
+  size_t workspace_bytes;
+} simsd_token_logprobs_desc;
+
+size_t simsd_token_logprobs_workspace_size(const simsd_token_logprobs_desc *d);
+simsd_status simsd_token_logprobs(const simsd_token_logprobs_desc *d, void *stream);
 
 /* ------------------------------------------------------------------------
  * simsd_read_status -- synchronise `stream`, copy the device status word of

@@ -15,7 +15,7 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsimsd.so")
 
-SIMSD_F32, SIMSD_BF16 = 0, 1
+SIMSD_F32, SIMSD_BF16, SIMSD_E4M3 = 0, 1, 2
 SIMSD_ACCEPT_SAMPLE, SIMSD_ACCEPT_GREEDY, SIMSD_ACCEPT_MATCH = 0, 1, 2
 SIMSD_ROPE_HALF, SIMSD_ROPE_INTERLEAVED = 0, 1
 SIMSD_ROPE_SCALING = {"plain": 0, "linear": 1, "ntk": 2, "yarn": 3, "banded": 4}
@@ -114,6 +114,40 @@ class KvqVerifyDesc(ctypes.Structure):
                 ("out", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
 
 
+class Kv4AppendDesc(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("page_size", _i32),
+                ("num_pages", _i32), ("max_pages_per_seq", _i32), ("total_n", _i32),
+                ("dtype", ctypes.c_int), ("rope", RopeSpec), ("k_row", _i64), ("v_row", _i64),
+                ("k", _vp), ("v", _vp), ("start", _vp), ("cu_n", _vp), ("take", _vp), ("cache", _vp),
+                ("block_table", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class Kv4ReadDesc(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("page_size", _i32),
+                ("num_pages", _i32), ("max_pages_per_seq", _i32), ("total_n", _i32),
+                ("dtype", ctypes.c_int), ("k_row", _i64), ("v_row", _i64), ("cache", _vp),
+                ("block_table", _vp), ("start", _vp), ("cu_n", _vp), ("k", _vp), ("v", _vp),
+                ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class Kv4VerifyDesc(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("num_q_heads", _i32), ("num_kv_heads", _i32),
+                ("head_dim", _i32), ("page_size", _i32), ("num_pages", _i32),
+                ("max_pages_per_seq", _i32), ("total_B", _i32), ("B_max", _i32),
+                ("dtype", ctypes.c_int), ("order", ctypes.c_int), ("node_size", _i32),
+                ("rope", RopeSpec), ("sm_scale", _f32), ("wait_polls", _i32),
+                ("q_row", _i64), ("k_row", _i64), ("v_row", _i64), ("q", _vp), ("cache", _vp),
+                ("block_table", _vp), ("k_new", _vp), ("v_new", _vp), ("tau", _vp), ("lens", _vp),
+                ("cu_B", _vp), ("out", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class TokenLogprobsDesc(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("vocab", _i32), ("top_k", _i32), ("dtype", ctypes.c_int),
+                ("temperature", _f32), ("row_stride", _i64), ("logits", _vp), ("tokens", _vp),
+                ("logprob", _vp), ("rank", _vp), ("entropy", _vp), ("top_ids", _vp),
+                ("top_logprobs", _vp), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
 class SimsdError(RuntimeError):
     def __init__(self, code, what):
         super().__init__("%s failed: %s (%d)" % (what, STATUS.get(code, "?"), code))
@@ -159,10 +193,11 @@ def lib():
         L.simsd_commit_workspace_size.argtypes = [ctypes.POINTER(CommitDesc)]
         L.simsd_commit.restype = ctypes.c_int
         L.simsd_commit.argtypes = [ctypes.POINTER(CommitDesc), _vp]
-        for name in ("rope", "page_map", "kvq_append", "kvq_verify"):   # descriptors as packed bytes
+        for name in ("rope", "page_map", "kvq_append", "kvq_verify", "kv4_append", "kv4_read", "kv4_verify",
+                     "token_logprobs"):          # descriptors as packed bytes
             f = getattr(L, "simsd_" + name)
             f.restype, f.argtypes = ctypes.c_int, [_vp, _vp]
-        for name in ("page_map", "kvq_verify"):
+        for name in ("page_map", "kvq_verify", "kv4_verify", "token_logprobs"):
             f = getattr(L, "simsd_%s_workspace_size" % name)
             f.restype, f.argtypes = _sz, [_vp]
         L.simsd_read_status.restype = ctypes.c_int
@@ -418,6 +453,10 @@ _PACK_ROPE = struct.Struct("@6i36s5P8q")
 _PACK_PAGE_MAP = struct.Struct("@5i11PN")
 _PACK_APPEND = struct.Struct("@8i36s2q11PN")
 _PACK_VERIFY = struct.Struct("@12i36sfi3q13PN")
+_PACK_APPEND4 = struct.Struct("@8i36s2q8PN")
+_PACK_READ4 = struct.Struct("@8i2q7PN")
+_PACK_VERIFY4 = struct.Struct("@12i36sfi3q10PN")
+_PACK_LOGPROBS = struct.Struct("@4ifq8PN")
 
 
 def _addr(t):
@@ -717,6 +756,192 @@ def kvq_verify(q, k_cache, v_cache, k_scale, v_scale, block_table, k_new, v_new,
                             cu_B, out, workspace, total_B, B_max, spec, sm_scale, order, node_size,
                             wait_polls, stream)
     _check(lib().simsd_kvq_verify(d, s), "simsd_kvq_verify")
+
+
+def kv4_page_bytes(head_dim):
+    """Bytes of a page and head of the 4-bit cache, a tensor uint8 [num_pages, Hkv, kv4_page_bytes(hd)]."""
+    if head_dim not in (64, 128):
+        raise ValueError("head_dim is 64 or 128")
+    return 18 * head_dim
+
+
+def _cache4(cache, dev):
+    """Whether the 4-bit cache is contiguous bytes on device dev."""
+    return cache.dtype is torch.uint8 and cache.get_device() == dev and cache.is_contiguous()
+
+
+def _check_cache4(cache):
+    if cache.dtype is not torch.uint8:
+        raise TypeError("cache is %s, not uint8" % cache.dtype)
+    if not cache.is_contiguous():
+        raise ValueError("cache is not contiguous")
+
+
+def _cache4_pages(cache, hkv, hd, what):
+    """num_pages of a 4-bit cache of hkv heads of hd."""
+    shape = cache.shape
+    if len(shape) != 3 or shape[1] != hkv or shape[2] != 18 * hd:
+        raise ValueError("%s: cache is [num_pages, Hkv, 18 head_dim]" % what)
+    return shape[0]
+
+
+def kv4_append(k, v, start, cu_n, cache, block_table, workspace, spec, take=None, stream=None):
+    """simsd_kv4_append: k (rotated by spec) and v [total_n, Hkv, hd] quantised
+    into the 4-bit cache, uint8 [num_pages, Hkv, kv4_page_bytes(hd)]."""
+    dev = k.get_device()
+    s = _stream_on(stream, dev, workspace)
+    if s is None or not _arrays(dev, torch.int32, start, cu_n, block_table, take) or not _rows_on(
+            dev, k.dtype, v) or not _cache4(cache, dev):
+        _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table, take=take)
+        _same_dtype(k, v=v)
+        _check_cache4(cache)
+        s = _run_on(stream, k, v, start, cu_n, cache, block_table, workspace, take)
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("kv4_append: k and v are [rows, heads, head_dim]")
+    total_n, hkv, hd = k.shape
+    num_pages = _cache4_pages(cache, hkv, hd, "kv4_append")
+    (batch,), (tables, width) = start.shape, block_table.shape
+    if cu_n.numel() != batch + 1 or tables != batch or (take is not None and take.numel() != batch):
+        raise ValueError("kv4_append: sizes of the arrays disagree")
+    d = _PACK_APPEND4.pack(batch, hkv, hd, 16, num_pages, width, total_n, _dtype_code(k), bytes(spec),
+                           _row_stride(k, "k"), _row_stride(v, "v"), k.data_ptr(), v.data_ptr(),
+                           start.data_ptr(), cu_n.data_ptr(), _addr(take), cache.data_ptr(),
+                           block_table.data_ptr(), *_ws(workspace))
+    _check(lib().simsd_kv4_append(d, s), "simsd_kv4_append")
+
+
+_ROW_TYPES = {torch.float32: SIMSD_F32, torch.bfloat16: SIMSD_BF16, torch.float8_e4m3fn: SIMSD_E4M3}
+
+
+def kv4_read(cache, block_table, start, cu_n, k, v, workspace, stream=None):
+    """simsd_kv4_read: positions start[b].. of each sequence back as rows k and
+    v [total_n, Hkv, hd] of fp32, bf16 or e4m3 (either may be None)."""
+    like = v if k is None else k
+    if like is None:
+        raise ValueError("kv4_read: neither k nor v is wanted")
+    dev = cache.get_device()
+    s = _stream_on(stream, dev, workspace)
+    if s is None or not _arrays(dev, torch.int32, start, cu_n, block_table) or not _cache4(cache, dev) or not _rows_on(
+            dev, like.dtype, *(t for t in (k, v) if t is not None)):
+        _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table)
+        _check_cache4(cache)
+        if k is not None and v is not None:
+            _same_dtype(k, v=v)
+        s = _run_on(stream, cache, block_table, start, cu_n, k, v, workspace)
+    if like.dtype not in _ROW_TYPES:
+        raise TypeError("unsupported dtype %s" % like.dtype)
+    if like.dim() != 3 or (k is not None and v is not None and v.shape != k.shape):
+        raise ValueError("kv4_read: k and v are [rows, heads, head_dim]")
+    total_n, hkv, hd = like.shape
+    num_pages = _cache4_pages(cache, hkv, hd, "kv4_read")
+    (batch,), (tables, width) = start.shape, block_table.shape
+    if cu_n.numel() != batch + 1 or tables != batch:
+        raise ValueError("kv4_read: sizes of the arrays disagree")
+    d = _PACK_READ4.pack(batch, hkv, hd, 16, num_pages, width, total_n, _ROW_TYPES[like.dtype],
+                         0 if k is None else _row_stride(k, "k"), 0 if v is None else _row_stride(v, "v"),
+                         cache.data_ptr(), block_table.data_ptr(), start.data_ptr(), cu_n.data_ptr(), _addr(k),
+                         _addr(v), *_ws(workspace))
+    _check(lib().simsd_kv4_read(d, s), "simsd_kv4_read")
+
+
+def _kv4_verify_desc(q, cache, block_table, k_new, v_new, tau, lens, cu_B, out, workspace, total_B, B_max, spec,
+                     sm_scale, order, node_size, wait_polls=0, stream=False):
+    """(stream, descriptor); stream False: for the workspace's size, no device needed."""
+    dev = q.get_device()
+    s = None if stream is False else _stream_on(stream, dev, workspace)
+    if s is None or not _arrays(dev, torch.int32, block_table, tau, lens, cu_B) or not _rows_on(
+            dev, q.dtype, k_new, v_new, out) or not _cache4(cache, dev):
+        _ints(torch.int32, block_table=block_table, tau=tau, lens=lens, cu_B=cu_B)
+        _same_dtype(q, k_new=k_new, v_new=v_new, out=out)
+        _check_cache4(cache)
+        if stream is not False:
+            s = _run_on(stream, q, cache, block_table, k_new, v_new, tau, lens, cu_B, out, workspace)
+    paired = order == SIMSD_ORDER_PAIRED
+    if q.dim() != 3 or k_new.dim() != 3 or out.shape != q.shape or v_new.shape != k_new.shape:
+        raise ValueError("kv4_verify: q, out and k_new, v_new are [rows, heads, head_dim]")
+    (T, hq, hd), (Tk, hkv, hdk) = q.shape, k_new.shape
+    num_pages = _cache4_pages(cache, hkv, hd, "kv4_verify")
+    (batch,), (tables, width) = lens.shape, block_table.shape
+    rows = 2 * total_B if paired else total_B
+    if (T < rows or Tk < rows or hdk != hd or cu_B.numel() != batch + 1 or tables != batch or
+            (paired and tau is not None and tau.numel() < total_B)):
+        raise ValueError("kv4_verify: sizes of the arrays disagree")
+    if not out.is_contiguous():
+        raise ValueError("out is not contiguous")
+    return s, _PACK_VERIFY4.pack(batch, hq, hkv, hd, 16, num_pages, width, total_B, B_max, _dtype_code(q), order,
+                                 node_size, bytes(spec), sm_scale, wait_polls, _row_stride(q, "q"),
+                                 _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), q.data_ptr(),
+                                 cache.data_ptr(), block_table.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+                                 _addr(tau), lens.data_ptr(), cu_B.data_ptr(), out.data_ptr(), *_ws(workspace))
+
+
+def kv4_verify_workspace_size(q, cache, block_table, k_new, v_new, tau, lens, cu_B, out, total_B, B_max, spec,
+                              sm_scale, order=SIMSD_ORDER_PAIRED, node_size=0):
+    _, d = _kv4_verify_desc(q, cache, block_table, k_new, v_new, tau, lens, cu_B, out, None, total_B, B_max, spec,
+                            sm_scale, order, node_size)
+    n = lib().simsd_kv4_verify_workspace_size(d)
+    if n == 0:
+        raise SimsdError(2, "simsd_kv4_verify_workspace_size")
+    return int(n)
+
+
+def kv4_verify(q, cache, block_table, k_new, v_new, tau, lens, cu_B, out, workspace, total_B, B_max, spec, sm_scale,
+               order=SIMSD_ORDER_PAIRED, node_size=0, wait_polls=0, stream=None):
+    """simsd_kv4_verify: attention of the new tokens over the 4-bit prompt cache
+    and themselves; as kvq_verify otherwise."""
+    s, d = _kv4_verify_desc(q, cache, block_table, k_new, v_new, tau, lens, cu_B, out, workspace, total_B, B_max, spec,
+                            sm_scale, order, node_size, wait_polls, stream)
+    _check(lib().simsd_kv4_verify(d, s), "simsd_kv4_verify")
+
+
+def _logprobs_desc(logits, tokens, logprob, rank, entropy, top_ids, top_logprobs, workspace, temperature=1.0,
+                   stream=False):
+    """(stream, descriptor); stream False: for the workspace's size, no device needed."""
+    dev = logits.get_device()
+    s = None if stream is False else _stream_on(stream, dev, workspace)
+    if s is None or not _arrays(dev, torch.int32, tokens, rank, top_ids) or not _arrays(
+            dev, torch.float32, logprob, entropy, top_logprobs):
+        _ints(torch.int32, tokens=tokens, rank=rank, top_ids=top_ids)
+        _ints(torch.float32, logprob=logprob, entropy=entropy, top_logprobs=top_logprobs)
+        if stream is not False:
+            s = _run_on(stream, logits, tokens, logprob, rank, entropy, top_ids, top_logprobs, workspace)
+    if logits.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits: expected [rows, vocab] with contiguous rows")
+    rows, vocab = logits.shape
+    stride = logits.stride(0) if rows > 1 else 0
+    if rows > 1 and stride < vocab:
+        raise ValueError("logits: rows that share memory")
+    for name, t in (("tokens", tokens), ("logprob", logprob), ("rank", rank), ("entropy", entropy)):
+        if t is not None and t.numel() != rows:
+            raise ValueError("%s: one for each row of logits" % name)
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs come together")
+    top = 0
+    if top_ids is not None:
+        if top_ids.dim() != 2 or top_ids.shape != top_logprobs.shape or top_ids.shape[0] != rows or top_ids.shape[1] < 1:
+            raise ValueError("top_ids and top_logprobs are [rows, top_k]")
+        top = top_ids.shape[1]
+    return s, _PACK_LOGPROBS.pack(rows, vocab, top, _dtype_code(logits), temperature, stride, logits.data_ptr(),
+                                  _addr(tokens), _addr(logprob), _addr(rank), _addr(entropy), _addr(top_ids),
+                                  _addr(top_logprobs), *_ws(workspace))
+
+
+def token_logprobs_workspace_size(logits, tokens, logprob, rank, entropy, top_ids, top_logprobs):
+    _, d = _logprobs_desc(logits, tokens, logprob, rank, entropy, top_ids, top_logprobs, None)
+    n = lib().simsd_token_logprobs_workspace_size(d)
+    if n == 0:
+        raise SimsdError(2, "simsd_token_logprobs_workspace_size")
+    return int(n)
+
+
+def token_logprobs(logits, tokens, logprob, rank, entropy, top_ids, top_logprobs, workspace, temperature=1.0,
+                   stream=None):
+    """simsd_token_logprobs: of each row of logits [rows, vocab] (any row
+    stride), ln p and rank of tokens[r] (-1: the row is left out), the entropy,
+    and the top_ids.shape[1] likeliest tokens; any output may be None (without
+    tokens, logprob and rank are)."""
+    s, d = _logprobs_desc(logits, tokens, logprob, rank, entropy, top_ids, top_logprobs, workspace, temperature, stream)
+    _check(lib().simsd_token_logprobs(d, s), "simsd_token_logprobs")
 
 
 def read_status(workspace, stream=None):

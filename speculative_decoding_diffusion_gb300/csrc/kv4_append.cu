@@ -1,0 +1,209 @@
+// kv4_append.cu -- simsd_kv4_append: rotated keys and values quantised into the
+// 4-bit cache.
+//
+// Every token has scales of its own (one for 16 neighbouring elements), so no
+// token's codes depend on another's and a row is written where it arrives.  A
+// CTA takes 16 rows: their places and angles are made once for all heads, then
+// a thread takes 32 elements of a key (two groups, partners of each other in
+// the rotation where the pairs allow it, so that each element is read once and
+// nothing is exchanged) or one group of a value.  A value byte holds two
+// neighbouring tokens of an element: the thread of the pair's first token in
+// the call takes both; where only one of them is written, it puts its four bits
+// into the byte that is there (no other thread of the call touches it).
+#include <limits.h>
+#include <math.h>
+
+#include "kv4.cuh"
+#include "rope_spec.cuh"
+#include "vec.cuh"
+
+namespace simsd {
+namespace {
+
+constexpr int kThreads = 256;
+
+struct Append4Args {
+  RopePlan plan;
+  Rows4 rows;
+  const void *k, *v;
+  uint8_t *cache;
+  int64_t k_row, v_row;
+  int Hkv;
+};
+
+// Sixteen elements to codes, two a byte, and their scale byte.
+__device__ __forceinline__ uint2 quantise16(const float *x, uint32_t *byte) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; i += 2) amax = absmax_nan(amax, x[i], x[i + 1]);
+  *byte = scale4_of(amax);
+  const Scaler c = scaler_of(*byte);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 16; i += 2)
+    w[i / 8] |= pack_e2m1x2(over(x[i], c), over(x[i + 1], c)) << (4 * (i % 8));
+  return make_uint2(w[0], w[1]);
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kThreads)
+kv4_append_kernel(const __grid_constant__ Append4Args a) {
+  using R = Record<HD>;
+  __shared__ __align__(16) float2 cs_s[kTileRows][HD / 2];
+  __shared__ Row4 row_s[kTileRows];
+  __shared__ int lead_s[kTileRows], n_lead_s;        // rows that write their value pair
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = blockIdx.x * kTileRows;
+  grid_dep_wait();
+  grid_dep_launch();
+  for (int r = warp; r < kTileRows; r += kThreads / 32) {
+    const Row4 w = find_row4(a.rows, row0 + r, lane);
+    if (lane == 0) row_s[r] = w;
+  }
+  check_rows4(a.rows);
+  __syncthreads();
+  if (warp == 0) {
+    const bool leads = lane < kTileRows && row_s[lane].leads();
+    const uint32_t m = __ballot_sync(0xffffffffu, leads);
+    if (leads) lead_s[__popc(m & ((1u << lane) - 1u))] = lane;
+    if (lane == 0) n_lead_s = __popc(m);
+  }
+  for (int e = threadIdx.x; e < kTileRows * (HD / 2); e += kThreads) {
+    const int r = e / (HD / 2), d = e % (HD / 2);
+    if (row_s[r].page >= 0)
+      cs_s[r][angle_at(d)] = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, row_s[r].pos) : make_float2(1.f, 0.f);
+  }
+  __syncthreads();
+  constexpr int KL = HD / 32, VL = HD / 16;          // threads of a key row, of a value row
+  const bool paired = !a.plan.interleaved && a.plan.half % 16 == 0;
+  const int turned = a.plan.half / 16;               // pairs of groups that are each other's partners
+  for (int e = threadIdx.x; e < kTileRows * a.Hkv * KL; e += kThreads) {
+    const int u = e % KL, rh = e / KL, h = rh % a.Hkv, r = rh / a.Hkv;
+    const Row4 w = row_s[r];
+    if (w.page < 0) continue;
+    const T *src = (const T *)a.k + (int64_t)(row0 + r) * a.k_row + h * HD;
+    const bool rot = paired && u < turned;
+    const int g0 = rot ? u : paired ? 2 * turned + 2 * (u - turned) : 2 * u, g1 = rot ? u + turned : g0 + 1;
+    float x[16], y[16];
+    if (paired) {
+      load_vec<T, 8>(src + g0 * 16, x);
+      load_vec<T, 8>(src + g0 * 16 + 8, x + 8);
+      load_vec<T, 8>(src + g1 * 16, y);
+      load_vec<T, 8>(src + g1 * 16 + 8, y + 8);
+      if (rot) {
+#pragma unroll
+        for (int c = 0; c < 16; c += 8) {
+          float2 z[8];
+          load_angles8(cs_s[r], g0 * 16 + c, z);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float p = x[c + i], q = y[c + i];
+            x[c + i] = p * z[i].x - q * z[i].y;
+            y[c + i] = q * z[i].x + p * z[i].y;
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 16; c += 8) {
+        rotate8(a.plan, cs_s[r], src, g0 * 16 + c, x + c);
+        rotate8(a.plan, cs_s[r], src, g1 * 16 + c, y + c);
+      }
+    }
+    uint8_t *rec = a.cache + ((int64_t)w.page * a.Hkv + h) * R::kBytes;
+    const int slot = w.pos & (kPage - 1);
+    uint32_t b0, b1;
+    const uint2 c0 = quantise16(x, &b0), c1 = quantise16(y, &b1);
+    *reinterpret_cast<uint2 *>(rec + slot * (HD / 2) + g0 * 8) = c0;
+    *reinterpret_cast<uint2 *>(rec + slot * (HD / 2) + g1 * 8) = c1;
+    rec[R::kKs + slot * (HD / 16) + g0] = (uint8_t)b0;
+    rec[R::kKs + slot * (HD / 16) + g1] = (uint8_t)b1;
+  }
+  const int n_lead = n_lead_s;
+  for (int e = threadIdx.x; e < n_lead * a.Hkv * VL; e += kThreads) {
+    const int g = e % VL, rh = e / VL, h = rh % a.Hkv, r = lead_s[rh / a.Hkv];
+    const Row4 w = row_s[r];
+    const bool even = w.has(0), odd = w.has(1);
+    const T *src = (const T *)a.v + (int64_t)(row0 + r) * a.v_row + h * HD + g * 16;
+    const T *src_odd = (w.pos & 1) ? src : src + a.v_row;
+    float x[16], y[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = y[i] = 0.f;
+    if (even) {
+      load_vec<T, 8>(src, x);
+      load_vec<T, 8>(src + 8, x + 8);
+    }
+    if (odd) {
+      load_vec<T, 8>(src_odd, y);
+      load_vec<T, 8>(src_odd + 8, y + 8);
+    }
+    uint8_t *rec = a.cache + ((int64_t)w.page * a.Hkv + h) * R::kBytes;
+    const int pair = (w.pos & (kPage - 1)) >> 1;
+    uint32_t *codes = reinterpret_cast<uint32_t *>(rec + R::v_at(pair, g));
+    uint8_t *scales = rec + R::vs_at(pair, g);
+    float ax = 0.f, ay = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      ax = absmax_nan(ax, x[i], x[i + 1]);
+      ay = absmax_nan(ay, y[i], y[i + 1]);
+    }
+    const uint32_t bx = scale4_of(ax), by = scale4_of(ay);
+    const Scaler cx = scaler_of(bx), cy = scaler_of(by);
+    uint32_t c[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) c[i / 4] |= pack_e2m1x2(over(x[i], cx), over(y[i], cy)) << (8 * (i % 4));
+    if (even && odd) {
+      *reinterpret_cast<uint4 *>(codes) = make_uint4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<uint16_t *>(scales) = (uint16_t)(bx | by << 8);
+    } else {                                         // the other token's four bits stay
+      const uint32_t keep = even ? 0xf0f0f0f0u : 0x0f0f0f0fu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) codes[i] = (codes[i] & keep) | (c[i] & ~keep);
+      scales[even ? 0 : 1] = (uint8_t)(even ? bx : by);
+    }
+  }
+}
+
+template <typename T>
+cudaError_t launch_append4(const Append4Args &a, int hd, cudaStream_t stream) {
+  const dim3 grid((unsigned)((a.rows.total_n + kTileRows - 1) / kTileRows)), block(kThreads);
+  return hd == 128 ? launch_pdl(kv4_append_kernel<T, 128>, grid, block, 0, stream, a)
+                   : launch_pdl(kv4_append_kernel<T, 64>, grid, block, 0, stream, a);
+}
+
+}  // namespace
+}  // namespace simsd
+
+using namespace simsd;
+
+extern "C" simsd_status simsd_kv4_append(const simsd_kv4_append_desc *d, void *stream_ptr) {
+  if (d == nullptr) return SIMSD_ERR_NULL;
+  if (d->dtype != SIMSD_F32 && d->dtype != SIMSD_BF16) return SIMSD_ERR_DTYPE;
+  if (d->batch < 1 || d->batch > (1 << 20) || d->num_kv_heads < 1 || d->num_kv_heads > 1024 ||
+      (d->head_dim != 64 && d->head_dim != 128) || d->page_size != kPageTokens || d->num_pages < 1 ||
+      d->max_pages_per_seq < 1 || d->max_pages_per_seq > (1 << 26) || d->total_n < 0 || d->k_row < 0 || d->v_row < 0)
+    return SIMSD_ERR_SHAPE;
+  Append4Args a;
+  const simsd_status st = make_rope_plan(d->rope, d->head_dim, &a.plan);
+  if (st != SIMSD_OK) return st;
+  if ((d->total_n > 0 && (!d->k || !d->v)) || !d->start || !d->cu_n || !d->cache || !d->block_table)
+    return SIMSD_ERR_NULL;
+  const int es = d->dtype == SIMSD_BF16 ? 2 : 4;
+  a.k_row = d->k_row ? d->k_row : (int64_t)d->num_kv_heads * d->head_dim;
+  a.v_row = d->v_row ? d->v_row : (int64_t)d->num_kv_heads * d->head_dim;
+  if (!aligned16(d->k) || !aligned16(d->v) || !aligned16(d->cache) || a.k_row * es % 16 != 0 || a.v_row * es % 16 != 0)
+    return SIMSD_ERR_ALIGN;
+  if (d->workspace == nullptr || (uintptr_t)d->workspace % kAlign != 0 || d->workspace_bytes < kAlign)
+    return SIMSD_ERR_WORKSPACE;
+  if (d->total_n == 0) return SIMSD_OK;
+  a.rows = {d->block_table, d->start, d->cu_n, d->take, (uint32_t *)d->workspace,
+            d->batch, d->max_pages_per_seq, d->num_pages, d->total_n};
+  a.k = d->k;
+  a.v = d->v;
+  a.cache = (uint8_t *)d->cache;
+  a.Hkv = d->num_kv_heads;
+  cudaStream_t stream = (cudaStream_t)stream_ptr;
+  const cudaError_t e = d->dtype == SIMSD_BF16 ? launch_append4<__nv_bfloat16>(a, d->head_dim, stream)
+                                               : launch_append4<float>(a, d->head_dim, stream);
+  return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
+}

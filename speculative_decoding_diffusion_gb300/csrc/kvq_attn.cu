@@ -22,6 +22,7 @@
 #include <algorithm>
 #include <atomic>
 
+#include "kv4.cuh"
 #include "kvq.cuh"
 #include "kvq_attn.cuh"
 #include "vec.cuh"
@@ -44,7 +45,88 @@ struct SimtSmem {
   float p[kRows][kTile];
 };
 
-template <typename T, int HD>
+// A tile of the prompt's keys and values, decoded; zeros past its end and for
+// pages outside the cache.
+template <int HD>
+__device__ __forceinline__ void load_tile8(const KvqParams &a, const KvqWork &w, const int32_t *bt, int base,
+                                           SimtSmem<HD> &s) {
+  constexpr int CH = HD / 16;                        // 16-byte chunks of a row
+  for (int e = threadIdx.x; e < 2 * kTile * CH; e += kThreads) {
+    const bool is_v = e >= kTile * CH;
+    const int j = (is_v ? e - kTile * CH : e) / CH, c = e % CH, key = base + j;
+    uint4 raw = make_uint4(0, 0, 0, 0);
+    float sc = 0.f;
+    if (key < w.k_end) {
+      const int page = __ldg(bt + key / kPage);
+      if (page >= 0 && page < a.num_pages) {
+        const int64_t at = (int64_t)page * a.Hkv + w.kvh;
+        raw = __ldg(reinterpret_cast<const uint4 *>((is_v ? a.v_cache : a.k_cache) + (at * kPage + key % kPage) * HD) + c);
+        sc = scale_value(__ldg((is_v ? a.v_scale : a.k_scale) + at));
+      } else {
+        raise_status(a.status, kStatusBadInput);
+      }
+    }
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+    float *dst = is_v ? &s.v[j][c * 16] : &s.k[j][c * 16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack_e4m3x2(u[i] & 0xffffu), g = unpack_e4m3x2(u[i] >> 16);
+      reinterpret_cast<float4 *>(dst)[i] = make_float4(f.x * sc, f.y * sc, g.x * sc, g.y * sc);
+    }
+  }
+}
+
+// The same of a 4-bit cache: a thread takes 16 elements of a key, or of the two
+// values that share their bytes.
+template <int HD>
+__device__ __forceinline__ void load_tile4(const KvqParams &a, const KvqWork &w, const int32_t *bt, int base,
+                                           SimtSmem<HD> &s) {
+  using R = Record<HD>;
+  constexpr int CH = HD / 16;
+  for (int e = threadIdx.x; e < (kTile + kTile / 2) * CH; e += kThreads) {
+    const bool is_v = e >= kTile * CH;
+    const int j = is_v ? (e - kTile * CH) / CH * 2 : e / CH, c = e % CH, key = base + j;
+    const uint8_t *rec = nullptr;
+    if (key < w.k_end) {
+      const int page = __ldg(bt + key / kPage);
+      if (page >= 0 && page < a.num_pages) rec = a.k_cache + ((int64_t)page * a.Hkv + w.kvh) * R::kBytes;
+      else raise_status(a.status, kStatusBadInput);
+    }
+    const int slot = key % kPage;
+    uint32_t x[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u}, y[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (rec != nullptr && !is_v) {
+      const uint2 q = __ldg(reinterpret_cast<const uint2 *>(rec + slot * (HD / 2) + c * 8));
+      const uint32_t sc = scale4_twice(__ldg(rec + R::kKs + slot * (HD / 16) + c), 0);
+      const uint4 h = unpack_e2m1x8(q.x), g = unpack_e2m1x8(q.y);
+      const uint32_t u[8] = {h.x, h.y, h.z, h.w, g.x, g.y, g.z, g.w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = mul_f16x2(u[i], sc);
+    } else if (rec != nullptr) {
+      const uint4 q = __ldg(reinterpret_cast<const uint4 *>(rec + R::v_at(slot >> 1, c)));
+      const uint32_t sc = scale4_pair(__ldg(reinterpret_cast<const uint16_t *>(rec + R::vs_at(slot >> 1, c))));
+      const uint32_t q4[4] = {q.x, q.y, q.z, q.w};
+      const bool both = key + 1 < w.k_end;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 h = unpack_e2m1x8(q4[i]);
+        const uint32_t a0 = mul_f16x2(h.x, sc), a1 = mul_f16x2(h.y, sc), a2 = mul_f16x2(h.z, sc), a3 = mul_f16x2(h.w, sc);
+        x[2 * i] = __byte_perm(a0, a1, 0x5410);
+        x[2 * i + 1] = __byte_perm(a2, a3, 0x5410);
+        y[2 * i] = both ? __byte_perm(a0, a1, 0x7632) : 0u;
+        y[2 * i + 1] = both ? __byte_perm(a2, a3, 0x7632) : 0u;
+      }
+    }
+    float *dst = is_v ? &s.v[j][c * 16] : &s.k[j][c * 16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<float2 *>(dst + 2 * i) = f16x2_to_float2(x[i]);
+    if (is_v) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) *reinterpret_cast<float2 *>(&s.v[j + 1][c * 16 + 2 * i]) = f16x2_to_float2(y[i]);
+    }
+  }
+}
+
+template <typename T, int HD, bool FOUR>
 __global__ void __launch_bounds__(kThreads)
 kvq_simt_kernel(const __grid_constant__ KvqParams a) {
   constexpr int PER = HD / 32;           // columns of a lane
@@ -126,30 +208,8 @@ kvq_simt_kernel(const __grid_constant__ KvqParams a) {
     if (!fresh) {
       __syncthreads();                                   // the last tile is read
       there = kvq_low_bits(w.k_end - base);
-      constexpr int CH = HD / 16;                        // 16-byte chunks of a row
-      for (int e = threadIdx.x; e < 2 * kTile * CH; e += kThreads) {
-        const bool is_v = e >= kTile * CH;
-        const int j = (is_v ? e - kTile * CH : e) / CH, c = e % CH, key = base + j;
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        float sc = 0.f;
-        if (key < w.k_end) {
-          const int page = __ldg(bt + key / kPage);
-          if (page >= 0 && page < a.num_pages) {
-            const int64_t at = (int64_t)page * a.Hkv + w.kvh;
-            raw = __ldg(reinterpret_cast<const uint4 *>((is_v ? a.v_cache : a.k_cache) + (at * kPage + key % kPage) * HD) + c);
-            sc = scale_value(__ldg((is_v ? a.v_scale : a.k_scale) + at));
-          } else {
-            raise_status(a.status, kStatusBadInput);
-          }
-        }
-        const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-        float *dst = is_v ? &s.v[j][c * 16] : &s.k[j][c * 16];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = unpack_e4m3x2(u[i] & 0xffffu), g = unpack_e4m3x2(u[i] >> 16);
-          reinterpret_cast<float4 *>(dst)[i] = make_float4(f.x * sc, f.y * sc, g.x * sc, g.y * sc);
-        }
-      }
+      if constexpr (FOUR) load_tile4<HD>(a, w, bt, base, s);
+      else load_tile8<HD>(a, w, bt, base, s);
       // keys of pages outside the cache count as absent
       for (int q = 0; q < kTile / kPage; ++q) {
         const int key = base + q * kPage;
@@ -323,9 +383,9 @@ kvq_merge_kernel(const __grid_constant__ KvqParams a) {
   }
 }
 
-template <typename T, int HD>
+template <typename T, int HD, bool FOUR>
 cudaError_t launch_simt_t(const KvqPlan &p, const KvqParams &a, cudaStream_t stream) {
-  auto kern = kvq_simt_kernel<T, HD>;
+  auto kern = kvq_simt_kernel<T, HD, FOUR>;
   const int smem = (int)sizeof(SimtSmem<HD>);
   static std::atomic<uint64_t> configured{0};   // one bit per device
   const int dev = current_device();
@@ -355,22 +415,22 @@ struct Cut {
 // `uneven`) as many long ones as fit the SMs at once while the units' short
 // ends take turns on the SMs that are left (8 sequences of 32768 keys, 8 heads:
 // 64 units in halves 179 us, in 112 + 112 + 33 blocks 164).
-Cut cut_units(int64_t units, int64_t blocks, int64_t slots, bool uneven) {
-  Cut best = {blocks, 1, (double)((units + slots - 1) / slots * (blocks + kRamp))};
+Cut cut_units(int64_t units, int64_t blocks, int64_t slots, bool uneven, int64_t ramp) {
+  Cut best = {blocks, 1, (double)((units + slots - 1) / slots * (blocks + ramp))};
   auto merged = [&](int64_t n) { return 2.0 + 2.0 * (double)(units * n) / (double)slots; };
   const int64_t most = std::min<int64_t>(std::min<int64_t>(kMaxSplits, blocks), 4 * slots / units + 1);
   for (int64_t s = 2; s <= most; ++s) {
     const int64_t per = (blocks + s - 1) / s;
     if ((blocks + per - 1) / per < s) continue;            // same split as a smaller s
-    const double t = (double)((units * s + slots - 1) / slots * (per + kRamp)) + merged(s);
+    const double t = (double)((units * s + slots - 1) / slots * (per + ramp)) + merged(s);
     if (t < best.time) best = {per, s, t};
   }
   const int64_t e = std::min<int64_t>(slots / units, kMaxSplits - 1), left = slots - e * units;
   if (uneven && e > 0 && left > 0) {
     const int64_t k = (units + left - 1) / left;           // ends an SM takes in turn
-    const int64_t per = (k * (blocks + kRamp) - kRamp + k * e) / (1 + k * e);
+    const int64_t per = (k * (blocks + ramp) - ramp + k * e) / (1 + k * e);
     if (per > 0 && e * per < blocks && blocks - e * per <= per) {
-      const double t = (double)std::max(per + kRamp, k * (blocks - e * per + kRamp)) + merged(e + 1);
+      const double t = (double)std::max(per + ramp, k * (blocks - e * per + ramp)) + merged(e + 1);
       if (t < best.time) best = {per, e + 1, t};
     }
   }
@@ -381,14 +441,14 @@ Cut cut_units(int64_t units, int64_t blocks, int64_t slots, bool uneven) {
 // pieces to fill the last wave, as simsd_verify_attn's plan (64 sequences of
 // 4096 keys, 56 units of 512 in the fourth wave: 162 us whole, 156 in halves, 158
 // in 15 + 15 + 3 blocks).
-void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t slots, KvqPlan *p) {
+void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t slots, int64_t ramp, KvqPlan *p) {
   const int64_t blocks = std::max<int64_t>(1, (max_keys + kBlockKeys - 1) / kBlockKeys);
   const int64_t pairs = batch * units_per_seq, W = pairs / slots, r = pairs - W * slots;
-  Cut cut = cut_units(pairs, blocks, slots, true);
+  Cut cut = cut_units(pairs, blocks, slots, true, ramp);
   int64_t whole = cut.n > 1 ? 0 : pairs;
   if (W > 0 && r > 0) {
-    const Cut tail = cut_units(r, blocks, slots, false);
-    if (tail.n > 1 && (double)(W * (blocks + kRamp)) + tail.time < cut.time) {
+    const Cut tail = cut_units(r, blocks, slots, false, ramp);
+    if (tail.n > 1 && (double)(W * (blocks + ramp)) + tail.time < cut.time) {
       cut = tail;
       whole = W * slots;
     }
@@ -402,7 +462,7 @@ void plan_splits(int64_t batch, int64_t units_per_seq, int64_t max_keys, int64_t
   p->ranked = p->grid > slots && pairs < kOrderWaves * slots && batch > 1 && batch <= kOrderMax;
 }
 
-simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {
+simsd_status kvq_plan(const simsd_kvq_verify_desc *d, bool four, KvqPlan *p) {
   if (d == nullptr) return SIMSD_ERR_NULL;
   if (d->dtype != SIMSD_F32 && d->dtype != SIMSD_BF16) return SIMSD_ERR_DTYPE;
   const bool paired = d->order == SIMSD_ORDER_PAIRED;
@@ -425,13 +485,14 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {
   p->esize = d->dtype == SIMSD_BF16 ? 2 : 4;
   const int max_n = p->per * d->B_max;
   const bool tc = d->dtype == SIMSD_BF16;
-  p->rows_per_tile = tc ? 128 : kRows;
   const int64_t max_rows = (int64_t)max_n * p->G;
+  p->four = four;
+  p->rows_per_tile = !tc ? kRows : four ? kv4_rows_per_tile(max_rows) : 128;
   p->row_tiles = (int)((max_rows + p->rows_per_tile - 1) / p->rows_per_tile);
   const int64_t per_seq = (int64_t)d->num_kv_heads * p->row_tiles;
   if (per_seq * d->batch * 64 >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
   plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens,
-              (tc ? 1 : 2) * device_sm_count(), p);
+              (!tc ? 2 : four ? kv4_ctas_per_sm(p->rows_per_tile) : 1) * device_sm_count(), tc && four ? 2 : kRamp, p);
   if ((int64_t)p->merge_seqs * max_n >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
   size_t off = kAlign;
   p->off_order = off;
@@ -451,8 +512,11 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, KvqPlan *p) {
 
 cudaError_t launch_kvq_simt(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                             cudaStream_t stream) {
-  return d->head_dim == 128 ? launch_simt_t<float, 128>(p, a, stream)
-                            : launch_simt_t<float, 64>(p, a, stream);
+  if (p.four)
+    return d->head_dim == 128 ? launch_simt_t<float, 128, true>(p, a, stream)
+                              : launch_simt_t<float, 64, true>(p, a, stream);
+  return d->head_dim == 128 ? launch_simt_t<float, 128, false>(p, a, stream)
+                            : launch_simt_t<float, 64, false>(p, a, stream);
 }
 
 cudaError_t launch_kvq_merge(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
@@ -466,20 +530,13 @@ cudaError_t launch_kvq_merge(const simsd_kvq_verify_desc *d, const KvqPlan &p, c
                             : launch_pdl(kvq_merge_kernel<float, 64>, grid, block, 0, stream, a);
 }
 
-}  // namespace simsd
+namespace {
 
-using namespace simsd;
-
-extern "C" {
-
-size_t simsd_kvq_verify_workspace_size(const simsd_kvq_verify_desc *d) {
+// The 8-bit cache's call, or (four) the 4-bit cache's, whose descriptor has been
+// brought to the same form: k_cache is its records, the other three are not read.
+simsd_status run_verify(const simsd_kvq_verify_desc *d, bool four, void *stream_ptr) {
   KvqPlan p;
-  return kvq_plan(d, &p) == SIMSD_OK ? p.total : 0;
-}
-
-simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream_ptr) {
-  KvqPlan p;
-  const simsd_status st = kvq_plan(d, &p);
+  const simsd_status st = kvq_plan(d, four, &p);
   if (st != SIMSD_OK) return st;
   if (!d->q || !d->k_cache || !d->v_cache || !d->k_scale || !d->v_scale || !d->block_table || !d->k_new ||
       !d->v_new || (d->order == SIMSD_ORDER_PAIRED && !d->tau) || !d->lens || !d->cu_B || !d->out)
@@ -526,9 +583,53 @@ simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream_ptr) 
     kvq_order_kernel<<<1, kOrderMax, 0, stream>>>(a);
     e = cudaGetLastError();
   }
-  if (e == cudaSuccess) e = d->dtype == SIMSD_BF16 ? launch_kvq_tc(d, p, a, stream) : launch_kvq_simt(d, p, a, stream);
+  if (e == cudaSuccess)
+    e = d->dtype != SIMSD_BF16 ? launch_kvq_simt(d, p, a, stream)
+        : four                 ? launch_kv4_mma(d, p, a, stream) : launch_kvq_tc(d, p, a, stream);
   if (e == cudaSuccess && p.n_splits > 1) e = launch_kvq_merge(d, p, a, stream);
   return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
+}
+
+// A 4-bit call's descriptor in the 8-bit call's form.
+simsd_kvq_verify_desc from_four(const simsd_kv4_verify_desc &f) {
+  simsd_kvq_verify_desc d;
+  d.batch = f.batch; d.num_q_heads = f.num_q_heads; d.num_kv_heads = f.num_kv_heads; d.head_dim = f.head_dim;
+  d.page_size = f.page_size; d.num_pages = f.num_pages; d.max_pages_per_seq = f.max_pages_per_seq;
+  d.total_B = f.total_B; d.B_max = f.B_max; d.dtype = f.dtype; d.order = f.order; d.node_size = f.node_size;
+  d.rope = f.rope; d.sm_scale = f.sm_scale; d.wait_polls = f.wait_polls;
+  d.q_row = f.q_row; d.k_row = f.k_row; d.v_row = f.v_row;
+  d.q = f.q; d.k_cache = d.v_cache = f.cache;
+  d.k_scale = d.v_scale = (const uint8_t *)f.cache;
+  d.block_table = f.block_table; d.k_new = f.k_new; d.v_new = f.v_new; d.tau = f.tau; d.lens = f.lens;
+  d.cu_B = f.cu_B; d.out = f.out; d.workspace = f.workspace; d.workspace_bytes = f.workspace_bytes;
+  return d;
+}
+
+}  // namespace
+}  // namespace simsd
+
+using namespace simsd;
+
+extern "C" {
+
+size_t simsd_kvq_verify_workspace_size(const simsd_kvq_verify_desc *d) {
+  KvqPlan p;
+  return kvq_plan(d, false, &p) == SIMSD_OK ? p.total : 0;
+}
+
+simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream) { return run_verify(d, false, stream); }
+
+size_t simsd_kv4_verify_workspace_size(const simsd_kv4_verify_desc *d) {
+  if (d == nullptr) return 0;
+  const simsd_kvq_verify_desc e = from_four(*d);
+  KvqPlan p;
+  return kvq_plan(&e, true, &p) == SIMSD_OK ? p.total : 0;
+}
+
+simsd_status simsd_kv4_verify(const simsd_kv4_verify_desc *d, void *stream) {
+  if (d == nullptr) return SIMSD_ERR_NULL;
+  const simsd_kvq_verify_desc e = from_four(*d);
+  return run_verify(&e, true, stream);
 }
 
 }  // extern "C"
