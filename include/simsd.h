@@ -941,7 +941,7 @@ simsd_status simsd_kv4_verify(const simsd_kv4_verify_desc *d, void *stream);
  * throughout or holds a NaN or +inf has NaN for logprob, entropy and
  * top_logprobs; its rank and ids are of no use (ids lie in 0..vocab-1).
  * Limits: 1 <= vocab <= 2^21; 0 <= rows <= 2^20; 0 <= top_k <= min(32, vocab);
- * T as in simsd_accept_desc.  rows = 0 returns SIMSD_OK.
+ * T as in simsd_accept_desc, at most 1e30.  rows = 0 returns SIMSD_OK.
  * Workspace: simsd_token_logprobs_workspace_size, 256 + rows * C * 48 bytes
  * rounded up to a multiple of 256, with C = ceil(vocab / 2048) + 1.
  * ---------------------------------------------------------------------- */

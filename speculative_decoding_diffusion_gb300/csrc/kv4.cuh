@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "vec.cuh"
 
 namespace simsd {
 
@@ -30,44 +31,55 @@ __device__ __forceinline__ float scale4_value(uint32_t byte) { return __half2flo
 __device__ __forceinline__ uint32_t scale4_pair(uint32_t two) { return (two & 0xffu) << 7 | (two & 0xff00u) << 15; }
 __device__ __forceinline__ uint32_t scale4_twice(uint32_t two, int b) { return ((two >> (8 * b)) & 0xffu) * ((1u << 7) | (1u << 23)); }
 
+// x / s, correctly rounded, from 1 / s in two parts: hi the rounded reciprocal,
+// lo its remainder, x / s = x hi + x lo to 2^-47, rounded once.
+struct Reciprocal {
+  float hi, lo;
+};
+__device__ __forceinline__ Reciprocal reciprocal_of(float s) {
+  Reciprocal r;
+  r.hi = __frcp_rn(s);
+  r.lo = fmaf(-r.hi, s, 1.f) * r.hi;
+  return r;
+}
+__device__ __forceinline__ float2 over(float2 x, const Reciprocal &r) {
+  return fma_f32x2(x, make_float2(r.hi, r.hi), mul_f32x2(x, make_float2(r.lo, r.lo)));
+}
+
 // The scale byte of a group whose largest magnitude is amax (NaN if it holds
 // one): nearest to amax / 6, ties to the even byte.  The correctly rounded
 // quotient lies on the same side of every middle between two scales as the
 // exact one, and on it only where that does: m * 6 is exact for such a middle
-// m (five bits), and amax differs from it by a step of its own or more.
+// m (five bits), and amax differs from it by a step of its own or more.  The
+// same holds for codes below: a middle between two codes times a scale has
+// seven bits.
 __device__ __forceinline__ uint32_t scale4_of(float amax) {
-  if (!(amax < INFINITY)) return kScale4Nan;
-  const float q = fminf(__fdiv_rn(amax, 6.f), kScale4Max);
+  // 1 / 6 in two parts
+  const float q = fminf(fmaf(amax, 0x1.555556p-3f, amax * -0x1.555556p-28f), kScale4Max);
   const uint32_t u = __float_as_uint(q);
   const uint32_t normal = ((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - ((127u - 15u) << 3);
-  return q < 6.103515625e-5f ? (uint32_t)__float2int_rn(q * 131072.f) : normal;   // below 2^-14: steps of 2^-17
+  const uint32_t low = (uint32_t)__float2int_rn(q * 131072.f);   // below 2^-14: steps of 2^-17
+  return !(amax < INFINITY) ? kScale4Nan : q < 6.103515625e-5f ? low : normal;
 }
 
-// Elements to codes: x / s for a scale s, correctly rounded, so that a middle
-// between two codes is met exactly where x / s lies on it.  With r the
-// correctly rounded 1 / s, a product and one correction by the remainder give
-// that quotient (P. Markstein, Computation of elementary functions on the IBM
-// RISC System/6000, 1990).
-struct Scaler {
-  float s, r;
-};
-__device__ __forceinline__ Scaler scaler_of(uint32_t byte) {
-  Scaler c;
-  c.s = scale4_value(byte);
-  c.r = byte == 0u ? 0.f : __frcp_rn(c.s);         // no scale: codes of zero
-  return c;
-}
-__device__ __forceinline__ float over(float x, const Scaler &c) {
-  const float q = x * c.r;
-  return fmaf(fmaf(-q, c.s, x), c.r, q);
+// The factor from elements to codes; no scale: codes of zero.
+__device__ __forceinline__ Reciprocal scaler_of(uint32_t byte) {
+  const Reciprocal r = reciprocal_of(scale4_value(byte == 0u ? 0x78u : byte));
+  return byte == 0u ? Reciprocal{0.f, 0.f} : r;
 }
 
-// Two elements to a byte (nearest, ties to even, saturating), lo in the low bits.
-__device__ __forceinline__ uint32_t pack_e2m1x2(float lo, float hi) {
+// Eight elements to codes (nearest, ties to even, saturating), the first one in
+// the low bits.
+__device__ __forceinline__ uint32_t pack_e2m1x8(float2 a, float2 b, float2 c, float2 d) {
   uint32_t w;
-  asm("{\n\t.reg .b8 b;\n\t"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\t"
-      "cvt.u32.u8 %0, b;\n\t}" : "=r"(w) : "f"(lo), "f"(hi));
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(w)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
   return w;
 }
 

@@ -31,25 +31,43 @@ struct Append4Args {
   int Hkv;
 };
 
-// Sixteen elements to codes, two a byte, and their scale byte.
-__device__ __forceinline__ uint2 quantise16(const float *x, uint32_t *byte) {
-  float amax = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; i += 2) amax = absmax_nan(amax, x[i], x[i + 1]);
-  *byte = scale4_of(amax);
-  const Scaler c = scaler_of(*byte);
-  uint32_t w[2] = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 16; i += 2)
-    w[i / 8] |= pack_e2m1x2(over(x[i], c), over(x[i + 1], c)) << (4 * (i % 8));
-  return make_uint2(w[0], w[1]);
+// Sixteen elements, as pairs.
+struct Pairs {
+  float2 p[8];
+};
+
+template <typename T>
+__device__ __forceinline__ Pairs load16(const T *row) {
+  Pairs x;
+  load_vec<T, 8>(row, reinterpret_cast<float *>(x.p));
+  load_vec<T, 8>(row + 8, reinterpret_cast<float *>(x.p) + 8);
+  return x;
 }
 
+__device__ __forceinline__ uint32_t scale_of(const Pairs &x) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = absmax_nan(amax, x.p[i].x, x.p[i].y);
+  return scale4_of(amax);
+}
+
+// Sixteen elements to codes, two neighbours a byte.
+__device__ __forceinline__ uint2 codes_of(const Pairs &x, uint32_t byte) {
+  const Reciprocal r = scaler_of(byte);
+  return make_uint2(pack_e2m1x8(over(x.p[0], r), over(x.p[1], r), over(x.p[2], r), over(x.p[3], r)),
+                    pack_e2m1x8(over(x.p[4], r), over(x.p[5], r), over(x.p[6], r), over(x.p[7], r)));
+}
+
+// Where pair d's cosine (and, kPlane floats on, its sine) lies in a row of the
+// fast path's angles: lanes read 16 pairs each, 80 bytes apart.
+__device__ __forceinline__ int plane_at(int d) { return d + 4 * (d >> 4); }
+template <int HD> constexpr int kPlane = HD / 2 + HD / 8;
+
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 kv4_append_kernel(const __grid_constant__ Append4Args a) {
   using R = Record<HD>;
-  __shared__ __align__(16) float2 cs_s[kTileRows][HD / 2];
+  __shared__ __align__(16) float angle_s[kTileRows][2 * kPlane<HD>];
   __shared__ Row4 row_s[kTileRows];
   __shared__ int lead_s[kTileRows], n_lead_s;        // rows that write their value pair
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -68,14 +86,21 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
     if (leads) lead_s[__popc(m & ((1u << lane) - 1u))] = lane;
     if (lane == 0) n_lead_s = __popc(m);
   }
+  // half pairs in whole groups: cosines and sines apart; else as rotate8 takes them
+  const bool paired = !a.plan.interleaved && a.plan.half % 16 == 0;
   for (int e = threadIdx.x; e < kTileRows * (HD / 2); e += kThreads) {
     const int r = e / (HD / 2), d = e % (HD / 2);
-    if (row_s[r].page >= 0)
-      cs_s[r][angle_at(d)] = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, row_s[r].pos) : make_float2(1.f, 0.f);
+    if (row_s[r].page < 0) continue;
+    const float2 cs = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, row_s[r].pos) : make_float2(1.f, 0.f);
+    if (paired) {
+      angle_s[r][plane_at(d)] = cs.x;
+      angle_s[r][kPlane<HD> + plane_at(d)] = cs.y;
+    } else {
+      reinterpret_cast<float2 *>(angle_s[r])[angle_at(d)] = cs;
+    }
   }
   __syncthreads();
   constexpr int KL = HD / 32, VL = HD / 16;          // threads of a key row, of a value row
-  const bool paired = !a.plan.interleaved && a.plan.half % 16 == 0;
   const int turned = a.plan.half / 16;               // pairs of groups that are each other's partners
   for (int e = threadIdx.x; e < kTileRows * a.Hkv * KL; e += kThreads) {
     const int u = e % KL, rh = e / KL, h = rh % a.Hkv, r = rh / a.Hkv;
@@ -84,36 +109,38 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
     const T *src = (const T *)a.k + (int64_t)(row0 + r) * a.k_row + h * HD;
     const bool rot = paired && u < turned;
     const int g0 = rot ? u : paired ? 2 * turned + 2 * (u - turned) : 2 * u, g1 = rot ? u + turned : g0 + 1;
-    float x[16], y[16];
+    Pairs x, y;
     if (paired) {
-      load_vec<T, 8>(src + g0 * 16, x);
-      load_vec<T, 8>(src + g0 * 16 + 8, x + 8);
-      load_vec<T, 8>(src + g1 * 16, y);
-      load_vec<T, 8>(src + g1 * 16 + 8, y + 8);
+      x = load16(src + g0 * 16);
+      y = load16(src + g1 * 16);
       if (rot) {
+        const float *cs = angle_s[r] + plane_at(g0 * 16);
 #pragma unroll
-        for (int c = 0; c < 16; c += 8) {
-          float2 z[8];
-          load_angles8(cs_s[r], g0 * 16 + c, z);
+        for (int i = 0; i < 8; i += 2) {
+          const float4 c = *reinterpret_cast<const float4 *>(cs + 2 * i);
+          const float4 s = *reinterpret_cast<const float4 *>(cs + kPlane<HD> + 2 * i);
+          const float2 c2[2] = {make_float2(c.x, c.y), make_float2(c.z, c.w)};
+          const float2 s2[2] = {make_float2(s.x, s.y), make_float2(s.z, s.w)};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float p = x[c + i], q = y[c + i];
-            x[c + i] = p * z[i].x - q * z[i].y;
-            y[c + i] = q * z[i].x + p * z[i].y;
+          for (int k = 0; k < 2; ++k) {
+            const float2 p = x.p[i + k], q = y.p[i + k], ns = make_float2(-s2[k].x, -s2[k].y);
+            x.p[i + k] = fma_f32x2(p, c2[k], mul_f32x2(q, ns));
+            y.p[i + k] = fma_f32x2(q, c2[k], mul_f32x2(p, s2[k]));
           }
         }
       }
     } else {
+      const float2 *cs = reinterpret_cast<const float2 *>(angle_s[r]);
 #pragma unroll
       for (int c = 0; c < 16; c += 8) {
-        rotate8(a.plan, cs_s[r], src, g0 * 16 + c, x + c);
-        rotate8(a.plan, cs_s[r], src, g1 * 16 + c, y + c);
+        rotate8(a.plan, cs, src, g0 * 16 + c, reinterpret_cast<float *>(x.p) + c);
+        rotate8(a.plan, cs, src, g1 * 16 + c, reinterpret_cast<float *>(y.p) + c);
       }
     }
     uint8_t *rec = a.cache + ((int64_t)w.page * a.Hkv + h) * R::kBytes;
     const int slot = w.pos & (kPage - 1);
-    uint32_t b0, b1;
-    const uint2 c0 = quantise16(x, &b0), c1 = quantise16(y, &b1);
+    const uint32_t b0 = scale_of(x), b1 = scale_of(y);
+    const uint2 c0 = codes_of(x, b0), c1 = codes_of(y, b1);
     *reinterpret_cast<uint2 *>(rec + slot * (HD / 2) + g0 * 8) = c0;
     *reinterpret_cast<uint2 *>(rec + slot * (HD / 2) + g1 * 8) = c1;
     rec[R::kKs + slot * (HD / 16) + g0] = (uint8_t)b0;
@@ -126,32 +153,24 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
     const bool even = w.has(0), odd = w.has(1);
     const T *src = (const T *)a.v + (int64_t)(row0 + r) * a.v_row + h * HD + g * 16;
     const T *src_odd = (w.pos & 1) ? src : src + a.v_row;
-    float x[16], y[16];
+    Pairs x, y;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = y[i] = 0.f;
-    if (even) {
-      load_vec<T, 8>(src, x);
-      load_vec<T, 8>(src + 8, x + 8);
-    }
-    if (odd) {
-      load_vec<T, 8>(src_odd, y);
-      load_vec<T, 8>(src_odd + 8, y + 8);
-    }
+    for (int i = 0; i < 8; ++i) x.p[i] = y.p[i] = make_float2(0.f, 0.f);
+    if (even) x = load16(src);
+    if (odd) y = load16(src_odd);
     uint8_t *rec = a.cache + ((int64_t)w.page * a.Hkv + h) * R::kBytes;
     const int pair = (w.pos & (kPage - 1)) >> 1;
     uint32_t *codes = reinterpret_cast<uint32_t *>(rec + R::v_at(pair, g));
     uint8_t *scales = rec + R::vs_at(pair, g);
-    float ax = 0.f, ay = 0.f;
+    const uint32_t bx = scale_of(x), by = scale_of(y);
+    const Reciprocal rx = scaler_of(bx), ry = scaler_of(by);
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      ax = absmax_nan(ax, x[i], x[i + 1]);
-      ay = absmax_nan(ay, y[i], y[i + 1]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 u = over(x.p[2 * i], rx), u2 = over(x.p[2 * i + 1], rx);
+      const float2 v = over(y.p[2 * i], ry), v2 = over(y.p[2 * i + 1], ry);
+      c[i] = pack_e2m1x8(make_float2(u.x, v.x), make_float2(u.y, v.y), make_float2(u2.x, v2.x), make_float2(u2.y, v2.y));
     }
-    const uint32_t bx = scale4_of(ax), by = scale4_of(ay);
-    const Scaler cx = scaler_of(bx), cy = scaler_of(by);
-    uint32_t c[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int i = 0; i < 16; ++i) c[i / 4] |= pack_e2m1x2(over(x[i], cx), over(y[i], cy)) << (8 * (i % 4));
     if (even && odd) {
       *reinterpret_cast<uint4 *>(codes) = make_uint4(c[0], c[1], c[2], c[3]);
       *reinterpret_cast<uint16_t *>(scales) = (uint16_t)(bx | by << 8);

@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "vec.cuh"
 
 namespace simsd {
 namespace {
@@ -27,6 +28,8 @@ constexpr int kPart = 2048, kSeg = 256, kSegs = kPart / kSeg;
 constexpr int kLane = kPart / 32;          // entries of a lane
 constexpr int kPassThreads = 256, kFinishThreads = 256;
 constexpr int kMaxTop = 32;
+constexpr float kMaxTemperature = 1e30f;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kCand = 1024;                // entries that reach the k-th maximum, kept aside
 
 struct Part {
@@ -44,7 +47,7 @@ struct LogprobArgs {
   uint32_t *status;
   int64_t stride;
   int rows, vocab, top_k, n_parts;
-  float c, inv_c;                          // log2(e) / T; ln 2
+  float c, inv_c, inv_t;                   // log2(e) / T and its inverse; 1 / T
 };
 
 // Entries (of T) in 16 bytes.
@@ -56,29 +59,30 @@ __device__ __forceinline__ int lead_of(const T *row) {
   return (int)(((uintptr_t)row & 15u) / sizeof(T));
 }
 
-// The vector that begins at entry e (its address is 16-byte aligned), -inf for
-// entries outside 0..vocab-1.
+// The 16 bytes that begin at entry e (an aligned address), -inf for entries
+// outside 0..vocab-1.
 template <typename T>
-__device__ __forceinline__ void load_entries(const T *row, int e, int vocab, float *x) {
+__device__ __forceinline__ uint4 load_entries(const T *row, int e, int vocab) {
   constexpr int V = kVec<T>;
+  uint4 v;
   if (e >= 0 && e + V <= vocab) {
-    uint4 v;
     asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(row + e));
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if constexpr (V == 8) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-      } else {
-        x[i] = __uint_as_float(u[i]);
-      }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = e + i >= 0 && e + i < vocab ? Elem<T>::load(row + e + i) : -INFINITY;
+    return v;
   }
+  float x[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) x[i] = e + i >= 0 && e + i < vocab ? Elem<T>::load(row + e + i) : -INFINITY;
+  if constexpr (V == 8)
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+  else
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+}
+
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+__device__ __forceinline__ float2 bf16_pair(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -106,32 +110,91 @@ __device__ __forceinline__ float warp_sum(float x) {
   return x;
 }
 
+// What a lane does with 16 bytes of entries, by type.  bf16: maxima, the lower
+// bound and the counts are taken two entries at a time, as they lie.
+template <typename T> struct Lane;
+
+template <> struct Lane<float> {
+  static __device__ __forceinline__ float max_of(const uint4 &v) {
+    return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+  }
+  // the smallest value above x
+  static __device__ __forceinline__ float above(float x) { return nextafterf(x, INFINITY); }
+  // a value of the type that is at most x, and below y
+  static __device__ __forceinline__ float below(float x, float y) { return fminf(x, nextafterf(y, -INFINITY)); }
+  static __device__ __forceinline__ float2 pair(const uint4 &v, int i, float least) {
+    return i == 0 ? make_float2(at_least(__uint_as_float(v.x), least), at_least(__uint_as_float(v.y), least))
+                  : make_float2(at_least(__uint_as_float(v.z), least), at_least(__uint_as_float(v.w), least));
+  }
+  static __device__ __forceinline__ int count(const uint4 &v, float least) {
+    return (__uint_as_float(v.x) >= least) + (__uint_as_float(v.y) >= least) + (__uint_as_float(v.z) >= least) +
+           (__uint_as_float(v.w) >= least);
+  }
+  static __device__ __forceinline__ float entry(const uint4 &v, int j) { return __uint_as_float(word_of(v, j)); }
+};
+
+template <> struct Lane<__nv_bfloat16> {
+  static __device__ __forceinline__ __nv_bfloat162 two(uint32_t u) { return *reinterpret_cast<__nv_bfloat162 *>(&u); }
+  static __device__ __forceinline__ uint32_t bits(__nv_bfloat162 x) { return *reinterpret_cast<uint32_t *>(&x); }
+  static __device__ __forceinline__ float max_of(const uint4 &v) {
+    const float2 m = bf16_pair(bits(__hmax2(__hmax2(two(v.x), two(v.y)), __hmax2(two(v.z), two(v.w)))));
+    return fmaxf(m.x, m.y);
+  }
+  static __device__ __forceinline__ float above(float x) {       // (x is a bf16 value)
+    const uint32_t u = __float_as_uint(x + 0.f);
+    return x == INFINITY ? x : u == 0u ? __uint_as_float(0x00010000u)
+           : __uint_as_float((int32_t)u < 0 ? u - 0x10000u : u + 0x10000u);
+  }
+  static __device__ __forceinline__ float below(float x, float y) {
+    const uint32_t u = __float_as_uint(x);                       // towards -inf: a negative magnitude up, a positive one down
+    const float down = __uint_as_float(((int32_t)u < 0 ? u + 0xffffu : u) & 0xffff0000u);
+    const uint32_t w = __float_as_uint(y + 0.f);                 // (a bf16 value)
+    const float next = w == 0u ? __uint_as_float(0x80010000u) : __uint_as_float((int32_t)w < 0 ? w + 0x10000u : w - 0x10000u);
+    return fminf(down, next);
+  }
+  static __device__ __forceinline__ float2 pair(const uint4 &v, int i, float least) {
+    const __nv_bfloat162 l = __float2bfloat162_rn(least);        // (exact)
+    return bf16_pair(bits(__hmax2_nan(two(word_of(v, i)), l)));
+  }
+  static __device__ __forceinline__ int count(const uint4 &v, float least) {
+    const __nv_bfloat162 l = __float2bfloat162_rn(least);
+    const float2 n = bf16_pair(bits(__hadd2(__hadd2(__hge2(two(v.x), l), __hge2(two(v.y), l)),
+                                            __hadd2(__hge2(two(v.z), l), __hge2(two(v.w), l)))));
+    return (int)(n.x + n.y);
+  }
+  static __device__ __forceinline__ float entry(const uint4 &v, int j) {
+    const float2 x = bf16_pair(word_of(v, j >> 1));
+    return (j & 1) ? x.y : x.x;
+  }
+};
+
 template <typename T>
-__global__ void __launch_bounds__(kPassThreads)
+__global__ void __launch_bounds__(kPassThreads, sizeof(T) == 2 ? 4 : 2)
 logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int V = kVec<T>, N = kLane / V;              // vectors of a lane
+  using L = Lane<T>;
   const int lane = threadIdx.x & 31;
-  const int64_t item = (int64_t)blockIdx.x * (kPassThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t item = blockIdx.x * (kPassThreads / 32) + (threadIdx.x >> 5);
   grid_dep_wait();
   grid_dep_launch();
-  const int r = (int)(item / a.n_parts), part = (int)(item - (int64_t)r * a.n_parts);
+  const int r = (int)(item / (uint32_t)a.n_parts), part = (int)(item - (uint32_t)r * (uint32_t)a.n_parts);
   if (r >= a.rows) return;
   const int tok = a.tokens != nullptr ? __ldg(a.tokens + r) : -2;
   if (tok == -1) return;
   const T *row = (const T *)a.logits + r * a.stride;
   const int lead = lead_of(row), e0 = part * kPart - lead;
-  float x[kLane];
+  if (e0 >= a.vocab) return;                             // (the second pass counts parts as this line does)
+  uint4 v[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) load_entries<T>(row, e0 + (i * 32 + lane) * V, a.vocab, x + i * V);
+  for (int i = 0; i < N; ++i) v[i] = load_entries<T>(row, e0 + (i * 32 + lane) * V, a.vocab);
   const bool given = a.rank != nullptr && tok >= 0 && tok < a.vocab;
   const float mine = given ? Elem<T>::load(row + tok) : 0.f;
   float m = -INFINITY, sm = -INFINITY;
   float keep = -INFINITY;                                // lane i: maximum of segment i
+  constexpr int PER = kSeg / (32 * V);                   // vectors of a segment
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int j = 0; j < V; ++j) sm = fmaxf(sm, x[i * V + j]);
-    constexpr int PER = kSeg / (32 * V);                 // vectors of a segment
+    sm = fmaxf(sm, L::max_of(v[i]));
     if ((i + 1) % PER == 0) {
       sm = warp_max(sm);
       if (lane == i / PER) keep = sm;
@@ -144,35 +207,53 @@ logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
   int ahead = 0;
   if (given) {
     // before the token an equal entry is ahead too, behind it only a larger one
-    const float up = nextafterf(mine, INFINITY);
+    const float up = L::above(mine);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int e = e0 + (i * 32 + lane) * V;
-      const float least = e + V <= tok ? mine : up;
-#pragma unroll
-      for (int j = 0; j < V; ++j) ahead += x[i * V + j] >= least ? 1 : 0;
+      ahead += L::count(v[i], e + V <= tok ? mine : up);
       if (e <= tok && tok < e + V) {
 #pragma unroll
-        for (int j = 0; j < V; ++j) ahead += e + j < tok && e + j >= 0 && x[i * V + j] == mine ? 1 : 0;
+        for (int j = 0; j < V; ++j) ahead += e + j < tok && e + j >= 0 && L::entry(v[i], j) == mine ? 1 : 0;
       } else if (e < 0 && e + V <= tok && mine == -INFINITY) {
         ahead += e;                                      // (entries that do not exist)
       }
     }
     ahead = __reduce_add_sync(0xffffffffu, ahead);
   }
-  const float ref = m == -INFINITY ? 0.f : m;
-  float s0 = 0.f, s1 = 0.f, w0 = 0.f, w1 = 0.f;
+  // t = c l - c m with one rounding: c m rounded is off by `shift`, the same for
+  // every entry, so the sums are brought back by 2^shift.  Entries whose weight
+  // is 0 all the same are raised to where t is finite (0 times it has to be 0).
+  const float ref = m == -INFINITY ? 0.f : m, cm = ref * a.c;
+  const float least = L::below(fmaxf(ref - 1000.f * a.inv_c, -3e38f), ref);
+  float2 s2 = make_float2(0.f, 0.f), w2 = s2;
+  float shift = 0.f;
+  if (fabsf(cm) < 1e30f && least > -INFINITY) {
+    shift = -fmaf(ref, a.c, -cm);
+    const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-cm, -cm);
 #pragma unroll
-  for (int i = 0; i < kLane; i += 2) {
-    // (below -1000 the weight is 0, and 0 times it has to be 0)
-    const float t0 = at_least((x[i] - ref) * a.c, -1000.f), t1 = at_least((x[i + 1] - ref) * a.c, -1000.f);
-    const float p0 = ex2(t0), p1 = ex2(t1);
-    s0 += p0;
-    s1 += p1;
-    w0 = fmaf(p0, t0, w0);
-    w1 = fmaf(p1, t1, w1);
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        const float2 t = fma_f32x2(L::pair(v[i], j, least), c2, m2);
+        const float2 p = make_float2(ex2(t.x), ex2(t.y));
+        s2 = add_f32x2(s2, p);
+        w2 = fma_f32x2(p, t, w2);
+      }
+  } else {                                               // logits of 1e30 and beyond: differences first
+#pragma unroll 1
+    for (int i = 0; i < kLane; ++i) {
+      const int e = e0 + ((i / V) * 32 + lane) * V + i % V;
+      const float x = e >= 0 && e < a.vocab ? Elem<T>::load(row + e) : -INFINITY;
+      const float t = at_least((x - ref) * a.c, -1000.f), p = ex2(t);
+      s2.x += p;
+      w2.x = fmaf(p, t, w2.x);
+    }
   }
-  const float s = warp_sum(s0 + s1), w = warp_sum(w0 + w1);
+  float s = warp_sum(s2.x + s2.y), w = warp_sum(w2.x + w2.y);
+  const float back = ex2(shift);                         // c (l - m) = t + shift
+  w = fmaf(shift, s, w) * back;
+  s *= back;
   if (lane == 0) a.parts[at] = {m, s, w, ahead};
 }
 
@@ -289,9 +370,9 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   if (threadIdx.x == 0) {
     if (a.tokens != nullptr && !given) raise_status(a.status, kStatusBadInput);
     if (a.logprob != nullptr)
-      a.logprob[r] = given ? ((mine - m) * a.c - log_s) * a.inv_c : __uint_as_float(0x7fc00000u);
+      a.logprob[r] = given ? (mine - m) * a.inv_t - log_s * kLn2 : __uint_as_float(0x7fc00000u);
     if (a.rank != nullptr) a.rank[r] = given ? ahead : -1;
-    if (a.entropy != nullptr) a.entropy[r] = (log_s - w / s) * a.inv_c;
+    if (a.entropy != nullptr) a.entropy[r] = (log_s - w / s) * kLn2;
   }
   if (a.top_k == 0) return;
   // --------------------------------------------- the k segments that matter
@@ -355,7 +436,7 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   if (lane < k) {
     a.top_ids[(int64_t)r * k + lane] = list == 0ull ? 0 : index_of(list);
     a.top_logprobs[(int64_t)r * k + lane] =
-        list == 0ull ? __uint_as_float(0x7fc00000u) : ((value_of(list) - m) * a.c - log_s) * a.inv_c;
+        list == 0ull ? __uint_as_float(0x7fc00000u) : (value_of(list) - m) * a.inv_t - log_s * kLn2;
   }
 }
 
@@ -365,7 +446,7 @@ simsd_status check(const simsd_token_logprobs_desc *d) {
   if (d == nullptr) return SIMSD_ERR_NULL;
   if (d->dtype != SIMSD_F32 && d->dtype != SIMSD_BF16) return SIMSD_ERR_DTYPE;
   if (d->rows < 0 || d->rows > (1 << 20) || d->vocab < 1 || d->vocab > (1 << 21) || d->top_k < 0 ||
-      d->top_k > kMaxTop || d->top_k > d->vocab || !(d->temperature >= 0.0f) || !(d->temperature < INFINITY) ||
+      d->top_k > kMaxTop || d->top_k > d->vocab || !(d->temperature >= 0.0f) || !(d->temperature <= kMaxTemperature) ||
       d->row_stride < 0 || (d->row_stride != 0 && d->row_stride < d->vocab && d->rows > 1))
     return SIMSD_ERR_SHAPE;
   return SIMSD_OK;
@@ -418,7 +499,8 @@ simsd_status simsd_token_logprobs(const simsd_token_logprobs_desc *d, void *stre
   a.rows = d->rows; a.vocab = d->vocab; a.top_k = d->top_k;
   const double T = d->temperature == 0.0f ? 1.0 : (double)d->temperature;
   a.c = (float)(1.4426950408889634 / T);
-  a.inv_c = 0.6931471805599453f;
+  a.inv_c = (float)(T / 1.4426950408889634);
+  a.inv_t = (float)(1.0 / T);
   cudaStream_t stream = (cudaStream_t)stream_ptr;
   const cudaError_t e = d->dtype == SIMSD_BF16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
   return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;

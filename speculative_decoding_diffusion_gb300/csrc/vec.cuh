@@ -50,6 +50,24 @@ struct __align__(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Raw {
   T x[N];
 };
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t f32x2(float2 a) { return *reinterpret_cast<uint64_t *>(&a); }
+__device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(f32x2(a)), "l"(f32x2(b)), "l"(f32x2(c)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f32x2(a)), "l"(f32x2(b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(f32x2(a)), "l"(f32x2(b)));
+  return *reinterpret_cast<float2 *>(&d);
+}
+
 // max(m, |a|, |b|), NaN if any is.
 __device__ __forceinline__ float absmax_nan(float m, float a, float b) {
   float d;
