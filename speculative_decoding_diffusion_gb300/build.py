@@ -18,7 +18,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libsimsd.so")
 SOURCES = ["api.cu", "rope_append.cu", "attn_tc.cu", "attn_f32.cu", "accept.cu", "loop.cu",
            "rope_apply.cu", "page_map.cu", "kvq_append.cu", "kvq_attn.cu", "kvq_attn_tc.cu",
-           "kv4_append.cu", "kv4_read.cu", "kv4_attn_mma.cu", "logprobs.cu"]
+           "kv4_append.cu", "kv4_read.cu", "kv4_attn_mma.cu",
+           "kv4_attn_tc.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-Wall", "-I", INCLUDE, "-I", CSRC]

@@ -492,7 +492,7 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, bool four, KvqPlan *p) {
   const int64_t per_seq = (int64_t)d->num_kv_heads * p->row_tiles;
   if (per_seq * d->batch * 64 >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
   plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens,
-              (!tc ? 2 : four ? kv4_ctas_per_sm(p->rows_per_tile) : 1) * device_sm_count(), tc && four ? 2 : kRamp, p);
+              (!tc ? 2 : four ? kv4_ctas_per_sm(p->rows_per_tile) : 1) * device_sm_count(), tc && four && p->rows_per_tile <= 32 ? 2 : kRamp, p);
   if ((int64_t)p->merge_seqs * max_n >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
   size_t off = kAlign;
   p->off_order = off;
@@ -585,7 +585,8 @@ simsd_status run_verify(const simsd_kvq_verify_desc *d, bool four, void *stream_
   }
   if (e == cudaSuccess)
     e = d->dtype != SIMSD_BF16 ? launch_kvq_simt(d, p, a, stream)
-        : four                 ? launch_kv4_mma(d, p, a, stream) : launch_kvq_tc(d, p, a, stream);
+        : !four                ? launch_kvq_tc(d, p, a, stream)
+        : p.rows_per_tile <= 32 ? launch_kv4_mma(d, p, a, stream) : launch_kv4_tc(d, p, a, stream);
   if (e == cudaSuccess && p.n_splits > 1) e = launch_kvq_merge(d, p, a, stream);
   return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
 }

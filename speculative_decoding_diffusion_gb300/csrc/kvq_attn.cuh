@@ -154,6 +154,8 @@ int kv4_rows_per_tile(int64_t max_rows);
 int kv4_ctas_per_sm(int rows_per_tile);
 cudaError_t launch_kv4_mma(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                            cudaStream_t stream);
+cudaError_t launch_kv4_tc(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
+                          cudaStream_t stream);
 cudaError_t launch_kvq_merge(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                              cudaStream_t stream);
 
