@@ -9,17 +9,16 @@
 // tile, sequence); rows stack new tokens x heads of the group, so a byte of the
 // cache is read and decoded once for all of them.
 //   warp 0       one bulk copy per page (18 hd bytes: keys, values, scales)
-//   warps 6-10   codes times scales to f16 tiles, swizzled for the MMA, a page of
-//                keys or of values at a time, in turns; the keys of the next
-//                block before the values of this one
-//   warp 1       TMEM owner; issues the score MMAs; warp 15 the P V MMAs
-//   warps 2-5 and 11-14  softmax, two warps per 32 rows: one thread of each
-//                per row, half of the block's keys each (scores stay in
-//                registers from the maximum to the weights; the halves agree
-//                on the row's reference through shared memory).  Rows of
-//                tiles of at most 64 rows are replicated and the copies split
-//                the keys again
-// Warps 2-5 and 7-14 first rotate the query rows and the new keys; the new tokens are a
+//   warp 1       TMEM owner; issues the score MMAs; warp 2 the P V MMAs
+//   warp 3       nothing (its place keeps the softmax warps on their TMEM lanes)
+//   warps 4-11   softmax, two warps per 32 rows: one thread of each per row,
+//                half of the block's keys each; the halves agree on the row's
+//                reference through shared memory.  Rows of tiles of at most 64
+//                rows are replicated and the copies split the keys again
+//   warps 12-19  codes times scales to f16 tiles, swizzled for the MMA, a page of
+//                keys or of values each; the keys of the next block before the
+//                values of this one
+// Warps 4-19 first rotate the query rows and the new keys; the new tokens are a
 // block of their own ahead of the prompt.  Lanes of a decoding warp are set on
 // elements so that neither their reads nor their writes meet in a bank.
 // Every wait is bounded (status bit, drain, return).
@@ -41,14 +40,18 @@ constexpr int kKeys = 128;           // keys per block
 static_assert(kKeys == kBlockKeys, "split chunks are whole blocks");
 constexpr int kStages = 4;
 constexpr int kPagesPerBlock = kKeys / kPage;
-constexpr int kDecodeWarp = 6, kDecodeWarps = 5, kSoftmaxB = 11, kPvWarp = 15, kWarps = 16;
+constexpr int kPvWarp = 2, kSoftmaxWarp = 4, kDecodeWarp = 12, kWarps = 20;
 constexpr int kThreads = kWarps * 32;
-constexpr int kPrep = 12 * 32;         // threads of the softmax warps and the last four decoding ones
+constexpr int kPrep = 16 * 32;         // threads of the softmax and decoding warps
 constexpr int kHalves = 2;            // softmax warps sharing 32 rows
 constexpr int kGone = 16;             // blocks whose missing pages are kept (a producer is at most 7 ahead of a softmax)
 constexpr float kHeadroom = 8.f;     // log2 units a row max may grow before O is rescaled
 constexpr float kLift = 7.f;         // log2 of the largest weight right after that
-constexpr uint32_t kColS = 0;        // two score tiles: columns 0 and kKeys; the weights, f16, go over their scores
+constexpr uint32_t kColS = 0;        // two score tiles: columns 0 and kKeys
+// The weights, f16, two keys a column, go over the scores they come from: those
+// of keys 0..63 from the tile's first column on, those of 64..127 from its 65th,
+// so that neither of a row's two warps writes where the other still reads.
+__host__ __device__ constexpr uint32_t weight_col(int key) { return (uint32_t)((key & 64) + (key & 63) / 2); }
 constexpr uint32_t kColO = 2 * kKeys;
 
 enum { kBarFull = 0, kBarEmpty = kBarFull + kStages, kBarKbFull = kBarEmpty + kStages, kBarVbFull = kBarKbFull + 2,
@@ -212,9 +215,9 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   }
   // the threads that rotate rows, their index among them, and the pair whose
   // angles each of them makes (its plan requested here)
-  const bool prep_warp = warp >= 2 && warp != kDecodeWarp && warp != kPvWarp;
-  const int pt = threadIdx.x - (warp < kDecodeWarp ? 64 : 96), pair = (pt + 64) % (HD / 2);
-  static_assert(kPrep % (HD / 2) == 0, "a thread's angles are of one pair");
+  const bool prep_warp = warp >= kSoftmaxWarp;
+  const int pt = threadIdx.x - 32 * kSoftmaxWarp, pair = threadIdx.x % (HD / 2);
+  static_assert(kPrep % (HD / 2) == 0 && 32 * kSoftmaxWarp % (HD / 2) == 0, "a thread's angles are of one pair");
   const float turn_hi = plan_by_lane(a.plan).hi[pair], turn_lo = plan_by_lane(a.plan).lo[pair];
   grid_dep_wait();                           // the units' order is there
   grid_dep_launch();                         // the split merge may be scheduled
@@ -271,8 +274,8 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     for (int i = lane; i < kNumBars; i += 32) {
       const bool rows = i >= kBarPFull && i < kBarPFull + 2;
       const bool tiles = i >= kBarKbFull && i < kBarVbFull + 2;                  // a page at a time
-      mbar_init(bar(i), rows ? n_valid : tiles ? kPagesPerBlock : i >= kBarEmpty && i < kBarEmpty + kStages ? 2 * kPagesPerBlock
-                      : i == kBarQReady || i == kBarNewRead ? 4 : 1);
+      mbar_init(bar(i), rows ? n_valid : tiles ? kPagesPerBlock : i >= kBarEmpty && i < kBarEmpty + kStages ? kPagesPerBlock
+                      : i == kBarQReady ? 4 : i == kBarNewRead ? kPagesPerBlock : 1);
     }
     if (lane == 0) {
       *flag_s = 0;
@@ -468,27 +471,28 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         if (depth == kKeys) {
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_bf16_ts(tmem + kColO, tP + kk * 8, dV + kk * 128, idO, j > 0 || kk > 0);
+            tc::mma_bf16_ts(tmem + kColO, tP + weight_col(16 * kk), dV + kk * 128, idO, j > 0 || kk > 0);
         } else {
           for (int kk = 0; kk < depth / 16; ++kk)
-            tc::mma_bf16_ts(tmem + kColO, tP + kk * 8, dV + kk * 128, idO, j > 0 || kk > 0);
+            tc::mma_bf16_ts(tmem + kColO, tP + weight_col(16 * kk), dV + kk * 128, idO, j > 0 || kk > 0);
         }
         tc::commit(bar(kBarPvDone + tb));
       }
       __syncwarp();
     }
     if (!ok && lane == 0) give_up();
-  } else if (warp >= kDecodeWarp && warp < kSoftmaxB) {
+  } else if (warp >= kDecodeWarp) {
     // ------------------------------------------------------------- decode
-    const int dw = warp - kDecodeWarp;       // 0: not one of those that prepare
-    if (dw > 0) prepare();
+    const int pg = warp - kDecodeWarp;       // this warp's page of every block
+    static_assert(kWarps - kDecodeWarp == kPagesPerBlock, "a warp for each page");
+    prepare();
     // (the tiles hold the angles and rows until the query is in TMEM)
     bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
-    if (ok && fresh && dw > 0) {             // the new keys are the first key tile, the values the first value tile
-      if (dw == 1 && lane == 0) mbar_arrive_n(bar(kBarKbFull), kPagesPerBlock);
+    if (ok && fresh) {                       // the new keys are the first key tile, the values the first value tile
+      if (lane == 0) mbar_arrive(bar(kBarKbFull));
       const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew) + kMaxNew * HD;
 #pragma unroll 1
-      for (int e = 32 * (dw - 1) + lane; e < n_pad * CH; e += 128) {
+      for (int e = 32 * pg + lane; e < n_pad * CH; e += 32 * kPagesPerBlock) {
         const int j = e / CH, c = e % CH;
         const float vdown = new_inv_s[j];
         float v[8];
@@ -503,47 +507,42 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(kBarNewRead));
-        mbar_arrive_n(bar(kBarVbFull), kPagesPerBlock / 4);
+        mbar_arrive(bar(kBarVbFull));
       }
     }
-    // Steps: keys of block 0, then keys of block i + 1 and values of block i in
-    // turn; a step is eight pages, which the warps take one after another.
-    const int steps = n_past > 0 ? 2 * n_past : 0;
-    int seen = -1, jp = 0, valid = 0;
-    bool keys = true;
-    uint32_t gone = 0;
-    for (int id = dw; ok && id < steps * kPagesPerBlock; id += kDecodeWarps) {
-      const int step = id / kPagesPerBlock, pg = id % kPagesPerBlock;
-      if (step != seen) {
-        seen = step;
-        keys = step == 0 || ((step & 1) && step != steps - 1);
-        jp = step == 0 ? 0 : step == steps - 1 ? n_past - 1 : keys ? (step + 1) >> 1 : (step >> 1) - 1;
-        const int j = jp + fresh, tb = j & 1;
-        ok = mbar_wait_warp(bar(kBarFull + (jp & (kStages - 1))), (jp / kStages) & 1, a.polls) &&
-             (j < 2 || mbar_wait_warp(bar((keys ? kBarSFull : kBarPvDone) + tb), ((j >> 1) - 1) & 1, a.polls));
-        if (!ok) break;
-        gone = gone_s[jp & (kGone - 1)];
-        valid = w.k_end - w.k_begin - jp * kKeys;
-      }
-      const int tb = (jp + fresh) & 1, s = jp & (kStages - 1);
-      const uint8_t *rec = sb + L::kOffRing + s * L::kStage + pg * L::kRec;
-      if (keys) decode_keys<HD>(rec, sb + L::kOffKb + tb * L::kTile, pg, lane);
-      else decode_values<HD>(rec, sb + L::kOffVb + tb * L::kTile, pg, (gone >> pg) & 1u ? 0 : valid, lane);
+    auto keys = [&](int jp) {                // of prompt block jp
+      const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1);
+      if (!mbar_wait_warp(bar(kBarFull + s), (jp / kStages) & 1, a.polls) ||
+          (j >= 2 && !mbar_wait_warp(bar(kBarSFull + tb), ((j >> 1) - 1) & 1, a.polls)))
+        return false;
+      decode_keys<HD>(sb + L::kOffRing + s * L::kStage + pg * L::kRec, sb + L::kOffKb + tb * L::kTile, pg, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kBarKbFull + tb));
+      return true;
+    };
+    if (ok && n_past > 0) ok = keys(0);
+    for (int jp = 0; ok && jp < n_past; ++jp) {
+      if (jp + 1 < n_past && !keys(jp + 1)) { ok = false; break; }
+      const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1);
+      if (j >= 2 && !mbar_wait_warp(bar(kBarPvDone + tb), ((j >> 1) - 1) & 1, a.polls)) { ok = false; break; }
+      const int valid = (gone_s[jp & (kGone - 1)] >> pg) & 1u ? 0 : w.k_end - w.k_begin - jp * kKeys;
+      decode_values<HD>(sb + L::kOffRing + s * L::kStage + pg * L::kRec, sb + L::kOffVb + tb * L::kTile, pg, valid, lane);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar((keys ? kBarKbFull : kBarVbFull) + tb));
+        mbar_arrive(bar(kBarVbFull + tb));
         mbar_arrive(bar(kBarEmpty + s));
       }
     }
     if (!ok && lane == 0) give_up();
-  } else {
+  } else if (warp >= kSoftmaxWarp) {
     // ------------------------------------------------------------ softmax
     // With at most 64 real rows the tile's rows are replicated across the
     // four TMEM lane quadrants (R = 4 or 2 copies) and the copies split each
     // block's keys; every copy keeps its own reference, its weights of the
     // other copies' keys stay zero, and the epilogue merges the copies.
-    const int half = warp >= kSoftmaxB;
+    const int half = (warp - kSoftmaxWarp) >> 2;
     const int q4 = warp & 3;                 // TMEM lane quadrant of this warp
     const int groups = 4 / R;
     const int g = q4 % groups, kp = q4 / groups;
@@ -589,52 +588,62 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         constexpr bool is_new = decltype(newc)::value != 0;
         const int tb = is_new ? 0 : j & 1, jp = is_new ? -1 : j - fresh;
         const uint32_t tS = trow + kColS + tb * kKeys + k_lo;
-        float f = is_new ? 1.f : rscale;     // t = f s
         // keys that count: all of a whole block's, else one bit each
         const int valid = is_new ? 0 : w.k_end - w.k_begin - jp * kKeys;
         ok = ok && mbar_wait_warp(bar(kBarSFull + tb), (j >> 1) & 1, a.polls);
         const uint32_t gone = is_new || !ok ? 0u : gone_s[jp & (kGone - 1)];
         const bool whole = !is_new && valid >= kKeys && gone == 0u;
-        tc::fence_after_sync();
-        uint32_t sr[KW];
-        if constexpr (KW == 16) {
-          tc::ld16(tS, sr);
-        } else {
-#pragma unroll
-          for (int q = 0; q < KW; q += 32) tc::ld32(tS + q, sr + q);
+        const float f = whole ? rscale : 1.f;      // t = f s
+        uint64_t vis = 0;
+        if (is_new) {
+          vis = shift_right(newvis, k_lo);
+        } else if (!whole) {
+          vis = kvq_low_bits(valid - k_lo);
+          for (int i = 0; i < KW / 16; ++i)
+            if ((gone >> (k_lo / 16 + i)) & 1u) vis &= ~(0xffffull << (16 * i));
         }
-        tc::wait_ld();
-        tc::fence_before_sync();
-        // the row's maximum over both warps' keys
-        float mx = -INFINITY;
-        if (!whole) {                        // keys that do not count score -inf from here on
+        tc::fence_after_sync();
+        // the scores of this warp's keys CW q ..; where some do not count, as t
+        // with -inf for those.  (64 keys are read twice, 32 at a time: once for the
+        // maximum, once for the weights.  That leaves registers for 20 warps.)
+        constexpr int CW = KW < 32 ? KW : 32;
+        uint32_t sr[CW];
+        auto fetch = [&](int q) {
+          if constexpr (CW == 16) tc::ld16(tS, sr);
+          else tc::ld32(tS + CW * q, sr);
+          tc::wait_ld();
+          if (whole) return;
           if (is_new) {
-            const uint64_t vis = shift_right(newvis, k_lo);
 #pragma unroll
-            for (int i = 0; i < KW; i += 2) {
-              const float4 x = load_shared4(base + L::kOffNewKv + (k_lo + i) * 8);   // of two keys
-              sr[i] = __float_as_uint((vis >> i) & 1ull ? fmaf(__uint_as_float(sr[i]), x.x * rscale, x.y) : -INFINITY);
-              sr[i + 1] = __float_as_uint((vis >> i) & 2ull ? fmaf(__uint_as_float(sr[i + 1]), x.z * rscale, x.w) : -INFINITY);
+            for (int i = 0; i < CW; i += 2) {
+              const float4 x = load_shared4(base + L::kOffNewKv + (k_lo + CW * q + i) * 8);   // of two keys
+              const uint32_t v = (uint32_t)(vis >> (CW * q + i));
+              sr[i] = __float_as_uint(v & 1u ? fmaf(__uint_as_float(sr[i]), x.x * rscale, x.y) : -INFINITY);
+              sr[i + 1] = __float_as_uint(v & 2u ? fmaf(__uint_as_float(sr[i + 1]), x.z * rscale, x.w) : -INFINITY);
             }
           } else {
-            uint64_t vis = kvq_low_bits(valid - k_lo);
-            for (int i = 0; i < KW / 16; ++i)
-              if ((gone >> (k_lo / 16 + i)) & 1u) vis &= ~(0xffffull << (16 * i));
+            const uint32_t v = (uint32_t)(vis >> (CW * q));
 #pragma unroll
-            for (int i = 0; i < KW; ++i)
-              sr[i] = __float_as_uint((vis >> i) & 1ull ? __uint_as_float(sr[i]) * rscale : -INFINITY);
-            f = 1.f;
+            for (int i = 0; i < CW; ++i)
+              sr[i] = __float_as_uint((v >> i) & 1u ? __uint_as_float(sr[i]) * rscale : -INFINITY);
+          }
+        };
+        // the row's maximum over both warps' keys
+        float mx = -INFINITY;
+#pragma unroll
+        for (int q = 0; q < KW / CW; ++q) {
+          fetch(q);
+#pragma unroll
+          for (int i = 0; i < CW; i += 16) {
+            float v[16];
+#pragma unroll
+            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(sr[i + c]);
+            const float m0 = max3(max3(v[0], v[1], v[2]), v[3], v[4]), m1 = max3(max3(v[5], v[6], v[7]), v[8], v[9]);
+            const float m2 = max3(max3(v[10], v[11], v[12]), v[13], v[14]);
+            mx = fmaxf(mx, max3(max3(m0, m1, m2), v[15], v[15]) * f);
           }
         }
-#pragma unroll
-        for (int i = 0; i < KW; i += 16) {
-          float v[16];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(sr[i + c]);
-          const float m0 = max3(max3(v[0], v[1], v[2]), v[3], v[4]), m1 = max3(max3(v[5], v[6], v[7]), v[8], v[9]);
-          const float m2 = max3(max3(v[10], v[11], v[12]), v[13], v[14]);
-          mx = fmaxf(mx, max3(max3(m0, m1, m2), v[15], v[15]) * f);
-        }
+        tc::fence_before_sync();
         both_s[(tb * kHalves + half) * kRows] = ok ? mx : __uint_as_float(0x7fc00000u);
         pair_sync();
         const float theirs = both_s[(tb * kHalves + (half ^ 1)) * kRows];
@@ -650,7 +659,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
           for (int e = 0; e < KW / 2; ++e) z[e] = 0u;
 #pragma unroll
           for (int c = 1; c < RC; ++c) {
-            const uint32_t at = tW + ((kp + c) % RC) * KW + half * (KW / 2);
+            const uint32_t at = tW + weight_col((kp + c) % RC * 2 * KW) + half * (KW / 2);
             if constexpr (KW == 16) tc::st8(at, z);
             else tc::st16(at, z);
           }
@@ -663,27 +672,6 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         m_ref = m_new;
         // weights 2^(t - m_ref) as f16 pairs
         const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        if (is_new) {                        // the new tokens' share of the sum, key by key
-#pragma unroll
-          for (int i = 0; i < KW; i += 4) {
-            const float4 x = load_shared4(base + L::kOffNewInv + (k_lo + i) * 4);
-            l = fmaf(ex2(__uint_as_float(sr[i]) - mu), x.x, l);
-            l = fmaf(ex2(__uint_as_float(sr[i + 1]) - mu), x.y, l);
-            l = fmaf(ex2(__uint_as_float(sr[i + 2]) - mu), x.z, l);
-            l = fmaf(ex2(__uint_as_float(sr[i + 3]) - mu), x.w, l);
-          }
-        }
-        uint32_t pw[KW / 2];
-        const float2 f2 = make_float2(f, f), b2 = make_float2(-mu, -mu);
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int e = 0; e < KW / 2; ++e) {
-          const float2 x = fma_f32x2(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, b2);
-          const float2 p = make_float2(ex2(x.x), ex2(x.y));
-          sum = add_f32x2(sum, p);
-          pw[e] = pack_f16x2(p.x, p.y);
-        }
-        if (!is_new) l += sum.x + sum.y;
         // O's rows may be scaled once the previous block's P V is done
         if (!is_new && __any_sync(0xffffffffu, move) && j > 0) {
           if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; return true; }
@@ -698,13 +686,34 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
             tc::st16(tO + half * (HD / 2) + 16 * c, o);
           }
         }
-        const uint32_t tP = tW + k_lo / 2;
-        if constexpr (KW == 16) {
-          tc::st8(tP, pw);
-        } else {
+        const uint32_t tP = tW + weight_col(k_lo);
+        const float2 f2 = make_float2(f, f), b2 = make_float2(-mu, -mu);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int q = 0; q < KW / 2; q += 16) tc::st16(tP + q, pw + q);
+        for (int q = 0; q < KW / CW; ++q) {
+          if (KW > CW) fetch(q);
+          if (is_new) {                      // the new tokens' share of the sum, key by key
+#pragma unroll
+            for (int i = 0; i < CW; i += 4) {
+              const float4 x = load_shared4(base + L::kOffNewInv + (k_lo + CW * q + i) * 4);
+              l = fmaf(ex2(__uint_as_float(sr[i]) - mu), x.x, l);
+              l = fmaf(ex2(__uint_as_float(sr[i + 1]) - mu), x.y, l);
+              l = fmaf(ex2(__uint_as_float(sr[i + 2]) - mu), x.z, l);
+              l = fmaf(ex2(__uint_as_float(sr[i + 3]) - mu), x.w, l);
+            }
+          }
+          uint32_t pw[CW / 2];
+#pragma unroll
+          for (int e = 0; e < CW / 2; ++e) {
+            const float2 x = fma_f32x2(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, b2);
+            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+            sum = add_f32x2(sum, p);
+            pw[e] = pack_f16x2(p.x, p.y);
+          }
+          if constexpr (CW == 16) tc::st8(tP, pw);
+          else tc::st16(tP + CW / 2 * q, pw);
         }
+        if (!is_new) l += sum.x + sum.y;
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
