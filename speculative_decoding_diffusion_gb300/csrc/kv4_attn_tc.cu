@@ -15,9 +15,8 @@
 //                half of the block's keys each; the halves agree on the row's
 //                reference through shared memory.  Rows of tiles of at most 64
 //                rows are replicated and the copies split the keys again
-//   warps 12-19  codes times scales to f16 tiles, swizzled for the MMA, a page of
-//                keys or of values each; the keys of the next block before the
-//                values of this one
+//   warps 12-15  codes times scales to f16 tiles, swizzled for the MMA: two pages
+//                of a block's keys each; warps 16-19 of its values
 // Warps 4-19 first rotate the query rows and the new keys; the new tokens are a
 // block of their own ahead of the prompt.  Lanes of a decoding warp are set on
 // elements so that neither their reads nor their writes meet in a bank.
@@ -40,7 +39,9 @@ constexpr int kKeys = 128;           // keys per block
 static_assert(kKeys == kBlockKeys, "split chunks are whole blocks");
 constexpr int kStages = 4;
 constexpr int kPagesPerBlock = kKeys / kPage;
-constexpr int kPvWarp = 2, kSoftmaxWarp = 4, kDecodeWarp = 12, kWarps = 20;
+constexpr int kPvWarp = 2, kSoftmaxWarp = 4, kDecodeWarp = 12, kValueWarp = 16, kWarps = 20;
+constexpr int kDecoders = 4;          // warps for a tile
+constexpr int kPagesPerWarp = kPagesPerBlock / kDecoders;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPrep = 16 * 32;         // threads of the softmax and decoding warps
 constexpr int kHalves = 2;            // softmax warps sharing 32 rows
@@ -273,9 +274,9 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   if (warp == kPvWarp) {
     for (int i = lane; i < kNumBars; i += 32) {
       const bool rows = i >= kBarPFull && i < kBarPFull + 2;
-      const bool tiles = i >= kBarKbFull && i < kBarVbFull + 2;                  // a page at a time
-      mbar_init(bar(i), rows ? n_valid : tiles ? kPagesPerBlock : i >= kBarEmpty && i < kBarEmpty + kStages ? kPagesPerBlock
-                      : i == kBarQReady ? 4 : i == kBarNewRead ? kPagesPerBlock : 1);
+      const bool tiles = i >= kBarKbFull && i < kBarVbFull + 2;
+      mbar_init(bar(i), rows ? n_valid : tiles ? kDecoders : i >= kBarEmpty && i < kBarEmpty + kStages ? 2 * kDecoders
+                      : i == kBarQReady ? 4 : i == kBarNewRead ? kDecoders : 1);
     }
     if (lane == 0) {
       *flag_s = 0;
@@ -483,16 +484,16 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     if (!ok && lane == 0) give_up();
   } else if (warp >= kDecodeWarp) {
     // ------------------------------------------------------------- decode
-    const int pg = warp - kDecodeWarp;       // this warp's page of every block
-    static_assert(kWarps - kDecodeWarp == kPagesPerBlock, "a warp for each page");
+    const bool values = warp >= kValueWarp;
+    const int pg0 = (warp - (values ? kValueWarp : kDecodeWarp)) * kPagesPerWarp;   // this warp's pages of every block
     prepare();
     // (the tiles hold the angles and rows until the query is in TMEM)
     bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
-    if (ok && fresh) {                       // the new keys are the first key tile, the values the first value tile
-      if (lane == 0) mbar_arrive(bar(kBarKbFull));
+    if (ok && fresh && !values && lane == 0) mbar_arrive(bar(kBarKbFull));          // the new keys are the first key tile
+    if (ok && fresh && values) {             // the new values, as f16, are the first value tile
       const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew) + kMaxNew * HD;
 #pragma unroll 1
-      for (int e = 32 * pg + lane; e < n_pad * CH; e += 32 * kPagesPerBlock) {
+      for (int e = threadIdx.x - 32 * kValueWarp; e < n_pad * CH; e += 32 * kDecoders) {
         const int j = e / CH, c = e % CH;
         const float vdown = new_inv_s[j];
         float v[8];
@@ -510,28 +511,28 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         mbar_arrive(bar(kBarVbFull));
       }
     }
-    auto keys = [&](int jp) {                // of prompt block jp
+    // a tile is free when the product that read it is done: scores for keys, P V for values
+    const int free_bar = values ? kBarPvDone : kBarSFull, full_bar = values ? kBarVbFull : kBarKbFull;
+    for (int jp = 0; ok && jp < n_past; ++jp) {
       const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1);
       if (!mbar_wait_warp(bar(kBarFull + s), (jp / kStages) & 1, a.polls) ||
-          (j >= 2 && !mbar_wait_warp(bar(kBarSFull + tb), ((j >> 1) - 1) & 1, a.polls)))
-        return false;
-      decode_keys<HD>(sb + L::kOffRing + s * L::kStage + pg * L::kRec, sb + L::kOffKb + tb * L::kTile, pg, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kBarKbFull + tb));
-      return true;
-    };
-    if (ok && n_past > 0) ok = keys(0);
-    for (int jp = 0; ok && jp < n_past; ++jp) {
-      if (jp + 1 < n_past && !keys(jp + 1)) { ok = false; break; }
-      const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1);
-      if (j >= 2 && !mbar_wait_warp(bar(kBarPvDone + tb), ((j >> 1) - 1) & 1, a.polls)) { ok = false; break; }
-      const int valid = (gone_s[jp & (kGone - 1)] >> pg) & 1u ? 0 : w.k_end - w.k_begin - jp * kKeys;
-      decode_values<HD>(sb + L::kOffRing + s * L::kStage + pg * L::kRec, sb + L::kOffVb + tb * L::kTile, pg, valid, lane);
+          (j >= 2 && !mbar_wait_warp(bar(free_bar + tb), ((j >> 1) - 1) & 1, a.polls))) { ok = false; break; }
+      const uint8_t *rec = sb + L::kOffRing + s * L::kStage + pg0 * L::kRec;
+      uint8_t *tile = sb + (values ? L::kOffVb : L::kOffKb) + tb * L::kTile;
+      if (values) {
+        const uint32_t gone = gone_s[jp & (kGone - 1)] >> pg0;
+        const int valid = w.k_end - w.k_begin - jp * kKeys;
+#pragma unroll
+        for (int i = 0; i < kPagesPerWarp; ++i)
+          decode_values<HD>(rec + i * L::kRec, tile, pg0 + i, (gone >> i) & 1u ? 0 : valid, lane);
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPagesPerWarp; ++i) decode_keys<HD>(rec + i * L::kRec, tile, pg0 + i, lane);
+      }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(bar(kBarVbFull + tb));
+        mbar_arrive(bar(full_bar + tb));
         mbar_arrive(bar(kBarEmpty + s));
       }
     }
