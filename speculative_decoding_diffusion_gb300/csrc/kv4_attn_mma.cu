@@ -563,7 +563,7 @@ cudaError_t launch_hd(const simsd_kvq_verify_desc *d, const KvqPlan &p, const Kv
 
 }  // namespace
 
-int kv4_rows_per_tile(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 128; }
+int kv4_rows_per_tile(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 128; }
 int kv4_ctas_per_sm(int rows_per_tile) {
   return rows_per_tile == 128 ? 1 : rows_per_tile == 32 ? 2 : rows_per_tile == 16 ? 3 : 4;
 }
