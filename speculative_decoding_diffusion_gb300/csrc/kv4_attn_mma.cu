@@ -27,17 +27,17 @@
 namespace simsd {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kBlock = 32;                 // keys that a warp takes at a time
 constexpr float kHeadroom = 8.f;           // log2 units a row's scores may outgrow its reference by
 constexpr float kLift = 7.f;               // log2 of the largest weight right after it moved
 
-template <int HD, int NT>
+template <int HD, int NT, int W>
 struct Lay {
+  static constexpr int kWarps = W, kThreads = 32 * W;
   static constexpr int kRows = 8 * NT;
   static constexpr int kRec = Record<HD>::kBytes, kStage = 2 * kRec;
-  static constexpr int kStages = HD == 64 ? 4 : NT == 1 ? 2 : 3;
-  static constexpr int kCtas = NT == 4 ? 2 : NT == 2 ? 3 : 4;   // of an SM
+  static constexpr int kStages = HD == 64 ? 4 : 2;
+  static constexpr int kCtas = W == 4 ? 4 : 2;             // of an SM
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kXld = 68;                      // floats of a row in the merge
   static constexpr int kOffQ = kRing;                  // query operands, lane by lane
@@ -53,10 +53,11 @@ struct Lay {
   static constexpr int kKnLd = HD * 2 + 16;            // bytes of a new key's row
   static_assert(kWarps * kRows * kXld * 4 <= kRing, "the merge fits the ring");
   static_assert(kOffVis % 8 == 0 && kOffBar % 8 == 0 && kOffNewKv % 8 == 0 && kOffDyn % 16 == 0, "alignment");
-  // new keys and values of up to n tokens and the angles of npos positions
+  // the query rows as they come; new keys and values of up to n tokens, and as
+  // they come; the angles of npos positions
   static int bytes(int n, int npos) {
     const int pad = (n + 15) & ~15;
-    return kOffDyn + pad * kKnLd + pad / 2 * HD * 4 + npos * (HD / 2) * 8;
+    return kOffDyn + kRows * HD * 2 + pad * kKnLd + pad / 2 * HD * 4 + 2 * n * HD * 2 + npos * (HD / 2) * 8;
   }
 };
 
@@ -100,11 +101,12 @@ __device__ __forceinline__ uint4 mul4(uint4 h, uint32_t s) {
 
 template <int V> struct IntC { static constexpr int value = V; };
 
-template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, (Lay<HD, NT>::kCtas))
+template <int HD, int NT, int W>
+__global__ void __launch_bounds__((Lay<HD, NT, W>::kThreads), (Lay<HD, NT, W>::kCtas))
 kv4_mma_kernel(const __grid_constant__ KvqParams a) {
-  using L = Lay<HD, NT>;
+  using L = Lay<HD, NT, W>;
   using R = Record<HD>;
+  constexpr int kWarps = L::kWarps, kThreads = L::kThreads;
   constexpr int J = HD / 32;               // words of codes of a lane and key = runs of 8 elements
   constexpr int MT = HD / 16;              // MMA tiles of the head's elements
   extern __shared__ __align__(128) uint8_t sb[];
@@ -166,10 +168,30 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
   for (; issued < min(mine, L::kStages); ++issued) issue(issued);
   // ------------------------------------------------------------------ set-up
   const int n_pad = (w.n + 15) & ~15;
-  uint8_t *kn = sb + L::kOffDyn;                       // [n_pad][kKnLd], f16
+  __nv_bfloat16 *q_raw = reinterpret_cast<__nv_bfloat16 *>(sb + L::kOffDyn), *k_raw = q_raw + L::kRows * HD;
+  __nv_bfloat16 *v_raw = k_raw + w.n * HD;
+  uint8_t *kn = reinterpret_cast<uint8_t *>(v_raw + w.n * HD);         // [n_pad][kKnLd], f16
   uint8_t *vn = kn + n_pad * L::kKnLd;                 // [n_pad / 2][HD] pairs of tokens, f16
   float2 *cs = reinterpret_cast<float2 *>(vn + n_pad / 2 * HD * 4);
   const int64_t t0 = (int64_t)a.per * w.c0;            // first new token's row
+  {
+    constexpr int CH = HD / 8;                         // 16-byte chunks of a row
+    const __nv_bfloat16 *qg = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
+    for (int e = threadIdx.x; e < L::kRows * CH; e += kThreads) {
+      const int r = e / CH, row = w.row0 + r, tok = div_by(row, a.by_G);
+      const bool take = r < rows;
+      copy16_async(smem_u32(q_raw + e * 8), take ? qg + tok * a.q_row + (row - tok * a.G) * HD + e % CH * 8 : (const void *)a.q, take);
+    }
+    if (fresh) {
+      const __nv_bfloat16 *kg = (const __nv_bfloat16 *)a.k_new + t0 * a.k_row + w.kvh * HD;
+      const __nv_bfloat16 *vg = (const __nv_bfloat16 *)a.v_new + t0 * a.v_row + w.kvh * HD;
+      for (int e = threadIdx.x; e < w.n * CH; e += kThreads) {
+        const int j = e / CH, c = e % CH * 8;
+        copy16_async(smem_u32(k_raw + e * 8), kg + j * a.k_row + c, true);
+        copy16_async(smem_u32(v_raw + e * 8), vg + j * a.v_row + c, true);
+      }
+    }
+  }
   const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
   if (threadIdx.x < 2) odd_s[threadIdx.x] = 0u;
   if (threadIdx.x == 0) *flag_s = 0;
@@ -179,25 +201,19 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
         d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, w.P + e / (HD / 2)) : make_float2(1.f, 0.f);
   }
   if (a.order == SIMSD_ORDER_PAIRED && threadIdx.x < w.B) tau_s[threadIdx.x] = __ldg(a.tau + w.c0 + threadIdx.x);
+  copy_async_wait_all();
   __syncthreads();
   constexpr int PL = HD / 16;                          // lanes of a row
-  const __nv_bfloat16 *qg = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
-  const __nv_bfloat16 *kg = (const __nv_bfloat16 *)a.k_new + t0 * a.k_row + w.kvh * HD;
-  const __nv_bfloat16 *vg = (const __nv_bfloat16 *)a.v_new + t0 * a.v_row + w.kvh * HD;
   const int n_q = L::kRows * PL, n_all = n_q + (fresh ? n_pad * PL : 0);   // (both whole warps)
 #pragma unroll 1
   for (int e = threadIdx.x; e < n_all; e += kThreads) {
     const bool query = e < n_q;
     const int r = (query ? e : e - n_q) / PL, c = e % PL;
     const bool real = query ? r < rows : r < w.n;
-    const int row = w.row0 + r, tok = !real ? 0 : query ? div_by(row, a.by_G) : r;
-    int c0 = 2 * c, c1 = 2 * c + 1;
-    float x[16], amax = 0.f, nan = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-    if (real)
-      rotate16(a.plan, cs + kvq_offset(a, w.B, tok) * (HD / 2),
-               query ? qg + tok * a.q_row + (row - tok * a.G) * HD : kg + tok * a.k_row, c, c0, c1, x);
+    const int tok = !real ? 0 : query ? div_by(w.row0 + r, a.by_G) : r;
+    int c0, c1;
+    float x[16], amax = 0.f, nan = 0.f;                // (query rows that do not exist are zeros)
+    rotate16(a.plan, cs + kvq_offset(a, w.B, tok) * (HD / 2), query ? q_raw + r * HD : k_raw + tok * HD, c, c0, c1, x);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {                     // (a NaN is not the maximum)
       nan = fmaf(x[i], 0.f, nan);
@@ -233,10 +249,13 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
     for (int e = threadIdx.x; e < n_pad * CH; e += kThreads) {            // (whole warps)
       const int j = e / CH, c = e % CH;
       float v[8], va = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.f;
       bool odd = false;
-      if (j < w.n) load_vec<__nv_bfloat16, 8>(vg + j * a.v_row + c * 8, v);
+      if (j < w.n) {
+        load_vec<__nv_bfloat16, 8>(v_raw + e * 8, v);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {                    // (an odd one times a weight of 0 would reach every row)
         odd |= !(fabsf(v[i]) < INFINITY);
@@ -539,10 +558,10 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
   }
 }
 
-template <int HD, int NT>
+template <int HD, int NT, int W>
 cudaError_t launch_nt(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a, cudaStream_t stream) {
-  using L = Lay<HD, NT>;
-  auto kern = kv4_mma_kernel<HD, NT>;
+  using L = Lay<HD, NT, W>;
+  auto kern = kv4_mma_kernel<HD, NT, W>;
   static std::atomic<uint64_t> configured{0};   // one bit per device
   const int dev = current_device();
   const uint64_t bit = (dev >= 0 && dev < 64) ? (1ull << dev) : 0;
@@ -552,21 +571,18 @@ cudaError_t launch_nt(const simsd_kvq_verify_desc *d, const KvqPlan &p, const Kv
     configured.fetch_or(bit);
   }
   const int n = p.per * d->B_max, npos = d->order == SIMSD_ORDER_NODES ? d->node_size : d->B_max;
-  return launch_pdl(kern, dim3((unsigned)p.grid), dim3(kThreads), L::bytes(n, npos), stream, a);
+  return launch_pdl(kern, dim3((unsigned)p.grid), dim3(L::kThreads), L::bytes(n, npos), stream, a);
 }
 
 template <int HD>
 cudaError_t launch_hd(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a, cudaStream_t stream) {
-  return p.rows_per_tile == 8    ? launch_nt<HD, 1>(d, p, a, stream)
-         : p.rows_per_tile == 16 ? launch_nt<HD, 2>(d, p, a, stream) : launch_nt<HD, 4>(d, p, a, stream);
+  return p.rows_per_tile == 16 ? launch_nt<HD, 2, 6>(d, p, a, stream)
+         : p.warps == 4        ? launch_nt<HD, 1, 4>(d, p, a, stream) : launch_nt<HD, 1, 8>(d, p, a, stream);
 }
 
 }  // namespace
 
 int kv4_rows_per_tile(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 128; }
-int kv4_ctas_per_sm(int rows_per_tile) {
-  return rows_per_tile == 128 ? 1 : rows_per_tile == 32 ? 2 : rows_per_tile == 16 ? 3 : 4;
-}
 
 cudaError_t launch_kv4_mma(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a, cudaStream_t stream) {
   return d->head_dim == 128 ? launch_hd<128>(d, p, a, stream) : launch_hd<64>(d, p, a, stream);

@@ -491,8 +491,14 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, bool four, KvqPlan *p) {
   p->row_tiles = (int)((max_rows + p->rows_per_tile - 1) / p->rows_per_tile);
   const int64_t per_seq = (int64_t)d->num_kv_heads * p->row_tiles;
   if (per_seq * d->batch * 64 >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
-  plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens,
-              (!tc ? 2 : four ? kv4_ctas_per_sm(p->rows_per_tile) : 1) * device_sm_count(), tc && four && p->rows_per_tile <= 32 ? 2 : kRamp, p);
+  const bool few = tc && four && p->rows_per_tile <= 16;
+  const int sms = device_sm_count();
+  // CTAs of an SM.  Few rows of a 4-bit cache: two, or where there are units for
+  // two waves of them four of half as many warps (256 sequences of 256..8192 keys,
+  // 4 rows: 214 and not 230 us; 64 of up to 4096, less than a wave: 55 and not 39).
+  p->warps = p->rows_per_tile == 16 ? 6 : per_seq * d->batch >= 8 * sms ? 4 : 8;
+  const int ctas = !tc ? 2 : !few ? 1 : p->warps == 4 ? 4 : 2;
+  plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens, ctas * sms, few ? 2 : kRamp, p);
   if ((int64_t)p->merge_seqs * max_n >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
   size_t off = kAlign;
   p->off_order = off;

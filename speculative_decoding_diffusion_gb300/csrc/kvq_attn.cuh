@@ -34,6 +34,7 @@ struct KvqPlan {
   int T, per, G, rows_per_tile, row_tiles;
   int n_splits, tail_from, s_tail, chunk_tail, tail_first, grid;
   bool four;                             // the 4-bit cache
+  int warps;                             // of a CTA (4-bit cache, few rows)
   bool ranked;                           // units by the sequences' lengths (kvq_order_kernel)
   int merge_seqs;                        // sequences (the last in the units' order) with split units
   size_t esize, off_order, off_opart, off_ml, total;
@@ -148,10 +149,8 @@ cudaError_t launch_kvq_simt(const simsd_kvq_verify_desc *d, const KvqPlan &p, co
                             cudaStream_t stream);
 cudaError_t launch_kvq_tc(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                           cudaStream_t stream);
-// The 4-bit cache, bf16: rows of a tile for units of up to max_rows rows, and the
-// CTAs of such tiles that an SM holds.
+// The 4-bit cache, bf16: rows of a tile for units of up to max_rows rows.
 int kv4_rows_per_tile(int64_t max_rows);
-int kv4_ctas_per_sm(int rows_per_tile);
 cudaError_t launch_kv4_mma(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                            cudaStream_t stream);
 cudaError_t launch_kv4_tc(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
