@@ -108,13 +108,21 @@ __device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
 }
 
 // ------------------------------------------------- rows of an append or a read
-constexpr int kTileRows = 16;              // rows that a CTA takes
+constexpr int kTileRows = 16;              // most rows that a CTA takes
 
 struct Rows4 {
   const int32_t *block_table, *start, *cu_n, *take;   // take: or null
   uint32_t *status;
   int batch, max_pages, num_pages, total_n;
+  int tile;                                // rows of a CTA: 16, or fewer where that leaves SMs without any
 };
+
+// 16 rows a CTA, halved while there would be fewer CTAs than SMs.
+inline int tile_rows4(int total_n) {
+  int t = kTileRows;
+  while (t > 1 && (total_n + t - 1) / t < device_sm_count()) t /= 2;
+  return t;
+}
 
 // Where a row lies: page id (-1: no row, or nothing to be done), position,
 // whether it is its sequence's first row and whether the next row is the

@@ -71,24 +71,33 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
   __shared__ Row4 row_s[kTileRows];
   __shared__ int lead_s[kTileRows], n_lead_s;        // rows that write their value pair
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.x * kTileRows;
+  const int tile = a.rows.tile, row0 = blockIdx.x * tile;
   grid_dep_wait();
   grid_dep_launch();
-  for (int r = warp; r < kTileRows; r += kThreads / 32) {
+  // the rows are on their way to L2 while their places are looked up
+  {
+    const int lines = a.Hkv * HD * (int)sizeof(T) / 128, n = min(tile, a.rows.total_n - row0);
+    for (int e = threadIdx.x; e < n * lines; e += kThreads) {
+      const int r = e / lines, at = e % lines * 128;
+      prefetch_l2((const char *)((const T *)a.k + (int64_t)(row0 + r) * a.k_row) + at);
+      prefetch_l2((const char *)((const T *)a.v + (int64_t)(row0 + r) * a.v_row) + at);
+    }
+  }
+  for (int r = warp; r < tile; r += kThreads / 32) {
     const Row4 w = find_row4(a.rows, row0 + r, lane);
     if (lane == 0) row_s[r] = w;
   }
   check_rows4(a.rows);
   __syncthreads();
   if (warp == 0) {
-    const bool leads = lane < kTileRows && row_s[lane].leads();
+    const bool leads = lane < tile && row_s[lane].leads();
     const uint32_t m = __ballot_sync(0xffffffffu, leads);
     if (leads) lead_s[__popc(m & ((1u << lane) - 1u))] = lane;
     if (lane == 0) n_lead_s = __popc(m);
   }
   // half pairs in whole groups: cosines and sines apart; else as rotate8 takes them
   const bool paired = !a.plan.interleaved && a.plan.half % 16 == 0;
-  for (int e = threadIdx.x; e < kTileRows * (HD / 2); e += kThreads) {
+  for (int e = threadIdx.x; e < tile * (HD / 2); e += kThreads) {
     const int r = e / (HD / 2), d = e % (HD / 2);
     if (row_s[r].page < 0) continue;
     const float2 cs = d < a.plan.half ? rope_plan_cs(plan_by_lane(a.plan), d, row_s[r].pos) : make_float2(1.f, 0.f);
@@ -102,7 +111,7 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
   __syncthreads();
   constexpr int KL = HD / 32, VL = HD / 16;          // threads of a key row, of a value row
   const int turned = a.plan.half / 16;               // pairs of groups that are each other's partners
-  for (int e = threadIdx.x; e < kTileRows * a.Hkv * KL; e += kThreads) {
+  for (int e = threadIdx.x; e < tile * a.Hkv * KL; e += kThreads) {
     const int u = e % KL, rh = e / KL, h = rh % a.Hkv, r = rh / a.Hkv;
     const Row4 w = row_s[r];
     if (w.page < 0) continue;
@@ -185,7 +194,7 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
 
 template <typename T>
 cudaError_t launch_append4(const Append4Args &a, int hd, cudaStream_t stream) {
-  const dim3 grid((unsigned)((a.rows.total_n + kTileRows - 1) / kTileRows)), block(kThreads);
+  const dim3 grid((unsigned)((a.rows.total_n + a.rows.tile - 1) / a.rows.tile)), block(kThreads);
   return hd == 128 ? launch_pdl(kv4_append_kernel<T, 128>, grid, block, 0, stream, a)
                    : launch_pdl(kv4_append_kernel<T, 64>, grid, block, 0, stream, a);
 }
@@ -216,7 +225,7 @@ extern "C" simsd_status simsd_kv4_append(const simsd_kv4_append_desc *d, void *s
     return SIMSD_ERR_WORKSPACE;
   if (d->total_n == 0) return SIMSD_OK;
   a.rows = {d->block_table, d->start, d->cu_n, d->take, (uint32_t *)d->workspace,
-            d->batch, d->max_pages_per_seq, d->num_pages, d->total_n};
+            d->batch, d->max_pages_per_seq, d->num_pages, d->total_n, tile_rows4(d->total_n)};
   a.k = d->k;
   a.v = d->v;
   a.cache = (uint8_t *)d->cache;

@@ -1,9 +1,7 @@
 // kv4_read.cu -- simsd_kv4_read: positions of the 4-bit cache back as rows.
 //
-// A CTA takes 16 rows of the output.  A thread takes one group: 16 elements of
-// a key, or of the two values that share their bytes; it multiplies codes by
-// their scale in f16 (exact) and writes 16 neighbouring elements of a row.
-// Bytes bound it: 9 in for every 16 elements, 16 to 64 out.
+// A CTA takes 16 rows of the output; codes are multiplied by their scale in f16
+// (exact).  Bytes bound it: 9 in for every 16 elements, 16 to 64 out.
 #include "kv4.cuh"
 #include "kvq.cuh"
 #include "vec.cuh"
@@ -21,40 +19,23 @@ struct Read4Args {
   int Hkv;
 };
 
-// Four elements of type T from two f16 pairs, as they lie in memory.
-template <typename T> struct Out4;
-template <> struct Out4<float> {
-  using type = float4;
-  static __device__ type of(float2 a, float2 b) { return make_float4(a.x, a.y, b.x, b.y); }
-};
-template <> struct Out4<__nv_bfloat16> {
-  using type = uint2;
-  static __device__ type of(float2 a, float2 b) { return make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y)); }
-};
-template <> struct Out4<__nv_fp8_e4m3> {
-  using type = uint32_t;
-  static __device__ float2 kept(float2 a) {                  // (the conversion would saturate an infinity)
-    return make_float2(fabsf(a.x) < INFINITY ? a.x : NAN, fabsf(a.y) < INFINITY ? a.y : NAN);
-  }
-  static __device__ type of(float2 a, float2 b) {
-    a = kept(a);
-    b = kept(b);
-    return pack_e4m3x2(a.x, a.y) | pack_e4m3x2(b.x, b.y) << 16;
-  }
-};
-
-// Sixteen elements, f16 pairs h, to a row.
-template <typename T>
-__device__ __forceinline__ void store16(T *dst, const uint32_t *h) {
-  constexpr int N = 16 / (4 * (int)sizeof(T));               // runs of four in 16 bytes
-#pragma unroll
-  for (int i = 0; i < 4; i += N) {
-    union { typename Out4<T>::type o[N]; uint4 v; } u;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      u.o[j] = Out4<T>::of(f16x2_to_float2(h[2 * (i + j)]), f16x2_to_float2(h[2 * (i + j) + 1]));
-    *reinterpret_cast<uint4 *>(dst + 4 * i) = u.v;
-  }
+// Eight elements, f16 pairs h, to a row.
+__device__ __forceinline__ void store8(float *dst, const uint4 &h) {
+  const float2 a = f16x2_to_float2(h.x), b = f16x2_to_float2(h.y), c = f16x2_to_float2(h.z), d = f16x2_to_float2(h.w);
+  reinterpret_cast<float4 *>(dst)[0] = make_float4(a.x, a.y, b.x, b.y);
+  reinterpret_cast<float4 *>(dst)[1] = make_float4(c.x, c.y, d.x, d.y);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16 *dst, const uint4 &h) {
+  const float2 a = f16x2_to_float2(h.x), b = f16x2_to_float2(h.y), c = f16x2_to_float2(h.z), d = f16x2_to_float2(h.w);
+  *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y),
+                                               pack_bf16x2(d.x, d.y));
+}
+__device__ __forceinline__ uint32_t e4m3x2(uint32_t h) {
+  const float2 f = f16x2_to_float2(h);                       // (the conversion would saturate an infinity)
+  return pack_e4m3x2(fabsf(f.x) < INFINITY ? f.x : NAN, fabsf(f.y) < INFINITY ? f.y : NAN);
+}
+__device__ __forceinline__ void store8(__nv_fp8_e4m3 *dst, const uint4 &h) {
+  *reinterpret_cast<uint2 *>(dst) = make_uint2(e4m3x2(h.x) | e4m3x2(h.y) << 16, e4m3x2(h.z) | e4m3x2(h.w) << 16);
 }
 
 template <typename T, int HD>
@@ -64,67 +45,93 @@ kv4_read_kernel(const __grid_constant__ Read4Args a) {
   __shared__ Row4 row_s[kTileRows];
   __shared__ int lead_s[kTileRows], n_lead_s;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row0 = blockIdx.x * kTileRows;
+  const int tile = a.rows.tile, row0 = blockIdx.x * tile;
   grid_dep_wait();
   grid_dep_launch();
-  for (int r = warp; r < kTileRows; r += kThreads / 32) {
+  for (int r = warp; r < tile; r += kThreads / 32) {
     const Row4 w = find_row4(a.rows, row0 + r, lane);
     if (lane == 0) row_s[r] = w;
   }
   check_rows4(a.rows);
   __syncthreads();
   if (warp == 0) {
-    const bool leads = lane < kTileRows && row_s[lane].leads();
+    const bool leads = lane < tile && row_s[lane].leads();
     const uint32_t m = __ballot_sync(0xffffffffu, leads);
     if (leads) lead_s[__popc(m & ((1u << lane) - 1u))] = lane;
     if (lane == 0) n_lead_s = __popc(m);
   }
   __syncthreads();
-  constexpr int L = HD / 16;                                 // threads of a row
+  // A thread takes eight elements of a key, or of the two values that share their
+  // bytes, so that neighbouring threads write neighbouring bytes; U of them are
+  // requested before the first is used.
+  constexpr int L = HD / 8, U = 4;                           // threads of a row
   const int n_lead = n_lead_s;
   if (a.k != nullptr)
-    for (int e = threadIdx.x; e < kTileRows * a.Hkv * L; e += kThreads) {
-      const int g = e % L, rh = e / L, h = rh % a.Hkv, r = rh / a.Hkv;
-      const Row4 w = row_s[r];
-      if (w.page < 0) continue;
-      const uint8_t *rec = a.cache + ((int64_t)w.page * a.Hkv + h) * R::kBytes;
-      const int slot = w.pos & (kPage - 1);
-      const uint2 c = __ldg(reinterpret_cast<const uint2 *>(rec + slot * (HD / 2) + g * 8));
-      const uint32_t s = scale4_twice(__ldg(rec + R::kKs + slot * (HD / 16) + g), 0);
-      const uint4 p = unpack_e2m1x8(c.x), q = unpack_e2m1x8(c.y);
-      uint32_t x[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w};
+    for (int e0 = threadIdx.x; e0 < tile * a.Hkv * L; e0 += U * kThreads) {
+      uint32_t c[U], sc[U];
+      T *dst[U];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = mul_f16x2(x[i], s);
-      store16((T *)a.k + (int64_t)(row0 + r) * a.k_row + h * HD + g * 16, x);
+      for (int i = 0; i < U; ++i) {
+        const int e = e0 + i * kThreads, u = e % L, rh = e / L, h = rh % a.Hkv, r = rh / a.Hkv;
+        const int page = r < tile ? row_s[r].page : -1;
+        c[i] = sc[i] = 0u;
+        dst[i] = nullptr;
+        if (page < 0) continue;
+        const uint8_t *rec = a.cache + ((int64_t)page * a.Hkv + h) * R::kBytes;
+        const int slot = row_s[r].pos & (kPage - 1);
+        c[i] = __ldg(reinterpret_cast<const uint32_t *>(rec + slot * (HD / 2) + u * 4));
+        sc[i] = __ldg(rec + R::kKs + slot * (HD / 16) + (u >> 1));
+        dst[i] = (T *)a.k + (int64_t)(row0 + r) * a.k_row + h * HD + u * 8;
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (dst[i] == nullptr) continue;
+        const uint32_t s = scale4_twice(sc[i], 0);
+        const uint4 p = unpack_e2m1x8(c[i]);
+        store8(dst[i], make_uint4(mul_f16x2(p.x, s), mul_f16x2(p.y, s), mul_f16x2(p.z, s), mul_f16x2(p.w, s)));
+      }
     }
   if (a.v != nullptr)
-    for (int e = threadIdx.x; e < n_lead * a.Hkv * L; e += kThreads) {
-      const int g = e % L, rh = e / L, h = rh % a.Hkv, r = lead_s[rh / a.Hkv];
-      const Row4 w = row_s[r];
-      const uint8_t *rec = a.cache + ((int64_t)w.page * a.Hkv + h) * R::kBytes;
-      const int pair = (w.pos & (kPage - 1)) >> 1;
-      const uint4 c = __ldg(reinterpret_cast<const uint4 *>(rec + R::v_at(pair, g)));
-      const uint32_t s = scale4_pair(__ldg(reinterpret_cast<const uint16_t *>(rec + R::vs_at(pair, g))));
-      const uint32_t w4[4] = {c.x, c.y, c.z, c.w};
-      uint32_t x[8], y[8];                                   // of the even and of the odd token
+    for (int e0 = threadIdx.x; e0 < n_lead * a.Hkv * L; e0 += U * kThreads) {
+      uint2 c[U];
+      uint32_t sc[U];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 p = unpack_e2m1x8(w4[i]);                // an element a pair: (even, odd)
-        const uint32_t a0 = mul_f16x2(p.x, s), a1 = mul_f16x2(p.y, s), a2 = mul_f16x2(p.z, s), a3 = mul_f16x2(p.w, s);
-        x[2 * i] = __byte_perm(a0, a1, 0x5410);
-        x[2 * i + 1] = __byte_perm(a2, a3, 0x5410);
-        y[2 * i] = __byte_perm(a0, a1, 0x7632);
-        y[2 * i + 1] = __byte_perm(a2, a3, 0x7632);
+      for (int i = 0; i < U; ++i) {
+        const int e = e0 + i * kThreads, u = e % L, rh = e / L, h = rh % a.Hkv, lead = rh / a.Hkv;
+        c[i] = make_uint2(0u, 0u);
+        sc[i] = 0u;
+        if (lead >= n_lead) continue;
+        const Row4 w = row_s[lead_s[lead]];
+        const uint8_t *rec = a.cache + ((int64_t)w.page * a.Hkv + h) * R::kBytes;
+        const int pair = (w.pos & (kPage - 1)) >> 1;
+        c[i] = __ldg(reinterpret_cast<const uint2 *>(rec + R::v_at(pair, u >> 1) + (u & 1) * 8));
+        sc[i] = __ldg(reinterpret_cast<const uint16_t *>(rec + R::vs_at(pair, u >> 1)));
       }
-      T *dst = (T *)a.v + (int64_t)(row0 + r) * a.v_row + h * HD + g * 16;
-      if (w.has(0)) store16(dst, x);
-      if (w.has(1)) store16((w.pos & 1) ? dst : dst + a.v_row, y);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int e = e0 + i * kThreads, u = e % L, rh = e / L, h = rh % a.Hkv, lead = rh / a.Hkv;
+        if (lead >= n_lead) continue;
+        const int r = lead_s[lead];
+        const Row4 w = row_s[r];
+        const uint32_t s = scale4_pair(sc[i]);
+        uint4 p = unpack_e2m1x8(c[i].x), q = unpack_e2m1x8(c[i].y);     // an element a pair: (even, odd) token
+        p = make_uint4(mul_f16x2(p.x, s), mul_f16x2(p.y, s), mul_f16x2(p.z, s), mul_f16x2(p.w, s));
+        q = make_uint4(mul_f16x2(q.x, s), mul_f16x2(q.y, s), mul_f16x2(q.z, s), mul_f16x2(q.w, s));
+        T *dst = (T *)a.v + (int64_t)(row0 + r) * a.v_row + h * HD + u * 8;
+        if (w.has(0))
+          store8(dst, make_uint4(__byte_perm(p.x, p.y, 0x5410), __byte_perm(p.z, p.w, 0x5410),
+                                 __byte_perm(q.x, q.y, 0x5410), __byte_perm(q.z, q.w, 0x5410)));
+        if (w.has(1))
+          store8((w.pos & 1) ? dst : dst + a.v_row,
+                 make_uint4(__byte_perm(p.x, p.y, 0x7632), __byte_perm(p.z, p.w, 0x7632),
+                            __byte_perm(q.x, q.y, 0x7632), __byte_perm(q.z, q.w, 0x7632)));
+      }
     }
 }
 
 template <typename T>
 cudaError_t launch_read4(const Read4Args &a, int hd, cudaStream_t stream) {
-  const dim3 grid((unsigned)((a.rows.total_n + kTileRows - 1) / kTileRows)), block(kThreads);
+  const dim3 grid((unsigned)((a.rows.total_n + a.rows.tile - 1) / a.rows.tile)), block(kThreads);
   return hd == 128 ? launch_pdl(kv4_read_kernel<T, 128>, grid, block, 0, stream, a)
                    : launch_pdl(kv4_read_kernel<T, 64>, grid, block, 0, stream, a);
 }
@@ -156,7 +163,7 @@ extern "C" simsd_status simsd_kv4_read(const simsd_kv4_read_desc *d, void *strea
     return SIMSD_ERR_WORKSPACE;
   if (d->total_n == 0) return SIMSD_OK;
   a.rows = {d->block_table, d->start, d->cu_n, nullptr, (uint32_t *)d->workspace,
-            d->batch, d->max_pages_per_seq, d->num_pages, d->total_n};
+            d->batch, d->max_pages_per_seq, d->num_pages, d->total_n, tile_rows4(d->total_n)};
   a.cache = (const uint8_t *)d->cache;
   a.k = d->k;
   a.v = d->v;

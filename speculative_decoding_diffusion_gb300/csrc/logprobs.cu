@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kPart = 2048, kSeg = 256, kSegs = kPart / kSeg;
 constexpr int kLane = kPart / 32;          // entries of a lane
-constexpr int kPassThreads = 256, kFinishThreads = 256;
+constexpr int kPassThreads = 256;
 constexpr int kMaxTop = 32;
 constexpr float kMaxTemperature = 1e30f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -59,17 +59,19 @@ __device__ __forceinline__ int lead_of(const T *row) {
   return (int)(((uintptr_t)row & 15u) / sizeof(T));
 }
 
+__device__ __forceinline__ uint4 load16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 // The 16 bytes that begin at entry e (an aligned address), -inf for entries
 // outside 0..vocab-1.
 template <typename T>
 __device__ __forceinline__ uint4 load_entries(const T *row, int e, int vocab) {
   constexpr int V = kVec<T>;
-  uint4 v;
-  if (e >= 0 && e + V <= vocab) {
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(row + e));
-    return v;
-  }
+  if (e >= 0 && e + V <= vocab) return load16(row + e);
   float x[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) x[i] = e + i >= 0 && e + i < vocab ? Elem<T>::load(row + e + i) : -INFINITY;
@@ -122,14 +124,23 @@ template <> struct Lane<float> {
   static __device__ __forceinline__ float above(float x) { return nextafterf(x, INFINITY); }
   // a value of the type that is at most x, and below y
   static __device__ __forceinline__ float below(float x, float y) { return fminf(x, nextafterf(y, -INFINITY)); }
-  static __device__ __forceinline__ float2 pair(const uint4 &v, int i, float least) {
+  using Bound = float;
+  static __device__ __forceinline__ Bound bound(float x) { return x; }
+  static __device__ __forceinline__ float2 pair(const uint4 &v, int i, Bound least) {
     return i == 0 ? make_float2(at_least(__uint_as_float(v.x), least), at_least(__uint_as_float(v.y), least))
                   : make_float2(at_least(__uint_as_float(v.z), least), at_least(__uint_as_float(v.w), least));
   }
-  static __device__ __forceinline__ int count(const uint4 &v, float least) {
-    return (__uint_as_float(v.x) >= least) + (__uint_as_float(v.y) >= least) + (__uint_as_float(v.z) >= least) +
+  // a running count of the entries of at least `least`
+  struct Count {
+    float least;
+    int n = 0;
+    __device__ explicit Count(float l) : least(l) {}
+    __device__ void add(const uint4 &v) {
+      n += (__uint_as_float(v.x) >= least) + (__uint_as_float(v.y) >= least) + (__uint_as_float(v.z) >= least) +
            (__uint_as_float(v.w) >= least);
-  }
+    }
+    __device__ int total() const { return n; }
+  };
   static __device__ __forceinline__ float entry(const uint4 &v, int j) { return __uint_as_float(word_of(v, j)); }
 };
 
@@ -152,16 +163,23 @@ template <> struct Lane<__nv_bfloat16> {
     const float next = w == 0u ? __uint_as_float(0x80010000u) : __uint_as_float((int32_t)w < 0 ? w + 0x10000u : w - 0x10000u);
     return fminf(down, next);
   }
-  static __device__ __forceinline__ float2 pair(const uint4 &v, int i, float least) {
-    const __nv_bfloat162 l = __float2bfloat162_rn(least);        // (exact)
-    return bf16_pair(bits(__hmax2_nan(two(word_of(v, i)), l)));
+  using Bound = __nv_bfloat162;
+  static __device__ __forceinline__ Bound bound(float x) { return __float2bfloat162_rn(x); }   // (exact)
+  static __device__ __forceinline__ float2 pair(const uint4 &v, int i, Bound least) {
+    return bf16_pair(bits(__hmax2_nan(two(word_of(v, i)), least)));
   }
-  static __device__ __forceinline__ int count(const uint4 &v, float least) {
-    const __nv_bfloat162 l = __float2bfloat162_rn(least);
-    const float2 n = bf16_pair(bits(__hadd2(__hadd2(__hge2(two(v.x), l), __hge2(two(v.y), l)),
-                                            __hadd2(__hge2(two(v.z), l), __hge2(two(v.w), l)))));
-    return (int)(n.x + n.y);
-  }
+  struct Count {                           // (exact: at most 32 in each half)
+    __nv_bfloat162 least, n;
+    __device__ explicit Count(float l) : least(__float2bfloat162_rn(l)), n(__float2bfloat162_rn(0.f)) {}
+    __device__ void add(const uint4 &v) {
+      n = __hadd2(n, __hadd2(__hadd2(__hge2(two(v.x), least), __hge2(two(v.y), least)),
+                             __hadd2(__hge2(two(v.z), least), __hge2(two(v.w), least))));
+    }
+    __device__ int total() const {
+      const float2 x = bf16_pair(bits(n));
+      return (int)(x.x + x.y);
+    }
+  };
   static __device__ __forceinline__ float entry(const uint4 &v, int j) {
     const float2 x = bf16_pair(word_of(v, j >> 1));
     return (j & 1) ? x.y : x.x;
@@ -185,8 +203,14 @@ logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
   const int lead = lead_of(row), e0 = part * kPart - lead;
   if (e0 >= a.vocab) return;                             // (the second pass counts parts as this line does)
   uint4 v[N];
+  if (e0 >= 0 && e0 + kPart <= a.vocab) {
+    const T *p = row + e0 + lane * V;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = load_entries<T>(row, e0 + (i * 32 + lane) * V, a.vocab);
+    for (int i = 0; i < N; ++i) v[i] = load16(p + i * 32 * V);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = load_entries<T>(row, e0 + (i * 32 + lane) * V, a.vocab);
+  }
   const bool given = a.rank != nullptr && tok >= 0 && tok < a.vocab;
   const float mine = given ? Elem<T>::load(row + tok) : 0.f;
   float m = -INFINITY, sm = -INFINITY;
@@ -208,15 +232,18 @@ logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
   if (given) {
     // before the token an equal entry is ahead too, behind it only a larger one
     const float up = L::above(mine);
+    if (tok < e0 || tok >= e0 + kPart) {                 // all behind it, or all before
+      typename L::Count n(tok < e0 ? up : mine);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = e0 + (i * 32 + lane) * V;
-      ahead += L::count(v[i], e + V <= tok ? mine : up);
-      if (e <= tok && tok < e + V) {
+      for (int i = 0; i < N; ++i) n.add(v[i]);
+      ahead = n.total();
+      if (tok >= e0 + kPart && mine == -INFINITY && e0 < 0 && lane == 0) ahead += e0;   // (entries that do not exist)
+    } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) ahead += e + j < tok && e + j >= 0 && L::entry(v[i], j) == mine ? 1 : 0;
-      } else if (e < 0 && e + V <= tok && mine == -INFINITY) {
-        ahead += e;                                      // (entries that do not exist)
+      for (int j = 0; j < kLane; ++j) {
+        const int e = e0 + ((j / V) * 32 + lane) * V + j % V;
+        const float x = L::entry(v[j / V], j % V);
+        ahead += x > mine || (x == mine && e < tok && e >= 0) ? 1 : 0;
       }
     }
     ahead = __reduce_add_sync(0xffffffffu, ahead);
@@ -231,11 +258,12 @@ logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
   if (fabsf(cm) < 1e30f && least > -INFINITY) {
     shift = -fmaf(ref, a.c, -cm);
     const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-cm, -cm);
+    const typename L::Bound low = L::bound(least);
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int j = 0; j < V / 2; ++j) {
-        const float2 t = fma_f32x2(L::pair(v[i], j, least), c2, m2);
+        const float2 t = fma_f32x2(L::pair(v[i], j, low), c2, m2);
         const float2 p = make_float2(ex2(t.x), ex2(t.y));
         s2 = add_f32x2(s2, p);
         w2 = fma_f32x2(p, t, w2);
@@ -298,10 +326,11 @@ __device__ __forceinline__ uint64_t add32(uint64_t list, uint64_t key, int k, in
   return merge32(list, sort32(key, lane), lane);
 }
 
-template <typename T>
+template <typename T, int kFinishThreads>
 __global__ void __launch_bounds__(kFinishThreads)
 logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int W = kFinishThreads / 32;
+  constexpr int AHEAD = 4;                               // maxima of a lane that are requested first of all
   __shared__ float red_s[3][W];
   __shared__ int ahead_s[W];
   __shared__ uint64_t list_s[W][32];
@@ -315,23 +344,26 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   const T *row = (const T *)a.logits + r * a.stride;
   const int lead = lead_of(row), n_parts = (a.vocab + lead + kPart - 1) / kPart;
   const Part *parts = a.parts + (int64_t)r * a.n_parts;
+  const int n_seg = (a.vocab + lead + kSeg - 1) / kSeg, k = a.top_k;
+  const float *seg_max = a.seg_max + (int64_t)r * a.n_parts * kSegs;
+  float first[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    const int j = threadIdx.x + i * kFinishThreads;
+    first[i] = k > 0 && j < n_seg ? __ldcg(seg_max + j) : 0.f;
+  }
   const bool given = tok >= 0 && tok < a.vocab;
   const float mine = given ? Elem<T>::load(row + tok) : 0.f;
   if (threadIdx.x == 0) n_cand_s = 0;
   // ------------------------------------------------------- the row's sums
-  constexpr int PER = (((1 << 21) / kPart + 1) + kFinishThreads - 1) / kFinishThreads;
-  Part p[PER];
-  float m = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int j = threadIdx.x + i * kFinishThreads;
-    p[i] = {-INFINITY, 0.f, 0.f, 0};
-    if (j < n_parts) {
-      const int4 v = __ldcg(reinterpret_cast<const int4 *>(parts + j));
-      p[i] = {__int_as_float(v.x), __int_as_float(v.y), __int_as_float(v.z), v.w};
-    }
-    m = fmaxf(m, p[i].m);
-  }
+  auto part = [&](int j) {
+    const int4 v = __ldcg(reinterpret_cast<const int4 *>(parts + j));
+    return Part{__int_as_float(v.x), __int_as_float(v.y), __int_as_float(v.z), v.w};
+  };
+  const bool any = threadIdx.x < n_parts;                // a thread's first part stays in registers
+  const Part p0 = any ? part(threadIdx.x) : Part{-INFINITY, 0.f, 0.f, 0};
+  float m = p0.m;
+  for (int j = threadIdx.x + kFinishThreads; j < n_parts; j += kFinishThreads) m = fmaxf(m, part(j).m);
   m = warp_max(m);
   if (lane == 0) red_s[0][warp] = m;
   __syncthreads();
@@ -339,16 +371,15 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   for (int i = 0; i < W; ++i) m = fmaxf(m, red_s[0][i]);
   float s = 0.f, w = 0.f;
   int ahead = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (threadIdx.x + i * kFinishThreads < n_parts) {
-      // a part that is -inf throughout has nothing but, maybe, a NaN in its sums
-      const float d = p[i].m == -INFINITY ? 0.f : at_least((p[i].m - m) * a.c, -1000.f), k = ex2(d);
-      s = fmaf(k, p[i].s, s);
-      w = fmaf(k, fmaf(d, p[i].s, p[i].w), w);
-      ahead += p[i].ahead;
-    }
-  }
+  auto add = [&](const Part &p) {
+    // a part that is -inf throughout has nothing but, maybe, a NaN in its sums
+    const float d = p.m == -INFINITY ? 0.f : at_least((p.m - m) * a.c, -1000.f), f = ex2(d);
+    s = fmaf(f, p.s, s);
+    w = fmaf(f, fmaf(d, p.s, p.w), w);
+    ahead += p.ahead;
+  };
+  if (any) add(p0);
+  for (int j = threadIdx.x + kFinishThreads; j < n_parts; j += kFinishThreads) add(part(j));
   s = warp_sum(s);
   w = warp_sum(w);
   ahead = __reduce_add_sync(0xffffffffu, ahead);
@@ -376,10 +407,14 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   }
   if (a.top_k == 0) return;
   // --------------------------------------------- the k segments that matter
-  const int n_seg = (a.vocab + lead + kSeg - 1) / kSeg, k = a.top_k;
-  const float *seg_max = a.seg_max + (int64_t)r * a.n_parts * kSegs;
   uint64_t list = 0;
-  for (int j0 = warp * 32; j0 < n_seg; j0 += kFinishThreads) {
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) {
+    const int j = threadIdx.x + i * kFinishThreads;
+    if (j - lane < n_seg) list = add32(list, j < n_seg ? key_of(first[i], j) : 0ull, k, lane);
+  }
+#pragma unroll 1
+  for (int j0 = AHEAD * kFinishThreads + warp * 32; j0 < n_seg; j0 += kFinishThreads) {
     const int j = j0 + lane;
     list = add32(list, j < n_seg ? key_of(__ldcg(seg_max + j), j) : 0ull, k, lane);
   }
@@ -462,7 +497,9 @@ cudaError_t launch(const LogprobArgs &a, cudaStream_t stream) {
   const int64_t items = (int64_t)a.rows * a.n_parts;
   const cudaError_t e = launch_pdl(logprob_pass_kernel<T>, dim3((unsigned)((items + W - 1) / W)), dim3(kPassThreads), 0, stream, a);
   if (e != cudaSuccess) return e;
-  return launch_pdl(logprob_finish_kernel<T>, dim3((unsigned)a.rows), dim3(kFinishThreads), 0, stream, a);
+  // few rows: more threads for each
+  return a.rows < 2 * device_sm_count() ? launch_pdl(logprob_finish_kernel<T, 256>, dim3((unsigned)a.rows), dim3(256), 0, stream, a)
+                                        : launch_pdl(logprob_finish_kernel<T, 128>, dim3((unsigned)a.rows), dim3(128), 0, stream, a);
 }
 
 }  // namespace
