@@ -220,6 +220,23 @@ __device__ __forceinline__ void grid_dep_launch() {
 }
 
 // ---------------------------------------------------------------- misc
+// n / d for 0 <= n < 2^31 (rounded-up reciprocal with one bit more than 32: the
+// method of Granlund and Montgomery).
+struct FastDiv {
+  uint32_t mul;
+  int shift, d;
+};
+
+inline FastDiv make_fast_div(int d) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  return {(uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - (uint64_t)d)) / (uint64_t)d + 1), l, d};
+}
+
+__device__ __forceinline__ int div_by(int n, const FastDiv &f) {
+  return (int)((__umulhi(f.mul, (uint32_t)n) + (uint32_t)n) >> f.shift);
+}
+
 __device__ __forceinline__ void prefetch_l2(const void *p) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
 }

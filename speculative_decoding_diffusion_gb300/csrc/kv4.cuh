@@ -136,49 +136,77 @@ struct Row4 {
   __device__ bool has(int odd) const { return (pos & 1) == odd || (odd == 1 && more); }
 };
 
-// Whether a sequence's numbers are out of range; its tokens to *n.
-__device__ __forceinline__ bool bad_sequence4(const Rows4 &a, int c0, int c1, int start, int b, int *n) {
-  *n = 0;
+// Whether a sequence's numbers are out of range; *n: its take, replaced by its
+// tokens where there is no such array.
+__device__ __forceinline__ bool bad_sequence4(const Rows4 &a, int c0, int c1, int start, int *n) {
   if (c0 < 0 || c1 < c0 || c1 > a.total_n || start < 0) return true;
-  *n = a.take != nullptr ? __ldg(a.take + b) : c1 - c0;
+  if (a.take == nullptr) *n = c1 - c0;
   return *n < 0 || *n > c1 - c0 || (int64_t)start + *n > (int64_t)a.max_pages * kPage;
 }
 
-// The row's place, found by a whole warp together: 32 bounds of cu_n are looked
-// at in each step (batch up to 32: one, up to 1024: two).  Where cu_n falls
-// somewhere a row may find none.
-__device__ __forceinline__ Row4 find_row4(const Rows4 &a, int row, int lane) {
-  Row4 w = {-1, 0, false, false};
-  if (row >= a.total_n) return w;
-  int lo = 0, hi = a.batch;                // the last b in [lo, hi) with cu_n[b] <= row
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-    const bool in = at < hi && __ldg(a.cu_n + at) <= row;
-    const uint32_t m = __ballot_sync(0xffffffffu, in);
-    const int k = m == 0u ? 0 : 31 - __clz(m);
-    lo += k * step;
-    hi = min(hi, lo + step);
+// The places of rows row0 + warp and row0 + warp + kWarps, found by the whole warp
+// for both at once: 32 bounds of cu_n are looked at in each step (batch up to
+// 32: one, up to 1024: two).  Where cu_n falls somewhere a row may find none.
+template <int kWarps>
+__device__ __forceinline__ void find_rows4(const Rows4 &a, int row0, int warp, int lane, Row4 *out) {
+  constexpr int N = kTileRows / kWarps;
+  int lo[N], hi[N];                        // the last b in [lo, hi) with cu_n[b] <= row
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    lo[i] = 0;
+    hi[i] = a.batch;
   }
-  const int b = lo;
-  const int c0 = __ldg(a.cu_n + b), c1 = __ldg(a.cu_n + b + 1), start = __ldg(a.start + b);
-  int n;
-  if (bad_sequence4(a, c0, c1, start, b, &n) || row < c0 || row - c0 >= n) return w;
-  const int i = row - c0;
-  w.pos = start + i;
-  w.first = i == 0;
-  w.more = i + 1 < n;
-  const int page = __ldg(a.block_table + (int64_t)b * a.max_pages + w.pos / kPage);
-  if (page >= 0 && page < a.num_pages) w.page = page;
-  else if (lane == 0) raise_status(a.status, kStatusBadInput);
-  return w;
+  for (int span = a.batch; span > 1; span = (span + 31) / 32) {
+    const int step = (span + 31) / 32;
+    uint32_t m[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = lo[i] + lane * step;
+      m[i] = __ballot_sync(0xffffffffu, at < hi[i] && __ldg(a.cu_n + at) <= row0 + warp + i * kWarps);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      lo[i] += (m[i] == 0u ? 0 : 31 - __clz(m[i])) * step;
+      hi[i] = min(hi[i], lo[i] + step);
+    }
+  }
+  int c0[N], c1[N], start[N], n[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    c0[i] = __ldg(a.cu_n + lo[i]);
+    c1[i] = __ldg(a.cu_n + lo[i] + 1);
+    start[i] = __ldg(a.start + lo[i]);
+    n[i] = a.take != nullptr ? __ldg(a.take + lo[i]) : -1;
+  }
+  int page[N];
+  bool any[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int row = row0 + warp + i * kWarps;
+    any[i] = row < a.total_n && !bad_sequence4(a, c0[i], c1[i], start[i], &n[i]) && row >= c0[i] && row - c0[i] < n[i];
+    page[i] = any[i] ? __ldg(a.block_table + (int64_t)lo[i] * a.max_pages + (start[i] + row - c0[i]) / kPage) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = warp + i * kWarps, k = row0 + r - c0[i];
+    Row4 w = {-1, 0, false, false};
+    if (any[i]) {
+      w.pos = start[i] + k;
+      w.first = k == 0;
+      w.more = k + 1 < n[i];
+      if (page[i] >= 0 && page[i] < a.num_pages) w.page = page[i];
+      else if (lane == 0 && r < a.tile) raise_status(a.status, kStatusBadInput);
+    }
+    if (lane == 0) out[r] = w;
+  }
 }
 
 // Every sequence's numbers, once in the grid.
 __device__ __forceinline__ void check_rows4(const Rows4 &a) {
   for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < a.batch; b += gridDim.x * blockDim.x) {
     const int c0 = __ldg(a.cu_n + b), c1 = __ldg(a.cu_n + b + 1), start = __ldg(a.start + b);
-    int n;
-    if (bad_sequence4(a, c0, c1, start, b, &n)) raise_status(a.status, kStatusBadInput);
+    int n = a.take != nullptr ? __ldg(a.take + b) : 0;
+    if (bad_sequence4(a, c0, c1, start, &n)) raise_status(a.status, kStatusBadInput);
   }
 }
 

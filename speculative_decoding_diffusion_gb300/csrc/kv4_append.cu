@@ -29,6 +29,7 @@ struct Append4Args {
   uint8_t *cache;
   int64_t k_row, v_row;
   int Hkv;
+  FastDiv by_kv;
 };
 
 // Sixteen elements, as pairs.
@@ -83,10 +84,7 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
       prefetch_l2((const char *)((const T *)a.v + (int64_t)(row0 + r) * a.v_row) + at);
     }
   }
-  for (int r = warp; r < tile; r += kThreads / 32) {
-    const Row4 w = find_row4(a.rows, row0 + r, lane);
-    if (lane == 0) row_s[r] = w;
-  }
+  find_rows4<kThreads / 32>(a.rows, row0, warp, lane, row_s);
   check_rows4(a.rows);
   __syncthreads();
   if (warp == 0) {
@@ -112,7 +110,7 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
   constexpr int KL = HD / 32, VL = HD / 16;          // threads of a key row, of a value row
   const int turned = a.plan.half / 16;               // pairs of groups that are each other's partners
   for (int e = threadIdx.x; e < tile * a.Hkv * KL; e += kThreads) {
-    const int u = e % KL, rh = e / KL, h = rh % a.Hkv, r = rh / a.Hkv;
+    const int u = e % KL, rh = e / KL, r = div_by(rh, a.by_kv), h = rh - r * a.Hkv;
     const Row4 w = row_s[r];
     if (w.page < 0) continue;
     const T *src = (const T *)a.k + (int64_t)(row0 + r) * a.k_row + h * HD;
@@ -157,7 +155,7 @@ kv4_append_kernel(const __grid_constant__ Append4Args a) {
   }
   const int n_lead = n_lead_s;
   for (int e = threadIdx.x; e < n_lead * a.Hkv * VL; e += kThreads) {
-    const int g = e % VL, rh = e / VL, h = rh % a.Hkv, r = lead_s[rh / a.Hkv];
+    const int g = e % VL, rh = e / VL, i = div_by(rh, a.by_kv), h = rh - i * a.Hkv, r = lead_s[i];
     const Row4 w = row_s[r];
     const bool even = w.has(0), odd = w.has(1);
     const T *src = (const T *)a.v + (int64_t)(row0 + r) * a.v_row + h * HD + g * 16;
@@ -230,6 +228,7 @@ extern "C" simsd_status simsd_kv4_append(const simsd_kv4_append_desc *d, void *s
   a.v = d->v;
   a.cache = (uint8_t *)d->cache;
   a.Hkv = d->num_kv_heads;
+  a.by_kv = make_fast_div(a.Hkv);
   cudaStream_t stream = (cudaStream_t)stream_ptr;
   const cudaError_t e = d->dtype == SIMSD_BF16 ? launch_append4<__nv_bfloat16>(a, d->head_dim, stream)
                                                : launch_append4<float>(a, d->head_dim, stream);

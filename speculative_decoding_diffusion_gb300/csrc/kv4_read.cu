@@ -17,25 +17,42 @@ struct Read4Args {
   void *k, *v;
   int64_t k_row, v_row;
   int Hkv;
+  FastDiv by_kv;
 };
 
-// Eight elements, f16 pairs h, to a row.
-__device__ __forceinline__ void store8(float *dst, const uint4 &h) {
-  const float2 a = f16x2_to_float2(h.x), b = f16x2_to_float2(h.y), c = f16x2_to_float2(h.z), d = f16x2_to_float2(h.w);
+// Elements that a thread takes at a time: 16 bytes of the output or more.
+template <typename T> constexpr int kItem = sizeof(T) == 1 ? 16 : 8;
+
+// N elements, f16 pairs h, to a row.
+__device__ __forceinline__ void store_item(float *dst, const uint32_t *h) {
+  const float2 a = f16x2_to_float2(h[0]), b = f16x2_to_float2(h[1]), c = f16x2_to_float2(h[2]), d = f16x2_to_float2(h[3]);
   reinterpret_cast<float4 *>(dst)[0] = make_float4(a.x, a.y, b.x, b.y);
   reinterpret_cast<float4 *>(dst)[1] = make_float4(c.x, c.y, d.x, d.y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *dst, const uint4 &h) {
-  const float2 a = f16x2_to_float2(h.x), b = f16x2_to_float2(h.y), c = f16x2_to_float2(h.z), d = f16x2_to_float2(h.w);
+__device__ __forceinline__ void store_item(__nv_bfloat16 *dst, const uint32_t *h) {
+  const float2 a = f16x2_to_float2(h[0]), b = f16x2_to_float2(h[1]), c = f16x2_to_float2(h[2]), d = f16x2_to_float2(h[3]);
   *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_bf16x2(a.x, a.y), pack_bf16x2(b.x, b.y), pack_bf16x2(c.x, c.y),
                                                pack_bf16x2(d.x, d.y));
 }
-__device__ __forceinline__ uint32_t e4m3x2(uint32_t h) {
-  const float2 f = f16x2_to_float2(h);                       // (the conversion would saturate an infinity)
-  return pack_e4m3x2(fabsf(f.x) < INFINITY ? f.x : NAN, fabsf(f.y) < INFINITY ? f.y : NAN);
+// Two f16 pairs as four e4m3 codes (nearest even, saturating).
+__device__ __forceinline__ uint32_t pack_e4m3x4(uint32_t a, uint32_t b) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 lo, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f16x2 hi, %2;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}" : "=r"(w) : "r"(a), "r"(b));
+  return w;
 }
-__device__ __forceinline__ void store8(__nv_fp8_e4m3 *dst, const uint4 &h) {
-  *reinterpret_cast<uint2 *>(dst) = make_uint2(e4m3x2(h.x) | e4m3x2(h.y) << 16, e4m3x2(h.z) | e4m3x2(h.w) << 16);
+__device__ __forceinline__ void store_item(__nv_fp8_e4m3 *dst, const uint32_t *h) {
+  *reinterpret_cast<uint4 *>(dst) = make_uint4(pack_e4m3x4(h[0], h[1]), pack_e4m3x4(h[2], h[3]), pack_e4m3x4(h[4], h[5]),
+                                               pack_e4m3x4(h[6], h[7]));
+}
+
+// A scale byte as the products take it: for e4m3, which has no infinity (and
+// whose conversion would make 448 of one), what is not finite is a NaN.
+template <typename T>
+__device__ __forceinline__ uint32_t scale_for(uint32_t byte) {
+  return sizeof(T) == 1 && byte >= 0xf8u ? kScale4Nan : byte;
 }
 
 template <typename T, int HD>
@@ -48,10 +65,7 @@ kv4_read_kernel(const __grid_constant__ Read4Args a) {
   const int tile = a.rows.tile, row0 = blockIdx.x * tile;
   grid_dep_wait();
   grid_dep_launch();
-  for (int r = warp; r < tile; r += kThreads / 32) {
-    const Row4 w = find_row4(a.rows, row0 + r, lane);
-    if (lane == 0) row_s[r] = w;
-  }
+  find_rows4<kThreads / 32>(a.rows, row0, warp, lane, row_s);
   check_rows4(a.rows);
   __syncthreads();
   if (warp == 0) {
@@ -61,70 +75,96 @@ kv4_read_kernel(const __grid_constant__ Read4Args a) {
     if (lane == 0) n_lead_s = __popc(m);
   }
   __syncthreads();
-  // A thread takes eight elements of a key, or of the two values that share their
-  // bytes, so that neighbouring threads write neighbouring bytes; U of them are
-  // requested before the first is used.
-  constexpr int L = HD / 8, U = 4;                           // threads of a row
+  // A thread takes N neighbouring elements of a key, or of the two values that
+  // share their bytes, so that neighbouring threads write neighbouring bytes; U of
+  // them are requested before the first is used.
+  constexpr int N = kItem<T>, L = HD / N, W = N / 8, U = sizeof(T) == 2 ? 1 : 2;  // L: threads of a row; W: words of a key's codes
   const int n_lead = n_lead_s;
   if (a.k != nullptr)
     for (int e0 = threadIdx.x; e0 < tile * a.Hkv * L; e0 += U * kThreads) {
-      uint32_t c[U], sc[U];
+      uint32_t c[U][W], sc[U];
       T *dst[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int e = e0 + i * kThreads, u = e % L, rh = e / L, h = rh % a.Hkv, r = rh / a.Hkv;
+        const int e = e0 + i * kThreads, u = e % L, rh = e / L, r = div_by(rh, a.by_kv), h = rh - r * a.Hkv;
         const int page = r < tile ? row_s[r].page : -1;
-        c[i] = sc[i] = 0u;
+        sc[i] = 0u;
         dst[i] = nullptr;
+#pragma unroll
+        for (int j = 0; j < W; ++j) c[i][j] = 0u;
         if (page < 0) continue;
         const uint8_t *rec = a.cache + ((int64_t)page * a.Hkv + h) * R::kBytes;
         const int slot = row_s[r].pos & (kPage - 1);
-        c[i] = __ldg(reinterpret_cast<const uint32_t *>(rec + slot * (HD / 2) + u * 4));
-        sc[i] = __ldg(rec + R::kKs + slot * (HD / 16) + (u >> 1));
-        dst[i] = (T *)a.k + (int64_t)(row0 + r) * a.k_row + h * HD + u * 8;
+        const uint8_t *src = rec + slot * (HD / 2) + u * (N / 2);
+        if constexpr (W == 2) {
+          const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
+          c[i][0] = x.x;
+          c[i][1] = x.y;
+        } else {
+          c[i][0] = __ldg(reinterpret_cast<const uint32_t *>(src));
+        }
+        sc[i] = __ldg(rec + R::kKs + slot * (HD / 16) + u * N / 16);
+        dst[i] = (T *)a.k + (int64_t)(row0 + r) * a.k_row + h * HD + u * N;
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         if (dst[i] == nullptr) continue;
-        const uint32_t s = scale4_twice(sc[i], 0);
-        const uint4 p = unpack_e2m1x8(c[i]);
-        store8(dst[i], make_uint4(mul_f16x2(p.x, s), mul_f16x2(p.y, s), mul_f16x2(p.z, s), mul_f16x2(p.w, s)));
+        const uint32_t s = scale4_twice(scale_for<T>(sc[i]), 0);
+        uint32_t x[4 * W];
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+          const uint4 p = unpack_e2m1x8(c[i][j]);
+          x[4 * j] = mul_f16x2(p.x, s);
+          x[4 * j + 1] = mul_f16x2(p.y, s);
+          x[4 * j + 2] = mul_f16x2(p.z, s);
+          x[4 * j + 3] = mul_f16x2(p.w, s);
+        }
+        store_item(dst[i], x);
       }
     }
   if (a.v != nullptr)
     for (int e0 = threadIdx.x; e0 < n_lead * a.Hkv * L; e0 += U * kThreads) {
-      uint2 c[U];
-      uint32_t sc[U];
+      uint32_t c[U][2 * W], sc[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int e = e0 + i * kThreads, u = e % L, rh = e / L, h = rh % a.Hkv, lead = rh / a.Hkv;
-        c[i] = make_uint2(0u, 0u);
+        const int e = e0 + i * kThreads, u = e % L, rh = e / L, lead = div_by(rh, a.by_kv), h = rh - lead * a.Hkv;
         sc[i] = 0u;
+#pragma unroll
+        for (int j = 0; j < 2 * W; ++j) c[i][j] = 0u;
         if (lead >= n_lead) continue;
         const Row4 w = row_s[lead_s[lead]];
         const uint8_t *rec = a.cache + ((int64_t)w.page * a.Hkv + h) * R::kBytes;
-        const int pair = (w.pos & (kPage - 1)) >> 1;
-        c[i] = __ldg(reinterpret_cast<const uint2 *>(rec + R::v_at(pair, u >> 1) + (u & 1) * 8));
-        sc[i] = __ldg(reinterpret_cast<const uint16_t *>(rec + R::vs_at(pair, u >> 1)));
+        const int pair = (w.pos & (kPage - 1)) >> 1, g = u * N / 16;
+        const uint8_t *src = rec + R::v_at(pair, g) + u * N % 16;
+        if constexpr (W == 2) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src));
+          c[i][0] = x.x; c[i][1] = x.y; c[i][2] = x.z; c[i][3] = x.w;
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src));
+          c[i][0] = x.x; c[i][1] = x.y;
+        }
+        sc[i] = __ldg(reinterpret_cast<const uint16_t *>(rec + R::vs_at(pair, g)));
       }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int e = e0 + i * kThreads, u = e % L, rh = e / L, h = rh % a.Hkv, lead = rh / a.Hkv;
+        const int e = e0 + i * kThreads, u = e % L, rh = e / L, lead = div_by(rh, a.by_kv), h = rh - lead * a.Hkv;
         if (lead >= n_lead) continue;
         const int r = lead_s[lead];
         const Row4 w = row_s[r];
-        const uint32_t s = scale4_pair(sc[i]);
-        uint4 p = unpack_e2m1x8(c[i].x), q = unpack_e2m1x8(c[i].y);     // an element a pair: (even, odd) token
-        p = make_uint4(mul_f16x2(p.x, s), mul_f16x2(p.y, s), mul_f16x2(p.z, s), mul_f16x2(p.w, s));
-        q = make_uint4(mul_f16x2(q.x, s), mul_f16x2(q.y, s), mul_f16x2(q.z, s), mul_f16x2(q.w, s));
-        T *dst = (T *)a.v + (int64_t)(row0 + r) * a.v_row + h * HD + u * 8;
-        if (w.has(0))
-          store8(dst, make_uint4(__byte_perm(p.x, p.y, 0x5410), __byte_perm(p.z, p.w, 0x5410),
-                                 __byte_perm(q.x, q.y, 0x5410), __byte_perm(q.z, q.w, 0x5410)));
-        if (w.has(1))
-          store8((w.pos & 1) ? dst : dst + a.v_row,
-                 make_uint4(__byte_perm(p.x, p.y, 0x7632), __byte_perm(p.z, p.w, 0x7632),
-                            __byte_perm(q.x, q.y, 0x7632), __byte_perm(q.z, q.w, 0x7632)));
+        const uint32_t s = scale4_pair(scale_for<T>(sc[i] & 0xffu) | scale_for<T>(sc[i] >> 8) << 8);
+        uint32_t x[4 * W], y[4 * W];                         // of the even and of the odd token
+#pragma unroll
+        for (int j = 0; j < 2 * W; ++j) {
+          const uint4 p = unpack_e2m1x8(c[i][j]);            // an element a pair: (even, odd)
+          const uint32_t p0 = mul_f16x2(p.x, s), p1 = mul_f16x2(p.y, s), p2 = mul_f16x2(p.z, s), p3 = mul_f16x2(p.w, s);
+          x[2 * j] = __byte_perm(p0, p1, 0x5410);
+          x[2 * j + 1] = __byte_perm(p2, p3, 0x5410);
+          y[2 * j] = __byte_perm(p0, p1, 0x7632);
+          y[2 * j + 1] = __byte_perm(p2, p3, 0x7632);
+        }
+        T *dst = (T *)a.v + (int64_t)(row0 + r) * a.v_row + h * HD + u * N;
+        if (w.has(0)) store_item(dst, x);
+        if (w.has(1)) store_item((w.pos & 1) ? dst : dst + a.v_row, y);
       }
     }
 }
@@ -168,6 +208,7 @@ extern "C" simsd_status simsd_kv4_read(const simsd_kv4_read_desc *d, void *strea
   a.k = d->k;
   a.v = d->v;
   a.Hkv = d->num_kv_heads;
+  a.by_kv = make_fast_div(a.Hkv);
   cudaStream_t stream = (cudaStream_t)stream_ptr;
   const cudaError_t e = d->dtype == SIMSD_F32    ? launch_read4<float>(a, d->head_dim, stream)
                         : d->dtype == SIMSD_BF16 ? launch_read4<__nv_bfloat16>(a, d->head_dim, stream)
