@@ -8,13 +8,12 @@
 //
 // First pass, every logit read once: a warp per part of 2048 entries, all of it
 // requested at once and held in registers; it leaves M, S, W, how many entries
-// are ahead of the row's token, and the maximum of each segment of 256.  The k
-// likeliest tokens lie in the k segments with the largest maxima (equal ones: the
-// first), since each of those has an entry ahead of any entry elsewhere.  So the
-// second pass, a CTA per row, merges the parts, picks k segments, reads them
-// again (k / 594 of a row of 151,936) and sorts the entries that reach the k-th
-// maximum.  A key of 64 bits, the value's ordered bits over the inverted index,
-// makes the order total.
+// are ahead of the row's token, and the maximum of each segment of 256.  The
+// second pass, a CTA per row, merges the parts; the k-th largest maximum over
+// any disjoint sets of segments is a bound that k entries reach, so only the
+// segments whose maximum reaches it are read again (some 22 of 594 for k = 20
+// and 151,936 entries) and only the entries that do are sorted.  A key of 64
+// bits, the value's ordered bits over the inverted index, makes the order total.
 #include <math.h>
 
 #include "common.cuh"
@@ -26,11 +25,11 @@ namespace {
 
 constexpr int kPart = 2048, kSeg = 256, kSegs = kPart / kSeg;
 constexpr int kLane = kPart / 32;          // entries of a lane
-constexpr int kPassThreads = 256;
+constexpr int kPassThreads = 128;
 constexpr int kMaxTop = 32;
 constexpr float kMaxTemperature = 1e30f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kCand = 1024;                // entries that reach the k-th maximum, kept aside
+constexpr int kSegList = 64, kCand = 1024;  // segments and entries that reach the bound, kept aside
 
 struct Part {
   float m, s, w;
@@ -187,7 +186,7 @@ template <> struct Lane<__nv_bfloat16> {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kPassThreads, sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(kPassThreads, sizeof(T) == 2 ? 8 : 4)
 logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
   constexpr int V = kVec<T>, N = kLane / V;              // vectors of a lane
   using L = Lane<T>;
@@ -286,23 +285,25 @@ logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
 }
 
 // ------------------------------------------------------------- order by keys
-__device__ __forceinline__ uint64_t key_of(float x, int i) {
+__device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);           // (-0 is 0)
-  return (uint64_t)(u ^ ((int32_t)u < 0 ? 0xffffffffu : 0x80000000u)) << 32 | (0xffffffffu - (uint32_t)i);
+  return u ^ ((int32_t)u < 0 ? 0xffffffffu : 0x80000000u);
 }
-__device__ __forceinline__ float value_of(uint64_t key) {
-  const uint32_t u = (uint32_t)(key >> 32);
-  return __uint_as_float(u ^ ((int32_t)u < 0 ? 0x80000000u : 0xffffffffu));
+__device__ __forceinline__ float value_of(uint32_t order) {
+  return __uint_as_float(order ^ ((int32_t)order < 0 ? 0x80000000u : 0xffffffffu));
 }
+__device__ __forceinline__ uint64_t key_of(float x, int i) { return (uint64_t)ordered(x) << 32 | (0xffffffffu - (uint32_t)i); }
 __device__ __forceinline__ int index_of(uint64_t key) { return (int)(0xffffffffu - (uint32_t)key); }
 
-__device__ __forceinline__ uint64_t exchange(uint64_t key, int lane, int j, bool down) {
-  const uint64_t other = __shfl_xor_sync(0xffffffffu, key, j);
+template <typename K>
+__device__ __forceinline__ K exchange(K key, int lane, int j, bool down) {
+  const K other = __shfl_xor_sync(0xffffffffu, key, j);
   return (((lane & j) == 0) == down) == (key > other) ? key : other;
 }
 
 // The warp's keys, largest in lane 0 (a bitonic sorting network).
-__device__ __forceinline__ uint64_t sort32(uint64_t key, int lane) {
+template <typename K>
+__device__ __forceinline__ K sort32(K key, int lane) {
 #pragma unroll
   for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
@@ -311,12 +312,29 @@ __device__ __forceinline__ uint64_t sort32(uint64_t key, int lane) {
 }
 
 // The 32 largest of two sorted lists.
-__device__ __forceinline__ uint64_t merge32(uint64_t a, uint64_t b, int lane) {
-  const uint64_t r = __shfl_sync(0xffffffffu, b, 31 - lane);
-  uint64_t key = a > r ? a : r;
+template <typename K>
+__device__ __forceinline__ K merge32(K a, K b, int lane) {
+  const K r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  K key = a > r ? a : r;
 #pragma unroll
   for (int j = 16; j > 0; j >>= 1) key = exchange(key, lane, j, true);
   return key;
+}
+
+// Warp 0's list: the 32 largest keys of all warps' lists, by way of at[].
+template <int W, typename K>
+__device__ __forceinline__ K merge_warps(K list, K (*at)[32], int warp, int lane) {
+  at[warp][lane] = list;
+  __syncthreads();
+#pragma unroll
+  for (int half = W / 2; half > 0; half >>= 1) {
+    if (warp < half) {
+      list = merge32(list, at[warp + half][lane], lane);
+      at[warp][lane] = list;
+    }
+    __syncthreads();
+  }
+  return list;
 }
 
 // `list` with a key a lane added (0: none); only the first k of it count.
@@ -334,8 +352,9 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   __shared__ float red_s[3][W];
   __shared__ int ahead_s[W];
   __shared__ uint64_t list_s[W][32];
+  __shared__ uint32_t top_s[W][32];
   __shared__ uint64_t cand_s[kCand];
-  __shared__ int n_cand_s;
+  __shared__ int seg_s[kSegList], n_cand_s, n_list_s;
   const int r = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   grid_dep_wait();
   grid_dep_launch();
@@ -354,7 +373,7 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   }
   const bool given = tok >= 0 && tok < a.vocab;
   const float mine = given ? Elem<T>::load(row + tok) : 0.f;
-  if (threadIdx.x == 0) n_cand_s = 0;
+  if (threadIdx.x == 0) n_cand_s = n_list_s = 0;
   // ------------------------------------------------------- the row's sums
   auto part = [&](int j) {
     const int4 v = __ldcg(reinterpret_cast<const int4 *>(parts + j));
@@ -406,72 +425,79 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
     if (a.entropy != nullptr) a.entropy[r] = (log_s - w / s) * kLn2;
   }
   if (a.top_k == 0) return;
-  // --------------------------------------------- the k segments that matter
-  uint64_t list = 0;
-#pragma unroll
-  for (int i = 0; i < AHEAD; ++i) {
+  // ------------------------------------------------ a bound for the k-th entry
+  // The k-th largest of the threads' maxima, each over the segments that are its
+  // own: k entries at least reach it, and few more do.
+  auto maximum = [&](int i) {                            // of this thread's segment i
     const int j = threadIdx.x + i * kFinishThreads;
-    if (j - lane < n_seg) list = add32(list, j < n_seg ? key_of(first[i], j) : 0ull, k, lane);
-  }
-#pragma unroll 1
-  for (int j0 = AHEAD * kFinishThreads + warp * 32; j0 < n_seg; j0 += kFinishThreads) {
-    const int j = j0 + lane;
-    list = add32(list, j < n_seg ? key_of(__ldcg(seg_max + j), j) : 0ull, k, lane);
-  }
-  list_s[warp][lane] = list;
-  __syncthreads();
-#pragma unroll 1
-  for (int half = W / 2; half > 0; half >>= 1) {
-    if (warp < half) {
-      list = merge32(list, list_s[warp + half][lane], lane);
-      list_s[warp][lane] = list;
-    }
-    __syncthreads();
-  }
-  const uint64_t last = list_s[0][k - 1];                // 0: fewer than k segments
-  const float least = last == 0ull ? -INFINITY : value_of(last);
-  // ---------------------------------------- their entries that reach the k-th
-  auto entry = [&](int i, int j) { return index_of(list_s[0][i]) * kSeg - lead + j; };   // entry j of segment i
-#pragma unroll 1
-  for (int i = warp; i < k; i += W) {
-    if (list_s[0][i] == 0ull) break;
-    float x[kSeg / 32];
+    return i < AHEAD ? first[i] : __ldcg(seg_max + j);
+  };
+  const int mine_n = (n_seg - (int)threadIdx.x + kFinishThreads - 1) / kFinishThreads;   // this thread's segments
+  float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < kSeg / 32; ++j) {
-      const int e = entry(i, j * 32 + lane);
-      x[j] = e >= 0 && e < a.vocab ? Elem<T>::load(row + e) : __uint_as_float(0x7fc00000u);
-    }
+  for (int i = 0; i < AHEAD; ++i)
+    if (i < mine_n) top = fmaxf(top, first[i]);
+  for (int i = AHEAD; i < mine_n; ++i) top = fmaxf(top, maximum(i));
+  (void)merge_warps<W>(sort32(mine_n > 0 ? ordered(top) : 0u, lane), top_s, warp, lane);
+  const uint32_t last = top_s[0][k - 1];                 // 0: fewer than k threads have a segment
+  const float least = last == 0u ? -INFINITY : value_of(last);
+  // ----------------------------------------------------- the entries that reach it
 #pragma unroll
-    for (int j = 0; j < kSeg / 32; ++j) {
-      const bool in = x[j] >= least;
-      const uint32_t mask = __ballot_sync(0xffffffffu, in);
-      if (mask == 0u) continue;
-      int at = 0;
-      if (lane == 0) at = atomicAdd(&n_cand_s, __popc(mask));
-      at = __shfl_sync(0xffffffffu, at, 0) + __popc(mask & ((1u << lane) - 1u));
-      if (in && at < kCand) cand_s[at] = key_of(x[j], entry(i, j * 32 + lane));
+  for (int i = 0; i < AHEAD; ++i)
+    if (i < mine_n && first[i] >= least) {
+      const int at = atomicAdd(&n_list_s, 1);
+      if (at < kSegList) seg_s[at] = threadIdx.x + i * kFinishThreads;
     }
-  }
+  for (int i = AHEAD; i < mine_n; ++i)
+    if (maximum(i) >= least) {
+      const int at = atomicAdd(&n_list_s, 1);
+      if (at < kSegList) seg_s[at] = threadIdx.x + i * kFinishThreads;
+    }
   __syncthreads();
-  if (warp != 0) return;
-  const int n_cand = n_cand_s;
-  list = 0;
-  if (n_cand <= kCand) {
+  const int n_list = n_list_s;
+  constexpr int V = kVec<T>;
+  if (n_list <= kSegList)
+    for (int i = warp; i < n_list; i += W)
+#pragma unroll
+      for (int q = 0; q < kSeg / (32 * V); ++q) {
+        const int e = seg_s[i] * kSeg - lead + (q * 32 + lane) * V;
+        const uint4 v = load_entries<T>(row, e, a.vocab);
+        if (Lane<T>::max_of(v) >= least) {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            const float x = Lane<T>::entry(v, j);
+            if (x >= least && e + j >= 0 && e + j < a.vocab) {
+              const int at = atomicAdd(&n_cand_s, 1);
+              if (at < kCand) cand_s[at] = key_of(x, e + j);
+            }
+          }
+        }
+      }
+  __syncthreads();
+  uint64_t list = 0;
+  if (n_list <= kSegList && n_cand_s <= kCand) {
+    if (warp != 0) return;
+    const int n_cand = n_cand_s;
     for (int j = 0; j < n_cand; j += 32) list = add32(list, j + lane < n_cand ? cand_s[j + lane] : 0ull, k, lane);
-  } else {                                               // (many equal ones: read once more, one warp in turn)
+  } else {
+    // many equal entries, or a vocabulary of few segments: each warp keeps the best
+    // of its segments in order as it reads them
+    for (int j = warp; j < n_seg; j += W) {
+      if (!(__ldcg(seg_max + j) >= least)) continue;
 #pragma unroll 1
-    for (int i = 0; i < k && list_s[0][i] != 0ull; ++i)
-#pragma unroll 1
-      for (int j = 0; j < kSeg; j += 32) {
-        const int e = entry(i, j + lane);
+      for (int q = 0; q < kSeg; q += 32) {
+        const int e = j * kSeg - lead + q + lane;
         const float x = e >= 0 && e < a.vocab ? Elem<T>::load(row + e) : __uint_as_float(0x7fc00000u);
         list = add32(list, x >= least ? key_of(x, e) : 0ull, k, lane);
       }
+    }
+    list = merge_warps<W>(list, list_s, warp, lane);
+    if (warp != 0) return;
   }
   if (lane < k) {
     a.top_ids[(int64_t)r * k + lane] = list == 0ull ? 0 : index_of(list);
     a.top_logprobs[(int64_t)r * k + lane] =
-        list == 0ull ? __uint_as_float(0x7fc00000u) : (value_of(list) - m) * a.inv_t - log_s * kLn2;
+        list == 0ull ? __uint_as_float(0x7fc00000u) : (value_of((uint32_t)(list >> 32)) - m) * a.inv_t - log_s * kLn2;
   }
 }
 
