@@ -765,9 +765,17 @@ def kv4_page_bytes(head_dim):
     return 18 * head_dim
 
 
-def _cache4(cache, dev):
-    """Whether the 4-bit cache is contiguous bytes on device dev."""
-    return cache.dtype is torch.uint8 and cache.get_device() == dev and cache.is_contiguous()
+# These calls' checks are written out in one expression each (a small call is
+# bound by the host, half of it by looking at the tensors); only where something
+# is wrong do the functions run that say what.
+_U8, _I32, _F32 = torch.uint8, torch.int32, torch.float32
+
+
+def _stream4(stream, dev, workspace):
+    """The stream to launch on; None: dev or the workspace's device is not the current one."""
+    if dev < 0 or dev != _device() or (workspace is not None and workspace.get_device() != dev):
+        return None
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream_on(stream, dev, workspace)
 
 
 def _check_cache4(cache):
@@ -789,9 +797,12 @@ def kv4_append(k, v, start, cu_n, cache, block_table, workspace, spec, take=None
     """simsd_kv4_append: k (rotated by spec) and v [total_n, Hkv, hd] quantised
     into the 4-bit cache, uint8 [num_pages, Hkv, kv4_page_bytes(hd)]."""
     dev = k.get_device()
-    s = _stream_on(stream, dev, workspace)
-    if s is None or not _arrays(dev, torch.int32, start, cu_n, block_table, take) or not _rows_on(
-            dev, k.dtype, v) or not _cache4(cache, dev):
+    s = _stream4(stream, dev, workspace)
+    if not (s is not None and start.dtype is _I32 and cu_n.dtype is _I32 and block_table.dtype is _I32 and
+            cache.dtype is _U8 and v.dtype is k.dtype and start.get_device() == dev and cu_n.get_device() == dev and
+            block_table.get_device() == dev and cache.get_device() == dev and v.get_device() == dev and
+            start.is_contiguous() and cu_n.is_contiguous() and block_table.is_contiguous() and cache.is_contiguous() and
+            (take is None or (take.dtype is _I32 and take.get_device() == dev and take.is_contiguous()))):
         _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table, take=take)
         _same_dtype(k, v=v)
         _check_cache4(cache)
@@ -820,9 +831,12 @@ def kv4_read(cache, block_table, start, cu_n, k, v, workspace, stream=None):
     if like is None:
         raise ValueError("kv4_read: neither k nor v is wanted")
     dev = cache.get_device()
-    s = _stream_on(stream, dev, workspace)
-    if s is None or not _arrays(dev, torch.int32, start, cu_n, block_table) or not _cache4(cache, dev) or not _rows_on(
-            dev, like.dtype, *(t for t in (k, v) if t is not None)):
+    s = _stream4(stream, dev, workspace)
+    if not (s is not None and start.dtype is _I32 and cu_n.dtype is _I32 and block_table.dtype is _I32 and
+            cache.dtype is _U8 and start.get_device() == dev and cu_n.get_device() == dev and
+            block_table.get_device() == dev and like.get_device() == dev and
+            start.is_contiguous() and cu_n.is_contiguous() and block_table.is_contiguous() and cache.is_contiguous() and
+            (k is None or v is None or (v.dtype is k.dtype and v.get_device() == dev))):
         _ints(torch.int32, start=start, cu_n=cu_n, block_table=block_table)
         _check_cache4(cache)
         if k is not None and v is not None:
@@ -847,10 +861,15 @@ def kv4_read(cache, block_table, start, cu_n, k, v, workspace, stream=None):
 def _kv4_verify_desc(q, cache, block_table, k_new, v_new, tau, lens, cu_B, out, workspace, total_B, B_max, spec,
                      sm_scale, order, node_size, wait_polls=0, stream=False):
     """(stream, descriptor); stream False: for the workspace's size, no device needed."""
-    dev = q.get_device()
-    s = None if stream is False else _stream_on(stream, dev, workspace)
-    if s is None or not _arrays(dev, torch.int32, block_table, tau, lens, cu_B) or not _rows_on(
-            dev, q.dtype, k_new, v_new, out) or not _cache4(cache, dev):
+    dev, dtype = q.get_device(), q.dtype
+    s = None if stream is False else _stream4(stream, dev, workspace)
+    if not (s is not None and block_table.dtype is _I32 and lens.dtype is _I32 and cu_B.dtype is _I32 and
+            cache.dtype is _U8 and k_new.dtype is dtype and v_new.dtype is dtype and out.dtype is dtype and
+            block_table.get_device() == dev and lens.get_device() == dev and cu_B.get_device() == dev and
+            cache.get_device() == dev and k_new.get_device() == dev and v_new.get_device() == dev and
+            out.get_device() == dev and block_table.is_contiguous() and lens.is_contiguous() and cu_B.is_contiguous() and
+            cache.is_contiguous() and
+            (tau is None or (tau.dtype is _I32 and tau.get_device() == dev and tau.is_contiguous()))):
         _ints(torch.int32, block_table=block_table, tau=tau, lens=lens, cu_B=cu_B)
         _same_dtype(q, k_new=k_new, v_new=v_new, out=out)
         _check_cache4(cache)
@@ -898,9 +917,8 @@ def _logprobs_desc(logits, tokens, logprob, rank, entropy, top_ids, top_logprobs
                    stream=False):
     """(stream, descriptor); stream False: for the workspace's size, no device needed."""
     dev = logits.get_device()
-    s = None if stream is False else _stream_on(stream, dev, workspace)
-    if s is None or not _arrays(dev, torch.int32, tokens, rank, top_ids) or not _arrays(
-            dev, torch.float32, logprob, entropy, top_logprobs):
+    s = None if stream is False else _stream4(stream, dev, workspace)
+    if s is None or not _arrays(dev, _I32, tokens, rank, top_ids) or not _arrays(dev, _F32, logprob, entropy, top_logprobs):
         _ints(torch.int32, tokens=tokens, rank=rank, top_ids=top_ids)
         _ints(torch.float32, logprob=logprob, entropy=entropy, top_logprobs=top_logprobs)
         if stream is not False:
@@ -911,9 +929,9 @@ def _logprobs_desc(logits, tokens, logprob, rank, entropy, top_ids, top_logprobs
     stride = logits.stride(0) if rows > 1 else 0
     if rows > 1 and stride < vocab:
         raise ValueError("logits: rows that share memory")
-    for name, t in (("tokens", tokens), ("logprob", logprob), ("rank", rank), ("entropy", entropy)):
-        if t is not None and t.numel() != rows:
-            raise ValueError("%s: one for each row of logits" % name)
+    if not ((tokens is None or tokens.numel() == rows) and (logprob is None or logprob.numel() == rows) and
+            (rank is None or rank.numel() == rows) and (entropy is None or entropy.numel() == rows)):
+        raise ValueError("tokens, logprob, rank and entropy: one for each row of logits")
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs come together")
     top = 0
