@@ -807,7 +807,8 @@ simsd_status simsd_kvq_verify(const simsd_kvq_verify_desc *d, void *stream);
  * below 6 * 2^-18 is zeros.  No other token's codes or scales change.
  * Arguments, checks and bad inputs as for simsd_kvq_append, and two sequences
  * must not write the same page in one call.
- * Limits: num_kv_heads <= 1024; batch <= 2^20; max_pages_per_seq <= 2^26.
+ * Limits: num_kv_heads <= 1024; batch <= 2^20; max_pages_per_seq <= 2^26;
+ * total_n <= 2^30.
  * Workspace: the status word (256 bytes).
  * ---------------------------------------------------------------------- */
 typedef struct {
@@ -847,8 +848,8 @@ simsd_status simsd_kv4_append(const simsd_kv4_append_desc *d, void *stream);
  *            too (scales below 2^-14 included); SIMSD_E4M3 rounds to nearest
  *            even, saturating at 448, NaN for what is not finite
  *   total_n  host: rows of k and v; 0: nothing is written
- * Bad inputs as for simsd_kv4_append: that sequence's rows, or those of that
- * page, are left as they were.
+ * Limits and bad inputs as for simsd_kv4_append: that sequence's rows, or
+ * those of that page, are left as they were.
  * ---------------------------------------------------------------------- */
 typedef struct {
   int32_t batch;
@@ -941,7 +942,7 @@ simsd_status simsd_kv4_verify(const simsd_kv4_verify_desc *d, void *stream);
  * throughout or holds a NaN or +inf has NaN for logprob, entropy and
  * top_logprobs; its rank and ids are of no use (ids lie in 0..vocab-1).
  * Limits: 1 <= vocab <= 2^21; 0 <= rows <= 2^20; 0 <= top_k <= min(32, vocab);
- * T as in simsd_accept_desc, at most 1e30.  rows = 0 returns SIMSD_OK.
+ * T as in simsd_accept_desc, within 1e-30..1e30.  rows = 0 returns SIMSD_OK.
  * Workspace: simsd_token_logprobs_workspace_size, 256 + rows * C * 48 bytes
  * rounded up to a multiple of 256, with C = ceil(vocab / 2048) + 1.
  * ---------------------------------------------------------------------- */

@@ -207,7 +207,7 @@ extern "C" simsd_status simsd_kv4_append(const simsd_kv4_append_desc *d, void *s
   if (d->dtype != SIMSD_F32 && d->dtype != SIMSD_BF16) return SIMSD_ERR_DTYPE;
   if (d->batch < 1 || d->batch > (1 << 20) || d->num_kv_heads < 1 || d->num_kv_heads > 1024 ||
       (d->head_dim != 64 && d->head_dim != 128) || d->page_size != kPageTokens || d->num_pages < 1 ||
-      d->max_pages_per_seq < 1 || d->max_pages_per_seq > (1 << 26) || d->total_n < 0 || d->k_row < 0 || d->v_row < 0)
+      d->max_pages_per_seq < 1 || d->max_pages_per_seq > (1 << 26) || d->total_n < 0 || d->total_n > (1 << 30) || d->k_row < 0 || d->v_row < 0)
     return SIMSD_ERR_SHAPE;
   Append4Args a;
   const simsd_status st = make_rope_plan(d->rope, d->head_dim, &a.plan);

@@ -186,7 +186,7 @@ extern "C" simsd_status simsd_kv4_read(const simsd_kv4_read_desc *d, void *strea
   if (d->dtype != SIMSD_F32 && d->dtype != SIMSD_BF16 && d->dtype != SIMSD_E4M3) return SIMSD_ERR_DTYPE;
   if (d->batch < 1 || d->batch > (1 << 20) || d->num_kv_heads < 1 || d->num_kv_heads > 1024 ||
       (d->head_dim != 64 && d->head_dim != 128) || d->page_size != kPageTokens || d->num_pages < 1 ||
-      d->max_pages_per_seq < 1 || d->max_pages_per_seq > (1 << 26) || d->total_n < 0 || d->k_row < 0 || d->v_row < 0)
+      d->max_pages_per_seq < 1 || d->max_pages_per_seq > (1 << 26) || d->total_n < 0 || d->total_n > (1 << 30) || d->k_row < 0 || d->v_row < 0)
     return SIMSD_ERR_SHAPE;
   if ((d->total_n > 0 && !d->k && !d->v) || !d->start || !d->cu_n || !d->cache || !d->block_table)
     return SIMSD_ERR_NULL;

@@ -27,7 +27,7 @@ constexpr int kPart = 2048, kSeg = 256, kSegs = kPart / kSeg;
 constexpr int kLane = kPart / 32;          // entries of a lane
 constexpr int kPassThreads = 128;
 constexpr int kMaxTop = 32;
-constexpr float kMaxTemperature = 1e30f;
+constexpr float kMinTemperature = 1e-30f, kMaxTemperature = 1e30f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kSegList = 64, kCand = 1024;  // segments and entries that reach the bound, kept aside
 
@@ -507,7 +507,7 @@ simsd_status check(const simsd_token_logprobs_desc *d) {
   if (d == nullptr) return SIMSD_ERR_NULL;
   if (d->dtype != SIMSD_F32 && d->dtype != SIMSD_BF16) return SIMSD_ERR_DTYPE;
   if (d->rows < 0 || d->rows > (1 << 20) || d->vocab < 1 || d->vocab > (1 << 21) || d->top_k < 0 ||
-      d->top_k > kMaxTop || d->top_k > d->vocab || !(d->temperature >= 0.0f) || !(d->temperature <= kMaxTemperature) ||
+      d->top_k > kMaxTop || d->top_k > d->vocab || !(d->temperature == 0.0f || (d->temperature >= kMinTemperature && d->temperature <= kMaxTemperature)) ||
       d->row_stride < 0 || (d->row_stride != 0 && d->row_stride < d->vocab && d->rows > 1))
     return SIMSD_ERR_SHAPE;
   return SIMSD_OK;

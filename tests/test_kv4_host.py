@@ -94,7 +94,7 @@ def logprobs_desc(**kw):
 COMMON = [(dict(batch=0), 2), (dict(num_kv_heads=0), 2), (dict(head_dim=96), 2), (dict(page_size=32), 2),
           (dict(num_pages=0), 2), (dict(max_pages_per_seq=0), 2), (dict(block_table=None), 1), (dict(cache=None), 1),
           (dict(cache=FAKE + 8), 8), (dict(workspace=None), 5), (dict(workspace=FAKE + 16), 5), (dict(workspace_bytes=255), 5)]
-ROWS = [(dict(total_n=-1), 2), (dict(k_row=-1), 2), (dict(num_kv_heads=1025), 2), (dict(batch=(1 << 20) + 1), 2),
+ROWS = [(dict(total_n=-1), 2), (dict(total_n=(1 << 30) + 1), 2), (dict(k_row=-1), 2), (dict(num_kv_heads=1025), 2), (dict(batch=(1 << 20) + 1), 2),
         (dict(max_pages_per_seq=(1 << 26) + 1), 2), (dict(k=FAKE + 2), 8), (dict(v_row=130), 8), (dict(start=None), 1),
         (dict(cu_n=None), 1)]
 
@@ -123,7 +123,7 @@ def test_verify_refusals(lib, bad, code):
 @pytest.mark.parametrize("bad,code", [
     (dict(rows=-1), 2), (dict(rows=(1 << 20) + 1), 2), (dict(vocab=0), 2), (dict(vocab=(1 << 21) + 1), 2), (dict(top_k=-1), 2),
     (dict(top_k=33), 2), (dict(vocab=3), 2), (dict(dtype=2), 4), (dict(temperature=-1.0), 2),
-    (dict(temperature=float("inf")), 2), (dict(temperature=2e30), 2), (dict(temperature=float("nan")), 2), (dict(row_stride=99), 2), (dict(logits=None), 1),
+    (dict(temperature=float("inf")), 2), (dict(temperature=2e30), 2), (dict(temperature=1e-31), 2), (dict(temperature=float("nan")), 2), (dict(row_stride=99), 2), (dict(logits=None), 1),
     (dict(tokens=None), 1), (dict(top_ids=None), 1), (dict(top_logprobs=None), 1), (dict(top_k=0), 1),
     (dict(logits=FAKE + 1), 8), (dict(dtype=0, logits=FAKE + 2), 8), (dict(workspace=None), 5),
     (dict(workspace_bytes=256 + 3 * 2 * 48 - 1), 5)])
