@@ -39,25 +39,32 @@ constexpr int kKeys = 128;           // keys per block
 static_assert(kKeys == kBlockKeys, "split chunks are whole blocks");
 constexpr int kStages = 4;
 constexpr int kPagesPerBlock = kKeys / kPage;
-constexpr int kPvWarp = 2, kSoftmaxWarp = 4, kDecodeWarp = 12, kValueWarp = 16, kWarps = 20;
+constexpr int kPvWarp = 2, kSecondProducer = 3, kSoftmaxWarp = 4, kDecodeWarp = 12, kValueWarp = 16, kWarps = 20;
 constexpr int kDecoders = 4;          // warps for a tile
 constexpr int kPagesPerWarp = kPagesPerBlock / kDecoders;
 constexpr int kThreads = kWarps * 32;
 constexpr int kPrep = 16 * 32;         // threads of the softmax and decoding warps
 constexpr int kHalves = 2;            // softmax warps sharing 32 rows
 constexpr int kGone = 16;             // blocks whose missing pages are kept (a producer is at most 7 ahead of a softmax)
-constexpr float kHeadroom = 8.f;     // log2 units a row max may grow before O is rescaled
-constexpr float kLift = 7.f;         // log2 of the largest weight right after that
-constexpr uint32_t kColS = 0;        // two score tiles: columns 0 and kKeys
-// The weights, f16, two keys a column, go over the scores they come from: those
-// of keys 0..63 from the tile's first column on, those of 64..127 from its 65th,
-// so that neither of a row's two warps writes where the other still reads.
-__host__ __device__ constexpr uint32_t weight_col(int key) { return (uint32_t)((key & 64) + (key & 63) / 2); }
-constexpr uint32_t kColO = 2 * kKeys;
+constexpr float kLift = 7.f;         // log2 of a row's largest weight right after its reference moved
+constexpr float kMostSum = 32768.f;  // sum of a thread's weights in a block that moves it
+// TMEM: five units of 64 columns, then the output, then the query.  Block j's
+// scores are in units j and j + 2 (mod 5; 64 keys each); its weights, f16, two
+// keys a column, go over the first of them, so that the scores of block j + 2
+// need wait only for block j's weights and for the P V of block j - 3: a cycle
+// of score, softmax, P V and score again would be longer than the softmax.  A
+// row's warp h has keys 32 h .. 32 h + 31 of both units and puts their weights
+// into columns 32 h .. 32 h + 31, where nobody else reads.
+constexpr int kUnits = 5;
+constexpr uint32_t kUnitCols = 64;
+constexpr uint32_t kColO = kUnits * kUnitCols;
+__device__ __forceinline__ uint32_t unit_col(int j, int which) { return (uint32_t)((j + 2 * which) % kUnits) * kUnitCols; }
+__host__ __device__ constexpr uint32_t weight_col(int key) { return (uint32_t)((key & 32) + (key >> 6) * 16 + (key & 31) / 2); }
+constexpr int kPvBars = 4;           // (the scores' warp looks three blocks back)
 
 enum { kBarFull = 0, kBarEmpty = kBarFull + kStages, kBarKbFull = kBarEmpty + kStages, kBarVbFull = kBarKbFull + 2,
        kBarSFull = kBarVbFull + 2, kBarPFull = kBarSFull + 2, kBarPvDone = kBarPFull + 2,
-       kBarQReady = kBarPvDone + 2, kBarNewRead = kBarQReady + 1, kNumBars = kBarNewRead + 1 };
+       kBarQReady = kBarPvDone + kPvBars, kBarNewRead = kBarQReady + 1, kBarRaw = kBarNewRead + 1, kNumBars = kBarRaw + 1 };
 
 template <int HD>
 struct Smem {
@@ -123,72 +130,95 @@ __device__ __forceinline__ void named_sync(int id, int n) {
 
 __device__ __forceinline__ uint64_t shift_right(uint64_t x, int s) { return s >= 64 ? 0ull : x >> s; }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 __device__ __forceinline__ uint4 mul4(uint4 h, uint32_t s) {
   return make_uint4(mul_f16x2(h.x, s), mul_f16x2(h.y, s), mul_f16x2(h.z, s), mul_f16x2(h.w, s));
 }
 
-// One page's keys to a tile: lane (row r and r + 8, 32 elements).  Lanes of the
-// upper half of the head take their runs of 8 in another order, so that eight
-// lanes write to eight different 16-byte columns.
+// One page's keys to a tile (rows of 64 elements of a key): a lane takes 32
+// elements of a row.  Which 32 depends on the row, so that eight lanes' reads lie
+// in all banks, and so do their writes (64 elements a head: only the writes).
 template <int HD>
 __device__ __forceinline__ void decode_keys(const uint8_t *rec, uint8_t *tile, int page, int lane) {
   constexpr int C = HD / 32;                         // lanes of a row
   constexpr int RPI = 32 / C;                        // rows in a step
-  const int c = lane % C, r0 = lane / C;
-  const bool swap = (c & 2) != 0;
 #pragma unroll
   for (int i = 0; i < kPage / RPI; ++i) {
-    const int r = r0 + i * RPI, row = page * kPage + r;
+    const int r = i * RPI + lane % RPI, row = page * kPage + r;
+    const int c = HD == 128 ? (lane / RPI) ^ ((r >> 1) & 3) : lane / RPI;
     const uint4 w = *reinterpret_cast<const uint4 *>(rec + r * (HD / 2) + c * 16);
     const uint32_t two = *reinterpret_cast<const uint16_t *>(rec + Record<HD>::kKs + r * (HD / 16) + 2 * c);
     const uint32_t s0 = scale4_twice(two, 0), s1 = scale4_twice(two, 1);
-    const uint32_t sa = swap ? s1 : s0, sb = swap ? s0 : s1;
-    const uint32_t k[4] = {swap ? w.z : w.x, swap ? w.w : w.y, swap ? w.x : w.z, swap ? w.y : w.w};
     uint8_t *dst = tile + (c >> 1) * Smem<HD>::kHalf;
-    const int c0 = (c & 1) * 4 + (swap ? 2 : 0);
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      *reinterpret_cast<uint4 *>(dst + swz(row, c0 ^ q)) = mul4(unpack_e2m1x8(k[q]), q < 2 ? sa : sb);
+    const int c0 = (c & 1) * 4;
+    *reinterpret_cast<uint4 *>(dst + swz(row, c0)) = mul4(unpack_e2m1x8(w.x), s0);
+    *reinterpret_cast<uint4 *>(dst + swz(row, c0 + 1)) = mul4(unpack_e2m1x8(w.y), s0);
+    *reinterpret_cast<uint4 *>(dst + swz(row, c0 + 2)) = mul4(unpack_e2m1x8(w.z), s1);
+    *reinterpret_cast<uint4 *>(dst + swz(row, c0 + 3)) = mul4(unpack_e2m1x8(w.w), s1);
   }
 }
 
-// One page's values to a tile: lane (pair of tokens, 16 elements of it), the
-// upper half of 32 elements writing its odd token first.  mask0, mask1: tokens
-// of the pair that count (f16 bits of the scales).
+// A quarter of a block's values to a tile (rows of 64 keys of an element of the
+// head, since a byte holds two keys of an element): warp `part` takes four pages
+// and half of the elements, a lane eight keys of 16 elements (of 8 with 64 elements
+// a head).  The four pairs of keys that make 16 bytes of a row stand there in
+// the order 0..3 xor (chunk mod 4), which lets eight lanes read from all banks; the
+// weights stand in that order too.  valid, gone: keys and pages that count.
+__host__ __device__ constexpr int pair_slot(int chunk, int pair) { return pair ^ (chunk & 3); }
 template <int HD>
-__device__ __forceinline__ void decode_values(const uint8_t *rec, uint8_t *tile, int page, int valid, int lane) {
+__device__ __forceinline__ void decode_values(const uint8_t *stage, uint8_t *tile, int part, int valid, uint32_t gone, int lane) {
   using R = Record<HD>;
-  const int half = lane & 1, pair = (lane >> 1) & 7, row = page * kPage + 2 * pair;
-  const uint32_t sel_a = half ? 0x7632u : 0x5410u, sel_b = half ? 0x5410u : 0x7632u;
-  const uint32_t keep = (row < valid ? 0xffffu : 0u) | (row + 1 < valid ? 0xffff0000u : 0u);
+  constexpr int W = HD / 32;                         // words of a pair
+  const int cc = lane & 7, chunk = 8 * (part >> 1) + cc, page = chunk >> 1;
+  const int step = HD == 128 ? part & 1 : lane >> 4;
+  const int g = 2 * (HD == 128 ? lane >> 3 : (lane >> 3) & 1) + (step ^ (cc >> 2));      // group of 16 elements
+  const int w0 = HD == 128 ? 0 : 2 * (part & 1);     // first word of the group
+  const uint8_t *rec = stage + page * R::kBytes;
+  const bool whole = valid >= kKeys && gone == 0u;
+  uint32_t k[4][W], s[4];
 #pragma unroll
-  for (int i = 0; i < HD / 64; ++i) {
-    const int g = 2 * (2 * i + (lane >> 4)) + half;  // group of 16 elements
-    const uint4 w = *reinterpret_cast<const uint4 *>(rec + R::kV + i * 512 + lane * 16);
-    const uint32_t s = scale4_pair(*reinterpret_cast<const uint16_t *>(rec + R::vs_at(pair, g))) & keep;
-    const uint32_t k[4] = {w.x, w.y, w.z, w.w};
-    uint32_t a[8], b[8];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 h = mul4(unpack_e2m1x8(k[q]), s);  // an element a pair: (even, odd) token
-      a[2 * q] = __byte_perm(h.x, h.y, sel_a);
-      a[2 * q + 1] = __byte_perm(h.z, h.w, sel_a);
-      b[2 * q] = __byte_perm(h.x, h.y, sel_b);
-      b[2 * q + 1] = __byte_perm(h.z, h.w, sel_b);
+  for (int i = 0; i < 4; ++i) {
+    const int pr = 4 * (cc & 1) + pair_slot(cc, i);
+    const uint8_t *src = rec + R::v_at(pr, g) + 4 * w0;
+    if constexpr (W == 4) {
+      const uint4 v = *reinterpret_cast<const uint4 *>(src);
+      k[i][0] = v.x; k[i][1] = v.y; k[i][2] = v.z; k[i][3] = v.w;
+    } else {
+      const uint2 v = *reinterpret_cast<const uint2 *>(src);
+      k[i][0] = v.x; k[i][1] = v.y;
     }
-    uint8_t *dst = tile + (g >> 2) * Smem<HD>::kHalf;
-    const int ch = (g & 3) * 2, ra = row + half, rb = row + 1 - half;
-    *reinterpret_cast<uint4 *>(dst + swz(ra, ch)) = make_uint4(a[0], a[1], a[2], a[3]);
-    *reinterpret_cast<uint4 *>(dst + swz(rb, ch)) = make_uint4(b[0], b[1], b[2], b[3]);
-    *reinterpret_cast<uint4 *>(dst + swz(ra, ch + 1)) = make_uint4(a[4], a[5], a[6], a[7]);
-    *reinterpret_cast<uint4 *>(dst + swz(rb, ch + 1)) = make_uint4(b[4], b[5], b[6], b[7]);
+    s[i] = scale4_pair(*reinterpret_cast<const uint16_t *>(rec + R::vs_at(pr, g)));
+    if (!whole) {                                    // no key, no value: not even a NaN
+      const int key = page * kPage + 2 * pr, n = (gone >> page) & 1u ? 0 : valid;
+      s[i] &= (key < n ? 0xffffu : 0u) | (key + 1 < n ? 0xffff0000u : 0u);
+    }
   }
+  uint8_t *dst = tile + (part >> 1) * (HD * 128);
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    uint4 h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = mul4(unpack_e2m1x8(k[i][w]), s[i]);
+    const int row = 16 * g + 4 * (w0 + w);
+    *reinterpret_cast<uint4 *>(dst + swz(row, cc)) = make_uint4(h[0].x, h[1].x, h[2].x, h[3].x);
+    *reinterpret_cast<uint4 *>(dst + swz(row + 1, cc)) = make_uint4(h[0].y, h[1].y, h[2].y, h[3].y);
+    *reinterpret_cast<uint4 *>(dst + swz(row + 2, cc)) = make_uint4(h[0].z, h[1].z, h[2].z, h[3].z);
+    *reinterpret_cast<uint4 *>(dst + swz(row + 3, cc)) = make_uint4(h[0].w, h[1].w, h[2].w, h[3].w);
+  }
+}
+
+// Whole warp: phases of two or three barriers.  All are tested before one is waited
+// for: a wait takes some 200 cycles even when its phase is complete, as it mostly is.
+struct Phase {
+  uint32_t bar, parity;
+};
+__device__ __forceinline__ bool wait_all(uint32_t polls, Phase a, Phase b, Phase c) {
+  const bool x = mbar_test(a.bar, a.parity), y = mbar_test(b.bar, b.parity), z = mbar_test(c.bar, c.parity);
+  return __all_sync(0xffffffffu, x && y && z) ||
+         (mbar_wait_warp(a.bar, a.parity, polls) && mbar_wait_warp(b.bar, b.parity, polls) && mbar_wait_warp(c.bar, c.parity, polls));
+}
+__device__ __forceinline__ bool wait_all(uint32_t polls, Phase a, Phase b) {
+  const bool x = mbar_test(a.bar, a.parity), y = mbar_test(b.bar, b.parity);
+  return __all_sync(0xffffffffu, x && y) || (mbar_wait_warp(a.bar, a.parity, polls) && mbar_wait_warp(b.bar, b.parity, polls));
 }
 
 template <int HD>
@@ -248,31 +278,56 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     const int key = w.k_begin + j * kKeys + (lane & 7) * kPage;
     return j < n_past && key < w.k_end ? __ldg(bt + key / kPage) : -1;
   };
-  int pages[kStages];
+  const bool producer = warp == 0 || warp == kSecondProducer;
+  const int odd_blocks = warp == 0 ? 0 : 1;  // a producer's blocks: every other one
+  int pages[kStages / 2];
   constexpr int CH = HD / 8;                 // 16-byte chunks of a bf16 row
-  if (warp == 0) {
+  if (producer) {
 #pragma unroll
-    for (int d = 0; d < kStages; ++d) pages[d] = block_page(d);
+    for (int d = 0; d < kStages / 2; ++d) pages[d] = block_page(2 * d + odd_blocks);
   } else if (prep_warp) {
-    // the query rows and the new tokens' keys and values come first of all,
-    // ahead of the stream of codes
-    const __nv_bfloat16 *qs = (const __nv_bfloat16 *)a.q + t0 * a.q_row + w.kvh * a.G * HD;
-    for (int e = pt; e < n_groups * 32 * CH; e += kPrep) {
-      const int r = e / CH, c = e % CH, row = w.row0 + r, tok = div_by(row, a.by_G);
-      const bool take = row < w.M;
-      copy16_async(base + L::kOffRaw + r * HD * 2 + c * 16,
-                   take ? qs + tok * a.q_row + (row - tok * a.G) * HD + c * 8 : (const void *)a.q, take);
+    // the query rows (a token's heads lie together) and the new tokens' keys and
+    // values come first of all, ahead of the stream of codes: one bulk copy each,
+    // a few of them a warp (a warp issues its lanes' one after another)
+    const int rows = min(kRows, w.M - w.row0), news = fresh ? w.n : 0;
+    if (pt == 0) {
+      mbar_init(bar(kBarRaw), 1);
+      fence_barrier_init();
+      mbar_arrive_expect_tx(bar(kBarRaw), (uint32_t)(rows + 2 * news) * HD * 2);
     }
-    if (fresh)
-      for (int e = pt; e < w.n * CH; e += kPrep) {
-        const int j = e / CH, c = e % CH;
-        const uint32_t dst = base + L::kOffNew + j * HD * 2 + c * 16;
-        copy16_async(dst, (const __nv_bfloat16 *)a.k_new + (t0 + j) * a.k_row + w.kvh * HD + c * 8, true);
-        copy16_async(dst + kMaxNew * HD * 2, (const __nv_bfloat16 *)a.v_new + (t0 + j) * a.v_row + w.kvh * HD + c * 8, true);
+    named_sync(1, kPrep);
+    const int tok0 = div_by(w.row0, a.by_G), n_tok = div_by(w.row0 + rows - 1, a.by_G) - tok0 + 1;
+    for (int e = (warp - kSoftmaxWarp) + 16 * lane; e < n_tok + 2 * news; e += 16 * 32) {
+      const __nv_bfloat16 *src;
+      uint32_t dst, bytes = HD * 2;
+      if (e < n_tok) {
+        const int t = tok0 + e, lo = max(w.row0, t * a.G), hi = min(w.row0 + rows, (t + 1) * a.G);
+        src = (const __nv_bfloat16 *)a.q + (t0 + t) * a.q_row + w.kvh * a.G * HD + (lo - t * a.G) * HD;
+        dst = L::kOffRaw + (lo - w.row0) * HD * 2;
+        bytes *= hi - lo;
+      } else {
+        const int i = e - n_tok, j = i < news ? i : i - news;
+        src = (i < news ? (const __nv_bfloat16 *)a.k_new + (t0 + j) * a.k_row : (const __nv_bfloat16 *)a.v_new + (t0 + j) * a.v_row) + w.kvh * HD;
+        dst = L::kOffNew + (i < news ? j : kMaxNew + j) * HD * 2;
       }
+      bulk_load(base + dst, src, bytes, bar(kBarRaw));
+    }
+    // angles of the new tokens' positions (identity past the rotated part)
+    float2 *cs_s = reinterpret_cast<float2 *>(sb + L::kOffCs);            // [kMaxNew][HD / 2]
+    const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
+#pragma unroll 1
+    for (int e = pt; e < npos * (HD / 2); e += kPrep) {
+      float2 cs = make_float2(1.f, 0.f);
+      if (pair < a.plan.half) {
+        cs = rope_angle(plan_by_lane(a.plan), turn_hi, turn_lo, pair, w.P + e / (HD / 2));
+        cs = make_float2(cs.x * a.plan.mul, cs.y * a.plan.mul);
+      }
+      cs_s[e - pair + angle_at(pair)] = cs;
+    }
+    if (a.order == SIMSD_ORDER_PAIRED && pt < w.B) tau_s[pt] = __ldg(a.tau + w.c0 + pt);
   }
   if (warp == kPvWarp) {
-    for (int i = lane; i < kNumBars; i += 32) {
+    for (int i = lane; i < kBarRaw; i += 32) {      // (that one is made)
       const bool rows = i >= kBarPFull && i < kBarPFull + 2;
       const bool tiles = i >= kBarKbFull && i < kBarVbFull + 2;
       mbar_init(bar(i), rows ? n_valid : tiles ? kDecoders : i >= kBarEmpty && i < kBarEmpty + kStages ? 2 * kDecoders
@@ -293,28 +348,17 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   int issued = 0;                            // producers: blocks whose loads were started
-  float2 *cs_s = reinterpret_cast<float2 *>(sb + L::kOffCs);            // [kMaxNew][HD / 2]
+  const float2 *cs_s = reinterpret_cast<const float2 *>(sb + L::kOffCs);
+  auto pv_done = [&](int j) { return Phase{bar(kBarPvDone + (j & (kPvBars - 1))), (uint32_t)(j / kPvBars) & 1u}; };
+  auto two = [&](int first, int j) { return Phase{bar(first + (j & 1)), (uint32_t)(j >> 1) & 1u}; };   // of a pair of barriers
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
   // These warps together rotate the query rows and, in the CTA that owns the new
   // tokens, their keys, to f16 relative to a power of two of each row's; rolled
   // loops, since each CTA runs them once.
   auto prepare = [&]() {
-    // angles of the new tokens' positions (identity past the rotated part)
-    const int npos = a.order == SIMSD_ORDER_PAIRED ? w.B : a.order == SIMSD_ORDER_NODES ? a.node_size : w.n;
-#pragma unroll 1
-    for (int e = pt; e < npos * (HD / 2); e += kPrep) {
-      float2 cs = make_float2(1.f, 0.f);
-      if (pair < a.plan.half) {
-        cs = rope_angle(plan_by_lane(a.plan), turn_hi, turn_lo, pair, w.P + e / (HD / 2));
-        cs = make_float2(cs.x * a.plan.mul, cs.y * a.plan.mul);
-      }
-      cs_s[e - pair + angle_at(pair)] = cs;
-    }
-    if (a.order == SIMSD_ORDER_PAIRED && pt < w.B) tau_s[pt] = __ldg(a.tau + w.c0 + pt);
-    copy_async_wait_all();
+    if (!mbar_wait_warp(bar(kBarRaw), 0, a.polls) && lane == 0) give_up();
     const __nv_bfloat16 *ks = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew), *vs = ks + kMaxNew * HD;
-    if (fresh) {                             // each token's ve: its largest finite value (CH lanes hold its row, each
-                                             // the chunk that it copied itself)
+    if (fresh) {                             // each token's ve: its largest finite value (CH lanes hold its row)
 #pragma unroll 1
       for (int e = pt; e - lane < w.n * CH; e += kPrep) {
         float va = 0.f;
@@ -365,7 +409,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
       int c0, c1;
       float x[16], amax = 0.f, nan = 0.f;
       rotate16(a.plan, cs_s + kvq_offset(a, w.B, tok) * (HD / 2), query ? qs + r * HD : ks + tok * HD, c, c0, c1, x);
-      if (!query && r >= w.n) {
+      if (query ? row >= w.M : r >= w.n) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) x[i] = 0.f;
       }
@@ -397,20 +441,20 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     named_sync(1, kPrep);
   };
 
-  if (warp == 0) {
-    // ---------------------------------------------------------- producer
+  if (producer) {
+    // --------------------------------------------------------- producers
     bool ok = true;
-    for (int j0 = 0; ok && j0 < n_past; j0 += kStages) {
+    for (int j0 = odd_blocks; ok && j0 < n_past; j0 += kStages) {
 #pragma unroll
-      for (int s = 0; s < kStages; ++s) {    // s: stage of block j
-        const int j = j0 + s;
+      for (int d = 0; d < kStages / 2; ++d) {
+        const int j = j0 + 2 * d, s = 2 * d + odd_blocks;                  // s: stage of block j
         if (j >= n_past) break;
-        const int page = pages[s];
+        const int page = pages[d];
         const bool there = lane < kPagesPerBlock && in_cache(page);
         const uint32_t have = __ballot_sync(0xffffffffu, there);
         // (the last two stages hold the new tokens until they are converted)
         if ((j >= kStages && !mbar_wait_warp(bar(kBarEmpty + s), ((j / kStages) - 1) & 1, a.polls)) ||
-            (j == kStages - 2 && fresh && !mbar_wait_warp(bar(kBarNewRead), 0, a.polls))) {
+            (j >= kStages - 2 && j < kStages && fresh && !mbar_wait_warp(bar(kBarNewRead), 0, a.polls))) {
           if (lane == 0) give_up();
           ok = false;
           break;
@@ -426,30 +470,32 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         else if (lane < kPagesPerBlock && w.k_begin + j * kKeys + lane * kPage < w.k_end)
           raise_status(a.status, kStatusBadInput);
         issued = j + 1;
-        pages[s] = block_page(j + kStages);
+        pages[d] = block_page(j + kStages);
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- scores
     // The whole warp keeps the loop (uniform addresses), one lane issues.
-    constexpr uint32_t idS = tc::idesc_f16(kRows, kKeys, 0), idSn = tc::idesc_f16(kRows, kMaxNew, 0);
+    static_assert(kMaxNew <= (int)kUnitCols, "the new tokens are one unit");
+    constexpr uint32_t idS = tc::idesc_f16(kRows, kUnitCols, 0);
     const uint64_t dK0 = tc::smem_desc_sw128(base + L::kOffKb, 16, 1024);
-    auto score = [&](uint32_t tS, int tb, uint32_t idesc) {
+    auto score = [&](uint32_t tS, int at) {       // 64 keys, from byte `at` of the tiles on
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
         tc::mma_bf16_ts(tS, tmem + L::kColQ + kk * 8,
-                        dK0 + ((uint32_t)(tb * L::kTile + (kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4), idesc, kk > 0);
+                        dK0 + ((uint32_t)(at + (kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4), idS, kk > 0);
     };
     bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
     for (int j = 0; ok && j < n_blocks; ++j) {
       const int tb = j & 1;
-      ok = mbar_wait_warp(bar(kBarKbFull + tb), (j >> 1) & 1, a.polls) &&
-           (j < 2 || mbar_wait_warp(bar(kBarPvDone + tb), ((j >> 1) - 1) & 1, a.polls));
+      const Phase keys = two(kBarKbFull, j), weights = two(kBarPFull, j - 2);
+      ok = j < 3 ? mbar_wait_warp(keys.bar, keys.parity, a.polls) && (j < 2 || mbar_wait_warp(weights.bar, weights.parity, a.polls))
+                 : wait_all(a.polls, pv_done(j - 3), keys, weights);
       if (!ok) break;
       tc::fence_after_sync();
       if (tc::elect_one()) {
-        if (j < fresh) score(tmem + kColS + tb * kKeys, tb, idSn);
-        else score(tmem + kColS + tb * kKeys, tb, idS);
+        score(tmem + unit_col(j, 0), tb * L::kTile);
+        if (j >= fresh) score(tmem + unit_col(j, 1), tb * L::kTile + 64 * 128);
         tc::commit(bar(kBarSFull + tb));
       }
       __syncwarp();
@@ -457,27 +503,28 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     if (!ok && lane == 0) give_up();
   } else if (warp == kPvWarp) {
     // ---------------------------------------------------------------- P V
-    constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 1);
-    const uint64_t dV0 = tc::smem_desc_sw128(base + L::kOffVb, L::kHalf, 1024);
+    constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 0);
+    auto value_at = [](int kk) { return (uint32_t)((kk >> 2) * (HD * 128) + (kk & 3) * 32) >> 4; };
+    const uint64_t dV0 = tc::smem_desc_sw128(base + L::kOffVb, 16, 1024);
     bool ok = true;
     for (int j = 0; j < n_blocks; ++j) {
       const int tb = j & 1, jp = j - fresh;
-      ok = mbar_wait_warp(bar(kBarVbFull + tb), (j >> 1) & 1, a.polls) && mbar_wait_warp(bar(kBarPFull + tb), (j >> 1) & 1, a.polls);
+      ok = wait_all(a.polls, two(kBarVbFull, j), two(kBarPFull, j));
       if (!ok) break;
       tc::fence_after_sync();
       const int depth = jp < 0 ? n_pad : min(kKeys, (w.k_end - w.k_begin - jp * kKeys + 15) & ~15);
       const uint64_t dV = dV0 + ((uint32_t)(tb * L::kTile) >> 4);
-      const uint32_t tP = tmem + kColS + tb * kKeys;
+      const uint32_t tP = tmem + unit_col(j, 0);
       if (tc::elect_one()) {
         if (depth == kKeys) {
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_bf16_ts(tmem + kColO, tP + weight_col(16 * kk), dV + kk * 128, idO, j > 0 || kk > 0);
+            tc::mma_bf16_ts(tmem + kColO, tP + weight_col(16 * kk), dV + value_at(kk), idO, j > 0 || kk > 0);
         } else {
           for (int kk = 0; kk < depth / 16; ++kk)
-            tc::mma_bf16_ts(tmem + kColO, tP + weight_col(16 * kk), dV + kk * 128, idO, j > 0 || kk > 0);
+            tc::mma_bf16_ts(tmem + kColO, tP + weight_col(16 * kk), dV + value_at(kk), idO, j > 0 || kk > 0);
         }
-        tc::commit(bar(kBarPvDone + tb));
+        tc::commit(bar(kBarPvDone + (j & (kPvBars - 1))));
       }
       __syncwarp();
     }
@@ -485,7 +532,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   } else if (warp >= kDecodeWarp) {
     // ------------------------------------------------------------- decode
     const bool values = warp >= kValueWarp;
-    const int pg0 = (warp - (values ? kValueWarp : kDecodeWarp)) * kPagesPerWarp;   // this warp's pages of every block
+    const int part = warp - (values ? kValueWarp : kDecodeWarp);            // this warp's quarter of every block
     prepare();
     // (the tiles hold the angles and rows until the query is in TMEM)
     bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
@@ -493,16 +540,21 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     if (ok && fresh && values) {             // the new values, as f16, are the first value tile
       const __nv_bfloat16 *vs = reinterpret_cast<const __nv_bfloat16 *>(sb + L::kOffNew) + kMaxNew * HD;
 #pragma unroll 1
-      for (int e = threadIdx.x - 32 * kValueWarp; e < n_pad * CH; e += 32 * kDecoders) {
-        const int j = e / CH, c = e % CH;
-        const float vdown = new_inv_s[j];
-        float v[8];
-        load_vec<__nv_bfloat16, 8>(vs + e * 8, v);
+      for (int e = threadIdx.x - 32 * kValueWarp; e < n_pad / 2 * CH; e += 32 * kDecoders) {
+        const int c = e / (n_pad / 2), j = 2 * (e - c * (n_pad / 2));       // a pair of tokens
+        float v[2][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)          // (an odd one times a weight of 0 would reach every row)
-          v[i] = j < w.n && fabsf(v[i]) < INFINITY ? v[i] * vdown : 0.f;
-        *reinterpret_cast<uint4 *>(sb + L::kOffVb + (c >> 3) * L::kHalf + swz(j, c & 7)) =
-            make_uint4(pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]), pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7]));
+        for (int t = 0; t < 2; ++t) {
+          const float vdown = new_inv_s[j + t];
+          load_vec<__nv_bfloat16, 8>(vs + (j + t) * HD + c * 8, v[t]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)        // (an odd one times a weight of 0 would reach every row)
+            v[t][i] = j + t < w.n && fabsf(v[t][i]) < INFINITY ? v[t][i] * vdown : 0.f;
+        }
+        uint8_t *dst = sb + L::kOffVb + 4 * pair_slot(j >> 3, (j >> 1) & 3);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint32_t *>(dst + swz(8 * c + i, j >> 3)) = pack_f16x2(v[0][i], v[1][i]);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -512,22 +564,20 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
       }
     }
     // a tile is free when the product that read it is done: scores for keys, P V for values
-    const int free_bar = values ? kBarPvDone : kBarSFull, full_bar = values ? kBarVbFull : kBarKbFull;
+    const int full_bar = values ? kBarVbFull : kBarKbFull;
     for (int jp = 0; ok && jp < n_past; ++jp) {
       const int j = jp + fresh, tb = j & 1, s = jp & (kStages - 1);
-      if (!mbar_wait_warp(bar(kBarFull + s), (jp / kStages) & 1, a.polls) ||
-          (j >= 2 && !mbar_wait_warp(bar(free_bar + tb), ((j >> 1) - 1) & 1, a.polls))) { ok = false; break; }
-      const uint8_t *rec = sb + L::kOffRing + s * L::kStage + pg0 * L::kRec;
+      const Phase full = {bar(kBarFull + s), (uint32_t)(jp / kStages) & 1u};
+      ok = j < 2 ? mbar_wait_warp(full.bar, full.parity, a.polls) : wait_all(a.polls, full, values ? pv_done(j - 2) : two(kBarSFull, j - 2));
+      if (!ok) break;
+      const uint8_t *stage = sb + L::kOffRing + s * L::kStage;
       uint8_t *tile = sb + (values ? L::kOffVb : L::kOffKb) + tb * L::kTile;
       if (values) {
-        const uint32_t gone = gone_s[jp & (kGone - 1)] >> pg0;
-        const int valid = w.k_end - w.k_begin - jp * kKeys;
-#pragma unroll
-        for (int i = 0; i < kPagesPerWarp; ++i)
-          decode_values<HD>(rec + i * L::kRec, tile, pg0 + i, (gone >> i) & 1u ? 0 : valid, lane);
+        decode_values<HD>(stage, tile, part, w.k_end - w.k_begin - jp * kKeys, gone_s[jp & (kGone - 1)], lane);
       } else {
 #pragma unroll
-        for (int i = 0; i < kPagesPerWarp; ++i) decode_keys<HD>(rec + i * L::kRec, tile, pg0 + i, lane);
+        for (int i = 0; i < kPagesPerWarp; ++i)
+          decode_keys<HD>(stage + (part * kPagesPerWarp + i) * L::kRec, tile, part * kPagesPerWarp + i, lane);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -554,7 +604,18 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
     // this row's values of the two warps that share it: [block parity][half]
     float *both_s = reinterpret_cast<float *>(sb + L::kOffMax) + 32 * q4 + lane;
+    // the scores are mostly there: a test costs an eighth of a wait
+    auto ready = [&](uint32_t b, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_test(b, parity)) || mbar_wait_warp(b, parity, a.polls);
+    };
+    auto pair_any = [&](bool x) {            // of the two warps that share a row
+      uint32_t r;
+      asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                   : "=r"(r) : "r"((uint32_t)x), "r"(4 + q4) : "memory");
+      return r != 0u;
+    };
     auto pair_sync = [&]() { named_sync(4 + q4, 64); };
+    const uint64_t newvis = fresh ? kvq_visible(a, w.B, tau_s, tok) : 0ull;
     prepare();
     const float rscale = row_s[32 * g + lane];
     if (half == 0) {
@@ -570,7 +631,6 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     tc::wait_st();
     tc::fence_before_sync();
     if (half == 0 && lane == 0) mbar_arrive(bar(kBarQReady));
-    const uint64_t newvis = fresh ? kvq_visible(a, w.B, tau_s, tok) : 0ull;
     const uint32_t tO = trow + kColO;
     // a row that sees a new token with an odd value is NaN
     const bool odd = (newvis & ((uint64_t)odd_s[1] << 32 | odd_s[0])) != 0ull;
@@ -582,139 +642,158 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     auto key_loop = [&](auto rc) {
       constexpr int RC = decltype(rc)::value;
       constexpr int KW = kKeys / (RC * kHalves);   // this warp's keys per block: 64, 32 or 16
-      const int k_lo = (kp * kHalves + half) * KW;
+      // keys k_lo .. (with 64 of them: 32 there, and 32 in the second unit)
+      const int k_lo = RC == 4 ? 64 * (kp >> 1) + 32 * half + 16 * (kp & 1) : 64 * kp + 32 * half;
       // A warp whose wait gave up still meets its partner once, with a NaN in
       // the maximum's place (a maximum is never NaN), so both leave the loop.
       auto block = [&](auto newc) {            // block j; false: leave the loop
         constexpr bool is_new = decltype(newc)::value != 0;
         const int tb = is_new ? 0 : j & 1, jp = is_new ? -1 : j - fresh;
-        const uint32_t tS = trow + kColS + tb * kKeys + k_lo;
+        const uint32_t tS[2] = {trow + unit_col(j, k_lo >> 6) + (k_lo & 63), trow + unit_col(j, 1) + (k_lo & 63)};
         // keys that count: all of a whole block's, else one bit each
         const int valid = is_new ? 0 : w.k_end - w.k_begin - jp * kKeys;
-        ok = ok && mbar_wait_warp(bar(kBarSFull + tb), (j >> 1) & 1, a.polls);
+        ok = ok && ready(bar(kBarSFull + tb), (j >> 1) & 1);
         const uint32_t gone = is_new || !ok ? 0u : gone_s[jp & (kGone - 1)];
         const bool whole = !is_new && valid >= kKeys && gone == 0u;
         const float f = whole ? rscale : 1.f;      // t = f s
-        uint64_t vis = 0;
-        if (is_new) {
-          vis = shift_right(newvis, k_lo);
-        } else if (!whole) {
-          vis = kvq_low_bits(valid - k_lo);
-          for (int i = 0; i < KW / 16; ++i)
-            if ((gone >> (k_lo / 16 + i)) & 1u) vis &= ~(0xffffull << (16 * i));
-        }
         tc::fence_after_sync();
-        // the scores of this warp's keys CW q ..; where some do not count, as t
-        // with -inf for those.  (64 keys are read twice, 32 at a time: once for the
-        // maximum, once for the weights.  That leaves registers for 20 warps.)
+        // the scores of this warp's keys, 32 at a time (q: those of the second
+        // unit); where some do not count, as t with -inf for those
         constexpr int CW = KW < 32 ? KW : 32;
         uint32_t sr[CW];
         auto fetch = [&](int q) {
-          if constexpr (CW == 16) tc::ld16(tS, sr);
-          else tc::ld32(tS + CW * q, sr);
+          if constexpr (CW == 16) tc::ld16(tS[q], sr);
+          else tc::ld32(tS[q], sr);
           tc::wait_ld();
           if (whole) return;
+          const int k0 = k_lo + 64 * q;
           if (is_new) {
+            const uint32_t v = (uint32_t)shift_right(newvis, k0);
 #pragma unroll
-            for (int i = 0; i < CW; i += 2) {
-              const float4 x = load_shared4(base + L::kOffNewKv + (k_lo + CW * q + i) * 8);   // of two keys
-              const uint32_t v = (uint32_t)(vis >> (CW * q + i));
-              sr[i] = __float_as_uint(v & 1u ? fmaf(__uint_as_float(sr[i]), x.x * rscale, x.y) : -INFINITY);
-              sr[i + 1] = __float_as_uint(v & 2u ? fmaf(__uint_as_float(sr[i + 1]), x.z * rscale, x.w) : -INFINITY);
+            for (int i = 0; i < CW; i += 8) {
+              if (k0 + i >= w.n) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sr[i + e] = __float_as_uint(-INFINITY);
+                continue;
+              }
+              float4 x[4];                   // of two keys each
+#pragma unroll
+              for (int e = 0; e < 4; ++e) x[e] = load_shared4(base + L::kOffNewKv + (k0 + i + 2 * e) * 8);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                uint32_t *t = sr + i + 2 * e;
+                t[0] = __float_as_uint((v >> (i + 2 * e)) & 1u ? fmaf(__uint_as_float(t[0]), x[e].x * rscale, x[e].y) : -INFINITY);
+                t[1] = __float_as_uint((v >> (i + 2 * e)) & 2u ? fmaf(__uint_as_float(t[1]), x[e].z * rscale, x[e].w) : -INFINITY);
+              }
             }
           } else {
-            const uint32_t v = (uint32_t)(vis >> (CW * q));
+            uint32_t v = (uint32_t)kvq_low_bits(valid - k0);
+            for (int i = 0; i < CW / 16; ++i)
+              if ((gone >> (k0 / 16 + i)) & 1u) v &= ~(0xffffu << (16 * i));
 #pragma unroll
             for (int i = 0; i < CW; ++i)
               sr[i] = __float_as_uint((v >> i) & 1u ? __uint_as_float(sr[i]) * rscale : -INFINITY);
           }
         };
-        // the row's maximum over both warps' keys
-        float mx = -INFINITY;
+        // weights 2^(t - mu) as f16 pairs, in the values' order, and their sum
+        uint32_t pw[KW / 2];
+        float2 sum;
+        auto weigh = [&](float mu, bool held) {      // held: sr holds the (only) scores
+          const float2 f2 = make_float2(f, f), b2 = make_float2(-mu, -mu);
+          sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int q = 0; q < KW / CW; ++q) {
-          fetch(q);
+          for (int q = 0; q < KW / CW; ++q) {
+            if (is_new && k_lo + 64 * q >= w.n) {
 #pragma unroll
-          for (int i = 0; i < CW; i += 16) {
-            float v[16];
+              for (int e = 0; e < CW / 2; ++e) pw[CW / 2 * q + e] = 0u;
+              continue;
+            }
+            if (!held) fetch(q);
+            float4 iv;                       // the new tokens' share of the sum
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(sr[i + c]);
-            const float m0 = max3(max3(v[0], v[1], v[2]), v[3], v[4]), m1 = max3(max3(v[5], v[6], v[7]), v[8], v[9]);
-            const float m2 = max3(max3(v[10], v[11], v[12]), v[13], v[14]);
-            mx = fmaxf(mx, max3(max3(m0, m1, m2), v[15], v[15]) * f);
+            for (int e = 0; e < CW / 2; ++e) {
+              const float2 x = fma_f32x2(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, b2);
+              const float2 p = make_float2(ex2(x.x), ex2(x.y));
+              if (is_new) {
+                if (e % 2 == 0) iv = load_shared4(base + L::kOffNewInv + (k_lo + 64 * q + 2 * e) * 4);
+                sum = fma_f32x2(p, e % 2 == 0 ? make_float2(iv.x, iv.y) : make_float2(iv.z, iv.w), sum);
+              } else {
+                sum = add_f32x2(sum, p);
+              }
+              pw[CW / 2 * q + (e & ~3) + pair_slot(e >> 2, e & 3)] = pack_f16x2(p.x, p.y);
+            }
           }
+          if constexpr (CW == 16) {          // (chunks 2 and 3 of 32 keys)
+            if (kp & 1) {
+#pragma unroll
+              for (int e = 0; e < 8; e += 4) {
+                const uint32_t x = pw[e], y = pw[e + 1];
+                pw[e] = pw[e + 2]; pw[e + 1] = pw[e + 3];
+                pw[e + 2] = x; pw[e + 3] = y;
+              }
+            }
+          }
+        };
+        // Mostly the reference holds, which a row's sum shows: no weight of a sum
+        // of at most 2^15 is above that.
+        bool moves = true;
+        if (!is_new && j > fresh) {          // (the first of the prompt's moves it)
+          if (ok) weigh(m_ref, false);
+          moves = pair_any(!ok || (row_valid && !(m_ref > -INFINITY && sum.x + sum.y <= kMostSum)));
         }
-        tc::fence_before_sync();
-        both_s[(tb * kHalves + half) * kRows] = ok ? mx : __uint_as_float(0x7fc00000u);
-        pair_sync();
-        const float theirs = both_s[(tb * kHalves + (half ^ 1)) * kRows];
-        if (!ok || theirs != theirs) { ok = false; return false; }
-        mx = fmaxf(mx, theirs);
-        // both warps have their scores: weights may go over them, zeros for the
-        // other copies' keys first (each warp half of them)
-        const uint32_t tW = trow + kColS + tb * kKeys;
-        tc::fence_after_sync();
+        if (moves) {
+          // the row's maximum over both warps' keys
+          float mx = -INFINITY;
+#pragma unroll
+          for (int q = 0; q < KW / CW; ++q) {
+            if (!ok || (is_new && k_lo + 64 * q >= w.n)) break;
+            fetch(q);
+#pragma unroll
+            for (int i = 0; i < CW; ++i) mx = fmaxf(mx, __uint_as_float(sr[i]) * f);
+          }
+          both_s[(tb * kHalves + half) * kRows] = ok ? mx : __uint_as_float(0x7fc00000u);
+          pair_sync();
+          const float theirs = both_s[(tb * kHalves + (half ^ 1)) * kRows];
+          if (!ok || theirs != theirs) { ok = false; return false; }
+          mx = fmaxf(mx, theirs);
+          const bool move = row_valid && mx > m_ref + kLift;
+          const float m_new = move ? mx - kLift : m_ref;
+          const float alpha = move ? ex2(m_ref - m_new) : 1.f;     // m_ref = -inf -> 0
+          l *= alpha;
+          m_ref = m_new;
+          // O's rows may be scaled once the previous block's P V is done
+          if (!is_new && __any_sync(0xffffffffu, move) && j > 0) {
+            if (!mbar_wait_warp(bar(kBarPvDone + ((j - 1) & (kPvBars - 1))), ((j - 1) / kPvBars) & 1, a.polls)) { ok = false; return true; }
+            tc::fence_after_sync();
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {  // this half of its columns
+              uint32_t o[16];
+              tc::ld16(tO + half * (HD / 2) + 16 * c, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tc::st16(tO + half * (HD / 2) + 16 * c, o);
+            }
+          }
+          weigh(m_ref == -INFINITY ? 0.f : m_ref, is_new || KW == CW);
+        }
+        // they go over the first unit's scores, zeros for the other copies' keys
+        const uint32_t tW = trow + unit_col(j, 0) + 32 * half;
         if constexpr (RC > 1) {
           uint32_t z[KW / 2];
 #pragma unroll
           for (int e = 0; e < KW / 2; ++e) z[e] = 0u;
 #pragma unroll
           for (int c = 1; c < RC; ++c) {
-            const uint32_t at = tW + weight_col((kp + c) % RC * 2 * KW) + half * (KW / 2);
+            const uint32_t at = tW + (kp + c) % RC * (KW / 2);
             if constexpr (KW == 16) tc::st8(at, z);
             else tc::st16(at, z);
           }
         }
-        // reference: moves only when this block's max outgrows it
-        const bool move = row_valid && mx > m_ref + kLift + kHeadroom;
-        const float m_new = move ? mx - kLift : m_ref;
-        const float alpha = move ? ex2(m_ref - m_new) : 1.f;     // m_ref = -inf -> 0
-        l *= alpha;
-        m_ref = m_new;
-        // weights 2^(t - m_ref) as f16 pairs
-        const float mu = m_ref == -INFINITY ? 0.f : m_ref;
-        // O's rows may be scaled once the previous block's P V is done
-        if (!is_new && __any_sync(0xffffffffu, move) && j > 0) {
-          if (!mbar_wait_warp(bar(kBarPvDone + (tb ^ 1)), ((j - 1) >> 1) & 1, a.polls)) { ok = false; return true; }
-          tc::fence_after_sync();
-#pragma unroll 1
-          for (int c = 0; c < HD / 32; ++c) {  // this half of its columns
-            uint32_t o[16];
-            tc::ld16(tO + half * (HD / 2) + 16 * c, o);
-            tc::wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::st16(tO + half * (HD / 2) + 16 * c, o);
-          }
-        }
-        const uint32_t tP = tW + weight_col(k_lo);
-        const float2 f2 = make_float2(f, f), b2 = make_float2(-mu, -mu);
-        float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int q = 0; q < KW / CW; ++q) {
-          if (KW > CW) fetch(q);
-          if (is_new) {                      // the new tokens' share of the sum, key by key
-#pragma unroll
-            for (int i = 0; i < CW; i += 4) {
-              const float4 x = load_shared4(base + L::kOffNewInv + (k_lo + CW * q + i) * 4);
-              l = fmaf(ex2(__uint_as_float(sr[i]) - mu), x.x, l);
-              l = fmaf(ex2(__uint_as_float(sr[i + 1]) - mu), x.y, l);
-              l = fmaf(ex2(__uint_as_float(sr[i + 2]) - mu), x.z, l);
-              l = fmaf(ex2(__uint_as_float(sr[i + 3]) - mu), x.w, l);
-            }
-          }
-          uint32_t pw[CW / 2];
-#pragma unroll
-          for (int e = 0; e < CW / 2; ++e) {
-            const float2 x = fma_f32x2(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, b2);
-            const float2 p = make_float2(ex2(x.x), ex2(x.y));
-            sum = add_f32x2(sum, p);
-            pw[e] = pack_f16x2(p.x, p.y);
-          }
-          if constexpr (CW == 16) tc::st8(tP, pw);
-          else tc::st16(tP + CW / 2 * q, pw);
-        }
-        if (!is_new) l += sum.x + sum.y;
+        if constexpr (KW == 16) tc::st8(tW + kp * 8, pw);
+        else if constexpr (KW == 32) tc::st16(tW + kp * 16, pw);
+        else tc::st32(tW, pw);
+        l += sum.x + sum.y;
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
@@ -732,57 +811,18 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     if (R == 4) key_loop(IntC<4>{});
     else if (R == 2) key_loop(IntC<2>{});
     else key_loop(IntC<1>{});
-    if (ok && j > 0 && !mbar_wait_warp(bar(kBarPvDone + ((j - 1) & 1)), ((j - 1) >> 1) & 1, a.polls)) ok = false;
+    if (ok && j > 0 && !mbar_wait_warp(bar(kBarPvDone + ((j - 1) & (kPvBars - 1))), ((j - 1) / kPvBars) & 1, a.polls)) ok = false;
     if (!ok && lane == 0) give_up();
     tc::fence_after_sync();
     // -------------------------------------------------------- epilogue
-    const bool failed = !ok || *(volatile int *)flag_s != 0;
-    const int64_t orow = (t0 + tok) * a.Hq + w.kvh * a.G + (row_valid ? grow - tok * a.G : 0);
-    // columns [c0, c0 + n), n <= 32, of this thread's row: sums v relative to
-    // reference mr, weights' sum lt
-    auto write_cols = [&](const float *v, int c0, int n, float lt, float mr) {
-      if (w.n_splits == 1) {
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out + orow * HD + c0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (8 * e < n) dst[e] = make_uint4(pack_bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
-                              pack_bf16x2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
-                              pack_bf16x2(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
-                              pack_bf16x2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
-      } else {
-        const int64_t prow = (int64_t)w.split * a.T * a.Hq + orow;
-        float4 *dst = reinterpret_cast<float4 *>(a.o_part + prow * HD + c0);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (4 * e < n) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        if (c0 == 0) a.ml_part[prow] = make_float2(mr, lt);
-      }
-    };
-    // the row's sum over both warps' keys (the maxima's places, block parity 0)
-    both_s[half * kRows] = l;
-    named_sync(3, 8 * 32);
-    l += both_s[(half ^ 1) * kRows];
-    if (R == 1) {
-      if (warp_valid) {
+    // Every row, and every copy of one, puts its output, reference and sums into
+    // the idle ring; then a warp takes four rows at a time, so that it writes whole lines.
+    constexpr int LD = HD + 4;
+    float *part = reinterpret_cast<float *>(sb + L::kOffRing);   // [R][groups * 32][LD]
+    if (warp_valid) {
+      float *mine = part + ((kp * groups + g) * 32 + lane) * LD;
 #pragma unroll 1
-        for (int c = 0; c < HD / 64; ++c) {
-          const int c0 = half * (HD / 2) + 32 * c;
-          uint32_t o[32];
-          tc::ld32(tO + c0, o);
-          tc::wait_ld();
-          if (!row_valid || failed) continue;
-          write_cols(reinterpret_cast<const float *>(o), c0, 32, l, m_ref);
-        }
-      }
-    } else {
-      // every copy puts its sums and reference in the idle ring; then each
-      // warp merges the R partials of its share of the columns
-      float *part = reinterpret_cast<float *>(sb + L::kOffRing);   // [R][groups][32][HD + 4]
-      float *mine = part + ((kp * groups + g) * 32 + lane) * (HD + 4);
-#pragma unroll 1
-      for (int c = 0; c < HD / 64; ++c) {
-        const int c0 = half * (HD / 2) + 32 * c;
+      for (int c0 = half * (HD / 2); c0 < (half + 1) * (HD / 2); c0 += 32) {
         uint32_t o[32];
         tc::ld32(tO + c0, o);
         tc::wait_ld();
@@ -793,33 +833,49 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
                           __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
       }
       if (half == 0) *reinterpret_cast<float2 *>(mine + HD) = make_float2(m_ref, l);
-      named_sync(3, 8 * 32);
-      if (row_valid && !failed) {
-        const int cw = HD / (R * kHalves), cb = (kp * kHalves + half) * cw;    // 8, 16 or 32 columns
-        const float *row = part + (g * 32 + lane) * (HD + 4);                  // copy 0; the others:
-        const int next = groups * 32 * (HD + 4);
-        float2 ml[4];                          // the copies' references and sums, read together
+      else mine[HD + 2] = l;
+    }
+    named_sync(3, 8 * 32);
+    const int n_rows = *(volatile int *)flag_s != 0 ? 0 : min(32 * groups, w.M - w.row0);
+    const int ln = lane & 7;                 // eight lanes a row, four columns of every 32 each
+    for (int r0 = 4 * (warp - kSoftmaxWarp); r0 < n_rows; r0 += 4 * 8) {
+      const int r = r0 + (lane >> 3);
+      if (r >= n_rows) continue;
+      const float *row = part + r * LD;      // copy 0; the others follow
+      const int next = groups * 32 * LD;
+      float4 ml[4], v[HD / 32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          ml[c] = c < R ? *reinterpret_cast<const float2 *>(row + c * next + HD) : make_float2(-INFINITY, 0.f);
-        const float mt = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
-        float lt = 0.f, v[32];
+      for (int c = 0; c < 4; ++c)
+        ml[c] = c < R ? *reinterpret_cast<const float4 *>(row + c * next + HD) : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+      const float mt = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+      float lt = 0.f;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+      for (int k = 0; k < HD / 32; ++k) v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= R) break;
-          const float wc = ex2(ml[c].x - (mt == -INFINITY ? 0.f : mt));   // -inf reference -> 0
-          lt += wc * ml[c].y;
+      for (int c = 0; c < 4; ++c) {
+        if (c >= R) break;
+        const float wc = ex2(ml[c].x - (mt == -INFINITY ? 0.f : mt));   // -inf reference -> 0
+        lt = fmaf(wc, ml[c].y + ml[c].z, lt);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (4 * e >= cw) break;
-            const float4 p4 = *reinterpret_cast<const float4 *>(row + c * next + cb + 4 * e);
-            v[4 * e] += wc * p4.x; v[4 * e + 1] += wc * p4.y;
-            v[4 * e + 2] += wc * p4.z; v[4 * e + 3] += wc * p4.w;
-          }
+        for (int k = 0; k < HD / 32; ++k) {
+          const float4 x = *reinterpret_cast<const float4 *>(row + c * next + 32 * k + 4 * ln);
+          v[k] = make_float4(fmaf(wc, x.x, v[k].x), fmaf(wc, x.y, v[k].y), fmaf(wc, x.z, v[k].z), fmaf(wc, x.w, v[k].w));
         }
-        write_cols(v, cb, cw, lt, mt);
+      }
+      const int at = w.row0 + r, token = div_by(at, a.by_G);
+      const int64_t orow = (t0 + token) * a.Hq + w.kvh * a.G + at - token * a.G;
+      if (w.n_splits == 1) {
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        uint2 *dst = reinterpret_cast<uint2 *>((__nv_bfloat16 *)a.out + orow * HD) + ln;
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k)
+          dst[8 * k] = make_uint2(pack_bf16x2(v[k].x * inv, v[k].y * inv), pack_bf16x2(v[k].z * inv, v[k].w * inv));
+      } else {
+        const int64_t prow = (int64_t)w.split * a.T * a.Hq + orow;
+        float4 *dst = reinterpret_cast<float4 *>(a.o_part + prow * HD) + ln;
+#pragma unroll
+        for (int k = 0; k < HD / 32; ++k) dst[8 * k] = v[k];
+        if (ln == 0) a.ml_part[prow] = make_float2(mt, lt);
       }
     }
   }
@@ -828,9 +884,11 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   __syncthreads();
   // after a wait that gave up, the copies still in flight land before the CTA
   // can exit (default limit)
-  if (warp == 0 && *(volatile int *)flag_s)
-    for (int j = max(0, issued - kStages); j < issued; ++j)
-      (void)mbar_wait_warp(bar(kBarFull + j % kStages), (j / kStages) & 1);
+  if (producer && *(volatile int *)flag_s) {
+    (void)mbar_wait_warp(bar(kBarRaw), 0);
+    for (int j = issued - 3; j < issued; j += 2)         // (issued: the last one's number and 1)
+      if (j >= 0) (void)mbar_wait_warp(bar(kBarFull + j % kStages), (j / kStages) & 1);
+  }
   if (warp == 1) {
     tc::fence_after_sync();
     tc::dealloc(tmem, L::kTmemCols);
