@@ -604,10 +604,6 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     const uint32_t trow = tmem + ((uint32_t)(32 * q4) << 16);
     // this row's values of the two warps that share it: [block parity][half]
     float *both_s = reinterpret_cast<float *>(sb + L::kOffMax) + 32 * q4 + lane;
-    // the scores are mostly there: a test costs an eighth of a wait
-    auto ready = [&](uint32_t b, uint32_t parity) {
-      return __all_sync(0xffffffffu, mbar_test(b, parity)) || mbar_wait_warp(b, parity, a.polls);
-    };
     auto pair_any = [&](bool x) {            // of the two warps that share a row
       uint32_t r;
       asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
@@ -635,7 +631,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     // a row that sees a new token with an odd value is NaN
     const bool odd = (newvis & ((uint64_t)odd_s[1] << 32 | odd_s[0])) != 0ull;
     float m_ref = -INFINITY, l = odd ? __uint_as_float(0x7fc00000u) : 0.f;
-    bool ok = true;
+    bool ok = true, next_ready = false;
     int j = 0;
     // the key loop, compiled once per copy count, the new tokens' block by itself
     // (a factor and a ve for each key)
@@ -652,7 +648,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         const uint32_t tS[2] = {trow + unit_col(j, k_lo >> 6) + (k_lo & 63), trow + unit_col(j, 1) + (k_lo & 63)};
         // keys that count: all of a whole block's, else one bit each
         const int valid = is_new ? 0 : w.k_end - w.k_begin - jp * kKeys;
-        ok = ok && ready(bar(kBarSFull + tb), (j >> 1) & 1);
+        ok = ok && (next_ready || mbar_wait_warp(bar(kBarSFull + tb), (j >> 1) & 1, a.polls));
         const uint32_t gone = is_new || !ok ? 0u : gone_s[jp & (kGone - 1)];
         const bool whole = !is_new && valid >= kKeys && gone == 0u;
         const float f = whole ? rscale : 1.f;      // t = f s
@@ -794,9 +790,12 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         else if constexpr (KW == 32) tc::st16(tW + kp * 16, pw);
         else tc::st32(tW, pw);
         l += sum.x + sum.y;
+        const Phase after = two(kBarSFull, j + 1);                         // (a test's latency passes here)
+        const bool there = mbar_test(after.bar, after.parity);
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
+        next_ready = __all_sync(0xffffffffu, there);
         if (lane == 0) mbar_arrive(bar(kBarPFull + tb));   // (one for each parity: a warp may be a block ahead of another)
         return true;
       };
