@@ -498,3 +498,24 @@ def test_other_stream_and_captured_chain():
         graph.replay()
         assert all(torch.equal(a, b) for a, b in zip(want, (out, cache, kr, vr)))
     assert pkg.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("B", [1, 2, 3, 6, 16])
+@pytest.mark.parametrize("hd", [128, 64])
+def test_verify_references_that_move_apart(B, hd):
+    """Rows of many sizes over pages of many sizes: each row's largest score moves at blocks of its own, by little and by
+    much; one row holds a NaN and one an infinity."""
+    lens, g = (1500, 333, 2049), torch.Generator().manual_seed(77 + B)
+    cache, table, cu, q, kn, vn, tau = case(B, lens, [B] * 3, "paired", "bf16", 4, 2, hd)
+    ks = cache[..., 16 * hd:17 * hd]
+    step = torch.randint(0, 6, cache.shape[:1] + (1, 1), generator=g)
+    spare = ks >= 0xf8
+    ks.copy_(torch.where(spare, ks, (0x50 + 8 * step + torch.randint(0, 8, ks.shape, generator=g)).to(torch.uint8)))
+    q *= 2.0 ** torch.randint(-3, 3, q.shape[:2] + (1,), generator=g).to(q)
+    q[1, 0, 3], q[0, 5, 7] = float("nan"), float("inf")
+    out, ws = verify(q.cuda(), cache.cuda(), table, kn.cuda(), vn.cuda(), i32(tau), lens, cu, B, dict(base=1e4), 0.09, "paired")
+    assert pkg.read_status(ws) == 0
+    want, off = ref.verify(q, cache, table, kn, vn, tau, lens, cu, dict(base=1e4), 0.09, "paired", 0, 2.0 ** -11)
+    # each of the at most 2049 + 32 products may be off by 2^-32 of its row's largest weight times the value
+    v = max(float(ref.rows(cache, table, b, 0, n)[1].abs().nan_to_num(0).max()) for b, n in enumerate(lens))
+    close(out, want, off + 2081 * 2.0 ** -32 * max(v, float(vn.abs().max())), "bf16")
