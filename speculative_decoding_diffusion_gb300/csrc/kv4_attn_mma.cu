@@ -1,20 +1,25 @@
 // kv4_attn_mma.cu -- simsd_kv4_verify for bf16 data, few query rows a KV head
 // (decode steps, short blocks).
 //
-// A CTA owns up to 32 rows of a (sequence, KV head) and a range of its keys; its
-// four warps take 32 keys (two pages) in turns, each with a running reference,
-// sums and an output of its own, merged at the end.  Codes go from shared
-// memory to registers, where a conversion and a product with the group's scale
-// make them the f16 operand of an MMA: S^T = K Q^T and O^T += V^T P^T, so that
-// keys (and the head's elements) fill the 16 rows of an MMA and the query rows
-// its 8 columns -- four rows cost an eighth of what 32 do, nothing decoded is
-// ever stored, and the cache's order of bytes is that of the operands: a lane's
-// elements of a key lie together, and a value byte holds the two neighbouring
-// keys that share a register.  The weights P change from the product's layout to
-// the operand's by transposing 8 x 8 tiles in registers.
+// A CTA owns up to 16 rows of a (sequence, KV head) and a range of its keys; its
+// warps take 32 keys (two pages) in turns, each with a running reference, sums and
+// an output of its own, merged at the end.  Codes go from shared memory to
+// registers, where a conversion and a product with the group's scale make them the
+// f16 operand of an MMA: S^T = K Q^T and O^T += V^T P^T, so that keys (and the
+// head's elements) fill the 16 rows of an MMA and the query rows its 8 columns,
+// nothing decoded is ever stored, and the cache's order of bytes is that of the
+// operands: a lane's elements of a key lie together, and a value byte holds the two
+// neighbouring keys that share a register.  The weights P change from the product's
+// layout to the operand's by transposing 8 x 8 tiles in registers.
 //
 // A page and head is one bulk copy of 18 hd bytes into the warp's own ring, so
 // warps meet only for the set-up and the merge.
+//
+// Bytes bound it where there are many units: 256 sequences of 256..8192 keys, one
+// token, 32 / 8 heads of 128, take 214 us, 0.92 of the copy rate; 64 of 1..4096 39 us
+// (0.60: set-up, rows and the last wave), 8 of 32768 61 us (0.74).  With 16 rows it is
+// the decoding and the MMAs, which feed 16 columns at a legacy rate: 64 x 4096, 92 us
+// (0.50).  At 32 rows the tcgen05 kernel is faster (64 x 4096: 131 us, here 158).
 #include <atomic>
 
 #include "common.cuh"

@@ -8,19 +8,28 @@
 // most 8 stale, so p <= 2^15 fits f16.  One CTA per (key split, KV head x 128-row
 // tile, sequence); rows stack new tokens x heads of the group, so a byte of the
 // cache is read and decoded once for all of them.
-//   warp 0       one bulk copy per page (18 hd bytes: keys, values, scales)
+//   warps 0, 3   one bulk copy per page (18 hd bytes: keys, values, scales), a
+//                block each in turns
 //   warp 1       TMEM owner; issues the score MMAs; warp 2 the P V MMAs
-//   warp 3       nothing (its place keeps the softmax warps on their TMEM lanes)
 //   warps 4-11   softmax, two warps per 32 rows: one thread of each per row,
-//                half of the block's keys each; the halves agree on the row's
-//                reference through shared memory.  Rows of tiles of at most 64
+//                half of the block's keys each.  Rows of tiles of at most 64
 //                rows are replicated and the copies split the keys again
 //   warps 12-15  codes times scales to f16 tiles, swizzled for the MMA: two pages
 //                of a block's keys each; warps 16-19 of its values
 // Warps 4-19 first rotate the query rows and the new keys; the new tokens are a
-// block of their own ahead of the prompt.  Lanes of a decoding warp are set on
-// elements so that neither their reads nor their writes meet in a bank.
+// block of their own ahead of the prompt.  A row's reference is not looked for in
+// every block: the weights are made with the one there is, and their sum, needed
+// anyhow, shows whether it holds (without the maxima 150 -> 137 us for 8 x 32768).
 // Every wait is bounded (status bit, drain, return).
+//
+// What bounds it (2.07 GHz): at 128 rows the softmax's chain, 2100 cycles a block of
+// 128 keys (scores from TMEM, 340 cycles of exponentials and packing twice, the
+// pair's barrier, weights to TMEM), where the tensor cores need 1024; at 64 rows
+// the decoding warps, 1600 to 1900 (700 to 1000 of it decoding, the rest the
+// latencies of waits and arrivals); and 14000 cycles of set-up and 4300 of epilogue
+// a CTA.  8 x 32768 keys, 16 + 16 new tokens, 32 / 8 heads of 128: 137 us, of 70
+// on the tensor cores; 64 x 4096, 8 + 8: 138 us, of 48 by bytes; 256 x 256..8192,
+// 4..8: 531 us, of 206 by bytes.
 #include <atomic>
 
 #include "common.cuh"

@@ -2,6 +2,8 @@
 //
 // A CTA takes 16 rows of the output; codes are multiplied by their scale in f16
 // (exact).  Bytes bound it: 9 in for every 16 elements, 16 to 64 out.
+// 262144 positions of 8 heads of 128 to bf16: 260 us, 5.3 TB/s (0.79 of the copy
+// rate); 576,000 to e4m3 395 us, 4.7 TB/s (0.70), where the conversions count too.
 #include "kv4.cuh"
 #include "kvq.cuh"
 #include "vec.cuh"

@@ -495,7 +495,8 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, bool four, KvqPlan *p) {
   const int sms = device_sm_count();
   // CTAs of an SM.  Few rows of a 4-bit cache: two, or where there are units for
   // two waves of them four of half as many warps (256 sequences of 256..8192 keys,
-  // 4 rows: 214 and not 230 us; 64 of up to 4096, less than a wave: 55 and not 39).
+  // 4 rows: 214 and not 230 us; 64 of up to 4096, less than a wave: 55 and not 39);
+  // six warps for 16 rows, whose sums take twice the registers.
   p->warps = p->rows_per_tile == 16 ? 6 : per_seq * d->batch >= 8 * sms ? 4 : 8;
   const int ctas = !tc ? 2 : !few ? 1 : p->warps == 4 ? 4 : 2;
   plan_splits(d->batch, per_seq, (int64_t)d->max_pages_per_seq * kPageTokens, ctas * sms, few ? 2 : kRamp, p);

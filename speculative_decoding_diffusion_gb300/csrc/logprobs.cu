@@ -14,6 +14,11 @@
 // segments whose maximum reaches it are read again (some 22 of 594 for k = 20
 // and 151,936 entries) and only the entries that do are sorted.  A key of 64
 // bits, the value's ordered bits over the inverted index, makes the order total.
+//
+// The first pass is bound by its reads: 1536 rows of 151,936 in bf16 87 us, 5.4 TB/s
+// (0.80 of the copy rate), in CTAs of 128 threads, eight an SM (ten: 2% less on many
+// rows, 10% more on few; 256 threads, four: 103 us).  Both passes: 101 us; four rows
+// 6.3 us, two launches and their round trips.
 #include <math.h>
 
 #include "common.cuh"
