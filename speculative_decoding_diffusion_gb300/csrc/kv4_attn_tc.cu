@@ -69,10 +69,13 @@ constexpr uint32_t kUnitCols = 64;
 constexpr uint32_t kColO = kUnits * kUnitCols;
 __device__ __forceinline__ uint32_t unit_col(int j, int which) { return (uint32_t)((j + 2 * which) % kUnits) * kUnitCols; }
 __host__ __device__ constexpr uint32_t weight_col(int key) { return (uint32_t)((key & 32) + (key >> 6) * 16 + (key & 31) / 2); }
-constexpr int kPvBars = 4;           // (the scores' warp looks three blocks back)
+// Barriers of the weights and of the P V, by block: the scores' warp looks three
+// blocks back, and the softmax can be two blocks ahead of a P V whose values are
+// late, so a pair of barriers would pass a phase that is still to be waited for.
+constexpr int kPvBars = 4;
 
 enum { kBarFull = 0, kBarEmpty = kBarFull + kStages, kBarKbFull = kBarEmpty + kStages, kBarVbFull = kBarKbFull + 2,
-       kBarSFull = kBarVbFull + 2, kBarPFull = kBarSFull + 2, kBarPvDone = kBarPFull + 2,
+       kBarSFull = kBarVbFull + 2, kBarPFull = kBarSFull + 2, kBarPvDone = kBarPFull + kPvBars,
        kBarQReady = kBarPvDone + kPvBars, kBarNewRead = kBarQReady + 1, kBarRaw = kBarNewRead + 1, kNumBars = kBarRaw + 1 };
 
 template <int HD>
@@ -337,7 +340,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   }
   if (warp == kPvWarp) {
     for (int i = lane; i < kBarRaw; i += 32) {      // (that one is made)
-      const bool rows = i >= kBarPFull && i < kBarPFull + 2;
+      const bool rows = i >= kBarPFull && i < kBarPFull + kPvBars;
       const bool tiles = i >= kBarKbFull && i < kBarVbFull + 2;
       mbar_init(bar(i), rows ? n_valid : tiles ? kDecoders : i >= kBarEmpty && i < kBarEmpty + kStages ? 2 * kDecoders
                       : i == kBarQReady ? 4 : i == kBarNewRead ? kDecoders : 1);
@@ -359,6 +362,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   int issued = 0;                            // producers: blocks whose loads were started
   const float2 *cs_s = reinterpret_cast<const float2 *>(sb + L::kOffCs);
   auto pv_done = [&](int j) { return Phase{bar(kBarPvDone + (j & (kPvBars - 1))), (uint32_t)(j / kPvBars) & 1u}; };
+  auto p_full = [&](int j) { return Phase{bar(kBarPFull + (j & (kPvBars - 1))), (uint32_t)(j / kPvBars) & 1u}; };
   auto two = [&](int first, int j) { return Phase{bar(first + (j & 1)), (uint32_t)(j >> 1) & 1u}; };   // of a pair of barriers
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
   // These warps together rotate the query rows and, in the CTA that owns the new
@@ -497,7 +501,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
     for (int j = 0; ok && j < n_blocks; ++j) {
       const int tb = j & 1;
-      const Phase keys = two(kBarKbFull, j), weights = two(kBarPFull, j - 2);
+      const Phase keys = two(kBarKbFull, j), weights = p_full(j - 2);
       ok = j < 3 ? mbar_wait_warp(keys.bar, keys.parity, a.polls) && (j < 2 || mbar_wait_warp(weights.bar, weights.parity, a.polls))
                  : wait_all(a.polls, pv_done(j - 3), keys, weights);
       if (!ok) break;
@@ -518,7 +522,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
     bool ok = true;
     for (int j = 0; j < n_blocks; ++j) {
       const int tb = j & 1, jp = j - fresh;
-      ok = wait_all(a.polls, two(kBarVbFull, j), two(kBarPFull, j));
+      ok = wait_all(a.polls, two(kBarVbFull, j), p_full(j));
       if (!ok) break;
       tc::fence_after_sync();
       const int depth = jp < 0 ? n_pad : min(kKeys, (w.k_end - w.k_begin - jp * kKeys + 15) & ~15);
@@ -805,7 +809,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         tc::fence_before_sync();
         __syncwarp();
         next_ready = __all_sync(0xffffffffu, there);
-        if (lane == 0) mbar_arrive(bar(kBarPFull + tb));   // (one for each parity: a warp may be a block ahead of another)
+        if (lane == 0) mbar_arrive(p_full(j).bar);
         return true;
       };
       if (!warp_valid) return;

@@ -186,3 +186,20 @@ def test_other_devices_are_refused():
             pkg.kv4_read(*a, None, ws)
         with pytest.raises(ValueError):
             pkg.kv4_append(a[4], k, a[2], a[3], a[0], a[1], ws, rope)
+
+
+@pytest.mark.parametrize("B", [3, 6, 16])
+def test_many_calls_wait_for_nothing_in_vain(B):
+    """Some thousand CTAs of ragged lengths: no call's waits run out, and each gives what the first gave."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 2500, (300,), generator=g).tolist()
+    cache, table, cu, q, kn, vn, tau = case(B, lens, [B] * 300, "paired", "bf16", 4, 1, 128)
+    args = [q.cuda(), cache.cuda(), i32(table), kn.cuda(), vn.cuda(), i32(tau), i32(lens), i32(cu)]
+    outs = [torch.empty_like(args[0]) for _ in range(2)]
+    rope = pkg.rope_spec()
+    ws = workspace(pkg.kv4_verify_workspace_size(*args, outs[0], B * 300, B, rope, 0.1, order=ORDER["paired"]))
+    for i in range(40):
+        pkg.kv4_verify(*args, outs[min(i, 1)], ws, B * 300, B, rope, 0.1, order=ORDER["paired"], wait_polls=50000)
+        if i:
+            assert torch.equal(outs[0], outs[1])
+    assert pkg.read_status(ws) == 0
