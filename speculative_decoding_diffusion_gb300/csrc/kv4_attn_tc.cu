@@ -28,8 +28,8 @@
 // the decoding warps, 1600 to 1900 (700 to 1000 of it decoding, the rest the
 // latencies of waits and arrivals); and 14000 cycles of set-up and 4300 of epilogue
 // a CTA.  8 x 32768 keys, 16 + 16 new tokens, 32 / 8 heads of 128: 137 us, of 70
-// on the tensor cores; 64 x 4096, 8 + 8: 138 us, of 48 by bytes; 256 x 256..8192,
-// 4..8: 531 us, of 206 by bytes.
+// on the tensor cores; 64 x 4096, 8 + 8: 140 us, of 48 by bytes; 256 x 256..8192,
+// 4..8: 532 us, of 206 by bytes.
 #include <atomic>
 
 #include "common.cuh"
