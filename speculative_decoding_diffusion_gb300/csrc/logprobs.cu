@@ -255,13 +255,17 @@ logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
   // t = c l - c m with one rounding: c m rounded is off by `shift`, the same for
   // every entry, so the sums are brought back by 2^shift.  Entries whose weight
   // is 0 all the same are raised to where t is finite (0 times it has to be 0).
+  // Up to 2^24 shift is at most a half; beyond (a part at a mask's finite fill, a
+  // temperature near 0) it would leave the exponential's range, and differences
+  // come first.
   const float ref = m == -INFINITY ? 0.f : m, cm = ref * a.c;
   const float least = L::below(fmaxf(ref - 1000.f * a.inv_c, -3e38f), ref);
   float2 s2 = make_float2(0.f, 0.f), w2 = s2;
   float shift = 0.f;
-  if (fabsf(cm) < 1e30f && least > -INFINITY) {
+  const float2 c2 = make_float2(a.c, a.c);
+  if (fabsf(cm) <= 16777216.f && least > -INFINITY) {
     shift = -fmaf(ref, a.c, -cm);
-    const float2 c2 = make_float2(a.c, a.c), m2 = make_float2(-cm, -cm);
+    const float2 m2 = make_float2(-cm, -cm);
     const typename L::Bound low = L::bound(least);
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -272,15 +276,18 @@ logprob_pass_kernel(const __grid_constant__ LogprobArgs a) {
         s2 = add_f32x2(s2, p);
         w2 = fma_f32x2(p, t, w2);
       }
-  } else {                                               // logits of 1e30 and beyond: differences first
-#pragma unroll 1
-    for (int i = 0; i < kLane; ++i) {
-      const int e = e0 + ((i / V) * 32 + lane) * V + i % V;
-      const float x = e >= 0 && e < a.vocab ? Elem<T>::load(row + e) : -INFINITY;
-      const float t = at_least((x - ref) * a.c, -1000.f), p = ex2(t);
-      s2.x += p;
-      w2.x = fmaf(p, t, w2.x);
-    }
+  } else {
+    const float2 m2 = make_float2(-ref, -ref);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) {
+        float2 t = mul_f32x2(add_f32x2(make_float2(L::entry(v[i], 2 * j), L::entry(v[i], 2 * j + 1)), m2), c2);
+        t = make_float2(at_least(t.x, -1000.f), at_least(t.y, -1000.f));
+        const float2 p = make_float2(ex2(t.x), ex2(t.y));
+        s2 = add_f32x2(s2, p);
+        w2 = fma_f32x2(p, t, w2);
+      }
   }
   float s = warp_sum(s2.x + s2.y), w = warp_sum(w2.x + w2.y);
   const float back = ex2(shift);                         // c (l - m) = t + shift
