@@ -51,7 +51,7 @@ struct LogprobArgs {
   uint32_t *status;
   int64_t stride;
   int rows, vocab, top_k, n_parts;
-  float c, inv_c, inv_t;                   // log2(e) / T and its inverse; 1 / T
+  float c, inv_c, inv_half_t;              // log2(e) / T and its inverse; 2 / T
 };
 
 // Entries (of T) in 16 bytes.
@@ -429,10 +429,12 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
     ahead += ahead_s[i];
   }
   const float log_s = m == -INFINITY ? __uint_as_float(0x7fc00000u) : log2f(s);   // NaN: nothing there
+  // ln p of a logit (halves: the difference of two finite ones stays finite)
+  auto log_p = [&](float x) { return (0.5f * x - 0.5f * m) * a.inv_half_t - log_s * kLn2; };
   if (threadIdx.x == 0) {
     if (a.tokens != nullptr && !given) raise_status(a.status, kStatusBadInput);
     if (a.logprob != nullptr)
-      a.logprob[r] = given ? (mine - m) * a.inv_t - log_s * kLn2 : __uint_as_float(0x7fc00000u);
+      a.logprob[r] = given ? log_p(mine) : __uint_as_float(0x7fc00000u);
     if (a.rank != nullptr) a.rank[r] = given ? ahead : -1;
     if (a.entropy != nullptr) a.entropy[r] = (log_s - w / s) * kLn2;
   }
@@ -509,7 +511,7 @@ logprob_finish_kernel(const __grid_constant__ LogprobArgs a) {
   if (lane < k) {
     a.top_ids[(int64_t)r * k + lane] = list == 0ull ? 0 : index_of(list);
     a.top_logprobs[(int64_t)r * k + lane] =
-        list == 0ull ? __uint_as_float(0x7fc00000u) : (value_of((uint32_t)(list >> 32)) - m) * a.inv_t - log_s * kLn2;
+        list == 0ull ? __uint_as_float(0x7fc00000u) : log_p(value_of((uint32_t)(list >> 32)));
   }
 }
 
@@ -575,7 +577,7 @@ simsd_status simsd_token_logprobs(const simsd_token_logprobs_desc *d, void *stre
   const double T = d->temperature == 0.0f ? 1.0 : (double)d->temperature;
   a.c = (float)(1.4426950408889634 / T);
   a.inv_c = (float)(T / 1.4426950408889634);
-  a.inv_t = (float)(1.0 / T);
+  a.inv_half_t = (float)(2.0 / T);
   cudaStream_t stream = (cudaStream_t)stream_ptr;
   const cudaError_t e = d->dtype == SIMSD_BF16 ? launch<__nv_bfloat16>(a, stream) : launch<float>(a, stream);
   return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;

@@ -50,3 +50,15 @@ def test_temperatures_of_the_whole_range(dtype, temperature):
     tokens = x.float().argmax(-1).cpu()
     check(x, tokens, 8, temperature)
     check(x, [0, 2, 7, 5002, 2999], 32, temperature)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("temperature", [4.0, 1e10, 1e30])
+def test_logits_further_apart_than_the_largest_number(dtype, temperature):
+    """l - M below -3.4e38, (l - M) / T inside fp32."""
+    x = torch.full((3, 4500), -3e38)
+    x[0, 5] = x[1, 4000] = x[1, 4400] = 3e38
+    x[2] = torch.linspace(-3e38, 3e38, 4500, dtype=torch.float64).float()   # (in 32 bits its step would be infinite)
+    x = x.cuda().to(DT[dtype])
+    check(x, [4, 4000, 0], 20, temperature)
+    check(x, [5, 17, 4499], 3, temperature)
