@@ -881,9 +881,12 @@ simsd_status simsd_kv4_read(const simsd_kv4_read_desc *d, void *stream);
  *   - the rotated query and each new key, relative to a power of two of the
  *     row's: an element is off by at most 2^-11 of itself or 2^-33 of the
  *     largest of its row, whichever is more;
- *   - each new value, relative to a power of two of its token's, likewise;
+ *   - each new value, relative to a power of two of its token's, likewise (or
+ *     2^-89, if that is more);
  *   - the weights that multiply the values: off by at most 2^-11 of themselves
- *     or 2^-32 of the row's largest product.
+ *     or 2^-32 of the row's largest product.  (The sum of weights has its own:
+ *     no token's share depends on any value.  Only beside a new value beyond
+ *     2^96 may it lack prompt keys that weigh less than 2^-29 of the largest.)
  * A row that sees a key of a marked group is NaN; one of a value, in that
  * group's elements; a row that sees a new token with a NaN or an infinity is
  * NaN.  A token that a row does not see has no effect on it.

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "internal.h"
+#include "kvq.cuh"
 #include "vec.cuh"
 
 namespace simsd {
@@ -106,6 +107,28 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ float2 f16x2_to_float2(uint32_t h) {
   return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
+
+// ------------------------------------------ new tokens' values in the attention
+// A new token's values are held as f16 relative to 2^ve, at most 65280 of it, and
+// its weight p = 2^(t + ve - M) multiplies them, M a reference over t + ve.  Its
+// share of the sum of weights, 2^(t - M), must not be taken from p: beside a token
+// of much larger values p is 0 where the share is not.  So the sum has an
+// exponential of its own, 2^(t - M + kShareLift), whose lift is taken back once a
+// block: t - M is at most kNewLift + 64 (ve >= -64) and, for the row's largest t, at
+// least kNewLift - 112.  M starts kNewLift below a row's largest t + ve, as far as
+// f16 weights go, so that the prompt's weights, relative to the same M, fall below
+// fp32's range only from 2^(112 - kNewLift - 126) = 2^-29 of the row's largest on.
+constexpr float kNewLift = 15.f, kShareLift = 32.f;
+constexpr float kShareUnlift = 1.f / 4294967296.f;       // 2^-kShareLift
+// 2^x, its subnormal results too (the square of the root's; for merges, whose
+// references lie as far apart): two instructions more than the approximation's, exp2f
+// takes 256 x 256..8192 keys from 539 to 541 us.
+__device__ __forceinline__ float ex2_low(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(0.5f * x));
+  return y * y;
+}
+__device__ __forceinline__ int value_exponent(float amax) { return scale_exponent(amax, -57, 119) - 7; }
 
 // ------------------------------------------------- rows of an append or a read
 constexpr int kTileRows = 16;              // most rows that a CTA takes

@@ -51,9 +51,9 @@ struct Lay {
   static constexpr int kOffMl = kOffVis + kRows * 8;   // [warps][rows] (reference, sum)
   static constexpr int kOffBar = kOffMl + kWarps * kRows * 8;
   static constexpr int kOffTau = kOffBar + kWarps * kStages * 8;
-  static constexpr int kOffNewKv = kOffTau + kMaxB * 4;        // new tokens: 2^ke, ve; 2^-ve
-  static constexpr int kOffNewInv = kOffNewKv + kMaxNew * 8;
-  static constexpr int kOffMisc = kOffNewInv + kMaxNew * 4;    // odd new values, failure
+  static constexpr int kOffNewKv = kOffTau + kMaxB * 4;        // new tokens: 2^ke, ve; kShareLift - ve
+  static constexpr int kOffNewShare = kOffNewKv + kMaxNew * 8;
+  static constexpr int kOffMisc = kOffNewShare + kMaxNew * 4;  // odd new values, failure
   static constexpr int kOffDyn = kOffMisc + 16;
   static constexpr int kKnLd = HD * 2 + 16;            // bytes of a new key's row
   static_assert(kWarps * kRows * kXld * 4 <= kRing, "the merge fits the ring");
@@ -120,7 +120,7 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
   float2 *ml_s = reinterpret_cast<float2 *>(sb + L::kOffMl);
   int *tau_s = reinterpret_cast<int *>(sb + L::kOffTau);
   float2 *new_kv_s = reinterpret_cast<float2 *>(sb + L::kOffNewKv);
-  float *new_inv_s = reinterpret_cast<float *>(sb + L::kOffNewInv);
+  float *new_share_s = reinterpret_cast<float *>(sb + L::kOffNewShare);
   uint32_t *odd_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc);
   int *flag_s = reinterpret_cast<int *>(sb + L::kOffMisc + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -270,11 +270,11 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
       if (odd) atomicOr(odd_s + (j >> 5), 1u << (j & 31));
 #pragma unroll
       for (int m = CH / 2; m > 0; m >>= 1) va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, m));
-      const int ve = scale_exponent(va, -64, 119);
+      const int ve = value_exponent(va);
       const float down = pow2i(-ve);
       if (c == 0) {
         new_kv_s[j].y = (float)ve;
-        new_inv_s[j] = down;
+        new_share_s[j] = kShareLift - (float)ve;
       }
       __half *dst = reinterpret_cast<__half *>(vn) + ((j >> 1) * HD + c * 8) * 2 + (j & 1);
 #pragma unroll
@@ -372,6 +372,7 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
         }
     }
     // references move only when a score outgrows them
+    constexpr float lift = is_new ? kNewLift : kLift;
     bool grows = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -389,8 +390,8 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
 #pragma unroll
           for (int k = 4; k < 32; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
           if (mx > m[nt][r] + (kLift + kHeadroom)) {
-            const float alpha = ex2(m[nt][r] - (mx - kLift));         // m = -inf -> 0
-            m[nt][r] = mx - kLift;
+            const float alpha = ex2(m[nt][r] - (mx - lift));          // m = -inf -> 0
+            m[nt][r] = mx - lift;
             l[nt][r] *= alpha;
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -402,14 +403,14 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
     }
     // weights 2^(t - m) as f16 operands (keys down, rows across -> transposed)
     uint32_t pw[2][NT][2];
-    float inv[2][2];
+    float share[2][2];
     if (is_new) {
 #pragma unroll
       for (int p = 0; p < 2; ++p)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int key = j0 + 16 * p + 8 * h + g;
-          inv[p][h] = key < w.n ? new_inv_s[key] : 0.f;
+          share[p][h] = key < w.n ? new_share_s[key] : 0.f;
         }
     }
 #pragma unroll
@@ -423,8 +424,8 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
         for (int h = 0; h < 2; ++h) {
           const float e0 = ex2(fmaf(s[p][nt][2 * h], ff[nt][0], -mu[0])), e1 = ex2(fmaf(s[p][nt][2 * h + 1], ff[nt][1], -mu[1]));
           if (is_new) {
-            l[nt][0] = fmaf(e0, inv[p][h], l[nt][0]);
-            l[nt][1] = fmaf(e1, inv[p][h], l[nt][1]);
+            l[nt][0] = fmaf(ex2(s[p][nt][2 * h] - mu[0] + share[p][h]), kShareUnlift, l[nt][0]);
+            l[nt][1] = fmaf(ex2(s[p][nt][2 * h + 1] - mu[1] + share[p][h]), kShareUnlift, l[nt][1]);
           } else {
             l[nt][0] += e0;
             l[nt][1] += e1;
@@ -511,7 +512,7 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
       float top = -INFINITY;
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) top = fmaxf(top, ml_s[k * L::kRows + 8 * nt + 2 * t + r].x);
-      f[nt][r] = m[nt][r] == -INFINITY ? 0.f : ex2(m[nt][r] - top);
+      f[nt][r] = m[nt][r] == -INFINITY ? 0.f : ex2_low(m[nt][r] - top);   // (below fp32's normal range too)
     }
 #pragma unroll
   for (int q = 0; q < MT / 4; ++q) {                   // 8 of a lane's elements at a time
@@ -539,7 +540,7 @@ kv4_mma_kernel(const __grid_constant__ KvqParams a) {
 #pragma unroll
       for (int k = 0; k < kWarps; ++k) {
         const float2 ml = ml_s[k * L::kRows + r];
-        sum = fmaf(ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2(ml.x - (top == -INFINITY ? 0.f : top)), ml.y, sum);
+        sum = fmaf(ml.x == -INFINITY && ml.y == 0.f ? 0.f : ex2_low(ml.x - (top == -INFINITY ? 0.f : top)), ml.y, sum);
         const float4 *src = reinterpret_cast<const float4 *>(part + (k * L::kRows + r) * L::kXld + 8 * ge);
         const float4 x = src[0], y = src[1];
         v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;

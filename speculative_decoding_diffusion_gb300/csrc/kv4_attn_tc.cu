@@ -99,8 +99,9 @@ struct Smem {
   static constexpr int kOffRow = kOffTau + kMaxB * 4;       // rows' score factors
   static constexpr int kOffMax = kOffRow + kRows * 4;       // [2 blocks][2 halves][4 quadrants][32]: row maxima, sums
   static constexpr int kOffNewKv = kOffMax + 2 * kHalves * kRows * 4;       // new tokens: 2^ke and ve of each,
-  static constexpr int kOffNewInv = kOffNewKv + kKeys * 8;                  // and 2^-ve (zeros past the last)
-  static constexpr int kOffGone = kOffNewInv + kKeys * 4;
+  static constexpr int kOffNewDown = kOffNewKv + kKeys * 8;                 // 2^-ve, and kShareLift - ve
+  static constexpr int kOffNewShare = kOffNewDown + kMaxNew * 4;
+  static constexpr int kOffGone = kOffNewShare + kMaxNew * 4;
   static constexpr int kOffMisc = kOffGone + kGone * 4;     // tmem address, error flag, odd new values
   static constexpr int kBytes = kOffMisc + 32;
   static constexpr int kAlloc = kBytes + 1024;              // 1024-byte alignment slack
@@ -249,7 +250,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   uint32_t *odd_s = reinterpret_cast<uint32_t *>(sb + L::kOffMisc + 8);   // new tokens whose values hold a NaN or an
                                                                           // infinity, one bit each
   float2 *new_kv_s = reinterpret_cast<float2 *>(sb + L::kOffNewKv);
-  float *new_inv_s = reinterpret_cast<float *>(sb + L::kOffNewInv);
+  float *new_down_s = reinterpret_cast<float *>(sb + L::kOffNewDown), *new_share_s = new_down_s + kMaxNew;
   uint32_t *gone_s = reinterpret_cast<uint32_t *>(sb + L::kOffGone);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 1) {
@@ -349,10 +350,8 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
       *flag_s = 0;
       odd_s[0] = odd_s[1] = 0u;
     }
-    for (int i = lane; i < kKeys; i += 32) {
-      new_kv_s[i] = make_float2(0.f, 0.f);
-      new_inv_s[i] = 0.f;
-    }
+    for (int i = lane; i < kKeys; i += 32) new_kv_s[i] = make_float2(0.f, 0.f);
+    for (int i = lane; i < kMaxNew; i += 32) new_down_s[i] = new_share_s[i] = 0.f;
     fence_barrier_init();
   }
   tc::fence_before_sync();
@@ -389,9 +388,10 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
 #pragma unroll
         for (int m = CH / 2; m > 0; m >>= 1) va = fmaxf(va, __shfl_xor_sync(0xffffffffu, va, m));
         if (e < w.n * CH && e % CH == 0) {
-          const int ve = scale_exponent(va, -64, 119);
+          const int ve = value_exponent(va);
           new_kv_s[e / CH].y = (float)ve;
-          new_inv_s[e / CH] = pow2i(-ve);
+          new_down_s[e / CH] = pow2i(-ve);
+          new_share_s[e / CH] = kShareLift - (float)ve;
         }
       }
     }
@@ -558,7 +558,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         float v[2][8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float vdown = new_inv_s[j + t];
+          const float vdown = new_down_s[j + t];
           load_vec<__nv_bfloat16, 8>(vs + (j + t) * HD + c * 8, v[t]);
 #pragma unroll
           for (int i = 0; i < 8; ++i)        // (an odd one times a weight of 0 would reach every row)
@@ -718,14 +718,15 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
               continue;
             }
             if (!held) fetch(q);
-            float4 iv;                       // the new tokens' share of the sum
+            float4 sh;                       // the new tokens' share of the sum
 #pragma unroll
             for (int e = 0; e < CW / 2; ++e) {
               const float2 x = fma_f32x2(make_float2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), f2, b2);
               const float2 p = make_float2(ex2(x.x), ex2(x.y));
               if (is_new) {
-                if (e % 2 == 0) iv = load_shared4(base + L::kOffNewInv + (k_lo + 64 * q + 2 * e) * 4);
-                sum = fma_f32x2(p, e % 2 == 0 ? make_float2(iv.x, iv.y) : make_float2(iv.z, iv.w), sum);
+                if (e % 2 == 0) sh = load_shared4(base + L::kOffNewShare + (k_lo + 64 * q + 2 * e) * 4);
+                const float2 y = add_f32x2(x, e % 2 == 0 ? make_float2(sh.x, sh.y) : make_float2(sh.z, sh.w));
+                sum = add_f32x2(sum, make_float2(ex2(y.x), ex2(y.y)));
               } else {
                 sum = add_f32x2(sum, p);
               }
@@ -765,8 +766,9 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
           const float theirs = both_s[(tb * kHalves + (half ^ 1)) * kRows];
           if (!ok || theirs != theirs) { ok = false; return false; }
           mx = fmaxf(mx, theirs);
-          const bool move = row_valid && mx > m_ref + kLift;
-          const float m_new = move ? mx - kLift : m_ref;
+          constexpr float lift = is_new ? kNewLift : kLift;
+          const bool move = row_valid && mx > m_ref + lift;
+          const float m_new = move ? mx - lift : m_ref;
           const float alpha = move ? ex2(m_ref - m_new) : 1.f;     // m_ref = -inf -> 0
           l *= alpha;
           m_ref = m_new;
@@ -802,7 +804,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         if constexpr (KW == 16) tc::st8(tW + kp * 8, pw);
         else if constexpr (KW == 32) tc::st16(tW + kp * 16, pw);
         else tc::st32(tW, pw);
-        l += sum.x + sum.y;
+        l = is_new ? fmaf(sum.x + sum.y, kShareUnlift, l) : l + (sum.x + sum.y);
         const Phase after = two(kBarSFull, j + 1);                         // (a test's latency passes here)
         const bool there = mbar_test(after.bar, after.parity);
         tc::wait_st();
@@ -866,7 +868,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         if (c >= R) break;
-        const float wc = ex2(ml[c].x - (mt == -INFINITY ? 0.f : mt));   // -inf reference -> 0
+        const float wc = ex2_low(ml[c].x - (mt == -INFINITY ? 0.f : mt));   // -inf reference -> 0; below the normal range too
         lt = fmaf(wc, ml[c].y + ml[c].z, lt);
 #pragma unroll
         for (int k = 0; k < HD / 32; ++k) {
