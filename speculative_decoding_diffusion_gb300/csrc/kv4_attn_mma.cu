@@ -582,13 +582,14 @@ cudaError_t launch_nt(const simsd_kvq_verify_desc *d, const KvqPlan &p, const Kv
 
 template <int HD>
 cudaError_t launch_hd(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a, cudaStream_t stream) {
-  return p.rows_per_tile == 16 ? launch_nt<HD, 2, 6>(d, p, a, stream)
-         : p.warps == 4        ? launch_nt<HD, 1, 4>(d, p, a, stream) : launch_nt<HD, 1, 8>(d, p, a, stream);
+  if (p.rows_per_tile == 16) return launch_nt<HD, 2, 6>(d, p, a, stream);
+  if (p.rows_per_tile != 8) return cudaErrorInvalidValue;      // no kernel of that tile
+  return p.warps == 4 ? launch_nt<HD, 1, 4>(d, p, a, stream) : launch_nt<HD, 1, 8>(d, p, a, stream);
 }
 
 }  // namespace
 
-int kv4_rows_per_tile(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= 16 ? 16 : 128; }
+int kv4_rows_per_tile(int64_t max_rows) { return max_rows <= 8 ? 8 : max_rows <= kFewRows ? kFewRows : 128; }
 
 cudaError_t launch_kv4_mma(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a, cudaStream_t stream) {
   return d->head_dim == 128 ? launch_hd<128>(d, p, a, stream) : launch_hd<64>(d, p, a, stream);

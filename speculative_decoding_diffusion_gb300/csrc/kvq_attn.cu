@@ -491,7 +491,7 @@ simsd_status kvq_plan(const simsd_kvq_verify_desc *d, bool four, KvqPlan *p) {
   p->row_tiles = (int)((max_rows + p->rows_per_tile - 1) / p->rows_per_tile);
   const int64_t per_seq = (int64_t)d->num_kv_heads * p->row_tiles;
   if (per_seq * d->batch * 64 >= ((int64_t)1 << 31)) return SIMSD_ERR_SHAPE;
-  const bool few = tc && four && p->rows_per_tile <= 16;
+  const bool few = p->few = tc && four && p->rows_per_tile <= kFewRows;
   const int sms = device_sm_count();
   // CTAs of an SM.  Few rows of a 4-bit cache: two, or where there are units for
   // two waves of them four of half as many warps (256 sequences of 256..8192 keys,
@@ -593,7 +593,7 @@ simsd_status run_verify(const simsd_kvq_verify_desc *d, bool four, void *stream_
   if (e == cudaSuccess)
     e = d->dtype != SIMSD_BF16 ? launch_kvq_simt(d, p, a, stream)
         : !four                ? launch_kvq_tc(d, p, a, stream)
-        : p.rows_per_tile <= 32 ? launch_kv4_mma(d, p, a, stream) : launch_kv4_tc(d, p, a, stream);
+        : p.few                ? launch_kv4_mma(d, p, a, stream) : launch_kv4_tc(d, p, a, stream);
   if (e == cudaSuccess && p.n_splits > 1) e = launch_kvq_merge(d, p, a, stream);
   return e == cudaSuccess ? SIMSD_OK : SIMSD_ERR_CUDA;
 }

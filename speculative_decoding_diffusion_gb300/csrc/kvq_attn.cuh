@@ -17,6 +17,7 @@ struct KvqPlan {
   int T, per, G, rows_per_tile, row_tiles;
   int n_splits, tail_from, s_tail, chunk_tail, tail_first, grid;
   bool four;                             // the 4-bit cache
+  bool few;                              // of it: the kernel for few rows (launch_kv4_mma)
   int warps;                             // of a CTA (4-bit cache, few rows)
   bool ranked;                           // units by the sequences' lengths (kvq_order_kernel)
   int merge_seqs;                        // sequences (the last in the units' order) with split units
@@ -132,7 +133,9 @@ cudaError_t launch_kvq_simt(const simsd_kvq_verify_desc *d, const KvqPlan &p, co
                             cudaStream_t stream);
 cudaError_t launch_kvq_tc(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                           cudaStream_t stream);
-// The 4-bit cache, bf16: rows of a tile for units of up to max_rows rows.
+// The 4-bit cache, bf16: rows of a tile for units of up to max_rows rows; up to
+// kFewRows of them are launch_kv4_mma's, 128 launch_kv4_tc's.
+constexpr int kFewRows = 16;
 int kv4_rows_per_tile(int64_t max_rows);
 cudaError_t launch_kv4_mma(const simsd_kvq_verify_desc *d, const KvqPlan &p, const KvqParams &a,
                            cudaStream_t stream);

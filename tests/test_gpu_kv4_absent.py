@@ -55,3 +55,10 @@ def test_pages_of_split_keys(dtype, order, B, node, hd):
     lens = [3000, 77, 1025]
     gone = [list(range(0, 24)) + [50, 99, 187], [1, 4], [63, 64]]
     check(B, lens, gone, [B] * 3, order, dtype, 4, 1, hd, node)
+
+
+@pytest.mark.parametrize("G,B", [(1, 8), (3, 3), (16, 1), (17, 1), (3, 6), (31, 1), (16, 2), (33, 1), (43, 3)])
+@pytest.mark.parametrize("hd", [128, 64])
+def test_rows_around_the_kernels_borders(G, B, hd):
+    """8, 9, 16, 17, 18, 31, 32, 33 and 129 rows of a KV head: every row is written, by whichever kernel takes them."""
+    check(G + B, [200, 0, 1300], [[2], [], [0, 80]], [B] * 3, "causal", "bf16", G, 2, hd)
