@@ -354,6 +354,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         raise_status(a.status, kStatusTimeout);
         atomicOr(flag_s, 1);
       }
+      // stay until the last products are done (default limit): after a wait that
+      // gave up elsewhere nobody else waits for them, and the tiles and tensor
+      // memory that they use go with the CTA
+      auto drain = [&](int bars, int n, int sent) {   // n barriers in turn, one a block
+        if (sent > 0) (void)mbar_wait(bar(bars + (sent - 1) % n), ((sent - 1) / n) & 1);
+      };
+      drain(kBarSFull, 2, ns);
+      drain(kBarKEmpty, kStages, ns);
+      drain(kBarPvDone, 2, np);
+      drain(kBarVEmpty, kStages, np);
     }
   } else {
     // ---------------------------------------------------------- softmax

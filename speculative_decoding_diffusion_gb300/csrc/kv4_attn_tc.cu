@@ -364,6 +364,12 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
   auto p_full = [&](int j) { return Phase{bar(kBarPFull + (j & (kPvBars - 1))), (uint32_t)(j / kPvBars) & 1u}; };
   auto two = [&](int first, int j) { return Phase{bar(first + (j & 1)), (uint32_t)(j >> 1) & 1u}; };   // of a pair of barriers
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
+  // An issuing warp stays until its last product is done (default limit): after a
+  // wait that gave up elsewhere nobody else waits for it, and the tiles and tensor
+  // memory that it uses go with the CTA.
+  auto drain = [&](int sent, auto phase) {
+    if (sent > 0) (void)mbar_wait_warp(phase(sent - 1).bar, phase(sent - 1).parity);
+  };
   // These warps together rotate the query rows and, in the CTA that owns the new
   // tokens, their keys, to f16 relative to a power of two of each row's; rolled
   // loops, since each CTA runs them once.
@@ -499,6 +505,7 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
                         dK0 + ((uint32_t)(at + (kk >> 2) * L::kHalf + (kk & 3) * 32) >> 4), idS, kk > 0);
     };
     bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
+    int sent = 0;                            // blocks whose products were issued
     for (int j = 0; ok && j < n_blocks; ++j) {
       const int tb = j & 1;
       const Phase keys = two(kBarKbFull, j), weights = p_full(j - 2);
@@ -512,14 +519,17 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         tc::commit(bar(kBarSFull + tb));
       }
       __syncwarp();
+      sent = j + 1;
     }
     if (!ok && lane == 0) give_up();
+    drain(sent, [&](int j) { return two(kBarSFull, j); });
   } else if (warp == kPvWarp) {
     // ---------------------------------------------------------------- P V
     constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 0);
     auto value_at = [](int kk) { return (uint32_t)((kk >> 2) * (HD * 128) + (kk & 3) * 32) >> 4; };
     const uint64_t dV0 = tc::smem_desc_sw128(base + L::kOffVb, 16, 1024);
     bool ok = true;
+    int sent = 0;
     for (int j = 0; j < n_blocks; ++j) {
       const int tb = j & 1, jp = j - fresh;
       ok = wait_all(a.polls, two(kBarVbFull, j), p_full(j));
@@ -540,8 +550,10 @@ kv4_tc_kernel(const __grid_constant__ KvqParams a) {
         tc::commit(bar(kBarPvDone + (j & (kPvBars - 1))));
       }
       __syncwarp();
+      sent = j + 1;
     }
     if (!ok && lane == 0) give_up();
+    drain(sent, pv_done);
   } else if (warp >= kDecodeWarp) {
     // ------------------------------------------------------------- decode
     const bool values = warp >= kValueWarp;

@@ -329,6 +329,12 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
   int issued = 0;                            // producers: blocks whose loads were started
   float2 *cs_s = reinterpret_cast<float2 *>(sb + L::kOffVb + L::kVb);   // [kMaxNew][HD / 2]
   auto give_up = [&]() { raise_status(a.status, kStatusTimeout); atomicOr(flag_s, 1); };
+  // An issuing warp stays until its last product is done (default limit): after a
+  // wait that gave up elsewhere nobody else waits for it, and the tiles and tensor
+  // memory that it uses go with the CTA.
+  auto drain = [&](int bars, int n, int sent) {   // n barriers in turn, one a block
+    if (sent > 0) (void)mbar_wait_warp(bar(bars + (sent - 1) % n), ((sent - 1) / n) & 1);
+  };
   // The softmax and decode warps together rotate the query rows into two e4m3
   // parts and, in the CTA that owns the new tokens, their keys likewise (the
   // decode warps then take their values); rolled loops, since each CTA runs them
@@ -517,6 +523,7 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
     };
     const uint32_t qhi = tmem + L::kColQ, qlo = qhi + HD / 4;
     bool ok = mbar_wait_warp(bar(kBarQReady), 0, a.polls);
+    int sent = 0;                            // blocks whose products were issued
     for (int j = 0; ok && j < n_blocks; ++j) {
       const int tb = j & 1, jp = j - fresh, s = jp & (kStages - 1);
       ok = (jp < 0 ? mbar_wait_warp(bar(kBarKnReady), 0, a.polls)
@@ -540,13 +547,17 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         }
       }
       __syncwarp();
+      sent = j + 1;
     }
     if (!ok && lane == 0) give_up();
+    drain(kBarSFull, 2, sent);
+    drain(kBarKEmpty, kStages, sent - fresh);
   } else if (warp == kPvWarp) {
     // ---------------------------------------------------------------- P V
     constexpr uint32_t idO = tc::idesc_f16(kRows, HD, 1);
     const uint64_t dV0 = tc::smem_desc_sw128(base + L::kOffVb, L::kHalf, 1024);
     bool ok = true;
+    int sent = 0;
     for (int j = 0; j < n_blocks; ++j) {
       const int tb = j & 1, jp = j - fresh;
       ok = mbar_wait_warp(bar(kBarVbFull + tb), (j >> 1) & 1, a.polls) && mbar_wait_warp(bar(kBarPFull + tb), (j >> 1) & 1, a.polls);
@@ -567,8 +578,10 @@ kvq_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ K
         tc::commit(bar(kBarPvDone + tb));
       }
       __syncwarp();
+      sent = j + 1;
     }
     if (!ok && lane == 0) give_up();
+    drain(kBarPvDone, 2, sent);
   } else if (warp >= kDecodeWarp && warp < kSoftmaxB) {
     // ------------------------------------------------------------- decode
     const int dw = warp - kDecodeWarp;
