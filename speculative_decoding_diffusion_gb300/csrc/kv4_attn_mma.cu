@@ -17,9 +17,14 @@
 //
 // Bytes bound it where there are many units: 256 sequences of 256..8192 keys, one
 // token, 32 / 8 heads of 128, take 214 us, 0.92 of the copy rate; 64 of 1..4096 39 us
-// (0.60: set-up, rows and the last wave), 8 of 32768 61 us (0.74).  With 16 rows it is
-// the decoding and the MMAs, which feed 16 columns at a legacy rate: 64 x 4096, 92 us
-// (0.50).  At 32 rows the tcgen05 kernel is faster (64 x 4096: 131 us, here 158).
+// (0.60: set-up, rows and the last wave), 8 of 32768 61 us (0.74).  With 16 rows no
+// unit is full (64 x 4096, 92 us, 0.50: issue slots 46%, tensor pipe 34%, DRAM 42%): 168
+// registers leave an SM twelve warps, too few to cover their own fixed latencies.
+// Beyond 16 rows the tcgen05 kernel takes over.  At 24 rows this one, in six warps, takes
+// 20 us of 16 x 1024 keys and 33 of 4 x 8192 where that one takes 15 and 26.5, but 123 of
+// 64 x 4096 and 445 of 256 x 256..8192 where that one takes 128 and 495: the border is the
+// few-unit one, and many units lose a tenth by it.  At 32 rows this one spills (215 us of
+// 64 x 4096, that one 129).
 #include <atomic>
 
 #include "common.cuh"

@@ -4,8 +4,9 @@
 // S = Q K^T and O += P V in f16 with fp32 sums (kind::f16).  The cache's values
 // are exact in f16 (an e2m1 code times a scale of four bits); a query row and a
 // new key or value is held relative to a power of two of its own.  A row's
-// weights are p = 2^(t - M + 7), t its scores in log2 units and M a reference at
-// most 8 stale, so p <= 2^15 fits f16.  One CTA per (key split, KV head x 128-row
+// weights are p = 2^(t - M), t its scores in log2 units (of new tokens: plus their
+// values' exponent) and M a reference that starts 7 (15 in the new tokens' block)
+// below the largest of them and moves before p passes 2^15, f16's range.  One CTA per (key split, KV head x 128-row
 // tile, sequence); rows stack new tokens x heads of the group, so a byte of the
 // cache is read and decoded once for all of them.
 //   warps 0, 3   one bulk copy per page (18 hd bytes: keys, values, scales), a
@@ -27,9 +28,9 @@
 // pair's barrier, weights to TMEM), where the tensor cores need 1024; at 64 rows
 // the decoding warps, 1600 to 1900 (700 to 1000 of it decoding, the rest the
 // latencies of waits and arrivals); and 14000 cycles of set-up and 4300 of epilogue
-// a CTA.  8 x 32768 keys, 16 + 16 new tokens, 32 / 8 heads of 128: 137 us, of 70
-// on the tensor cores; 64 x 4096, 8 + 8: 140 us, of 48 by bytes; 256 x 256..8192,
-// 4..8: 532 us, of 206 by bytes.
+// a CTA.  8 x 32768 keys, 16 + 16 new tokens, 32 / 8 heads of 128: 136 us, of 70
+// on the tensor cores; 64 x 4096, 8 + 8: 139 us, of 48 by bytes; 256 x 256..8192,
+// 4..8: 541 us, of 206 by bytes.
 #include <atomic>
 
 #include "common.cuh"

@@ -1,9 +1,11 @@
 // kv4_read.cu -- simsd_kv4_read: positions of the 4-bit cache back as rows.
 //
 // A CTA takes 16 rows of the output; codes are multiplied by their scale in f16
-// (exact).  Bytes bound it: 9 in for every 16 elements, 16 to 64 out.
-// 262144 positions of 8 heads of 128 to bf16: 260 us, 5.3 TB/s (0.79 of the copy
-// rate); 576,000 to e4m3 395 us, 4.7 TB/s (0.70), where the conversions count too.
+// (exact).  Bytes: 9 in for every 16 elements, 16 to 64 out.
+// 262144 positions of 8 heads of 128 to bf16: 258 us, 5.3 TB/s (0.80 of the copy
+// rate), to fp32 439 us (0.83), to e4m3 184 us (0.68).  No unit is full (bf16: DRAM 64%,
+// issue slots 68%, ALU 53%; e4m3: 49%, 62%, 55%, and its 52 registers leave an SM four
+// CTAs, whose warps wait for their reads five cycles of each instruction's eleven).
 #include "kv4.cuh"
 #include "kvq.cuh"
 #include "vec.cuh"

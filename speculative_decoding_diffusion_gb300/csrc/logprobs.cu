@@ -15,10 +15,11 @@
 // and 151,936 entries) and only the entries that do are sorted.  A key of 64
 // bits, the value's ordered bits over the inverted index, makes the order total.
 //
-// The first pass is bound by its reads: 1536 rows of 151,936 in bf16 87 us, 5.4 TB/s
-// (0.80 of the copy rate), in CTAs of 128 threads, eight an SM (ten: 2% less on many
-// rows, 10% more on few; 256 threads, four: 103 us).  Both passes: 101 us; four rows
-// 6.3 us, two launches and their round trips.
+// 1536 rows of 151,936 take the first pass 87 us in bf16, 5.4 TB/s (0.80 of the copy
+// rate; DRAM 68%, issue slots 67%, ALU 50%: reads and arithmetic share it), in CTAs of
+// 128 threads, eight an SM (ten: 2% less on many rows, 10% more on few; 256 threads,
+// four: 103 us).  Both passes: 99.5 us, in fp32 152 (0.92), with nine tenths of the
+// entries at -1e9 and T = 0.3 101; four rows 6.2 us, two launches and their round trips.
 #include <math.h>
 
 #include "common.cuh"
